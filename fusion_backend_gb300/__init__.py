@@ -29,6 +29,7 @@ ERR_DEVICE = -7
 
 ACT_F32 = 0
 ACT_BF16 = 1
+ACT_F16 = 2
 W_BF16 = 0
 W_Q4B32 = 1
 W_I8 = 2
@@ -36,6 +37,13 @@ W_I8 = 2
 QUERY_PATH = 0
 QUERY_LAUNCHES_PER_EXECUTE = 1
 QUERY_TWO_STREAM_WORKSPACE = 2
+
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+GATE_LINEAR = 0
+GATE_SIGMOID = 1
 
 EXPORTS = (
     "moe_ffn_prepare",
@@ -51,6 +59,10 @@ EXPORTS = (
     "moe_ffn_execute_static_scratch",
     "moe_ffn_last_cuda_error",
     "moe_ffn_execute_two_stream",
+    "moe_ffn_route",
+    "moe_ffn_norm_residual",
+    "moe_ffn_adapters_workspace",
+    "moe_ffn_add_adapters",
 )
 
 STATIC_SCRATCH_BYTES = 1 << 24
@@ -68,6 +80,25 @@ class Shapes(ctypes.Structure):
 
 class DType(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("wfmt", ctypes.c_int32)]
+
+
+def _fields(i32="", f32="", i64=""):
+    return [(n, t) for names, t in ((i32, ctypes.c_int32), (f32, ctypes.c_float), (i64, ctypes.c_int64))
+            for n in names.split()]
+
+
+class RouteArgs(ctypes.Structure):
+    _fields_ = _fields("T E top_k score groups top_groups group_score renorm dtype", "scale", "row_stride")
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = _fields("T H y_dtype res_dtype normed_dtype gate_dtype w_post_dtype w_pre_dtype post_norm gate_layout "
+                       "gate_sigmoid", "alpha beta w_offset eps",
+                       "y_stride res_stride res_out_stride normed_stride gate_stride")
+
+
+class AdaptersArgs(ctypes.Structure):
+    _fields_ = _fields("T K N R n_adapters x_dtype y_dtype", "", "x_stride y_stride out_stride")
 
 
 _lib = None
@@ -111,6 +142,14 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_last_cuda_error.argtypes = []
         L.moe_ffn_execute_two_stream.restype = ctypes.c_int
         L.moe_ffn_execute_two_stream.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp, vp]
+        L.moe_ffn_route.restype = ctypes.c_int
+        L.moe_ffn_route.argtypes = [ctypes.POINTER(RouteArgs), vp, vp, vp, vp, vp]
+        L.moe_ffn_norm_residual.restype = ctypes.c_int
+        L.moe_ffn_norm_residual.argtypes = [ctypes.POINTER(NormArgs), vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_ffn_adapters_workspace.restype = ctypes.c_int
+        L.moe_ffn_adapters_workspace.argtypes = [ctypes.POINTER(AdaptersArgs), ctypes.POINTER(sz)]
+        L.moe_ffn_add_adapters.restype = ctypes.c_int
+        L.moe_ffn_add_adapters.argtypes = [ctypes.POINTER(AdaptersArgs), vp, vp, sz, vp, vp, vp, vp, vp, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -239,6 +278,187 @@ def moe_ffn_execute_two_stream(plan, workspace, x, router_w, expert_w, shexp_w, 
                                             ev(fork_event), ev(join_event), _ptr(workspace), nbytes, _ptr(x),
                                             _ptr(router_w), _ptr(expert_w), _ptr(shexp_w), _ptr(shexp_gate_w),
                                             _ptr(out)), "moe_ffn_execute_two_stream")
+
+
+# ----------------------------------------------------------------------------
+# Operators around the layer.  Types, layouts and strides come from the
+# tensors: matrices [rows, columns] with adjacent columns, in rows of any
+# stride; a tensor of another type, shape or device raises ValueError.  Outputs
+# that are not given are allocated on the call's stream.
+
+
+_CODES: dict = {}
+
+
+def _code(t, name: str, allowed=(ACT_F32, ACT_BF16, ACT_F16)) -> int:
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.float32: ACT_F32, torch.bfloat16: ACT_BF16, torch.float16: ACT_F16})
+    c = _CODES.get(t.dtype)
+    if c not in allowed:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported")
+    return c
+
+
+def _require(ok: bool, message: str) -> None:
+    if not ok:
+        raise ValueError(message)
+
+
+def _matrix(t, rows: int, cols: int, name: str) -> int:
+    """Row stride of t, a [rows, cols] tensor with adjacent columns."""
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the columns of a row must be adjacent")
+    # a single row has no stride of its own (the tensor's may be anything)
+    return t.stride(0) if rows > 1 else cols
+
+
+def _whole(t, shape, dtype, name: str) -> None:
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+
+
+def _on_device(first, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device != first.device):
+            raise ValueError(f"{name}: must be on the call's CUDA device")
+
+
+def _new(stream, shape, dtype, device):
+    """A tensor allocated on the stream that the call runs on."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def moe_ffn_route(logits, top_k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,
+                  group_score: int = GROUP_MAX, renorm: bool = True, scale: float = 1.0, ids=None, weights=None,
+                  stream=None):
+    """Experts (int32 [T, top_k], best first, -1 where none is left) and weights (fp32 [T, top_k]) of every row of
+    ``logits`` [T, E]; the scores, the balance ``bias`` [E], the groups and the weights as in ``moe_ffn_route`` of
+    ``include/moe_ffn.h``.  Returns (ids, weights)."""
+    import torch
+
+    _require(logits.dim() == 2, "logits: expected [T, E]")
+    T, E = logits.shape
+    a = RouteArgs(T, E, top_k, score, groups, top_groups, group_score, bool(renorm), _code(logits, "logits"), scale,
+                  _matrix(logits, T, E, "logits"))
+    if bias is not None:
+        _whole(bias, (E,), torch.float32, "bias")
+    if ids is not None:
+        _whole(ids, (T, top_k), torch.int32, "ids")
+    if weights is not None:
+        _whole(weights, (T, top_k), torch.float32, "weights")
+    _on_device(logits, logits=logits, bias=bias, ids=ids, weights=weights)
+    if ids is None:
+        ids = _new(stream, (T, max(top_k, 0)), torch.int32, logits.device)
+    if weights is None:
+        weights = _new(stream, (T, max(top_k, 0)), torch.float32, logits.device)
+    _check(lib().moe_ffn_route(a, _stream(stream), logits.data_ptr(), _ptr(bias), ids.data_ptr(), weights.data_ptr()),
+           "moe_ffn_route")
+    return ids, weights
+
+
+def moe_ffn_norm_residual(res, y=None, post_norm: bool = False, w_post=None, gate=None, gate_act: int = GATE_LINEAR,
+                          alpha: float = 1.0, beta: float = 1.0, w_pre=None, w_offset: float = 0.0,
+                          eps: float = 1e-6, res_out=None, normed=None, norm_dtype=None, stream=None):
+    """``res_out = alpha res + beta a(gate) z``, z being the block's output ``y`` or (``post_norm``) its RMSNorm, and
+    ``normed``, the RMSNorm of res_out for the next block (see ``include/moe_ffn.h``).  ``gate``: [H] per channel,
+    [T, 1] per token or [T, H].  res_out defaults to ``res`` (in place; not written where ``y`` is None and alpha is
+    1), normed to a new tensor of ``norm_dtype`` (bf16).  Returns (res_out, normed)."""
+    import torch
+
+    _require(res.dim() == 2, "res: expected [T, H]")
+    T, H = res.shape
+    if res_out is None:
+        res_out = res
+    _require(res_out.dtype == res.dtype, "res_out: must have res's dtype")
+    rd = _code(res, "res")
+    rs = _matrix(res, T, H, "res")
+    os_ = _matrix(res_out, T, H, "res_out")
+    yd, ys = (_code(y, "y"), _matrix(y, T, H, "y")) if y is not None else (ACT_F32, H)
+    layout, gd, gs = 0, ACT_F32, H
+    if gate is not None:
+        gd = _code(gate, "gate")
+        if gate.dim() == 1:
+            _whole(gate, (H,), gate.dtype, "gate")
+        elif gate.shape == (T, 1):
+            layout, gs = 1, gate.stride(0) if T > 1 else 1
+        else:
+            layout, gs = 2, _matrix(gate, T, H, "gate")
+    wcode = lambda w, name: ACT_F32 if w is None else _code(w, name, (ACT_F32, ACT_BF16))  # noqa: E731
+    pd, nd = wcode(w_post, "w_post"), wcode(w_pre, "w_pre")
+    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if w is not None:
+            _whole(w, (H,), w.dtype, name)
+    if normed is not None:
+        _require(norm_dtype is None or norm_dtype == normed.dtype, "normed: not of norm_dtype")
+        _code(normed, "normed")
+        _matrix(normed, T, H, "normed")
+    _on_device(res, res=res, y=y, w_post=w_post, gate=gate, w_pre=w_pre, res_out=res_out, normed=normed)
+    if normed is None:
+        normed = _new(stream, (T, H), norm_dtype or torch.bfloat16, res.device)
+    a = NormArgs(T, H, yd, rd, _code(normed, "normed"), gd, pd, nd, bool(post_norm), layout, gate_act == GATE_SIGMOID,
+                 alpha, beta, w_offset, eps, ys, rs, os_, _matrix(normed, T, H, "normed"), gs)
+    unchanged = y is None and alpha == 1.0 and res_out is res
+    _check(lib().moe_ffn_norm_residual(a, _stream(stream), res.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate),
+                                       _ptr(w_pre), None if unchanged else res_out.data_ptr(), normed.data_ptr()),
+           "moe_ffn_norm_residual")
+    return res_out, normed
+
+
+def moe_ffn_adapters_workspace(T: int, K: int, N: int, R: int) -> int:
+    """Workspace bytes of moe_ffn_add_adapters for T tokens, widths K and N and a pool of rank R."""
+    n = ctypes.c_size_t()
+    a = AdaptersArgs(T, K, N, R, 0, ACT_BF16, ACT_F32, (K + 7) // 8 * 8, N, N)
+    _check(lib().moe_ffn_adapters_workspace(a, ctypes.byref(n)), "moe_ffn_adapters_workspace")
+    return max(n.value, 256)
+
+
+def moe_ffn_add_adapters(y, x, adapter_ids, a, b, ranks=None, scales=None, out=None, workspace=None, stream=None,
+                         workspace_bytes=None):
+    """``out_t = y_t + scales_i b_i (a_i x_t)`` with i = ``adapter_ids[t]`` (int32 [T]; -1: no adapter).  x [T, K],
+    y [T, N], a [n, R, K], b [n, N, R], ranks int32 [n], scales fp32 [n] (see ``include/moe_ffn.h``).  out defaults to
+    y (in place), the workspace to a new one.  Returns out."""
+    import torch
+
+    _require(x.dim() == 2 and y.dim() == 2 and a.dim() == 3 and b.dim() == 3,
+             "expected x [T, K], y [T, N], a [n, R, K], b [n, N, R]")
+    T, K = x.shape
+    n, R = a.shape[:2]
+    N = b.shape[1]
+    if out is None:
+        out = y
+    xd = _code(x, "x", (ACT_BF16, ACT_F16))
+    _whole(a, (n, R, K), x.dtype, "a")
+    _whole(b, (n, N, R), x.dtype, "b")
+    _whole(adapter_ids, (T,), torch.int32, "adapter_ids")
+    _require(out.dtype == y.dtype, "out: must have y's dtype")
+    if ranks is not None:
+        _whole(ranks, (n,), torch.int32, "ranks")
+    if scales is not None:
+        _whole(scales, (n,), torch.float32, "scales")
+    xs = _matrix(x, T, K, "x")
+    args = AdaptersArgs(T, K, N, R, n, xd, _code(y, "y"), xs if T > 1 else (K + 7) // 8 * 8, _matrix(y, T, N, "y"),
+                        _matrix(out, T, N, "out"))
+    _on_device(x, x=x, y=y, adapter_ids=adapter_ids, a=a, b=b, ranks=ranks, scales=scales, out=out,
+               workspace=None if isinstance(workspace, int) else workspace)
+    if workspace is None:
+        workspace = _new(stream, (moe_ffn_adapters_workspace(T, K, N, R),), torch.uint8, x.device)
+    nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    _check(lib().moe_ffn_add_adapters(args, _stream(stream), _ptr(workspace), nbytes, x.data_ptr(),
+                                      adapter_ids.data_ptr(), _ptr(a), _ptr(b), _ptr(ranks), _ptr(scales),
+                                      y.data_ptr(), out.data_ptr()), "moe_ffn_add_adapters")
+    return out
 
 
 def moe_ffn_strerror(status: int) -> str:

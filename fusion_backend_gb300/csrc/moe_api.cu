@@ -481,6 +481,174 @@ const char* moe_ffn_strerror(int status) {
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Operators around the layer: checks of the argument blocks and launches (see
+// moe_ffn.h).
+namespace {
+
+bool valid_elem(int d) { return d == MOE_FFN_ACT_F32 || d == MOE_FFN_ACT_BF16 || d == MOE_FFN_ACT_F16; }
+bool elem_aligned(const void* p, int d) { return aligned(p, d == MOE_FFN_ACT_F32 ? 4 : 2); }
+bool finite(float v) { return v - v == 0.f; }
+
+// The current device is a GB300.
+int check_device() {
+  DeviceInfo* dev = nullptr;
+  return device_info(&dev);
+}
+
+int check_adapters(const moe_ffn_adapters_args* a) {
+  if (!a || a->T < 0 || a->n_adapters < 0) return MOE_FFN_ERR_INVALID_ARG;
+  if ((a->x_dtype != MOE_FFN_ACT_BF16 && a->x_dtype != MOE_FFN_ACT_F16) || !valid_elem(a->y_dtype))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->R < 1 || a->R > kAdapterMaxRank || a->K < 8 || a->K > 65536 || a->K % 8 || a->N < 1 || a->N > (1 << 20))
+    return MOE_FFN_ERR_UNSUPPORTED;
+  if (a->x_stride < a->K || a->y_stride < a->N || a->out_stride < a->N) return MOE_FFN_ERR_INVALID_ARG;
+  if (a->x_stride % 8) return MOE_FFN_ERR_MISALIGNED;
+  return MOE_FFN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_ffn_route(const moe_ffn_route_args* a, moe_ffn_stream_t stream, const void* logits, const float* bias,
+                  int32_t* ids, float* w) {
+  if (!a || a->T < 0 || !valid_elem(a->dtype)) return MOE_FFN_ERR_INVALID_ARG;
+  if ((a->score != MOE_FFN_SCORE_SOFTMAX && a->score != MOE_FFN_SCORE_SIGMOID) ||
+      (a->group_score != MOE_FFN_GROUP_MAX && a->group_score != MOE_FFN_GROUP_TOP2) || !finite(a->scale))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->E < 1 || a->E > kMaxExperts || a->top_k < 1 || a->top_k > kMaxTopK || a->top_k > a->E || a->groups < 1 ||
+      a->groups > kRouteMaxGroups || a->E % a->groups || a->top_groups < 1 || a->top_groups > a->groups ||
+      a->top_k > a->top_groups * (a->E / a->groups))
+    return MOE_FFN_ERR_UNSUPPORTED;
+  if (a->row_stride < a->E) return MOE_FFN_ERR_INVALID_ARG;
+  if (a->T == 0) return MOE_FFN_OK;
+  if (!logits || !ids || !w) return MOE_FFN_ERR_INVALID_ARG;
+  if (!elem_aligned(logits, a->dtype) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
+    return MOE_FFN_ERR_MISALIGNED;
+  const int rc = check_device();
+  if (rc != MOE_FFN_OK) return rc;
+  RouteParams P;
+  P.T = a->T;
+  P.E = a->E;
+  P.K = a->top_k;
+  P.G = a->top_groups == a->groups ? 1 : a->groups;  // every group kept: no group stage
+  P.gs = a->E / P.G;
+  P.top_groups = a->top_groups;
+  P.sigmoid = a->score == MOE_FFN_SCORE_SIGMOID;
+  P.top2 = a->group_score == MOE_FFN_GROUP_TOP2;
+  P.renorm = a->renorm != 0;
+  P.dtype = a->dtype;
+  P.scale = a->scale;
+  P.stride = a->row_stride;
+  P.logits = logits;
+  P.bias = bias;
+  P.ids = ids;
+  P.w = w;
+  return cuda_status(launch_route(P, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_ffn_norm_residual(const moe_ffn_norm_args* a, moe_ffn_stream_t stream, const void* res, const void* y,
+                          const void* w_post, const void* gate, const void* w_pre, void* res_out, void* normed) {
+  if (!a || a->T < 0) return MOE_FFN_ERR_INVALID_ARG;
+  if (!valid_elem(a->y_dtype) || !valid_elem(a->res_dtype) || !valid_elem(a->normed_dtype) ||
+      !valid_elem(a->gate_dtype) || (a->w_post_dtype != MOE_FFN_ACT_F32 && a->w_post_dtype != MOE_FFN_ACT_BF16) ||
+      (a->w_pre_dtype != MOE_FFN_ACT_F32 && a->w_pre_dtype != MOE_FFN_ACT_BF16) || a->gate_layout < 0 ||
+      a->gate_layout > MOE_FFN_GATE_FULL || !(a->eps >= 0.f) || !finite(a->eps) || !finite(a->alpha) ||
+      !finite(a->beta) || !finite(a->w_offset))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->H < 1 || a->H > kNormMaxH) return MOE_FFN_ERR_UNSUPPORTED;
+  if (a->T == 0) return MOE_FFN_OK;
+  if (!res || (!res_out && !normed)) return MOE_FFN_ERR_INVALID_ARG;
+  if (a->res_stride < a->H || (y && a->y_stride < a->H) || (res_out && a->res_out_stride < a->H) ||
+      (normed && a->normed_stride < a->H) ||
+      (y && gate && a->gate_layout == MOE_FFN_GATE_TOKEN && a->gate_stride < 1) ||
+      (y && gate && a->gate_layout == MOE_FFN_GATE_FULL && a->gate_stride < a->H))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (!elem_aligned(res, a->res_dtype) || !elem_aligned(res_out, a->res_dtype) || !elem_aligned(y, a->y_dtype) ||
+      !elem_aligned(normed, a->normed_dtype) || !elem_aligned(gate, a->gate_dtype) ||
+      !elem_aligned(w_post, a->w_post_dtype) || !elem_aligned(w_pre, a->w_pre_dtype))
+    return MOE_FFN_ERR_MISALIGNED;
+  const int rc = check_device();
+  if (rc != MOE_FFN_OK) return rc;
+  NormParams P;
+  P.T = a->T;
+  P.H = a->H;
+  P.y_dtype = a->y_dtype;
+  P.r_dtype = a->res_dtype;
+  P.n_dtype = a->normed_dtype;
+  P.g_dtype = a->gate_dtype;
+  P.wpost_dtype = a->w_post_dtype;
+  P.wpre_dtype = a->w_pre_dtype;
+  P.post_norm = y && a->post_norm;
+  P.gate_layout = a->gate_layout;
+  P.gate_sigmoid = a->gate_sigmoid != 0;
+  P.alpha = a->alpha;
+  P.beta = a->beta;
+  P.w_offset = a->w_offset;
+  P.eps = a->eps;
+  P.y_stride = a->y_stride;
+  P.r_stride = a->res_stride;
+  P.ro_stride = a->res_out_stride;
+  P.n_stride = a->normed_stride;
+  P.g_stride = a->gate_stride;
+  P.res = res;
+  P.y = y;
+  P.w_post = w_post;
+  P.gate = y ? gate : nullptr;
+  P.w_pre = w_pre;
+  P.res_out = res_out;
+  P.normed = normed;
+  return cuda_status(launch_norm(P, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_ffn_adapters_workspace(const moe_ffn_adapters_args* a, size_t* bytes) {
+  if (!bytes) return MOE_FFN_ERR_INVALID_ARG;
+  const int rc = check_adapters(a);
+  if (rc != MOE_FFN_OK) return rc;
+  *bytes = adapters_workspace(a->T, a->K, a->N, a->R);
+  return MOE_FFN_OK;
+}
+
+int moe_ffn_add_adapters(const moe_ffn_adapters_args* a, moe_ffn_stream_t stream, void* workspace,
+                         size_t workspace_bytes, const void* x, const int32_t* adapter_ids, const void* A,
+                         const void* B, const int32_t* ranks, const float* scales, const void* y, void* out) {
+  int rc = check_adapters(a);
+  if (rc != MOE_FFN_OK) return rc;
+  if (a->T == 0) return MOE_FFN_OK;
+  if (!workspace || !x || !adapter_ids || !y || !out || (a->n_adapters > 0 && (!A || !B)))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (workspace_bytes < adapters_workspace(a->T, a->K, a->N, a->R)) return MOE_FFN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(adapter_ids, 4) ||
+      !aligned(ranks, 4) || !aligned(scales, 4) || !elem_aligned(y, a->y_dtype) || !elem_aligned(out, a->y_dtype))
+    return MOE_FFN_ERR_MISALIGNED;
+  rc = check_device();
+  if (rc != MOE_FFN_OK) return rc;
+  AdapterParams P;
+  P.T = a->T;
+  P.K = a->K;
+  P.N = a->N;
+  P.R = a->R;
+  P.n = a->n_adapters;
+  P.f16 = a->x_dtype == MOE_FFN_ACT_F16;
+  P.y_dtype = a->y_dtype;
+  P.x_stride = a->x_stride;
+  P.y_stride = a->y_stride;
+  P.out_stride = a->out_stride;
+  P.x = static_cast<const uint16_t*>(x);
+  P.A = static_cast<const uint16_t*>(A);
+  P.B = static_cast<const uint16_t*>(B);
+  P.ids = adapter_ids;
+  P.ranks = ranks;
+  P.scales = scales;
+  P.y = y;
+  P.out = out;
+  P.v = static_cast<float*>(workspace);
+  return cuda_status(launch_adapters(P, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // Allocation-free entry point: the scratch lives in a file-scope device array
 // instead of a caller-provided workspace (see moe_ffn.h).
 namespace {

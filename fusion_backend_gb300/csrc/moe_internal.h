@@ -244,4 +244,47 @@ constexpr int kLaunchesPerExecute = 1;
 // two-stream form (moe_rows.cu).
 cudaError_t launch_join_add(const float* a, const float* b, float* out, int n, cudaStream_t stream);
 
+// ---- operators around the layer (moe_route.cu, moe_norm.cu,
+// moe_adapters.cu); fields as in the public argument blocks.
+constexpr int kRouteMaxGroups = 32;  // a lane holds one group's value
+constexpr int kNormMaxH = 32768;
+constexpr int kAdapterMaxRank = 128;
+
+struct RouteParams {
+  int T, E, K, G, gs, top_groups;  // gs experts a group
+  int sigmoid, top2, renorm, dtype;
+  float scale;
+  long long stride;
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float* w;
+};
+cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
+
+struct NormParams {
+  int T, H;
+  int y_dtype, r_dtype, n_dtype, g_dtype, wpost_dtype, wpre_dtype;
+  int post_norm, gate_layout, gate_sigmoid;
+  float alpha, beta, w_offset, eps;
+  long long y_stride, r_stride, ro_stride, n_stride, g_stride;
+  const void *res, *y, *w_post, *gate, *w_pre;
+  void *res_out, *normed;
+};
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
+
+struct AdapterParams {
+  int T, K, N, R, n;
+  int f16, y_dtype;
+  long long x_stride, y_stride, out_stride;
+  const uint16_t *x, *A, *B;
+  const int32_t *ids, *ranks;
+  const float* scales;
+  const void* y;
+  void* out;
+  float* v;  // workspace: A_a x of every token
+};
+size_t adapters_workspace(int T, int K, int N, int R);
+cudaError_t launch_adapters(const AdapterParams& p, cudaStream_t stream);
+
 }  // namespace moe

@@ -74,7 +74,8 @@ typedef struct {
   int32_t T, H, E, top_k, I, Is;
 } moe_ffn_shapes;
 
-typedef enum { MOE_FFN_ACT_F32 = 0, MOE_FFN_ACT_BF16 = 1 } moe_ffn_act_dtype;
+/* MOE_FFN_ACT_F16: the operators around the layer only (not a plan's x). */
+typedef enum { MOE_FFN_ACT_F32 = 0, MOE_FFN_ACT_BF16 = 1, MOE_FFN_ACT_F16 = 2 } moe_ffn_act_dtype;
 
 /* Weight format of the routed experts and of the shared expert.  The router
  * and the shared-gate vector are bf16 in both formats. */
@@ -266,6 +267,111 @@ int moe_ffn_execute_two_stream(moe_ffn_plan_t plan, moe_ffn_stream_t stream, moe
                                moe_ffn_event_t fork_event, moe_ffn_event_t join_event, void* workspace,
                                size_t workspace_bytes, const void* x, const void* router_w, const void* expert_w,
                                const void* shexp_w, const void* shexp_gate_w, float* out);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the layer.  They need no plan: a call checks its argument
+ * block on the host, enqueues on `stream` and returns without synchronising;
+ * each can be captured in a CUDA graph, allocates nothing and is bitwise
+ * reproducible.  Row strides are in elements and at least the row's width.
+ * Tensors need the alignment of their element type only (16-byte aligned rows
+ * are faster), unless stated.  T = 0 is a call that does nothing.
+ */
+
+/*
+ * Routing: scores, selection and weights from router logits.
+ *   l_te  logit (fp32, bf16 or fp16); -inf and NaN mask expert e for token t,
+ *         +inf counts as the largest fp32 number
+ *   s_te  = exp(l_te) / sum_i exp(l_ti)  (MOE_FFN_SCORE_SOFTMAX, over the
+ *           experts that are not masked), or 1 / (1 + exp(-l_te))
+ *           (MOE_FFN_SCORE_SIGMOID)
+ *   c_te  = s_te + bias_e   (bias for balance, fp32; used for the choice alone.
+ *           -inf and NaN mask the expert for every token, +inf counts as the
+ *           largest fp32 number).  bias NULL: c_te = s_te
+ *   groups: the experts form `groups` groups of E / groups neighbours; a group's
+ *           value is its largest c (MOE_FFN_GROUP_MAX) or the sum of its two
+ *           largest (MOE_FFN_GROUP_TOP2; of one, where only one is left); the
+ *           top_groups groups of the largest values keep their experts, equal
+ *           values going to the lower group
+ *   ids   = the top_k largest c of the kept experts, larger first, equal c
+ *           ordered by the larger logit, then by the lower expert index
+ *   w_tj  = scale s_{t,ids_j}, divided by sum_i s_{t,ids_i} when renorm != 0
+ * Where fewer than top_k experts are left the last ids are -1 and their
+ * weights 0 (a wholly masked token: all of them); moe_ffn_execute_routed drops
+ * such choices.  The choice is the one of c in fp64: scores closer than fp32
+ * can tell apart are compared in fp64.
+ * 1 <= E <= 1024, 1 <= top_k <= min(E, 32), groups <= 32 and a divisor of E,
+ * 1 <= top_groups <= groups, top_k <= top_groups E / groups.
+ */
+typedef enum { MOE_FFN_SCORE_SOFTMAX = 0, MOE_FFN_SCORE_SIGMOID = 1 } moe_ffn_score;
+typedef enum { MOE_FFN_GROUP_MAX = 0, MOE_FFN_GROUP_TOP2 = 1 } moe_ffn_group_score;
+typedef struct {
+  int32_t T, E, top_k;
+  int32_t score;               /* moe_ffn_score */
+  int32_t groups, top_groups;  /* 1, 1: no groups */
+  int32_t group_score;         /* moe_ffn_group_score */
+  int32_t renorm;
+  int32_t dtype;               /* moe_ffn_act_dtype of the logits */
+  float scale;                 /* finite */
+  int64_t row_stride;          /* of the logits */
+} moe_ffn_route_args;
+/* logits [T,E], bias [E] or NULL, ids int32 [T,top_k], w fp32 [T,top_k]. */
+int moe_ffn_route(const moe_ffn_route_args* args, moe_ffn_stream_t stream, const void* logits, const float* bias,
+                  int32_t* ids, float* w);
+
+/*
+ * The norms after one block and before the next, with the block's gate and
+ * the residual scale between them.  Per token:
+ *   z      = y rsqrt(mean(y^2) + eps) (w_offset + w_post)  if post_norm, else y
+ *   r'     = alpha r + beta a(gate) z        a(g) = g or 1 / (1 + exp(-g));
+ *            gate NULL: a = 1.  y NULL: r' = alpha r
+ *   normed = r' rsqrt(mean(r'^2) + eps) (w_offset + w_pre)
+ * All in fp32; r' enters the second norm unrounded; res_out and normed are
+ * rounded once.  w_post, w_pre fp32 or bf16 [H] (NULL: w_offset + w = 1).
+ * gate: [H] (MOE_FFN_GATE_CHANNEL), [T] (MOE_FFN_GATE_TOKEN, gate_stride apart)
+ * or [T,H] (MOE_FFN_GATE_FULL).  res_out may be res (same dtype and stride),
+ * normed may be y (same); either may be NULL, not both.  Any other overlap is
+ * undefined.  1 <= H <= 32768.
+ */
+typedef enum { MOE_FFN_GATE_CHANNEL = 0, MOE_FFN_GATE_TOKEN = 1, MOE_FFN_GATE_FULL = 2 } moe_ffn_gate_layout;
+typedef struct {
+  int32_t T, H;
+  int32_t y_dtype, res_dtype, normed_dtype, gate_dtype;  /* moe_ffn_act_dtype; res_dtype: res and res_out */
+  int32_t w_post_dtype, w_pre_dtype;                     /* MOE_FFN_ACT_F32 or MOE_FFN_ACT_BF16 */
+  int32_t post_norm;
+  int32_t gate_layout;   /* moe_ffn_gate_layout */
+  int32_t gate_sigmoid;  /* a(g): 0 linear, 1 sigmoid */
+  float alpha, beta, w_offset, eps;  /* finite, eps >= 0 */
+  int64_t y_stride, res_stride, res_out_stride, normed_stride, gate_stride;
+} moe_ffn_norm_args;
+int moe_ffn_norm_residual(const moe_ffn_norm_args* args, moe_ffn_stream_t stream, const void* res, const void* y,
+                          const void* w_post, const void* gate, const void* w_pre, void* res_out, void* normed);
+
+/*
+ * Low-rank adapters of many requests beside a projection (or the layer) that
+ * they share.  Per token t with adapter a = adapter_ids[t]:
+ *   out_t = y_t + scales_a B_a (A_a x_t)
+ * A [n_adapters,R,K] and B [n_adapters,N,R] bf16 or fp16 as x, contiguous and
+ * 16-byte aligned; x [T,K] 16-byte aligned, its stride a multiple of 8; y and
+ * out [T,N] of one dtype.  out may be y (same stride).
+ * adapter_ids int32 [T]; outside 0..n_adapters-1 (-1 by convention): out_t =
+ * y_t.  ranks int32 [n_adapters] or NULL (all R): only the first ranks_a rows
+ * of A_a and columns of B_a count (clamped to 0..R; what the others hold does
+ * not matter).  scales fp32 [n_adapters] or NULL (1).
+ * Sums are in fp32.
+ * 1 <= R <= 128, 8 <= K <= 65536 a multiple of 8, 1 <= N <= 1048576.
+ * The workspace (256-byte aligned, scratch) holds what
+ * moe_ffn_adapters_workspace reports for the argument block.
+ */
+typedef struct {
+  int32_t T, K, N, R, n_adapters;
+  int32_t x_dtype;  /* MOE_FFN_ACT_BF16 or MOE_FFN_ACT_F16: x, A and B */
+  int32_t y_dtype;  /* moe_ffn_act_dtype: y and out */
+  int64_t x_stride, y_stride, out_stride;
+} moe_ffn_adapters_args;
+int moe_ffn_adapters_workspace(const moe_ffn_adapters_args* args, size_t* bytes);
+int moe_ffn_add_adapters(const moe_ffn_adapters_args* args, moe_ffn_stream_t stream, void* workspace,
+                         size_t workspace_bytes, const void* x, const int32_t* adapter_ids, const void* A,
+                         const void* B, const int32_t* ranks, const float* scales, const void* y, void* out);
 
 /* Queries on a plan. */
 typedef enum {
