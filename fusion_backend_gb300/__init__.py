@@ -59,6 +59,7 @@ EXPORTS = (
     "moe_ffn_execute_static_scratch",
     "moe_ffn_last_cuda_error",
     "moe_ffn_execute_two_stream",
+    "moe_ffn_execute_routed",
     "moe_ffn_route",
     "moe_ffn_norm_residual",
     "moe_ffn_adapters_workspace",
@@ -142,6 +143,8 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_last_cuda_error.argtypes = []
         L.moe_ffn_execute_two_stream.restype = ctypes.c_int
         L.moe_ffn_execute_two_stream.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp, vp]
+        L.moe_ffn_execute_routed.restype = ctypes.c_int
+        L.moe_ffn_execute_routed.argtypes = [vp, vp, vp, sz, vp, vp, vp, vp, vp, vp, vp]
         L.moe_ffn_route.restype = ctypes.c_int
         L.moe_ffn_route.argtypes = [ctypes.POINTER(RouteArgs), vp, vp, vp, vp, vp]
         L.moe_ffn_norm_residual.restype = ctypes.c_int
@@ -278,6 +281,16 @@ def moe_ffn_execute_two_stream(plan, workspace, x, router_w, expert_w, shexp_w, 
                                             ev(fork_event), ev(join_event), _ptr(workspace), nbytes, _ptr(x),
                                             _ptr(router_w), _ptr(expert_w), _ptr(shexp_w), _ptr(shexp_gate_w),
                                             _ptr(out)), "moe_ffn_execute_two_stream")
+
+
+def moe_ffn_execute_routed(plan, workspace, x, ids, weights, expert_w, shexp_w, shexp_gate_w, out, stream=None,
+                           workspace_bytes=None):
+    """The layer for a routing that the caller brings: ``ids`` int32 and ``weights`` fp32 [T, top_k], an id outside
+    0..E-1 dropping the choice.  shexp_gate_w None: the shared expert is not gated; shexp_w None: no shared expert."""
+    nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    _check(lib().moe_ffn_execute_routed(plan, _stream(stream), _ptr(workspace), nbytes, _ptr(x), _ptr(ids),
+                                        _ptr(weights), _ptr(expert_w), _ptr(shexp_w), _ptr(shexp_gate_w), _ptr(out)),
+           "moe_ffn_execute_routed")
 
 
 # ----------------------------------------------------------------------------
@@ -497,6 +510,20 @@ class MoeFFN:
         moe_ffn_execute_block(self.plan, self.workspace, x_res, router_w, expert_w, shexp_w, shexp_gate_w, eps,
                               topk_ids, None, stream)
         return x_res
+
+    def routed(self, x, ids, weights, expert_w, shexp_w=None, shexp_gate_w=None, out=None, stream=None):
+        """The layer for a given routing (moe_ffn_execute_routed); returns out."""
+        import torch
+
+        s = self.shapes
+        _whole(ids, (s.T, s.top_k), torch.int32, "ids")
+        _whole(weights, (s.T, s.top_k), torch.float32, "weights")
+        _on_device(x, x=x, ids=ids, weights=weights)
+        if out is None:
+            out = _new(stream, (s.T, s.H), torch.float32, x.device)
+        moe_ffn_execute_routed(self.plan, self.workspace, x, ids, weights, expert_w, shexp_w, shexp_gate_w, out,
+                               stream)
+        return out
 
     def status(self, stream=None) -> int:
         return moe_ffn_read_status(self.plan, self.workspace, stream)

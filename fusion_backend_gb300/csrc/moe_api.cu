@@ -110,12 +110,15 @@ void fill_params(const moe_ffn_plan* plan, LayerParams& P, void* ws) {
   P.r_nactive = reinterpret_cast<int32_t*>(w + plan->ws.nactive);
 }
 
+// given_ids: the caller's routing [T,top_k] instead of the router's (router_w
+// is then null); the shared expert and its gate may be missing with it.
 int run(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* workspace, size_t workspace_bytes, const void* x,
         const void* router_w, const void* expert_w, const void* shexp_w, const void* shexp_gate_w, float* out,
-        int32_t* topk_ids, float* topk_w, int block_mode, float eps) {
+        int32_t* topk_ids, float* topk_w, int block_mode, float eps, const int32_t* given_ids = nullptr,
+        const float* given_w = nullptr) {
   if (!valid_plan(plan)) return MOE_FFN_ERR_INVALID_ARG;
-  if (!workspace || !x || !router_w || !expert_w || !shexp_w || !shexp_gate_w || !out)
-    return MOE_FFN_ERR_INVALID_ARG;
+  if (!workspace || !x || !expert_w || !out) return MOE_FFN_ERR_INVALID_ARG;
+  if (!given_ids && (!router_w || !shexp_w || !shexp_gate_w)) return MOE_FFN_ERR_INVALID_ARG;
   if (workspace_bytes < plan->ws.total) return MOE_FFN_ERR_WORKSPACE;
   if (!aligned(workspace, 256) || !aligned(x, 16) || !aligned(router_w, 16) || !aligned(expert_w, 16) ||
       !aligned(shexp_w, 16) || !aligned(shexp_gate_w, 16) || !aligned(out, 16) || !aligned(topk_ids, 4) ||
@@ -137,11 +140,13 @@ int run(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* workspace, size_t wo
     B.E = s.E;
     B.K = s.top_k;
     B.I = s.I;
-    B.Is = s.Is;
+    B.Is = shexp_w ? s.Is : 0;
     B.G = dev->sm_count < kMaxGrid ? dev->sm_count : kMaxGrid;
     B.x = static_cast<const uint16_t*>(x);
     B.router_w = static_cast<const uint16_t*>(router_w);
     B.gate_w = static_cast<const uint16_t*>(shexp_gate_w);
+    B.given_ids = given_ids;
+    B.given_w = given_w;
     B.expert_w = static_cast<const uint8_t*>(expert_w);
     B.shexp_w = static_cast<const uint8_t*>(shexp_w);
     B.out = out;
@@ -159,7 +164,7 @@ int run(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* workspace, size_t wo
     B.slot_w = reinterpret_cast<float*>(w + L.slot_w);
     B.x_perm = reinterpret_cast<uint16_t*>(w + L.x_perm);
     B.h_ws = reinterpret_cast<uint16_t*>(w + L.h_ws);
-    B.hw = s.I > s.Is ? s.I : s.Is;
+    B.hw = s.I > B.Is ? s.I : B.Is;
     B.wfmt = plan->wfmt;
     B.rb = plan->wfmt == MOE_FFN_W_Q4B32 ? (long long)s.H / 2 + s.H / 16 : 2LL * s.H;
     B.y_ws = reinterpret_cast<float*>(w + L.y_ws);
@@ -185,6 +190,14 @@ int run(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* workspace, size_t wo
   P.out = out;
   P.topk_ids = topk_ids;
   P.topk_w = topk_w;
+  P.given_ids = given_ids;
+  P.given_w = given_w;
+  if (!shexp_w) {
+    P.part = 1;
+    P.gate_w = nullptr;
+    P.shexp_w = P.expert_w;  // for the tensor maps, which no copy uses
+    P.Is = P.I;
+  }
   P.block_mode = block_mode;
   P.eps = eps;
   P.G = dev->sm_count < kMaxGrid ? dev->sm_count : kMaxGrid;
@@ -374,6 +387,15 @@ int moe_ffn_execute_block(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* wo
   if (!(eps >= 0.f)) return MOE_FFN_ERR_INVALID_ARG;
   return run(plan, stream, workspace, workspace_bytes, x_res, router_w, expert_w, shexp_w, shexp_gate_w, x_res,
              topk_ids, topk_w, 1, eps);
+}
+
+int moe_ffn_execute_routed(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* workspace, size_t workspace_bytes,
+                           const void* x, const int32_t* ids, const float* w, const void* expert_w,
+                           const void* shexp_w, const void* shexp_gate_w, float* out) {
+  if (!ids || !w) return MOE_FFN_ERR_INVALID_ARG;
+  if (!aligned(ids, 4) || !aligned(w, 4)) return MOE_FFN_ERR_MISALIGNED;
+  return run(plan, stream, workspace, workspace_bytes, x, nullptr, expert_w, shexp_w, shexp_w ? shexp_gate_w : nullptr,
+             out, nullptr, nullptr, 0, 0.f, ids, w);
 }
 
 int moe_ffn_read_status(moe_ffn_plan_t plan, const void* workspace, moe_ffn_stream_t stream,

@@ -297,6 +297,65 @@ __global__ void __launch_bounds__(256) k_topk_b(const __grid_constant__ BatchPar
   }
 }
 
+// The caller's routing in the place of the router and its top-k.  Blocks
+// 0 .. tw-1: the 32 tokens of bitmap word b -- the choices that stand (an id
+// outside 0..E-1 drops the choice; a repeated id is one choice with the
+// weights added in rank order) and the word of every expert, built in shared
+// memory, so no word has to be cleared first.  The blocks behind them: the
+// shared gate of eight tokens each, a warp a token (and, 4-bit weights, the
+// shared slots' B rows).
+__global__ void __launch_bounds__(256) k_given_b(const __grid_constant__ BatchParams P) {
+  __shared__ uint32_t s_word[kBatchMaxE];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = P.K;
+  pdl_launch_dependents();
+  pdl_wait();
+  if ((int)blockIdx.x < P.tw) {
+    if (blockIdx.x == 0 && tid < kCtrlWords) P.ctrl[tid] = 0u;
+    for (int e = tid; e < P.E; e += 256) s_word[e] = 0u;
+    __syncthreads();
+    for (int b = warp; b < 32; b += 8) {
+      const int t = 32 * blockIdx.x + b;
+      if (t >= P.T) break;
+      const size_t at = (size_t)t * K + lane;
+      int e = lane < K ? P.given_ids[at] : -1;
+      const float w = lane < K ? P.given_w[at] : 0.f;
+      if (e < 0 || e >= P.E) e = -1;
+      float sum = 0.f;
+      bool repeat = false;
+      for (int j = 0; j < K; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j);
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        if (ej == e) {
+          sum += wj;
+          repeat |= j < lane;
+        }
+      }
+      if (lane < K) {
+        const bool keep = e >= 0 && !repeat;
+        P.ids[at] = keep ? e : -1;
+        P.p[at] = sum;
+        if (keep)
+          atomicOr(&s_word[e], 1u << b);
+        else
+          P.slot_of[at] = -1;  // the others' slots come from the bucketing
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < P.E; e += 256) P.bitmap[(size_t)e * P.tw + blockIdx.x] = s_word[e];
+    return;
+  }
+  const int t = 8 * ((int)blockIdx.x - P.tw) + warp;
+  if (t >= P.T || P.Is == 0) return;
+  float s = 1.f;
+  if (P.gate_w) s = 1.0f / (1.0f + expf(-exact_logit(P, t, P.E)));
+  if (lane == 0) P.slot_w[(size_t)P.T * K + t] = s;
+  if (P.wfmt == 1) {
+    const uint4* src = reinterpret_cast<const uint4*>(P.x + (size_t)t * P.H);
+    uint4* dst = reinterpret_cast<uint4*>(P.x_perm + ((size_t)P.T * K + t) * P.H);
+    for (int q = lane; q < P.H / 8; q += 32) dst[q] = x8_f16_order(src[q]);
+  }
+}
+
 // Blocks (e, 0 .. kGatherSplit-1): the expert's count, offset (counts of the
 // experts below) and active index; block (e, 0) writes them and the slots of
 // its tokens (ascending), their weights and choice indices; every block
@@ -380,7 +439,8 @@ __global__ void __launch_bounds__(256) k_combine_b(const __grid_constant__ Batch
   for (int c = 8 * threadIdx.x; c < P.H; c += 8 * 256) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k <= P.K; ++k) {
-      const int slot = k < P.K ? P.slot_of[(size_t)t * P.K + k] : P.T * P.K + t;
+      const int slot = k < P.K ? P.slot_of[(size_t)t * P.K + k] : P.Is > 0 ? P.T * P.K + t : -1;
+      if (slot < 0) continue;  // a dropped choice, or no shared expert
       const float4* src = reinterpret_cast<const float4*>(P.y_ws + (size_t)slot * P.H + c);
       const float4 a = src[0], b = src[1];
       acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
@@ -414,7 +474,8 @@ static cudaError_t launch_pdl(Kern kern, dim3 grid, int threads, size_t smem, cu
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-cudaError_t launch_batch(const BatchParams& p, cudaStream_t stream) {
+// Logits and top-k.
+static cudaError_t launch_router(const BatchParams& p, cudaStream_t stream) {
   const size_t route_smem = (size_t)kRouteTokens * p.H * 2;
   if (route_smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_route_b, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)route_smem);
@@ -424,6 +485,12 @@ cudaError_t launch_batch(const BatchParams& p, cudaStream_t stream) {
                                dim3((p.T + kRouteTokens - 1) / kRouteTokens, (p.E + 1 + kRouteRows - 1) / kRouteRows),
                                128, route_smem, stream, p);
   if (err == cudaSuccess) err = launch_pdl(k_topk_b, dim3(p.T), 256, 0, stream, p);
+  return err;
+}
+
+cudaError_t launch_batch(const BatchParams& p, cudaStream_t stream) {
+  cudaError_t err = p.given_ids ? launch_pdl(k_given_b, dim3(p.tw + (p.T + 7) / 8), 256, 0, stream, p)
+                                : launch_router(p, stream);
   if (err == cudaSuccess) err = launch_pdl(k_bucket_b, dim3(p.E, kGatherSplit), 256, 0, stream, p);
   if (err != cudaSuccess) return err;
   err = p.wfmt == 1 ? launch_gemm_gate_up_q4(p, stream) : launch_gemm_gate_up(p, stream);

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   const int T = P.T, K = P.K;
   // weight tiles per slot chunk: gate / up 64 rows of I (Is), down 256 columns of H
   const int MT = PHASE == 0 ? P.I / 64 : P.H / 256;
-  const int MT_s = PHASE == 0 ? P.Is / 64 : P.H / 256;
+  const int MT_s = PHASE == 0 ? P.Is / 64 : P.Is > 0 ? P.H / 256 : 0;  // Is = 0: no shared units
 
   pdl_launch_dependents();
   // ---- barriers (thread 64) and tensor memory (warp 1) before the wait on
@@ -410,21 +410,23 @@ bool encode_q4(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void*
 cudaError_t batch_tensor_maps(BatchParams& p) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = gemm_encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const long long er = (long long)p.E * 3 * p.I, sr = 3LL * p.Is, TK = (long long)p.T * p.K;
+  // (without a shared expert its maps are the experts', and not used)
+  const uint8_t* const sw = p.Is > 0 ? p.shexp_w : p.expert_w;
+  const long long er = (long long)p.E * 3 * p.I, sr = p.Is > 0 ? 3LL * p.Is : er, TK = (long long)p.T * p.K;
   if (p.wfmt == 1) {
     // 4-bit rows: codes and scales of the expert and shared blocks; B rows
     // in fp16: x_perm (routed slots, then the shared slots T K + t) and h_ws
     if (!encode_q4(fn, &p.tm_qn_e, p.expert_w, er, p.rb, 128, true) ||
         !encode_q4(fn, &p.tm_qs_e, p.expert_w, er, p.rb, 16, false) ||
-        !encode_q4(fn, &p.tm_qn_s, p.shexp_w, sr, p.rb, 128, true) ||
-        !encode_q4(fn, &p.tm_qs_s, p.shexp_w, sr, p.rb, 16, false) ||
+        !encode_q4(fn, &p.tm_qn_s, sw, sr, p.rb, 128, true) ||
+        !encode_q4(fn, &p.tm_qs_s, sw, sr, p.rb, 16, false) ||
         !encode_2d(fn, &p.tm_xp, p.x_perm, TK + p.T, p.H, 64, 16) ||
         !encode_2d(fn, &p.tm_h, p.h_ws, TK + p.T, p.hw, 64, 16))
       return cudaErrorInvalidValue;
     return cudaSuccess;
   }
   if (!encode_2d(fn, &p.tm_w64_e, p.expert_w, er, p.H, 64, 64) ||
-      !encode_2d(fn, &p.tm_w64_s, p.shexp_w, sr, p.H, 64, 64) ||
+      !encode_2d(fn, &p.tm_w64_s, sw, sr, p.H, 64, 64) ||
       !encode_2d(fn, &p.tm_xp, p.x_perm, TK, p.H, 64, 16) || !encode_2d(fn, &p.tm_x, p.x, p.T, p.H, 64, 16) ||
       !encode_2d(fn, &p.tm_h, p.h_ws, TK + p.T, 2 * p.hw, 64, 16))
     return cudaErrorInvalidValue;

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) k_gemm_q4(const __grid_constant
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int T = P.T, K = P.K;
   const int MT = PHASE == 0 ? P.I / 64 : P.H / 256;
-  const int MT_s = PHASE == 0 ? P.Is / 64 : P.H / 256;
+  const int MT_s = PHASE == 0 ? P.Is / 64 : P.Is > 0 ? P.H / 256 : 0;  // Is = 0: no shared units
 
   pdl_launch_dependents();
   if (tid == 64) {

@@ -76,11 +76,15 @@ struct LayerParams {
   // (ffn_moe_out); 2: the gated shared expert only, out = s FFN_shared(x)
   // (ffn_shexp).  Parts 1 and 2 are the two branches of the two-stream form.
   int part;
+  // the caller's routing (GIVEN instances): [T][K] ids, an id outside 0..E-1
+  // drops the choice, and their weights
+  const int32_t* given_ids;
+  const float* given_w;
 
   // caller tensors
   const void* x;  // [T,H] (block mode: fp32 x_res)
   const uint16_t* router_w;
-  const uint16_t* gate_w;
+  const uint16_t* gate_w;  // GIVEN: null where the shared expert is not gated
   const uint8_t* expert_w;
   const uint8_t* shexp_w;
   float* out;
@@ -145,6 +149,10 @@ struct BatchParams {
   float* out;                // [T][H]
   int32_t* topk_ids;         // optional [T][K]
   float* topk_w;             // optional [T][K]
+  // the caller's routing instead of the router's (null: the layer routes), see
+  // LayerParams; gate_w null: s = 1; Is = 0: no shared expert
+  const int32_t* given_ids;  // [T][K]
+  const float* given_w;      // [T][K]
   // workspace
   uint32_t* ctrl;
   float* logits;  // [T][ls] fp32 logits (plain sums)
@@ -154,7 +162,7 @@ struct BatchParams {
   float* p;           // [T][K] their weights
   uint32_t* bitmap;   // [E][tw] tokens of each expert
   int tw;             // bitmap words per expert: ceil(T / 32)
-  int32_t* slot_of;   // [T][K] slot (row of the expert-sorted order) of each choice
+  int32_t* slot_of;   // [T][K] slot (row of the expert-sorted order) of each choice, -1: dropped
   float* slot_w;      // [T K + T] weight of each slot (routed p, then the shared gate per token)
   uint16_t* x_perm;   // [T K][H] bf16, x of each routed slot (4-bit weights: [T K + T][H] fp16)
   uint16_t* h_ws;     // h of each slot (weight applied): bf16 weights [T K + T][2 hw], the bf16 hi part in
@@ -189,7 +197,7 @@ struct BatchParams {
 cudaError_t batch_tensor_maps(BatchParams& p);
 // Enqueues the whole batched layer (kBatchLaunches kernels).
 cudaError_t launch_batch(const BatchParams& p, cudaStream_t stream);
-constexpr int kBatchLaunches = 6;
+constexpr int kBatchLaunches = 6;  // 5 with the caller's routing
 // Ring depth and stage bytes of the GEMM kernels: gate / up stages hold
 // kGemmKSub0 pairs of a 128 x 64 A tile (64 gate rows over 64 up rows) and
 // an NC x 64 B tile;

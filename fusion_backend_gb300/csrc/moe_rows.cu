@@ -15,6 +15,10 @@ cudaError_t launch_rows_bf16_fast(const LayerParams& p, cudaStream_t stream);
 cudaError_t launch_rows_q4_fast(const LayerParams& p, cudaStream_t stream);
 cudaError_t launch_rows_i8_fast(const LayerParams& p, cudaStream_t stream);
 cudaError_t launch_rows_generic(const LayerParams& p, cudaStream_t stream);
+cudaError_t launch_rows_bf16_given(const LayerParams& p, cudaStream_t stream);
+cudaError_t launch_rows_q4_given(const LayerParams& p, cudaStream_t stream);
+cudaError_t launch_rows_i8_given(const LayerParams& p, cudaStream_t stream);
+cudaError_t launch_rows_generic_given(const LayerParams& p, cudaStream_t stream);
 
 namespace {
 
@@ -195,6 +199,14 @@ cudaError_t launch_join_add(const float* a, const float* b, float* out, int n, c
 }
 
 cudaError_t launch_rows(const LayerParams& p, cudaStream_t stream) {
+  if (p.given_ids) {
+    if (!rows_fast(p)) return launch_rows_generic_given(p, stream);
+    switch (p.wfmt) {
+      case kWkQ4: return launch_rows_q4_given(p, stream);
+      case kWkI8: return launch_rows_i8_given(p, stream);
+      default: return launch_rows_bf16_given(p, stream);
+    }
+  }
   if (!rows_fast(p)) return launch_rows_generic(p, stream);
   switch (p.wfmt) {
     case kWkQ4: return launch_rows_q4_fast(p, stream);

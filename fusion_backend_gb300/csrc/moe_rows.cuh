@@ -350,8 +350,12 @@ constexpr int kBarSplit = 3;  // named barrier: main and down-projection warps m
 // ------------------------------------------------------------------- kernel
 // TMAX: token capacity (T <= TMAX).  WK: weight kind (kWkBf16, kWkQ4,
 // kWkI8).  FAST: H = 2048, E <= 256 and a bf16-exact activation (the
-// tensor-core loops; bf16 and 4-bit weights).
-template <int TMAX, int WK, bool FAST, int NCH>
+// tensor-core loops; bf16 and 4-bit weights).  GIVEN: the routing is the
+// caller's (P.given_ids, P.given_w), so there are no router logits to
+// exchange: every block builds the tables itself and issues the first routed
+// stages before it has seen x, and only the one-token form keeps the first
+// grid-wide barrier (for the marks of its tagged words), behind those copies.
+template <int TMAX, int WK, bool FAST, int NCH, bool GIVEN = false>
 __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_rows(const __grid_constant__ LayerParams Pk) {
   constexpr bool Q4 = WK == kWkQ4;
   constexpr bool I8 = WK == kWkI8;              // int8 weights and activation
@@ -619,6 +623,65 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
     }
   }
 
+  // Active experts in ascending order (active index u), by warp 0 from the
+  // selection bitmap: word l on lane l, an exclusive scan of the word counts;
+  // then the tokens of every active expert and their weights.
+  auto active_table = [&]() {
+    const int nw = (P.E + 31) / 32;
+    const uint32_t w = lane < nw ? tb.bitmap[lane] : 0u;
+    const int c = __popc(w);
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int U = __shfl_sync(0xffffffffu, incl, 31);
+    int u = incl - c;
+    for (uint32_t m = w; m; m &= m - 1u, ++u) {
+      const int e = 32 * lane + __ffs((int)m) - 1;
+      tb.active[u] = e;
+      tb.inv_u[e] = static_cast<int16_t>(u);
+    }
+    __syncwarp();
+    for (int t = 0; t < T; ++t)
+      for (int k = lane; k < K; k += 32) {
+        const int ts = t * K + k;
+        if (GIVEN && tb.ids[ts] < 0) continue;
+        const int ua = tb.inv_u[tb.ids[ts]];
+        atomicOr(&tb.mask[ua], 1u << t);
+        tb.wt[ua * T + t] = tb.p[ts];
+      }
+    if (lane == 0) tb.misc[0] = U;
+  };
+  // the routed run [q0, q1) of this block in the flattened (active expert,
+  // group) order when U experts are active, shared + routed groups balanced
+  // over the blocks
+  auto routed_run = [&](int U, uint32_t& q0, uint32_t& q1) {
+    const uint32_t R = (uint32_t)U * (uint32_t)gI, G = P.G, cc = cta;
+    if (R >= G) {
+      q0 = muldiv(R + gS, cc, G) - gs0;
+      q1 = muldiv(R + gS, cc + 1, G) - gs1;
+    } else {
+      q0 = muldiv(R, cc, G);
+      q1 = muldiv(R, cc + 1, G);
+    }
+  };
+  // the first routed stages of the rings, issued by the warps in turn
+  auto issue_routed = [&]() {
+    int j = 0;
+    while (ci.k + 1 < min(n_stages, NS)) {
+      advance(ci, NS);
+      if (tid == 32 * (j++ & (kRowWarps - 1))) issue(ci);
+    }
+    if constexpr (FAST) {
+      while (cd.k + 1 < min(n_stages, P.nsd)) {
+        advance(cd, P.nsd);
+        if (tid == 32 * (j++ & (kRowWarps - 1))) issue_d(cd);
+      }
+    }
+  };
+
   // ---- before the wait (nothing the previous kernel writes is read), side
   // by side: warp 0 initialises the barriers and issues the shared expert's
   // first stages (their weights do not depend on the previous kernel), warp 1
@@ -642,19 +705,10 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
     for (int i = lane; i < T; i += 32) tb.xmax[i] = 0u;
   } else if (warp == 2) {
     // the routed run of this block for every possible count U of active
-    // experts (K <= U <= min(E, T K)): groups [q0, q1) of the flattened
-    // (active expert, group) order, so that shared + routed groups are
-    // balanced over the blocks
-    for (int j = lane; j <= min(P.E, TK) - K; j += 32) {
-      const uint32_t R = (uint32_t)(K + j) * (uint32_t)gI, G = P.G, cc = cta;
+    // experts (K <= U <= min(E, T K))
+    for (int j = lane; !GIVEN && j <= min(P.E, TK) - K; j += 32) {
       uint32_t q0, q1;
-      if (R >= G) {
-        q0 = muldiv(R + gS, cc, G) - gs0;
-        q1 = muldiv(R + gS, cc + 1, G) - gs1;
-      } else {
-        q0 = muldiv(R, cc, G);
-        q1 = muldiv(R, cc + 1, G);
-      }
+      routed_run(K + j, q0, q1);
       const uint32_t u0 = q0 / (uint32_t)gI;
       tb.qtab[4 * j] = (int)(q1 - q0);
       tb.qtab[4 * j + 1] = (int)u0;
@@ -694,9 +748,10 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
   // weights; any other predecessor has completed before this kernel starts).
   constexpr int kRC = kMaxH / (kRowThreads * 8);  // 8-element chunks of a row per thread
   uint4 wr[kRC];
-  // the shared-expert part needs only the shared-gate row (block 0)
-  const int r_first = P.part == 2 ? (cta == 0 ? P.E : P.E + 1) : cta;
-  const int r_step = P.part == 2 ? P.E + 1 : P.G;
+  // the shared-expert part needs only the shared-gate row (block 0); with a
+  // given routing every block takes that row for itself
+  const int r_first = GIVEN ? (P.gate_w ? P.E : P.E + 1) : P.part == 2 ? (cta == 0 ? P.E : P.E + 1) : cta;
+  const int r_step = GIVEN || P.part == 2 ? P.E + 1 : P.G;
   {
     const uint16_t* w = r_first < P.E ? P.router_w + (size_t)r_first * H : P.gate_w;
 #pragma unroll
@@ -734,6 +789,43 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
     for (int c = P.G + tid; c < kMaxGrid; c += kRowThreads) sync->status[c] = 0;
   }
   bool timed_out = false;
+  if constexpr (GIVEN) {
+    // the caller's routing, token t on warp 7 - t: an id outside 0..E-1 drops
+    // the choice (-1 in the table), a repeated id is one choice with the
+    // weights added in rank order
+    const int t = kRowWarps - 1 - warp;
+    if (t < T) {
+      int e = lane < K ? P.given_ids[t * K + lane] : -1;
+      const float w = lane < K ? P.given_w[t * K + lane] : 0.f;
+      if (e >= P.E) e = -1;
+      float sum = 0.f;
+      bool repeat = false;
+      for (int j = 0; j < K; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j);
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        if (ej == e) {
+          sum += wj;
+          repeat |= j < lane;
+        }
+      }
+      if (lane < K) {
+        const bool keep = e >= 0 && !repeat;
+        tb.ids[t * K + lane] = keep ? e : -1;
+        tb.p[t * K + lane] = keep ? sum : 0.f;
+        if (keep) atomicOr(&tb.bitmap[e >> 5], 1u << (e & 31));
+      }
+    }
+    if (tid < T) tb.s[tid] = 1.f;
+    blk_sync<SYNC_NT>();
+    if (warp == 0) active_table();
+    blk_sync<SYNC_NT>();
+    uint32_t q0, q1;
+    routed_run(tb.misc[0], q0, q1);
+    n_stages = n_sh + (int)(q1 - q0);
+    ur0 = (int)(q0 / (uint32_t)gI);
+    gr0 = (int)(q0 - (uint32_t)ur0 * (uint32_t)gI);
+    issue_routed();
+  }
   if (!mbar_wait(xbar, 0)) timed_out = true;
   // block form: RMSNorm factors of the fp32 rows, all warps (scratch: the
   // partials region, unused before the stage loop; ends with a barrier)
@@ -804,7 +896,10 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
           S = tt;
           C = __fadd_rn(__fadd_rn(C, red[(w * TMAX + tid) * 2 + 1]), e);
         }
-        __stcg(P.logits + (size_t)tid * P.ls + r, __fadd_rn(S, C));
+        if constexpr (GIVEN)
+          tb.s[tid] = 1.0f / (1.0f + expf(-__fadd_rn(S, C)));
+        else
+          __stcg(P.logits + (size_t)tid * P.ls + r, __fadd_rn(S, C));
       }
       blk_sync<SYNC_NT>();
     }
@@ -965,12 +1060,20 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
       }
     }
   }
-  // ---- every block's logits (first barrier; see RowSync)
-  if (!grid_barrier<SYNC_NT>(sync, 0, fast_sync, P.G, epoch, cta, true)) timed_out = true;
+  // ---- every block's logits (first barrier; see RowSync).  A given routing
+  // needs it for the marks of the tagged words alone; without them the second
+  // barrier is the call's first.
+  if constexpr (!GIVEN || TAGGED) {
+    if (!grid_barrier<SYNC_NT>(sync, 0, fast_sync, P.G, epoch, cta, true)) timed_out = true;
+  } else {
+    blk_sync<SYNC_NT>();  // x in its compute form
+  }
   // routing, every block from all logits: top-k of token t on warp 7 - t
   // (the chosen experts, their softmax weights and their bits in the
   // selection bitmap) and the shared gate sigmoid(logit_E)
-  if (P.part == 2) {
+  if constexpr (GIVEN) {
+    // (the tables are there)
+  } else if (P.part == 2) {
     // shared-expert part: only the gate s of every token
     if (tid < T) tb.s[tid] = 1.0f / (1.0f + expf(-__ldcg(P.logits + (size_t)tid * P.ls + P.E)));
   } else {
@@ -1002,57 +1105,16 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
     }
   }
   blk_sync<SYNC_NT>();
-  if (TMAX > 1 && warp == 0 && P.part != 2) {
-    // active experts in ascending order (active index u): bitmap word l on
-    // lane l, an exclusive scan of the word counts
-    const int nw = (P.E + 31) / 32;
-    const uint32_t w = lane < nw ? tb.bitmap[lane] : 0u;
-    const int c = __popc(w);
-    int incl = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int U = __shfl_sync(0xffffffffu, incl, 31);
-    int u = incl - c;
-    for (uint32_t m = w; m; m &= m - 1u, ++u) {
-      const int e = 32 * lane + __ffs((int)m) - 1;
-      tb.active[u] = e;
-      tb.inv_u[e] = static_cast<int16_t>(u);
-    }
-    __syncwarp();
-    // tokens of every active expert and their weights
-    for (int t = 0; t < T; ++t)
-      for (int k = lane; k < K; k += 32) {
-        const int ts = t * K + k;
-        const int ua = tb.inv_u[tb.ids[ts]];
-        atomicOr(&tb.mask[ua], 1u << t);
-        tb.wt[ua * T + t] = tb.p[ts];
-      }
-    if (lane == 0) tb.misc[0] = U;
-  }
-  if (TMAX > 1 && P.part != 2) blk_sync<SYNC_NT>();
+  if (!GIVEN && TMAX > 1 && warp == 0 && P.part != 2) active_table();
+  if (!GIVEN && TMAX > 1 && P.part != 2) blk_sync<SYNC_NT>();
   const int U = P.part == 2 ? 0 : tb.misc[0];
-  if (P.part != 2) {
+  if (!GIVEN && P.part != 2) {
     const int32_t* q = tb.qtab + 4 * (U - K);
     n_stages = n_sh + q[0];
     ur0 = q[1];
     gr0 = q[2];
   }
-  // the first routed stages of the rings, issued by the warps in turn
-  {
-    int j = 0;
-    while (ci.k + 1 < min(n_stages, NS)) {
-      advance(ci, NS);
-      if (tid == 32 * (j++ & (kRowWarps - 1))) issue(ci);
-    }
-    if constexpr (FAST)
-      while (cd.k + 1 < min(n_stages, P.nsd)) {
-        advance(cd, P.nsd);
-        if (tid == 32 * (j++ & (kRowWarps - 1))) issue_d(cd);
-      }
-  }
+  if (!GIVEN) issue_routed();
   if constexpr (NTB > kRowThreads) {
     // warps 8..15 take the stage count, the first routed stage and the
     // call's tag from here (they wait at kBarSplit since their start)
@@ -1093,6 +1155,7 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
       if (P.topk_ids) P.topk_ids[ts] = tb.ids[ts];
       if (P.topk_w) P.topk_w[ts] = tb.p[ts];
       const int t = ts / K, e = tb.ids[ts];
+      if (GIVEN && e < 0) continue;
       P.r_perm[P.r_offsets[e] + __popc(tb.mask[tb.inv_u[e]] & ((1u << t) - 1u))] = ts;
     }
     for (int u = lane; u < U; u += 32) P.r_active[u] = tb.active[u];
@@ -1832,7 +1895,7 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
   float resid = 0.f;
   if (P.block_mode && tid < O) resid = __ldcg(P.out + (size_t)(tid / nD) * H + da + tid % nD);
   bool tail_timed_out = false;
-  if constexpr (!TAGGED) tail_timed_out = !grid_barrier<SYNC_NT>(sync, 1, fast_sync, P.G, epoch, cta, false);
+  if constexpr (!TAGGED) tail_timed_out = !grid_barrier<SYNC_NT>(sync, 1, fast_sync, P.G, epoch, cta, GIVEN);
   // The O sums of G partials.  Thread (sp, o) adds partials sp, sp + S, ...
   // in order, up to 16 loads in flight together; the S part sums are then
   // added in order.
@@ -1882,10 +1945,10 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
 // blocks (G <= the SM count) resident at once.  A launch whose blocks could
 // not all be resident is refused (cudaErrorCooperativeLaunchTooLarge) instead
 // of ending in a timed-out barrier.
-template <int TMAX, int WK, bool FAST, int NCH>
+template <int TMAX, int WK, bool FAST, int NCH, bool GIVEN>
 inline cudaError_t rows_configure(int smem, int G) {
   // one record per instance (the statics of each template instantiation)
-  auto* const kern = k_rows<TMAX, WK, FAST, NCH>;
+  auto* const kern = k_rows<TMAX, WK, FAST, NCH, GIVEN>;
   constexpr int kDevs = 64;
   static std::atomic<int> done_smem[kDevs];
   static std::mutex mu;
@@ -1908,9 +1971,9 @@ inline cudaError_t rows_configure(int smem, int G) {
   return cudaSuccess;
 }
 
-template <int TMAX, int WK, bool FAST, int NCH = 1>
+template <int TMAX, int WK, bool FAST, int NCH = 1, bool GIVEN = false>
 inline cudaError_t launch_rows_t(const LayerParams& p, cudaStream_t stream) {
-  cudaError_t err = rows_configure<TMAX, WK, FAST, NCH>(p.smem, p.G);
+  cudaError_t err = rows_configure<TMAX, WK, FAST, NCH, GIVEN>(p.smem, p.G);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1922,7 +1985,7 @@ inline cudaError_t launch_rows_t(const LayerParams& p, cudaStream_t stream) {
   cfg.gridDim = dim3(p.G);
   cfg.blockDim = dim3(rows_threads(WK, FAST));
   cfg.dynamicSmemBytes = p.smem;
-  return cudaLaunchKernelEx(&cfg, k_rows<TMAX, WK, FAST, NCH>, p);
+  return cudaLaunchKernelEx(&cfg, k_rows<TMAX, WK, FAST, NCH, GIVEN>, p);
 }
 
 }  // namespace moe

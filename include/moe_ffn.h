@@ -268,6 +268,26 @@ int moe_ffn_execute_two_stream(moe_ffn_plan_t plan, moe_ffn_stream_t stream, moe
                                size_t workspace_bytes, const void* x, const void* router_w, const void* expert_w,
                                const void* shexp_w, const void* shexp_gate_w, float* out);
 
+/*
+ * moe_ffn_execute for a routing that the caller brings (another router's, or
+ * moe_ffn_route's) instead of the layer's own:
+ *   out_t = sum_{j=0..top_k-1} w[t,j] FFN_{ids[t,j]}(x_t)  +  s FFN_shared(x_t)
+ *   ids  int32 [T,top_k]; an id outside 0..E-1 (-1 by convention) drops the
+ *        choice, whatever its weight; an expert named twice by a token counts
+ *        once with the sum of its weights
+ *   w    fp32 [T,top_k], used as they stand
+ * shexp_gate_w NULL: the shared expert is not gated (s = 1).  shexp_w NULL: no
+ * shared term (shexp_gate_w is then ignored, and so is the plan's Is).  A token
+ * whose choices are all dropped gets the shared term alone (0 without one).
+ * Results are bitwise reproducible.  Other arguments, plans and paths as
+ * moe_ffn_execute; ids and w 4-byte aligned.  out may alias x exactly.
+ * moe_ffn_read_routing reports the buckets of the kept choices: offsets[E]
+ * entries of perm.
+ */
+int moe_ffn_execute_routed(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* workspace, size_t workspace_bytes,
+                           const void* x, const int32_t* ids, const float* w, const void* expert_w,
+                           const void* shexp_w, const void* shexp_gate_w, float* out);
+
 /* ---------------------------------------------------------------------------
  * Operators around the layer.  They need no plan: a call checks its argument
  * block on the host, enqueues on `stream` and returns without synchronising;

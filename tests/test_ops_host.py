@@ -218,3 +218,33 @@ def test_binding_checks_adapters():
         fb.moe_ffn_add_adapters(y, x, ids, a, b, ranks=torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="out"):
         fb.moe_ffn_add_adapters(y, x, ids, a, b, out=y.bfloat16())
+
+
+def test_execute_routed_refuses(lib):
+    plan, ws = fb.moe_ffn_prepare(fb.Shapes(2, 256, 8, 2, 128, 128), fb.ACT_BF16, fb.W_BF16)
+    f = lib.moe_ffn_execute_routed
+    try:
+        assert f(None, None, P, ws, P, P, P, P, P, P, P) == fb.ERR_INVALID_ARG
+        for i in (0, 2, 3, 4, 5, 8):  # workspace, x, ids, w, expert_w, out are required
+            a = [P, ws, P, P, P, P, P, P, P]
+            a[i] = None
+            assert f(plan, None, *a) == fb.ERR_INVALID_ARG, i
+        assert f(plan, None, P, ws - 1, P, P, P, P, P, P, P) == fb.ERR_WORKSPACE
+        for i, off in ((0, 128), (2, 8), (3, 2), (4, 2), (5, 8), (6, 8), (7, 8), (8, 8)):
+            a = [P, ws, P, P, P, P, P, P, P]
+            a[i] += off
+            assert f(plan, None, *a) == fb.ERR_MISALIGNED, i
+    finally:
+        fb.moe_ffn_destroy(plan)
+
+
+def test_binding_checks_routed():
+    m = fb.MoeFFN.__new__(fb.MoeFFN)
+    m.plan, m.shapes = None, fb.Shapes(2, 256, 8, 2, 128, 128)
+    x, ids, w = torch.zeros(2, 256), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        m.routed(x, ids, w, x)
+    with pytest.raises(ValueError, match="ids"):
+        m.routed(x, ids.long(), w, x)
+    with pytest.raises(ValueError, match="weights"):
+        m.routed(x, ids, w[:, :1], x)
