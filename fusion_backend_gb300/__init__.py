@@ -298,9 +298,34 @@ def moe_ffn_execute_routed(plan, workspace, x, ids, weights, expert_w, shexp_w, 
 # tensors: matrices [rows, columns] with adjacent columns, in rows of any
 # stride; a tensor of another type, shape or device raises ValueError.  Outputs
 # that are not given are allocated on the call's stream.
+#
+# The checks and the argument block depend on the tensors' shapes, strides,
+# types and device alone, so a block is built once per such signature (never
+# per tensor) and found again in _blocks: a call of a few microseconds on the
+# GPU would otherwise wait for 10 microseconds of Python.
 
 
 _CODES: dict = {}
+_blocks: dict = {}
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _remember(key, block):
+    if len(_blocks) >= 4096:
+        _blocks.clear()
+    _blocks[key] = block
+    return block
+
+
+def _raw_stream(stream, t) -> int | None:
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
 
 
 def _code(t, name: str, allowed=(ACT_F32, ACT_BF16, ACT_F16)) -> int:
@@ -353,12 +378,7 @@ def _new(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def moe_ffn_route(logits, top_k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,
-                  group_score: int = GROUP_MAX, renorm: bool = True, scale: float = 1.0, ids=None, weights=None,
-                  stream=None):
-    """Experts (int32 [T, top_k], best first, -1 where none is left) and weights (fp32 [T, top_k]) of every row of
-    ``logits`` [T, E]; the scores, the balance ``bias`` [E], the groups and the weights as in ``moe_ffn_route`` of
-    ``include/moe_ffn.h``.  Returns (ids, weights)."""
+def _route_block(logits, top_k, bias, score, groups, top_groups, group_score, renorm, scale, ids, weights):
     import torch
 
     _require(logits.dim() == 2, "logits: expected [T, E]")
@@ -372,13 +392,64 @@ def moe_ffn_route(logits, top_k: int, bias=None, score: int = SCORE_SOFTMAX, gro
     if weights is not None:
         _whole(weights, (T, top_k), torch.float32, "weights")
     _on_device(logits, logits=logits, bias=bias, ids=ids, weights=weights)
-    if ids is None:
-        ids = _new(stream, (T, max(top_k, 0)), torch.int32, logits.device)
-    if weights is None:
-        weights = _new(stream, (T, max(top_k, 0)), torch.float32, logits.device)
-    _check(lib().moe_ffn_route(a, _stream(stream), logits.data_ptr(), _ptr(bias), ids.data_ptr(), weights.data_ptr()),
-           "moe_ffn_route")
+    return a
+
+
+def moe_ffn_route(logits, top_k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,
+                  group_score: int = GROUP_MAX, renorm: bool = True, scale: float = 1.0, ids=None, weights=None,
+                  stream=None):
+    """Experts (int32 [T, top_k], best first, -1 where none is left) and weights (fp32 [T, top_k]) of every row of
+    ``logits`` [T, E]; the scores, the balance ``bias`` [E], the groups and the weights as in ``moe_ffn_route`` of
+    ``include/moe_ffn.h``.  Returns (ids, weights)."""
+    key = (0, _sig(logits), top_k, _sig(bias), score, groups, top_groups, group_score, renorm, scale, _sig(ids),
+           _sig(weights))
+    a = _blocks.get(key) or _remember(key, _route_block(logits, top_k, bias, score, groups, top_groups, group_score,
+                                                        renorm, scale, ids, weights))
+    if ids is None or weights is None:
+        import torch
+
+        shape = (a.T, max(top_k, 0))
+        ids = _new(stream, shape, torch.int32, logits.device) if ids is None else ids
+        weights = _new(stream, shape, torch.float32, logits.device) if weights is None else weights
+    rc = (_lib or lib()).moe_ffn_route(a, _raw_stream(stream, logits), logits.data_ptr(),
+                                       None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr())
+    if rc:
+        _check(rc, "moe_ffn_route")
     return ids, weights
+
+
+def _norm_block(res, y, post_norm, w_post, gate, gate_act, alpha, beta, w_pre, w_offset, eps, res_out, normed,
+                norm_dtype):
+    _require(res.dim() == 2, "res: expected [T, H]")
+    T, H = res.shape
+    _require(res_out.dtype == res.dtype, "res_out: must have res's dtype")
+    rd, rs, os_ = _code(res, "res"), _matrix(res, T, H, "res"), _matrix(res_out, T, H, "res_out")
+    yd, ys = (_code(y, "y"), _matrix(y, T, H, "y")) if y is not None else (ACT_F32, H)
+    layout, gd, gs = 0, ACT_F32, H
+    if gate is not None:
+        gd = _code(gate, "gate")
+        if gate.dim() == 1:
+            _whole(gate, (H,), gate.dtype, "gate")
+        elif tuple(gate.shape) == (T, 1):
+            layout, gs = 1, gate.stride(0) if T > 1 else 1
+        else:
+            layout, gs = 2, _matrix(gate, T, H, "gate")
+    codes = []
+    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        codes.append(ACT_F32 if w is None else _code(w, name, (ACT_F32, ACT_BF16)))
+        if w is not None:
+            _whole(w, (H,), w.dtype, name)
+    nd, ns = ACT_BF16, H
+    if normed is not None:
+        _require(norm_dtype is None or norm_dtype == normed.dtype, "normed: not of norm_dtype")
+        nd, ns = _code(normed, "normed"), _matrix(normed, T, H, "normed")
+    elif norm_dtype is not None:
+        _code(res, "res")
+        _require(norm_dtype in _CODES, f"norm_dtype: {norm_dtype} is not supported")
+        nd = _CODES[norm_dtype]
+    _on_device(res, res=res, y=y, w_post=w_post, gate=gate, w_pre=w_pre, res_out=res_out, normed=normed)
+    return NormArgs(T, H, yd, rd, nd, gd, codes[0], codes[1], bool(post_norm), layout, gate_act == GATE_SIGMOID, alpha,
+                    beta, w_offset, eps, ys, rs, os_, ns, gs)
 
 
 def moe_ffn_norm_residual(res, y=None, post_norm: bool = False, w_post=None, gate=None, gate_act: int = GATE_LINEAR,
@@ -388,44 +459,23 @@ def moe_ffn_norm_residual(res, y=None, post_norm: bool = False, w_post=None, gat
     ``normed``, the RMSNorm of res_out for the next block (see ``include/moe_ffn.h``).  ``gate``: [H] per channel,
     [T, 1] per token or [T, H].  res_out defaults to ``res`` (in place; not written where ``y`` is None and alpha is
     1), normed to a new tensor of ``norm_dtype`` (bf16).  Returns (res_out, normed)."""
-    import torch
-
-    _require(res.dim() == 2, "res: expected [T, H]")
-    T, H = res.shape
     if res_out is None:
         res_out = res
-    _require(res_out.dtype == res.dtype, "res_out: must have res's dtype")
-    rd = _code(res, "res")
-    rs = _matrix(res, T, H, "res")
-    os_ = _matrix(res_out, T, H, "res_out")
-    yd, ys = (_code(y, "y"), _matrix(y, T, H, "y")) if y is not None else (ACT_F32, H)
-    layout, gd, gs = 0, ACT_F32, H
-    if gate is not None:
-        gd = _code(gate, "gate")
-        if gate.dim() == 1:
-            _whole(gate, (H,), gate.dtype, "gate")
-        elif gate.shape == (T, 1):
-            layout, gs = 1, gate.stride(0) if T > 1 else 1
-        else:
-            layout, gs = 2, _matrix(gate, T, H, "gate")
-    wcode = lambda w, name: ACT_F32 if w is None else _code(w, name, (ACT_F32, ACT_BF16))  # noqa: E731
-    pd, nd = wcode(w_post, "w_post"), wcode(w_pre, "w_pre")
-    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if w is not None:
-            _whole(w, (H,), w.dtype, name)
-    if normed is not None:
-        _require(norm_dtype is None or norm_dtype == normed.dtype, "normed: not of norm_dtype")
-        _code(normed, "normed")
-        _matrix(normed, T, H, "normed")
-    _on_device(res, res=res, y=y, w_post=w_post, gate=gate, w_pre=w_pre, res_out=res_out, normed=normed)
+    key = (1, _sig(res), _sig(y), post_norm, _sig(w_post), _sig(gate), gate_act, alpha, beta, _sig(w_pre), w_offset,
+           eps, _sig(res_out), _sig(normed), norm_dtype)
+    a = _blocks.get(key) or _remember(key, _norm_block(res, y, post_norm, w_post, gate, gate_act, alpha, beta, w_pre,
+                                                       w_offset, eps, res_out, normed, norm_dtype))
     if normed is None:
-        normed = _new(stream, (T, H), norm_dtype or torch.bfloat16, res.device)
-    a = NormArgs(T, H, yd, rd, _code(normed, "normed"), gd, pd, nd, bool(post_norm), layout, gate_act == GATE_SIGMOID,
-                 alpha, beta, w_offset, eps, ys, rs, os_, _matrix(normed, T, H, "normed"), gs)
+        import torch
+
+        normed = _new(stream, (a.T, a.H), norm_dtype or torch.bfloat16, res.device)
     unchanged = y is None and alpha == 1.0 and res_out is res
-    _check(lib().moe_ffn_norm_residual(a, _stream(stream), res.data_ptr(), _ptr(y), _ptr(w_post), _ptr(gate),
-                                       _ptr(w_pre), None if unchanged else res_out.data_ptr(), normed.data_ptr()),
-           "moe_ffn_norm_residual")
+    rc = (_lib or lib()).moe_ffn_norm_residual(
+        a, _raw_stream(stream, res), res.data_ptr(), None if y is None else y.data_ptr(),
+        None if w_post is None else w_post.data_ptr(), None if gate is None else gate.data_ptr(),
+        None if w_pre is None else w_pre.data_ptr(), None if unchanged else res_out.data_ptr(), normed.data_ptr())
+    if rc:
+        _check(rc, "moe_ffn_norm_residual")
     return res_out, normed
 
 
@@ -437,11 +487,7 @@ def moe_ffn_adapters_workspace(T: int, K: int, N: int, R: int) -> int:
     return max(n.value, 256)
 
 
-def moe_ffn_add_adapters(y, x, adapter_ids, a, b, ranks=None, scales=None, out=None, workspace=None, stream=None,
-                         workspace_bytes=None):
-    """``out_t = y_t + scales_i b_i (a_i x_t)`` with i = ``adapter_ids[t]`` (int32 [T]; -1: no adapter).  x [T, K],
-    y [T, N], a [n, R, K], b [n, N, R], ranks int32 [n], scales fp32 [n] (see ``include/moe_ffn.h``).  out defaults to
-    y (in place), the workspace to a new one.  Returns out."""
+def _adapters_block(y, x, adapter_ids, a, b, ranks, scales, out, workspace):
     import torch
 
     _require(x.dim() == 2 and y.dim() == 2 and a.dim() == 3 and b.dim() == 3,
@@ -449,8 +495,6 @@ def moe_ffn_add_adapters(y, x, adapter_ids, a, b, ranks=None, scales=None, out=N
     T, K = x.shape
     n, R = a.shape[:2]
     N = b.shape[1]
-    if out is None:
-        out = y
     xd = _code(x, "x", (ACT_BF16, ACT_F16))
     _whole(a, (n, R, K), x.dtype, "a")
     _whole(b, (n, N, R), x.dtype, "b")
@@ -464,13 +508,31 @@ def moe_ffn_add_adapters(y, x, adapter_ids, a, b, ranks=None, scales=None, out=N
     args = AdaptersArgs(T, K, N, R, n, xd, _code(y, "y"), xs if T > 1 else (K + 7) // 8 * 8, _matrix(y, T, N, "y"),
                         _matrix(out, T, N, "out"))
     _on_device(x, x=x, y=y, adapter_ids=adapter_ids, a=a, b=b, ranks=ranks, scales=scales, out=out,
-               workspace=None if isinstance(workspace, int) else workspace)
+               workspace=workspace)
+    if workspace is not None:
+        _require(workspace.is_contiguous(), "workspace: must be contiguous")
+    return args
+
+
+def moe_ffn_add_adapters(y, x, adapter_ids, a, b, ranks=None, scales=None, out=None, workspace=None, stream=None):
+    """``out_t = y_t + scales_i b_i (a_i x_t)`` with i = ``adapter_ids[t]`` (int32 [T]; -1: no adapter).  x [T, K],
+    y [T, N], a [n, R, K], b [n, N, R], ranks int32 [n], scales fp32 [n] (see ``include/moe_ffn.h``).  out defaults to
+    y (in place), the workspace (a tensor of moe_ffn_adapters_workspace bytes) to a new one.  Returns out."""
+    if out is None:
+        out = y
+    key = (2, _sig(y), _sig(x), _sig(adapter_ids), _sig(a), _sig(b), _sig(ranks), _sig(scales), _sig(out),
+           _sig(workspace))
+    args = _blocks.get(key) or _remember(key, _adapters_block(y, x, adapter_ids, a, b, ranks, scales, out, workspace))
     if workspace is None:
-        workspace = _new(stream, (moe_ffn_adapters_workspace(T, K, N, R),), torch.uint8, x.device)
-    nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
-    _check(lib().moe_ffn_add_adapters(args, _stream(stream), _ptr(workspace), nbytes, x.data_ptr(),
-                                      adapter_ids.data_ptr(), _ptr(a), _ptr(b), _ptr(ranks), _ptr(scales),
-                                      y.data_ptr(), out.data_ptr()), "moe_ffn_add_adapters")
+        import torch
+
+        workspace = _new(stream, (moe_ffn_adapters_workspace(args.T, args.K, args.N, args.R),), torch.uint8, x.device)
+    rc = (_lib or lib()).moe_ffn_add_adapters(
+        args, _raw_stream(stream, x), workspace.data_ptr(), workspace.numel() * workspace.element_size(), x.data_ptr(),
+        adapter_ids.data_ptr(), a.data_ptr(), b.data_ptr(), None if ranks is None else ranks.data_ptr(),
+        None if scales is None else scales.data_ptr(), y.data_ptr(), out.data_ptr())
+    if rc:
+        _check(rc, "moe_ffn_add_adapters")
     return out
 
 
@@ -513,16 +575,21 @@ class MoeFFN:
 
     def routed(self, x, ids, weights, expert_w, shexp_w=None, shexp_gate_w=None, out=None, stream=None):
         """The layer for a given routing (moe_ffn_execute_routed); returns out."""
-        import torch
-
         s = self.shapes
-        _whole(ids, (s.T, s.top_k), torch.int32, "ids")
-        _whole(weights, (s.T, s.top_k), torch.float32, "weights")
-        _on_device(x, x=x, ids=ids, weights=weights)
+        key = (3, s.T, s.H, s.top_k, _sig(ids), _sig(weights), x.get_device())
+        if key not in _blocks:
+            import torch
+
+            _whole(ids, (s.T, s.top_k), torch.int32, "ids")
+            _whole(weights, (s.T, s.top_k), torch.float32, "weights")
+            _on_device(x, x=x, ids=ids, weights=weights)
+            _remember(key, True)
         if out is None:
+            import torch
+
             out = _new(stream, (s.T, s.H), torch.float32, x.device)
         moe_ffn_execute_routed(self.plan, self.workspace, x, ids, weights, expert_w, shexp_w, shexp_gate_w, out,
-                               stream)
+                               _raw_stream(stream, x), self.workspace_bytes)
         return out
 
     def status(self, stream=None) -> int:
