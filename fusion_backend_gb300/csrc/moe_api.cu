@@ -549,7 +549,7 @@ int moe_ffn_route(const moe_ffn_route_args* a, moe_ffn_stream_t stream, const vo
     return MOE_FFN_ERR_MISALIGNED;
   const int rc = check_device();
   if (rc != MOE_FFN_OK) return rc;
-  RouteParams P;
+  RouteParams P = {};
   P.T = a->T;
   P.E = a->E;
   P.K = a->top_k;
@@ -592,7 +592,7 @@ int moe_ffn_norm_residual(const moe_ffn_norm_args* a, moe_ffn_stream_t stream, c
     return MOE_FFN_ERR_MISALIGNED;
   const int rc = check_device();
   if (rc != MOE_FFN_OK) return rc;
-  NormParams P;
+  NormParams P = {};
   P.T = a->T;
   P.H = a->H;
   P.y_dtype = a->y_dtype;
@@ -645,7 +645,7 @@ int moe_ffn_add_adapters(const moe_ffn_adapters_args* a, moe_ffn_stream_t stream
     return MOE_FFN_ERR_MISALIGNED;
   rc = check_device();
   if (rc != MOE_FFN_OK) return rc;
-  AdapterParams P;
+  AdapterParams P = {};
   P.T = a->T;
   P.K = a->K;
   P.N = a->N;

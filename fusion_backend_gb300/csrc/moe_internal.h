@@ -261,6 +261,7 @@ constexpr int kAdapterMaxRank = 128;
 struct RouteParams {
   int T, E, K, G, gs, top_groups;  // gs experts a group
   int sigmoid, top2, renorm, dtype;
+  int lpg, per, vec;  // set by the launch: lanes a group, experts a lane, loads of four experts
   float scale;
   long long stride;
   const void* logits;
@@ -268,7 +269,7 @@ struct RouteParams {
   int32_t* ids;
   float* w;
 };
-cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
+cudaError_t launch_route(RouteParams p, cudaStream_t stream);
 
 struct NormParams {
   int T, H;
@@ -290,9 +291,14 @@ struct AdapterParams {
   const float* scales;
   const void* y;
   void* out;
-  float* v;  // workspace: A_a x of every token
+  // workspace: A_a x of every token, for each part of K; tokens in the order
+  // of their adapters, and per window of tokens its tiles
+  float* v;
+  int32_t *order, *n_tiles;
+  void* tiles;
+  int tile, slots, splits, vec;  // set by the launch: tokens a tile, tiles a window at most, parts of K, loads of four
 };
 size_t adapters_workspace(int T, int K, int N, int R);
-cudaError_t launch_adapters(const AdapterParams& p, cudaStream_t stream);
+cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream);
 
 }  // namespace moe

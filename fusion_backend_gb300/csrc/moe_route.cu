@@ -5,6 +5,18 @@
 // E / G neighbours has LPG = 32 / (G rounded up to a power of two) lanes, each
 // with EPL or fewer consecutive experts, so a lower lane (then a lower slot)
 // is a lower index and a group's value is a reduction over its lanes.
+//
+// The choice is made on fp32 keys: one warp maximum a round (the hardware's
+// reduction over order keys), only the winner's lane looks for its next best.
+// Without a bias the key is the logit itself, since the scores rise with it:
+// the choice is then exact, and scores are formed only where the groups or the
+// weights need them.  With a bias the key is c = s + b in fp32, which is off by
+// less than `slack` (below); where two neighbours in the order of the choice,
+// or the groups on the two sides of the cut, lie closer than that, the warp
+// makes the whole choice again in fp64.  That is one token in some hundreds on
+// logits of a spread of two; fp64 for every token, the first form of this
+// kernel, ran 176 us on 4096 tokens x 256 experts and 536 us on 16381 x 200
+// (the GPU's fp64 rate is a small share of its fp32 rate).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -15,49 +27,70 @@ namespace moe {
 
 namespace {
 
+constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kFltMax = 3.402823466e38f;
+constexpr int kWarps = 4;
 
-MOE_DEV double warp_max(double v) {
+template <typename F>
+MOE_DEV F warp_max(F v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
   return v;
 }
-MOE_DEV double warp_sum(double v) {
+template <typename F>
+MOE_DEV F warp_sum(F v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
+MOE_DEV float key_float(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+// NaN: masked; +inf: the largest number
+MOE_DEV float clean(float v) { return v != v ? -INFINITY : fminf(v, kFltMax); }
 
-// (c, l, e) before (c2, l2, e2) in the order of the choice
-MOE_DEV bool before(double c, float l, int e, double c2, float l2, int e2) {
-  return c > c2 || (c == c2 && (l > l2 || (l == l2 && e < e2)));
-}
+struct Owned {
+  int lpg, grp, n, e0;  // lanes a group, the lane's group, its experts e0 .. e0 + n - 1
+};
 
-template <int EPL>
-__global__ void __launch_bounds__(128) k_route(const __grid_constant__ RouteParams P) {
-  const int lane = threadIdx.x & 31, t = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (t >= P.T) return;
-  int lpg = 32;
-  for (int g = 1; g < P.G; g <<= 1) lpg >>= 1;
-  const int per = (P.gs + lpg - 1) / lpg;  // experts a lane, <= EPL
-  const int grp = lane / lpg, first = (lane % lpg) * per;
-  const int n = grp < P.G ? max(0, min(per, P.gs - first)) : 0;
-  const int e0 = grp * P.gs + first;
-
-  float l[EPL];
-  double c[EPL];
+// The lane's two largest c and, after the reduction, its group's: the group's
+// value on each of its lanes, -inf where the group has nothing left.
+template <int EPL, typename F>
+MOE_DEV F group_value(const F (&c)[EPL], int lpg, bool top2) {
+  F a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    float v = -INFINITY;
-    if (i < n) v = elem_load(P.logits, P.dtype, (size_t)t * P.stride + e0 + i);
-    l[i] = v != v ? -INFINITY : fminf(v, kFltMax);
+    a2 = fmax(a2, fmin(a1, c[i]));
+    a1 = fmax(a1, c[i]);
   }
-  // c: -inf where the expert cannot be chosen
-  double m = -INFINITY;
+  for (int o = lpg >> 1; o; o >>= 1) {
+    const F b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
+    a2 = fmax(fmax(a2, b2), fmin(a1, b1));
+    a1 = fmax(a1, b1);
+  }
+  return top2 && a2 != -INFINITY ? a1 + a2 : a1;
+}
+
+// The lane's group's place among the G group values (equal: the lower group).
+template <typename F>
+MOE_DEV int group_rank(F val, int G, const Owned& o) {
+  int rank = 0;
+  for (int g = 0; g < G; ++g) {
+    const F v = __shfl_sync(kAll, val, g * o.lpg);
+    rank += v > val || (v == val && g < o.grp);
+  }
+  return rank;
+}
+
+// The choice in fp64 (bias present, or groups by two largest): lane j gets the
+// j-th expert and its logit.
+template <int EPL>
+MOE_DEV void choose_exact(const RouteParams& P, const float (&l)[EPL], const float (&b)[EPL], const Owned& o, int& id,
+                          float& lj) {
+  const int lane = threadIdx.x & 31;
+  double c[EPL];
+  double m = -INFINITY, z = 0.0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) m = fmax(m, (double)l[i]);
   m = warp_max(m);
-  double z = 0.0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     c[i] = 0.0;
@@ -68,106 +101,249 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     if (!P.sigmoid && z > 0.0) c[i] /= z;
-    float b = P.bias && i < n ? P.bias[e0 + i] : 0.f;
-    b = b != b ? -INFINITY : fminf(b, kFltMax);
-    c[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : c[i] + (double)b;
+    c[i] = l[i] == -INFINITY || b[i] == -INFINITY ? -INFINITY : c[i] + (double)b[i];
   }
-  // groups: value of the lane's group on each of its lanes
-  if (P.G > 1) {
-    double a1 = -INFINITY, a2 = -INFINITY;
+  if (P.G > 1 && group_rank(group_value(c, o.lpg, P.top2), P.G, o) >= P.top_groups) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      a2 = fmax(a2, fmin(a1, c[i]));
-      a1 = fmax(a1, c[i]);
-    }
-    for (int o = lpg >> 1; o; o >>= 1) {
-      const double b1 = __shfl_xor_sync(0xffffffffu, a1, o), b2 = __shfl_xor_sync(0xffffffffu, a2, o);
-      a2 = fmax(fmax(a2, b2), fmin(a1, b1));
-      a1 = fmax(a1, b1);
-    }
-    const double val = P.top2 && a2 != -INFINITY ? a1 + a2 : a1;
-    int rank = 0;  // groups before this one
-    for (int g = 0; g < P.G; ++g) {
-      const double o = __shfl_sync(0xffffffffu, val, g * lpg);
-      rank += o > val || (o == val && g < grp);
-    }
-    if (rank >= P.top_groups) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) c[i] = -INFINITY;
-    }
+    for (int i = 0; i < EPL; ++i) c[i] = -INFINITY;
   }
-  // the choice, one expert a round; lane j keeps the j-th
-  int my_id = -1;
-  float my_l = -INFINITY;
+  id = -1;
+  lj = -INFINITY;
   for (int j = 0; j < P.K; ++j) {
     double bc = -INFINITY;
     float bl = -INFINITY;
     int be = 1 << 30;
+    // c, then the logit, then the lower index
+    auto take = [&](double c2, float l2, int e2) {
+      if (c2 > bc || (c2 == bc && (l2 > bl || (l2 == bl && e2 < be)))) {
+        bc = c2;
+        bl = l2;
+        be = e2;
+      }
+    };
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (c[i] != -INFINITY && before(c[i], l[i], e0 + i, bc, bl, be)) {
-        bc = c[i];
-        bl = l[i];
-        be = e0 + i;
-      }
+      if (c[i] != -INFINITY) take(c[i], l[i], o.e0 + i);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const double oc = __shfl_xor_sync(0xffffffffu, bc, o);
-      const float ol = __shfl_xor_sync(0xffffffffu, bl, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (before(oc, ol, oe, bc, bl, be)) {
-        bc = oc;
-        bl = ol;
-        be = oe;
-      }
-    }
+    for (int d = 16; d; d >>= 1)
+      take(__shfl_xor_sync(kAll, bc, d), __shfl_xor_sync(kAll, bl, d), __shfl_xor_sync(kAll, be, d));
     if (bc == -INFINITY) break;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (e0 + i == be && i < n) c[i] = -INFINITY;
+      if (o.e0 + i == be && i < o.n) c[i] = -INFINITY;
     if (lane == j) {
-      my_id = be;
-      my_l = bl;
+      id = be;
+      lj = bl;
     }
   }
-  // weights from the chosen logits.  Renormalised, the softmax needs no other
-  // logit, and the sigmoid is exp(l) to below fp64's resolution where every
-  // chosen logit is far below 0 (the ratio is then formed before it can
-  // underflow).
-  double v = 0.0;
-  const double top = warp_max((double)my_l);
-  if (my_id >= 0) {
-    if (P.renorm && (!P.sigmoid || top < -60.0))
-      v = exp((double)my_l - top);
-    else
-      v = P.sigmoid ? 1.0 / (1.0 + exp(-(double)my_l)) : exp((double)my_l - m) / z;
+}
+
+template <int EPL>
+__global__ void __launch_bounds__(32 * kWarps) k_route(const __grid_constant__ RouteParams P) {
+  const int lane = threadIdx.x & 31, t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Owned o;
+  o.lpg = P.lpg;
+  o.grp = lane / P.lpg;
+  const int first = (lane - o.grp * P.lpg) * P.per;
+  o.n = o.grp < P.G ? max(0, min(P.per, P.gs - first)) : 0;
+  o.e0 = o.grp * P.gs + first;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (t >= P.T) return;
+
+  float l[EPL], b[EPL], c[EPL];
+  const size_t row = (size_t)t * P.stride + o.e0;
+  if (EPL >= 4 && P.vec) {
+#pragma unroll
+    for (int i = 0; i + 4 <= EPL; i += 4) {
+      l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
+      if (i < o.n) {
+        if (P.dtype == kF32) {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(P.logits) + row + i);
+          l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.logits) + row + i);
+          if (P.dtype == kBf16) {
+            l[i] = bf16_lo(v.x), l[i + 1] = bf16_hi(v.x), l[i + 2] = bf16_lo(v.y), l[i + 3] = bf16_hi(v.y);
+          } else {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+            l[i] = p.x, l[i + 1] = p.y, l[i + 2] = q.x, l[i + 3] = q.y;
+          }
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = i < o.n ? elem_load(P.logits, P.dtype, row + i) : -INFINITY;
   }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    l[i] = clean(l[i]);
+    b[i] = P.bias && i < o.n ? clean(P.bias[o.e0 + i]) : 0.f;
+  }
+  // c in fp32 (the logit where the choice can go by it), the softmax's sum
+  const bool biased = P.bias != nullptr;
+  const bool scored = biased || (P.G > 1 && P.top2);   // c holds scores
+  float m = 0.f, z = 1.f, smax = 1.f;
+  if (!P.sigmoid && (scored || !P.renorm)) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+    m = key_float(__reduce_max_sync(kAll, float_order_key(m)));
+    z = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      c[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+      z += c[i];
+    }
+    z = warp_sum(z);
+    smax = 1.f / z;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    if (!scored)
+      c[i] = l[i];
+    else if (l[i] == -INFINITY || b[i] == -INFINITY)
+      c[i] = -INFINITY;
+    else
+      c[i] = (P.sigmoid ? __fdividef(1.f, 1.f + expf(-l[i])) : c[i] * smax) + b[i];
+  }
+  // How far apart two fp32 values of c have to be for their order to be that of
+  // fp64.  Sigmoid: exp, sum and quotient are off by less than 2^-21 of s <= 1
+  // together.  Softmax: the exponent's argument rounds by |x| 2^-24 (and
+  // exp(-|x|) |x| < 1), exp, the sum of EPL terms a lane and 5 levels, the
+  // reciprocal and the product: less than 2^-17 of the largest s.  Both sides of
+  // a comparison count, and the rounding of s + b: 2^-24 |c| each.
+  auto slack = [&](float v) { return smax * (P.sigmoid ? 0x1p-20f : 0x1p-16f) + fabsf(v) * 0x1p-22f + 0x1p-120f; };
+  bool unsure = false;
+  if (P.G > 1) {
+    const float val = group_value(c, P.lpg, P.top2);
+    const int rank = group_rank(val, P.G, o);
+    if (scored) {
+      // the last group kept and the first one left out
+      const uint32_t in = __ballot_sync(kAll, o.grp < P.G && rank == P.top_groups - 1);
+      const uint32_t out = __ballot_sync(kAll, o.grp < P.G && rank == P.top_groups);
+      const float vi = __shfl_sync(kAll, val, __ffs(in) - 1), vo = __shfl_sync(kAll, val, __ffs(out) - 1);
+      unsure = vo != -INFINITY && vi - vo <= 2.f * slack(vi);
+    }
+    if (!scored || biased) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = rank < P.top_groups ? c[i] : -INFINITY;
+    } else {  // no bias: the choice inside the groups goes by the logits
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = rank < P.top_groups ? l[i] : -INFINITY;
+    }
+  }
+  // The choice.  Every lane holds the order key of its best expert (0: none).
+  uint32_t key[EPL], best = 0u;
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    key[i] = c[i] == -INFINITY ? 0u : float_order_key(c[i]);
+    if (key[i] > best) {
+      best = key[i];
+      at = i;
+    }
+  }
+  int id = -1;
+  float lj = -INFINITY;
+  float c_last = 0.f, c_cut = 0.f, l_last = 0.f;
+  int e_last = 0;
+  if (!unsure) {
+    // with a bias, rounds go on behind the last choice until one is clearly
+    // below it (a run of more than 8 near ones is left to fp64)
+    for (int j = 0; j < P.K + (biased ? 9 : 0); ++j) {
+      const uint32_t top = __reduce_max_sync(kAll, best);
+      if (top == 0u) break;
+      const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
+      const int e = __shfl_sync(kAll, o.e0 + at, src);
+      const float cj = key_float(top);
+      float lw = cj;
+      if (biased) {
+        float la = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) la = at == i ? l[i] : la;
+        lw = __shfl_sync(kAll, la, src);
+        if (j >= P.K && c_cut - cj > slack(c_cut)) break;
+        if (j == P.K + 8) {
+          unsure = true;
+          break;
+        }
+        if (j > 0 && c_last - cj <= slack(c_last)) {
+          // too near to tell in fp32, unless the biases are the same: then the
+          // logits decide, or for equal ones the index
+          const float bl = clean(P.bias[e_last]), be = clean(P.bias[e]);
+          if (!(bl == be && (l_last > lw || (l_last == lw && e_last < e)))) {
+            unsure = true;
+            break;
+          }
+        }
+        c_last = cj;
+        l_last = lw;
+        e_last = e;
+        if (j == P.K - 1) c_cut = cj;
+      }
+      if (lane == j && j < P.K) {
+        id = e;
+        lj = lw;
+      }
+      if (lane == src) {
+        best = 0u;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (i == at) key[i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (key[i] > best) {
+            best = key[i];
+            at = i;
+          }
+      }
+    }
+  }
+  if (unsure) choose_exact(P, l, b, o, id, lj);
+
+  // Weights from the chosen logits.  Renormalised, the softmax needs no other
+  // logit, and the sigmoid is exp(l) to fp32's resolution where every chosen
+  // logit is far below 0 (the ratio is then formed before it can underflow).
+  float v = 0.f;
   if (P.renorm) {
-    const double total = warp_sum(v);
-    if (total > 0.0) v /= total;
+    const float top = warp_max(lj);
+    if (id >= 0) v = !P.sigmoid || top < -60.f ? expf(lj - top) : 1.f / (1.f + expf(-lj));
+    const float total = warp_sum(v);
+    if (id >= 0) v = v / total;
+  } else if (id >= 0) {
+    v = P.sigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - m) / z;
   }
   if (lane < P.K) {
-    P.ids[(size_t)t * P.K + lane] = my_id;
-    P.w[(size_t)t * P.K + lane] = (float)(v * (double)P.scale);
+    P.ids[(size_t)t * P.K + lane] = id;
+    P.w[(size_t)t * P.K + lane] = v * P.scale;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
-  int lpg = 32;
-  for (int g = 1; g < p.G; g <<= 1) lpg >>= 1;
-  const int per = (p.gs + lpg - 1) / lpg;
-  const dim3 grid((p.T + 3) / 4);
-  if (per <= 4)
-    k_route<4><<<grid, 128, 0, stream>>>(p);
-  else if (per <= 8)
-    k_route<8><<<grid, 128, 0, stream>>>(p);
-  else if (per <= 32)
-    k_route<32><<<grid, 128, 0, stream>>>(p);
-  else
-    k_route<64><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_route(RouteParams p, cudaStream_t stream) {
+  p.lpg = 32;
+  for (int g = 1; g < p.G; g <<= 1) p.lpg >>= 1;
+  p.per = (p.gs + p.lpg - 1) / p.lpg;
+  // four experts a load: rows, groups and lanes start on a load's boundary
+  if (p.per > 2) {
+    const int per4 = (p.per + 3) & ~3;
+    const uintptr_t bytes = p.dtype == kF32 ? 16 : 8;
+    p.vec = p.gs % 4 == 0 && p.stride % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % bytes == 0;
+    if (p.vec) p.per = per4;
+  }
+  const dim3 grid((p.T + kWarps - 1) / kWarps);
+  const int threads = 32 * kWarps;
+  if (p.per <= 2) return launch_behind(k_route<2>, grid, threads, 0, stream, p);
+  if (p.per <= 4) return launch_behind(k_route<4>, grid, threads, 0, stream, p);
+  if (p.per <= 8) return launch_behind(k_route<8>, grid, threads, 0, stream, p);
+  if (p.per <= 16) return launch_behind(k_route<16>, grid, threads, 0, stream, p);
+  if (p.per <= 32) return launch_behind(k_route<32>, grid, threads, 0, stream, p);
+  return launch_behind(k_route<64>, grid, threads, 0, stream, p);
 }
 
 }  // namespace moe
