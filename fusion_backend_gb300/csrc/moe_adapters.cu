@@ -12,8 +12,11 @@
 // give, so the tiles need no shared-memory staging or tensor memory.
 //
 // Tiles.  Up to kScanT tokens: block t looks through all adapter ids and owns a
-// tile if its token is the first, 33rd, .. of its adapter.  More tokens: k_order
-// sorts each window of kWindow tokens by adapter and lists the tiles.
+// tile if its token is the first, (8 NT + 1)th, .. of its adapter.  More tokens:
+// k_order ranks the tokens of each window of kWindow by adapter (counting, all
+// against all, spread over 32 blocks; a bitonic sort of the window in one block
+// took 12 us) and marks the places where a tile starts; block s of a window then
+// finds the s-th mark.
 //
 // K is split over the warps of a block and, where there are few tiles, over
 // blocks; the parts are summed in a fixed order.
@@ -29,13 +32,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kScanT = 2 * kThreads;  // two ids a thread
-constexpr int kWindow = 1024, kWindowLog = 10;
+constexpr int kScanT = 64;            // two ids a lane
+constexpr int kWindow = 1024;
+constexpr int kOrderTokens = 32;      // tokens a block of k_order ranks, eight threads a token
 constexpr int kRankChunk = 64;        // rows of A a block of k_shrink takes
-
-struct TileEntry {
-  int adapter, start, n;  // -1: tokens without an adapter; order[start .. start + n)
-};
 
 MOE_DEV int adapter_of(const AdapterParams& P, int t) {
   const int a = P.ids[t];
@@ -60,142 +60,129 @@ MOE_DEV void mma16816(bool f16, float* d, uint32_t a0, uint32_t a1, uint32_t a2,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Sorts the window's tokens by (adapter, token) and lists its tiles: runs of
-// one adapter cut every `tile` tokens.
-__global__ void __launch_bounds__(kWindow / 2) k_order(const __grid_constant__ AdapterParams P) {
-  __shared__ unsigned long long key[kWindow];
-  __shared__ int s_warp[kWindow / 64];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Places of the window's tokens in the order (adapter, token): a token's place
+// is the number of tokens before it.  Eight threads a token, each against an
+// eighth of the window.  marks[place]: the tokens of the tile that starts
+// there, 0 where none does (a run of one adapter is cut every P.tile tokens).
+__global__ void __launch_bounds__(8 * kOrderTokens) k_order(const __grid_constant__ AdapterParams P) {
+  __shared__ __align__(16) int s_a[kWindow];
+  const int tid = threadIdx.x, part = tid & 7;
   const int t0 = blockIdx.x * kWindow, n = min(kWindow, P.T - t0);
+  const int i = blockIdx.y * kOrderTokens + (tid >> 3);
   pdl_wait();
   pdl_launch_dependents();
-  for (int i = tid; i < kWindow; i += kWindow / 2)
-    key[i] = i < n ? ((unsigned long long)(uint32_t)(adapter_of(P, t0 + i) + 1) << kWindowLog) | i : ~0ull;
-  // bitonic sort; thread i compares the pair that its index spells with a 0
-  // put in at bit j's place
-  for (int k = 2; k <= kWindow; k <<= 1)
-    for (int j = k >> 1; j; j >>= 1) {
-      __syncthreads();
-      const int a = ((tid & ~(j - 1)) << 1) | (tid & (j - 1)), b = a | j;
-      const unsigned long long x = key[a], y = key[b];
-      if ((x > y) == ((a & k) == 0)) {
-        key[a] = y;
-        key[b] = x;
-      }
+  // (no adapter comes first; past the window nothing is counted)
+  for (int j = tid; j < kWindow; j += 8 * kOrderTokens) s_a[j] = j < n ? adapter_of(P, t0 + j) : 0x7FFFFFFF;
+  __syncthreads();
+  const int a = s_a[i];
+  int before = 0, same_before = 0, same = 0;
+#pragma unroll 4
+  for (int j0 = 4 * part; j0 < n; j0 += 32) {
+    const int4 v = *reinterpret_cast<const int4*>(s_a + j0);
+    const int o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      before += o[e] < a;
+      same += o[e] == a;
+      same_before += o[e] == a && j0 + e < i;
     }
-  __syncthreads();
-  // places 2 tid and 2 tid + 1: the start of their run (a running maximum),
-  // then whether a tile starts there (a running sum)
-  auto adapter_at = [&](int i) { return (uint32_t)(key[i] >> kWindowLog); };
-  int start[2], m = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = 2 * tid + i;
-    if (p > 0 && p < n && adapter_at(p) != adapter_at(p - 1)) m = p;
-    start[i] = m;
   }
-  int run = m;
+  before += same_before;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run = max(run, v);
+  for (int o = 1; o < 8; o <<= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    same += __shfl_xor_sync(0xffffffffu, same, o);
+    same_before += __shfl_xor_sync(0xffffffffu, same_before, o);
   }
-  if (lane == 31) s_warp[warp] = run;
-  int before = __shfl_up_sync(0xffffffffu, run, 1);
-  if (lane == 0) before = 0;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) before = max(before, s_warp[w]);
-  __syncthreads();
-  bool lead[2];
-  int cnt = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = 2 * tid + i;
-    start[i] = max(start[i], before);
-    lead[i] = p < n && (p - start[i]) % P.tile == 0;
-    cnt += lead[i];
+  if (part == 0 && i < n) {
+    P.order[t0 + before] = t0 + i;
+    P.adapter_at[t0 + before] = a;
+    P.marks[t0 + before] = static_cast<uint8_t>(same_before % P.tile ? 0 : min(P.tile, same - same_before));
   }
-  int incl = cnt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  int at = incl - cnt;
-  for (int w = 0; w < warp; ++w) at += s_warp[w];
-  TileEntry* tiles = reinterpret_cast<TileEntry*>(P.tiles) + (size_t)blockIdx.x * kWindow;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = 2 * tid + i;
-    if (lead[i]) {
-      int c = 1;
-      while (c < P.tile && p + c < n && adapter_at(p + c) == adapter_at(p)) ++c;
-      tiles[at++] = TileEntry{(int)adapter_at(p) - 1, t0 + p, c};
-    }
-    if (p < n) P.order[t0 + p] = t0 + (int)(key[p] & (kWindow - 1));
-  }
-  if (tid == kWindow / 2 - 1) P.n_tiles[blockIdx.x] = at;
 }
 
 // The tile of this block (blockIdx.x): its adapter (-1: none), its tokens in
 // `list`; false where the block has no tile.
 template <int TILE>
 MOE_DEV bool find_tile(const AdapterParams& P, int* list, int& a, int& n) {
-  __shared__ int s_cnt[2][kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (P.T > kScanT) {
-    const int w = blockIdx.x / P.slots, s = blockIdx.x - w * P.slots;
-    if (s >= P.n_tiles[w]) return false;
-    const TileEntry e = reinterpret_cast<const TileEntry*>(P.tiles)[(size_t)w * kWindow + s];
-    a = e.adapter;
-    n = e.n;
-    if (tid < n) list[tid] = P.order[e.start + tid];
-    __syncthreads();
-    return true;
-  }
-  const int t = blockIdx.x;
-  a = adapter_of(P, t);
-  int before = 0, cnt = 0;
-  bool hit[2];
+  __shared__ int s_tile[2];  // adapter, tokens
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    n = 0;
+    a = -1;
+    if (P.T > kScanT) {
+      // the s-th mark of window w: 32 marks a lane
+      const int w = blockIdx.x / P.slots, s = blockIdx.x - w * P.slots;
+      const int t0 = w * kWindow, len = min(kWindow, P.T - t0);
+      uint32_t m[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int j = 2 * tid + i;
-    const bool same = j < P.T && adapter_of(P, j) == a;
-    hit[i] = same && j >= t;
-    before += same && j < t;
-    cnt += hit[i];
-  }
-  int incl = cnt;
+      for (int i = 0; i < 8; i += 4) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const int at = 32 * lane + 4 * i;
+        if (at < len) v = *reinterpret_cast<const uint4*>(P.marks + t0 + at);  // (marks are padded to 16 bytes)
+        m[i] = v.x, m[i + 1] = v.y, m[i + 2] = v.z, m[i + 3] = v.w;
+      }
+      int c = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  if (lane == 31) {
-    s_cnt[0][warp] = before;
-    s_cnt[1][warp] = incl;
-  }
-  __syncthreads();
-  int rank = 0, at = incl - cnt, total = 0;
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    rank += s_cnt[0][w];
-    at += w < warp ? s_cnt[1][w] : 0;
-    total += s_cnt[1][w];
-  }
-  if (rank % TILE) return false;
+        for (int e = 0; e < 4; ++e) {
+          const int at = 32 * lane + 4 * i + e;
+          if (at >= len) m[i] &= ~(0xFFu << (8 * e));
+          c += (m[i] >> (8 * e) & 0xFFu) != 0u;
+        }
+      int incl = c;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (hit[i]) {
-      if (at < TILE) list[at] = 2 * tid + i;
-      ++at;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      int skip = s - (incl - c), place = 0;  // the lane's mark of that number
+      if (skip >= 0 && skip < c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int v = m[i] >> (8 * e) & 0xFFu;
+            if (v && skip-- == 0) {
+              n = v;
+              place = t0 + 32 * lane + 4 * i + e;
+            }
+          }
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, n > 0);
+      if (who) {
+        n = __shfl_sync(0xffffffffu, n, __ffs(who) - 1);
+        place = __shfl_sync(0xffffffffu, place, __ffs(who) - 1);
+        if (lane < n) list[lane] = P.order[place + lane];
+        a = P.adapter_at[place];
+      }
+    } else {
+      const int t = blockIdx.x;
+      a = adapter_of(P, t);
+      // tokens of the adapter, as bits
+      const uint32_t lo = __ballot_sync(0xffffffffu, lane < P.T && adapter_of(P, min(lane, P.T - 1)) == a);
+      const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < P.T && adapter_of(P, min(lane + 32, P.T - 1)) == a);
+      const unsigned long long all = (unsigned long long)hi << 32 | lo;
+      if (__popcll(all & ((1ull << t) - 1)) % TILE == 0) {
+        const unsigned long long rest = all & ~((1ull << t) - 1);
+        n = min(TILE, __popcll(rest));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = lane + 32 * i, at = __popcll(rest & ((1ull << j) - 1));
+          if ((rest >> j & 1ull) && at < TILE) list[at] = j;
+        }
+      }
     }
-  n = min(TILE, total);
+    if (lane == 0) {
+      s_tile[0] = a;
+      s_tile[1] = n;
+    }
+  }
   __syncthreads();
-  return true;
+  a = s_tile[0];
+  n = s_tile[1];
+  return n > 0;
 }
 
 // Blocks (tile, part of K, 64 rows of A).  The warps take 32-column blocks of K
@@ -272,14 +259,20 @@ __global__ void __launch_bounds__(kThreads) k_shrink(const __grid_constant__ Ada
   }
 }
 
-// Blocks (tile, 256 columns); warp w columns 32 w .. of them, two 16-row tiles
-// of B whose rows are dealt so that a lane ends with four neighbouring columns
-// n0 + 4g .. + 3 of tokens 2q and 2q + 1.  v enters as two numbers of the
-// operands' type (bf16: hi + lo, 16 bits and more of v; fp16: 22 bits, scaled
-// by a power of two to a largest element near 1, since v may pass fp16's
-// range).  y, the ids and the adapter are read ahead of the wait on k_shrink.
-template <bool F16, int NT>
-__global__ void __launch_bounds__(kThreads) k_expand(const __grid_constant__ AdapterParams P) {
+// Blocks (tile, columns): the block goes through its columns 256 at a time, warp
+// w taking 32 w .. of them as two 16-row tiles of B, whose rows are dealt so
+// that a lane ends with four neighbouring columns n0 + 4g .. + 3 of tokens 2q
+// and 2q + 1.  The loads of y and of B (ST 16-wide steps of the rank at once) go
+// out together, and no warp waits for another between them: one memory latency
+// a round, covered by the other warps.  v enters as two numbers of the operands'
+// type (bf16: hi + lo, 16 bits and more of v; fp16: 22 bits, scaled by a power
+// of two to a largest element near 1, since v may pass fp16's range).  The ids,
+// the order and the first y are read ahead of the wait on k_shrink.
+//
+// YK: y and out are fp32 (0) or 16-bit (1) in rows that allow accesses of four
+// elements, or anything (2).
+template <bool F16, int NT, int ST, int YK>
+__global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ AdapterParams P) {
   constexpr int TILE = 8 * NT;
   extern __shared__ uint32_t vs[];  // [2][TILE][pitch / 2]: hi, then lo; pitch in elements
   __shared__ int list[TILE];
@@ -291,59 +284,60 @@ __global__ void __launch_bounds__(kThreads) k_expand(const __grid_constant__ Ada
     pdl_launch_dependents();
     return;
   }
-  const int rank = adapter_rank(P, a), steps = (rank + 15) / 16;
+  const int rank = adapter_rank(P, a);
   const int Rp = (P.R + 15) & ~15;
   const int pitch = (Rp / 16) & 1 ? Rp : Rp + 16;  // 32 (mod 64) bytes a row: no bank conflicts
-  const int n0 = 256 * blockIdx.y + 32 * warp + 4 * g;
-  // y of the lane's columns and tokens
-  float acc[NT][2][4];
+  const int c_end = min(P.N, (int)(blockIdx.y + 1) * P.cols);
+  int n0 = P.cols * blockIdx.y + 32 * warp + 4 * g;
+  int row[NT][2];  // the lane's tokens, -1: none
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 8 * j + 2 * q + h;
+    for (int h = 0; h < 2; ++h) row[j][h] = 8 * j + 2 * q + h < n ? list[8 * j + 2 * q + h] : -1;
+  float acc[NT][2][4];
+  auto load_y = [&]() {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[j][h][c] = 0.f;
-      if (i >= n) continue;
-      const size_t at = (size_t)list[i] * P.y_stride + n0;
-      if (P.vec) {
-        if (n0 < P.N) {
-          if (P.y_dtype == kF32) {
-            const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(P.y) + at);
-            acc[j][h][0] = f.x, acc[j][h][1] = f.y, acc[j][h][2] = f.z, acc[j][h][3] = f.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.y) + at);
-            unpack2(P.y_dtype, u.x, acc[j][h][0], acc[j][h][1]);
-            unpack2(P.y_dtype, u.y, acc[j][h][2], acc[j][h][3]);
-          }
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[j][h][c] = 0.f;
+        if (row[j][h] < 0 || n0 >= c_end) continue;
+        const size_t at = (size_t)row[j][h] * P.y_stride + n0;
+        if (YK == 0) {
+          const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(P.y) + at);
+          acc[j][h][0] = f.x, acc[j][h][1] = f.y, acc[j][h][2] = f.z, acc[j][h][3] = f.w;
+        } else if (YK == 1) {
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.y) + at);
+          unpack2(P.y_dtype, u.x, acc[j][h][0], acc[j][h][1]);
+          unpack2(P.y_dtype, u.y, acc[j][h][2], acc[j][h][3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (n0 + c < c_end) acc[j][h][c] = elem_load(P.y, P.y_dtype, at + c);
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n0 + c < P.N) acc[j][h][c] = elem_load(P.y, P.y_dtype, at + c);
       }
-    }
+  };
+  load_y();
   pdl_wait();
   pdl_launch_dependents();
+  if (rank == 0 && P.out == P.y) return;
   if (rank > 0) {
     // v of the tile: 256 / TILE threads a token
     constexpr int TPT = kThreads / TILE;
-    const int tok = tid / TPT, part = tid % TPT;
+    const int tok = tid / TPT, part = tid % TPT, padded = (rank + 15) & ~15;
     float top = 0.f;
     uint16_t* hi = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
     uint16_t* lo = hi + TILE * pitch;
-    auto v_of = [&](int r) {
-      float s = 0.f;
-      if (tok < n && r < rank)
-        for (int k = 0; k < P.splits; ++k) s += __ldcg(P.v + ((size_t)k * P.T + list[tok]) * P.R + r);
-      return s;
-    };
     float keep[kAdapterMaxRank / TPT];
 #pragma unroll
     for (int i = 0; i < kAdapterMaxRank / TPT; ++i) {
       const int r = part + TPT * i;
-      if (r >= 16 * steps) break;
-      keep[i] = v_of(r);
+      keep[i] = 0.f;
+      if (tok < n && r < rank) {
+        const float* v = P.v + (size_t)list[tok] * P.R + r;
+        for (int k = 0; k < P.splits; ++k) keep[i] += __ldcg(v + (size_t)k * P.T * P.R);
+      }
       top = fmaxf(top, fabsf(keep[i]));
     }
     float up = 1.f, down = 1.f;
@@ -360,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) k_expand(const __grid_constant__ Ada
 #pragma unroll
     for (int i = 0; i < kAdapterMaxRank / TPT; ++i) {
       const int r = part + TPT * i;
-      if (r >= 16 * steps) break;
+      if (r >= padded) break;
       const float v = keep[i] * down;
       const uint32_t h = pack2(F16 ? kF16 : kBf16, v, 0.f);
       float vh, none;
@@ -370,77 +364,94 @@ __global__ void __launch_bounds__(kThreads) k_expand(const __grid_constant__ Ada
     }
     if (part == 0) s_scale[tok] = up * (P.scales ? P.scales[a] : 1.f);
     __syncthreads();
-
-    float d[2][NT][4];
+  }
+  for (int c0 = P.cols * blockIdx.y; c0 < c_end; c0 += kThreads, n0 += kThreads) {
+    if (c0 > P.cols * (int)blockIdx.y) load_y();
+    if (rank > 0) {
+      float d[2][NT][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
-    const uint16_t* br = P.B + ((size_t)a * P.N + n0) * P.R;
-    for (int s = 0; s < steps; ++s) {
-      const int r = 16 * s + 4 * q;  // the lane's four k of the step
-      uint2 bv[4];
+        for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
+      const uint16_t* br = P.B + ((size_t)a * P.N + n0) * P.R;
+      for (int s0 = 0; 16 * s0 < rank; s0 += ST) {
+        uint2 bv[ST][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        bv[c] = make_uint2(0u, 0u);
-        if (n0 + c >= P.N || r >= rank) continue;
-        const uint16_t* row = br + (size_t)c * P.R + r;
-        if (P.R % 4 == 0) {
-          bv[c] = *reinterpret_cast<const uint2*>(row);
-          if (r + 4 > rank) {
-            if (r + 1 >= rank) bv[c].x &= 0xFFFFu;
-            bv[c].y = r + 2 >= rank ? 0u : bv[c].y & 0xFFFFu;
+        for (int s = 0; s < ST; ++s) {
+          const int r = 16 * (s0 + s) + 4 * q;  // the lane's four k of the step
+#pragma unroll
+          for (int c = 0; c < 4; ++c) bv[s][c] = make_uint2(0u, 0u);
+          if (r >= rank) continue;
+          if (P.R % 4 == 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (n0 + c < c_end) bv[s][c] = *reinterpret_cast<const uint2*>(br + (size_t)c * P.R + r);
+            if (r + 4 > rank) {  // what lies past the rank does not count
+              const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 2 < rank ? 0xFFFFu : 0u;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                bv[s][c].x &= mx;
+                bv[s][c].y &= my;
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < min(4, rank - r); ++e)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t v = n0 + c < c_end ? (uint32_t)br[(size_t)c * P.R + r + e] << 16 * (e & 1) : 0u;
+                if (e < 2)
+                  bv[s][c].x |= v;
+                else
+                  bv[s][c].y |= v;
+              }
           }
-        } else {
-          bv[c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
-          bv[c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
+        }
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+          if (16 * (s0 + s) >= rank) break;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (8 * j >= n) continue;
+            const uint16_t* vp = reinterpret_cast<const uint16_t*>(vs) + (8 * j + g) * pitch + 16 * (s0 + s) + 4 * q;
+            const uint2 vh = *reinterpret_cast<const uint2*>(vp), vl = *reinterpret_cast<const uint2*>(vp + TILE * pitch);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint2 b0 = bv[s][2 * i], b1 = bv[s][2 * i + 1];
+              mma16816(F16, d[i][j], b0.x, b1.x, b0.y, b1.y, vl.x, vl.y);
+              mma16816(F16, d[i][j], b0.x, b1.x, b0.y, b1.y, vh.x, vh.y);
+            }
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (8 * j >= n) continue;
-        const uint16_t* vp = reinterpret_cast<const uint16_t*>(vs) + (8 * j + g) * pitch + r;
-        const uint2 vh = *reinterpret_cast<const uint2*>(vp), vl = *reinterpret_cast<const uint2*>(vp + TILE * pitch);
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma16816(F16, d[i][j], bv[2 * i].x, bv[2 * i + 1].x, bv[2 * i].y, bv[2 * i + 1].y, vl.x, vl.y);
-          mma16816(F16, d[i][j], bv[2 * i].x, bv[2 * i + 1].x, bv[2 * i].y, bv[2 * i + 1].y, vh.x, vh.y);
+        for (int h = 0; h < 2; ++h) {
+          const float s = s_scale[8 * j + 2 * q + h];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[j][h][c] = fmaf(s, d[c >> 1][j][2 * (c & 1) + h], acc[j][h][c]);
         }
-      }
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float s = s_scale[8 * j + 2 * q + h];
+        if (row[j][h] < 0 || n0 >= c_end) continue;
+        const size_t at = (size_t)row[j][h] * P.out_stride + n0;
+        const float* v = acc[j][h];
+        if (YK == 0) {
+          *reinterpret_cast<float4*>(static_cast<float*>(P.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else if (YK == 1) {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at) =
+              make_uint2(pack2(P.y_dtype, v[0], v[1]), pack2(P.y_dtype, v[2], v[3]));
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[j][h][c] = fmaf(s, d[c >> 1][j][2 * (c & 1) + h], acc[j][h][c]);
-      }
-  } else if (P.out == P.y) {
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 8 * j + 2 * q + h;
-      if (i >= n) continue;
-      const size_t at = (size_t)list[i] * P.out_stride + n0;
-      const float* v = acc[j][h];
-      if (P.vec) {
-        if (n0 < P.N) {
-          if (P.y_dtype == kF32)
-            *reinterpret_cast<float4*>(static_cast<float*>(P.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at) =
-                make_uint2(pack2(P.y_dtype, v[0], v[1]), pack2(P.y_dtype, v[2], v[3]));
+          for (int c = 0; c < 4; ++c)
+            if (n0 + c < c_end) elem_store(P.out, P.y_dtype, at + c, v[c]);
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n0 + c < P.N) elem_store(P.out, P.y_dtype, at + c, v[c]);
       }
-    }
+  }
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -450,7 +461,7 @@ int windows(int T) { return (T + kWindow - 1) / kWindow; }
 // one 32-column block.
 int splits_for(int tiles, int K) {
   const int most = (K + 32 * kWarps - 1) / (32 * kWarps);
-  const int want = 2 * 152 / (tiles > 0 ? tiles : 1);
+  const int want = 4 * 152 / (tiles > 0 ? tiles : 1);
   const int s = want < 8 ? want : 8;
   return s < 1 ? 1 : s < most ? s : most;
 }
@@ -473,46 +484,56 @@ cudaError_t launch_tiles(const AdapterParams& p, int blocks, cudaStream_t stream
                   : p.R <= 32 ? launch_shrink<F16, 2, NT>(p, grid, stream)
                               : launch_shrink<F16, 4, NT>(p, grid, stream);
   if (e != cudaSuccess) return e;
-  const int Rp = (p.R + 15) & ~15, pitch = (Rp / 16) & 1 ? Rp : Rp + 16;
-  return launch_behind(k_expand<F16, NT>, dim3(blocks, (p.N + 255) / 256), kThreads, 2 * 8 * NT * pitch * 2, stream,
-                       p);
+  const int Rp = (p.R + 15) & ~15, pitch = (Rp / 16) & 1 ? Rp : Rp + 16, smem = 2 * 8 * NT * pitch * 2;
+  const dim3 eg(blocks, (p.N + p.cols - 1) / p.cols);
+  auto expand = [&](auto kern) { return launch_behind(kern, eg, kThreads, smem, stream, p); };
+  if (!p.vec) return expand(k_expand<F16, NT, 2, 2>);
+  if (p.y_dtype == kF32)
+    return p.R <= 16 ? expand(k_expand<F16, NT, 1, 0>) : p.R <= 32 ? expand(k_expand<F16, NT, 2, 0>)
+                                                                   : expand(k_expand<F16, NT, 4, 0>);
+  return p.R <= 16 ? expand(k_expand<F16, NT, 1, 1>) : p.R <= 32 ? expand(k_expand<F16, NT, 2, 1>)
+                                                                 : expand(k_expand<F16, NT, 4, 1>);
 }
 
 }  // namespace
 
-// v for every part of K, then (many tokens) the order and the tiles.  The
+// v for every part of K, then (many tokens) the order and the marks.  The
 // fewest tiles that T tokens can make give the most parts.
 size_t adapters_workspace(int T, int K, int N, int R) {
   (void)N;
   const size_t v = align256((size_t)splits_for((T + 31) / 32, K) * T * R * 4);
-  if (T <= kScanT) return v;
-  return v + align256((size_t)T * 4) + align256((size_t)windows(T) * 4) +
-         align256((size_t)windows(T) * kWindow * sizeof(TileEntry));
+  return T <= kScanT ? v : v + 2 * align256((size_t)T * 4) + align256((size_t)T);
 }
 
 cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream) {
-  // tokens a tile: 8 for a call of at most 8 tokens, else 32
-  const bool small = p.T <= 8;
+  // tokens a tile: 32, or 8 where an adapter has no more than that on average
+  // (a quarter of the registers; an adapter with more is read once every 8)
+  const bool small = p.T <= 8 || p.T / 8 <= p.n;
   p.tile = small ? 8 : 32;
-  const int least = (p.T + p.tile - 1) / p.tile;
-  p.splits = splits_for(least > p.n ? least : p.n < p.T ? p.n : p.T, p.K);
+  const int least = (p.T + p.tile - 1) / p.tile, likely = least > p.n ? least : p.n < p.T ? p.n : p.T;
+  p.splits = splits_for(likely, p.K);
+  // columns a block of k_expand goes through: the v of a tile is staged once a
+  // block, so as many as leave two blocks for every SM
+  const int chunks = (p.N + kThreads - 1) / kThreads;
+  int parts = (4 * 152 + likely - 1) / likely;
+  parts = parts < 1 ? 1 : parts > chunks ? chunks : parts;
+  p.cols = (chunks + parts - 1) / parts * kThreads;
   const uintptr_t four = p.y_dtype == kF32 ? 16 : 8;
   p.vec = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % four == 0 &&
           reinterpret_cast<uintptr_t>(p.out) % four == 0 && (p.T == 1 || (p.y_stride % 4 == 0 && p.out_stride % 4 == 0));
   int blocks = p.T;
   if (p.T > kScanT) {
-    const int wn = windows(p.T);
+    const int wn = (p.T + kWindow - 1) / kWindow, len = p.T < kWindow ? p.T : kWindow;
     uint8_t* w = reinterpret_cast<uint8_t*>(p.v) + align256((size_t)splits_for((p.T + 31) / 32, p.K) * p.T * p.R * 4);
     p.order = reinterpret_cast<int32_t*>(w);
-    w += align256((size_t)p.T * 4);
-    p.n_tiles = reinterpret_cast<int32_t*>(w);
-    w += align256((size_t)wn * 4);
-    p.tiles = w;
+    p.adapter_at = reinterpret_cast<int32_t*>(w + align256((size_t)p.T * 4));
+    p.marks = w + 2 * align256((size_t)p.T * 4);
     // tiles of a window at most: full ones, and a last one of each adapter (and of the tokens that have none)
-    p.slots = p.n + 1 < kWindow ? kWindow / p.tile + p.n + 1 : kWindow;
-    if (p.slots > kWindow) p.slots = kWindow;
+    p.slots = p.n < len ? len / p.tile + p.n + 1 : len;
+    if (p.slots > len) p.slots = len;
     blocks = wn * p.slots;
-    const cudaError_t e = launch_behind(k_order, dim3(wn), kWindow / 2, 0, stream, p);
+    const cudaError_t e = launch_behind(k_order, dim3(wn, (len + kOrderTokens - 1) / kOrderTokens), 8 * kOrderTokens,
+                                        0, stream, p);
     if (e != cudaSuccess) return e;
   }
   if (p.f16) return small ? launch_tiles<true, 1>(p, blocks, stream) : launch_tiles<true, 4>(p, blocks, stream);

@@ -292,11 +292,12 @@ struct AdapterParams {
   const void* y;
   void* out;
   // workspace: A_a x of every token, for each part of K; tokens in the order
-  // of their adapters, and per window of tokens its tiles
+  // of their adapters, and where the tiles start in it
   float* v;
-  int32_t *order, *n_tiles;
-  void* tiles;
-  int tile, slots, splits, vec;  // set by the launch: tokens a tile, tiles a window at most, parts of K, loads of four
+  int32_t *order, *adapter_at;
+  uint8_t* marks;
+  // set by the launch: tokens a tile, tiles a window at most, parts of K, columns a block, loads of four
+  int tile, slots, splits, cols, vec;
 };
 size_t adapters_workspace(int T, int K, int N, int R);
 cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream);

@@ -11,12 +11,15 @@
 // Without a bias the key is the logit itself, since the scores rise with it:
 // the choice is then exact, and scores are formed only where the groups or the
 // weights need them.  With a bias the key is c = s + b in fp32, which is off by
-// less than `slack` (below); where two neighbours in the order of the choice,
-// or the groups on the two sides of the cut, lie closer than that, the warp
-// makes the whole choice again in fp64.  That is one token in some hundreds on
-// logits of a spread of two; fp64 for every token, the first form of this
-// kernel, ran 176 us on 4096 tokens x 256 experts and 536 us on 16381 x 200
-// (the GPU's fp64 rate is a small share of its fp32 rate).
+// less than `slack` (below); where two neighbours in the order of the choice
+// lie closer than that, the candidates' c are formed and ordered in fp64, one a
+// lane, and where the groups on the two sides of the cut do (or more candidates
+// than lanes), the warp makes the whole choice again in fp64.  The first is one
+// token in some hundreds on logits of a spread of two, the second one in
+// thousands; fp64 for every token, the first form of this kernel, ran 176 us on
+// 4096 tokens x 256 experts and 536 us on 16381 x 200, and the whole choice in
+// fp64 for every near pair still 36 and 48 us (the GPU's fp64 rate is a small
+// share of its fp32 rate, and one such token is all that an SM waits for).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -107,35 +110,90 @@ MOE_DEV void choose_exact(const RouteParams& P, const float (&l)[EPL], const flo
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = -INFINITY;
   }
+  // order keys of c (0: cannot be chosen): integer comparisons from here on
+  unsigned long long key[EPL], best = 0ull;
+  uint32_t best_l = 0u;
+  int at = 0;
+  auto local_best = [&]() {
+    best = 0ull;
+    best_l = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t k = float_order_key(l[i]);
+      if (key[i] > best || (key[i] == best && key[i] != 0ull && k > best_l)) {
+        best = key[i];
+        best_l = k;
+        at = i;
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(c[i] + 0.0);
+    key[i] = c[i] == -INFINITY ? 0ull : u >> 63 ? ~u : u | 1ull << 63;
+  }
+  local_best();
   id = -1;
   lj = -INFINITY;
   for (int j = 0; j < P.K; ++j) {
-    double bc = -INFINITY;
-    float bl = -INFINITY;
-    int be = 1 << 30;
-    // c, then the logit, then the lower index
-    auto take = [&](double c2, float l2, int e2) {
-      if (c2 > bc || (c2 == bc && (l2 > bl || (l2 == bl && e2 < be)))) {
-        bc = c2;
-        bl = l2;
-        be = e2;
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (c[i] != -INFINITY) take(c[i], l[i], o.e0 + i);
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-      take(__shfl_xor_sync(kAll, bc, d), __shfl_xor_sync(kAll, bl, d), __shfl_xor_sync(kAll, be, d));
-    if (bc == -INFINITY) break;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (o.e0 + i == be && i < o.n) c[i] = -INFINITY;
+    // the largest c, then the largest logit, then the lowest lane and slot
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(best >> 32));
+    if (hi == 0u) break;
+    bool in = (uint32_t)(best >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(kAll, in ? (uint32_t)best : 0u);
+    in = in && (uint32_t)best == lo;
+    const uint32_t lk = __reduce_max_sync(kAll, in ? best_l : 0u);
+    const int src = __ffs(__ballot_sync(kAll, in && best_l == lk)) - 1;
+    const int e = __shfl_sync(kAll, o.e0 + at, src);
     if (lane == j) {
-      id = be;
-      lj = bl;
+      id = e;
+      lj = key_float(lk);
+    }
+    if (lane == src) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i == at) key[i] = 0ull;
+      local_best();
     }
   }
+}
+
+// The n candidates on lanes 0 .. n - 1 (expert id, logit lj; with a bias), in
+// the order of their c in fp64: a lane forms one c, counts the candidates
+// before it and the candidates change lanes.
+template <int EPL>
+MOE_DEV void settle(const RouteParams& P, const float (&l)[EPL], int n, int& id, float& lj) {
+  const int lane = threadIdx.x & 31;
+  double c = -INFINITY;
+  if (P.sigmoid) {
+    if (id >= 0) c = 1.0 / (1.0 + exp(-(double)lj));
+  } else {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+    m = key_float(__reduce_max_sync(kAll, float_order_key(m)));
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (l[i] != -INFINITY) z += exp((double)l[i] - (double)m);
+    z = warp_sum(z);
+    if (id >= 0) c = exp((double)lj - (double)m) / z;
+  }
+  if (id >= 0) c += (double)clean(P.bias[id]);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double cj = __shfl_sync(kAll, c, j);
+    const float l2 = __shfl_sync(kAll, lj, j);
+    const int e2 = __shfl_sync(kAll, id, j);
+    rank += cj > c || (cj == c && (l2 > lj || (l2 == lj && e2 < id)));
+  }
+  int src = lane;
+  for (int j = 0; j < n; ++j) {
+    const int from = __ffs(__ballot_sync(kAll, lane < n && rank == j)) - 1;
+    if (lane == j) src = from;
+  }
+  id = __shfl_sync(kAll, id, src);
+  lj = __shfl_sync(kAll, lj, src);
 }
 
 template <int EPL>
@@ -248,45 +306,25 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const __grid_constant__ R
   }
   int id = -1;
   float lj = -INFINITY;
-  float c_last = 0.f, c_cut = 0.f, l_last = 0.f;
-  int e_last = 0;
   if (!unsure) {
-    // with a bias, rounds go on behind the last choice until one is clearly
-    // below it (a run of more than 8 near ones is left to fp64)
-    for (int j = 0; j < P.K + (biased ? 9 : 0); ++j) {
+    // With a bias, rounds go on behind the K-th until one is clearly below it
+    // (while a lane is free to hold it).
+    float c_last = INFINITY, c_cut = INFINITY;
+    bool near = false;
+    int n = 0;
+    for (; n < (biased ? 32 : P.K); ++n) {
       const uint32_t top = __reduce_max_sync(kAll, best);
       if (top == 0u) break;
+      const float cj = key_float(top);
+      if (n >= P.K && c_cut - cj > slack(c_cut)) break;
       const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
       const int e = __shfl_sync(kAll, o.e0 + at, src);
-      const float cj = key_float(top);
-      float lw = cj;
-      if (biased) {
-        float la = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) la = at == i ? l[i] : la;
-        lw = __shfl_sync(kAll, la, src);
-        if (j >= P.K && c_cut - cj > slack(c_cut)) break;
-        if (j == P.K + 8) {
-          unsure = true;
-          break;
-        }
-        if (j > 0 && c_last - cj <= slack(c_last)) {
-          // too near to tell in fp32, unless the biases are the same: then the
-          // logits decide, or for equal ones the index
-          const float bl = clean(P.bias[e_last]), be = clean(P.bias[e]);
-          if (!(bl == be && (l_last > lw || (l_last == lw && e_last < e)))) {
-            unsure = true;
-            break;
-          }
-        }
-        c_last = cj;
-        l_last = lw;
-        e_last = e;
-        if (j == P.K - 1) c_cut = cj;
-      }
-      if (lane == j && j < P.K) {
+      near |= c_last - cj <= slack(cj);
+      c_last = cj;
+      if (n < P.K) c_cut = cj;
+      if (lane == n) {
         id = e;
-        lj = lw;
+        lj = cj;
       }
       if (lane == src) {
         best = 0u;
@@ -300,6 +338,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const __grid_constant__ R
             best = key[i];
             at = i;
           }
+      }
+    }
+    if (biased) {
+      // no lane left, and the next one is near the cut
+      const uint32_t next = __reduce_max_sync(kAll, best);
+      unsure = n == 32 && next != 0u && c_cut - key_float(next) <= slack(c_cut);
+      lj = id >= 0 ? clean(elem_load(P.logits, P.dtype, (size_t)t * P.stride + id)) : -INFINITY;
+      if (near && !unsure) settle<EPL>(P, l, n, id, lj);
+      if (lane >= P.K) {
+        id = -1;
+        lj = -INFINITY;
       }
     }
   }
