@@ -37,6 +37,13 @@ constexpr int kWindow = 1024;
 constexpr int kOrderTokens = 32;      // tokens a block of k_order ranks, eight threads a token
 constexpr int kRankChunk = 64;        // rows of A a block of k_shrink takes
 
+// k_expand's shared memory: elements between two tokens' v (32 modulo 64 bytes:
+// no bank conflicts), and the bytes of a stage.
+__host__ __device__ constexpr int expand_pitch(int R) { return (R + 15) / 16 % 2 ? (R + 15) / 16 * 16 : (R + 15) / 16 * 16 + 16; }
+__host__ __device__ constexpr int expand_stage(int R, int NT, int yb) {
+  return kThreads * (NT * 2 * yb + (R + 15) / 16 * 4 * 8);
+}
+
 MOE_DEV int adapter_of(const AdapterParams& P, int t) {
   const int a = P.ids[t];
   return a < 0 || a >= P.n ? -1 : a;
@@ -259,22 +266,104 @@ __global__ void __launch_bounds__(kThreads) k_shrink(const __grid_constant__ Ada
   }
 }
 
+// v of a tile as the B operand of the second product, two numbers of the
+// operands' type an element: bf16 hi + lo keep 16 bits and more of v; fp16 keeps
+// 22, of v scaled by a power of two to a largest element near 1, since v may
+// pass fp16's range.  s_scale: what takes the token's product back, times the
+// adapter's scale.  256 / TILE threads a token; ends with a block barrier.
+template <bool F16, int TILE>
+MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int rank, int pitch, uint32_t* vs,
+                     float* s_scale) {
+  const int tid = threadIdx.x;
+  constexpr int TPT = kThreads / TILE;
+  const int tok = tid / TPT, part = tid % TPT, padded = (rank + 15) & ~15;
+  float top = 0.f;
+  uint16_t* hi = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
+  uint16_t* lo = hi + TILE * pitch;
+  float keep[kAdapterMaxRank / TPT];
+#pragma unroll
+  for (int i = 0; i < kAdapterMaxRank / TPT; ++i) {
+    const int r = part + TPT * i;
+    keep[i] = 0.f;
+    if (tok < n && r < rank) {
+      const float* v = P.v + (size_t)list[tok] * P.R + r;
+      for (int k = 0; k < P.splits; ++k) keep[i] += __ldcg(v + (size_t)k * P.T * P.R);
+    }
+    top = fmaxf(top, fabsf(keep[i]));
+  }
+  float up = 1.f, down = 1.f;
+  if (F16) {
+#pragma unroll
+    for (int o = TPT >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^e with 2^e <= top < 2^(e + 1), kept within the normal numbers on both sides
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+    if (top > 0.f && top < INFINITY) {
+      up = __uint_as_float(e << 23);
+      down = __uint_as_float((254u - e) << 23);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kAdapterMaxRank / TPT; ++i) {
+    const int r = part + TPT * i;
+    if (r >= padded) break;
+    const float v = keep[i] * down;
+    const uint32_t h = pack2(F16 ? kF16 : kBf16, v, 0.f);
+    float vh, none;
+    unpack2(F16 ? kF16 : kBf16, h, vh, none);
+    hi[r] = static_cast<uint16_t>(h);
+    lo[r] = fabsf(vh) < INFINITY ? static_cast<uint16_t>(pack2(F16 ? kF16 : kBf16, v - vh, 0.f)) : 0;
+  }
+  if (part == 0) s_scale[tok] = up * (P.scales ? P.scales[a] : 1.f);
+  __syncthreads();
+}
+
+MOE_DEV void mask_rank(uint2& b, int left) {  // keep the first `left` of four elements
+  if (left >= 4) return;
+  b.x &= left > 1 ? ~0u : 0xFFFFu;
+  b.y &= left > 2 ? 0xFFFFu : 0u;
+}
+
+// One 16-wide step of the rank: the lane's four rows of B (four k each) against
+// v of the tile's tokens (v: hi of the lane's token and k; lo_at further: lo).
+template <bool F16, int NT>
+MOE_DEV void mma_step(const uint2 (&b)[4], const uint16_t* v, int lo_at, int n, float (&d)[2][NT][4], int pitch) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if (8 * j >= n) continue;
+    const uint2 vh = *reinterpret_cast<const uint2*>(v + 8 * j * pitch);
+    const uint2 vl = *reinterpret_cast<const uint2*>(v + 8 * j * pitch + lo_at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mma16816(F16, d[i][j], b[2 * i].x, b[2 * i + 1].x, b[2 * i].y, b[2 * i + 1].y, vl.x, vl.y);
+      mma16816(F16, d[i][j], b[2 * i].x, b[2 * i + 1].x, b[2 * i].y, b[2 * i + 1].y, vh.x, vh.y);
+    }
+  }
+}
+
+template <int BYTES>
+MOE_DEV void cp_async(void* dst, const void* src, bool valid) {
+  const uint32_t size = valid ? BYTES : 0;  // 0: zeros
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(size) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES), "r"(size)
+                 : "memory");
+}
+
 // Blocks (tile, columns): the block goes through its columns 256 at a time, warp
 // w taking 32 w .. of them as two 16-row tiles of B, whose rows are dealt so
 // that a lane ends with four neighbouring columns n0 + 4g .. + 3 of tokens 2q
-// and 2q + 1.  The loads of y and of B (ST 16-wide steps of the rank at once) go
-// out together, and no warp waits for another between them: one memory latency
-// a round, covered by the other warps.  v enters as two numbers of the operands'
-// type (bf16: hi + lo, 16 bits and more of v; fp16: 22 bits, scaled by a power
-// of two to a largest element near 1, since v may pass fp16's range).  The ids,
-// the order and the first y are read ahead of the wait on k_shrink.
-//
-// YK: y and out are fp32 (0) or 16-bit (1) in rows that allow accesses of four
-// elements, or anything (2).
-template <bool F16, int NT, int ST, int YK>
+// and 2q + 1.  What a lane needs of y and B of the next two rounds is on its way
+// into shared memory (asynchronous copies, a place of its own for every lane,
+// so no thread waits for another) while it works on one: the loads of a round
+// held in registers instead ran 46 us at 8192 x 2048 fp32 columns, rank 32.
+// The first two rounds are asked for ahead of the wait on k_shrink, which
+// writes neither y nor B.  YK: y and out are fp32 (0) or 16-bit (1); rows allow
+// accesses of four elements, R % 4 == 0.
+template <bool F16, int NT, int YK>
 __global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ AdapterParams P) {
-  constexpr int TILE = 8 * NT;
-  extern __shared__ uint32_t vs[];  // [2][TILE][pitch / 2]: hi, then lo; pitch in elements
+  constexpr int TILE = 8 * NT, YB = YK == 0 ? 16 : 8;
+  extern __shared__ __align__(16) uint32_t vs[];  // v: [2][TILE][pitch / 2], then two stages
   __shared__ int list[TILE];
   __shared__ float s_scale[TILE];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
@@ -284,184 +373,169 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ 
     pdl_launch_dependents();
     return;
   }
-  const int rank = adapter_rank(P, a);
-  const int Rp = (P.R + 15) & ~15;
-  const int pitch = (Rp / 16) & 1 ? Rp : Rp + 16;  // 32 (mod 64) bytes a row: no bank conflicts
-  const int c_end = min(P.N, (int)(blockIdx.y + 1) * P.cols);
-  int n0 = P.cols * blockIdx.y + 32 * warp + 4 * g;
+  const int rank = adapter_rank(P, a), steps = (rank + 15) / 16, pitch = expand_pitch(P.R);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(vs) + 2 * TILE * pitch * 2;
+  const int stage_bytes = expand_stage(P.R, NT, YB);
+  const int c_first = P.cols * blockIdx.y, c_end = min(P.N, c_first + P.cols);
+  const int col = 32 * warp + 4 * g;
   int row[NT][2];  // the lane's tokens, -1: none
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int h = 0; h < 2; ++h) row[j][h] = 8 * j + 2 * q + h < n ? list[8 * j + 2 * q + h] : -1;
-  float acc[NT][2][4];
-  auto load_y = [&]() {
+  // the lane's places: y [NT][2][256] of YB bytes, B [steps][4][256] of 8
+  auto fetch = [&](int c0, int stage) {
+    const int n0 = c0 + col;
+    if (n0 < c_end) {
+      uint8_t* ys = ring + stage * stage_bytes + tid * YB;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
+          if (row[j][h] >= 0)
+            cp_async<YB>(ys + (2 * j + h) * kThreads * YB,
+                         static_cast<const uint8_t*>(P.y) + ((size_t)row[j][h] * P.y_stride + n0) * (YB / 4), true);
+      uint8_t* bs = ring + stage * stage_bytes + NT * 2 * kThreads * YB + tid * 8;
+      const uint16_t* br = P.B + ((size_t)max(a, 0) * P.N + n0) * P.R + 4 * q;
+      for (int s = 0; s < steps; ++s)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[j][h][c] = 0.f;
-        if (row[j][h] < 0 || n0 >= c_end) continue;
-        const size_t at = (size_t)row[j][h] * P.y_stride + n0;
-        if (YK == 0) {
-          const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(P.y) + at);
-          acc[j][h][0] = f.x, acc[j][h][1] = f.y, acc[j][h][2] = f.z, acc[j][h][3] = f.w;
-        } else if (YK == 1) {
-          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.y) + at);
-          unpack2(P.y_dtype, u.x, acc[j][h][0], acc[j][h][1]);
-          unpack2(P.y_dtype, u.y, acc[j][h][2], acc[j][h][3]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (n0 + c < c_end) acc[j][h][c] = elem_load(P.y, P.y_dtype, at + c);
-        }
-      }
+        for (int c = 0; c < 4; ++c)
+          cp_async<8>(bs + (4 * s + c) * kThreads * 8, 16 * s + 4 * q < rank ? br + (size_t)c * P.R + 16 * s : P.B,
+                      16 * s + 4 * q < rank);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  load_y();
+  fetch(c_first, 0);
+  fetch(c_first + kThreads, 1);
   pdl_wait();
   pdl_launch_dependents();
-  if (rank == 0 && P.out == P.y) return;
-  if (rank > 0) {
-    // v of the tile: 256 / TILE threads a token
-    constexpr int TPT = kThreads / TILE;
-    const int tok = tid / TPT, part = tid % TPT, padded = (rank + 15) & ~15;
-    float top = 0.f;
-    uint16_t* hi = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
-    uint16_t* lo = hi + TILE * pitch;
-    float keep[kAdapterMaxRank / TPT];
-#pragma unroll
-    for (int i = 0; i < kAdapterMaxRank / TPT; ++i) {
-      const int r = part + TPT * i;
-      keep[i] = 0.f;
-      if (tok < n && r < rank) {
-        const float* v = P.v + (size_t)list[tok] * P.R + r;
-        for (int k = 0; k < P.splits; ++k) keep[i] += __ldcg(v + (size_t)k * P.T * P.R);
-      }
-      top = fmaxf(top, fabsf(keep[i]));
-    }
-    float up = 1.f, down = 1.f;
-    if (F16) {
-#pragma unroll
-      for (int o = TPT >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^e with 2^e <= top < 2^(e + 1), kept within the normal numbers on both sides
-      const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
-      if (top > 0.f && top < INFINITY) {
-        up = __uint_as_float(e << 23);
-        down = __uint_as_float((254u - e) << 23);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kAdapterMaxRank / TPT; ++i) {
-      const int r = part + TPT * i;
-      if (r >= padded) break;
-      const float v = keep[i] * down;
-      const uint32_t h = pack2(F16 ? kF16 : kBf16, v, 0.f);
-      float vh, none;
-      unpack2(F16 ? kF16 : kBf16, h, vh, none);
-      hi[r] = static_cast<uint16_t>(h);
-      lo[r] = fabsf(vh) < INFINITY ? static_cast<uint16_t>(pack2(F16 ? kF16 : kBf16, v - vh, 0.f)) : 0;
-    }
-    if (part == 0) s_scale[tok] = up * (P.scales ? P.scales[a] : 1.f);
-    __syncthreads();
-  }
-  for (int c0 = P.cols * blockIdx.y; c0 < c_end; c0 += kThreads, n0 += kThreads) {
-    if (c0 > P.cols * (int)blockIdx.y) load_y();
-    if (rank > 0) {
+  if (rank > 0) stage_v<F16, TILE>(P, list, a, n, rank, pitch, vs, s_scale);
+  for (int c0 = c_first, stage = 0; c0 < c_end; c0 += kThreads, stage ^= 1) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int n0 = c0 + col;
+    // (the products are a whole warp's: lanes past the last column take part)
+    if (c0 + 32 * warp < c_end && !(rank == 0 && P.out == P.y)) {
+      const uint8_t* ys = ring + stage * stage_bytes + tid * YB;
+      const uint8_t* bs = ring + stage * stage_bytes + NT * 2 * kThreads * YB + tid * 8;
       float d[2][NT][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
-      const uint16_t* br = P.B + ((size_t)a * P.N + n0) * P.R;
-      for (int s0 = 0; 16 * s0 < rank; s0 += ST) {
-        uint2 bv[ST][4];
+      const uint16_t* v = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
+      for (int s = 0; s < steps; ++s) {
+        uint2 bv[4];
 #pragma unroll
-        for (int s = 0; s < ST; ++s) {
-          const int r = 16 * (s0 + s) + 4 * q;  // the lane's four k of the step
-#pragma unroll
-          for (int c = 0; c < 4; ++c) bv[s][c] = make_uint2(0u, 0u);
-          if (r >= rank) continue;
-          if (P.R % 4 == 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (n0 + c < c_end) bv[s][c] = *reinterpret_cast<const uint2*>(br + (size_t)c * P.R + r);
-            if (r + 4 > rank) {  // what lies past the rank does not count
-              const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 2 < rank ? 0xFFFFu : 0u;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                bv[s][c].x &= mx;
-                bv[s][c].y &= my;
-              }
-            }
-          } else {
-#pragma unroll 1
-            for (int e = 0; e < min(4, rank - r); ++e)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t v = n0 + c < c_end ? (uint32_t)br[(size_t)c * P.R + r + e] << 16 * (e & 1) : 0u;
-                if (e < 2)
-                  bv[s][c].x |= v;
-                else
-                  bv[s][c].y |= v;
-              }
-          }
+        for (int c = 0; c < 4; ++c) {
+          bv[c] = *reinterpret_cast<const uint2*>(bs + (4 * s + c) * kThreads * 8);
+          mask_rank(bv[c], rank - 16 * s - 4 * q);
         }
-#pragma unroll
-        for (int s = 0; s < ST; ++s) {
-          if (16 * (s0 + s) >= rank) break;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if (8 * j >= n) continue;
-            const uint16_t* vp = reinterpret_cast<const uint16_t*>(vs) + (8 * j + g) * pitch + 16 * (s0 + s) + 4 * q;
-            const uint2 vh = *reinterpret_cast<const uint2*>(vp), vl = *reinterpret_cast<const uint2*>(vp + TILE * pitch);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint2 b0 = bv[s][2 * i], b1 = bv[s][2 * i + 1];
-              mma16816(F16, d[i][j], b0.x, b1.x, b0.y, b1.y, vl.x, vl.y);
-              mma16816(F16, d[i][j], b0.x, b1.x, b0.y, b1.y, vh.x, vh.y);
-            }
-          }
-        }
+        mma_step<F16, NT>(bv, v + 16 * s, TILE * pitch, n, d, pitch);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float s = s_scale[8 * j + 2 * q + h];
+          if (row[j][h] < 0 || n0 >= c_end) continue;
+          const float s = rank > 0 ? s_scale[8 * j + 2 * q + h] : 0.f;
+          const uint8_t* yp = ys + (2 * j + h) * kThreads * YB;
+          float y[4];
+          if (YK == 0) {
+            const float4 f = *reinterpret_cast<const float4*>(yp);
+            y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(yp);
+            unpack2(P.y_dtype, u.x, y[0], y[1]);
+            unpack2(P.y_dtype, u.y, y[2], y[3]);
+          }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[j][h][c] = fmaf(s, d[c >> 1][j][2 * (c & 1) + h], acc[j][h][c]);
+          for (int c = 0; c < 4; ++c) y[c] = fmaf(s, d[c >> 1][j][2 * (c & 1) + h], y[c]);
+          uint8_t* o = static_cast<uint8_t*>(P.out) + ((size_t)row[j][h] * P.out_stride + n0) * (YB / 4);
+          if (YK == 0)
+            *reinterpret_cast<float4*>(o) = make_float4(y[0], y[1], y[2], y[3]);
+          else
+            *reinterpret_cast<uint2*>(o) = make_uint2(pack2(P.y_dtype, y[0], y[1]), pack2(P.y_dtype, y[2], y[3]));
         }
+    }
+    fetch(c0 + 2 * kThreads, stage);  // what the lane had there has been used
+  }
+}
+
+// The same for rows that do not allow accesses of four elements, or a pool
+// whose R is no multiple of 4: element by element.
+template <bool F16, int NT>
+__global__ void __launch_bounds__(kThreads) k_expand_any(const __grid_constant__ AdapterParams P) {
+  constexpr int TILE = 8 * NT;
+  extern __shared__ __align__(16) uint32_t vs[];
+  __shared__ int list[TILE];
+  __shared__ float s_scale[TILE];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  int a, n;
+  const bool found = find_tile<TILE>(P, list, a, n);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!found) return;
+  const int rank = adapter_rank(P, a), steps = (rank + 15) / 16, pitch = expand_pitch(P.R);
+  if (rank == 0 && P.out == P.y) return;
+  if (rank > 0) stage_v<F16, TILE>(P, list, a, n, rank, pitch, vs, s_scale);
+  const int c_first = P.cols * blockIdx.y, c_end = min(P.N, c_first + P.cols);
+  for (int n0 = c_first + 32 * warp + 4 * g; n0 - 4 * g < c_end; n0 += kThreads) {
+    float y[NT][2][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 8 * j + 2 * q + h;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          y[j][h][c] =
+              i < n && n0 + c < c_end ? elem_load(P.y, P.y_dtype, (size_t)list[i] * P.y_stride + n0 + c) : 0.f;
+      }
+    float d[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
+    for (int s = 0; s < steps; ++s) {
+      const int r = 16 * s + 4 * q;
+      uint2 bv[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          e[k] = n0 + c < c_end && r + k < rank ? P.B[((size_t)a * P.N + n0 + c) * P.R + r + k] : 0u;
+        bv[c] = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+      }
+      mma_step<F16, NT>(bv, v + 16 * s, TILE * pitch, n, d, pitch);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (row[j][h] < 0 || n0 >= c_end) continue;
-        const size_t at = (size_t)row[j][h] * P.out_stride + n0;
-        const float* v = acc[j][h];
-        if (YK == 0) {
-          *reinterpret_cast<float4*>(static_cast<float*>(P.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        } else if (YK == 1) {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at) =
-              make_uint2(pack2(P.y_dtype, v[0], v[1]), pack2(P.y_dtype, v[2], v[3]));
-        } else {
+        const int i = 8 * j + 2 * q + h;
+        if (i >= n) continue;
+        const float s = rank > 0 ? s_scale[i] : 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (n0 + c < c_end) elem_store(P.out, P.y_dtype, at + c, v[c]);
-        }
+        for (int c = 0; c < 4; ++c)
+          if (n0 + c < c_end)
+            elem_store(P.out, P.y_dtype, (size_t)list[i] * P.out_stride + n0 + c,
+                       fmaf(s, d[c >> 1][j][2 * (c & 1) + h], y[j][h][c]));
       }
   }
 }
+
+constexpr int kMaxSms = 192;  // the workspace does not depend on the device
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 int windows(int T) { return (T + kWindow - 1) / kWindow; }
 
 // Parts of K: enough blocks for the GPU from `tiles` tiles, each warp at least
 // one 32-column block.
-int splits_for(int tiles, int K) {
+int splits_for(int sms, int tiles, int K) {
   const int most = (K + 32 * kWarps - 1) / (32 * kWarps);
-  const int want = 4 * 152 / (tiles > 0 ? tiles : 1);
+  const int want = 2 * sms / (tiles > 0 ? tiles : 1);
   const int s = want < 8 ? want : 8;
   return s < 1 ? 1 : s < most ? s : most;
 }
@@ -484,15 +558,18 @@ cudaError_t launch_tiles(const AdapterParams& p, int blocks, cudaStream_t stream
                   : p.R <= 32 ? launch_shrink<F16, 2, NT>(p, grid, stream)
                               : launch_shrink<F16, 4, NT>(p, grid, stream);
   if (e != cudaSuccess) return e;
-  const int Rp = (p.R + 15) & ~15, pitch = (Rp / 16) & 1 ? Rp : Rp + 16, smem = 2 * 8 * NT * pitch * 2;
   const dim3 eg(blocks, (p.N + p.cols - 1) / p.cols);
-  auto expand = [&](auto kern) { return launch_behind(kern, eg, kThreads, smem, stream, p); };
-  if (!p.vec) return expand(k_expand<F16, NT, 2, 2>);
-  if (p.y_dtype == kF32)
-    return p.R <= 16 ? expand(k_expand<F16, NT, 1, 0>) : p.R <= 32 ? expand(k_expand<F16, NT, 2, 0>)
-                                                                   : expand(k_expand<F16, NT, 4, 0>);
-  return p.R <= 16 ? expand(k_expand<F16, NT, 1, 1>) : p.R <= 32 ? expand(k_expand<F16, NT, 2, 1>)
-                                                                 : expand(k_expand<F16, NT, 4, 1>);
+  const int v_bytes = 2 * 8 * NT * expand_pitch(p.R) * 2;
+  if (!p.vec) return launch_behind(k_expand_any<F16, NT>, eg, kThreads, v_bytes, stream, p);
+  auto ring = [&](auto kern, int yb) {
+    const int smem = v_bytes + 2 * expand_stage(p.R, NT, yb);
+    if (smem > 48 * 1024) {
+      const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err != cudaSuccess) return err;
+    }
+    return launch_behind(kern, eg, kThreads, smem, stream, p);
+  };
+  return p.y_dtype == kF32 ? ring(k_expand<F16, NT, 0>, 16) : ring(k_expand<F16, NT, 1>, 8);
 }
 
 }  // namespace
@@ -501,7 +578,7 @@ cudaError_t launch_tiles(const AdapterParams& p, int blocks, cudaStream_t stream
 // fewest tiles that T tokens can make give the most parts.
 size_t adapters_workspace(int T, int K, int N, int R) {
   (void)N;
-  const size_t v = align256((size_t)splits_for((T + 31) / 32, K) * T * R * 4);
+  const size_t v = align256((size_t)splits_for(kMaxSms, (T + 31) / 32, K) * T * R * 4);
   return T <= kScanT ? v : v + 2 * align256((size_t)T * 4) + align256((size_t)T);
 }
 
@@ -511,20 +588,20 @@ cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream) {
   const bool small = p.T <= 8 || p.T / 8 <= p.n;
   p.tile = small ? 8 : 32;
   const int least = (p.T + p.tile - 1) / p.tile, likely = least > p.n ? least : p.n < p.T ? p.n : p.T;
-  p.splits = splits_for(likely, p.K);
-  // columns a block of k_expand goes through: the v of a tile is staged once a
-  // block, so as many as leave two blocks for every SM
+  p.splits = splits_for(p.sms, likely, p.K);
+  // columns a block of k_expand goes through: finding the tile and staging its v
+  // are paid once a block, so as many as leave about two blocks for every SM
   const int chunks = (p.N + kThreads - 1) / kThreads;
-  int parts = (4 * 152 + likely - 1) / likely;
+  int parts = 2 * p.sms / likely;
   parts = parts < 1 ? 1 : parts > chunks ? chunks : parts;
   p.cols = (chunks + parts - 1) / parts * kThreads;
   const uintptr_t four = p.y_dtype == kF32 ? 16 : 8;
-  p.vec = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % four == 0 &&
+  p.vec = p.N % 4 == 0 && p.R % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % four == 0 &&
           reinterpret_cast<uintptr_t>(p.out) % four == 0 && (p.T == 1 || (p.y_stride % 4 == 0 && p.out_stride % 4 == 0));
   int blocks = p.T;
   if (p.T > kScanT) {
     const int wn = (p.T + kWindow - 1) / kWindow, len = p.T < kWindow ? p.T : kWindow;
-    uint8_t* w = reinterpret_cast<uint8_t*>(p.v) + align256((size_t)splits_for((p.T + 31) / 32, p.K) * p.T * p.R * 4);
+    uint8_t* w = reinterpret_cast<uint8_t*>(p.v) + align256((size_t)splits_for(kMaxSms, (p.T + 31) / 32, p.K) * p.T * p.R * 4);
     p.order = reinterpret_cast<int32_t*>(w);
     p.adapter_at = reinterpret_cast<int32_t*>(w + align256((size_t)p.T * 4));
     p.marks = w + 2 * align256((size_t)p.T * 4);

@@ -511,10 +511,12 @@ bool valid_elem(int d) { return d == MOE_FFN_ACT_F32 || d == MOE_FFN_ACT_BF16 ||
 bool elem_aligned(const void* p, int d) { return aligned(p, d == MOE_FFN_ACT_F32 ? 4 : 2); }
 bool finite(float v) { return v - v == 0.f; }
 
-// The current device is a GB300.
-int check_device() {
+// The current device is a GB300; its SMs.
+int check_device(int* sms) {
   DeviceInfo* dev = nullptr;
-  return device_info(&dev);
+  const int rc = device_info(&dev);
+  if (rc == MOE_FFN_OK) *sms = dev->sm_count < kMaxGrid ? dev->sm_count : kMaxGrid;
+  return rc;
 }
 
 int check_adapters(const moe_ffn_adapters_args* a) {
@@ -547,7 +549,8 @@ int moe_ffn_route(const moe_ffn_route_args* a, moe_ffn_stream_t stream, const vo
   if (!logits || !ids || !w) return MOE_FFN_ERR_INVALID_ARG;
   if (!elem_aligned(logits, a->dtype) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
     return MOE_FFN_ERR_MISALIGNED;
-  const int rc = check_device();
+  int sms = 0;
+  const int rc = check_device(&sms);
   if (rc != MOE_FFN_OK) return rc;
   RouteParams P = {};
   P.T = a->T;
@@ -590,11 +593,13 @@ int moe_ffn_norm_residual(const moe_ffn_norm_args* a, moe_ffn_stream_t stream, c
       !elem_aligned(normed, a->normed_dtype) || !elem_aligned(gate, a->gate_dtype) ||
       !elem_aligned(w_post, a->w_post_dtype) || !elem_aligned(w_pre, a->w_pre_dtype))
     return MOE_FFN_ERR_MISALIGNED;
-  const int rc = check_device();
+  int sms = 0;
+  const int rc = check_device(&sms);
   if (rc != MOE_FFN_OK) return rc;
   NormParams P = {};
   P.T = a->T;
   P.H = a->H;
+  P.sms = sms;
   P.y_dtype = a->y_dtype;
   P.r_dtype = a->res_dtype;
   P.n_dtype = a->normed_dtype;
@@ -643,7 +648,8 @@ int moe_ffn_add_adapters(const moe_ffn_adapters_args* a, moe_ffn_stream_t stream
   if (!aligned(workspace, 256) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(adapter_ids, 4) ||
       !aligned(ranks, 4) || !aligned(scales, 4) || !elem_aligned(y, a->y_dtype) || !elem_aligned(out, a->y_dtype))
     return MOE_FFN_ERR_MISALIGNED;
-  rc = check_device();
+  int sms = 0;
+  rc = check_device(&sms);
   if (rc != MOE_FFN_OK) return rc;
   AdapterParams P = {};
   P.T = a->T;
@@ -651,6 +657,7 @@ int moe_ffn_add_adapters(const moe_ffn_adapters_args* a, moe_ffn_stream_t stream
   P.N = a->N;
   P.R = a->R;
   P.n = a->n_adapters;
+  P.sms = sms;
   P.f16 = a->x_dtype == MOE_FFN_ACT_F16;
   P.y_dtype = a->y_dtype;
   P.x_stride = a->x_stride;

@@ -50,29 +50,39 @@ MOE_DEV void unpack2(int dtype, uint32_t w, float& lo, float& hi) {
     hi = bf16_hi(w);
   }
 }
-// Eight consecutive elements, their address 16-byte aligned.
-MOE_DEV void elem_load8(const void* p, int dtype, size_t i, float* v) {
+// One element, and four consecutive ones (their address aligned to the four), as
+// they lie in memory: the loads of several tensors go out one behind the other,
+// since nothing waits for a value between them, and are converted where they are
+// used.  Four, not eight: neighbouring lanes then cover whole sectors in one
+// access with fp32 too (16 bytes a lane), and a thread's columns are the same for
+// tensors of every type.
+MOE_DEV uint32_t raw_load(const void* p, int dtype, size_t i) {
+  if (dtype == kF32) return static_cast<const uint32_t*>(p)[i];
+  return static_cast<const uint16_t*>(p)[i];
+}
+MOE_DEV float raw_value(uint32_t w, int dtype) {
+  if (dtype == kF32) return __uint_as_float(w);
+  return dtype == kBf16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((unsigned short)w));
+}
+MOE_DEV uint4 raw_load4(const void* p, int dtype, size_t i) {
+  if (dtype == kF32) return *reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p) + i);
+  const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  return make_uint4(v.x, v.y, 0u, 0u);
+}
+MOE_DEV void raw_values4(const uint4& w, int dtype, float* v) {
   if (dtype == kF32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    unpack2(dtype, a.x, v[0], v[1]);
-    unpack2(dtype, a.y, v[2], v[3]);
-    unpack2(dtype, a.z, v[4], v[5]);
-    unpack2(dtype, a.w, v[6], v[7]);
+    unpack2(dtype, w.x, v[0], v[1]);
+    unpack2(dtype, w.y, v[2], v[3]);
   }
 }
-MOE_DEV void elem_store8(void* p, int dtype, size_t i, const float* v) {
-  if (dtype == kF32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(
-        pack2(dtype, v[0], v[1]), pack2(dtype, v[2], v[3]), pack2(dtype, v[4], v[5]), pack2(dtype, v[6], v[7]));
-  }
+MOE_DEV void elem_store4(void* p, int dtype, size_t i, const float* v) {
+  if (dtype == kF32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+        make_uint2(pack2(dtype, v[0], v[1]), pack2(dtype, v[2], v[3]));
 }
 
 // Launch behind the previous kernel of the stream with programmatic stream

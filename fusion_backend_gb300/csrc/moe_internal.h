@@ -272,7 +272,7 @@ struct RouteParams {
 cudaError_t launch_route(RouteParams p, cudaStream_t stream);
 
 struct NormParams {
-  int T, H;
+  int T, H, sms;
   int y_dtype, r_dtype, n_dtype, g_dtype, wpost_dtype, wpre_dtype;
   int post_norm, gate_layout, gate_sigmoid;
   float alpha, beta, w_offset, eps;
@@ -283,7 +283,7 @@ struct NormParams {
 cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
 
 struct AdapterParams {
-  int T, K, N, R, n;
+  int T, K, N, R, n, sms;
   int f16, y_dtype;
   long long x_stride, y_stride, out_stride;
   const uint16_t *x, *A, *B;

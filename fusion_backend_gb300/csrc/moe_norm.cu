@@ -3,15 +3,19 @@
 //
 // One pass over the data: a row's res and y are read once into registers, y's
 // mean square is reduced, r' formed, its mean square reduced, and res_out and
-// normed are written.  Two reductions a row are the only synchronisation; the
-// kernel is bound by HBM for many rows and by the latency of load, reduction,
-// reduction, store for a few, so everything a row needs is loaded at the start.
-// A row has a warp (H <= 512, four rows a block) or a block of H / 8 or H / 16
-// threads; past H = 8192 a thread holds 16 or 32 columns of r' and reads y twice
-// (the second time from cache) instead of holding it, to stay within the
-// registers of a block of 1024 threads.
+// normed are written.  The work is bound by HBM for many rows and by the latency
+// of load, reduction, reduction, store for a few.
+//   k_norm       a warp a row (H <= 512, four rows a block) or a block a row,
+//                everything a row needs asked for at the start.  A call of few
+//                rows, and rows past 8192 columns (16 or 32 of them a thread).
+//   k_norm_rows  as many blocks as fit on the GPU, each going through its rows
+//                with the next two on their way into shared memory
+//                (asynchronous copies) while it works on one; the weights stay
+//                in registers.  With a block a row the loads of a block stand
+//                still while it reduces and stores: 25 us on 4096 x 2048 fp32
+//                rows, where the copy rate allows 17.
 // The first form (256 threads and three passes over the row, element by
-// element) ran 57 us on 4096 x 2048 fp32 rows.
+// element) ran 57 us there.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -24,30 +28,51 @@ namespace {
 
 constexpr int kRowsPerBlock = 4;  // rows of a block whose rows have a warp each
 constexpr int kWarpRows = 32 * kRowsPerBlock;  // threads of such a block, and of no other
+constexpr int kStages = 3;        // rows of k_norm_rows in shared memory
 
-// Columns of the thread: VEC: eight neighbours a group, 16-byte accesses;
-// otherwise (rows or H that rule those out) neighbours on neighbouring threads.
-// Groups past the row hold zeros.
+// Columns of the thread, in groups of eight: VEC: two times four neighbours,
+// accesses of four elements; otherwise (rows or H that rule those out)
+// neighbours on neighbouring threads.  Columns past the row hold zeros.
 template <bool VEC>
 struct Columns {
   int tid, threads, H;
-  MOE_DEV int at(int j, int e) const { return VEC ? 8 * (tid + threads * j) + e : threads * (8 * j + e) + tid; }
-  MOE_DEV void load(const void* p, int dtype, size_t base, int j, float* v) const {
-    if (VEC) {
-      if (at(j, 0) < H) {
-        elem_load8(p, dtype, base + at(j, 0), v);
-      } else {
+  MOE_DEV int at(int j, int e) const {
+    return VEC ? 4 * (tid + threads * (2 * j + (e >> 2))) + (e & 3) : threads * (8 * j + e) + tid;
+  }
+  MOE_DEV void load(const void* p, int dtype, size_t base, int j, uint4* w) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      }
+    for (int h = 0; h < 2; ++h) w[h] = make_uint4(0u, 0u, 0u, 0u);
+    if (VEC) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (at(j, 4 * h) < H) w[h] = raw_load4(p, dtype, base + at(j, 4 * h));
+    } else {
+      uint32_t e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = at(j, i) < H ? raw_load(p, dtype, base + at(j, i)) : 0u;
+      w[0] = make_uint4(e[0], e[1], e[2], e[3]);
+      w[1] = make_uint4(e[4], e[5], e[6], e[7]);
+    }
+  }
+  MOE_DEV void values(const uint4* w, int dtype, float* v) const {
+    if (VEC) {
+      raw_values4(w[0], dtype, v);
+      raw_values4(w[1], dtype, v + 4);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = at(j, e) < H ? elem_load(p, dtype, base + at(j, e)) : 0.f;
+      for (int h = 0; h < 2; ++h) {
+        v[4 * h] = raw_value(w[h].x, dtype);
+        v[4 * h + 1] = raw_value(w[h].y, dtype);
+        v[4 * h + 2] = raw_value(w[h].z, dtype);
+        v[4 * h + 3] = raw_value(w[h].w, dtype);
+      }
     }
   }
   MOE_DEV void store(void* p, int dtype, size_t base, int j, const float* v) const {
     if (VEC) {
-      if (at(j, 0) < H) elem_store8(p, dtype, base + at(j, 0), v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (at(j, 4 * h) < H) elem_store4(p, dtype, base + at(j, 4 * h), v + 4 * h);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -74,11 +99,89 @@ MOE_DEV float row_sum(float v, float* red) {
   return v;
 }
 
-// THREADS: the most that a block has.  ALL: the weights and the gate too are
-// loaded at the start.
-template <int NV, bool VEC, int THREADS, bool ALL>
+// A row from res (r) and y in registers to its stores.  again(j, y): reads y's
+// group j a second time (or keeps what is there); post, gate, pre (j, v): the
+// group's weights or gate.
+template <int NV, bool VEC, int THREADS, bool WARP, typename Again, typename Post, typename Gate, typename Pre>
+MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t, float (&r)[NV][8], float (&y)[NV][8],
+                        float (*red)[32], Again again, Post post, Gate gate, Pre pre) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[j][e] *= P.alpha;
+  if (P.y) {
+    float scale = P.beta;
+    if (P.gate && P.gate_layout == 1) {
+      const float v = elem_load(P.gate, P.g_dtype, t * P.g_stride);
+      scale *= P.gate_sigmoid ? 1.f / (1.f + expf(-v)) : v;
+    }
+    if (P.post_norm) {
+      float q = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(y[j][e], y[j][e], q);
+      scale *= rsqrtf(row_sum<THREADS, WARP>(q, red[0]) / (float)P.H + P.eps);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      again(j, y[j]);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[j][e] *= scale;
+      if (P.post_norm && P.w_post) {
+        post(j, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[j][e] *= P.w_offset + v[e];
+      }
+      if (P.gate && P.gate_layout != 1) {
+        gate(j, v);
+        if (P.gate_sigmoid) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 1.f / (1.f + expf(-v[e]));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[j][e] *= v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[j][e] += y[j][e];
+    }
+  }
+  if (P.res_out) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) cols.store(P.res_out, P.r_dtype, t * P.ro_stride, j, r[j]);
+  }
+  if (P.normed) {
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      // columns past the row hold 0 times factors that may be infinite: they do
+      // not enter the sum
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (cols.at(j, VEC ? e & 4 : e) < P.H) q = fmaf(r[j][e], r[j][e], q);
+    }
+    const float inv = rsqrtf(row_sum<THREADS, WARP>(q, red[1]) / (float)P.H + P.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[j][e] *= inv;
+      if (P.w_pre) {
+        float v[8];
+        pre(j, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[j][e] *= P.w_offset + v[e];
+      }
+      cols.store(P.normed, P.n_dtype, t * P.n_stride, j, r[j]);
+    }
+  }
+}
+
+// THREADS: the most that a block has.
+template <int NV, bool VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ NormParams P) {
   constexpr bool WARP = THREADS == kWarpRows;
+  constexpr bool ALL = NV == 1;  // the weights and the gate too are asked for at the start
   constexpr bool AGAIN = NV * THREADS > 1024;  // y is read a second time
   __shared__ float red[2][32];
   const size_t t = WARP ? (size_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
@@ -90,131 +193,341 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ NormPa
   pdl_launch_dependents();
   if (WARP && t >= (size_t)P.T) return;
 
-  const bool per_column = P.gate && P.gate_layout != 1;
-  float r[NV][8], y[NV][8], g[ALL ? NV : 1][8], wp[ALL ? NV : 1][8], wn[ALL ? NV : 1][8];
+  uint4 rw[NV][2], yw[NV][2], gw[2], pw[2], nw[2];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) cols.load(P.res, P.r_dtype, t * P.r_stride, j, r[j]);
+  for (int j = 0; j < NV; ++j) cols.load(P.res, P.r_dtype, t * P.r_stride, j, rw[j]);
   if (P.y) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) cols.load(P.y, P.y_dtype, t * P.y_stride, j, y[j]);
+    for (int j = 0; j < NV; ++j) cols.load(P.y, P.y_dtype, t * P.y_stride, j, yw[j]);
   }
   const size_t g_row = P.gate_layout == 2 ? t * P.g_stride : 0;
+  auto load_gate = [&](int j) { cols.load(P.gate, P.g_dtype, g_row, j, gw); };
+  auto load_post = [&](int j) { cols.load(P.w_post, P.wpost_dtype, 0, j, pw); };
+  auto load_pre = [&](int j) { cols.load(P.w_pre, P.wpre_dtype, 0, j, nw); };
   if (ALL) {
+    if (P.gate && P.gate_layout != 1) load_gate(0);
+    if (P.w_post) load_post(0);
+    if (P.w_pre) load_pre(0);
+  }
+  float r[NV][8], y[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) cols.values(rw[j], P.r_dtype, r[j]);
+  if (P.y) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) cols.values(yw[j], P.y_dtype, y[j]);
+  }
+  finish_row<NV, VEC, THREADS, WARP>(
+      P, cols, t, r, y, red,
+      [&](int j, float* v) {
+        if (!AGAIN) return;
+        cols.load(P.y, P.y_dtype, t * P.y_stride, j, yw[j]);
+        cols.values(yw[j], P.y_dtype, v);
+      },
+      [&](int j, float* v) {
+        if (!ALL) load_post(j);
+        cols.values(pw, P.wpost_dtype, v);
+      },
+      [&](int j, float* v) {
+        if (!ALL) load_gate(j);
+        cols.values(gw, P.g_dtype, v);
+      },
+      [&](int j, float* v) {
+        if (!ALL) load_pre(j);
+        cols.values(nw, P.wpre_dtype, v);
+      });
+}
+
+// Two floats in one instruction (fma.rn.f32x2 and its kin): the arithmetic of
+// k_norm_rows, whose rows are otherwise bound by the instructions they issue.
+struct F2 {
+  unsigned long long v;
+};
+MOE_DEV F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+MOE_DEV F2 f2(float a) { return f2(a, a); }
+MOE_DEV void f2_get(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+MOE_DEV F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+MOE_DEV F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// One tensor's rows on their way through shared memory: a thread copies and
+// reads its own groups of four columns ([group][thread]), so no thread waits for
+// another.  F32: fp32 elements, otherwise 16-bit ones (dtype).
+template <bool F32>
+struct Stream {
+  static constexpr int kSize = F32 ? 4 : 2;
+  const uint8_t* next;  // the thread's first column of the row to copy next; null: absent
+  int dtype;
+  size_t stride;  // bytes from a row of the block to its next
+  MOE_DEV void init(const void* base, int dt, long long row_stride) {
+    dtype = dt;
+    stride = (size_t)(row_stride * kSize) * gridDim.x;
+    next = base ? static_cast<const uint8_t*>(base) + ((size_t)blockIdx.x * row_stride + 4 * threadIdx.x) * kSize : nullptr;
+  }
+  // place: the thread's first group in the tensor's part of the stage
+  template <int NV>
+  MOE_DEV void fetch(uint32_t place, const bool (&in)[NV]) {
+    if (!next) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (per_column) cols.load(P.gate, P.g_dtype, g_row, j, g[j]);
-      if (P.w_post) cols.load(P.w_post, P.wpost_dtype, 0, j, wp[j]);
-      if (P.w_pre) cols.load(P.w_pre, P.wpre_dtype, 0, j, wn[j]);
+      const int at = j * (int)blockDim.x * 4 * kSize;
+      if (!in[j]) continue;
+      if (F32)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place + at), "l"(next + at) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(place + at), "l"(next + at) : "memory");
+    }
+    next += stride;
+  }
+  MOE_DEV void read(const uint8_t* place, int j, F2* v) const {
+    place += j * (int)blockDim.x * 4 * kSize;
+    if (F32) {
+      const float4 f = *reinterpret_cast<const float4*>(place);
+      v[0] = f2(f.x, f.y);
+      v[1] = f2(f.z, f.w);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(place);
+      float f[4];
+      raw_values4(make_uint4(w.x, w.y, 0u, 0u), dtype, f);
+      v[0] = f2(f[0], f[1]);
+      v[1] = f2(f[2], f[3]);
     }
   }
+};
 
-  if (P.y) {
-    float scale = P.beta;
-    if (P.gate && !per_column) {
-      const float v = elem_load(P.gate, P.g_dtype, t * P.g_stride);
-      scale *= P.gate_sigmoid ? 1.f / (1.f + expf(-v)) : v;
+// NV groups of four columns a thread, accesses of four elements throughout.
+// R32, Y32, N32: res, y (and a gate of every element), normed are fp32.
+template <int NV, int THREADS, bool R32, bool Y32, bool N32>
+__global__ void __launch_bounds__(THREADS) k_norm_rows(const __grid_constant__ NormParams P) {
+  __shared__ float red[2][2][32];  // by the row's parity: a row may have one reduction alone, hence one barrier
+  extern __shared__ __align__(16) uint8_t stages[];  // [kStages][res | y | gate]
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const bool per_row = P.gate && P.gate_layout == 2;
+  constexpr int RB = R32 ? 4 : 2, YB = Y32 ? 4 : 2;
+  Stream<R32> sr;
+  Stream<Y32> sy, sg;
+  sr.init(P.res, P.r_dtype, P.r_stride);
+  sy.init(P.y, P.y_dtype, P.y_stride);
+  sg.init(per_row ? P.gate : nullptr, P.g_dtype, P.g_stride);
+  const int r_bytes = NV * 4 * threads * RB, y_bytes = P.y ? NV * 4 * threads * YB : 0;
+  const int bytes = r_bytes + y_bytes + (per_row ? y_bytes : 0);
+  bool in[NV];  // the group is inside the row
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = 4 * (tid + threads * j) < P.H;
+  auto fetch = [&](int t, int s) {
+    if (t < P.T) {
+      const uint32_t place = smem_u32(stages) + s * bytes;
+      sr.fetch(place + 4 * RB * tid, in);
+      sy.fetch(place + r_bytes + 4 * YB * tid, in);
+      sg.fetch(place + r_bytes + y_bytes + 4 * YB * tid, in);
     }
-    if (P.post_norm) {
-      float q = 0.f;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  pdl_wait();
+  pdl_launch_dependents();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + s * gridDim.x, s);
+  // what a column of y and of r' is multiplied by in every row: w_offset +
+  // w_post and a gate per column as one factor, w_offset + w_pre
+  F2 wy[NV][2], wn[NV][2];
+  const bool by_column = (P.post_norm && P.w_post) || (P.gate && P.gate_layout == 0);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float post[4], pre[4], g[4];
+    const size_t c = 4 * (tid + threads * j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) post[e] = pre[e] = 1.f;
+    if (in[j]) {
+      if (P.post_norm && P.w_post) {
+        raw_values4(raw_load4(P.w_post, P.wpost_dtype, c), P.wpost_dtype, post);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) post[e] += P.w_offset;
+      }
+      if (P.gate && P.gate_layout == 0) {
+        raw_values4(raw_load4(P.gate, P.g_dtype, c), P.g_dtype, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) post[e] *= P.gate_sigmoid ? 1.f / (1.f + expf(-g[e])) : g[e];
+      }
+      if (P.w_pre) {
+        raw_values4(raw_load4(P.w_pre, P.wpre_dtype, c), P.wpre_dtype, pre);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pre[e] += P.w_offset;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      wy[j][e] = f2(post[2 * e], post[2 * e + 1]);
+      wn[j][e] = f2(pre[2 * e], pre[2 * e + 1]);
+    }
+  }
+  const float per_column = 1.f / (float)P.H;
+  const F2 alpha = f2(P.alpha);
+  auto square = [&](const F2 (&v)[NV][2]) {
+    F2 q = f2(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (in[j]) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) q = f2_fma(v[j][e], v[j][e], q);
+      }
+    float a, b;
+    f2_get(q, a, b);
+    return a + b;
+  };
+  // the thread's first column of a row of an output, the block's rows apart
+  auto store = [&](uint8_t* row, bool f32, int dtype, const F2 (&v)[NV][2]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!in[j]) continue;
+      float f[4];
+      f2_get(v[j][0], f[0], f[1]);
+      f2_get(v[j][1], f[2], f[3]);
+      if (f32)
+        *reinterpret_cast<float4*>(row + 16 * threads * j) = make_float4(f[0], f[1], f[2], f[3]);
+      else
+        *reinterpret_cast<uint2*>(row + 8 * threads * j) = make_uint2(pack2(dtype, f[0], f[1]), pack2(dtype, f[2], f[3]));
+    }
+  };
+  constexpr int NB = N32 ? 4 : 2;
+  uint8_t* ro = static_cast<uint8_t*>(P.res_out) + ((size_t)blockIdx.x * P.ro_stride + 4 * tid) * RB;
+  uint8_t* no = static_cast<uint8_t*>(P.normed) + ((size_t)blockIdx.x * P.n_stride + 4 * tid) * NB;
+  const size_t ro_step = (size_t)P.ro_stride * RB * gridDim.x, no_step = (size_t)P.n_stride * NB * gridDim.x;
+  int s = 0, odd = 0;
+  for (int t = blockIdx.x; t < P.T; t += gridDim.x, ro += ro_step, no += no_step) {
+    // into the stage of the row before, which the thread has read
+    fetch(t + (kStages - 1) * gridDim.x, s == 0 ? kStages - 1 : s - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    const uint8_t* place = stages + s * bytes;
+    F2 r[NV][2];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      sr.read(place + 4 * RB * tid, j, r[j]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) r[j][e] = f2_mul(r[j][e], alpha);
+    }
+    if (P.y) {
+      F2 y[NV][2];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) sy.read(place + r_bytes + 4 * YB * tid, j, y[j]);
+      float scale = P.beta;
+      if (P.gate && P.gate_layout == 1) {
+        const float v = elem_load(P.gate, P.g_dtype, (size_t)t * P.g_stride);
+        scale *= P.gate_sigmoid ? 1.f / (1.f + expf(-v)) : v;
+      }
+      if (P.post_norm) scale *= rsqrtf(row_sum<THREADS, false>(square(y), red[odd][0]) * per_column + P.eps);
+      const F2 f = f2(scale);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (by_column) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) y[j][e] = f2_mul(y[j][e], wy[j][e]);
+        }
+        if (per_row) {
+          F2 g[2];
+          sg.read(place + r_bytes + y_bytes + 4 * YB * tid, j, g);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (P.gate_sigmoid) {
+              float a, b;
+              f2_get(g[e], a, b);
+              g[e] = f2(__fdividef(1.f, 1.f + expf(-a)), __fdividef(1.f, 1.f + expf(-b)));
+            }
+            y[j][e] = f2_mul(y[j][e], g[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) r[j][e] = f2_fma(y[j][e], f, r[j][e]);
+      }
+    }
+    if (P.res_out) store(ro, R32, P.r_dtype, r);
+    if (P.normed) {
+      const F2 inv = f2(rsqrtf(row_sum<THREADS, false>(square(r), red[odd][1]) * per_column + P.eps));
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(y[j][e], y[j][e], q);
-      scale *= 1.f / sqrtf(row_sum<THREADS, WARP>(q, red[0]) / (float)P.H + P.eps);
+        for (int e = 0; e < 2; ++e) r[j][e] = f2_mul(f2_mul(r[j][e], inv), wn[j][e]);
+      store(no, N32, P.n_dtype, r);
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (AGAIN) cols.load(P.y, P.y_dtype, t * P.y_stride, j, y[j]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[j][e] *= scale;
-      if (P.post_norm && P.w_post) {
-        float* w = wp[ALL ? j : 0];
-        if (!ALL) cols.load(P.w_post, P.wpost_dtype, 0, j, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[j][e] *= P.w_offset + w[e];
-      }
-      if (per_column) {
-        float* v = g[ALL ? j : 0];
-        if (!ALL) cols.load(P.gate, P.g_dtype, g_row, j, v);
-        if (P.gate_sigmoid) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 1.f / (1.f + expf(-v[e]));
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[j][e] *= v[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[j][e] = fmaf(P.alpha, r[j][e], y[j][e]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[j][e] *= P.alpha;
-  }
-  if (P.res_out) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) cols.store(P.res_out, P.r_dtype, t * P.ro_stride, j, r[j]);
-  }
-  if (!P.normed) return;
-  float q = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    // columns past the row hold 0 times factors that may be infinite: they do
-    // not enter the sum
-    if (VEC && cols.at(j, 0) >= P.H) continue;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (VEC || cols.at(j, e) < P.H) q = fmaf(r[j][e], r[j][e], q);
-  }
-  const float inv = 1.f / sqrtf(row_sum<THREADS, WARP>(q, red[1]) / (float)P.H + P.eps);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[j][e] *= inv;
-    if (P.w_pre) {
-      float* w = wn[ALL ? j : 0];
-      if (!ALL) cols.load(P.w_pre, P.wpre_dtype, 0, j, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[j][e] *= P.w_offset + w[e];
-    }
-    cols.store(P.normed, P.n_dtype, t * P.n_stride, j, r[j]);
+    s = s + 1 == kStages ? 0 : s + 1;
+    odd ^= 1;
   }
 }
 
-// Rows of p start on 16-byte boundaries (an absent tensor always does).
-bool rows16(const void* p, int dtype, long long stride, int T) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (T == 1 || stride * elem_bytes(dtype) % 16 == 0));
+// Rows of p allow accesses of four elements (an absent tensor always does).
+bool rows4(const void* p, int dtype, long long stride, int T) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (4 * elem_bytes(dtype)) == 0 && (T == 1 || stride % 4 == 0));
 }
 
-template <int NV, int THREADS, bool ALL>
+template <int NV, int THREADS>
 cudaError_t launch(const NormParams& p, bool vec, cudaStream_t stream) {
   constexpr bool WARP = THREADS == kWarpRows;
   const dim3 grid(WARP ? (p.T + kRowsPerBlock - 1) / kRowsPerBlock : p.T);
   const int threads = WARP ? THREADS : (p.H + 256 * NV - 1) / (256 * NV) * 32;
-  return vec ? launch_behind(k_norm<NV, true, THREADS, ALL>, grid, threads, 0, stream, p)
-             : launch_behind(k_norm<NV, false, THREADS, ALL>, grid, threads, 0, stream, p);
+  return vec ? launch_behind(k_norm<NV, true, THREADS>, grid, threads, 0, stream, p)
+             : launch_behind(k_norm<NV, false, THREADS>, grid, threads, 0, stream, p);
+}
+
+// As many blocks as are resident at once.
+template <int NV, int THREADS, bool R32, bool Y32, bool N32>
+cudaError_t launch_rows_of(const NormParams& p, cudaStream_t stream) {
+  const int threads = (p.H + 128 * NV - 1) / (128 * NV) * 32;
+  const int each = (R32 ? 4 : 2) + (Y32 ? 4 : 2) * ((p.y ? 1 : 0) + (p.gate && p.gate_layout == 2 ? 1 : 0));
+  const int smem = kStages * threads * 4 * NV * each;
+  auto* const kern = k_norm_rows<NV, THREADS, R32, Y32, N32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int per_sm = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  if (e != cudaSuccess) return e;
+  const int blocks = p.sms * (per_sm > 0 ? per_sm : 1);
+  return launch_behind(kern, dim3(p.T < blocks ? p.T : blocks), threads, smem, stream, p);
+}
+
+template <int NV, int THREADS>
+cudaError_t launch_rows(const NormParams& p, cudaStream_t stream) {
+  const bool r32 = p.r_dtype == kF32, y32 = p.y && p.y_dtype == kF32, n32 = p.n_dtype == kF32;
+  if (r32)
+    return y32 ? n32 ? launch_rows_of<NV, THREADS, true, true, true>(p, stream)
+                     : launch_rows_of<NV, THREADS, true, true, false>(p, stream)
+               : n32 ? launch_rows_of<NV, THREADS, true, false, true>(p, stream)
+                     : launch_rows_of<NV, THREADS, true, false, false>(p, stream);
+  return y32 ? n32 ? launch_rows_of<NV, THREADS, false, true, true>(p, stream)
+                   : launch_rows_of<NV, THREADS, false, true, false>(p, stream)
+             : n32 ? launch_rows_of<NV, THREADS, false, false, true>(p, stream)
+                   : launch_rows_of<NV, THREADS, false, false, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
-  const bool vec = p.H % 8 == 0 && rows16(p.res, p.r_dtype, p.r_stride, p.T) &&
-                   rows16(p.res_out, p.r_dtype, p.ro_stride, p.T) && rows16(p.y, p.y_dtype, p.y_stride, p.T) &&
-                   rows16(p.normed, p.n_dtype, p.n_stride, p.T) && rows16(p.w_post, p.wpost_dtype, 0, 1) &&
-                   rows16(p.w_pre, p.wpre_dtype, 0, 1) &&
-                   (p.gate_layout == 1 || rows16(p.gate, p.g_dtype, p.gate_layout ? p.g_stride : 0, p.T));
-  if (p.H <= 256) return launch<1, kWarpRows, true>(p, vec, stream);
-  if (p.H <= 512) return launch<2, kWarpRows, false>(p, vec, stream);
-  // few rows: the latency of one row counts, a thread has 8 columns and loads
-  // all it needs at once; many: 16 columns a thread, fewer instructions a row
-  const bool few = p.T <= 2 * 152;
-  if (p.H <= 2048 && few) return launch<1, 256, true>(p, vec, stream);
-  if (p.H <= 8192 && few) return launch<1, 1024, true>(p, vec, stream);
-  if (p.H <= 4096) return launch<2, 256, false>(p, vec, stream);
-  if (p.H <= 8192) return launch<2, 512, false>(p, vec, stream);
-  if (p.H <= 16384) return launch<2, 1024, false>(p, vec, stream);
-  return launch<4, 1024, false>(p, vec, stream);
+  const bool vec = p.H % 4 == 0 && rows4(p.res, p.r_dtype, p.r_stride, p.T) &&
+                   rows4(p.res_out, p.r_dtype, p.ro_stride, p.T) && rows4(p.y, p.y_dtype, p.y_stride, p.T) &&
+                   rows4(p.normed, p.n_dtype, p.n_stride, p.T) && rows4(p.w_post, p.wpost_dtype, 0, 1) &&
+                   rows4(p.w_pre, p.wpre_dtype, 0, 1) &&
+                   (p.gate_layout == 1 || rows4(p.gate, p.g_dtype, p.gate_layout ? p.g_stride : 0, p.T));
+  if (p.H <= 256) return launch<1, kWarpRows>(p, vec, stream);
+  if (p.H <= 512) return launch<2, kWarpRows>(p, vec, stream);
+  if (p.H > 16384) return launch<4, 1024>(p, vec, stream);
+  if (p.H > 8192) return launch<2, 1024>(p, vec, stream);
+  // (the streaming kernel takes a gate of every element in y's size)
+  const bool gate_fits = !p.gate || p.gate_layout != 2 || (p.g_dtype == kF32) == (p.y_dtype == kF32);
+  if (vec && gate_fits && p.T > 4 * p.sms) {
+    if (p.H <= 2048) return launch_rows<4, 128>(p, stream);
+    if (p.H <= 4096) return launch_rows<4, 256>(p, stream);
+    return launch_rows<4, 512>(p, stream);
+  }
+  // few rows (each has a block of its own at once), or rows of any alignment
+  if (p.T > 4 * p.sms && p.H <= 4096) return launch<2, 256>(p, vec, stream);
+  return p.H <= 2048 ? launch<1, 256>(p, vec, stream) : launch<1, 1024>(p, vec, stream);
 }
 
 }  // namespace moe

@@ -54,16 +54,10 @@ struct Owned {
   int lpg, grp, n, e0;  // lanes a group, the lane's group, its experts e0 .. e0 + n - 1
 };
 
-// The lane's two largest c and, after the reduction, its group's: the group's
-// value on each of its lanes, -inf where the group has nothing left.
-template <int EPL, typename F>
-MOE_DEV F group_value(const F (&c)[EPL], int lpg, bool top2) {
-  F a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    a2 = fmax(a2, fmin(a1, c[i]));
-    a1 = fmax(a1, c[i]);
-  }
+// From the lane's two largest c the value of its group, on each of the group's
+// lanes; -inf where the group has nothing left.
+template <typename F>
+MOE_DEV F group_value(F a1, F a2, int lpg, bool top2) {
   for (int o = lpg >> 1; o; o >>= 1) {
     const F b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
     a2 = fmax(fmax(a2, b2), fmin(a1, b1));
@@ -83,58 +77,78 @@ MOE_DEV int group_rank(F val, int G, const Owned& o) {
   return rank;
 }
 
-// The choice in fp64 (bias present, or groups by two largest): lane j gets the
-// j-th expert and its logit.
-template <int EPL>
-MOE_DEV void choose_exact(const RouteParams& P, const float (&l)[EPL], const float (&b)[EPL], const Owned& o, int& id,
-                          float& lj) {
-  const int lane = threadIdx.x & 31;
-  double c[EPL];
-  double m = -INFINITY, z = 0.0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) m = fmax(m, (double)l[i]);
-  m = warp_max(m);
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    c[i] = 0.0;
-    if (l[i] != -INFINITY) c[i] = P.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - m);
-    z += c[i];
+// c of one expert in fp64.  Not inlined, and the loops around it not unrolled:
+// straight-line code that one warp runs once is paid for in instruction fetches
+// (the unrolled form held its SM for 30 us).
+__device__ __noinline__ double exact_c(bool sigmoid, float l, float b, double m, double z) {
+  const double e = exp(sigmoid ? -(double)l : (double)l - m);
+  return (sigmoid ? 1.0 / (1.0 + e) : e / z) + (double)b;
+}
+
+MOE_DEV float logit(const RouteParams& P, int t, int e) {
+  return clean(elem_load(P.logits, P.dtype, (size_t)t * P.stride + e));
+}
+MOE_DEV float bias_of(const RouteParams& P, int e) { return P.bias ? clean(P.bias[e]) : 0.f; }
+
+// The softmax's largest logit and sum in fp64.
+__device__ __noinline__ void exact_sum(const RouteParams& P, int t, const Owned& o, double& m, double& z) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < o.n; ++i) top = fmaxf(top, logit(P, t, o.e0 + i));
+  m = warp_max(top);
+  z = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < o.n; ++i) {
+    const float l = logit(P, t, o.e0 + i);
+    if (l != -INFINITY) z += exp((double)l - m);
   }
   z = warp_sum(z);
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    if (!P.sigmoid && z > 0.0) c[i] /= z;
-    c[i] = l[i] == -INFINITY || b[i] == -INFINITY ? -INFINITY : c[i] + (double)b[i];
-  }
-  if (P.G > 1 && group_rank(group_value(c, o.lpg, P.top2), P.G, o) >= P.top_groups) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = -INFINITY;
-  }
+}
+
+// The whole choice in fp64: lane j gets the j-th expert and its logit.
+template <int EPL>
+__device__ __noinline__ void choose_exact(const RouteParams& P, int t, const Owned& o, int& id, float& lj) {
+  const int lane = threadIdx.x & 31;
+  double m = 0.0, z = 1.0;
+  if (!P.sigmoid) exact_sum(P, t, o, m, z);
   // order keys of c (0: cannot be chosen): integer comparisons from here on
-  unsigned long long key[EPL], best = 0ull;
+  unsigned long long key[EPL];
+  double a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < o.n; ++i) {
+    const float l = logit(P, t, o.e0 + i), b = bias_of(P, o.e0 + i);
+    key[i] = 0ull;
+    if (l == -INFINITY || b == -INFINITY) continue;
+    const double c = exact_c(P.sigmoid, l, b, m, z);
+    a2 = fmax(a2, fmin(a1, c));
+    a1 = fmax(a1, c);
+    const unsigned long long u = (unsigned long long)__double_as_longlong(c + 0.0);
+    key[i] = u >> 63 ? ~u : u | 1ull << 63;
+  }
+  bool kept = true;
+  if (P.G > 1) kept = group_rank(group_value(a1, a2, o.lpg, P.top2), P.G, o) < P.top_groups;
+  unsigned long long best = 0ull;
   uint32_t best_l = 0u;
   int at = 0;
   auto local_best = [&]() {
     best = 0ull;
     best_l = 0u;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const uint32_t k = float_order_key(l[i]);
-      if (key[i] > best || (key[i] == best && key[i] != 0ull && k > best_l)) {
-        best = key[i];
+#pragma unroll 1
+    for (int i = 0; kept && i < o.n; ++i) {
+      // without a bias the logits decide inside the groups
+      const uint32_t k = float_order_key(logit(P, t, o.e0 + i));
+      const unsigned long long c = key[i] && !P.bias ? 1ull << 63 : key[i];
+      if (c > best || (c == best && c != 0ull && k > best_l)) {
+        best = c;
         best_l = k;
         at = i;
       }
     }
   };
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(c[i] + 0.0);
-    key[i] = c[i] == -INFINITY ? 0ull : u >> 63 ? ~u : u | 1ull << 63;
-  }
   local_best();
   id = -1;
   lj = -INFINITY;
+#pragma unroll 1
   for (int j = 0; j < P.K; ++j) {
     // the largest c, then the largest logit, then the lowest lane and slot
     const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(best >> 32));
@@ -150,9 +164,7 @@ MOE_DEV void choose_exact(const RouteParams& P, const float (&l)[EPL], const flo
       lj = key_float(lk);
     }
     if (lane == src) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == at) key[i] = 0ull;
+      key[at] = 0ull;
       local_best();
     }
   }
@@ -161,26 +173,13 @@ MOE_DEV void choose_exact(const RouteParams& P, const float (&l)[EPL], const flo
 // The n candidates on lanes 0 .. n - 1 (expert id, logit lj; with a bias), in
 // the order of their c in fp64: a lane forms one c, counts the candidates
 // before it and the candidates change lanes.
-template <int EPL>
-MOE_DEV void settle(const RouteParams& P, const float (&l)[EPL], int n, int& id, float& lj) {
+__device__ __noinline__ void settle(const RouteParams& P, int t, const Owned& o, int n, int& id, float& lj) {
   const int lane = threadIdx.x & 31;
-  double c = -INFINITY;
-  if (P.sigmoid) {
-    if (id >= 0) c = 1.0 / (1.0 + exp(-(double)lj));
-  } else {
-    float m = l[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
-    m = key_float(__reduce_max_sync(kAll, float_order_key(m)));
-    double z = 0.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (l[i] != -INFINITY) z += exp((double)l[i] - (double)m);
-    z = warp_sum(z);
-    if (id >= 0) c = exp((double)lj - (double)m) / z;
-  }
-  if (id >= 0) c += (double)clean(P.bias[id]);
+  double m = 0.0, z = 1.0, c = -INFINITY;
+  if (!P.sigmoid) exact_sum(P, t, o, m, z);
+  if (id >= 0) c = exact_c(P.sigmoid, lj, bias_of(P, id), m, z);
   int rank = 0;
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const double cj = __shfl_sync(kAll, c, j);
     const float l2 = __shfl_sync(kAll, lj, j);
@@ -188,6 +187,7 @@ MOE_DEV void settle(const RouteParams& P, const float (&l)[EPL], int n, int& id,
     rank += cj > c || (cj == c && (l2 > lj || (l2 == lj && e2 < id)));
   }
   int src = lane;
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int from = __ffs(__ballot_sync(kAll, lane < n && rank == j)) - 1;
     if (lane == j) src = from;
@@ -276,7 +276,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const __grid_constant__ R
   auto slack = [&](float v) { return smax * (P.sigmoid ? 0x1p-20f : 0x1p-16f) + fabsf(v) * 0x1p-22f + 0x1p-120f; };
   bool unsure = false;
   if (P.G > 1) {
-    const float val = group_value(c, P.lpg, P.top2);
+    float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      a2 = fmaxf(a2, fminf(a1, c[i]));
+      a1 = fmaxf(a1, c[i]);
+    }
+    const float val = group_value(a1, a2, P.lpg, P.top2);
     const int rank = group_rank(val, P.G, o);
     if (scored) {
       // the last group kept and the first one left out
@@ -344,15 +350,15 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const __grid_constant__ R
       // no lane left, and the next one is near the cut
       const uint32_t next = __reduce_max_sync(kAll, best);
       unsure = n == 32 && next != 0u && c_cut - key_float(next) <= slack(c_cut);
-      lj = id >= 0 ? clean(elem_load(P.logits, P.dtype, (size_t)t * P.stride + id)) : -INFINITY;
-      if (near && !unsure) settle<EPL>(P, l, n, id, lj);
+      lj = id >= 0 ? logit(P, t, id) : -INFINITY;
+      if (near && !unsure) settle(P, t, o, n, id, lj);
       if (lane >= P.K) {
         id = -1;
         lj = -INFINITY;
       }
     }
   }
-  if (unsure) choose_exact(P, l, b, o, id, lj);
+  if (unsure) choose_exact<EPL>(P, t, o, id, lj);
 
   // Weights from the chosen logits.  Renormalised, the softmax needs no other
   // logit, and the sigmoid is exp(l) to fp32's resolution where every chosen
