@@ -323,6 +323,15 @@ MOE_DEV void mask_rank(uint2& b, int left) {  // keep the first `left` of four e
   b.y &= left > 2 ? 0xFFFFu : 0u;
 }
 
+// One 16-wide step of the rank for 8 tokens: the two 16-row tiles of B against v.
+template <bool F16>
+MOE_DEV void mma_pair(const uint2 (&b)[4], uint2 vh, uint2 vl, float* d0, float* d1) {
+  mma16816(F16, d0, b[0].x, b[1].x, b[0].y, b[1].y, vl.x, vl.y);
+  mma16816(F16, d1, b[2].x, b[3].x, b[2].y, b[3].y, vl.x, vl.y);
+  mma16816(F16, d0, b[0].x, b[1].x, b[0].y, b[1].y, vh.x, vh.y);
+  mma16816(F16, d1, b[2].x, b[3].x, b[2].y, b[3].y, vh.x, vh.y);
+}
+
 // One 16-wide step of the rank: the lane's four rows of B (four k each) against
 // v of the tile's tokens (v: hi of the lane's token and k; lo_at further: lo).
 template <bool F16, int NT>
@@ -332,11 +341,7 @@ MOE_DEV void mma_step(const uint2 (&b)[4], const uint16_t* v, int lo_at, int n, 
     if (8 * j >= n) continue;
     const uint2 vh = *reinterpret_cast<const uint2*>(v + 8 * j * pitch);
     const uint2 vl = *reinterpret_cast<const uint2*>(v + 8 * j * pitch + lo_at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mma16816(F16, d[i][j], b[2 * i].x, b[2 * i + 1].x, b[2 * i].y, b[2 * i + 1].y, vl.x, vl.y);
-      mma16816(F16, d[i][j], b[2 * i].x, b[2 * i + 1].x, b[2 * i].y, b[2 * i + 1].y, vh.x, vh.y);
-    }
+    mma_pair<F16>(b, vh, vl, d[0][j], d[1][j]);
   }
 }
 
@@ -360,7 +365,10 @@ MOE_DEV void cp_async(void* dst, const void* src, bool valid) {
 // The first two rounds are asked for ahead of the wait on k_shrink, which
 // writes neither y nor B.  YK: y and out are fp32 (0) or 16-bit (1); rows allow
 // accesses of four elements, R % 4 == 0.
-template <bool F16, int NT, int YK>
+//
+// VS: steps of the rank whose v the lane keeps in registers (every round and
+// every warp reads the same), 0: read from shared memory in every round.
+template <bool F16, int NT, int YK, int VS>
 __global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ AdapterParams P) {
   constexpr int TILE = 8 * NT, YB = YK == 0 ? 16 : 8;
   extern __shared__ __align__(16) uint32_t vs[];  // v: [2][TILE][pitch / 2], then two stages
@@ -410,6 +418,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ 
   pdl_wait();
   pdl_launch_dependents();
   if (rank > 0) stage_v<F16, TILE>(P, list, a, n, rank, pitch, vs, s_scale);
+  const uint16_t* const v = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
+  uint2 vk[VS > 0 ? VS : 1][NT][2];
+  float scale[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int s = 0; s < VS; ++s) {
+      const bool has = s < steps && 8 * j < n;
+      vk[s][j][0] = has ? *reinterpret_cast<const uint2*>(v + 8 * j * pitch + 16 * s) : make_uint2(0u, 0u);
+      vk[s][j][1] = has ? *reinterpret_cast<const uint2*>(v + (8 * j + TILE) * pitch + 16 * s) : make_uint2(0u, 0u);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) scale[j][h] = row[j][h] >= 0 && rank > 0 ? s_scale[8 * j + 2 * q + h] : 0.f;
+  }
   for (int c0 = c_first, stage = 0; c0 < c_end; c0 += kThreads, stage ^= 1) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     const int n0 = c0 + col;
@@ -422,22 +444,37 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ 
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
-      const uint16_t* v = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
-      for (int s = 0; s < steps; ++s) {
-        uint2 bv[4];
+      auto rows_of_b = [&](int s, uint2 (&bv)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           bv[c] = *reinterpret_cast<const uint2*>(bs + (4 * s + c) * kThreads * 8);
           mask_rank(bv[c], rank - 16 * s - 4 * q);
         }
-        mma_step<F16, NT>(bv, v + 16 * s, TILE * pitch, n, d, pitch);
+      };
+      if (VS > 0) {
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          if (s >= steps) break;
+          uint2 bv[4];
+          rows_of_b(s, bv);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (8 * j >= n) continue;
+            mma_pair<F16>(bv, vk[s][j][0], vk[s][j][1], d[0][j], d[1][j]);
+          }
+        }
+      } else {
+        for (int s = 0; s < steps; ++s) {
+          uint2 bv[4];
+          rows_of_b(s, bv);
+          mma_step<F16, NT>(bv, v + 16 * s, TILE * pitch, n, d, pitch);
+        }
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (row[j][h] < 0 || n0 >= c_end) continue;
-          const float s = rank > 0 ? s_scale[8 * j + 2 * q + h] : 0.f;
           const uint8_t* yp = ys + (2 * j + h) * kThreads * YB;
           float y[4];
           if (YK == 0) {
@@ -449,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_expand(const __grid_constant__ 
             unpack2(P.y_dtype, u.y, y[2], y[3]);
           }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) y[c] = fmaf(s, d[c >> 1][j][2 * (c & 1) + h], y[c]);
+          for (int c = 0; c < 4; ++c) y[c] = fmaf(scale[j][h], d[c >> 1][j][2 * (c & 1) + h], y[c]);
           uint8_t* o = static_cast<uint8_t*>(P.out) + ((size_t)row[j][h] * P.out_stride + n0) * (YB / 4);
           if (YK == 0)
             *reinterpret_cast<float4*>(o) = make_float4(y[0], y[1], y[2], y[3]);
@@ -569,7 +606,8 @@ cudaError_t launch_tiles(const AdapterParams& p, int blocks, cudaStream_t stream
     }
     return launch_behind(kern, eg, kThreads, smem, stream, p);
   };
-  return p.y_dtype == kF32 ? ring(k_expand<F16, NT, 0>, 16) : ring(k_expand<F16, NT, 1>, 8);
+  if (p.R <= 32) return p.y_dtype == kF32 ? ring(k_expand<F16, NT, 0, 2>, 16) : ring(k_expand<F16, NT, 1, 2>, 8);
+  return p.y_dtype == kF32 ? ring(k_expand<F16, NT, 0, 0>, 16) : ring(k_expand<F16, NT, 1, 0>, 8);
 }
 
 }  // namespace

@@ -558,6 +558,7 @@ int moe_ffn_route(const moe_ffn_route_args* a, moe_ffn_stream_t stream, const vo
   P.K = a->top_k;
   P.G = a->top_groups == a->groups ? 1 : a->groups;  // every group kept: no group stage
   P.gs = a->E / P.G;
+  P.sms = sms;
   P.top_groups = a->top_groups;
   P.sigmoid = a->score == MOE_FFN_SCORE_SIGMOID;
   P.top2 = a->group_score == MOE_FFN_GROUP_TOP2;

@@ -259,9 +259,9 @@ constexpr int kNormMaxH = 32768;
 constexpr int kAdapterMaxRank = 128;
 
 struct RouteParams {
-  int T, E, K, G, gs, top_groups;  // gs experts a group
+  int T, E, K, G, gs, top_groups, sms;  // gs experts a group
   int sigmoid, top2, renorm, dtype;
-  int lpg, per, vec;  // set by the launch: lanes a group, experts a lane, loads of four experts
+  int lpg_log, per, vec;  // set by the launch: lanes a group (log2), experts a lane, loads of four experts
   float scale;
   long long stride;
   const void* logits;

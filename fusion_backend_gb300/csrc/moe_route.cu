@@ -6,20 +6,21 @@
 // with EPL or fewer consecutive experts, so a lower lane (then a lower slot)
 // is a lower index and a group's value is a reduction over its lanes.
 //
-// The choice is made on fp32 keys: one warp maximum a round (the hardware's
-// reduction over order keys), only the winner's lane looks for its next best.
-// Without a bias the key is the logit itself, since the scores rise with it:
+// The choice is made on fp32 values: the K-th largest of the lanes' largest
+// bounds the candidates (K or somewhat more), which then lie one a lane and count
+// those before them; a round a choice (warp maximum, its lane's next best)
+// took twice the instructions, and the kernel is bound by those for many tokens.
+// Without a bias the value is the logit itself, since the scores rise with it:
 // the choice is then exact, and scores are formed only where the groups or the
-// weights need them.  With a bias the key is c = s + b in fp32, which is off by
-// less than `slack` (below); where two neighbours in the order of the choice
-// lie closer than that, the candidates' c are formed and ordered in fp64, one a
-// lane, and where the groups on the two sides of the cut do (or more candidates
-// than lanes), the warp makes the whole choice again in fp64.  The first is one
-// token in some hundreds on logits of a spread of two, the second one in
-// thousands; fp64 for every token, the first form of this kernel, ran 176 us on
-// 4096 tokens x 256 experts and 536 us on 16381 x 200, and the whole choice in
-// fp64 for every near pair still 36 and 48 us (the GPU's fp64 rate is a small
-// share of its fp32 rate, and one such token is all that an SM waits for).
+// weights need them.  With a bias it is c = s + b in fp32, which is off by less
+// than `slack` (below); where two neighbours in the order of the choice lie closer
+// than that, the candidates' c are formed and ordered in fp64, one a lane, and
+// where the groups on the two sides of the cut do (or more candidates than
+// lanes), the warp makes the whole choice again in fp64.  The first is one token
+// in some hundreds on logits of a spread of two, the second one in thousands;
+// fp64 for every token, the first form of this kernel, ran 176 us on 4096 tokens
+// x 256 experts and 536 us on 16381 x 200 (the GPU's fp64 rate is a small share
+// of its fp32 rate, and one such token is all that an SM waits for).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -77,7 +78,14 @@ MOE_DEV int group_rank(F val, int G, const Owned& o) {
   return rank;
 }
 
-// c of one expert in fp64.  Not inlined, and the loops around it not unrolled:
+// Monotone map double -> unsigned (-0 as +0): the order of c by integer
+// comparisons, fp64 ones have a latency of 64 cycles here.
+MOE_DEV unsigned long long order_key64(double v) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+
+// c of one expert in fp64 (about 1500 cycles).  Not inlined, and the loops around it not unrolled:
 // straight-line code that one warp runs once is paid for in instruction fetches
 // (the unrolled form held its SM for 30 us).
 __device__ __noinline__ double exact_c(bool sigmoid, float l, float b, double m, double z) {
@@ -97,7 +105,7 @@ __device__ __noinline__ void exact_sum(const RouteParams& P, int t, const Owned&
   for (int i = 0; i < o.n; ++i) top = fmaxf(top, logit(P, t, o.e0 + i));
   m = warp_max(top);
   z = 0.0;
-#pragma unroll 1
+#pragma unroll 4
   for (int i = 0; i < o.n; ++i) {
     const float l = logit(P, t, o.e0 + i);
     if (l != -INFINITY) z += exp((double)l - m);
@@ -122,8 +130,7 @@ __device__ __noinline__ void choose_exact(const RouteParams& P, int t, const Own
     const double c = exact_c(P.sigmoid, l, b, m, z);
     a2 = fmax(a2, fmin(a1, c));
     a1 = fmax(a1, c);
-    const unsigned long long u = (unsigned long long)__double_as_longlong(c + 0.0);
-    key[i] = u >> 63 ? ~u : u | 1ull << 63;
+    key[i] = order_key64(c);
   }
   bool kept = true;
   if (P.G > 1) kept = group_rank(group_value(a1, a2, o.lpg, P.top2), P.G, o) < P.top_groups;
@@ -178,13 +185,15 @@ __device__ __noinline__ void settle(const RouteParams& P, int t, const Owned& o,
   double m = 0.0, z = 1.0, c = -INFINITY;
   if (!P.sigmoid) exact_sum(P, t, o, m, z);
   if (id >= 0) c = exact_c(P.sigmoid, lj, bias_of(P, id), m, z);
+  const unsigned long long key = order_key64(c);
+  const uint32_t lk = float_order_key(lj);
   int rank = 0;
-#pragma unroll 1
+#pragma unroll 2
   for (int j = 0; j < n; ++j) {
-    const double cj = __shfl_sync(kAll, c, j);
-    const float l2 = __shfl_sync(kAll, lj, j);
+    const unsigned long long k2 = __shfl_sync(kAll, key, j);
+    const uint32_t l2 = __shfl_sync(kAll, lk, j);
     const int e2 = __shfl_sync(kAll, id, j);
-    rank += cj > c || (cj == c && (l2 > lj || (l2 == lj && e2 < id)));
+    rank += k2 > key || (k2 == key && (l2 > lk || (l2 == lk && e2 < id)));
   }
   int src = lane;
 #pragma unroll 1
@@ -196,194 +205,321 @@ __device__ __noinline__ void settle(const RouteParams& P, int t, const Owned& o,
   lj = __shfl_sync(kAll, lj, src);
 }
 
+// The K best (and, with a bias, those near the cut) one a round, when there are
+// too many candidates for one a lane: every lane offers its best.
+template <int EPL, typename Slack>
+MOE_DEV void choose_rounds(const RouteParams& P, float (&c)[EPL], const Owned& o, bool biased, Slack slack, int& n,
+                           int& id, float& cj, bool& unsure) {
+  const int lane = threadIdx.x & 31;
+  id = -1;
+  cj = -INFINITY;
+  float cut = INFINITY;
+  float best;
+  int at;
+  auto local_best = [&]() {
+    best = -INFINITY;
+    at = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (c[i] > best) {
+        best = c[i];
+        at = i;
+      }
+  };
+  local_best();
+#pragma unroll 1
+  for (n = 0; n < (biased ? 32 : P.K); ++n) {
+    const float top = key_float(__reduce_max_sync(kAll, float_order_key(best)));
+    if (top == -INFINITY || (n >= P.K && cut - top > slack(cut))) break;
+    const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    const int e = __shfl_sync(kAll, o.e0 + at, src);
+    if (n < P.K) cut = top;
+    if (lane == n) {
+      id = e;
+      cj = top;
+    }
+    if (lane == src) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i == at) c[i] = -INFINITY;
+      local_best();
+    }
+  }
+  // no lane left, and the next one is near the cut
+  const float next = key_float(__reduce_max_sync(kAll, float_order_key(best)));
+  unsure = biased && n == 32 && next != -INFINITY && cut - next <= slack(cut);
+}
+
+// Values of the groups on the two sides of the cut in fp64: true if the one left
+// out comes before the other.  c: fp32, off by less than `err`; only a group's
+// experts that may be among its two largest are formed again.
 template <int EPL>
-__global__ void __launch_bounds__(32 * kWarps) k_route(const __grid_constant__ RouteParams P) {
-  const int lane = threadIdx.x & 31, t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+MOE_DEV bool border_swaps(const RouteParams& P, int t, const Owned& o, const float (&c)[EPL], float a1, float a2,
+                          float err, int in_grp, int out_grp) {
+  double m = 0.0, z = 1.0;
+  if (!P.sigmoid) exact_sum(P, t, o, m, z);
+  // the group's two largest in fp32, on its lanes
+  for (int d = o.lpg >> 1; d; d >>= 1) {
+    const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+    a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
+    a1 = fmaxf(a1, b1);
+  }
+  const float least = (P.top2 && a2 != -INFINITY ? a2 : a1) - err;
+  uint32_t todo = 0u;  // of the lane's experts
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (EPL <= 32 && (o.grp == in_grp || o.grp == out_grp) && c[i] != -INFINITY && c[i] >= least) todo |= 1u << i;
+  double x1 = -INFINITY, x2 = -INFINITY;
+  while (__any_sync(kAll, todo != 0u)) {
+    if (todo) {
+      const int e = o.e0 + __ffs(todo) - 1;
+      const double x = exact_c(P.sigmoid, logit(P, t, e), bias_of(P, e), m, z);
+      x2 = fmax(x2, fmin(x1, x));
+      x1 = fmax(x1, x);
+      todo &= todo - 1u;
+    }
+    __syncwarp();
+  }
+  const double val = group_value(x1, x2, o.lpg, P.top2);
+  const double vi = __shfl_sync(kAll, val, in_grp * o.lpg), vo = __shfl_sync(kAll, val, out_grp * o.lpg);
+  return vo > vi || (vo == vi && out_grp < in_grp);
+}
+
+template <int EPL>
+__global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const __grid_constant__ RouteParams P) {
+  __shared__ float2 s_cand[kWarps][32];  // a candidate's c and id
+  __shared__ float s_logit[kWarps][32];  // and its logit
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float2* const cand = s_cand[warp];
+  float* const cand_l = s_logit[warp];
   Owned o;
-  o.lpg = P.lpg;
-  o.grp = lane / P.lpg;
-  const int first = (lane - o.grp * P.lpg) * P.per;
+  o.lpg = 1 << P.lpg_log;
+  o.grp = lane >> P.lpg_log;
+  const int first = (lane & (o.lpg - 1)) * P.per;
   o.n = o.grp < P.G ? max(0, min(P.per, P.gs - first)) : 0;
   o.e0 = o.grp * P.gs + first;
   pdl_wait();
   pdl_launch_dependents();
-  if (t >= P.T) return;
-
-  float l[EPL], b[EPL], c[EPL];
-  const size_t row = (size_t)t * P.stride + o.e0;
-  if (EPL >= 4 && P.vec) {
-#pragma unroll
-    for (int i = 0; i + 4 <= EPL; i += 4) {
-      l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
-      if (i < o.n) {
-        if (P.dtype == kF32) {
-          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(P.logits) + row + i);
-          l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.logits) + row + i);
-          if (P.dtype == kBf16) {
-            l[i] = bf16_lo(v.x), l[i + 1] = bf16_hi(v.x), l[i + 2] = bf16_lo(v.y), l[i + 3] = bf16_hi(v.y);
-          } else {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-            l[i] = p.x, l[i + 1] = p.y, l[i + 2] = q.x, l[i + 3] = q.y;
-          }
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = i < o.n ? elem_load(P.logits, P.dtype, row + i) : -INFINITY;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    l[i] = clean(l[i]);
-    b[i] = P.bias && i < o.n ? clean(P.bias[o.e0 + i]) : 0.f;
-  }
-  // c in fp32 (the logit where the choice can go by it), the softmax's sum
   const bool biased = P.bias != nullptr;
-  const bool scored = biased || (P.G > 1 && P.top2);   // c holds scores
-  float m = 0.f, z = 1.f, smax = 1.f;
-  if (!P.sigmoid && (scored || !P.renorm)) {
-    m = l[0];
+  const bool scored = biased || (P.G > 1 && P.top2);  // c holds scores
+  float b[EPL];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
-    m = key_float(__reduce_max_sync(kAll, float_order_key(m)));
-    z = 0.f;
+  for (int i = 0; i < EPL; ++i) b[i] = biased && i < o.n ? clean(P.bias[o.e0 + i]) : 0.f;
+
+  // a token's logits as they lie in memory: those of the warp's next token are
+  // asked for before it works on one
+  uint32_t w[EPL];
+  auto ask = [&](int t) {
+    if (t >= P.T) return;
+    const size_t row = (size_t)t * P.stride + o.e0;
+    if (EPL >= 4 && P.vec) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      c[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
-      z += c[i];
-    }
-    z = warp_sum(z);
-    smax = 1.f / z;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    if (!scored)
-      c[i] = l[i];
-    else if (l[i] == -INFINITY || b[i] == -INFINITY)
-      c[i] = -INFINITY;
-    else
-      c[i] = (P.sigmoid ? __fdividef(1.f, 1.f + expf(-l[i])) : c[i] * smax) + b[i];
-  }
-  // How far apart two fp32 values of c have to be for their order to be that of
-  // fp64.  Sigmoid: exp, sum and quotient are off by less than 2^-21 of s <= 1
-  // together.  Softmax: the exponent's argument rounds by |x| 2^-24 (and
-  // exp(-|x|) |x| < 1), exp, the sum of EPL terms a lane and 5 levels, the
-  // reciprocal and the product: less than 2^-17 of the largest s.  Both sides of
-  // a comparison count, and the rounding of s + b: 2^-24 |c| each.
-  auto slack = [&](float v) { return smax * (P.sigmoid ? 0x1p-20f : 0x1p-16f) + fabsf(v) * 0x1p-22f + 0x1p-120f; };
-  bool unsure = false;
-  if (P.G > 1) {
-    float a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      a2 = fmaxf(a2, fminf(a1, c[i]));
-      a1 = fmaxf(a1, c[i]);
-    }
-    const float val = group_value(a1, a2, P.lpg, P.top2);
-    const int rank = group_rank(val, P.G, o);
-    if (scored) {
-      // the last group kept and the first one left out
-      const uint32_t in = __ballot_sync(kAll, o.grp < P.G && rank == P.top_groups - 1);
-      const uint32_t out = __ballot_sync(kAll, o.grp < P.G && rank == P.top_groups);
-      const float vi = __shfl_sync(kAll, val, __ffs(in) - 1), vo = __shfl_sync(kAll, val, __ffs(out) - 1);
-      unsure = vo != -INFINITY && vi - vo <= 2.f * slack(vi);
-    }
-    if (!scored || biased) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) c[i] = rank < P.top_groups ? c[i] : -INFINITY;
-    } else {  // no bias: the choice inside the groups goes by the logits
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) c[i] = rank < P.top_groups ? l[i] : -INFINITY;
-    }
-  }
-  // The choice.  Every lane holds the order key of its best expert (0: none).
-  uint32_t key[EPL], best = 0u;
-  int at = 0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    key[i] = c[i] == -INFINITY ? 0u : float_order_key(c[i]);
-    if (key[i] > best) {
-      best = key[i];
-      at = i;
-    }
-  }
-  int id = -1;
-  float lj = -INFINITY;
-  if (!unsure) {
-    // With a bias, rounds go on behind the K-th until one is clearly below it
-    // (while a lane is free to hold it).
-    float c_last = INFINITY, c_cut = INFINITY;
-    bool near = false;
-    int n = 0;
-    for (; n < (biased ? 32 : P.K); ++n) {
-      const uint32_t top = __reduce_max_sync(kAll, best);
-      if (top == 0u) break;
-      const float cj = key_float(top);
-      if (n >= P.K && c_cut - cj > slack(c_cut)) break;
-      const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
-      const int e = __shfl_sync(kAll, o.e0 + at, src);
-      near |= c_last - cj <= slack(cj);
-      c_last = cj;
-      if (n < P.K) c_cut = cj;
-      if (lane == n) {
-        id = e;
-        lj = cj;
-      }
-      if (lane == src) {
-        best = 0u;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          if (i == at) key[i] = 0u;
+      for (int i = 0; i + 4 <= EPL; i += 4)
+        if (i < o.n) {
+          const uint4 v = raw_load4(P.logits, P.dtype, row + i);
+          w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i < o.n) w[i] = raw_load(P.logits, P.dtype, row + i);
+    }
+  };
+  ask(blockIdx.x * kWarps + warp);
+  for (int t = blockIdx.x * kWarps + warp; t < P.T; t += gridDim.x * kWarps) {
+    float l[EPL], c[EPL];
+    if (EPL >= 4 && P.vec) {
+#pragma unroll
+      for (int i = 0; i + 4 <= EPL; i += 4)
+        raw_values4(make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]), P.dtype, l + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] = raw_value(w[i], P.dtype);
+    }
+    ask(t + gridDim.x * kWarps);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = i < o.n ? clean(l[i]) : -INFINITY;
+    // c in fp32 (the logit where the choice can go by it), the softmax's sum
+    float m = 0.f, z = 1.f, smax = 1.f;
+    if (!P.sigmoid && (scored || !P.renorm)) {
+      m = l[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+      m = key_float(__reduce_max_sync(kAll, float_order_key(m)));
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        c[i] = l[i] == -INFINITY ? 0.f : __expf(l[i] - m);
+        z += c[i];
+      }
+      z = warp_sum(z);
+      smax = 1.f / z;
+    }
+    if (!scored) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = l[i];
+    } else {
+      if (P.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] = __fdividef(1.f, 1.f + __expf(-l[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] *= smax;
+      }
+      // (a bias of -inf masks by itself)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = l[i] == -INFINITY ? -INFINITY : c[i] + b[i];
+    }
+    // How far apart two fp32 values of c have to be for their order to be that of
+    // fp64, in units of 2^-24.  Sigmoid: the fast exp is off by 4 and 2 |l|
+    // relative, which s takes up times 1 - s (|l| s (1 - s) < 1/4), sum and
+    // quotient by 4: less than 8 of s <= 1.  Softmax, of the largest s: exp by 4
+    // and 2 |x| (exp(-|x|) |x| < 1/2), the sum of such terms by 4 and twice their
+    // mean |x| (at most ln E < 7) and its EPL + 5 additions, the reciprocal and
+    // the product 3: less than EPL + 32.  Both sides of a comparison count, and
+    // the rounding of s + b: |c| each.
+    constexpr float kSoft = (2 * EPL + 64) * 0x1p-24f;
+    auto slack = [&](float v) { return smax * (P.sigmoid ? 0x1p-20f : kSoft) + fabsf(v) * 0x1p-22f + 0x1p-120f; };
+    bool unsure = false;
+    if (P.G > 1) {
+      float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        a2 = fmaxf(a2, fminf(a1, c[i]));
+        a1 = fmaxf(a1, c[i]);
+      }
+      const float val = group_value(a1, a2, o.lpg, P.top2);
+      int rank = group_rank(val, P.G, o);
+      if (scored) {
+        // the last group kept, the first one left out and their neighbours
+        auto at_rank = [&](int k, int& g) {
+          const uint32_t who = __ballot_sync(kAll, o.grp < P.G && rank == k);
+          g = (__ffs(who) - 1) >> P.lpg_log;
+          return who ? __shfl_sync(kAll, val, __ffs(who) - 1) : k < 0 ? INFINITY : -INFINITY;
+        };
+        int gi, go, g;
+        const float vi = at_rank(P.top_groups - 1, gi), vo = at_rank(P.top_groups, go);
+        const float err = 2.f * slack(vi);
+        if (vo != -INFINITY && vi - vo <= err) {
+          const float before = at_rank(P.top_groups - 2, g), after = at_rank(P.top_groups + 1, g);
+          if (EPL > 32 || before - vo <= err || vi - after <= err)
+            unsure = true;  // more than two
+          else if (border_swaps<EPL>(P, t, o, c, a1, a2, err, gi, go))
+            rank = o.grp == gi ? P.top_groups : o.grp == go ? P.top_groups - 1 : rank;
+        }
+      }
+      // no bias: the choice inside the groups goes by the logits
+      const bool kept = rank < P.top_groups;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = !kept ? -INFINITY : biased ? c[i] : l[i];
+    }
+    // The choice.  The K-th largest of the lanes' largest c bounds the K-th
+    // largest c from below: what reaches it (with a bias: to within the slack)
+    // are the candidates, K or somewhat more, and with one a lane each counts
+    // those before it.
+    int id = -1, n = 0;
+    float cj = -INFINITY, lj = -INFINITY;
+    if (!unsure) {
+      float top = c[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) top = fmaxf(top, c[i]);
+      uint32_t key = float_order_key(top), bar_key = 0u;
+      for (int have = 0; have < P.K;) {
+        bar_key = __reduce_max_sync(kAll, key);
+        const bool mine = key == bar_key;
+        have += __popc(__ballot_sync(kAll, mine));
+        key = mine ? 0u : key;  // (below every float's key)
+      }
+      float bar = key_float(bar_key);
+      if (biased) bar -= slack(bar);
+      bar = fmaxf(bar, -kFltMax);  // -inf: not a candidate
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) mine += c[i] >= bar;
+      int at = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(kAll, at, d);
+        if (lane >= d) at += v;
+      }
+      n = __shfl_sync(kAll, at, 31);
+      at -= mine;
+      if (n <= 32) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (key[i] > best) {
-            best = key[i];
-            at = i;
+          if (c[i] >= bar) {
+            cand[at] = make_float2(c[i], __int_as_float(o.e0 + i));
+            cand_l[at++] = l[i];
           }
       }
-    }
-    if (biased) {
-      // no lane left, and the next one is near the cut
-      const uint32_t next = __reduce_max_sync(kAll, best);
-      unsure = n == 32 && next != 0u && c_cut - key_float(next) <= slack(c_cut);
-      lj = id >= 0 ? logit(P, t, id) : -INFINITY;
-      if (near && !unsure) settle(P, t, o, n, id, lj);
-      if (lane >= P.K) {
-        id = -1;
-        lj = -INFINITY;
+      __syncwarp();
+      if (n <= 32) {
+        if (lane < n) {
+          const float2 v = cand[lane];
+          cj = v.x;
+          id = __float_as_int(v.y);
+          lj = cand_l[lane];
+        }
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const float2 v = cand[j];
+          rank += v.x > cj || (v.x == cj && __float_as_int(v.y) < id);
+        }
+        __syncwarp();
+        if (lane < n) {
+          cand[rank] = make_float2(cj, __int_as_float(id));
+          cand_l[rank] = lj;
+        }
+        __syncwarp();
+        if (lane < n) {
+          const float2 v = cand[lane];
+          cj = v.x;
+          id = __float_as_int(v.y);
+          lj = cand_l[lane];
+        }
+        __syncwarp();
+      } else {
+        choose_rounds<EPL>(P, c, o, biased, slack, n, id, cj, unsure);
+        lj = id >= 0 ? logit(P, t, id) : -INFINITY;
       }
     }
-  }
-  if (unsure) choose_exact<EPL>(P, t, o, id, lj);
+    if (biased && !unsure) {
+      // neighbours closer than the slack: the candidates change places by fp64
+      const float next = __shfl_down_sync(kAll, cj, 1);
+      if (__any_sync(kAll, lane + 1 < n && cj - next <= slack(cj))) settle(P, t, o, n, id, lj);
+    }
+    if (unsure) choose_exact<EPL>(P, t, o, id, lj);
+    if (lane >= P.K) {
+      id = -1;
+      lj = -INFINITY;
+    }
 
-  // Weights from the chosen logits.  Renormalised, the softmax needs no other
-  // logit, and the sigmoid is exp(l) to fp32's resolution where every chosen
-  // logit is far below 0 (the ratio is then formed before it can underflow).
-  float v = 0.f;
-  if (P.renorm) {
-    const float top = warp_max(lj);
-    if (id >= 0) v = !P.sigmoid || top < -60.f ? expf(lj - top) : 1.f / (1.f + expf(-lj));
-    const float total = warp_sum(v);
-    if (id >= 0) v = v / total;
-  } else if (id >= 0) {
-    v = P.sigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - m) / z;
-  }
-  if (lane < P.K) {
-    P.ids[(size_t)t * P.K + lane] = id;
-    P.w[(size_t)t * P.K + lane] = v * P.scale;
+    // Weights from the chosen logits.  Renormalised, the softmax needs no other
+    // logit, and the sigmoid is exp(l) to fp32's resolution where every chosen
+    // logit is far below 0 (the ratio is then formed before it can underflow).
+    float v = 0.f;
+    if (P.renorm) {
+      const float top = warp_max(lj);
+      if (id >= 0) v = !P.sigmoid || top < -60.f ? expf(lj - top) : 1.f / (1.f + expf(-lj));
+      const float total = warp_sum(v);
+      if (id >= 0) v = __fdividef(v, total);
+    } else if (id >= 0) {
+      v = P.sigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - m) / z;
+    }
+    if (lane < P.K) {
+      P.ids[(size_t)t * P.K + lane] = id;
+      P.w[(size_t)t * P.K + lane] = v * P.scale;
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_route(RouteParams p, cudaStream_t stream) {
-  p.lpg = 32;
-  for (int g = 1; g < p.G; g <<= 1) p.lpg >>= 1;
-  p.per = (p.gs + p.lpg - 1) / p.lpg;
+  p.lpg_log = 5;
+  for (int g = 1; g < p.G; g <<= 1) --p.lpg_log;
+  p.per = (p.gs + (1 << p.lpg_log) - 1) >> p.lpg_log;
   // four experts a load: rows, groups and lanes start on a load's boundary
   if (p.per > 2) {
     const int per4 = (p.per + 3) & ~3;
@@ -391,7 +527,9 @@ cudaError_t launch_route(RouteParams p, cudaStream_t stream) {
     p.vec = p.gs % 4 == 0 && p.stride % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % bytes == 0;
     if (p.vec) p.per = per4;
   }
-  const dim3 grid((p.T + kWarps - 1) / kWarps);
+  // a warp goes through several tokens where there are more than run at once
+  const int blocks = (p.T + kWarps - 1) / kWarps, most = 6 * p.sms;
+  const dim3 grid(blocks < most ? blocks : most);
   const int threads = 32 * kWarps;
   if (p.per <= 2) return launch_behind(k_route<2>, grid, threads, 0, stream, p);
   if (p.per <= 4) return launch_behind(k_route<4>, grid, threads, 0, stream, p);
