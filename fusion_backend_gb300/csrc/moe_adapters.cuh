@@ -1,0 +1,542 @@
+#pragma once
+
+// Low-rank adapters of many requests beside a shared projection
+// (moe_ffn_add_adapters): v_t = A_a x_t (k_shrink), then
+// out_t = y_t + scale_a B_a v_t (k_expand).
+//
+// Both products run on tiles of up to 8 or 64 tokens that share an adapter, as
+// mma.m16n8k16 with the adapter's rows as the 16 A rows and the tokens as the
+// B columns, fp32 accumulators, operands straight from global memory: a lane
+// takes 16 (A, x) or 8 (B) consecutive bytes of a row and the k index of the
+// product is permuted alike on both sides, so every 32-byte sector read is used
+// whole.  The work is bound by bytes (x, y, out once; an adapter once a tile),
+// at R = 64 by 64 flops a byte: far below what the warp-level instructions
+// give, so the tiles need no shared-memory staging or tensor memory.
+//
+// Tiles.  Up to kScanT tokens: block t looks through all adapter ids and owns a
+// tile if its token is the first, 9th (65th), .. of its adapter.  More tokens:
+// k_order ranks the tokens of each window of kWindow by adapter (counting, all
+// against all, spread over 32 blocks; a bitonic sort of the window in one block
+// took 12 us) and marks the places where a tile starts; block s of a window then
+// finds the s-th mark.
+//
+// K is split over the warps of a block and, where there are few tiles, over
+// blocks; the parts are summed in a fixed order.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_elem.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kScanT = 64;            // two ids a lane
+constexpr int kWindow = 1024;
+constexpr int kRankChunk = 64;        // rows of A a block of k_shrink takes
+
+// Elements between two tokens' v in shared memory: 32 modulo 64 bytes, no bank
+// conflicts.
+__host__ __device__ constexpr int expand_pitch(int R) { return (R + 15) / 16 % 2 ? (R + 15) / 16 * 16 : (R + 15) / 16 * 16 + 16; }
+
+MOE_DEV int adapter_of(const AdapterParams& P, int t) {
+  const int a = P.ids[t];
+  return a < 0 || a >= P.n ? -1 : a;
+}
+MOE_DEV int adapter_rank(const AdapterParams& P, int a) {
+  if (a < 0) return 0;
+  return P.ranks ? max(0, min(P.R, P.ranks[a])) : P.R;
+}
+
+// d += A B (ZERO: d = A B), one m16n8k16.
+template <bool F16, bool ZERO = false>
+MOE_DEV void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  const float c0 = ZERO ? 0.f : d[0], c1 = ZERO ? 0.f : d[1], c2 = ZERO ? 0.f : d[2], c3 = ZERO ? 0.f : d[3];
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// The tile of this block (blockIdx.x): its adapter (-1: none), its tokens in
+// `list`; false where the block has no tile.
+template <int TILE>
+MOE_DEV bool find_tile(const AdapterParams& P, int* list, int& a, int& n) {
+  __shared__ int s_tile[2];  // adapter, tokens
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    n = 0;
+    a = -1;
+    if (P.T > kScanT) {
+      // the s-th mark of window w: 32 marks a lane
+      const int w = blockIdx.x / P.slots, s = blockIdx.x - w * P.slots;
+      const int t0 = w * kWindow, len = min(kWindow, P.T - t0);
+      uint32_t m[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const int at = 32 * lane + 4 * i;
+        if (at < len) v = *reinterpret_cast<const uint4*>(P.marks + t0 + at);  // (marks are padded to 16 bytes)
+        m[i] = v.x, m[i + 1] = v.y, m[i + 2] = v.z, m[i + 3] = v.w;
+      }
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = 32 * lane + 4 * i + e;
+          if (at >= len) m[i] &= ~(0xFFu << (8 * e));
+          c += (m[i] >> (8 * e) & 0xFFu) != 0u;
+        }
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      int skip = s - (incl - c), place = 0;  // the lane's mark of that number
+      if (skip >= 0 && skip < c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int v = m[i] >> (8 * e) & 0xFFu;
+            if (v && skip-- == 0) {
+              n = v;
+              place = t0 + 32 * lane + 4 * i + e;
+            }
+          }
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, n > 0);
+      if (who) {
+        n = __shfl_sync(0xffffffffu, n, __ffs(who) - 1);
+        place = __shfl_sync(0xffffffffu, place, __ffs(who) - 1);
+        for (int i = lane; i < n; i += 32) list[i] = P.order[place + i];
+        a = P.adapter_at[place];
+      }
+    } else {
+      const int t = blockIdx.x;
+      a = adapter_of(P, t);
+      // tokens of the adapter, as bits
+      const uint32_t lo = __ballot_sync(0xffffffffu, lane < P.T && adapter_of(P, min(lane, P.T - 1)) == a);
+      const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < P.T && adapter_of(P, min(lane + 32, P.T - 1)) == a);
+      const unsigned long long all = (unsigned long long)hi << 32 | lo;
+      if (__popcll(all & ((1ull << t) - 1)) % TILE == 0) {
+        const unsigned long long rest = all & ~((1ull << t) - 1);
+        n = min(TILE, __popcll(rest));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = lane + 32 * i, at = __popcll(rest & ((1ull << j) - 1));
+          if ((rest >> j & 1ull) && at < TILE) list[at] = j;
+        }
+      }
+    }
+    if (lane == 0) {
+      s_tile[0] = a;
+      s_tile[1] = n;
+    }
+  }
+  __syncthreads();
+  a = s_tile[0];
+  n = s_tile[1];
+  return n > 0;
+}
+
+// Few tokens an adapter.  Blocks (tile of 8 tokens, part of K, 64 rows of A).
+// The warps take 32-column blocks of K in turn, MT 16-row tiles of A; D
+// fragments meet in shared memory, summed over the warps in order.
+template <bool F16, int MT>
+__global__ void __launch_bounds__(kThreads) k_shrink(const __grid_constant__ AdapterParams P) {
+  constexpr int NT = 1, TILE = 8 * NT, ROWS = 16 * MT;
+  extern __shared__ float red[];  // [kWarps][TILE][ROWS + 1]
+  __shared__ int list[TILE];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
+  int a, n;
+  if (!find_tile<TILE>(P, list, a, n)) return;
+  const int r0 = blockIdx.z * kRankChunk, rank = adapter_rank(P, a) - r0;  // rows left
+  if (rank <= 0) return;  // k_expand reads no v of such rows
+
+  const uint16_t* xr[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int i = 8 * j + g;
+    xr[j] = i < n ? P.x + (size_t)list[i] * P.x_stride : nullptr;
+  }
+  const uint16_t* ar = P.A + ((size_t)a * P.R + r0) * P.K;
+  float d[MT][NT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int step = 32 * kWarps * P.splits;
+#pragma unroll 2
+  for (int k = 32 * (blockIdx.y * kWarps + warp) + 8 * q; k - 8 * q < P.K; k += step) {
+    const bool in = k < P.K;
+    uint4 xv[NT], av[MT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xv[j] = in && xr[j] ? *reinterpret_cast<const uint4*>(xr[j] + k) : zero;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 16 * i + 8 * h + g;
+        av[i][h] = in && r < rank ? *reinterpret_cast<const uint4*>(ar + (size_t)r * P.K + k) : zero;
+      }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (8 * j >= n) continue;
+        mma16816<F16>(d[i][j], av[i][0].x, av[i][1].x, av[i][0].y, av[i][1].y, xv[j].x, xv[j].y);
+        mma16816<F16>(d[i][j], av[i][0].z, av[i][1].z, av[i][0].w, av[i][1].w, xv[j].z, xv[j].w);
+      }
+  }
+  float* mine = red + (size_t)warp * TILE * (ROWS + 1);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (8 * j >= n) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mine[(8 * j + 2 * q + (c & 1)) * (ROWS + 1) + 16 * i + 8 * (c >> 1) + g] = d[i][j][c];
+    }
+  __syncthreads();
+  const int rows = min(ROWS, P.R - r0);  // rows past the rank are zeros
+  float* v = P.v + (size_t)blockIdx.y * P.T * P.R + r0;
+  for (int i = tid; i < n * ROWS; i += kThreads) {
+    const int tok = i / ROWS, r = i - tok * ROWS;
+    if (r >= rows) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += red[(size_t)w * TILE * (ROWS + 1) + tok * (ROWS + 1) + r];
+    v[(size_t)list[tok] * P.R + r] = s;
+  }
+}
+
+// Many tokens an adapter.  Blocks (tile of 64 tokens, part of K, 64 rows of A):
+// warp w has tokens 8 w .. of the tile and the whole part of K, so nothing is
+// summed between warps; the adapter's rows come from L1 for all but the first
+// warp that asks.  UN 32-column blocks of x are asked for at once.
+template <bool F16, int MT>
+__global__ void __launch_bounds__(kThreads, 2) k_shrink_wide(const __grid_constant__ AdapterParams P) {
+  constexpr int UN = 4;
+  __shared__ int list[64];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
+  int a, n;
+  if (!find_tile<64>(P, list, a, n)) return;
+  const int r0 = blockIdx.z * kRankChunk, rank = adapter_rank(P, a) - r0;
+  if (rank <= 0 || 8 * warp >= n) return;
+  const int part = (P.K + 32 * P.splits - 1) / (32 * P.splits) * 32;
+  const int k_end = min(P.K, part * ((int)blockIdx.y + 1));
+  const int i = 8 * warp + g;
+  const uint16_t* const xr = i < n ? P.x + (size_t)list[i] * P.x_stride : nullptr;
+  const uint16_t* const ar = P.A + ((size_t)a * P.R + r0) * P.K;
+  float d[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) d[m][0] = d[m][1] = d[m][2] = d[m][3] = 0.f;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 xv[UN];
+  auto ask = [&](int k, uint4& v) { v = xr && k < k_end ? *reinterpret_cast<const uint4*>(xr + k) : zero; };
+  const int k_first = part * blockIdx.y + 8 * q;
+#pragma unroll
+  for (int u = 0; u < UN; ++u) ask(k_first + 32 * u, xv[u]);
+  for (int k0 = k_first; k0 - 8 * q < k_end; k0 += 32 * UN) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int k = k0 + 32 * u;
+      const uint4 x = xv[u];
+      ask(k + 32 * UN, xv[u]);
+      uint4 av[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * m + 8 * h + g;
+          av[m][h] = k < k_end && r < rank ? *reinterpret_cast<const uint4*>(ar + (size_t)r * P.K + k) : zero;
+        }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma16816<F16>(d[m], av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y, x.x, x.y);
+        mma16816<F16>(d[m], av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w, x.z, x.w);
+      }
+    }
+  }
+  // D: row 16 m + g (+ 8), token 2q (+ 1) of the warp's eight
+  float* const v = P.v + (size_t)blockIdx.y * P.T * P.R + r0;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int r = 16 * m + 8 * (c >> 1) + g, tok = 8 * warp + 2 * q + (c & 1);
+      if (tok < n && r0 + r < P.R) v[(size_t)list[tok] * P.R + r] = d[m][c];
+    }
+}
+
+// v of a tile as the B operand of the second product, two numbers of the
+// operands' type an element: bf16 hi + lo keep 16 bits and more of v; fp16 keeps
+// 22, of v scaled by a power of two to a largest element near 1, since v may
+// pass fp16's range.  s_scale: what takes the token's product back, times the
+// adapter's scale.  256 / TILE threads a token; ends with a block barrier.
+template <bool F16, int TILE>
+MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int rank, int pitch, uint32_t* vs,
+                     float* s_scale) {
+  const int tid = threadIdx.x;
+  constexpr int TPT = kThreads / TILE;
+  const int tok = tid / TPT, part = tid % TPT, padded = (rank + 15) & ~15;
+  const float* const v = P.v + (tok < n ? (size_t)list[tok] * P.R : 0);
+  auto v_of = [&](int r) {
+    float sum = 0.f;
+    if (tok < n && r < rank)
+      for (int k = 0; k < P.splits; ++k) sum += __ldcg(v + (size_t)k * P.T * P.R + r);
+    return sum;
+  };
+  float up = 1.f, down = 1.f;
+  if (F16) {
+    float top = 0.f;
+    for (int r = part; r < rank; r += TPT) top = fmaxf(top, fabsf(v_of(r)));
+#pragma unroll
+    for (int o = TPT >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^e with 2^e <= top < 2^(e + 1), kept within the normal numbers on both sides
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+    if (top > 0.f && top < INFINITY) {
+      up = __uint_as_float(e << 23);
+      down = __uint_as_float((254u - e) << 23);
+    }
+  }
+  uint16_t* const hi = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
+  uint16_t* const lo = hi + TILE * pitch;
+#pragma unroll 4
+  for (int r = part; r < padded; r += TPT) {
+    const float x = v_of(r) * down;
+    const uint32_t h = pack2(F16 ? kF16 : kBf16, x, 0.f);
+    float xh, none;
+    unpack2(F16 ? kF16 : kBf16, h, xh, none);
+    hi[r] = static_cast<uint16_t>(h);
+    lo[r] = fabsf(xh) < INFINITY ? static_cast<uint16_t>(pack2(F16 ? kF16 : kBf16, x - xh, 0.f)) : 0;
+  }
+  if (part == 0) s_scale[tok] = up * (P.scales ? P.scales[a] : 1.f);
+  __syncthreads();
+}
+
+// One 16-wide step of the rank for 8 tokens: the two 16-row tiles of B against v.
+template <bool F16, bool ZERO>
+MOE_DEV void mma_pair(const uint2 (&b)[4], uint2 vh, uint2 vl, float* d0, float* d1) {
+  mma16816<F16, ZERO>(d0, b[0].x, b[1].x, b[0].y, b[1].y, vl.x, vl.y);
+  mma16816<F16, ZERO>(d1, b[2].x, b[3].x, b[2].y, b[3].y, vl.x, vl.y);
+  mma16816<F16>(d0, b[0].x, b[1].x, b[0].y, b[1].y, vh.x, vh.y);
+  mma16816<F16>(d1, b[2].x, b[3].x, b[2].y, b[3].y, vh.x, vh.y);
+}
+
+// Blocks (tile, columns, 256 at a time); warp w has 32 w .. of them as two 16-row
+// tiles of B, whose rows are dealt so that a lane ends with four neighbouring
+// columns n0 + 4g .. + 3 of tokens 2q and 2q + 1.  B stays in registers (ST 16-wide
+// steps of the rank) while the warp goes through the tile's tokens, D groups of
+// eight at a time, whose y is asked for a round ahead; nothing is waited for
+// between warps.  The ids, the order, B and the first y are read ahead of the wait
+// on the first product, which writes none of them.  YK: y and out are fp32 (0) or
+// 16-bit (1) in rows that allow accesses of four elements, or anything (2).
+// The whole call at 8192 tokens, 2048 x 2048, rank 32, fp32 y: 69 us (2.5 TB/s).
+// Two blocks an SM and as many columns a block as give every SM two: three with
+// fewer columns 76 us, six 82; B streamed through shared memory under a tile's
+// fixed tokens 76 us; the first form (a thread an output element) 1180 us.
+template <bool F16, int TILE, int ST, int YK>
+__global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
+  constexpr int D = TILE == 8 || YK == 2 ? 1 : 4;
+  constexpr int YB = YK == 0 ? 4 : 2;
+  extern __shared__ __align__(16) uint32_t vs[];  // [2][TILE][pitch / 2]: hi, then lo; pitch in elements
+  __shared__ int list[TILE];
+  __shared__ __align__(8) float s_scale[TILE];
+  __shared__ __align__(16) longlong2 s_row[TILE];  // bytes to the token's row of y and of out
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  int a, n;
+  if (!find_tile<TILE>(P, list, a, n)) {
+    pdl_wait();
+    pdl_launch_dependents();
+    return;
+  }
+  // (rows past the tile's last are its last: their loads need no test)
+  if (tid < TILE) {
+    const long long t = list[min(tid, n - 1)];
+    s_row[tid] = make_longlong2(t * P.y_stride * YB, t * P.out_stride * YB);
+    s_scale[tid] = 0.f;
+  }
+  const int rank = adapter_rank(P, a), pitch = expand_pitch(P.R);
+  const int c_first = P.cols * blockIdx.y, c_end = min(P.N, c_first + P.cols);
+  __syncthreads();
+  const uint16_t* const v0 = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
+  bool staged = false;
+  for (int w0 = c_first + 32 * warp; w0 - 32 * warp < c_end; w0 += kThreads) {
+    const int n0 = w0 + 4 * g;
+    const bool in = n0 < c_end;
+    // B: the lane's four columns, four k a step
+    uint2 bv[ST][4];
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      const int r = 16 * s + 4 * q;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) bv[s][c] = make_uint2(0u, 0u);
+      if (r >= rank) continue;
+      const uint16_t* row = P.B + ((size_t)a * P.N + n0) * P.R + r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (n0 + c < P.N) {
+          if (P.R % 4 == 0) {
+            bv[s][c] = *reinterpret_cast<const uint2*>(row);
+          } else {
+            bv[s][c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
+            bv[s][c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
+          }
+        }
+        row += P.R;
+      }
+      if (r + 4 > rank) {  // what lies past the rank does not count
+        const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 3 < rank ? ~0u : r + 2 < rank ? 0xFFFFu : 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          bv[s][c].x &= mx;
+          bv[s][c].y &= my;
+        }
+      }
+    }
+    // y of tokens 8 j + 2q (+ 1), as it lies in memory (YK < 2)
+    const uint8_t* const y0 = static_cast<const uint8_t*>(P.y) + (size_t)n0 * YB;
+    uint8_t* const o0 = static_cast<uint8_t*>(P.out) + (size_t)n0 * YB;
+    uint4 yv[D][2];
+    auto ask = [&](int j0) {
+      if (!in || YK == 2) return;
+#pragma unroll
+      for (int u = 0; u < D; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* at = y0 + s_row[8 * (j0 + u) + 2 * q + h].x;
+          if (YK == 0) {
+            yv[u][h] = *reinterpret_cast<const uint4*>(at);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(at);
+            yv[u][h].x = w.x, yv[u][h].y = w.y;
+          }
+        }
+    };
+    ask(0);
+    if (!staged) {
+      pdl_wait();
+      pdl_launch_dependents();
+      if (rank == 0 && P.out == P.y) return;
+      if (rank > 0) stage_v<F16, TILE>(P, list, a, n, rank, pitch, vs, s_scale);
+      staged = true;
+    }
+    // D groups of eight tokens at a time, whole ones (v of tokens past the last
+    // is 0, their y is the last's; they are not stored)
+    for (int j0 = 0; 8 * j0 < n; j0 += D) {
+      float d[D][2][4];
+      if (rank > 0) {
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+          if (16 * s >= rank) break;
+#pragma unroll
+          for (int u = 0; u < D; ++u) {
+            const uint16_t* v = v0 + 8 * (j0 + u) * pitch + 16 * s;
+            const uint2 vh = *reinterpret_cast<const uint2*>(v), vl = *reinterpret_cast<const uint2*>(v + TILE * pitch);
+            if (s == 0)
+              mma_pair<F16, true>(bv[s], vh, vl, d[u][0], d[u][1]);
+            else
+              mma_pair<F16, false>(bv[s], vh, vl, d[u][0], d[u][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < D; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) d[u][0][c] = d[u][1][c] = 0.f;
+      }
+      float y[D][2][4];
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        const float2 scale = *reinterpret_cast<const float2*>(s_scale + 8 * (j0 + u) + 2 * q);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (YK < 2) {
+            raw_values4(yv[u][h], YK == 0 ? kF32 : P.y_dtype, y[u][h]);
+          } else {
+            const size_t at = (size_t)list[min(8 * (j0 + u) + 2 * q + h, n - 1)] * P.y_stride + n0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[u][h][c] = n0 + c < c_end ? elem_load(P.y, P.y_dtype, at + c) : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            y[u][h][c] = fmaf(h ? scale.y : scale.x, d[u][c >> 1][2 * (c & 1) + h], y[u][h][c]);
+        }
+      }
+      if (8 * (j0 + D) < n) ask(j0 + D);
+#pragma unroll
+      for (int u = 0; u < D; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 8 * (j0 + u) + 2 * q + h;
+          if (!in || i >= n) continue;
+          const float* v = y[u][h];
+          if (YK == 0) {
+            *reinterpret_cast<float4*>(o0 + s_row[i].y) = make_float4(v[0], v[1], v[2], v[3]);
+          } else if (YK == 1) {
+            *reinterpret_cast<uint2*>(o0 + s_row[i].y) =
+                make_uint2(pack2(P.y_dtype, v[0], v[1]), pack2(P.y_dtype, v[2], v[3]));
+          } else {
+            const size_t at = (size_t)list[i] * P.out_stride + n0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (n0 + c < c_end) elem_store(P.out, P.y_dtype, at + c, v[c]);
+          }
+        }
+    }
+  }
+}
+
+template <bool F16>
+cudaError_t launch_products(const AdapterParams& p, int blocks, cudaStream_t stream) {
+  const dim3 grid(blocks, p.splits, (p.R + kRankChunk - 1) / kRankChunk);
+  auto shrink = [&](auto kern, int rows) {
+    return launch_behind(kern, grid, kThreads, rows ? kWarps * 8 * (rows + 1) * 4 : 0, stream, p);
+  };
+  const bool wide = p.tile == 64;
+  cudaError_t e = wide ? p.R <= 16   ? shrink(k_shrink_wide<F16, 1>, 0)
+                         : p.R <= 32 ? shrink(k_shrink_wide<F16, 2>, 0)
+                                     : shrink(k_shrink_wide<F16, 4>, 0)
+                  : p.R <= 16 ? shrink(k_shrink<F16, 1>, 16)
+                  : p.R <= 32 ? shrink(k_shrink<F16, 2>, 32)
+                              : shrink(k_shrink<F16, 4>, 64);
+  if (e != cudaSuccess) return e;
+  const dim3 eg(blocks, (p.N + p.cols - 1) / p.cols);
+  const int smem = 2 * p.tile * expand_pitch(p.R) * 2;
+  auto expand = [&](auto kern) {
+    if (smem > 48 * 1024) {
+      const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err != cudaSuccess) return err;
+    }
+    return launch_behind(kern, eg, kThreads, smem, stream, p);
+  };
+  if (!p.vec) return wide ? expand(k_expand<F16, 64, 8, 2>) : expand(k_expand<F16, 8, 8, 2>);
+#define MOE_EXPAND(TILE, YK)                                 \
+  (p.R <= 16   ? expand(k_expand<F16, TILE, 1, YK>)          \
+   : p.R <= 32 ? expand(k_expand<F16, TILE, 2, YK>)          \
+   : p.R <= 64 ? expand(k_expand<F16, TILE, 4, YK>)          \
+               : expand(k_expand<F16, TILE, 8, YK>))
+  if (p.y_dtype == kF32) return wide ? MOE_EXPAND(64, 0) : MOE_EXPAND(8, 0);
+  return wide ? MOE_EXPAND(64, 1) : MOE_EXPAND(8, 1);
+#undef MOE_EXPAND
+}
+
+}  // namespace
+
+}  // namespace moe
