@@ -30,56 +30,118 @@ constexpr int kRowsPerBlock = 4;  // rows of a block whose rows have a warp each
 constexpr int kWarpRows = 32 * kRowsPerBlock;  // threads of such a block, and of no other
 constexpr int kStages = 3;        // rows of k_norm_rows in shared memory
 
-// Columns of the thread, in groups of eight: VEC: two times four neighbours,
-// accesses of four elements; otherwise (rows or H that rule those out)
-// neighbours on neighbouring threads.  Columns past the row hold zeros.
+// Columns of the thread: in a group of eight, two times four neighbours, so that
+// neighbouring lanes cover whole sectors in one access.  VEC: every row allows
+// accesses of four elements and H % 4 == 0.  Otherwise each row is looked at by
+// itself: one that starts between two such boundaries is read element by element
+// (the four accesses hit the same sectors) and written in fours all the same,
+// each lane taking the end of its neighbour's columns, so that a sector is not
+// written in four parts.  Columns past the row hold zeros.
 template <bool VEC>
 struct Columns {
   int tid, threads, H;
-  MOE_DEV int at(int j, int e) const {
-    return VEC ? 4 * (tid + threads * (2 * j + (e >> 2))) + (e & 3) : threads * (8 * j + e) + tid;
+  MOE_DEV int at(int j, int h) const { return 4 * (tid + threads * (2 * j + h)); }  // of the half h of group j
+  // a row of a tensor, and the elements from a four-element boundary to it
+  struct Row {
+    uint8_t* p;
+    int dtype, m;
+  };
+  MOE_DEV static Row row(const void* p, int dtype, size_t first) {
+    Row r;
+    r.p = const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + first * elem_bytes(dtype);
+    r.dtype = dtype;
+    r.m = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(r.p) >> (dtype == kF32 ? 2 : 1)) & 3;
+    return r;
   }
-  MOE_DEV void load(const void* p, int dtype, size_t base, int j, uint4* w) const {
+  MOE_DEV void load(const Row& r, int j, uint4* w) const {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) w[h] = make_uint4(0u, 0u, 0u, 0u);
-    if (VEC) {
+    for (int h = 0; h < 2; ++h) {
+      const int c = at(j, h);
+      w[h] = make_uint4(0u, 0u, 0u, 0u);
+      if (VEC ? c < H : r.m == 0 && c + 4 <= H) {
+        w[h] = raw_load4(r.p, r.dtype, c);
+      } else if (!VEC) {
+        uint32_t e[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (at(j, 4 * h) < H) w[h] = raw_load4(p, dtype, base + at(j, 4 * h));
-    } else {
-      uint32_t e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = at(j, i) < H ? raw_load(p, dtype, base + at(j, i)) : 0u;
-      w[0] = make_uint4(e[0], e[1], e[2], e[3]);
-      w[1] = make_uint4(e[4], e[5], e[6], e[7]);
-    }
-  }
-  MOE_DEV void values(const uint4* w, int dtype, float* v) const {
-    if (VEC) {
-      raw_values4(w[0], dtype, v);
-      raw_values4(w[1], dtype, v + 4);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v[4 * h] = raw_value(w[h].x, dtype);
-        v[4 * h + 1] = raw_value(w[h].y, dtype);
-        v[4 * h + 2] = raw_value(w[h].z, dtype);
-        v[4 * h + 3] = raw_value(w[h].w, dtype);
+        for (int i = 0; i < 4; ++i) e[i] = c + i < H ? raw_load(r.p, r.dtype, c + i) : 0u;
+        w[h] = r.dtype == kF32 ? make_uint4(e[0], e[1], e[2], e[3]) : make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, 0u, 0u);
       }
     }
   }
-  MOE_DEV void store(void* p, int dtype, size_t base, int j, const float* v) const {
-    if (VEC) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (at(j, 4 * h) < H) elem_store4(p, dtype, base + at(j, 4 * h), v + 4 * h);
+  MOE_DEV void values(const uint4* w, int dtype, float* v) const {
+    raw_values4(w[0], dtype, v);
+    raw_values4(w[1], dtype, v + 4);
+  }
+  // N words of four elements (fp32: 4, 16-bit: 2) from column c, those inside the row
+  template <int N>
+  MOE_DEV void store4(const Row& r, int c, const uint32_t (&u)[N]) const {
+    if (c + 4 <= H) {
+      if (N == 4)
+        *reinterpret_cast<uint4*>(r.p + 4 * c) = make_uint4(u[0], u[1], u[N - 2], u[N - 1]);
+      else
+        *reinterpret_cast<uint2*>(r.p + 2 * c) = make_uint2(u[0], u[1]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at(j, e) < H) elem_store(p, dtype, base + at(j, e), v[e]);
+      for (int e = 0; e < 4; ++e) store1(r, c + e, u, e);
+    }
+  }
+  template <int N>
+  MOE_DEV void store1(const Row& r, int c, const uint32_t (&u)[N], int e) const {
+    if (c >= H) return;
+    if (N == 4)
+      *reinterpret_cast<uint32_t*>(r.p + 4 * c) = u[e & (N - 1)];
+    else
+      *reinterpret_cast<uint16_t*>(r.p + 2 * c) = static_cast<uint16_t>(u[e >> 1] >> (16 * (e & 1)));
+  }
+  template <int N>
+  MOE_DEV void store_words(const Row& r, int c, const uint32_t (&u)[N]) const {
+    const int m = r.m, lane = threadIdx.x & 31;
+    if (m == 0) {
+      store4(r, c, u);
+      return;
+    }
+    // columns c - m .. c - m + 3: the last m of the lane below, then the lane's;
+    // the warp's first 4 - m and last m columns one by one
+    uint32_t p[N], o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = __shfl_up_sync(0xffffffffu, u[i], 1);
+    if (N == 4) {
+      o[0] = m == 1 ? p[N - 1] : m == 2 ? p[N - 2] : p[1];
+      o[1] = m == 1 ? u[0] : m == 2 ? p[N - 1] : p[N - 2];
+      o[N - 2] = m == 1 ? u[1] : m == 2 ? u[0] : p[N - 1];
+      o[N - 1] = m == 1 ? u[N - 2] : m == 2 ? u[1] : u[0];
+    } else {
+      const uint32_t a = m == 3 ? p[0] : p[1], b = m == 3 ? p[1] : u[0], d = m == 3 ? u[0] : u[1];
+      o[0] = m == 2 ? p[1] : __funnelshift_r(a, b, 16);
+      o[1] = m == 2 ? u[0] : __funnelshift_r(b, d, 16);
+    }
+    if (lane > 0) store4(r, c - m, o);
+    if (lane == 0 || lane == 31) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((lane == 0) == (e < 4 - m)) store1(r, c + e, u, e);
+    }
+  }
+  // called by whole warps
+  MOE_DEV void store(const Row& r, int j, const float* v) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = at(j, h);
+      const float* f = v + 4 * h;
+      if (VEC) {
+        if (c < H) elem_store4(r.p, r.dtype, c, f);
+      } else if (r.dtype == kF32) {
+        const uint32_t u[4] = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+        store_words(r, c, u);
+      } else {
+        const uint32_t u[2] = {pack2(r.dtype, f[0], f[1]), pack2(r.dtype, f[2], f[3])};
+        store_words(r, c, u);
+      }
     }
   }
 };
+
+MOE_DEV float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
 
 // Sum over the row's threads, the same on each: a warp's butterfly, then (a
 // block a row) the warps' sums in shared memory.
@@ -113,7 +175,7 @@ MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t,
     float scale = P.beta;
     if (P.gate && P.gate_layout == 1) {
       const float v = elem_load(P.gate, P.g_dtype, t * P.g_stride);
-      scale *= P.gate_sigmoid ? 1.f / (1.f + expf(-v)) : v;
+      scale *= P.gate_sigmoid ? sigmoid(v) : v;
     }
     if (P.post_norm) {
       float q = 0.f;
@@ -138,7 +200,7 @@ MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t,
         gate(j, v);
         if (P.gate_sigmoid) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 1.f / (1.f + expf(-v[e]));
+          for (int e = 0; e < 8; ++e) v[e] = sigmoid(v[e]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[j][e] *= v[e];
@@ -149,7 +211,7 @@ MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t,
   }
   if (P.res_out) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) cols.store(P.res_out, P.r_dtype, t * P.ro_stride, j, r[j]);
+    for (int j = 0; j < NV; ++j) cols.store(cols.row(P.res_out, P.r_dtype, t * P.ro_stride), j, r[j]);
   }
   if (P.normed) {
     float q = 0.f;
@@ -159,7 +221,7 @@ MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t,
       // not enter the sum
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (cols.at(j, VEC ? e & 4 : e) < P.H) q = fmaf(r[j][e], r[j][e], q);
+        if (cols.at(j, e >> 2) + (VEC ? 0 : e & 3) < P.H) q = fmaf(r[j][e], r[j][e], q);
     }
     const float inv = rsqrtf(row_sum<THREADS, WARP>(q, red[1]) / (float)P.H + P.eps);
 #pragma unroll
@@ -172,7 +234,7 @@ MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t,
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[j][e] *= P.w_offset + v[e];
       }
-      cols.store(P.normed, P.n_dtype, t * P.n_stride, j, r[j]);
+      cols.store(cols.row(P.normed, P.n_dtype, t * P.n_stride), j, r[j]);
     }
   }
 }
@@ -191,19 +253,19 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ NormPa
   cols.H = P.H;
   pdl_wait();
   pdl_launch_dependents();
-  if (WARP && t >= (size_t)P.T) return;
+  if (WARP && t >= (size_t)P.T) return;  // (whole warps)
 
   uint4 rw[NV][2], yw[NV][2], gw[2], pw[2], nw[2];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) cols.load(P.res, P.r_dtype, t * P.r_stride, j, rw[j]);
+  for (int j = 0; j < NV; ++j) cols.load(cols.row(P.res, P.r_dtype, t * P.r_stride), j, rw[j]);
   if (P.y) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) cols.load(P.y, P.y_dtype, t * P.y_stride, j, yw[j]);
+    for (int j = 0; j < NV; ++j) cols.load(cols.row(P.y, P.y_dtype, t * P.y_stride), j, yw[j]);
   }
   const size_t g_row = P.gate_layout == 2 ? t * P.g_stride : 0;
-  auto load_gate = [&](int j) { cols.load(P.gate, P.g_dtype, g_row, j, gw); };
-  auto load_post = [&](int j) { cols.load(P.w_post, P.wpost_dtype, 0, j, pw); };
-  auto load_pre = [&](int j) { cols.load(P.w_pre, P.wpre_dtype, 0, j, nw); };
+  auto load_gate = [&](int j) { cols.load(cols.row(P.gate, P.g_dtype, g_row), j, gw); };
+  auto load_post = [&](int j) { cols.load(cols.row(P.w_post, P.wpost_dtype, 0), j, pw); };
+  auto load_pre = [&](int j) { cols.load(cols.row(P.w_pre, P.wpre_dtype, 0), j, nw); };
   if (ALL) {
     if (P.gate && P.gate_layout != 1) load_gate(0);
     if (P.w_post) load_post(0);
@@ -220,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ NormPa
       P, cols, t, r, y, red,
       [&](int j, float* v) {
         if (!AGAIN) return;
-        cols.load(P.y, P.y_dtype, t * P.y_stride, j, yw[j]);
+        cols.load(cols.row(P.y, P.y_dtype, t * P.y_stride), j, yw[j]);
         cols.values(yw[j], P.y_dtype, v);
       },
       [&](int j, float* v) {
@@ -356,7 +418,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rows(const __grid_constant__ N
       if (P.gate && P.gate_layout == 0) {
         raw_values4(raw_load4(P.gate, P.g_dtype, c), P.g_dtype, g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) post[e] *= P.gate_sigmoid ? 1.f / (1.f + expf(-g[e])) : g[e];
+        for (int e = 0; e < 4; ++e) post[e] *= P.gate_sigmoid ? sigmoid(g[e]) : g[e];
       }
       if (P.w_pre) {
         raw_values4(raw_load4(P.w_pre, P.wpre_dtype, c), P.wpre_dtype, pre);
@@ -422,7 +484,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rows(const __grid_constant__ N
       float scale = P.beta;
       if (P.gate && P.gate_layout == 1) {
         const float v = elem_load(P.gate, P.g_dtype, (size_t)t * P.g_stride);
-        scale *= P.gate_sigmoid ? 1.f / (1.f + expf(-v)) : v;
+        scale *= P.gate_sigmoid ? sigmoid(v) : v;
       }
       if (P.post_norm) scale *= rsqrtf(row_sum<THREADS, false>(square(y), red[odd][0]) * per_column + P.eps);
       const F2 f = f2(scale);
@@ -440,7 +502,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rows(const __grid_constant__ N
             if (P.gate_sigmoid) {
               float a, b;
               f2_get(g[e], a, b);
-              g[e] = f2(__fdividef(1.f, 1.f + expf(-a)), __fdividef(1.f, 1.f + expf(-b)));
+              g[e] = f2(sigmoid(a), sigmoid(b));
             }
             y[j][e] = f2_mul(y[j][e], g[e]);
           }
