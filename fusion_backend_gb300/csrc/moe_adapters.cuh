@@ -284,12 +284,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_shrink_wide(const __grid_consta
     }
 }
 
-// v of a tile as the B operand of the second product, two numbers of the
-// operands' type an element: bf16 hi + lo keep 16 bits and more of v; fp16 keeps
-// 22, of v scaled by a power of two to a largest element near 1, since v may
-// pass fp16's range.  s_scale: what takes the token's product back, times the
-// adapter's scale.  256 / TILE threads a token; ends with a block barrier.
-template <bool F16, int TILE>
+// Numbers of the operands' type that v enters the second product as: what its
+// 8-bit (bf16) or 11-bit (fp16) significands add up to is 16 and more bits of v
+// for a 16-bit result, 22 and more for an fp32 one.
+template <bool F16, int YK>
+constexpr int kTerms = F16 || YK == 1 ? 2 : 3;
+
+// v of a tile as the B operand of the second product, TERMS numbers an element,
+// the largest first.  fp16: of v scaled by a power of two to a largest element
+// near 1, since v may pass fp16's range.  s_scale: what takes the token's product
+// back, times the adapter's scale.  256 / TILE threads a token; ends with a block
+// barrier.
+template <bool F16, int TILE, int TERMS>
 MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int rank, int pitch, uint32_t* vs,
                      float* s_scale) {
   const int tid = threadIdx.x;
@@ -315,28 +321,38 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
       down = __uint_as_float((254u - e) << 23);
     }
   }
-  uint16_t* const hi = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
-  uint16_t* const lo = hi + TILE * pitch;
+  uint16_t* const out = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
 #pragma unroll 4
   for (int r = part; r < padded; r += TPT) {
-    const float x = v_of(r) * down;
-    const uint32_t h = pack2(F16 ? kF16 : kBf16, x, 0.f);
-    float xh, none;
-    unpack2(F16 ? kF16 : kBf16, h, xh, none);
-    hi[r] = static_cast<uint16_t>(h);
-    lo[r] = fabsf(xh) < INFINITY ? static_cast<uint16_t>(pack2(F16 ? kF16 : kBf16, x - xh, 0.f)) : 0;
+    float x = v_of(r) * down;
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+      const uint32_t h = pack2(F16 ? kF16 : kBf16, x, 0.f);
+      float xh, none;
+      unpack2(F16 ? kF16 : kBf16, h, xh, none);
+      out[i * TILE * pitch + r] = static_cast<uint16_t>(h);
+      x = fabsf(xh) < INFINITY ? x - xh : 0.f;  // exact
+    }
   }
   if (part == 0) s_scale[tok] = up * (P.scales ? P.scales[a] : 1.f);
   __syncthreads();
 }
 
-// One 16-wide step of the rank for 8 tokens: the two 16-row tiles of B against v.
-template <bool F16, bool ZERO>
-MOE_DEV void mma_pair(const uint2 (&b)[4], uint2 vh, uint2 vl, float* d0, float* d1) {
-  mma16816<F16, ZERO>(d0, b[0].x, b[1].x, b[0].y, b[1].y, vl.x, vl.y);
-  mma16816<F16, ZERO>(d1, b[2].x, b[3].x, b[2].y, b[3].y, vl.x, vl.y);
-  mma16816<F16>(d0, b[0].x, b[1].x, b[0].y, b[1].y, vh.x, vh.y);
-  mma16816<F16>(d1, b[2].x, b[3].x, b[2].y, b[3].y, vh.x, vh.y);
+// One 16-wide step of the rank for 8 tokens: the two 16-row tiles of B against
+// the terms of v (v: the lane's first; term_at elements to the next), the smallest
+// first.
+template <bool F16, int TERMS, bool ZERO>
+MOE_DEV void mma_terms(const uint2 (&b)[4], const uint16_t* v, int term_at, float* d0, float* d1) {
+  uint2 t[TERMS];
+#pragma unroll
+  for (int i = 0; i < TERMS; ++i) t[i] = *reinterpret_cast<const uint2*>(v + i * term_at);
+  mma16816<F16, ZERO>(d0, b[0].x, b[1].x, b[0].y, b[1].y, t[TERMS - 1].x, t[TERMS - 1].y);
+  mma16816<F16, ZERO>(d1, b[2].x, b[3].x, b[2].y, b[3].y, t[TERMS - 1].x, t[TERMS - 1].y);
+#pragma unroll
+  for (int i = TERMS - 2; i >= 0; --i) {
+    mma16816<F16>(d0, b[0].x, b[1].x, b[0].y, b[1].y, t[i].x, t[i].y);
+    mma16816<F16>(d1, b[2].x, b[3].x, b[2].y, b[3].y, t[i].x, t[i].y);
+  }
 }
 
 // Blocks (tile, columns, 256 at a time); warp w has 32 w .. of them as two 16-row
@@ -354,8 +370,8 @@ MOE_DEV void mma_pair(const uint2 (&b)[4], uint2 vh, uint2 vl, float* d0, float*
 template <bool F16, int TILE, int ST, int YK>
 __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
   constexpr int D = TILE == 8 || YK == 2 ? 1 : 4;
-  constexpr int YB = YK == 0 ? 4 : 2;
-  extern __shared__ __align__(16) uint32_t vs[];  // [2][TILE][pitch / 2]: hi, then lo; pitch in elements
+  constexpr int YB = YK == 0 ? 4 : 2, TERMS = kTerms<F16, YK>;
+  extern __shared__ __align__(16) uint32_t vs[];  // [TERMS][TILE][pitch / 2]; pitch in elements
   __shared__ int list[TILE];
   __shared__ __align__(8) float s_scale[TILE];
   __shared__ __align__(16) longlong2 s_row[TILE];  // bytes to the token's row of y and of out
@@ -434,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
       pdl_wait();
       pdl_launch_dependents();
       if (rank == 0 && P.out == P.y) return;
-      if (rank > 0) stage_v<F16, TILE>(P, list, a, n, rank, pitch, vs, s_scale);
+      if (rank > 0) stage_v<F16, TILE, TERMS>(P, list, a, n, rank, pitch, vs, s_scale);
       staged = true;
     }
     // D groups of eight tokens at a time, whole ones (v of tokens past the last
@@ -448,11 +464,10 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 #pragma unroll
           for (int u = 0; u < D; ++u) {
             const uint16_t* v = v0 + 8 * (j0 + u) * pitch + 16 * s;
-            const uint2 vh = *reinterpret_cast<const uint2*>(v), vl = *reinterpret_cast<const uint2*>(v + TILE * pitch);
             if (s == 0)
-              mma_pair<F16, true>(bv[s], vh, vl, d[u][0], d[u][1]);
+              mma_terms<F16, TERMS, true>(bv[s], v, TILE * pitch, d[u][0], d[u][1]);
             else
-              mma_pair<F16, false>(bv[s], vh, vl, d[u][0], d[u][1]);
+              mma_terms<F16, TERMS, false>(bv[s], v, TILE * pitch, d[u][0], d[u][1]);
           }
         }
       } else {
@@ -518,7 +533,7 @@ cudaError_t launch_products(const AdapterParams& p, int blocks, cudaStream_t str
                               : shrink(k_shrink<F16, 4>, 64);
   if (e != cudaSuccess) return e;
   const dim3 eg(blocks, (p.N + p.cols - 1) / p.cols);
-  const int smem = 2 * p.tile * expand_pitch(p.R) * 2;
+  const int smem = (!p.vec || p.y_dtype == kF32 ? kTerms<F16, 0> : kTerms<F16, 1>) * p.tile * expand_pitch(p.R) * 2;
   auto expand = [&](auto kern) {
     if (smem > 48 * 1024) {
       const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

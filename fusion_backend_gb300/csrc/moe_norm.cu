@@ -241,7 +241,7 @@ MOE_DEV void finish_row(const NormParams& P, const Columns<VEC>& cols, size_t t,
 
 // THREADS: the most that a block has.
 template <int NV, bool VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ NormParams P) {
+__global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ NormParams P) {
   constexpr bool WARP = THREADS == kWarpRows;
   constexpr bool ALL = NV == 1;  // the weights and the gate too are asked for at the start
   constexpr bool AGAIN = NV * THREADS > 1024;  // y is read a second time
