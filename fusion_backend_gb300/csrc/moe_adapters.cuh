@@ -541,12 +541,12 @@ cudaError_t launch_products(const AdapterParams& p, int blocks, cudaStream_t str
     }
     return launch_behind(kern, eg, kThreads, smem, stream, p);
   };
-  if (!p.vec) return wide ? expand(k_expand<F16, 64, 8, 2>) : expand(k_expand<F16, 8, 8, 2>);
 #define MOE_EXPAND(TILE, YK)                                 \
   (p.R <= 16   ? expand(k_expand<F16, TILE, 1, YK>)          \
    : p.R <= 32 ? expand(k_expand<F16, TILE, 2, YK>)          \
    : p.R <= 64 ? expand(k_expand<F16, TILE, 4, YK>)          \
                : expand(k_expand<F16, TILE, 8, YK>))
+  if (!p.vec) return wide ? MOE_EXPAND(64, 2) : MOE_EXPAND(8, 2);
   if (p.y_dtype == kF32) return wide ? MOE_EXPAND(64, 0) : MOE_EXPAND(8, 0);
   return wide ? MOE_EXPAND(64, 1) : MOE_EXPAND(8, 1);
 #undef MOE_EXPAND
