@@ -523,7 +523,7 @@ int check_adapters(const moe_ffn_adapters_args* a) {
   if (!a || a->T < 0 || a->n_adapters < 0) return MOE_FFN_ERR_INVALID_ARG;
   if ((a->x_dtype != MOE_FFN_ACT_BF16 && a->x_dtype != MOE_FFN_ACT_F16) || !valid_elem(a->y_dtype))
     return MOE_FFN_ERR_INVALID_ARG;
-  if (a->R < 1 || a->R > kAdapterMaxRank || a->K < 8 || a->K > 65536 || a->K % 8 || a->N < 1 || a->N > (1 << 20))
+  if (a->T > kAdapterMaxT || a->R < 1 || a->R > kAdapterMaxRank || a->K < 8 || a->K > 65536 || a->K % 8 || a->N < 1 || a->N > (1 << 20))
     return MOE_FFN_ERR_UNSUPPORTED;
   if (a->x_stride < a->K || a->y_stride < a->N || a->out_stride < a->N) return MOE_FFN_ERR_INVALID_ARG;
   if (a->x_stride % 8) return MOE_FFN_ERR_MISALIGNED;

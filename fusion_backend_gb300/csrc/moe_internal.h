@@ -257,6 +257,7 @@ cudaError_t launch_join_add(const float* a, const float* b, float* out, int n, c
 constexpr int kRouteMaxGroups = 32;  // a lane holds one group's value
 constexpr int kNormMaxH = 32768;
 constexpr int kAdapterMaxRank = 128;
+constexpr int kAdapterMaxT = 1 << 24;
 
 struct RouteParams {
   int T, E, K, G, gs, top_groups, sms;  // gs experts a group

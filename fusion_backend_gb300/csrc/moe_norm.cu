@@ -539,12 +539,18 @@ cudaError_t launch(const NormParams& p, bool vec, cudaStream_t stream) {
              : launch_behind(k_norm<NV, false, THREADS>, grid, threads, 0, stream, p);
 }
 
+// Bytes of shared memory that a row and the two behind it take.
+int rows_smem(const NormParams& p, int nv) {
+  const int each = elem_bytes(p.r_dtype) + (p.y ? elem_bytes(p.y_dtype) : 0) +
+                   (p.gate && p.gate_layout == 2 ? elem_bytes(p.g_dtype) : 0);
+  return kStages * ((p.H + 128 * nv - 1) / (128 * nv) * 32) * 4 * nv * each;
+}
+
 // As many blocks as are resident at once.
 template <int NV, int THREADS, bool R32, bool Y32, bool N32>
 cudaError_t launch_rows_of(const NormParams& p, cudaStream_t stream) {
   const int threads = (p.H + 128 * NV - 1) / (128 * NV) * 32;
-  const int each = (R32 ? 4 : 2) + (Y32 ? 4 : 2) * ((p.y ? 1 : 0) + (p.gate && p.gate_layout == 2 ? 1 : 0));
-  const int smem = kStages * threads * 4 * NV * each;
+  const int smem = rows_smem(p, NV);
   auto* const kern = k_norm_rows<NV, THREADS, R32, Y32, N32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   int per_sm = 0;
@@ -580,9 +586,11 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
   if (p.H <= 512) return launch<2, kWarpRows>(p, vec, stream);
   if (p.H > 16384) return launch<4, 1024>(p, vec, stream);
   if (p.H > 8192) return launch<2, 1024>(p, vec, stream);
-  // (the streaming kernel takes a gate of every element in y's size)
-  const bool gate_fits = !p.gate || p.gate_layout != 2 || (p.g_dtype == kF32) == (p.y_dtype == kF32);
-  if (vec && gate_fits && p.T > 4 * p.sms) {
+  // (the streaming kernel takes a gate of every element in y's size, and three
+  // rows in shared memory)
+  const bool fits = (!p.gate || p.gate_layout != 2 || (p.g_dtype == kF32) == (p.y_dtype == kF32)) &&
+                    rows_smem(p, 4) <= 220 * 1024;
+  if (vec && fits && p.T > 4 * p.sms) {
     if (p.H <= 2048) return launch_rows<4, 128>(p, stream);
     if (p.H <= 4096) return launch_rows<4, 256>(p, stream);
     return launch_rows<4, 512>(p, stream);

@@ -93,13 +93,13 @@ __device__ __noinline__ double exact_c(bool sigmoid, float l, float b, double m,
   return (sigmoid ? 1.0 / (1.0 + e) : e / z) + (double)b;
 }
 
-MOE_DEV float logit(const RouteParams& P, int t, int e) {
+MOE_DEV float logit(const RouteParams& P, uint32_t t, int e) {
   return clean(elem_load(P.logits, P.dtype, (size_t)t * P.stride + e));
 }
 MOE_DEV float bias_of(const RouteParams& P, int e) { return P.bias ? clean(P.bias[e]) : 0.f; }
 
 // The softmax's largest logit and sum in fp64.
-__device__ __noinline__ void exact_sum(const RouteParams& P, int t, const Owned& o, double& m, double& z) {
+__device__ __noinline__ void exact_sum(const RouteParams& P, uint32_t t, const Owned& o, double& m, double& z) {
   float top = -INFINITY;
 #pragma unroll 1
   for (int i = 0; i < o.n; ++i) top = fmaxf(top, logit(P, t, o.e0 + i));
@@ -115,7 +115,7 @@ __device__ __noinline__ void exact_sum(const RouteParams& P, int t, const Owned&
 
 // The whole choice in fp64: lane j gets the j-th expert and its logit.
 template <int EPL>
-__device__ __noinline__ void choose_exact(const RouteParams& P, int t, const Owned& o, int& id, float& lj) {
+__device__ __noinline__ void choose_exact(const RouteParams& P, uint32_t t, const Owned& o, int& id, float& lj) {
   const int lane = threadIdx.x & 31;
   double m = 0.0, z = 1.0;
   if (!P.sigmoid) exact_sum(P, t, o, m, z);
@@ -180,7 +180,7 @@ __device__ __noinline__ void choose_exact(const RouteParams& P, int t, const Own
 // The n candidates on lanes 0 .. n - 1 (expert id, logit lj; with a bias), in
 // the order of their c in fp64: a lane forms one c, counts the candidates
 // before it and the candidates change lanes.
-__device__ __noinline__ void settle(const RouteParams& P, int t, const Owned& o, int n, int& id, float& lj) {
+__device__ __noinline__ void settle(const RouteParams& P, uint32_t t, const Owned& o, int n, int& id, float& lj) {
   const int lane = threadIdx.x & 31;
   double m = 0.0, z = 1.0, c = -INFINITY;
   if (!P.sigmoid) exact_sum(P, t, o, m, z);
@@ -254,7 +254,7 @@ MOE_DEV void choose_rounds(const RouteParams& P, float (&c)[EPL], const Owned& o
 // out comes before the other.  c: fp32, off by less than `err`; only a group's
 // experts that may be among its two largest are formed again.
 template <int EPL>
-MOE_DEV bool border_swaps(const RouteParams& P, int t, const Owned& o, const float (&c)[EPL], float a1, float a2,
+MOE_DEV bool border_swaps(const RouteParams& P, uint32_t t, const Owned& o, const float (&c)[EPL], float a1, float a2,
                           float err, int in_grp, int out_grp) {
   double m = 0.0, z = 1.0;
   if (!P.sigmoid) exact_sum(P, t, o, m, z);
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
   // a token's logits as they lie in memory: those of the warp's next token are
   // asked for before it works on one
   uint32_t w[EPL];
-  auto ask = [&](int t) {
-    if (t >= P.T) return;
+  auto ask = [&](uint32_t t) {
+    if (t >= (uint32_t)P.T) return;
     const size_t row = (size_t)t * P.stride + o.e0;
     if (EPL >= 4 && P.vec) {
 #pragma unroll
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
     }
   };
   ask(blockIdx.x * kWarps + warp);
-  for (int t = blockIdx.x * kWarps + warp; t < P.T; t += gridDim.x * kWarps) {
+  for (uint32_t t = blockIdx.x * kWarps + warp; t < (uint32_t)P.T; t += gridDim.x * kWarps) {
     float l[EPL], c[EPL];
     if (EPL >= 4 && P.vec) {
 #pragma unroll

@@ -317,8 +317,8 @@ int moe_ffn_execute_routed(moe_ffn_plan_t plan, moe_ffn_stream_t stream, void* w
  *   w_tj  = scale s_{t,ids_j}, divided by sum_i s_{t,ids_i} when renorm != 0
  * Where fewer than top_k experts are left the last ids are -1 and their
  * weights 0 (a wholly masked token: all of them); moe_ffn_execute_routed drops
- * such choices.  The choice is the one of c in fp64: scores closer than fp32
- * can tell apart are compared in fp64.
+ * such choices.  The choice is that of c to the resolution of fp64: scores
+ * closer than fp32 can tell apart are compared in fp64.
  * 1 <= E <= 1024, 1 <= top_k <= min(E, 32), groups <= 32 and a divisor of E,
  * 1 <= top_groups <= groups, top_k <= top_groups E / groups.
  */
@@ -377,8 +377,10 @@ int moe_ffn_norm_residual(const moe_ffn_norm_args* args, moe_ffn_stream_t stream
  * y_t.  ranks int32 [n_adapters] or NULL (all R): only the first ranks_a rows
  * of A_a and columns of B_a count (clamped to 0..R; what the others hold does
  * not matter).  scales fp32 [n_adapters] or NULL (1).
- * Sums are in fp32.
- * 1 <= R <= 128, 8 <= K <= 65536 a multiple of 8, 1 <= N <= 1048576.
+ * Sums are in fp32.  A_a x_t enters the second product as the sum of numbers of
+ * x's type: 22 bits of it and more where y is fp32, else 16 bits and more.
+ * T <= 16777216, 1 <= R <= 128, 8 <= K <= 65536 a multiple of 8, 1 <= N <=
+ * 1048576.
  * The workspace (256-byte aligned, scratch) holds what
  * moe_ffn_adapters_workspace reports for the argument block.
  */

@@ -175,3 +175,52 @@ def test_repeats_streams_graph():
 def test_no_tokens():
     r, n = fb.moe_ffn_norm_residual(torch.zeros(0, 64, device="cuda"))
     assert r.shape == n.shape == (0, 64)
+
+
+@pytest.mark.parametrize("H", [516, 1024, 2048, 2052, 4096, 6000, 8192])
+@pytest.mark.parametrize("kind", ["none", "channel", "token", "full"])
+def test_many_rows(H, kind):
+    """More rows than the GPU holds at once, in every combination of element sizes."""
+    T = 1300 if H < 4000 else 700
+    gen = torch.Generator(device="cuda").manual_seed(H)
+    for i, (yd, rd, nd) in enumerate([(F32, F32, BF16), (BF16, F32, F32), (F16, BF16, F16), (F32, BF16, F32)]):
+        gate = make_gate(gen, kind, T, H, yd)
+        check(rand(gen, T, H, dtype=rd), rand(gen, T, H, dtype=yd), post_norm=i != 2, w_post=rand(gen, H) if i else None,
+              gate=gate, sigmoid=i % 2 == 1, alpha=0.75, beta=1.25, w_pre=rand(gen, H, dtype=BF16) if i != 1 else None,
+              w_offset=1.0, norm_dtype=nd, in_place=i == 3)
+
+
+@pytest.mark.parametrize("H", [520, 2048, 5000])
+def test_many_rows_norm_alone_and_padded(H):
+    gen = torch.Generator(device="cuda").manual_seed(H + 1)
+    T = 900
+    check(rand(gen, T, H), w_pre=rand(gen, H), norm_dtype=F32)
+    check(rand(gen, T, H, dtype=BF16), alpha=0.5, w_pre=rand(gen, H))
+    # rows of a wider matrix; outputs left out in turn
+    res, y = rand(gen, T, H + 12)[:, :H], rand(gen, T, H + 8, dtype=BF16)[:, :H]
+    want_r, dr, want_n, dn = reference(res, y, True, None, None, False, 1.0, 1.0, None, 0.0, 1e-6)
+    out, n = fb.moe_ffn_norm_residual(res, y, True, res_out=torch.empty(T, H, device="cuda"), norm_dtype=F32)
+    assert float(((out.double() - want_r).abs() - dr - half_step(want_r.abs() + dr, F32)).max()) <= 0
+    assert float(((n.double() - want_n).abs() - dn - half_step(want_n.abs() + dn, F32)).max()) <= 0
+    _, only = fb.moe_ffn_norm_residual(res, norm_dtype=F32)
+    want = reference(res, None, False, None, None, False, 1.0, 1.0, None, 0.0, 1e-6)
+    assert float(((only.double() - want[2]).abs() - want[3] - half_step(want[2].abs() + want[3], F32)).max()) <= 0
+    # a zero row between others: nothing of theirs may reach it
+    res = rand(gen, T, H)
+    res[T // 2] = 0
+    _, n = fb.moe_ffn_norm_residual(res, norm_dtype=F32)
+    assert float(n[T // 2].abs().max()) == 0
+
+
+def test_residual_alone():
+    """No second norm: the C entry with normed left out."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    for T, H in ((3, 100), (700, 2048), (700, 2050)):
+        res, y = rand(gen, T, H), rand(gen, T, H)
+        want = fb.moe_ffn_norm_residual(res, y, True, res_out=torch.empty_like(res))[0]
+        out = torch.zeros_like(res)
+        a = fb.NormArgs(T, H, 0, 0, 1, 0, 0, 0, 1, 0, 0, 1.0, 1.0, 0.0, 1e-6, H, H, H, H, H)
+        rc = fb.lib().moe_ffn_norm_residual(a, torch.cuda.current_stream().cuda_stream, res.data_ptr(), y.data_ptr(),
+                                            None, None, None, out.data_ptr(), None)
+        torch.cuda.synchronize()
+        assert rc == fb.OK and torch.equal(out, want)

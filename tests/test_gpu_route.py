@@ -194,3 +194,29 @@ def test_repeats_and_streams_and_graph():
 def test_no_tokens():
     ids, w = fb.moe_ffn_route(torch.zeros(0, 16, device="cuda"), 4)
     assert ids.shape == (0, 4) and w.shape == (0, 4)
+
+
+@pytest.mark.parametrize("T,E,k,groups,top_groups,dtype", [
+    (6000, 64, 6, 1, 1, torch.float32), (5000, 64, 4, 8, 4, torch.bfloat16), (4000, 50, 8, 1, 1, torch.float16),
+])
+def test_many_tokens(T, E, k, groups, top_groups, dtype):
+    """More tokens than the GPU has warps for at once."""
+    lg = make(T, E, dtype, seed=T)
+    for score in (fb.SCORE_SOFTMAX, fb.SCORE_SIGMOID):
+        check(lg, k, make_bias(E), score, groups, top_groups, fb.GROUP_TOP2)
+    check(lg, k, None, fb.SCORE_SOFTMAX, groups, top_groups)
+
+
+@pytest.mark.parametrize("k", [8, 20, 32])
+def test_more_candidates_than_lanes(k):
+    """Long runs of scores next to the cut, equal and almost equal."""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    lg = (torch.randn(6, 256, generator=g, device="cuda") * 1e-7).float()
+    lg[1] = 0.5
+    lg[2, ::2] = 0.5
+    lg[3] = (torch.randn(256, generator=g, device="cuda") * 2).bfloat16().float()
+    for bias in (None, torch.zeros(256, device="cuda"), make_bias(256) * 1e-7):
+        for score in (fb.SCORE_SOFTMAX, fb.SCORE_SIGMOID):
+            check(lg, k, bias, score)
+            check(lg, k, bias, score, 8, 4, fb.GROUP_TOP2)
+            check(lg, k, bias, score, 4, 2, fb.GROUP_MAX)

@@ -130,6 +130,7 @@ def adapters_args(**kw):
         (dict(K=60), fb.ERR_UNSUPPORTED),
         (dict(K=0), fb.ERR_UNSUPPORTED),
         (dict(N=0), fb.ERR_UNSUPPORTED),
+        (dict(T=(1 << 24) + 1), fb.ERR_UNSUPPORTED),
     ],
 )
 def test_adapters_refuse(lib, change, status):
