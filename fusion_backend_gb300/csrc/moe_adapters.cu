@@ -63,34 +63,38 @@ int splits_for(int sms, int tiles, int K) {
   return s < 1 ? 1 : s < most ? s : most;
 }
 
+// Parts of K at most: the fewest tiles that T tokens can make, an even number.
+int most_splits(int T, int K) { return (splits_for(kMaxSms, (T + 63) / 64, K) + 1) / 2 * 2; }
+
 }  // namespace
 
-// v for every part of K, then (many tokens) the order and the marks.  The
-// fewest tiles that T tokens can make give the most parts.
+// v for every part of K, then (many tokens) the order and the marks.
 size_t adapters_workspace(int T, int K, int N, int R) {
   (void)N;
-  const size_t v = align256((size_t)splits_for(kMaxSms, (T + 63) / 64, K) * T * R * 4);
+  const size_t v = align256((size_t)most_splits(T, K) * T * R * 4);
   return T <= kScanT ? v : v + 2 * align256((size_t)T * 4) + align256((size_t)T);
 }
 
 cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream) {
+  const uintptr_t four = p.y_dtype == kF32 ? 16 : 8;
+  p.vec = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % four == 0 &&
+          reinterpret_cast<uintptr_t>(p.out) % four == 0 && (p.T == 1 || (p.y_stride % 4 == 0 && p.out_stride % 4 == 0));
   // tokens a tile: 64, or 8 where an adapter has no more than that on average
   // (an adapter with more is then read once every 8)
   p.tile = p.T <= 8 || p.T / 8 <= p.n ? 8 : 64;
   const int least = (p.T + p.tile - 1) / p.tile, likely = least > p.n ? least : p.n < p.T ? p.n : p.T;
   p.splits = splits_for(p.sms, likely, p.K);
+  if (p.tile == 64) p.splits = (p.splits + 1) / 2 * 2;
   // columns a block of k_expand goes through: finding the tile and staging its v
   // are paid once a block, so as many as leave two blocks for every SM
-  const int chunks = (p.N + kThreads - 1) / kThreads;
-  int each = (int)(((long long)likely * chunks + 2 * p.sms - 1) / (2 * p.sms));
-  p.cols = (each > chunks ? chunks : each) * kThreads;
-  const uintptr_t four = p.y_dtype == kF32 ? 16 : 8;
-  p.vec = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % four == 0 &&
-          reinterpret_cast<uintptr_t>(p.out) % four == 0 && (p.T == 1 || (p.y_stride % 4 == 0 && p.out_stride % 4 == 0));
+  const int step = p.tile == 64 && p.N >= 512 && p.vec ? 2 * kThreads : kThreads;
+  const int chunks = (p.N + step - 1) / step;
+  const int each = (int)(((long long)likely * chunks + 2 * p.sms - 1) / (2 * p.sms));
+  p.cols = (each > chunks ? chunks : each) * step;
   int blocks = p.T;
   if (p.T > kScanT) {
     const int wn = (p.T + kWindow - 1) / kWindow, len = p.T < kWindow ? p.T : kWindow;
-    uint8_t* w = reinterpret_cast<uint8_t*>(p.v) + align256((size_t)splits_for(kMaxSms, (p.T + 63) / 64, p.K) * p.T * p.R * 4);
+    uint8_t* w = reinterpret_cast<uint8_t*>(p.v) + align256((size_t)most_splits(p.T, p.K) * p.T * p.R * 4);
     p.order = reinterpret_cast<int32_t*>(w);
     p.adapter_at = reinterpret_cast<int32_t*>(w + align256((size_t)p.T * 4));
     p.marks = w + 2 * align256((size_t)p.T * 4);

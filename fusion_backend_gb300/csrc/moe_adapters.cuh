@@ -223,10 +223,12 @@ __global__ void __launch_bounds__(kThreads) k_shrink(const __grid_constant__ Ada
   }
 }
 
-// Many tokens an adapter.  Blocks (tile of 64 tokens, part of K, 64 rows of A):
-// warp w has tokens 8 w .. of the tile and the whole part of K, so nothing is
-// summed between warps; the adapter's rows come from L1 for all but the first
-// warp that asks.  UN 32-column blocks of x are asked for at once.
+// Many tokens an adapter.  Blocks (tile of 64 tokens, two parts of K, 64 rows of
+// A): warp w has tokens 16 (w mod 4) .. of the tile and the part 2 blockIdx.y +
+// w / 4 of K, so nothing is summed between warps; the adapter's rows come from L1
+// for all but the first warp that asks.  What bounds it is the L1 cycles of those
+// reads (eight rows an access), so a warp takes two 8-token tiles against every
+// row it reads.  UN 32-column blocks of x are asked for at once.
 template <bool F16, int MT>
 __global__ void __launch_bounds__(kThreads, 2) k_shrink_wide(const __grid_constant__ AdapterParams P) {
   constexpr int UN = 4;
@@ -236,51 +238,65 @@ __global__ void __launch_bounds__(kThreads, 2) k_shrink_wide(const __grid_consta
   pdl_launch_dependents();
   int a, n;
   if (!find_tile<64>(P, list, a, n)) return;
-  const int r0 = blockIdx.z * kRankChunk, rank = adapter_rank(P, a) - r0;
-  if (rank <= 0 || 8 * warp >= n) return;
-  const int part = (P.K + 32 * P.splits - 1) / (32 * P.splits) * 32;
-  const int k_end = min(P.K, part * ((int)blockIdx.y + 1));
-  const int i = 8 * warp + g;
-  const uint16_t* const xr = i < n ? P.x + (size_t)list[i] * P.x_stride : nullptr;
-  const uint16_t* const ar = P.A + ((size_t)a * P.R + r0) * P.K;
-  float d[MT][4];
+  const int r0 = blockIdx.z * kRankChunk, rank = adapter_rank(P, a) - r0, t0 = 16 * (warp & 3);
+  if (rank <= 0 || t0 >= n) return;
+  const int split = 2 * blockIdx.y + (warp >> 2), part = (P.K + 32 * P.splits - 1) / (32 * P.splits) * 32;
+  const int k_end = min(P.K, part * (split + 1));
+  // (a token past the tile's last is its last: its product is not stored)
+  const uint16_t* const x0 = P.x + (size_t)list[min(t0 + g, n - 1)] * P.x_stride;
+  const uint16_t* const x1 = P.x + (size_t)list[min(t0 + 8 + g, n - 1)] * P.x_stride;
+  const uint16_t* const ar = P.A + ((size_t)a * P.R + r0 + g) * P.K;
+  float d[MT][2][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) d[m][0] = d[m][1] = d[m][2] = d[m][3] = 0.f;
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) d[m][j][0] = d[m][j][1] = d[m][j][2] = d[m][j][3] = 0.f;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 xv[UN];
-  auto ask = [&](int k, uint4& v) { v = xr && k < k_end ? *reinterpret_cast<const uint4*>(xr + k) : zero; };
-  const int k_first = part * blockIdx.y + 8 * q;
+  uint4 xv[UN][2];
+  auto ask = [&](int k, uint4 (&v)[2]) {
+    v[0] = k < k_end ? *reinterpret_cast<const uint4*>(x0 + k) : zero;
+    v[1] = k < k_end ? *reinterpret_cast<const uint4*>(x1 + k) : zero;
+  };
+  const int k_first = part * split + 8 * q;
 #pragma unroll
   for (int u = 0; u < UN; ++u) ask(k_first + 32 * u, xv[u]);
   for (int k0 = k_first; k0 - 8 * q < k_end; k0 += 32 * UN) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int k = k0 + 32 * u;
-      const uint4 x = xv[u];
+      const uint4 xa = xv[u][0], xb = xv[u][1];
       ask(k + 32 * UN, xv[u]);
-      uint4 av[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint4 av[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          av[h] = k < k_end && 16 * m + 8 * h + g < rank
+                      ? *reinterpret_cast<const uint4*>(ar + (size_t)(16 * m + 8 * h) * P.K + k)
+                      : zero;
+        mma16816<F16>(d[m][0], av[0].x, av[1].x, av[0].y, av[1].y, xa.x, xa.y);
+        mma16816<F16>(d[m][1], av[0].x, av[1].x, av[0].y, av[1].y, xb.x, xb.y);
+        mma16816<F16>(d[m][0], av[0].z, av[1].z, av[0].w, av[1].w, xa.z, xa.w);
+        mma16816<F16>(d[m][1], av[0].z, av[1].z, av[0].w, av[1].w, xb.z, xb.w);
+      }
+    }
+  }
+  // D: row 16 m + g (+ 8), token 2q (+ 1) of the eight
+  float* const v = P.v + (size_t)split * P.T * P.R + r0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int tok = t0 + 8 * j + 2 * q + c;
+      if (tok >= n) continue;
+      float* const row = v + (size_t)list[tok] * P.R;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = 16 * m + 8 * h + g;
-          av[m][h] = k < k_end && r < rank ? *reinterpret_cast<const uint4*>(ar + (size_t)r * P.K + k) : zero;
+          if (r0 + r < P.R) row[r] = d[m][j][2 * h + c];
         }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma16816<F16>(d[m], av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y, x.x, x.y);
-        mma16816<F16>(d[m], av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w, x.z, x.w);
-      }
-    }
-  }
-  // D: row 16 m + g (+ 8), token 2q (+ 1) of the warp's eight
-  float* const v = P.v + (size_t)blockIdx.y * P.T * P.R + r0;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int r = 16 * m + 8 * (c >> 1) + g, tok = 8 * warp + 2 * q + (c & 1);
-      if (tok < n && r0 + r < P.R) v[(size_t)list[tok] * P.R + r] = d[m][c];
     }
 }
 
@@ -302,10 +318,14 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
   constexpr int TPT = kThreads / TILE;
   const int tok = tid / TPT, part = tid % TPT, padded = (rank + 15) & ~15;
   const float* const v = P.v + (tok < n ? (size_t)list[tok] * P.R : 0);
+  const size_t part_step = (size_t)P.T * P.R;  // from a part of K to the next
   auto v_of = [&](int r) {
     float sum = 0.f;
-    if (tok < n && r < rank)
-      for (int k = 0; k < P.splits; ++k) sum += __ldcg(v + (size_t)k * P.T * P.R + r);
+    if (tok < n && r < rank) {
+      const float* p = v + r;
+#pragma unroll 2
+      for (int k = 0; k < P.splits; ++k, p += part_step) sum += __ldcg(p);
+    }
     return sum;
   };
   float up = 1.f, down = 1.f;
@@ -338,38 +358,24 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
   __syncthreads();
 }
 
-// One 16-wide step of the rank for 8 tokens: the two 16-row tiles of B against
-// the terms of v (v: the lane's first; term_at elements to the next), the smallest
-// first.
-template <bool F16, int TERMS, bool ZERO>
-MOE_DEV void mma_terms(const uint2 (&b)[4], const uint16_t* v, int term_at, float* d0, float* d1) {
-  uint2 t[TERMS];
-#pragma unroll
-  for (int i = 0; i < TERMS; ++i) t[i] = *reinterpret_cast<const uint2*>(v + i * term_at);
-  mma16816<F16, ZERO>(d0, b[0].x, b[1].x, b[0].y, b[1].y, t[TERMS - 1].x, t[TERMS - 1].y);
-  mma16816<F16, ZERO>(d1, b[2].x, b[3].x, b[2].y, b[3].y, t[TERMS - 1].x, t[TERMS - 1].y);
-#pragma unroll
-  for (int i = TERMS - 2; i >= 0; --i) {
-    mma16816<F16>(d0, b[0].x, b[1].x, b[0].y, b[1].y, t[i].x, t[i].y);
-    mma16816<F16>(d1, b[2].x, b[3].x, b[2].y, b[3].y, t[i].x, t[i].y);
-  }
-}
-
-// Blocks (tile, columns, 256 at a time); warp w has 32 w .. of them as two 16-row
-// tiles of B, whose rows are dealt so that a lane ends with four neighbouring
-// columns n0 + 4g .. + 3 of tokens 2q and 2q + 1.  B stays in registers (ST 16-wide
-// steps of the rank) while the warp goes through the tile's tokens, D groups of
-// eight at a time, whose y is asked for a round ahead; nothing is waited for
-// between warps.  The ids, the order, B and the first y are read ahead of the wait
-// on the first product, which writes none of them.  YK: y and out are fp32 (0) or
-// 16-bit (1) in rows that allow accesses of four elements, or anything (2).
-// The whole call at 8192 tokens, 2048 x 2048, rank 32, fp32 y: 69 us (2.5 TB/s).
-// Two blocks an SM and as many columns a block as give every SM two: three with
-// fewer columns 76 us, six 82; B streamed through shared memory under a tile's
-// fixed tokens 76 us; the first form (a thread an output element) 1180 us.
-template <bool F16, int TILE, int ST, int YK>
-__global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
-  constexpr int D = TILE == 8 || YK == 2 ? 1 : 4;
+// Blocks (tile, columns, 256 HV at a time); warp w has 32 HV w .. of them, HV times
+// 32 as two 16-row tiles of B, whose rows are dealt so that a lane ends with four
+// neighbouring columns n0 + 4g .. + 3 of tokens 2q and 2q + 1.  B stays in
+// registers (ST 16-wide steps of the rank) while the warp goes through the tile's
+// tokens, D groups of eight at a time, whose y is asked for a round ahead; nothing
+// is waited for between warps.  The ids, the order, B and the first y are read
+// ahead of the wait on the first product, which writes none of them.  YK: y and
+// out are fp32 (0) or 16-bit (1) in rows that allow accesses of four elements, or
+// anything (2).
+// For many tokens the L1 cycles of shared and global accesses bound it, then the
+// products (16 cycles an instruction and scheduler); HV = 2 reads a token's v and
+// its row's place once for 64 columns instead of 32 (the whole call at 8192 tokens,
+// 2048 x 2048, rank 32, fp32 y: 71 -> 67 us, 2.5 TB/s; the first form, a thread an
+// output element, 1180 us).  Two blocks an SM and as many columns a block as give
+// every SM two: with three 76 against 69 us, with six 82.
+template <bool F16, int TILE, int ST, int YK, int HV>
+__global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
+  constexpr int D = TILE == 8 || YK == 2 ? 1 : HV == 2 ? 2 : 4;
   constexpr int YB = YK == 0 ? 4 : 2, TERMS = kTerms<F16, YK>;
   extern __shared__ __align__(16) uint32_t vs[];  // [TERMS][TILE][pitch / 2]; pitch in elements
   __shared__ int list[TILE];
@@ -393,55 +399,63 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
   __syncthreads();
   const uint16_t* const v0 = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
   bool staged = false;
-  for (int w0 = c_first + 32 * warp; w0 - 32 * warp < c_end; w0 += kThreads) {
-    const int n0 = w0 + 4 * g;
-    const bool in = n0 < c_end;
+  for (int b0 = c_first; b0 < c_end; b0 += HV * kThreads) {
+    const int n0 = b0 + 32 * HV * warp + 4 * g;  // and n0 + 32
+    bool in[HV];
+#pragma unroll
+    for (int v = 0; v < HV; ++v) in[v] = n0 + 32 * v < c_end;
     // B: the lane's four columns, four k a step
-    uint2 bv[ST][4];
+    uint2 bv[ST][HV][4];
 #pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      const int r = 16 * s + 4 * q;
+    for (int s = 0; s < ST; ++s)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) bv[s][c] = make_uint2(0u, 0u);
-      if (r >= rank) continue;
-      const uint16_t* row = P.B + ((size_t)a * P.N + n0) * P.R + r;
+      for (int v = 0; v < HV; ++v) {
+        uint2(&b)[4] = bv[s][v];
+        const int r = 16 * s + 4 * q, nv = n0 + 32 * v;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (n0 + c < P.N) {
-          if (P.R % 4 == 0) {
-            bv[s][c] = *reinterpret_cast<const uint2*>(row);
-          } else {
-            bv[s][c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
-            bv[s][c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
-          }
-        }
-        row += P.R;
-      }
-      if (r + 4 > rank) {  // what lies past the rank does not count
-        const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 3 < rank ? ~0u : r + 2 < rank ? 0xFFFFu : 0u;
+        for (int c = 0; c < 4; ++c) b[c] = make_uint2(0u, 0u);
+        if (r >= rank) continue;
+        const uint16_t* row = P.B + ((size_t)a * P.N + nv) * P.R + r;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          bv[s][c].x &= mx;
-          bv[s][c].y &= my;
+          if (nv + c < P.N) {
+            if (P.R % 4 == 0) {
+              b[c] = *reinterpret_cast<const uint2*>(row);
+            } else {
+              b[c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
+              b[c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
+            }
+          }
+          row += P.R;
+        }
+        if (r + 4 > rank) {  // what lies past the rank does not count
+          const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 3 < rank ? ~0u : r + 2 < rank ? 0xFFFFu : 0u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            b[c].x &= mx;
+            b[c].y &= my;
+          }
         }
       }
-    }
     // y of tokens 8 j + 2q (+ 1), as it lies in memory (YK < 2)
     const uint8_t* const y0 = static_cast<const uint8_t*>(P.y) + (size_t)n0 * YB;
     uint8_t* const o0 = static_cast<uint8_t*>(P.out) + (size_t)n0 * YB;
-    uint4 yv[D][2];
+    uint4 yv[D][2][HV];
     auto ask = [&](int j0) {
-      if (!in || YK == 2) return;
 #pragma unroll
-      for (int u = 0; u < D; ++u)
+      for (int u = 0; u < (YK < 2 ? D : 0); ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint8_t* at = y0 + s_row[8 * (j0 + u) + 2 * q + h].x;
-          if (YK == 0) {
-            yv[u][h] = *reinterpret_cast<const uint4*>(at);
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(at);
-            yv[u][h].x = w.x, yv[u][h].y = w.y;
+#pragma unroll
+          for (int v = 0; v < HV; ++v) {
+            if (!in[v]) continue;
+            if (YK == 0) {
+              yv[u][h][v] = *reinterpret_cast<const uint4*>(at + 32 * v * YB);
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(at + 32 * v * YB);
+              yv[u][h][v].x = w.x, yv[u][h][v].y = w.y;
+            }
           }
         }
     };
@@ -456,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
     // D groups of eight tokens at a time, whole ones (v of tokens past the last
     // is 0, their y is the last's; they are not stored)
     for (int j0 = 0; 8 * j0 < n; j0 += D) {
-      float d[D][2][4];
+      float d[D][HV][2][4];
       if (rank > 0) {
 #pragma unroll
         for (int s = 0; s < ST; ++s) {
@@ -464,35 +478,51 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 #pragma unroll
           for (int u = 0; u < D; ++u) {
             const uint16_t* v = v0 + 8 * (j0 + u) * pitch + 16 * s;
-            if (s == 0)
-              mma_terms<F16, TERMS, true>(bv[s], v, TILE * pitch, d[u][0], d[u][1]);
-            else
-              mma_terms<F16, TERMS, false>(bv[s], v, TILE * pitch, d[u][0], d[u][1]);
+            uint2 t[TERMS];
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i) t[i] = *reinterpret_cast<const uint2*>(v + i * TILE * pitch);
+            // the smallest term first
+#pragma unroll
+            for (int i = TERMS - 1; i >= 0; --i)
+#pragma unroll
+              for (int w = 0; w < HV; ++w)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  const uint2 b0 = bv[s][w][2 * m], b1 = bv[s][w][2 * m + 1];
+                  if (s == 0 && i == TERMS - 1)
+                    mma16816<F16, true>(d[u][w][m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
+                  else
+                    mma16816<F16>(d[u][w][m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
+                }
           }
         }
       } else {
 #pragma unroll
         for (int u = 0; u < D; ++u)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) d[u][0][c] = d[u][1][c] = 0.f;
+          for (int w = 0; w < HV; ++w)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) d[u][w][0][c] = d[u][w][1][c] = 0.f;
       }
-      float y[D][2][4];
+      float y[D][2][HV][4];
 #pragma unroll
       for (int u = 0; u < D; ++u) {
         const float2 scale = *reinterpret_cast<const float2*>(s_scale + 8 * (j0 + u) + 2 * q);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (YK < 2) {
-            raw_values4(yv[u][h], YK == 0 ? kF32 : P.y_dtype, y[u][h]);
-          } else {
-            const size_t at = (size_t)list[min(8 * (j0 + u) + 2 * q + h, n - 1)] * P.y_stride + n0;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[u][h][c] = n0 + c < c_end ? elem_load(P.y, P.y_dtype, at + c) : 0.f;
+          for (int v = 0; v < HV; ++v) {
+            float(&z)[4] = y[u][h][v];
+            if (YK < 2) {
+              raw_values4(yv[u][h][v], YK == 0 ? kF32 : P.y_dtype, z);
+            } else {
+              const size_t at = (size_t)list[min(8 * (j0 + u) + 2 * q + h, n - 1)] * P.y_stride + n0 + 32 * v;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) z[c] = n0 + 32 * v + c < c_end ? elem_load(P.y, P.y_dtype, at + c) : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) z[c] = fmaf(h ? scale.y : scale.x, d[u][v][c >> 1][2 * (c & 1) + h], z[c]);
           }
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            y[u][h][c] = fmaf(h ? scale.y : scale.x, d[u][c >> 1][2 * (c & 1) + h], y[u][h][c]);
-        }
       }
       if (8 * (j0 + D) < n) ask(j0 + D);
 #pragma unroll
@@ -500,18 +530,23 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int i = 8 * (j0 + u) + 2 * q + h;
-          if (!in || i >= n) continue;
-          const float* v = y[u][h];
-          if (YK == 0) {
-            *reinterpret_cast<float4*>(o0 + s_row[i].y) = make_float4(v[0], v[1], v[2], v[3]);
-          } else if (YK == 1) {
-            *reinterpret_cast<uint2*>(o0 + s_row[i].y) =
-                make_uint2(pack2(P.y_dtype, v[0], v[1]), pack2(P.y_dtype, v[2], v[3]));
-          } else {
-            const size_t at = (size_t)list[i] * P.out_stride + n0;
+          if (i >= n) continue;
+          uint8_t* const at = o0 + s_row[i].y;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (n0 + c < c_end) elem_store(P.out, P.y_dtype, at + c, v[c]);
+          for (int v = 0; v < HV; ++v) {
+            if (!in[v]) continue;
+            const float(&z)[4] = y[u][h][v];
+            if (YK == 0) {
+              *reinterpret_cast<float4*>(at + 32 * v * YB) = make_float4(z[0], z[1], z[2], z[3]);
+            } else if (YK == 1) {
+              *reinterpret_cast<uint2*>(at + 32 * v * YB) =
+                  make_uint2(pack2(P.y_dtype, z[0], z[1]), pack2(P.y_dtype, z[2], z[3]));
+            } else {
+              const size_t to = (size_t)list[i] * P.out_stride + n0 + 32 * v;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (n0 + 32 * v + c < c_end) elem_store(P.out, P.y_dtype, to + c, z[c]);
+            }
           }
         }
     }
@@ -520,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 
 template <bool F16>
 cudaError_t launch_products(const AdapterParams& p, int blocks, cudaStream_t stream) {
-  const dim3 grid(blocks, p.splits, (p.R + kRankChunk - 1) / kRankChunk);
+  const bool wide = p.tile == 64;
+  const dim3 grid(blocks, wide ? p.splits / 2 : p.splits, (p.R + kRankChunk - 1) / kRankChunk);
   auto shrink = [&](auto kern, int rows) {
     return launch_behind(kern, grid, kThreads, rows ? kWarps * 8 * (rows + 1) * 4 : 0, stream, p);
   };
-  const bool wide = p.tile == 64;
   cudaError_t e = wide ? p.R <= 16   ? shrink(k_shrink_wide<F16, 1>, 0)
                          : p.R <= 32 ? shrink(k_shrink_wide<F16, 2>, 0)
                                      : shrink(k_shrink_wide<F16, 4>, 0)
@@ -541,14 +576,16 @@ cudaError_t launch_products(const AdapterParams& p, int blocks, cudaStream_t str
     }
     return launch_behind(kern, eg, kThreads, smem, stream, p);
   };
-#define MOE_EXPAND(TILE, YK)                                 \
-  (p.R <= 16   ? expand(k_expand<F16, TILE, 1, YK>)          \
-   : p.R <= 32 ? expand(k_expand<F16, TILE, 2, YK>)          \
-   : p.R <= 64 ? expand(k_expand<F16, TILE, 4, YK>)          \
-               : expand(k_expand<F16, TILE, 8, YK>))
-  if (!p.vec) return wide ? MOE_EXPAND(64, 2) : MOE_EXPAND(8, 2);
-  if (p.y_dtype == kF32) return wide ? MOE_EXPAND(64, 0) : MOE_EXPAND(8, 0);
-  return wide ? MOE_EXPAND(64, 1) : MOE_EXPAND(8, 1);
+#define MOE_EXPAND(TILE, YK, HV)                                 \
+  (p.R <= 16   ? expand(k_expand<F16, TILE, 1, YK, HV>)          \
+   : p.R <= 32 ? expand(k_expand<F16, TILE, 2, YK, HV>)          \
+   : p.R <= 64 ? expand(k_expand<F16, TILE, 4, YK, HV>)          \
+               : expand(k_expand<F16, TILE, 8, YK, 1>))
+  // (64 columns a warp where there are columns for every warp of a block then)
+  if (!p.vec) return wide ? MOE_EXPAND(64, 2, 1) : MOE_EXPAND(8, 2, 1);
+  if (!wide) return p.y_dtype == kF32 ? MOE_EXPAND(8, 0, 1) : MOE_EXPAND(8, 1, 1);
+  if (p.N < 512) return p.y_dtype == kF32 ? MOE_EXPAND(64, 0, 1) : MOE_EXPAND(64, 1, 1);
+  return p.y_dtype == kF32 ? MOE_EXPAND(64, 0, 2) : MOE_EXPAND(64, 1, 2);
 #undef MOE_EXPAND
 }
 
