@@ -63,8 +63,8 @@ int splits_for(int sms, int tiles, int K) {
   return s < 1 ? 1 : s < most ? s : most;
 }
 
-// Parts of K at most: the fewest tiles that T tokens can make, an even number.
-int most_splits(int T, int K) { return (splits_for(kMaxSms, (T + 63) / 64, K) + 1) / 2 * 2; }
+// Parts of K at most: those of the fewest tiles that T tokens can make.
+int most_splits(int T, int K) { return 2 * splits_for(kMaxSms, (T + 63) / 64, K); }
 
 }  // namespace
 
@@ -84,7 +84,7 @@ cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream) {
   p.tile = p.T <= 8 || p.T / 8 <= p.n ? 8 : 64;
   const int least = (p.T + p.tile - 1) / p.tile, likely = least > p.n ? least : p.n < p.T ? p.n : p.T;
   p.splits = splits_for(p.sms, likely, p.K);
-  if (p.tile == 64) p.splits = (p.splits + 1) / 2 * 2;
+  if (p.tile == 64) p.splits *= 2;  // two parts a block
   // columns a block of k_expand goes through: finding the tile and staging its v
   // are paid once a block, so as many as leave two blocks for every SM
   const int step = p.tile == 64 && p.N >= 512 && p.vec ? 2 * kThreads : kThreads;

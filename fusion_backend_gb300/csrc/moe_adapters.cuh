@@ -370,8 +370,8 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
 // For many tokens the L1 cycles of shared and global accesses bound it, then the
 // products (16 cycles an instruction and scheduler); HV = 2 reads a token's v and
 // its row's place once for 64 columns instead of 32 (the whole call at 8192 tokens,
-// 2048 x 2048, rank 32, fp32 y: 71 -> 67 us, 2.5 TB/s; the first form, a thread an
-// output element, 1180 us).  Two blocks an SM and as many columns a block as give
+// 2048 x 2048, rank 32, fp32 y: 71 -> 67 us, now 63 us, 2.7 TB/s; the first form,
+// a thread an output element, 1180 us).  Two blocks an SM and as many columns a block as give
 // every SM two: with three 76 against 69 us, with six 82.
 template <bool F16, int TILE, int ST, int YK, int HV>
 __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
