@@ -371,8 +371,8 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
 // products (16 cycles an instruction and scheduler); HV = 2 reads a token's v and
 // its row's place once for 64 columns instead of 32 (the whole call at 8192 tokens,
 // 2048 x 2048, rank 32, fp32 y: 71 -> 67 us, now 63 us, 2.7 TB/s; the first form,
-// a thread an output element, 1180 us).  Two blocks an SM and as many columns a block as give
-// every SM two: with three 76 against 69 us, with six 82.
+// a thread an output element, 1171 us).  Two blocks an SM, and as many columns a block
+// as give every SM two: 63 us, with one 79, with four 67.
 template <bool F16, int TILE, int ST, int YK, int HV>
 __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
   constexpr int D = TILE == 8 || YK == 2 ? 1 : HV == 2 ? 2 : 4;
