@@ -358,24 +358,163 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
   __syncthreads();
 }
 
-// Blocks (tile, columns, 256 HV at a time); warp w has 32 HV w .. of them, HV times
-// 32 as two 16-row tiles of B, whose rows are dealt so that a lane ends with four
-// neighbouring columns n0 + 4g .. + 3 of tokens 2q and 2q + 1.  B stays in
-// registers (ST 16-wide steps of the rank) while the warp goes through the tile's
-// tokens, D groups of eight at a time, whose y is asked for a round ahead; nothing
-// is waited for between warps.  The ids, the order, B and the first y are read
-// ahead of the wait on the first product, which writes none of them.  YK: y and
-// out are fp32 (0) or 16-bit (1) in rows that allow accesses of four elements, or
-// anything (2).
-// For many tokens the L1 cycles of shared and global accesses bound it, then the
-// products (16 cycles an instruction and scheduler); HV = 2 reads a token's v and
-// its row's place once for 64 columns instead of 32 (the whole call at 8192 tokens,
-// 2048 x 2048, rank 32, fp32 y: 71 -> 67 us, now 63 us, 2.7 TB/s; the first form,
-// a thread an output element, 1171 us).  Two blocks an SM, and as many columns a block
-// as give every SM two: 63 us, with one 79, with four 67.
-template <bool F16, int TILE, int ST, int YK, int HV>
-__global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
-  constexpr int D = TILE == 8 || YK == 2 ? 1 : HV == 2 ? 2 : 4;
+// Blocks (tile of 8 tokens, columns, 256 at a time); warp w has 32 w .. of them as
+// two 16-row tiles of B, whose rows are dealt so that a lane ends with four
+// neighbouring columns n0 + 4g .. + 3 of tokens 2q and 2q + 1.  The ids, the order,
+// B and y are read ahead of the wait on the first product, which writes none of
+// them.  YK: y and out are fp32 (0) or 16-bit (1) in rows that allow accesses of
+// four elements, or anything (2).
+template <bool F16, int ST, int YK>
+__global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __grid_constant__ AdapterParams P) {
+  constexpr int TILE = 8, YB = YK == 0 ? 4 : 2, TERMS = kTerms<F16, YK>;
+  extern __shared__ __align__(16) uint32_t vs[];  // [TERMS][TILE][pitch / 2]; pitch in elements
+  __shared__ int list[TILE];
+  __shared__ __align__(8) float s_scale[TILE];
+  __shared__ __align__(16) longlong2 s_row[TILE];  // bytes to the token's row of y and of out
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  int a, n;
+  if (!find_tile<TILE>(P, list, a, n)) {
+    pdl_wait();
+    pdl_launch_dependents();
+    return;
+  }
+  // (rows past the tile's last are its last: their loads need no test)
+  if (tid < TILE) {
+    const long long t = list[min(tid, n - 1)];
+    s_row[tid] = make_longlong2(t * P.y_stride * YB, t * P.out_stride * YB);
+    s_scale[tid] = 0.f;
+  }
+  const int rank = adapter_rank(P, a), pitch = expand_pitch(P.R);
+  const int c_first = P.cols * blockIdx.y, c_end = min(P.N, c_first + P.cols);
+  __syncthreads();
+  const uint16_t* const v0 = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
+  bool staged = false;
+  for (int b0 = c_first; b0 < c_end; b0 += kThreads) {
+    const int n0 = b0 + 32 * warp + 4 * g;
+    const bool in = n0 < c_end;
+    // B: the lane's four columns, four k a step
+    uint2 bv[ST][4];
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      uint2(&b)[4] = bv[s];
+      const int r = 16 * s + 4 * q;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) b[c] = make_uint2(0u, 0u);
+      if (r >= rank) continue;
+      const uint16_t* row = P.B + ((size_t)a * P.N + n0) * P.R + r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (n0 + c < P.N) {
+          if (P.R % 4 == 0) {
+            b[c] = *reinterpret_cast<const uint2*>(row);
+          } else {
+            b[c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
+            b[c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
+          }
+        }
+        row += P.R;
+      }
+      if (r + 4 > rank) {  // what lies past the rank does not count
+        const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 3 < rank ? ~0u : r + 2 < rank ? 0xFFFFu : 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          b[c].x &= mx;
+          b[c].y &= my;
+        }
+      }
+    }
+    // y of tokens 2q (+ 1), as it lies in memory (YK < 2)
+    uint4 yv[2];
+    if (YK < 2 && in) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* const at = static_cast<const uint8_t*>(P.y) + (size_t)n0 * YB + s_row[2 * q + h].x;
+        if (YK == 0) {
+          yv[h] = *reinterpret_cast<const uint4*>(at);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(at);
+          yv[h].x = w.x, yv[h].y = w.y;
+        }
+      }
+    }
+    if (!staged) {
+      pdl_wait();
+      pdl_launch_dependents();
+      if (rank == 0 && P.out == P.y) return;
+      if (rank > 0) stage_v<F16, TILE, TERMS>(P, list, a, n, rank, pitch, vs, s_scale);
+      staged = true;
+    }
+    // (v of tokens past the last is 0, their y is the last's; they are not stored)
+    float d[2][4];
+    if (rank > 0) {
+#pragma unroll
+      for (int s = 0; s < ST; ++s) {
+        if (16 * s >= rank) break;
+        uint2 t[TERMS];
+#pragma unroll
+        for (int i = 0; i < TERMS; ++i) t[i] = *reinterpret_cast<const uint2*>(v0 + i * TILE * pitch + 16 * s);
+        // the smallest term first
+#pragma unroll
+        for (int i = TERMS - 1; i >= 0; --i)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint2 b0 = bv[s][2 * m], b1 = bv[s][2 * m + 1];
+            if (s == 0 && i == TERMS - 1)
+              mma16816<F16, true>(d[m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
+            else
+              mma16816<F16>(d[m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
+          }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) d[0][c] = d[1][c] = 0.f;
+    }
+    const float2 scale = *reinterpret_cast<const float2*>(s_scale + 2 * q);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 2 * q + h;
+      if (i >= n || !in) continue;
+      float z[4];
+      if (YK < 2) {
+        raw_values4(yv[h], YK == 0 ? kF32 : P.y_dtype, z);
+      } else {
+        const size_t at = (size_t)list[i] * P.y_stride + n0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[c] = n0 + c < c_end ? elem_load(P.y, P.y_dtype, at + c) : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[c] = fmaf(h ? scale.y : scale.x, d[c >> 1][2 * (c & 1) + h], z[c]);
+      uint8_t* const at = static_cast<uint8_t*>(P.out) + (size_t)n0 * YB + s_row[i].y;
+      if (YK == 0) {
+        *reinterpret_cast<float4*>(at) = make_float4(z[0], z[1], z[2], z[3]);
+      } else if (YK == 1) {
+        *reinterpret_cast<uint2*>(at) = make_uint2(pack2(P.y_dtype, z[0], z[1]), pack2(P.y_dtype, z[2], z[3]));
+      } else {
+        const size_t to = (size_t)list[i] * P.out_stride + n0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n0 + c < c_end) elem_store(P.out, P.y_dtype, to + c, z[c]);
+      }
+    }
+  }
+}
+
+// The same for tiles of 64 tokens and 256 HV columns at a time, with the tokens as
+// the rows of the products: a lane ends with four neighbouring columns n0 + 16 p ..
+// + 3 of tokens g and g + 8, its three neighbours with the twelve behind them, so
+// that a quarter of a warp has 64 bytes each of two rows of y in one access.  (With
+// the columns as the rows it has 32 bytes each of four, and the L1's cycles, four
+// times an access's bytes, bound the kernel: 63 against 58 us for the whole call at
+// 8192 tokens, 2048 x 2048, rank 32, fp32 y.)  B stays in registers while the warp
+// goes through the tile's tokens, G times sixteen at a time, whose y is asked for a
+// round ahead; nothing is waited for between warps.  HV = 2 reads a token's v once
+// for 64 columns (71 -> 67 us there, the columns as the rows).  What is left are the
+// loads that are waited for at 16 warps an SM: the call runs at 2.9 TB/s; the first
+// form, a thread an output element, took 1171 us.  Two blocks an SM, and as many
+// columns a block as give every SM two: with one 79, with four 67 against 63 us.
+template <bool F16, int ST, int YK, int HV>
+__global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand_wide(const __grid_constant__ AdapterParams P) {
+  constexpr int TILE = 64, G = YK == 2 || HV == 2 ? 1 : 2, NP = 2 * HV;
   constexpr int YB = YK == 0 ? 4 : 2, TERMS = kTerms<F16, YK>;
   extern __shared__ __align__(16) uint32_t vs[];  // [TERMS][TILE][pitch / 2]; pitch in elements
   __shared__ int list[TILE];
@@ -400,61 +539,56 @@ __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 
   const uint16_t* const v0 = reinterpret_cast<const uint16_t*>(vs) + g * pitch + 4 * q;
   bool staged = false;
   for (int b0 = c_first; b0 < c_end; b0 += HV * kThreads) {
-    const int n0 = b0 + 32 * HV * warp + 4 * g;  // and n0 + 32
-    bool in[HV];
+    const int w0 = b0 + 32 * HV * warp, n0 = w0 + 4 * q;  // the lane's: n0 + 16 p
+    bool in[NP];
 #pragma unroll
-    for (int v = 0; v < HV; ++v) in[v] = n0 + 32 * v < c_end;
-    // B: the lane's four columns, four k a step
-    uint2 bv[ST][HV][4];
+    for (int p = 0; p < NP; ++p) in[p] = n0 + 16 * p < c_end;
+    // B: a column of each product's eight, four k a step
+    uint2 bv[ST][2 * NP];
 #pragma unroll
-    for (int s = 0; s < ST; ++s)
+    for (int s = 0; s < ST; ++s) {
+      uint2(&b)[2 * NP] = bv[s];
+      const int r = 16 * s + 4 * q;
 #pragma unroll
-      for (int v = 0; v < HV; ++v) {
-        uint2(&b)[4] = bv[s][v];
-        const int r = 16 * s + 4 * q, nv = n0 + 32 * v;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) b[c] = make_uint2(0u, 0u);
-        if (r >= rank) continue;
-        const uint16_t* row = P.B + ((size_t)a * P.N + nv) * P.R + r;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (nv + c < P.N) {
-            if (P.R % 4 == 0) {
-              b[c] = *reinterpret_cast<const uint2*>(row);
-            } else {
-              b[c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
-              b[c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
-            }
-          }
-          row += P.R;
-        }
-        if (r + 4 > rank) {  // what lies past the rank does not count
-          const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 3 < rank ? ~0u : r + 2 < rank ? 0xFFFFu : 0u;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            b[c].x &= mx;
-            b[c].y &= my;
-          }
+      for (int c = 0; c < 2 * NP; ++c) {
+        const int nc = w0 + 16 * (c >> 1) + 4 * (g >> 1) + 2 * (c & 1) + (g & 1);
+        b[c] = make_uint2(0u, 0u);
+        if (r >= rank || nc >= P.N) continue;
+        const uint16_t* const row = P.B + ((size_t)a * P.N + nc) * P.R + r;
+        if (P.R % 4 == 0) {
+          b[c] = *reinterpret_cast<const uint2*>(row);
+        } else {
+          b[c].x = row[0] | (r + 1 < rank ? (uint32_t)row[1] << 16 : 0u);
+          b[c].y = (r + 2 < rank ? row[2] : 0u) | (r + 3 < rank ? (uint32_t)row[3] << 16 : 0u);
         }
       }
-    // y of tokens 8 j + 2q (+ 1), as it lies in memory (YK < 2)
+      if (r + 4 > rank) {  // what lies past the rank does not count
+        const uint32_t mx = r + 1 < rank ? ~0u : 0xFFFFu, my = r + 3 < rank ? ~0u : r + 2 < rank ? 0xFFFFu : 0u;
+#pragma unroll
+        for (int c = 0; c < 2 * NP; ++c) {
+          b[c].x &= mx;
+          b[c].y &= my;
+        }
+      }
+    }
+    // y of tokens 16 j + g (+ 8), as it lies in memory (YK < 2)
     const uint8_t* const y0 = static_cast<const uint8_t*>(P.y) + (size_t)n0 * YB;
     uint8_t* const o0 = static_cast<uint8_t*>(P.out) + (size_t)n0 * YB;
-    uint4 yv[D][2][HV];
+    uint4 yv[G][2][NP];
     auto ask = [&](int j0) {
 #pragma unroll
-      for (int u = 0; u < (YK < 2 ? D : 0); ++u)
+      for (int u = 0; u < (YK < 2 ? G : 0); ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* at = y0 + s_row[8 * (j0 + u) + 2 * q + h].x;
+          const uint8_t* const at = y0 + s_row[16 * (j0 + u) + 8 * h + g].x;
 #pragma unroll
-          for (int v = 0; v < HV; ++v) {
-            if (!in[v]) continue;
+          for (int p = 0; p < NP; ++p) {
+            if (!in[p]) continue;
             if (YK == 0) {
-              yv[u][h][v] = *reinterpret_cast<const uint4*>(at + 32 * v * YB);
+              yv[u][h][p] = *reinterpret_cast<const uint4*>(at + 16 * p * YB);
             } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(at + 32 * v * YB);
-              yv[u][h][v].x = w.x, yv[u][h][v].y = w.y;
+              const uint2 w = *reinterpret_cast<const uint2*>(at + 16 * p * YB);
+              yv[u][h][p].x = w.x, yv[u][h][p].y = w.y;
             }
           }
         }
@@ -467,85 +601,80 @@ __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 
       if (rank > 0) stage_v<F16, TILE, TERMS>(P, list, a, n, rank, pitch, vs, s_scale);
       staged = true;
     }
-    // D groups of eight tokens at a time, whole ones (v of tokens past the last
-    // is 0, their y is the last's; they are not stored)
-    for (int j0 = 0; 8 * j0 < n; j0 += D) {
-      float d[D][HV][2][4];
+    // (v of tokens past the last is 0, their y is the last's; they are not stored)
+    for (int j0 = 0; 16 * j0 < n; j0 += G) {
+      float d[G][2 * NP][4];
       if (rank > 0) {
 #pragma unroll
         for (int s = 0; s < ST; ++s) {
           if (16 * s >= rank) break;
 #pragma unroll
-          for (int u = 0; u < D; ++u) {
-            const uint16_t* v = v0 + 8 * (j0 + u) * pitch + 16 * s;
-            uint2 t[TERMS];
-#pragma unroll
-            for (int i = 0; i < TERMS; ++i) t[i] = *reinterpret_cast<const uint2*>(v + i * TILE * pitch);
+          for (int u = 0; u < G; ++u) {
+            const uint16_t* const v = v0 + 16 * (j0 + u) * pitch + 16 * s;
             // the smallest term first
 #pragma unroll
-            for (int i = TERMS - 1; i >= 0; --i)
+            for (int i = TERMS - 1; i >= 0; --i) {
+              const uint2 t0 = *reinterpret_cast<const uint2*>(v + i * TILE * pitch);
+              const uint2 t1 = *reinterpret_cast<const uint2*>(v + (i * TILE + 8) * pitch);
 #pragma unroll
-              for (int w = 0; w < HV; ++w)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  const uint2 b0 = bv[s][w][2 * m], b1 = bv[s][w][2 * m + 1];
-                  if (s == 0 && i == TERMS - 1)
-                    mma16816<F16, true>(d[u][w][m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
-                  else
-                    mma16816<F16>(d[u][w][m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
-                }
+              for (int c = 0; c < 2 * NP; ++c) {
+                if (s == 0 && i == TERMS - 1)
+                  mma16816<F16, true>(d[u][c], t0.x, t1.x, t0.y, t1.y, bv[s][c].x, bv[s][c].y);
+                else
+                  mma16816<F16>(d[u][c], t0.x, t1.x, t0.y, t1.y, bv[s][c].x, bv[s][c].y);
+              }
+            }
           }
         }
       } else {
 #pragma unroll
-        for (int u = 0; u < D; ++u)
+        for (int u = 0; u < G; ++u)
 #pragma unroll
-          for (int w = 0; w < HV; ++w)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) d[u][w][0][c] = d[u][w][1][c] = 0.f;
+          for (int c = 0; c < 2 * NP; ++c) d[u][c][0] = d[u][c][1] = d[u][c][2] = d[u][c][3] = 0.f;
       }
-      float y[D][2][HV][4];
+      float y[G][2][NP][4];
 #pragma unroll
-      for (int u = 0; u < D; ++u) {
-        const float2 scale = *reinterpret_cast<const float2*>(s_scale + 8 * (j0 + u) + 2 * q);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int v = 0; v < HV; ++v) {
-            float(&z)[4] = y[u][h][v];
-            if (YK < 2) {
-              raw_values4(yv[u][h][v], YK == 0 ? kF32 : P.y_dtype, z);
-            } else {
-              const size_t at = (size_t)list[min(8 * (j0 + u) + 2 * q + h, n - 1)] * P.y_stride + n0 + 32 * v;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) z[c] = n0 + 32 * v + c < c_end ? elem_load(P.y, P.y_dtype, at + c) : 0.f;
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) z[c] = fmaf(h ? scale.y : scale.x, d[u][v][c >> 1][2 * (c & 1) + h], z[c]);
-          }
-      }
-      if (8 * (j0 + D) < n) ask(j0 + D);
-#pragma unroll
-      for (int u = 0; u < D; ++u)
+      for (int u = 0; u < G; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int i = 8 * (j0 + u) + 2 * q + h;
+          const int i = 16 * (j0 + u) + 8 * h + g;
+          const float scale = s_scale[i];
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            float(&z)[4] = y[u][h][p];
+            if (YK < 2) {
+              raw_values4(yv[u][h][p], YK == 0 ? kF32 : P.y_dtype, z);
+            } else {
+              const size_t at = (size_t)list[min(i, n - 1)] * P.y_stride + n0 + 16 * p;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) z[c] = n0 + 16 * p + c < c_end ? elem_load(P.y, P.y_dtype, at + c) : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) z[c] = fmaf(scale, d[u][2 * p + (c >> 1)][2 * h + (c & 1)], z[c]);
+          }
+        }
+      if (16 * (j0 + G) < n) ask(j0 + G);
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 16 * (j0 + u) + 8 * h + g;
           if (i >= n) continue;
           uint8_t* const at = o0 + s_row[i].y;
 #pragma unroll
-          for (int v = 0; v < HV; ++v) {
-            if (!in[v]) continue;
-            const float(&z)[4] = y[u][h][v];
+          for (int p = 0; p < NP; ++p) {
+            if (!in[p]) continue;
+            const float(&z)[4] = y[u][h][p];
             if (YK == 0) {
-              *reinterpret_cast<float4*>(at + 32 * v * YB) = make_float4(z[0], z[1], z[2], z[3]);
+              *reinterpret_cast<float4*>(at + 16 * p * YB) = make_float4(z[0], z[1], z[2], z[3]);
             } else if (YK == 1) {
-              *reinterpret_cast<uint2*>(at + 32 * v * YB) =
+              *reinterpret_cast<uint2*>(at + 16 * p * YB) =
                   make_uint2(pack2(P.y_dtype, z[0], z[1]), pack2(P.y_dtype, z[2], z[3]));
             } else {
-              const size_t to = (size_t)list[i] * P.out_stride + n0 + 32 * v;
+              const size_t to = (size_t)list[i] * P.out_stride + n0 + 16 * p;
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                if (n0 + 32 * v + c < c_end) elem_store(P.out, P.y_dtype, to + c, z[c]);
+                if (n0 + 16 * p + c < c_end) elem_store(P.out, P.y_dtype, to + c, z[c]);
             }
           }
         }
@@ -576,16 +705,22 @@ cudaError_t launch_products(const AdapterParams& p, int blocks, cudaStream_t str
     }
     return launch_behind(kern, eg, kThreads, smem, stream, p);
   };
-#define MOE_EXPAND(TILE, YK, HV)                                 \
-  (p.R <= 16   ? expand(k_expand<F16, TILE, 1, YK, HV>)          \
-   : p.R <= 32 ? expand(k_expand<F16, TILE, 2, YK, HV>)          \
-   : p.R <= 64 ? expand(k_expand<F16, TILE, 4, YK, HV>)          \
-               : expand(k_expand<F16, TILE, 8, YK, 1>))
+#define MOE_EXPAND(YK)                          \
+  (p.R <= 16   ? expand(k_expand<F16, 1, YK>)   \
+   : p.R <= 32 ? expand(k_expand<F16, 2, YK>)   \
+   : p.R <= 64 ? expand(k_expand<F16, 4, YK>)   \
+               : expand(k_expand<F16, 8, YK>))
+#define MOE_EXPAND_WIDE(YK, HV)                        \
+  (p.R <= 16   ? expand(k_expand_wide<F16, 1, YK, HV>) \
+   : p.R <= 32 ? expand(k_expand_wide<F16, 2, YK, HV>) \
+   : p.R <= 64 ? expand(k_expand_wide<F16, 4, YK, HV>) \
+               : expand(k_expand_wide<F16, 8, YK, 1>))
   // (64 columns a warp where there are columns for every warp of a block then)
-  if (!p.vec) return wide ? MOE_EXPAND(64, 2, 1) : MOE_EXPAND(8, 2, 1);
-  if (!wide) return p.y_dtype == kF32 ? MOE_EXPAND(8, 0, 1) : MOE_EXPAND(8, 1, 1);
-  if (p.N < 512) return p.y_dtype == kF32 ? MOE_EXPAND(64, 0, 1) : MOE_EXPAND(64, 1, 1);
-  return p.y_dtype == kF32 ? MOE_EXPAND(64, 0, 2) : MOE_EXPAND(64, 1, 2);
+  if (!p.vec) return wide ? MOE_EXPAND_WIDE(2, 1) : MOE_EXPAND(2);
+  if (!wide) return p.y_dtype == kF32 ? MOE_EXPAND(0) : MOE_EXPAND(1);
+  if (p.N < 512) return p.y_dtype == kF32 ? MOE_EXPAND_WIDE(0, 1) : MOE_EXPAND_WIDE(1, 1);
+  return p.y_dtype == kF32 ? MOE_EXPAND_WIDE(0, 2) : MOE_EXPAND_WIDE(1, 2);
+#undef MOE_EXPAND_WIDE
 #undef MOE_EXPAND
 }
 

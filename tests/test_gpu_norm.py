@@ -224,3 +224,44 @@ def test_residual_alone():
                                             None, None, None, out.data_ptr(), None)
         torch.cuda.synchronize()
         assert rc == fb.OK and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("H", [517, 1026, 2883, 4095])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_many_rows_of_any_alignment(H, dtype):
+    """More rows than four an SM whose starts go through every offset from a four-element boundary."""
+    gen = torch.Generator(device="cuda").manual_seed(H)
+    T = 640
+    wide = lambda pad, dt=dtype: rand(gen, T, H + pad, dtype=dt)  # noqa: E731
+    # every tensor at an offset of its own; then one of them in fp32, each in turn, and rows on the boundary
+    for odd, pads in ((None, (1, 2, 3, 4, 5)), (0, (3, 1, 1, 2, 7)), (1, (5, 3, 2, 1, 2)), (2, (2, 5, 7, 3, 1)),
+                      (3, (1, 1, 1, 1, 1)), (None, tuple([-H % 4] * 5))):
+        dts = [F32 if odd == i else dtype for i in range(4)]  # res, y, gate, normed
+        res, y, gate = (wide(p, d)[:, p // 2:p // 2 + H] for p, d in zip(pads, dts[:3]))
+        w_post, w_pre = rand(gen, H + 1, dtype=BF16)[1:], rand(gen, H)
+        want_r, dr, want_n, dn = reference(res, y, True, w_post, gate, True, 0.9, 0.5, w_pre, 1.0, 1e-6)
+        ro, no = wide(pads[3], dts[0]), wide(pads[4], dts[3])
+        kr, kn = ro.clone(), no.clone()
+        fb.moe_ffn_norm_residual(res, y, True, w_post, gate, fb.GATE_SIGMOID, 0.9, 0.5, w_pre, 1.0,
+                                 res_out=ro[:, pads[3] - 1:][:, :H] if pads[3] else ro, normed=no[:, :H])
+        torch.cuda.synchronize()
+        first = max(pads[3] - 1, 0)
+        got = ro[:, first:first + H].double()
+        assert float(((got - want_r).abs() - dr - half_step(want_r.abs() + dr, dts[0])).max()) <= 0
+        assert float(((no[:, :H].double() - want_n).abs() - dn - half_step(want_n.abs() + dn, dts[3])).max()) <= 0
+        assert torch.equal(ro[:, :first], kr[:, :first]) and torch.equal(ro[:, first + H:], kr[:, first + H:])
+        assert torch.equal(no[:, H:], kn[:, H:])
+    # in place, without a norm between the reads and the writes
+    check(rand(gen, T, H, dtype=dtype), rand(gen, T, H, dtype=dtype), alpha=0.5, in_place=True)
+    check(rand(gen, T, H, dtype=dtype), alpha=0.5, in_place=True, norm_dtype=dtype)
+
+
+def test_a_row_ends_where_the_neighbour_holds_nan():
+    """What lies before, behind and between the rows enters no row."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for T, H in ((3, 61), (640, 517), (640, 2883)):
+        for shift in range(4):
+            hold = torch.full((T, H + 7), math.nan, dtype=BF16, device="cuda")
+            hold[:, shift + 1:shift + 1 + H] = rand(gen, T, H, dtype=BF16)
+            res = hold[:, shift + 1:shift + 1 + H]
+            check(res, res.clone(), post_norm=True, gate=res.clone(), w_pre=rand(gen, H))
