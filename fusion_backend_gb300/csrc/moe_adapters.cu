@@ -10,9 +10,11 @@ namespace {
 constexpr int kOrderTokens = 32;  // tokens a block of k_order ranks, eight threads a token
 
 // Places of the window's tokens in the order (adapter, token): a token's place
-// is the number of tokens before it.  Eight threads a token, each against an
-// eighth of the window.  marks[place]: the tokens of the tile that starts
-// there, 0 where none does (a run of one adapter is cut every P.tile tokens).
+// is the number of tokens before it, and its place in its adapter's run that less
+// the number of tokens of lower adapters: two counts (with a third, of the
+// run, 58.1 against 55.5 us for the whole call at 8192 tokens; the tile finds its
+// end itself).  Eight threads a token, each against an eighth of the window.  marks[place]: whether a tile
+// starts there (a run of one adapter is cut every P.tile tokens).
 __global__ void __launch_bounds__(8 * kOrderTokens) k_order(const __grid_constant__ AdapterParams P) {
   __shared__ __align__(16) int s_a[kWindow];
   const int tid = threadIdx.x, part = tid & 7;
@@ -24,29 +26,30 @@ __global__ void __launch_bounds__(8 * kOrderTokens) k_order(const __grid_constan
   for (int j = tid; j < kWindow; j += 8 * kOrderTokens) s_a[j] = j < n ? adapter_of(P, t0 + j) : 0x7FFFFFFF;
   __syncthreads();
   const int a = s_a[i];
-  int before = 0, same_before = 0, same = 0;
+  int place = 0, start = 0;
 #pragma unroll 4
   for (int j0 = 4 * part; j0 < n; j0 += 32) {
     const int4 v = *reinterpret_cast<const int4*>(s_a + j0);
     const int o[4] = {v.x, v.y, v.z, v.w};
+    const int below = a + (j0 + 4 <= i);  // tokens before this one count with the same adapter too
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      before += o[e] < a;
-      same += o[e] == a;
-      same_before += o[e] == a && j0 + e < i;
+      place += o[e] < below;
+      start += o[e] < a;
     }
   }
-  before += same_before;
+  // those of the token's own four
+  if (part == (i >> 2 & 7))
+    for (int j = i & ~3; j < i; ++j) place += s_a[j] == a;
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    same += __shfl_xor_sync(0xffffffffu, same, o);
-    same_before += __shfl_xor_sync(0xffffffffu, same_before, o);
+    place += __shfl_xor_sync(0xffffffffu, place, o);
+    start += __shfl_xor_sync(0xffffffffu, start, o);
   }
   if (part == 0 && i < n) {
-    P.order[t0 + before] = t0 + i;
-    P.adapter_at[t0 + before] = a;
-    P.marks[t0 + before] = static_cast<uint8_t>(same_before % P.tile ? 0 : min(P.tile, same - same_before));
+    P.order[t0 + place] = t0 + i;
+    P.adapter_at[t0 + place] = a;
+    P.marks[t0 + place] = (place - start) % P.tile == 0;
   }
 }
 

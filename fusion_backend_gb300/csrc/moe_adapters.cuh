@@ -116,10 +116,24 @@ MOE_DEV bool find_tile(const AdapterParams& P, int* list, int& a, int& n) {
       }
       const uint32_t who = __ballot_sync(0xffffffffu, n > 0);
       if (who) {
-        n = __shfl_sync(0xffffffffu, n, __ffs(who) - 1);
         place = __shfl_sync(0xffffffffu, place, __ffs(who) - 1);
-        for (int i = lane; i < n; i += 32) list[i] = P.order[place + i];
-        a = P.adapter_at[place];
+        // the tokens from there on that have the same adapter
+        const int left = min(TILE, t0 + len - place);
+        int at[(TILE + 31) / 32], id[(TILE + 31) / 32];
+#pragma unroll
+        for (int i = 0; i < (TILE + 31) / 32; ++i) {
+          const int j = place + min(lane + 32 * i, left - 1);
+          at[i] = P.order[j];
+          id[i] = P.adapter_at[j];
+        }
+        a = __shfl_sync(0xffffffffu, id[0], 0);
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < (TILE + 31) / 32; ++i) {
+          const bool mine = lane + 32 * i < left && id[i] == a;
+          if (mine) list[lane + 32 * i] = at[i];
+          n += __popc(__ballot_sync(0xffffffffu, mine));
+        }
       }
     } else {
       const int t = blockIdx.x;
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 // goes through the tile's tokens, G times sixteen at a time, whose y is asked for a
 // round ahead; nothing is waited for between warps.  HV = 2 reads a token's v once
 // for 64 columns (71 -> 67 us there, the columns as the rows).  What is left are the
-// loads that are waited for at 16 warps an SM: the call runs at 2.9 TB/s; the first
+// loads that are waited for at 16 warps an SM: the call runs at 3.1 TB/s; the first
 // form, a thread an output element, took 1171 us.  Two blocks an SM, and as many
 // columns a block as give every SM two: with one 79, with four 67 against 63 us.
 template <bool F16, int ST, int YK, int HV>
