@@ -522,10 +522,11 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 // 8192 tokens, 2048 x 2048, rank 32, fp32 y.)  B stays in registers while the warp
 // goes through the tile's tokens, G times sixteen at a time, whose y is asked for a
 // round ahead; nothing is waited for between warps.  HV = 2 reads a token's v once
-// for 64 columns (71 -> 67 us there, the columns as the rows).  What is left are the
-// loads that are waited for at 16 warps an SM: the call runs at 3.1 TB/s; the first
-// form, a thread an output element, took 1171 us.  Two blocks an SM, and as many
-// columns a block as give every SM two: with one 79, with four 67 against 63 us.
+// for 64 columns (55.8 us for the call as it is now, with HV = 1 56.9).  What is
+// left are the loads that are waited for at 16 warps an SM: the call runs at 3.0
+// TB/s; the first form, a thread an output element, took 1171 us.  Two blocks an SM,
+// and as many columns a block as give every SM two: 55.8 us, with one 67, with four
+// 61.
 template <bool F16, int ST, int YK, int HV>
 __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand_wide(const __grid_constant__ AdapterParams P) {
   constexpr int TILE = 64, G = YK == 2 || HV == 2 ? 1 : 2, NP = 2 * HV;
