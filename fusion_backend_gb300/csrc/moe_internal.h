@@ -7,6 +7,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
+
 namespace moe {
 
 constexpr int kDecodeMaxT = 8;    // tokens of the decode path
@@ -251,6 +254,30 @@ constexpr int kLaunchesPerExecute = 1;
 // out[i] = a[i] + b[i], i < n: the join add(ffn_moe_out, ffn_shexp) of the
 // two-stream form (moe_rows.cu).
 cudaError_t launch_join_add(const float* a, const float* b, float* out, int n, cudaStream_t stream);
+
+// The dynamic shared memory that launches of one kernel may ask for (a static of
+// its launcher).  The limit is the kernel's, not a call's: calls of other sizes on
+// other host threads launch the same kernel, so it is only ever raised.
+class SmemLimit {
+ public:
+  cudaError_t raise(const void* kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevs) return cudaErrorInvalidDevice;
+    if (bytes_[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(mu_);
+    if (bytes_[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) bytes_[dev].store(bytes, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevs = 64;
+  std::atomic<int> bytes_[kDevs] = {};
+  std::mutex mu_;
+};
 
 // ---- operators around the layer (moe_route.cu, moe_norm.cu,
 // moe_adapters.cu); fields as in the public argument blocks.

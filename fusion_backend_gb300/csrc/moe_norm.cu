@@ -553,7 +553,8 @@ cudaError_t launch_rows_of(const NormParams& p, cudaStream_t stream) {
   const int threads = (p.H + 128 * NV - 1) / (128 * NV) * 32;
   const int smem = rows_smem(p, NV);
   auto* const kern = k_norm_rows<NV, THREADS, R32, Y32, N32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), smem);
   int per_sm = 0;
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
   if (e != cudaSuccess) return e;

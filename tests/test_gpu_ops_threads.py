@@ -1,0 +1,84 @@
+"""Calls of different sizes from several host threads, each on a stream of its own: what one call needs of a kernel
+that both use is not taken back by the other, and a thread that has made no CUDA call before can make these."""
+
+import ctypes
+import shutil
+import subprocess
+import threading
+
+import pytest
+
+import fusion_backend_gb300 as fb
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+HAMMER = r"""
+typedef int (*call_t)(void*, void*, void*, void*, void*, void*, void*, void*, void*);
+extern "C" long hammer(call_t f, void** a, long rounds) {
+  long bad = 0;
+  for (long i = 0; i < rounds; ++i) bad += f(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]) != 0;
+  return bad;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def hammer(tmp_path_factory):
+    """A loop over a C entry of nine words, outside the interpreter and its lock."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("hammer")
+    (d / "hammer.cc").write_text(HAMMER)
+    subprocess.run([cxx, "-O2", "-shared", "-fPIC", str(d / "hammer.cc"), "-o", str(d / "libhammer.so")], check=True)
+    f = ctypes.CDLL(str(d / "libhammer.so")).hammer
+    f.restype, f.argtypes = ctypes.c_long, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_long]
+    return f
+
+
+def words(args):
+    return (ctypes.c_void_p * 9)(*[ctypes.addressof(a) if isinstance(a, ctypes.Structure) else a for a in args])
+
+
+def run_together(hammer, entry, calls, rounds):
+    """Every call (its nine arguments without the stream, which comes second) on a thread and stream of its own,
+    `rounds` times; how many of each were refused."""
+    start, bad = threading.Barrier(len(calls)), [None] * len(calls)
+    streams = [torch.cuda.Stream() for _ in calls]
+
+    def loop(i):
+        a = words((calls[i][0], streams[i].cuda_stream, *calls[i][1:]))
+        start.wait()
+        bad[i] = hammer(ctypes.cast(entry, ctypes.c_void_p), a, rounds)
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad
+
+
+def test_norms_of_different_widths(hammer):
+    """Rows of 2048 columns with a gate of every element take six times the shared memory of 516 without one."""
+    T = 700
+    calls, wants, outs, keep = [], [], [], []
+    for H, wide in ((2048, True), (516, False), (2048, True), (516, False)):
+        g = torch.Generator(device="cuda").manual_seed(H)
+        res, y, gate = (torch.randn(T, H, generator=g, device="cuda") for _ in range(3))
+        kw = dict(gate=gate) if wide else {}
+        wants.append(fb.moe_ffn_norm_residual(res.clone(), y, True, norm_dtype=torch.float32, **kw)[1])
+        out, normed = torch.empty_like(res), torch.empty(T, H, device="cuda")
+        outs.append(normed)
+        block = fb.NormArgs(T, H, 0, 0, 0, 0, 0, 0, 1, 2, 0, 1.0, 1.0, 0.0, 1e-6, H, H, H, H, H)
+        ptr = lambda t: t.data_ptr()  # noqa: E731
+        calls.append((block, ptr(res), ptr(y), None, ptr(gate) if wide else None, None, ptr(out),
+                      ptr(normed)))
+        keep += [res, y, gate, out]
+    torch.cuda.synchronize()
+    assert run_together(hammer, fb.lib().moe_ffn_norm_residual, calls, 20000) == [0] * 4
+    for got, want in zip(outs, wants):
+        assert torch.equal(got, want)
