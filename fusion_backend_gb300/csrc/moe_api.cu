@@ -49,6 +49,16 @@ struct DeviceInfo {
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
+thread_local char t_last_cuda_error[256];
+
+// MOE_FFN_OK, or MOE_FFN_ERR_CUDA with the runtime's text kept for
+// moe_ffn_last_cuda_error.
+int cuda_status(cudaError_t err) {
+  if (err == cudaSuccess) return MOE_FFN_OK;
+  snprintf(t_last_cuda_error, sizeof(t_last_cuda_error), "%s: %s", cudaGetErrorName(err), cudaGetErrorString(err));
+  return MOE_FFN_ERR_CUDA;
+}
+
 // Device properties are read once per device, lazily on the first execute
 // (prepare never touches the device).
 int device_info(DeviceInfo** out) {
@@ -68,18 +78,18 @@ int device_info(DeviceInfo** out) {
     }
   }
   if (d.major != 10 || d.minor != 3) return MOE_FFN_ERR_DEVICE;
+  // The driver's encoding of tensor maps wants a current context, which a host
+  // thread that has only asked for properties does not have: asking for one of
+  // the context's limits gives it the device's (and leaves one that the caller
+  // has set).
+  thread_local int bound = -1;
+  if (bound != dev) {
+    size_t limit = 0;
+    if (const cudaError_t e = cudaDeviceGetLimit(&limit, cudaLimitStackSize); e != cudaSuccess) return cuda_status(e);
+    bound = dev;
+  }
   *out = &d;
   return MOE_FFN_OK;
-}
-
-thread_local char t_last_cuda_error[256];
-
-// MOE_FFN_OK, or MOE_FFN_ERR_CUDA with the runtime's text kept for
-// moe_ffn_last_cuda_error.
-int cuda_status(cudaError_t err) {
-  if (err == cudaSuccess) return MOE_FFN_OK;
-  snprintf(t_last_cuda_error, sizeof(t_last_cuda_error), "%s: %s", cudaGetErrorName(err), cudaGetErrorString(err));
-  return MOE_FFN_ERR_CUDA;
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -82,3 +82,28 @@ def test_norms_of_different_widths(hammer):
     assert run_together(hammer, fb.lib().moe_ffn_norm_residual, calls, 20000) == [0] * 4
     for got, want in zip(outs, wants):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_layer_on_a_thread_of_its_own(T):
+    """The first CUDA calls that a host thread makes are the layer's (tensor maps on both paths)."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    bf = lambda *s: (torch.randn(*s, generator=g, device="cuda") * 0.02).bfloat16()  # noqa: E731
+    H, E, k, I, Is = 2048, 8, 2, 128, 128
+    x, router, gate, expert, shared = bf(T, H) * 50, bf(E, H), bf(H), bf(E, 3, I, H), bf(3, Is, H)
+    m = fb.MoeFFN(fb.Shapes(T, H, E, k, I, Is), fb.ACT_BF16, fb.W_BF16)
+    ids = torch.arange(T * k, device="cuda", dtype=torch.int32).view(T, k) % E
+    w = torch.rand(T, k, generator=g, device="cuda")
+    want = m(x, router, expert, shared, gate), m.routed(x, ids, w, expert, shared, gate)
+    ptr = lambda *ts: [t.data_ptr() for t in ts]  # noqa: E731
+    stream = torch.cuda.Stream()
+    for f, args, expect in ((fb.lib().moe_ffn_execute, (x, router, expert, shared, gate), want[0]),
+                            (fb.lib().moe_ffn_execute_routed, (x, ids, w, expert, shared, gate), want[1])):
+        out, rc = torch.zeros_like(expect), []
+        torch.cuda.synchronize()
+        a = (m.plan, stream.cuda_stream, m.workspace.data_ptr(), m.workspace_bytes, *ptr(*args, out))
+        t = threading.Thread(target=lambda: rc.append(f(*a)))  # noqa: B023
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert rc == [fb.OK] and torch.equal(out, expect)
