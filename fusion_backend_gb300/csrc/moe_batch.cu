@@ -478,7 +478,8 @@ static cudaError_t launch_pdl(Kern kern, dim3 grid, int threads, size_t smem, cu
 static cudaError_t launch_router(const BatchParams& p, cudaStream_t stream) {
   const size_t route_smem = (size_t)kRouteTokens * p.H * 2;
   if (route_smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_route_b, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)route_smem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k_route_b), (int)route_smem);
     if (e != cudaSuccess) return e;
   }
   cudaError_t err = launch_pdl(k_route_b,

@@ -15,10 +15,13 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 HAMMER = r"""
-typedef int (*call_t)(void*, void*, void*, void*, void*, void*, void*, void*, void*);
-extern "C" long hammer(call_t f, void** a, long rounds) {
+typedef int (*call9_t)(void*, void*, void*, void*, void*, void*, void*, void*, void*);
+typedef int (*call10_t)(void*, void*, void*, void*, void*, void*, void*, void*, void*, void*);
+extern "C" long hammer(void* f, void** a, long words, long rounds) {
   long bad = 0;
-  for (long i = 0; i < rounds; ++i) bad += f(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]) != 0;
+  for (long i = 0; i < rounds; ++i)
+    bad += (words == 9 ? ((call9_t)f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8])
+                       : ((call10_t)f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9])) != 0;
   return bad;
 }
 """
@@ -26,7 +29,7 @@ extern "C" long hammer(call_t f, void** a, long rounds) {
 
 @pytest.fixture(scope="module")
 def hammer(tmp_path_factory):
-    """A loop over a C entry of nine words, outside the interpreter and its lock."""
+    """A loop over a C entry of nine or ten words, outside the interpreter and its lock."""
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         pytest.skip("no C++ compiler")
@@ -34,16 +37,16 @@ def hammer(tmp_path_factory):
     (d / "hammer.cc").write_text(HAMMER)
     subprocess.run([cxx, "-O2", "-shared", "-fPIC", str(d / "hammer.cc"), "-o", str(d / "libhammer.so")], check=True)
     f = ctypes.CDLL(str(d / "libhammer.so")).hammer
-    f.restype, f.argtypes = ctypes.c_long, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_long]
+    f.restype, f.argtypes = ctypes.c_long, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_long, ctypes.c_long]
     return f
 
 
 def words(args):
-    return (ctypes.c_void_p * 9)(*[ctypes.addressof(a) if isinstance(a, ctypes.Structure) else a for a in args])
+    return (ctypes.c_void_p * len(args))(*[ctypes.addressof(a) if isinstance(a, ctypes.Structure) else a for a in args])
 
 
 def run_together(hammer, entry, calls, rounds):
-    """Every call (its nine arguments without the stream, which comes second) on a thread and stream of its own,
+    """Every call (its arguments without the stream, which comes second) on a thread and stream of its own,
     `rounds` times; how many of each were refused."""
     start, bad = threading.Barrier(len(calls)), [None] * len(calls)
     streams = [torch.cuda.Stream() for _ in calls]
@@ -51,7 +54,7 @@ def run_together(hammer, entry, calls, rounds):
     def loop(i):
         a = words((calls[i][0], streams[i].cuda_stream, *calls[i][1:]))
         start.wait()
-        bad[i] = hammer(ctypes.cast(entry, ctypes.c_void_p), a, rounds)
+        bad[i] = hammer(ctypes.cast(entry, ctypes.c_void_p), a, len(a), rounds)
 
     threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(calls))]
     for t in threads:
@@ -80,6 +83,26 @@ def test_norms_of_different_widths(hammer):
         keep += [res, y, gate, out]
     torch.cuda.synchronize()
     assert run_together(hammer, fb.lib().moe_ffn_norm_residual, calls, 20000) == [0] * 4
+    for got, want in zip(outs, wants):
+        assert torch.equal(got, want)
+
+
+def test_batched_layers_of_different_widths(hammer):
+    """The router of a batched plan keeps eight rows of x in shared memory: 64 KB at H = 4096, 52 at 3328."""
+    calls, wants, outs, keep = [], [], [], []
+    for H in (4096, 3328, 4096, 3328):
+        T, E, k, I, Is = 16, 4, 2, 128, 128
+        g = torch.Generator(device="cuda").manual_seed(H)
+        bf = lambda *s: (torch.randn(*s, generator=g, device="cuda") * 0.02).bfloat16()  # noqa: E731,B023
+        x, router, gate, expert, shared = bf(T, H) * 50, bf(E, H), bf(H), bf(E, 3, I, H), bf(3, Is, H)
+        m = fb.MoeFFN(fb.Shapes(T, H, E, k, I, Is), fb.ACT_BF16, fb.W_BF16)
+        wants.append(m(x, router, expert, shared, gate))
+        outs.append(torch.zeros_like(wants[-1]))
+        calls.append((m.plan, m.workspace.data_ptr(), m.workspace_bytes,
+                      *(t.data_ptr() for t in (x, router, expert, shared, gate, outs[-1]))))
+        keep += [x, router, gate, expert, shared, m]
+    torch.cuda.synchronize()
+    assert run_together(hammer, fb.lib().moe_ffn_execute, calls, 3000) == [0] * 4
     for got, want in zip(outs, wants):
         assert torch.equal(got, want)
 
