@@ -11,6 +11,7 @@ not a GB300 (sm_103), the calls raise.
 from __future__ import annotations
 
 import ctypes
+import numbers
 import os
 from dataclasses import dataclass
 
@@ -313,10 +314,16 @@ def _sig(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
+def _by_value(v) -> bool:
+    return v is None or isinstance(v, (numbers.Number, tuple)) or type(v).__name__ == "dtype"
+
+
 def _remember(key, block):
-    if len(_blocks) >= 4096:
-        _blocks.clear()
-    _blocks[key] = block
+    # a number held in a tensor is found by the tensor's identity and may change: its block serves one call
+    if all(_by_value(v) for v in key):
+        if len(_blocks) >= 4096:
+            _blocks.clear()
+        _blocks[key] = block
     return block
 
 
