@@ -89,6 +89,14 @@ def _fields(i32="", f32="", i64=""):
             for n in names.split()]
 
 
+def _block(cls, *values):
+    """An argument block; ctypes would take a number past a field's 32 bits modulo 2^32."""
+    for (name, kind), v in zip(cls._fields_, values):
+        if kind is ctypes.c_int32 and not -(2**31) <= v < 2**31:
+            raise ValueError(f"{name}: {v} does not fit in 32 bits")
+    return cls(*values)
+
+
 class RouteArgs(ctypes.Structure):
     _fields_ = _fields("T E top_k score groups top_groups group_score renorm dtype", "scale", "row_stride")
 
@@ -390,8 +398,8 @@ def _route_block(logits, top_k, bias, score, groups, top_groups, group_score, re
 
     _require(logits.dim() == 2, "logits: expected [T, E]")
     T, E = logits.shape
-    a = RouteArgs(T, E, top_k, score, groups, top_groups, group_score, bool(renorm), _code(logits, "logits"), scale,
-                  _matrix(logits, T, E, "logits"))
+    a = _block(RouteArgs, T, E, top_k, score, groups, top_groups, group_score, bool(renorm), _code(logits, "logits"),
+               scale, _matrix(logits, T, E, "logits"))
     if bias is not None:
         _whole(bias, (E,), torch.float32, "bias")
     if ids is not None:
@@ -455,8 +463,8 @@ def _norm_block(res, y, post_norm, w_post, gate, gate_act, alpha, beta, w_pre, w
         _require(norm_dtype in _CODES, f"norm_dtype: {norm_dtype} is not supported")
         nd = _CODES[norm_dtype]
     _on_device(res, res=res, y=y, w_post=w_post, gate=gate, w_pre=w_pre, res_out=res_out, normed=normed)
-    return NormArgs(T, H, yd, rd, nd, gd, codes[0], codes[1], bool(post_norm), layout, gate_act == GATE_SIGMOID, alpha,
-                    beta, w_offset, eps, ys, rs, os_, ns, gs)
+    return _block(NormArgs, T, H, yd, rd, nd, gd, codes[0], codes[1], bool(post_norm), layout,
+                  gate_act == GATE_SIGMOID, alpha, beta, w_offset, eps, ys, rs, os_, ns, gs)
 
 
 def moe_ffn_norm_residual(res, y=None, post_norm: bool = False, w_post=None, gate=None, gate_act: int = GATE_LINEAR,
@@ -489,7 +497,7 @@ def moe_ffn_norm_residual(res, y=None, post_norm: bool = False, w_post=None, gat
 def moe_ffn_adapters_workspace(T: int, K: int, N: int, R: int) -> int:
     """Workspace bytes of moe_ffn_add_adapters for T tokens, widths K and N and a pool of rank R."""
     n = ctypes.c_size_t()
-    a = AdaptersArgs(T, K, N, R, 0, ACT_BF16, ACT_F32, (K + 7) // 8 * 8, N, N)
+    a = _block(AdaptersArgs, T, K, N, R, 0, ACT_BF16, ACT_F32, (K + 7) // 8 * 8, N, N)
     _check(lib().moe_ffn_adapters_workspace(a, ctypes.byref(n)), "moe_ffn_adapters_workspace")
     return max(n.value, 256)
 
@@ -512,8 +520,8 @@ def _adapters_block(y, x, adapter_ids, a, b, ranks, scales, out, workspace):
     if scales is not None:
         _whole(scales, (n,), torch.float32, "scales")
     xs = _matrix(x, T, K, "x")
-    args = AdaptersArgs(T, K, N, R, n, xd, _code(y, "y"), xs if T > 1 else (K + 7) // 8 * 8, _matrix(y, T, N, "y"),
-                        _matrix(out, T, N, "out"))
+    args = _block(AdaptersArgs, T, K, N, R, n, xd, _code(y, "y"), xs if T > 1 else (K + 7) // 8 * 8,
+                  _matrix(y, T, N, "y"), _matrix(out, T, N, "out"))
     _on_device(x, x=x, y=y, adapter_ids=adapter_ids, a=a, b=b, ranks=ranks, scales=scales, out=out,
                workspace=workspace)
     if workspace is not None:

@@ -52,3 +52,23 @@ def test_numbers_of_equal_value_find_one_block(rec):
     for alpha in (0.5, 0.5, 1.0, 0.5):
         fb.moe_ffn_norm_residual(r, alpha=alpha, normed=n, stream=1)
     assert [c[1][0].alpha for c in rec.calls] == [0.5, 0.5, 1.0, 0.5] and len(fb._blocks) == 2
+
+
+def test_numbers_past_32_bits_are_refused(rec):
+    lg = torch.zeros(1, 8)
+    with pytest.raises(ValueError, match="32 bits"):
+        fb.moe_ffn_route(lg.expand(2**32 + 1, 8), 2, stream=1)
+    with pytest.raises(ValueError, match="32 bits"):
+        fb.moe_ffn_route(lg, 2**32 + 2, stream=1)
+    with pytest.raises(ValueError, match="32 bits"):
+        fb.moe_ffn_norm_residual(torch.zeros(1, 1).expand(2**32 + 1, 1), stream=1)
+    bf = torch.bfloat16
+    a, b = torch.zeros(1, 1, 8, dtype=bf), torch.zeros(1, 1, 1, dtype=bf)
+    T = 2**32 + 1
+    x, y = torch.zeros(1, 8, dtype=bf).expand(T, 8), torch.zeros(1, 1).expand(T, 1)
+    ids = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fb.moe_ffn_add_adapters(y, x, ids.expand(T), a, b, stream=1)
+    with pytest.raises(ValueError, match="32 bits"):
+        fb.moe_ffn_adapters_workspace(2**32 + 1, 64, 64, 8)
+    assert rec.calls == []
