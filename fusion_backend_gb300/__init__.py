@@ -588,17 +588,48 @@ class MoeFFN:
                               topk_ids, None, stream)
         return x_res
 
-    def routed(self, x, ids, weights, expert_w, shexp_w=None, shexp_gate_w=None, out=None, stream=None):
-        """The layer for a given routing (moe_ffn_execute_routed); returns out."""
-        s = self.shapes
-        key = (3, s.T, s.H, s.top_k, _sig(ids), _sig(weights), x.get_device())
-        if key not in _blocks:
-            import torch
+    def _check_routed(self, x, ids, weights, expert_w, shexp_w, shexp_gate_w, out):
+        import torch
 
-            _whole(ids, (s.T, s.top_k), torch.int32, "ids")
-            _whole(weights, (s.T, s.top_k), torch.float32, "weights")
-            _on_device(x, x=x, ids=ids, weights=weights)
-            _remember(key, True)
+        s = self.shapes
+        _whole(ids, (s.T, s.top_k), torch.int32, "ids")
+        _whole(weights, (s.T, s.top_k), torch.float32, "weights")
+        _on_device(x, x=x, ids=ids, weights=weights)
+        x_types = (torch.float32,) if self.act == ACT_F32 else (torch.bfloat16, torch.int16, torch.uint16)
+        for t, types, name in ((x, x_types, "x"), (out, (torch.float32,), "out")):
+            if t is None or isinstance(t, int):
+                continue
+            if t.dtype not in types or t.numel() != s.T * s.H or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous tensor of shape {(s.T, s.H)} and {types[0]}, got "
+                                 f"{tuple(t.shape)}, {t.dtype}")
+        row = {W_BF16: 2 * s.H, W_Q4B32: s.H // 2 + s.H // 16, W_I8: s.H + 16}[self.wfmt]
+        gate = shexp_gate_w if shexp_w is not None else None  # ignored without a shared expert
+        need = {"expert_w": (expert_w, 3 * s.E * s.I * row, self.wfmt), "shexp_w": (shexp_w, 3 * s.Is * row, self.wfmt),
+                "shexp_gate_w": (gate, 2 * s.H, W_BF16)}
+        for name, (t, nbytes, wfmt) in need.items():
+            if t is None or isinstance(t, int):
+                continue
+            if t.dtype.is_floating_point and (wfmt != W_BF16 or t.dtype != torch.bfloat16):
+                raise ValueError(f"{name}: dtype {t.dtype} is not that of the plan's weights")
+            if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+                raise ValueError(f"{name}: expected a contiguous tensor of {nbytes} bytes, got "
+                                 f"{t.numel() * t.element_size()}")
+        rest = dict(expert_w=expert_w, shexp_w=shexp_w, shexp_gate_w=gate, out=out)
+        _on_device(x, **{n: t for n, t in rest.items() if not isinstance(t, int)})
+
+    def routed(self, x, ids, weights, expert_w, shexp_w=None, shexp_gate_w=None, out=None, stream=None):
+        """The layer for a given routing (moe_ffn_execute_routed); returns out.  x [T, H] of the plan's type and out
+        fp32 [T, H], both contiguous; the weights contiguous, of bf16 or as bytes, at least as many as the plan's."""
+        s = self.shapes
+        key = tuple(0 if isinstance(t, int) else _sig(t)
+                    for t in (x, ids, weights, expert_w, shexp_w, shexp_gate_w, out))
+        # signatures that this layer has checked
+        passed = self.__dict__.setdefault("_routed", set())
+        if key not in passed:
+            self._check_routed(x, ids, weights, expert_w, shexp_w, shexp_gate_w, out)
+            if len(passed) >= 4096:
+                passed.clear()
+            passed.add(key)
         if out is None:
             import torch
 
