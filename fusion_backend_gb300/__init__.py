@@ -336,11 +336,13 @@ def _remember(key, block):
 
 
 def _raw_stream(stream, t) -> int | None:
-    if stream is None:
-        import torch
+    """The call's stream; the library launches on the current device, so t has to be there."""
+    import torch
 
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return _stream(stream)
+    device, current = t.get_device(), torch._C._cuda_getDevice()
+    if device != current:
+        raise ValueError(f"the call's tensors are on cuda:{device}, the current device is cuda:{current}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _code(t, name: str, allowed=(ACT_F32, ACT_BF16, ACT_F16)) -> int:

@@ -30,6 +30,8 @@ def rec(monkeypatch):
     monkeypatch.setattr(fb, "_lib", r)
     monkeypatch.setattr(fb, "_blocks", {})
     monkeypatch.setattr(fb, "_on_device", lambda first, **tensors: None)
+    # tensors on the CPU pass for tensors on the current device
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
     return r
 
 
@@ -164,3 +166,24 @@ def test_routed_takes_plans_apart(rec):
     with pytest.raises(ValueError, match="x"):
         f32.routed(**tensors(small), stream=1)
     f32.routed(**tensors(f32), stream=1)
+
+
+def test_tensors_of_another_device_than_the_current_one(rec, monkeypatch):
+    m = layer()
+    t = tensors(m)
+    bf = torch.bfloat16
+    a, b = torch.zeros(1, 8, 256, dtype=bf), torch.zeros(1, 256, 8, dtype=bf)
+    calls = [
+        lambda: m.routed(**t, stream=1),
+        lambda: fb.moe_ffn_route(t["out"], 2, ids=t["ids"], weights=t["weights"], stream=1),
+        lambda: fb.moe_ffn_norm_residual(t["out"], normed=t["out"].clone(), stream=1),
+        lambda: fb.moe_ffn_add_adapters(t["out"], t["x"], t["ids"][:, 0].clone(), a, b,
+                                        workspace=torch.zeros(1 << 20, dtype=torch.uint8), stream=1),
+    ]
+    for c in calls:
+        c()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for c in calls:  # (also where the same call has passed before)
+        with pytest.raises(ValueError, match="current"):
+            c()
+    assert len(rec.calls) == len(calls)
