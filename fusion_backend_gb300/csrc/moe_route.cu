@@ -48,6 +48,7 @@ MOE_DEV F warp_sum(F v) {
   return v;
 }
 MOE_DEV float key_float(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+MOE_DEV float reduce_max(float v) { return key_float(__reduce_max_sync(kAll, float_order_key(v))); }
 // NaN: masked; +inf: the largest number
 MOE_DEV float clean(float v) { return v != v ? -INFINITY : fminf(v, kFltMax); }
 
@@ -55,16 +56,24 @@ struct Owned {
   int lpg, grp, n, e0;  // lanes a group, the lane's group, its experts e0 .. e0 + n - 1
 };
 
-// From the lane's two largest c the value of its group, on each of the group's
-// lanes; -inf where the group has nothing left.
+// The lane's two largest c to those of its group, on each of the group's lanes.
 template <typename F>
-MOE_DEV F group_value(F a1, F a2, int lpg, bool top2) {
+MOE_DEV void group_best(F& a1, F& a2, int lpg) {
   for (int o = lpg >> 1; o; o >>= 1) {
     const F b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
     a2 = fmax(fmax(a2, b2), fmin(a1, b1));
     a1 = fmax(a1, b1);
   }
+}
+// The group's value; -inf where it has nothing left.
+template <typename F>
+MOE_DEV F value_of(F a1, F a2, bool top2) {
   return top2 && a2 != -INFINITY ? a1 + a2 : a1;
+}
+template <typename F>
+MOE_DEV F group_value(F a1, F a2, int lpg, bool top2) {
+  group_best(a1, a2, lpg);
+  return value_of(a1, a2, top2);
 }
 
 // The lane's group's place among the G group values (equal: the lower group).
@@ -250,21 +259,14 @@ MOE_DEV void choose_rounds(const RouteParams& P, float (&c)[EPL], const Owned& o
   unsure = biased && n == 32 && next != -INFINITY && cut - next <= slack(cut);
 }
 
-// Values of the groups on the two sides of the cut in fp64: true if the one left
-// out comes before the other.  c: fp32, off by less than `err`; only a group's
-// experts that may be among its two largest are formed again.
+// Values of the two groups at the cut in fp64: true if the one left out comes
+// before the other.  Only experts that may be among their group's best (c in fp32
+// from `least` on) are formed again.
 template <int EPL>
-MOE_DEV bool border_swaps(const RouteParams& P, uint32_t t, const Owned& o, const float (&c)[EPL], float a1, float a2,
-                          float err, int in_grp, int out_grp) {
+MOE_DEV bool border_swaps(const RouteParams& P, uint32_t t, const Owned& o, const float (&c)[EPL], float least,
+                          int in_grp, int out_grp) {
   double m = 0.0, z = 1.0;
   if (!P.sigmoid) exact_sum(P, t, o, m, z);
-  // the group's two largest in fp32, on its lanes
-  for (int d = o.lpg >> 1; d; d >>= 1) {
-    const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
-    a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
-    a1 = fmaxf(a1, b1);
-  }
-  const float least = (P.top2 && a2 != -INFINITY ? a2 : a1) - err;
   uint32_t todo = 0u;  // of the lane's experts
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
@@ -388,23 +390,28 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
         a2 = fmaxf(a2, fminf(a1, c[i]));
         a1 = fmaxf(a1, c[i]);
       }
-      const float val = group_value(a1, a2, o.lpg, P.top2);
+      group_best(a1, a2, o.lpg);
+      const float val = value_of(a1, a2, P.top2);
       int rank = group_rank(val, P.G, o);
       if (scored) {
-        // the last group kept, the first one left out and their neighbours
-        auto at_rank = [&](int k, int& g) {
-          const uint32_t who = __ballot_sync(kAll, o.grp < P.G && rank == k);
-          g = (__ffs(who) - 1) >> P.lpg_log;
-          return who ? __shfl_sync(kAll, val, __ffs(who) - 1) : k < 0 ? INFINITY : -INFINITY;
-        };
-        int gi, go, g;
-        const float vi = at_rank(P.top_groups - 1, gi), vo = at_rank(P.top_groups, go);
-        const float err = 2.f * slack(vi);
-        if (vo != -INFINITY && vi - vo <= err) {
-          const float before = at_rank(P.top_groups - 2, g), after = at_rank(P.top_groups + 1, g);
-          if (EPL > 32 || before - vo <= err || vi - after <= err)
-            unsure = true;  // more than two
-          else if (border_swaps<EPL>(P, t, o, c, a1, a2, err, gi, go))
+        // A group's value is off by less than a band of its own: that of the
+        // scores, and the roundings of each c and of their sum, which go by the
+        // magnitudes of the two c (the sum may cancel).  Groups kept and left out
+        // whose bands meet are told apart in fp64, one of each by themselves.
+        const bool two = P.top2 && a2 != -INFINITY;
+        const float w = two ? a2 : a1, mag = fabsf(a1) + (two ? fabsf(a2) : 0.f);
+        const float band = smax * (P.sigmoid ? 0x1p-20f : kSoft) * (P.top2 ? 1.f : 0.5f) + mag * 0x1p-22f + 0x1p-120f;
+        const bool live = o.grp < P.G && val != -INFINITY, in = rank < P.top_groups;
+        const float lo = -reduce_max(live && in ? band - val : -INFINITY);
+        const float hi = reduce_max(live && !in ? val + band : -INFINITY);
+        if (lo <= hi) {
+          const bool one = (lane & (o.lpg - 1)) == 0;  // of the group's lanes
+          const uint32_t kept = __ballot_sync(kAll, one && live && in && val - band <= hi);
+          const uint32_t left = __ballot_sync(kAll, one && live && !in && val + band >= lo);
+          const int gi = (__ffs(kept) - 1) >> P.lpg_log, go = (__ffs(left) - 1) >> P.lpg_log;
+          if (EPL > 32 || __popc(kept) != 1 || __popc(left) != 1)
+            unsure = true;
+          else if (border_swaps<EPL>(P, t, o, c, w - 2.f * slack(w), gi, go))
             rank = o.grp == gi ? P.top_groups : o.grp == go ? P.top_groups - 1 : rank;
         }
       }

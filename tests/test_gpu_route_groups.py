@@ -1,0 +1,47 @@
+"""Groups of experts whose values lie near each other, against the 64-bit definition."""
+
+import pytest
+
+import fusion_backend_gb300 as fb
+from test_gpu_route import check
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+SCORES = [fb.SCORE_SOFTMAX, fb.SCORE_SIGMOID]
+
+
+def pinned(E, groups, size, g):
+    """A bias of +size for one expert of every group and of -size for the others (size: one number, or one a group)."""
+    gs = E // groups
+    size = torch.as_tensor(size, dtype=torch.float32).expand(groups)
+    bias = -size.repeat_interleave(gs)
+    at = torch.arange(groups) * gs + torch.randint(0, gs, (groups,), generator=g)
+    bias[at] = size
+    return bias.cuda()
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("size", [4.0, 16.0, 1000.0, 1e4])
+@pytest.mark.parametrize("steps", [1, 8, 64])
+def test_sums_of_two_that_cancel(score, size, steps):
+    """c of a group's two best is about +size and -size: their sum keeps what fp32 rounds away of each."""
+    g = torch.Generator().manual_seed(int(size) + steps)
+    E, groups = 64, 8
+    # scores of an expert in a group differ by some `steps` of fp32 at `size`
+    spread = steps * size * 2.0**-23 * (E if score == fb.SCORE_SOFTMAX else 4)
+    lg = (torch.randn(200, E, generator=g) * min(spread, 2.0)).cuda()
+    check(lg, 6, pinned(E, groups, size, g), score, groups, 4, fb.GROUP_TOP2)
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_groups_of_very_different_magnitudes(score):
+    """A group far from the cut in the order of the rounded sums, and within its own rounding of it."""
+    g = torch.Generator().manual_seed(3)
+    size = [0.0, 1e5, 3.0, 1e6, 0.0, 1e3, 30.0, 1e6]
+    for E in (64, 256):
+        lg = (torch.randn(200, E, generator=g) * 0.3).cuda()
+        for top_groups in (1, 3, 5, 7):
+            check(lg, 5, pinned(E, 8, size, g), score, 8, top_groups, fb.GROUP_TOP2)
+            check(lg, 5, pinned(E, 8, size, g), score, 8, top_groups, fb.GROUP_MAX)
