@@ -316,6 +316,7 @@ def moe_ffn_execute_routed(plan, workspace, x, ids, weights, expert_w, shexp_w, 
 
 _CODES: dict = {}
 _blocks: dict = {}
+_torch_c = None
 
 
 def _sig(t):
@@ -337,12 +338,15 @@ def _remember(key, block):
 
 def _raw_stream(stream, t) -> int | None:
     """The call's stream; the library launches on the current device, so t has to be there."""
-    import torch
+    global _torch_c
+    if _torch_c is None:
+        import torch
 
-    device, current = t.get_device(), torch._C._cuda_getDevice()
+        _torch_c = torch._C
+    device, current = t.get_device(), _torch_c._cuda_getDevice()
     if device != current:
         raise ValueError(f"the call's tensors are on cuda:{device}, the current device is cuda:{current}")
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    return _torch_c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _code(t, name: str, allowed=(ACT_F32, ACT_BF16, ACT_F16)) -> int:
