@@ -391,7 +391,9 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
         a1 = fmaxf(a1, c[i]);
       }
       group_best(a1, a2, o.lpg);
-      const float val = value_of(a1, a2, P.top2);
+      // (half of a sum of two: it stays within fp32's range, and a group held back
+      // by the lowest number comes before one that has nothing left)
+      const float half = P.top2 ? 0.5f : 1.f, val = value_of(half * a1, half * a2, P.top2);
       int rank = group_rank(val, P.G, o);
       if (scored) {
         // A group's value is off by less than a band of its own: that of the
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
         // magnitudes of the two c (the sum may cancel).  Groups kept and left out
         // whose bands meet are told apart in fp64, one of each by themselves.
         const bool two = P.top2 && a2 != -INFINITY;
-        const float w = two ? a2 : a1, mag = fabsf(a1) + (two ? fabsf(a2) : 0.f);
-        const float band = smax * (P.sigmoid ? 0x1p-20f : kSoft) * (P.top2 ? 1.f : 0.5f) + mag * 0x1p-22f + 0x1p-120f;
+        const float w = two ? a2 : a1, mag = half * fabsf(a1) + (two ? half * fabsf(a2) : 0.f);
+        const float band = smax * (P.sigmoid ? 0x1p-21f : 0.5f * kSoft) + mag * 0x1p-22f + 0x1p-120f;
         const bool live = o.grp < P.G && val != -INFINITY, in = rank < P.top_groups;
         const float lo = -reduce_max(live && in ? band - val : -INFINITY);
         const float hi = reduce_max(live && !in ? val + band : -INFINITY);

@@ -1,4 +1,6 @@
-"""Groups of experts whose values lie near each other, against the 64-bit definition."""
+"""Groups of experts whose values lie near each other or past fp32's range, against the 64-bit definition."""
+
+import math
 
 import pytest
 
@@ -45,3 +47,22 @@ def test_groups_of_very_different_magnitudes(score):
         for top_groups in (1, 3, 5, 7):
             check(lg, 5, pinned(E, 8, size, g), score, 8, top_groups, fb.GROUP_TOP2)
             check(lg, 5, pinned(E, 8, size, g), score, 8, top_groups, fb.GROUP_MAX)
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_sums_of_two_past_fp32(score):
+    g = torch.Generator().manual_seed(5)
+    lg = torch.randn(20, 32, generator=g).cuda()
+    low = torch.finfo(torch.float32).min
+    # a masked group before groups held back by the type's lowest value: they come before it all the same
+    bias = torch.zeros(32, device="cuda")
+    bias[:8] = -math.inf
+    bias[8:16] = low
+    bias[24:] = low
+    got, _ = check(lg, 12, bias, score, 4, 2, fb.GROUP_TOP2)
+    assert (got >= 8).all()
+    # sums above the largest number keep their order
+    for values in ([3.0e38, 3.4e38, 3.2e38, 1.0], [1.0, 3.4e38, math.inf, 3.0e38], [-3.0e38, -3.4e38, -2.0e38, -math.inf]):
+        bias = torch.tensor(values, device="cuda").repeat_interleave(8)
+        for top_groups in (1, 2, 3):
+            check(lg, 5, bias, score, 4, top_groups, fb.GROUP_TOP2)
