@@ -11,13 +11,14 @@
 // those before them; a round a choice (warp maximum, its lane's next best)
 // took twice the instructions, and the kernel is bound by those for many tokens.
 // Without a bias the value is the logit itself, since the scores rise with it:
-// the choice is then exact, and scores are formed only where the groups or the
-// weights need them.  With a bias it is c = s + b in fp32, which is off by less
-// than `slack` (below); where two neighbours in the order of the choice lie closer
-// than that, the candidates' c are formed and ordered in fp64, one a lane, and
-// where the groups on the two sides of the cut do (or more candidates than
-// lanes), the warp makes the whole choice again in fp64.  The first is one token
-// in some hundreds on logits of a spread of two, the second one in thousands;
+// the choice is then exact (but for groups whose scores fp64 may not tell apart),
+// and scores are formed only where sums of two or the weights need them.  With a
+// bias it is c = s + b in fp32, which is off by less than `slack` (below); where
+// two neighbours in the order of the choice lie closer than that, the candidates'
+// c are formed and ordered in fp64, one a lane, and where groups across the cut
+// do, the two are, or (more than two, or more candidates than lanes) the warp
+// makes the whole choice again in fp64.  The first is one token in some hundreds
+// on logits of a spread of two, the last one in thousands;
 // fp64 for every token, the first form of this kernel, ran 176 us on 4096 tokens
 // x 256 experts and 537 us on 16381 x 200, now 11 and 26 us (the GPU's fp64 rate is a small share
 // of its fp32 rate, and one such token is all that an SM waits for).
@@ -395,7 +396,25 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
       // by the lowest number comes before one that has nothing left)
       const float half = P.top2 ? 0.5f : 1.f, val = value_of(half * a1, half * a2, P.top2);
       int rank = group_rank(val, P.G, o);
-      if (scored) {
+      const bool live = o.grp < P.G && val != -INFINITY, in = rank < P.top_groups;
+      if (!scored) {
+        // By the largest logit, which orders the groups as their scores do but
+        // where these are equal in fp64 and the logits are not: both 1 or 0, or
+        // the logits closer than a score's rounding.  Equal values go to the lower
+        // group, so where the cut may lie between two such the choice is made in
+        // fp64.  Elsewhere scores differ by 2^-24 e^-16 and more (softmax, and the
+        // sigmoid of negative logits: by 2^-24 of the score).
+        auto at_rank = [&](int k) {
+          return __shfl_sync(kAll, val, __ffs(__ballot_sync(kAll, o.grp < P.G && rank == k)) - 1);
+        };
+        const float lo = at_rank(P.top_groups - 1), hi = at_rank(P.top_groups);
+        if (hi != -INFINITY) {
+          // the lane's group against the nearest one across the cut
+          const float x = in ? val : lo, y = in ? hi : val;
+          const bool equal = P.sigmoid ? x <= -690.f || y >= 15.f : val - lo >= 690.f;
+          unsure = __any_sync(kAll, live && x > y && (x - y <= 0x1p-24f || equal));
+        }
+      } else {
         // A group's value is off by less than a band of its own: that of the
         // scores, and the roundings of each c and of their sum, which go by the
         // magnitudes of the two c (the sum may cancel).  Groups kept and left out
@@ -403,7 +422,6 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
         const bool two = P.top2 && a2 != -INFINITY;
         const float w = two ? a2 : a1, mag = half * fabsf(a1) + (two ? half * fabsf(a2) : 0.f);
         const float band = smax * (P.sigmoid ? 0x1p-21f : 0.5f * kSoft) + mag * 0x1p-22f + 0x1p-120f;
-        const bool live = o.grp < P.G && val != -INFINITY, in = rank < P.top_groups;
         const float lo = -reduce_max(live && in ? band - val : -INFINITY);
         const float hi = reduce_max(live && !in ? val + band : -INFINITY);
         if (lo <= hi) {

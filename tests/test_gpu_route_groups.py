@@ -1,7 +1,9 @@
-"""Groups of experts whose values lie near each other or past fp32's range, against the 64-bit definition."""
+"""Groups of experts whose values lie near each other or past fp32's range, or are equal in 64 bits although their
+logits are not, against the 64-bit definition."""
 
 import math
 
+import numpy as np
 import pytest
 
 import fusion_backend_gb300 as fb
@@ -66,3 +68,43 @@ def test_sums_of_two_past_fp32(score):
         bias = torch.tensor(values, device="cuda").repeat_interleave(8)
         for top_groups in (1, 2, 3):
             check(lg, 5, bias, score, 4, top_groups, fb.GROUP_TOP2)
+
+
+def both(lg, k, score, groups, top_groups):
+    """Without a bias and with one of zeros: one definition, one answer."""
+    a, _ = check(lg, k, None, score, groups, top_groups, fb.GROUP_MAX)
+    b, _ = check(lg, k, torch.zeros(lg.shape[1], device="cuda"), score, groups, top_groups, fb.GROUP_MAX)
+    assert np.array_equal(a, b)
+
+
+def test_group_maxima_of_equal_scores():
+    """Logits that differ where the scores in 64 bits do not: equal values of groups go to the lower group."""
+    lg = torch.full((6, 16), -1.0, device="cuda")
+    lg[0, 3], lg[0, 9] = 40.0, 45.0           # sigmoid: 1 in 64 bits
+    lg[1] = -800.0
+    lg[1, 14] = -760.0                        # 0 in 64 bits
+    lg[2, :] = -5.0
+    lg[2, 6], lg[2, 11] = 0.0, 1e-20          # 1/2 (softmax: the same power)
+    lg[3, 0::4] = torch.tensor([50.0, 60.0, 55.0, 40.0], device="cuda")
+    lg[4] = -2000.0
+    lg[4, 12], lg[4, 4], lg[4, 8] = 0.0, -900.0, -800.0   # softmax: 1, 0, 0
+    lg[5, :] = -math.inf
+    lg[5, 9], lg[5, 2] = 90.0, 80.0
+    for score in SCORES:
+        for groups, top_groups in ((2, 1), (4, 1), (4, 2), (4, 3), (8, 3)):
+            both(lg, 2, score, groups, top_groups)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_group_maxima_of_many_rows(score, dtype):
+    """Rows drawn from few values, so that groups are equal in the logit, in the score alone, or in neither."""
+    g = torch.Generator().manual_seed(7)
+    values = torch.tensor([-3000.0, -800.0, -60.0, -2.0, 0.0, 1e-20, 0.5, 3.0, 14.0, 18.0, 40.0, 48.0])
+    for E, groups in ((32, 8), (96, 4), (128, 32)):
+        # mostly low values, so that the maxima of groups spread over all of them
+        at = (torch.rand(300, E, generator=g) ** (E / groups / 2) * len(values)).long().clamp(max=len(values) - 1)
+        for top_groups in (1, groups // 2, groups - 1):
+            both(values[at].to(dtype).cuda(), 2, score, groups, top_groups)
+    lg = torch.randn(500, 64, generator=g).to(dtype).cuda()
+    both(lg, 4, score, 8, 3)
