@@ -319,12 +319,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_shrink_wide(const __grid_consta
 // for a 16-bit result, 22 and more for an fp32 one.
 template <bool F16, int YK>
 constexpr int kTerms = F16 || YK == 1 ? 2 : 3;
+constexpr float kLow = 0x1p11f;  // fp16: the second number's factor
 
-// v of a tile as the B operand of the second product, TERMS numbers an element,
-// the largest first.  fp16: of v scaled by a power of two to a largest element
-// near 1, since v may pass fp16's range.  s_scale: what takes the token's product
-// back, times the adapter's scale.  256 / TILE threads a token; ends with a block
-// barrier.
+// v of a tile as an operand of the second product, TERMS numbers an element, the
+// largest first.  fp16: of v scaled by a power of two to a largest element of 2^14
+// and more, since v may pass fp16's range, and the second number times 2^11: both
+// are then normal fp16 numbers down to 2^-28 of the largest element (unscaled, the
+// second one lost bits from 2^-3 of it on).  s_scale: what takes the token's
+// product back, times the adapter's scale.  256 / TILE threads a token; ends with a
+// block barrier.
 template <bool F16, int TILE, int TERMS>
 MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int rank, int pitch, uint32_t* vs,
                      float* s_scale) {
@@ -348,11 +351,11 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
     for (int r = part; r < rank; r += TPT) top = fmaxf(top, fabsf(v_of(r)));
 #pragma unroll
     for (int o = TPT >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^e with 2^e <= top < 2^(e + 1), kept within the normal numbers on both sides
-    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+    // 2^(e - 127) <= top < 2^(e - 126), the factors kept within the normal numbers
+    const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
     if (top > 0.f && top < INFINITY) {
-      up = __uint_as_float(e << 23);
-      down = __uint_as_float((254u - e) << 23);
+      up = __uint_as_float((e - 14u) << 23);
+      down = __uint_as_float((268u - e) << 23);
     }
   }
   uint16_t* const out = reinterpret_cast<uint16_t*>(vs) + tok * pitch;
@@ -366,6 +369,7 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
       unpack2(F16 ? kF16 : kBf16, h, xh, none);
       out[i * TILE * pitch + r] = static_cast<uint16_t>(h);
       x = fabsf(xh) < INFINITY ? x - xh : 0.f;  // exact
+      if (F16) x *= kLow;
     }
   }
   if (part == 0) s_scale[tok] = up * (P.scales ? P.scales[a] : 1.f);
@@ -461,23 +465,29 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
     // (v of tokens past the last is 0, their y is the last's; they are not stored)
     float d[2][4];
     if (rank > 0) {
+      // the smallest term first; fp16: its whole product, then the other's
 #pragma unroll
-      for (int s = 0; s < ST; ++s) {
-        if (16 * s >= rank) break;
-        uint2 t[TERMS];
+      for (int pass = F16 ? TERMS - 1 : 0; pass >= 0; --pass) {
+        if (F16 && pass < TERMS - 1) {
 #pragma unroll
-        for (int i = 0; i < TERMS; ++i) t[i] = *reinterpret_cast<const uint2*>(v0 + i * TILE * pitch + 16 * s);
-        // the smallest term first
+          for (int c = 0; c < 4; ++c) d[0][c] *= 1.f / kLow, d[1][c] *= 1.f / kLow;
+        }
 #pragma unroll
-        for (int i = TERMS - 1; i >= 0; --i)
+        for (int s = 0; s < ST; ++s) {
+          if (16 * s >= rank) break;
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint2 b0 = bv[s][2 * m], b1 = bv[s][2 * m + 1];
-            if (s == 0 && i == TERMS - 1)
-              mma16816<F16, true>(d[m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
-            else
-              mma16816<F16>(d[m], b0.x, b1.x, b0.y, b1.y, t[i].x, t[i].y);
+          for (int i = F16 ? pass : TERMS - 1; i >= pass; --i) {
+            const uint2 t = *reinterpret_cast<const uint2*>(v0 + i * TILE * pitch + 16 * s);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const uint2 b0 = bv[s][2 * m], b1 = bv[s][2 * m + 1];
+              if (s == 0 && i == TERMS - 1)
+                mma16816<F16, true>(d[m], b0.x, b1.x, b0.y, b1.y, t.x, t.y);
+              else
+                mma16816<F16>(d[m], b0.x, b1.x, b0.y, b1.y, t.x, t.y);
+            }
           }
+        }
       }
     } else {
 #pragma unroll
@@ -620,23 +630,34 @@ __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 
     for (int j0 = 0; 16 * j0 < n; j0 += G) {
       float d[G][2 * NP][4];
       if (rank > 0) {
+        // the smallest term first; fp16: its whole product, then the other's
 #pragma unroll
-        for (int s = 0; s < ST; ++s) {
-          if (16 * s >= rank) break;
+        for (int pass = F16 ? TERMS - 1 : 0; pass >= 0; --pass) {
+          if (F16 && pass < TERMS - 1) {
 #pragma unroll
-          for (int u = 0; u < G; ++u) {
-            const uint16_t* const v = v0 + 16 * (j0 + u) * pitch + 16 * s;
-            // the smallest term first
+            for (int u = 0; u < G; ++u)
 #pragma unroll
-            for (int i = TERMS - 1; i >= 0; --i) {
-              const uint2 t0 = *reinterpret_cast<const uint2*>(v + i * TILE * pitch);
-              const uint2 t1 = *reinterpret_cast<const uint2*>(v + (i * TILE + 8) * pitch);
+              for (int c = 0; c < 2 * NP; ++c)
 #pragma unroll
-              for (int c = 0; c < 2 * NP; ++c) {
-                if (s == 0 && i == TERMS - 1)
-                  mma16816<F16, true>(d[u][c], t0.x, t1.x, t0.y, t1.y, bv[s][c].x, bv[s][c].y);
-                else
-                  mma16816<F16>(d[u][c], t0.x, t1.x, t0.y, t1.y, bv[s][c].x, bv[s][c].y);
+                for (int e = 0; e < 4; ++e) d[u][c][e] *= 1.f / kLow;
+          }
+#pragma unroll
+          for (int s = 0; s < ST; ++s) {
+            if (16 * s >= rank) break;
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+              const uint16_t* const v = v0 + 16 * (j0 + u) * pitch + 16 * s;
+#pragma unroll
+              for (int i = F16 ? pass : TERMS - 1; i >= pass; --i) {
+                const uint2 t0 = *reinterpret_cast<const uint2*>(v + i * TILE * pitch);
+                const uint2 t1 = *reinterpret_cast<const uint2*>(v + (i * TILE + 8) * pitch);
+#pragma unroll
+                for (int c = 0; c < 2 * NP; ++c) {
+                  if (s == 0 && i == TERMS - 1)
+                    mma16816<F16, true>(d[u][c], t0.x, t1.x, t0.y, t1.y, bv[s][c].x, bv[s][c].y);
+                  else
+                    mma16816<F16>(d[u][c], t0.x, t1.x, t0.y, t1.y, bv[s][c].x, bv[s][c].y);
+                }
               }
             }
           }

@@ -378,7 +378,9 @@ int moe_ffn_norm_residual(const moe_ffn_norm_args* args, moe_ffn_stream_t stream
  * of A_a and columns of B_a count (clamped to 0..R; what the others hold does
  * not matter).  scales fp32 [n_adapters] or NULL (1).
  * Sums are in fp32.  A_a x_t enters the second product as the sum of numbers of
- * x's type: 22 bits of it and more where y is fp32, else 16 bits and more.
+ * x's type: 22 bits of each element and more where y is fp32, else 16 bits and
+ * more (fp16: of elements from 2^-28 of the token's largest on; smaller ones are
+ * off by at most 2^-50 of it).
  * T <= 16777216, 1 <= R <= 128, 8 <= K <= 65536 a multiple of 8, 1 <= N <=
  * 1048576.
  * The workspace (256-byte aligned, scratch) holds what
