@@ -348,12 +348,15 @@ MOE_DEV void stage_v(const AdapterParams& P, const int* list, int a, int n, int 
   float up = 1.f, down = 1.f;
   if (F16) {
     float top = 0.f;
-    for (int r = part; r < rank; r += TPT) top = fmaxf(top, fabsf(v_of(r)));
+    for (int r = part; r < rank; r += TPT) {
+      const float x = fabsf(v_of(r));
+      if (x < INFINITY) top = fmaxf(top, x);  // what is finite stays so beside what is not
+    }
 #pragma unroll
     for (int o = TPT >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // 2^(e - 127) <= top < 2^(e - 126), the factors kept within the normal numbers
     const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
-    if (top > 0.f && top < INFINITY) {
+    if (top > 0.f) {
       up = __uint_as_float((e - 14u) << 23);
       down = __uint_as_float((268u - e) << 23);
     }

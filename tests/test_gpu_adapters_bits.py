@@ -76,3 +76,19 @@ def test_bits_at_any_size_of_the_whole(scale):
                                   out=torch.empty_like(y))
     torch.cuda.synchronize()
     assert float(((got.double() / scale - want).abs() - want.abs() * 2.0**-22).max()) <= 0
+
+
+@pytest.mark.parametrize("T,N", [(3, 64), (3, 37), (70, 600)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_finite_beside_infinite(T, N, dtype):
+    """An element of A_a x past fp16's range, finite, beside an infinite one: the infinity alone decides."""
+    x, a, b = torch.ones(T, 64), torch.zeros(1, 4, 64), torch.zeros(1, N, 4)
+    x[:, 1] = 32768.0
+    a[0, 0, 0], a[0, 1, 1] = float("inf"), 8.0
+    sign = torch.where(torch.arange(N) % 2 == 0, 1.0, -1.0)
+    b[0, :, 0], b[0, :, 1] = sign, -sign
+    y = torch.zeros(T, N, device="cuda")
+    got = fb.moe_ffn_add_adapters(y, x.to(dtype).cuda(), torch.zeros(T, dtype=torch.int32, device="cuda"),
+                                  a.to(dtype).cuda(), b.to(dtype).cuda(), out=torch.empty_like(y))
+    torch.cuda.synchronize()
+    assert torch.equal(got, (sign * float("inf")).cuda().expand(T, N))
