@@ -492,9 +492,9 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
           }
         }
       }
-    } else {
+    } else {  // (the scale is 0 then: -0 leaves y as it is, a zero's sign too)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) d[0][c] = d[1][c] = 0.f;
+      for (int c = 0; c < 4; ++c) d[0][c] = d[1][c] = -0.f;
     }
     const float2 scale = *reinterpret_cast<const float2*>(s_scale + 2 * q);
 #pragma unroll
@@ -665,11 +665,11 @@ __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 
             }
           }
         }
-      } else {
+      } else {  // (the scale is 0 then: -0 leaves y as it is, a zero's sign too)
 #pragma unroll
         for (int u = 0; u < G; ++u)
 #pragma unroll
-          for (int c = 0; c < 2 * NP; ++c) d[u][c][0] = d[u][c][1] = d[u][c][2] = d[u][c][3] = 0.f;
+          for (int c = 0; c < 2 * NP; ++c) d[u][c][0] = d[u][c][1] = d[u][c][2] = d[u][c][3] = -0.f;
       }
       float y[G][2][NP][4];
 #pragma unroll

@@ -92,3 +92,22 @@ def test_finite_beside_infinite(T, N, dtype):
                                   a.to(dtype).cuda(), b.to(dtype).cuda(), out=torch.empty_like(y))
     torch.cuda.synchronize()
     assert torch.equal(got, (sign * float("inf")).cuda().expand(T, N))
+
+
+@pytest.mark.parametrize("T", [3, 64, 300])
+@pytest.mark.parametrize("N", [64, 37, 600])
+@pytest.mark.parametrize("ydtype", [F32, BF16, F16])
+def test_minus_zero_without_an_adapter(T, N, ydtype):
+    """A token without an adapter, or with one of rank 0, keeps y bit for bit."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    y = torch.where(torch.rand(T, N, generator=g, device="cuda") < 0.5, -0.0, 0.0).to(ydtype)
+    bits = torch.int32 if ydtype == F32 else torch.int16
+    x = torch.randn(T, 64, generator=g, device="cuda").to(BF16)
+    a, b = torch.randn(3, 8, 64, device="cuda").to(BF16), torch.randn(3, N, 8, device="cuda").to(BF16)
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    ids[1::2] = 2
+    ranks = torch.tensor([8, 8, 0], dtype=torch.int32, device="cuda")
+    for got in (fb.moe_ffn_add_adapters(y, x, ids, a, b, ranks, out=torch.ones_like(y)),
+                fb.moe_ffn_add_adapters(y.clone(), x, ids, a, b, ranks)):
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(bits), y.view(bits))
