@@ -534,7 +534,7 @@ bool rows4(const void* p, int dtype, long long stride, int T) {
 template <int NV, int THREADS>
 cudaError_t launch(const NormParams& p, bool vec, cudaStream_t stream) {
   constexpr bool WARP = THREADS == kWarpRows;
-  const dim3 grid(WARP ? (p.T + kRowsPerBlock - 1) / kRowsPerBlock : p.T);
+  const dim3 grid(WARP ? 1 + (p.T - 1) / kRowsPerBlock : p.T);
   const int threads = WARP ? THREADS : (p.H + 256 * NV - 1) / (256 * NV) * 32;
   return vec ? launch_behind(k_norm<NV, true, THREADS>, grid, threads, 0, stream, p)
              : launch_behind(k_norm<NV, false, THREADS>, grid, threads, 0, stream, p);

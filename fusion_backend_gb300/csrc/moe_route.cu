@@ -555,7 +555,7 @@ cudaError_t launch_route(RouteParams p, cudaStream_t stream) {
     if (p.vec) p.per = per4;
   }
   // a warp goes through several tokens where there are more than run at once
-  const int blocks = (p.T + kWarps - 1) / kWarps, most = 6 * p.sms;
+  const int blocks = 1 + (p.T - 1) / kWarps, most = 6 * p.sms;
   const dim3 grid(blocks < most ? blocks : most);
   const int threads = 32 * kWarps;
   if (p.per <= 2) return launch_behind(k_route<2>, grid, threads, 0, stream, p);
