@@ -396,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
   int a, n;
   if (!find_tile<TILE>(P, list, a, n)) {
     pdl_wait();
-    pdl_launch_dependents();
     return;
   }
   // (rows past the tile's last are its last: their loads need no test)
@@ -460,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
     }
     if (!staged) {
       pdl_wait();
-      pdl_launch_dependents();
       if (rank == 0 && P.out == P.y) return;
       if (rank > 0) stage_v<F16, TILE, TERMS>(P, list, a, n, rank, pitch, vs, s_scale);
       staged = true;
@@ -552,7 +550,6 @@ __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 
   int a, n;
   if (!find_tile<TILE>(P, list, a, n)) {
     pdl_wait();
-    pdl_launch_dependents();
     return;
   }
   // (rows past the tile's last are its last: their loads need no test)
@@ -624,7 +621,6 @@ __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 
     ask(0);
     if (!staged) {
       pdl_wait();
-      pdl_launch_dependents();
       if (rank == 0 && P.out == P.y) return;
       if (rank > 0) stage_v<F16, TILE, TERMS>(P, list, a, n, rank, pitch, vs, s_scale);
       staged = true;

@@ -87,9 +87,15 @@ MOE_DEV void elem_store4(void* p, int dtype, size_t i, const float* v) {
 
 // Launch behind the previous kernel of the stream with programmatic stream
 // serialisation.  The kernels launched this way wait (griddepcontrol.wait)
-// before they touch what an earlier kernel may write, and let the next one
-// start only behind that wait: so a kernel that starts early knows every
-// kernel before its predecessor to be complete.
+// before they touch what an earlier kernel may write.  The routing, the order and
+// the first product of the adapters let the next kernel start right behind that
+// wait: so a kernel that starts early knows every kernel before its predecessor to
+// be complete.  The norms and the adapters' second product do not: the caller may
+// take what they write for weights, which the layer's row kernel reads ahead of
+// its own wait.  (That costs a norm and the layer behind it 1.1 us of 25.5 at one
+// token; calls of many rows got faster, without the next call's blocks waiting on
+// their SMs: 24.5 -> 23.7 us for 4096 x 2048 fp32 rows, 55.5 -> 48.5 for adapters of
+// 8192 tokens.)
 template <typename Kern, typename Params>
 inline cudaError_t launch_behind(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                  const Params& p) {

@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
   cols.threads = WARP ? 32 : blockDim.x;
   cols.H = P.H;
   pdl_wait();
-  pdl_launch_dependents();
   if (WARP && t >= (size_t)P.T) return;  // (whole warps)
 
   uint4 rw[NV][2], yw[NV][2], gw[2], pw[2], nw[2];
@@ -397,7 +396,6 @@ __global__ void __launch_bounds__(THREADS) k_norm_rows(const __grid_constant__ N
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   pdl_wait();
-  pdl_launch_dependents();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + s * gridDim.x, s);
   // what a column of y and of r' is multiplied by in every row: w_offset +

@@ -746,8 +746,9 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
 
   // Router row of this block (row cta of router_w; row E is the shared-gate
   // vector), read before the wait: the weights are never written by a kernel
-  // that lets this one start early (only this kernel does, and it writes no
-  // weights; any other predecessor has completed before this kernel starts).
+  // that lets this one start early (this kernel, the batched path's, the routing
+  // and the adapters' first kernels do, and write no weights; any other
+  // predecessor has completed before this kernel starts).
   constexpr int kRC = kMaxH / (kRowThreads * 8);  // 8-element chunks of a row per thread
   uint4 wr[kRC];
   // the shared-expert part needs only the shared-gate row (block 0); with a
