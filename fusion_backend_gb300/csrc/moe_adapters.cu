@@ -11,10 +11,11 @@ constexpr int kOrderTokens = 32;  // tokens a block of k_order ranks, eight thre
 
 // Places of the window's tokens in the order (adapter, token): a token's place
 // is the number of tokens before it, and its place in its adapter's run that less
-// the number of tokens of lower adapters: two counts (with a third, of the
-// run, 58.1 against 55.5 us for the whole call at 8192 tokens; the tile finds its
-// end itself).  Eight threads a token, each against an eighth of the window.  marks[place]: whether a tile
-// starts there (a run of one adapter is cut every P.tile tokens).
+// the number of tokens of lower adapters: two counts (a third, of the run,
+// took 2.6 us more of the whole call at 8192 tokens; the tile finds its end
+// itself).  Eight threads a token, each against an eighth of the window.
+// marks[place]: whether a tile starts there (a run of one adapter is cut every
+// P.tile tokens).
 __global__ void __launch_bounds__(8 * kOrderTokens) k_order(const __grid_constant__ AdapterParams P) {
   __shared__ __align__(16) int s_a[kWindow];
   const int tid = threadIdx.x, part = tid & 7;

@@ -529,15 +529,14 @@ __global__ void __launch_bounds__(kThreads, ST <= 4 ? 2 : 1) k_expand(const __gr
 // + 3 of tokens g and g + 8, its three neighbours with the twelve behind them, so
 // that a quarter of a warp has 64 bytes each of two rows of y in one access.  (With
 // the columns as the rows it has 32 bytes each of four, and the L1's cycles, four
-// times an access's bytes, bound the kernel: 63 against 58 us for the whole call at
-// 8192 tokens, 2048 x 2048, rank 32, fp32 y.)  B stays in registers while the warp
+// times an access's bytes, bound the kernel: 5 us more for the whole call at 8192
+// tokens, 2048 x 2048, rank 32, fp32 y.)  B stays in registers while the warp
 // goes through the tile's tokens, G times sixteen at a time, whose y is asked for a
 // round ahead; nothing is waited for between warps.  HV = 2 reads a token's v once
-// for 64 columns (55.8 us for the call as it is now, with HV = 1 56.9).  What is
-// left are the loads that are waited for at 16 warps an SM: the call runs at 3.0
-// TB/s; the first form, a thread an output element, took 1171 us.  Two blocks an SM,
-// and as many columns a block as give every SM two: 55.8 us, with one 67, with four
-// 61.
+// for 64 columns (48.4 us for the call, with HV = 1 50.2).  What is left are the
+// loads that are waited for at 16 warps an SM: the call runs at 3.5 TB/s; the first
+// form, a thread an output element, took 1171 us.  Two blocks an SM, and as many
+// columns a block as give every SM two: 48.4 us, with one 63, with four 54.
 template <bool F16, int ST, int YK, int HV>
 __global__ void __launch_bounds__(kThreads, ST <= 2 || (ST <= 4 && HV == 1) ? 2 : 1) k_expand_wide(const __grid_constant__ AdapterParams P) {
   constexpr int TILE = 64, G = YK == 2 || HV == 2 ? 1 : 2, NP = 2 * HV;

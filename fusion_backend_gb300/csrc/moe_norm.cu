@@ -12,9 +12,10 @@
 //                with the next two on their way into shared memory
 //                (asynchronous copies) while it works on one; the weights stay
 //                in registers.  With a block a row the loads of a block stand
-//                still while it reduces and stores.  4096 x 2048 fp32 rows: 24.4 us
-//                (4.8 TB/s) against 25.0 with a block a row, where the copy
-//                rate allows 17.
+//                still while it reduces and stores.  4096 x 2048 rows, against a
+//                block a row: fp32 with a gate a column 23.6 us (5.0 TB/s, where
+//                the copy rate allows 17) and 23.7, bf16 17.1 and 18.6; 2048 x 8192
+//                bf16 29.6 and 48.4; 1024 x 2048 bf16 9.0 and 6.7.
 // The first form (256 threads and three passes over the row, element by
 // element) ran 57 us there.
 #include <cuda_runtime.h>

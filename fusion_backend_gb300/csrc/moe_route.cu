@@ -20,8 +20,9 @@
 // makes the whole choice again in fp64.  The first is one token in some hundreds
 // on logits of a spread of two, the last one in thousands;
 // fp64 for every token, the first form of this kernel, ran 176 us on 4096 tokens
-// x 256 experts and 537 us on 16381 x 200, now 11 and 26 us (the GPU's fp64 rate is a small share
-// of its fp32 rate, and one such token is all that an SM waits for).
+// x 256 experts and 537 us on 16381 x 200, now 11.5 and 26 us (the GPU's fp64 rate
+// is a small share of its fp32 rate, and one such token is all that an SM waits
+// for).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
