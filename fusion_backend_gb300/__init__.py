@@ -327,6 +327,11 @@ def _by_value(v) -> bool:
     return v is None or isinstance(v, (numbers.Number, tuple)) or type(v).__name__ == "dtype"
 
 
+def _flat(t):
+    """The signature of a tensor whose shape does not matter (an address has none)."""
+    return None if t is None else 0 if isinstance(t, int) else (t.is_contiguous(), t.nbytes, t.dtype, t.get_device())
+
+
 def _remember(key, block):
     # a number held in a tensor is found by the tensor's identity and may change: its block serves one call
     if all(_by_value(v) for v in key):
@@ -627,10 +632,11 @@ class MoeFFN:
         """The layer for a given routing (moe_ffn_execute_routed); returns out.  x [T, H] of the plan's type and out
         fp32 [T, H], both contiguous; the weights contiguous, of bf16 or as bytes, at least as many as the plan's."""
         s = self.shapes
-        key = tuple(0 if isinstance(t, int) else _sig(t)
-                    for t in (x, ids, weights, expert_w, shexp_w, shexp_gate_w, out))
+        key = (_sig(ids), _sig(weights), _flat(x), _flat(expert_w), _flat(shexp_w), _flat(shexp_gate_w), _flat(out))
         # signatures that this layer has checked
-        passed = self.__dict__.setdefault("_routed", set())
+        passed = getattr(self, "_routed", None)
+        if passed is None:
+            passed = self._routed = set()
         if key not in passed:
             self._check_routed(x, ids, weights, expert_w, shexp_w, shexp_gate_w, out)
             if len(passed) >= 4096:
