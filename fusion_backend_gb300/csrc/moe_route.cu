@@ -524,12 +524,19 @@ __global__ void __launch_bounds__(32 * kWarps, EPL <= 8 ? 6 : 1) k_route(const _
     }
 
     // Weights from the chosen logits.  Renormalised, the softmax needs no other
-    // logit, and the sigmoid is exp(l) to fp32's resolution where every chosen
-    // logit is far below 0 (the ratio is then formed before it can underflow).
+    // logit, and the sigmoid, e^l / (1 + e^l), is formed times e^-top where every
+    // chosen logit is below 0: a ratio of two small scores then does not underflow.
     float v = 0.f;
     if (P.renorm) {
       const float top = warp_max(lj);
-      if (id >= 0) v = !P.sigmoid || top < -60.f ? expf(lj - top) : 1.f / (1.f + expf(-lj));
+      if (id >= 0) {
+        if (P.sigmoid && !(top < 0.f)) {
+          v = 1.f / (1.f + expf(-lj));
+        } else {
+          v = expf(lj - top);
+          if (P.sigmoid) v /= 1.f + expf(lj);
+        }
+      }
       const float total = warp_sum(v);
       if (id >= 0) v = __fdividef(v, total);
     } else if (id >= 0) {
