@@ -30,26 +30,31 @@ constexpr int kXPitch = 4160;            // tensor-core loops: bytes per token r
 enum : int { kCtrlStatus = 0, kCtrlProbe = 2, kCtrlWords = 64 };
 
 // Decode row kernel: its grid-wide synchronisation words (in the workspace,
-// after the control words).  The call's epoch e is one more than the value in
-// `epoch`, which every block reads after the wait on the previous kernel.  A
-// barrier: block c stores e into its own slot of a flag array (release);
-// block 0 waits until every slot holds e, then stores e into the barrier's
-// `go` word (release); every block waits until `go` holds e.  Nothing has to
-// be reset between calls: each call overwrites every word it waits on with a
-// value no earlier call stored (the previous call stored e - 1).  Block 0
-// advances `epoch` once all blocks have read it (in the first barrier, after
-// it has seen every slot).  Each block also writes its own status slot (0 or
-// the timeout status) on every call.
+// after the control words).  Nothing is assumed of what they hold: a fresh
+// workspace, one that other calls left or that another user wrote into, in part
+// or as a whole.  The call's epoch e is one more than the value in `epoch`, which
+// every block reads after the wait on the previous kernel; block 0 advances it
+// once all blocks have read it (in the call's first barrier).
 //
-// Fast path: once a call has run to its first barrier on this workspace, the
-// two arrival counters of the next call (count[e + 1 parity]) are zero --
-// block 0 clears them after that barrier, when no block of this call can
-// touch them -- and `sig` holds ~e.  A call that finds sig == ~epoch uses the
-// counters (each block adds one; a barrier is complete at G), one hop through
-// L2 instead of two; any other state (a workspace that another user
-// overwrote, or never initialised) takes the flag barrier, which needs no
-// prior state.  Both decisions are the same in every block: they read
-// `epoch` and `sig` before any block can change them.
+// A barrier by flags: block c stores a token into its own slot of a flag array
+// (release); block 0 waits until every slot holds it, then stores it into the
+// barrier's `go` word (release); every block waits until `go` holds it and then
+// clears its slot.
+// The token is a hash of the call's epoch and of what the two `go` words hold
+// before the barrier, the same in every block: so it differs from what the `go`
+// words hold, and from the slots, which no call leaves set.  (The epoch by itself
+// may come back: with its word overwritten, a call could find it in slots and `go`
+// words that had kept it from an earlier call.)
+//
+// Fast path: once a call has run to its first barrier on this workspace, `epoch`
+// is e, `sig` is ~e, and the two arrival counters of the next call (count[e + 1
+// parity]) hold a number of that call's, set by block 0 after that barrier, when
+// no block of this call can touch them.  A call that finds all of this, the
+// counters less than G arrivals on, uses them (each block adds one; a barrier is
+// complete at G): one hop through L2 instead of two.  In any other state the
+// barriers go by flags.  The decision is the same in every block: they read the
+// words before any block can change them but by arriving.  Each block also writes
+// its own status slot (0 or the timeout status) on every call.
 //
 // With one token the second barrier is not used: each partial output is a word
 // tagged with the call (the low half of e above the fp32 value).  Each block

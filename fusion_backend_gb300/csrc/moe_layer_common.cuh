@@ -62,28 +62,72 @@ MOE_DEV bool grid_flags_wait(const unsigned long long* flags, int G, unsigned lo
   return __all_sync(0xffffffffu, ok);
 }
 
+// Where the arrivals of epoch e count from: 4096 apart from epoch to epoch, more
+// than a barrier adds, and nothing that a word holds by chance.
+MOE_DEV uint32_t arrivals_from(unsigned long long epoch) { return ((uint32_t)epoch << 12) + 0x6D6F6566u; }
+// A barrier's token: a hash (multiplications and shifts) of the call's epoch and of
+// the release words before it.
+MOE_DEV unsigned long long sync_token(const RowSync* sy, unsigned long long epoch) {
+  unsigned long long v = epoch * 0xD6E8FEB86659FD93ull + __ldcg(&sy->go[0]) * 0xA5CB9243F0AEF5ADull + __ldcg(&sy->go[1]) +
+                         0x6D6F655F66666E00ull;
+  v = (v ^ (v >> 31)) * 0xD6E8FEB86659FD93ull;
+  return v ^ (v >> 32);
+}
+
+// The words of RowSync are as the call before leaves them for the one after
+// prev_epoch (arrivals of other blocks may be among them, this block's are not).
+MOE_DEV bool sync_fast(const RowSync* sy, unsigned long long prev_epoch, int G) {
+  const unsigned long long sig = __ldcg(&sy->sig);
+  const uint4 c = __ldcg(reinterpret_cast<const uint4*>(sy->count));
+  const uint32_t from = arrivals_from(prev_epoch + 1ull);
+  const bool odd = !(prev_epoch & 1);  // the call's own epoch
+  return sig == ~prev_epoch && (odd ? c.z : c.x) - from < (uint32_t)G && (odd ? c.w : c.y) - from < (uint32_t)G;
+}
+
+// The barrier by flags: a warp of every block (out of line: calls that follow one
+// another do not come here).
+static __device__ __noinline__ bool flag_barrier(RowSync* sy, int which, int G, unsigned long long epoch, int cta) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long* const flags = which ? sy->partial_ready : sy->logits_ready;
+  // (no block changes the release words before all have arrived)
+  const unsigned long long token = sync_token(sy, epoch);
+  __syncwarp();
+  if (lane == 0) st_release_gpu_u64(flags + cta, token);
+  bool ok = true;
+  if (cta == 0) {
+    ok = grid_flags_wait(flags, G, token);
+    if (ok && lane == 0) st_release_gpu_u64(&sy->go[which], token);
+  }
+  if (ok && lane == 0) ok = word_wait(&sy->go[which], token);
+  ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  if (lane == 0) flags[cta] = 0ull;  // (block 0 has seen it)
+  return ok;
+}
+
 // A grid-wide barrier of the decode row kernel (see RowSync), called by
 // every thread of every block after the block's writes that the barrier
-// publishes.  fast: each block adds one to *count (release) and waits until
-// it reaches G.  Otherwise block c stores `epoch` into flags[c] (release);
-// block 0's warp 0 waits for every slot and releases *go; every block waits
-// for *go.  first: the call's first barrier -- block 0 then (after every
-// block has arrived, hence has read RowSync's epoch and sig) clears the next
-// call's counters and advances epoch and sig.  Returns false in every thread
+// publishes.  Where *fast_word (shared memory, sync_fast of one of the block's
+// threads) says so, each block adds one to *count (release) and waits for G
+// arrivals.  Otherwise flag_barrier.  first: the call's first barrier -- block 0
+// then (after every block has arrived, hence has read RowSync's words) sets the
+// next call's counters and advances epoch and sig.  Returns false in every thread
 // of the block when a wait gave up (bounded, about a second).
 // NT: the threads of the block that take part (blk_sync).
 template <int NT = 0>
-MOE_DEV bool grid_barrier(RowSync* sy, int which, bool fast, int G, unsigned long long epoch, int cta, bool first) {
-  const int tid = threadIdx.x, lane = tid & 31;
+MOE_DEV bool grid_barrier(RowSync* sy, int which, const int32_t* fast_word, int G, unsigned long long epoch, int cta,
+                          bool first) {
+  const int tid = threadIdx.x;
   blk_sync<NT>();
   bool ok = true;
-  uint32_t* count = &sy->count[epoch & 1][which];
+  const bool fast = *fast_word != 0;
+  uint32_t* const count = &sy->count[epoch & 1][which];
   if (tid == 0) {
     if (fast) {
       red_release_gpu_add(count, 1u);
+      const uint32_t from = arrivals_from(epoch);
       unsigned long long t0 = 0;
       for (uint32_t it = 0;; ++it) {
-        if (ld_acquire_gpu(count) >= (uint32_t)G) break;
+        if (ld_acquire_gpu(count) - from >= (uint32_t)G) break;
         if (it == 16) t0 = global_ns();
         if (it >= kSpinLimit || (it > 16 && (it & 15) == 0 && global_ns() - t0 > kWaitLimitNs)) {
           ok = false;
@@ -91,26 +135,19 @@ MOE_DEV bool grid_barrier(RowSync* sy, int which, bool fast, int G, unsigned lon
         }
         if (it > 16) __nanosleep(32);
       }
-    } else {
-      st_release_gpu_u64((which ? sy->partial_ready : sy->logits_ready) + cta, epoch);
     }
   }
-  if (!fast && tid < 32) {
-    if (cta == 0) {
-      ok = grid_flags_wait(which ? sy->partial_ready : sy->logits_ready, G, epoch);
-      if (ok && lane == 0) st_release_gpu_u64(&sy->go[which], epoch);
-    }
-    if (ok && lane == 0) ok = word_wait(&sy->go[which], epoch);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-  }
+  if (!fast && tid < 32) ok = flag_barrier(sy, which, G, epoch, cta);
   if (first && cta == 0 && tid == 0 && ok) {
-    // every block has read epoch and sig: prepare the next call's fast path
-    sy->count[(epoch + 1) & 1][0] = 0u;
-    sy->count[(epoch + 1) & 1][1] = 0u;
+    // every block has read the words: prepare the next call's fast path
+    const uint32_t from = arrivals_from(epoch + 1ull);
+    sy->count[(epoch + 1) & 1][0] = from;
+    sy->count[(epoch + 1) & 1][1] = from;
     sy->epoch = epoch;
     __threadfence();
     sy->sig = ~epoch;
   }
+  if (first && tid == 0 && !ok) sy->sig = epoch;  // counters that stopped in between are not used again
   return !blk_sync_or<NT>(!ok);
 }
 

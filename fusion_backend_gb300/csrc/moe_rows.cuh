@@ -37,8 +37,7 @@
 //      the G partials of its own output columns in block order and writes
 //      out (adding x_res in the block form).  All orders are fixed, so
 //      results are bitwise repeatable.
-// The grid-wide barriers use per-block flag slots tagged with the call's
-// epoch (RowSync), so no workspace word has to be reset between calls.
+// The grid-wide barriers (RowSync) assume nothing of what the workspace holds.
 //
 // Tensor-core instances (H = 2048, bf16-exact activation): the stage loops
 // run on mma.m16n8k16 over the swizzled tensor-copy boxes, one
@@ -86,7 +85,8 @@ struct RowTab {
   int32_t* active;   // [T*K] selected experts, ascending
   uint32_t* mask;    // [T*K] tokens of active expert u (bit t)
   float* wt;         // [T*K][T] weight of token t for active expert u (0 if not routed)
-  int32_t* misc;     // [8] the number of active experts U; (split blocks) n_stages, first routed stage, call tag
+  int32_t* misc;     // [8] the number of active experts U; (split blocks) n_stages, first routed stage, call tag;
+                     // [5] the barriers go by counters
   int32_t* qtab;     // [T*K - K + 1][4] per possible U: routed stages, first active expert, first group
   uint32_t* xmax;    // [T] int8 activation: bits of max |x| of token t
   float* xsc;        // [T] int8 activation: x_scale = max|x| / 127 of token t
@@ -782,8 +782,9 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
   RowSync* const sync = P.sync;
   const unsigned long long prev_epoch = __ldcg(&sync->epoch);
   const unsigned long long epoch = prev_epoch + 1ull;
-  const bool fast_sync = __ldcg(&sync->sig) == ~prev_epoch;
   const uint32_t tag = (uint32_t)epoch;
+  // (one thread of a warp with nothing else to read here)
+  if (tid == 32 * (kRowWarps - 2)) tb.misc[5] = sync_fast(sync, prev_epoch, P.G);
   // tagged partials: kept in L2 (evict-last; rewritten every call, read
   // within microseconds)
   const uint64_t pol_keep = policy_evict_last();
@@ -1067,7 +1068,7 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
   // needs it for the marks of the tagged words alone; without them the second
   // barrier is the call's first.
   if constexpr (!GIVEN || TAGGED) {
-    if (!grid_barrier<SYNC_NT>(sync, 0, fast_sync, P.G, epoch, cta, true)) timed_out = true;
+    if (!grid_barrier<SYNC_NT>(sync, 0, tb.misc + 5, P.G, epoch, cta, true)) timed_out = true;
   } else {
     blk_sync<SYNC_NT>();  // x in its compute form
   }
@@ -1898,7 +1899,7 @@ __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_
   float resid = 0.f;
   if (P.block_mode && tid < O) resid = __ldcg(P.out + (size_t)(tid / nD) * H + da + tid % nD);
   bool tail_timed_out = false;
-  if constexpr (!TAGGED) tail_timed_out = !grid_barrier<SYNC_NT>(sync, 1, fast_sync, P.G, epoch, cta, GIVEN);
+  if constexpr (!TAGGED) tail_timed_out = !grid_barrier<SYNC_NT>(sync, 1, tb.misc + 5, P.G, epoch, cta, GIVEN);
   // The O sums of G partials.  Thread (sp, o) adds partials sp, sp + S, ...
   // in order, up to 16 loads in flight together; the S part sums are then
   // added in order.
