@@ -355,8 +355,8 @@ constexpr int kBarSplit = 3;  // named barrier: main and down-projection warps m
 // exchange: every block builds the tables itself and issues the first routed
 // stages before it has seen x, and only the one-token form keeps the first
 // grid-wide barrier (for the marks of its tagged words), behind those copies:
-// on one routing, H = 2048, E = 128, top-8, gated shared expert, 22.7 us against
-// 24.4 with the layer's router (bf16, one token), 37.6 against 40.4 (4-bit, four).
+// on one routing, H = 2048, E = 128, top-8, gated shared expert, 22.9 us against
+// 24.4 with the layer's router (bf16, one token), 38.8 against 41.1 (4-bit, four).
 template <int TMAX, int WK, bool FAST, int NCH, bool GIVEN = false>
 __global__ void __maxnreg__(rows_threads(WK, FAST) > kRowThreads ? 128 : 224) k_rows(const __grid_constant__ LayerParams Pk) {
   constexpr bool Q4 = WK == kWkQ4;
