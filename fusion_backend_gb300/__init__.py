@@ -65,6 +65,10 @@ EXPORTS = (
     "moe_ffn_norm_residual",
     "moe_ffn_adapters_workspace",
     "moe_ffn_add_adapters",
+    "moe_ffn_project",
+    "moe_ffn_append_kv",
+    "moe_ffn_attend_workspace",
+    "moe_ffn_attend",
 )
 
 STATIC_SCRATCH_BYTES = 1 << 24
@@ -109,6 +113,24 @@ class NormArgs(ctypes.Structure):
 
 class AdaptersArgs(ctypes.Structure):
     _fields_ = _fields("T K N R n_adapters x_dtype y_dtype", "", "x_stride y_stride out_stride")
+
+
+class ProjectArgs(ctypes.Structure):
+    _fields_ = _fields("T K N group x_dtype y_dtype", "", "x_stride y_stride w_stride")
+
+
+_CACHES = "kc_page_stride kc_slot_stride kc_head_stride vc_page_stride vc_slot_stride vc_head_stride"
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = _fields("T q_heads kv_heads D rot interleaved x_dtype q_out_dtype cache_dtype page_size pages", "scale",
+                       "q_stride q_head_stride k_stride k_head_stride v_stride v_head_stride q_out_stride "
+                       f"q_out_head_stride {_CACHES}")
+
+
+class AttendArgs(ctypes.Structure):
+    _fields_ = _fields("T B q_heads kv_heads D dtype out_dtype page_size pages max_pages mask_words", "scale softcap",
+                       f"q_stride q_head_stride out_stride out_head_stride {_CACHES} table_stride mask_stride")
 
 
 _lib = None
@@ -162,6 +184,14 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_adapters_workspace.argtypes = [ctypes.POINTER(AdaptersArgs), ctypes.POINTER(sz)]
         L.moe_ffn_add_adapters.restype = ctypes.c_int
         L.moe_ffn_add_adapters.argtypes = [ctypes.POINTER(AdaptersArgs), vp, vp, sz, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_ffn_project.restype = ctypes.c_int
+        L.moe_ffn_project.argtypes = [ctypes.POINTER(ProjectArgs), vp, vp, vp, vp, vp]
+        L.moe_ffn_append_kv.restype = ctypes.c_int
+        L.moe_ffn_append_kv.argtypes = [ctypes.POINTER(AppendArgs)] + 10 * [vp]
+        L.moe_ffn_attend_workspace.restype = ctypes.c_int
+        L.moe_ffn_attend_workspace.argtypes = [ctypes.POINTER(AttendArgs), ctypes.POINTER(sz)]
+        L.moe_ffn_attend.restype = ctypes.c_int
+        L.moe_ffn_attend.argtypes = [ctypes.POINTER(AttendArgs), vp, vp, sz] + 9 * [vp]
         _lib = L
     return _lib
 
@@ -393,15 +423,16 @@ def _on_device(first, **tensors) -> None:
             raise ValueError(f"{name}: must be on the call's CUDA device")
 
 
-def _new(stream, shape, dtype, device):
-    """A tensor allocated on the stream that the call runs on."""
+def _new(stream, shape, dtype, device, zero=False):
+    """A tensor allocated (and filled with zeros) on the stream that the call runs on."""
     import torch
 
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
 
 
 def _route_block(logits, top_k, bias, score, groups, top_groups, group_score, renorm, scale, ids, weights):
@@ -559,6 +590,195 @@ def moe_ffn_add_adapters(y, x, adapter_ids, a, b, ranks=None, scales=None, out=N
         None if scales is None else scales.data_ptr(), y.data_ptr(), out.data_ptr())
     if rc:
         _check(rc, "moe_ffn_add_adapters")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# The attention half of a block: products with 4-bit weights, the paged cache
+# and attention over it.  Heads are [tokens, heads, D] tensors with adjacent
+# elements of a head, caches [pages, page_size, kv_heads, D]; other strides are
+# free (a transposed cache whose pages hold their heads one behind the other
+# included).
+
+
+def _project_block(x, w, group, bias, out):
+    import torch
+
+    _require(x.dim() == 2 and w.dim() == 2, "expected x [T, K], w [N, row bytes]")
+    _require(group in (32, 64, 128), f"group: {group}, expected 32, 64 or 128")
+    T, K = x.shape
+    N = w.shape[0]
+    _require(w.dtype == torch.uint8, f"w: dtype {w.dtype}, expected uint8 rows of codes and scales")
+    _require(K % group == 0, f"x: {K} columns are no multiple of the group")
+    need = K // 2 + 2 * (K // group)
+    _require(w.shape[1] >= need, f"w: rows of {w.shape[1]} bytes, expected {need}")
+    _require(w.stride(1) == 1, "w: the bytes of a row must be adjacent")
+    if bias is not None:
+        _whole(bias, (N,), torch.float32, "bias")
+    xs = _matrix(x, T, K, "x")
+    a = _block(ProjectArgs, T, K, N, group, _code(x, "x", (ACT_BF16, ACT_F16)), _code(out, "out"),
+               xs if T > 1 else (K + 7) // 8 * 8, _matrix(out, T, N, "out"),
+               w.stride(0) if N > 1 else (need + 15) // 16 * 16)
+    _on_device(x, x=x, w=w, bias=bias, out=out)
+    return a
+
+
+def moe_ffn_project(x, w, group: int = 32, bias=None, out=None, out_dtype=None, stream=None):
+    """``out = x W^T + bias`` for few tokens: x [T, K] bf16 or fp16, w uint8 [N, row bytes] in rows of K/2 bytes of
+    4-bit codes and K/group fp16 scales (the layer's 4-bit rows with group 32; see ``include/moe_ffn.h``), bias fp32
+    [N].  out [T, N] defaults to a new tensor of ``out_dtype`` (x's type).  Returns out."""
+    if out is None:
+        _require(x.dim() == 2 and w.dim() == 2, "expected x [T, K], w [N, row bytes]")
+        out = _new(stream, (x.shape[0], w.shape[0]), out_dtype or x.dtype, x.device)
+    else:
+        _require(out_dtype is None or out_dtype == out.dtype, "out: not of out_dtype")
+    key = (3, _sig(x), _sig(w), group, _sig(bias), _sig(out))
+    a = _blocks.get(key) or _remember(key, _project_block(x, w, group, bias, out))
+    rc = (_lib or lib()).moe_ffn_project(a, _raw_stream(stream, x), x.data_ptr(), w.data_ptr(),
+                                         None if bias is None else bias.data_ptr(), out.data_ptr())
+    if rc:
+        _check(rc, "moe_ffn_project")
+    return out
+
+
+def _heads(t, T: int, H: int, D: int, name: str):
+    """Token and head strides of t, a [T, H, D] tensor with adjacent elements of a head."""
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({T}, {H}, {D})")
+    if D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    # a single token or head has no stride of its own
+    return t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D
+
+
+def _cache_strides(t, shape, name: str):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    own = (shape[3] + 7) // 8 * 8
+    return tuple(t.stride(i) if shape[i] > 1 else own for i in range(3))
+
+
+def _append_block(k, v, positions, slots, inv_freq, k_cache, v_cache, q, q_out, interleaved, scale):
+    import torch
+
+    _require(k.dim() == 3 and k_cache.dim() == 4, "expected k [T, kv_heads, D], k_cache [pages, page_size, kv_heads, D]")
+    T, Hkv, D = k.shape
+    pages, page_size = k_cache.shape[:2]
+    shape = (pages, page_size, Hkv, D)
+    _require(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), "q, k, v: must have one dtype")
+    _require(v_cache.dtype == k_cache.dtype, "k_cache, v_cache: must have one dtype")
+    _require((q is None) == (q_out is None), "q_out: given without q")
+    _whole(positions, (T,), torch.int32, "positions")
+    _whole(slots, (T,), torch.int32, "slots")
+    rot = 0
+    if inv_freq is not None:
+        _require(inv_freq.dim() == 1, "inv_freq: expected [rot / 2]")
+        rot = 2 * inv_freq.shape[0]
+        _whole(inv_freq, (rot // 2,), torch.float32, "inv_freq")
+        _require(rot <= D, f"inv_freq: {rot} rotated elements of heads of {D}")
+    Hq, qs, qos, qod = 0, (D, D), (D, D), ACT_F32
+    if q is not None:
+        _require(q.dim() == 3, "q: expected [T, q_heads, D]")
+        Hq = q.shape[1]
+        qs, qos, qod = _heads(q, T, Hq, D, "q"), _heads(q_out, T, Hq, D, "q_out"), _code(q_out, "q_out")
+    a = _block(AppendArgs, T, Hq, Hkv, D, rot, bool(interleaved), _code(k, "k"), qod, _code(k_cache, "k_cache"),
+               page_size, pages, scale, *qs, *_heads(k, T, Hkv, D, "k"), *_heads(v, T, Hkv, D, "v"), *qos,
+               *_cache_strides(k_cache, shape, "k_cache"), *_cache_strides(v_cache, shape, "v_cache"))
+    _on_device(k, k=k, v=v, positions=positions, slots=slots, inv_freq=inv_freq, k_cache=k_cache, v_cache=v_cache, q=q,
+               q_out=q_out)
+    return a
+
+
+def moe_ffn_append_kv(k, v, positions, slots, inv_freq, k_cache, v_cache, q=None, q_out=None,
+                      interleaved: bool = False, scale: float = 1.0, stream=None):
+    """k and v [T, kv_heads, D] into the caches [pages, page_size, kv_heads, D] at ``slots`` (int32 [T], page *
+    page_size + slot, -1: padding), k and q [T, q_heads, D] rotated by ``positions`` (int32 [T]) times ``inv_freq``
+    (fp32 [rot / 2]; None: no rotation) on the way (see ``include/moe_ffn.h``).  q_out defaults to q (in place).
+    Returns q_out."""
+    if q_out is None:
+        q_out = q
+    key = (4, _sig(k), _sig(v), _sig(positions), _sig(slots), _sig(inv_freq), _sig(k_cache), _sig(v_cache), _sig(q),
+           _sig(q_out), interleaved, scale)
+    a = _blocks.get(key) or _remember(key, _append_block(k, v, positions, slots, inv_freq, k_cache, v_cache, q, q_out,
+                                                         interleaved, scale))
+    rc = (_lib or lib()).moe_ffn_append_kv(
+        a, _raw_stream(stream, k), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        positions.data_ptr(), slots.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
+        None if q_out is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
+    if rc:
+        _check(rc, "moe_ffn_append_kv")
+    return q_out
+
+
+def moe_ffn_attend_workspace(T: int, B: int, q_heads: int, kv_heads: int, D: int) -> int:
+    """Workspace bytes of moe_ffn_attend for T rows of B sequences and heads of D elements."""
+    n = ctypes.c_size_t()
+    a = _block(AttendArgs, T, B, q_heads, kv_heads, D, ACT_BF16, ACT_F32, 1, 0, 0, 0, 1.0, 0.0, *(10 * [256]), 0, 0)
+    _check(lib().moe_ffn_attend_workspace(a, ctypes.byref(n)), "moe_ffn_attend_workspace")
+    return max(n.value, 256)
+
+
+def _attend_block(q, k_cache, v_cache, page_table, lens, q_start, mask, scale, softcap, out, lse, workspace):
+    import torch
+
+    _require(q.dim() == 3 and k_cache.dim() == 4 and page_table.dim() == 2,
+             "expected q [T, q_heads, D], k_cache [pages, page_size, kv_heads, D], page_table [B, max_pages]")
+    T, Hq, D = q.shape
+    pages, page_size, Hkv = k_cache.shape[:3]
+    B, max_pages = page_table.shape
+    shape = (pages, page_size, Hkv, D)
+    _require(k_cache.dtype == q.dtype and v_cache.dtype == q.dtype, "k_cache, v_cache: must have q's dtype")
+    for t, name in ((page_table, "page_table"), (mask, "mask")):
+        _require(t is None or t.dtype == torch.int32, f"{name}: expected int32")
+    _whole(lens, (B,), torch.int32, "lens")
+    _whole(q_start, (B + 1,), torch.int32, "q_start")
+    words, ms = 0, 0
+    if mask is not None:
+        _require(mask.dim() == 2, "mask: expected [T, words]")
+        words = mask.shape[1]
+        ms = _matrix(mask, T, words, "mask")
+    if lse is not None:
+        _whole(lse, (T, Hq), torch.float32, "lse")
+    qs, os_ = _heads(q, T, Hq, D, "q"), _heads(out, T, Hq, D, "out")
+    a = _block(AttendArgs, T, B, Hq, Hkv, D, _code(q, "q", (ACT_BF16, ACT_F16)), _code(out, "out"), page_size, pages,
+               max_pages, words, D**-0.5 if scale is None else scale, softcap, *qs, *os_,
+               *_cache_strides(k_cache, shape, "k_cache"), *_cache_strides(v_cache, shape, "v_cache"),
+               _matrix(page_table, B, max_pages, "page_table"), ms)
+    _on_device(q, q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, lens=lens, q_start=q_start, mask=mask,
+               out=out, lse=lse, workspace=workspace)
+    if workspace is not None:
+        _require(workspace.is_contiguous(), "workspace: must be contiguous")
+    return a
+
+
+def moe_ffn_attend(q, k_cache, v_cache, page_table, lens, q_start, mask=None, scale=None, softcap: float = 0.0,
+                   out=None, lse=None, workspace=None, stream=None):
+    """Attention of B sequences' newest tokens over the paged cache that holds them.  q [T, q_heads, D]; sequence b's
+    rows are ``q_start[b] .. q_start[b + 1]`` (int32 [B + 1]), the last of its ``lens[b]`` cached tokens (int32 [B]),
+    which lie in the pages ``page_table[b]`` (int32 [B, max_pages]).  mask int32 [T, words]: which of its sequence's
+    rows a row sees (bit j: the j-th), None: those up to itself.  scale defaults to D ** -0.5; softcap 0: no cap (see
+    ``include/moe_ffn.h``).  out defaults to a new tensor of q's shape and type (rows of no sequence are then 0), lse
+    (fp32 [T, q_heads]) is written where given.  workspace (a tensor of moe_ffn_attend_workspace bytes) defaults to a new
+    one.  Returns out."""
+    if out is None:
+        out = _new(stream, q.shape, q.dtype, q.device, zero=True)
+    key = (5, _sig(q), _sig(k_cache), _sig(v_cache), _sig(page_table), _sig(lens), _sig(q_start), _sig(mask), scale,
+           softcap, _sig(out), _sig(lse), _sig(workspace))
+    a = _blocks.get(key) or _remember(key, _attend_block(q, k_cache, v_cache, page_table, lens, q_start, mask, scale,
+                                                         softcap, out, lse, workspace))
+    if workspace is None:
+        import torch
+
+        workspace = _new(stream, (moe_ffn_attend_workspace(a.T, a.B, a.q_heads, a.kv_heads, a.D),), torch.uint8,
+                         q.device)
+    rc = (_lib or lib()).moe_ffn_attend(
+        a, _raw_stream(stream, q), workspace.data_ptr(), workspace.numel() * workspace.element_size(), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lens.data_ptr(), q_start.data_ptr(),
+        None if mask is None else mask.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr())
+    if rc:
+        _check(rc, "moe_ffn_attend")
     return out
 
 

@@ -540,6 +540,42 @@ int check_adapters(const moe_ffn_adapters_args* a) {
   return MOE_FFN_OK;
 }
 
+constexpr int64_t kMaxSlots = 2147483647;  // slots of a cache, tokens of a sequence
+
+int check_attend(const moe_ffn_attend_args* a) {
+  if (!a || a->T < 0 || a->B < 0 || a->pages < 0 || a->max_pages < 0 || a->mask_words < 0)
+    return MOE_FFN_ERR_INVALID_ARG;
+  if ((a->dtype != MOE_FFN_ACT_BF16 && a->dtype != MOE_FFN_ACT_F16) || !valid_elem(a->out_dtype) ||
+      !finite(a->scale) || !finite(a->softcap) || a->softcap < 0.f)
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->T > kAttendMaxT || a->B > kAttendMaxB || a->kv_heads < 1 || a->q_heads < 1 || a->q_heads % a->kv_heads ||
+      a->q_heads / a->kv_heads > kAttendMaxGroup || a->kv_heads > kMaxHeads || a->D < 8 || a->D > kAttendMaxD ||
+      a->D % 8 || a->page_size < 1 || (int64_t)a->pages * a->page_size > kMaxSlots ||
+      (int64_t)a->max_pages * a->page_size > kMaxSlots)
+    return MOE_FFN_ERR_UNSUPPORTED;
+  const int64_t row = (int64_t)a->D;
+  if (a->q_stride < row || a->q_head_stride < row || a->out_stride < row || a->out_head_stride < row ||
+      a->kc_page_stride < row || a->kc_slot_stride < row || a->kc_head_stride < row || a->vc_page_stride < row ||
+      a->vc_slot_stride < row || a->vc_head_stride < row || a->table_stride < a->max_pages ||
+      a->mask_stride < a->mask_words)
+    return MOE_FFN_ERR_INVALID_ARG;
+  if ((a->kc_page_stride | a->kc_slot_stride | a->kc_head_stride | a->vc_page_stride | a->vc_slot_stride |
+       a->vc_head_stride) % 8)
+    return MOE_FFN_ERR_MISALIGNED;
+  return MOE_FFN_OK;
+}
+
+void attend_sizes(const moe_ffn_attend_args* a, AttendParams& P) {
+  P.T = a->T;
+  P.B = a->B;
+  P.Hq = a->q_heads;
+  P.Hkv = a->kv_heads;
+  P.G = a->q_heads / a->kv_heads;
+  P.D = a->D;
+  P.f16 = a->dtype == MOE_FFN_ACT_F16;
+  P.out_dtype = a->out_dtype;
+}
+
 }  // namespace
 
 extern "C" {
@@ -684,6 +720,168 @@ int moe_ffn_add_adapters(const moe_ffn_adapters_args* a, moe_ffn_stream_t stream
   P.out = out;
   P.v = static_cast<float*>(workspace);
   return cuda_status(launch_adapters(P, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_ffn_project(const moe_ffn_project_args* a, moe_ffn_stream_t stream, const void* x, const void* w,
+                    const float* bias, void* y) {
+  if (!a || a->T < 0) return MOE_FFN_ERR_INVALID_ARG;
+  if ((a->x_dtype != MOE_FFN_ACT_BF16 && a->x_dtype != MOE_FFN_ACT_F16) || !valid_elem(a->y_dtype))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->T > kProjectMaxT || (a->group != 32 && a->group != 64 && a->group != 128) || a->K < a->group ||
+      a->K > 65536 || a->K % a->group || a->N < 1 || a->N > (1 << 24))
+    return MOE_FFN_ERR_UNSUPPORTED;
+  if (a->x_stride < a->K || a->y_stride < a->N || a->w_stride < a->K / 2 + a->K / a->group * 2)
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->x_stride % 8 || a->w_stride % 16) return MOE_FFN_ERR_MISALIGNED;
+  if (a->T == 0) return MOE_FFN_OK;
+  if (!x || !w || !y) return MOE_FFN_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !elem_aligned(y, a->y_dtype))
+    return MOE_FFN_ERR_MISALIGNED;
+  int sms = 0;
+  const int rc = check_device(&sms);
+  if (rc != MOE_FFN_OK) return rc;
+  ProjectParams P = {};
+  P.T = a->T;
+  P.K = a->K;
+  P.N = a->N;
+  P.group = a->group;
+  P.sms = sms;
+  P.f16 = a->x_dtype == MOE_FFN_ACT_F16;
+  P.y_dtype = a->y_dtype;
+  P.x_stride = a->x_stride;
+  P.y_stride = a->y_stride;
+  P.w_stride = a->w_stride;
+  P.x = static_cast<const uint16_t*>(x);
+  P.w = static_cast<const uint8_t*>(w);
+  P.bias = bias;
+  P.y = y;
+  return cuda_status(launch_project(P, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_ffn_append_kv(const moe_ffn_append_args* a, moe_ffn_stream_t stream, const void* q, const void* k,
+                      const void* v, const int32_t* positions, const int32_t* slots, const float* inv_freq,
+                      void* q_out, void* k_cache, void* v_cache) {
+  if (!a || a->T < 0 || a->pages < 0 || a->q_heads < 0) return MOE_FFN_ERR_INVALID_ARG;
+  if (!valid_elem(a->x_dtype) || !valid_elem(a->q_out_dtype) || !valid_elem(a->cache_dtype) || !finite(a->scale))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->T > kAppendMaxT || a->kv_heads < 1 || a->kv_heads > kMaxHeads || a->q_heads > kMaxHeads || a->D < 1 ||
+      a->D > kAppendMaxD || a->rot < 0 || a->rot > a->D || a->rot % 2 || a->page_size < 1 ||
+      (int64_t)a->pages * a->page_size > kMaxSlots)
+    return MOE_FFN_ERR_UNSUPPORTED;
+  const int64_t row = a->D;
+  if (a->k_stride < row || a->k_head_stride < row || a->v_stride < row || a->v_head_stride < row ||
+      (q && (a->q_stride < row || a->q_head_stride < row || a->q_out_stride < row || a->q_out_head_stride < row)) ||
+      a->kc_page_stride < row || a->kc_slot_stride < row || a->kc_head_stride < row || a->vc_page_stride < row ||
+      a->vc_slot_stride < row || a->vc_head_stride < row)
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (a->T == 0 || a->pages == 0) return MOE_FFN_OK;
+  if (!k || !v || !positions || !slots || (a->rot > 0 && !inv_freq) || !k_cache || !v_cache || !q != !q_out ||
+      (q && a->q_heads < 1))
+    return MOE_FFN_ERR_INVALID_ARG;
+  if (!elem_aligned(q, a->x_dtype) || !elem_aligned(k, a->x_dtype) || !elem_aligned(v, a->x_dtype) ||
+      !aligned(positions, 4) || !aligned(slots, 4) || !aligned(inv_freq, 4) || !elem_aligned(q_out, a->q_out_dtype) ||
+      !elem_aligned(k_cache, a->cache_dtype) || !elem_aligned(v_cache, a->cache_dtype))
+    return MOE_FFN_ERR_MISALIGNED;
+  int sms = 0;
+  const int rc = check_device(&sms);
+  if (rc != MOE_FFN_OK) return rc;
+  AppendParams P = {};
+  P.T = a->T;
+  P.Hq = q ? a->q_heads : 0;
+  P.Hkv = a->kv_heads;
+  P.D = a->D;
+  P.rot = a->rot;
+  P.sms = sms;
+  P.interleaved = a->interleaved != 0;
+  P.x_dtype = a->x_dtype;
+  P.q_dtype = a->q_out_dtype;
+  P.c_dtype = a->cache_dtype;
+  P.page_size = a->page_size;
+  P.slots = a->pages * a->page_size;
+  P.scale = a->scale;
+  P.q_stride = a->q_stride;
+  P.q_head = a->q_head_stride;
+  P.k_stride = a->k_stride;
+  P.k_head = a->k_head_stride;
+  P.v_stride = a->v_stride;
+  P.v_head = a->v_head_stride;
+  P.qo_stride = a->q_out_stride;
+  P.qo_head = a->q_out_head_stride;
+  P.kc_page = a->kc_page_stride;
+  P.kc_slot = a->kc_slot_stride;
+  P.kc_head = a->kc_head_stride;
+  P.vc_page = a->vc_page_stride;
+  P.vc_slot = a->vc_slot_stride;
+  P.vc_head = a->vc_head_stride;
+  P.q = q;
+  P.k = k;
+  P.v = v;
+  P.positions = positions;
+  P.slot = slots;
+  P.inv_freq = inv_freq;
+  P.q_out = q_out;
+  P.k_cache = k_cache;
+  P.v_cache = v_cache;
+  return cuda_status(launch_append(P, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_ffn_attend_workspace(const moe_ffn_attend_args* a, size_t* bytes) {
+  if (!bytes) return MOE_FFN_ERR_INVALID_ARG;
+  const int rc = check_attend(a);
+  if (rc != MOE_FFN_OK) return rc;
+  AttendParams P = {};
+  attend_sizes(a, P);
+  *bytes = attend_workspace(P);
+  return MOE_FFN_OK;
+}
+
+int moe_ffn_attend(const moe_ffn_attend_args* a, moe_ffn_stream_t stream, void* workspace, size_t workspace_bytes,
+                   const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                   const int32_t* lens, const int32_t* q_start, const int32_t* mask, void* out, float* lse) {
+  int rc = check_attend(a);
+  if (rc != MOE_FFN_OK) return rc;
+  if (a->T == 0 || a->B == 0) return MOE_FFN_OK;
+  const bool cached = a->pages > 0 && a->max_pages > 0;
+  if (!workspace || !q || (cached && (!k_cache || !v_cache || !page_table)) || !lens || !q_start || !out)
+    return MOE_FFN_ERR_INVALID_ARG;
+  AttendParams P = {};
+  attend_sizes(a, P);
+  if (workspace_bytes < attend_workspace(P)) return MOE_FFN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256) || !aligned(q, 2) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(q_start, 4) || !aligned(mask, 4) ||
+      !elem_aligned(out, a->out_dtype) || !aligned(lse, 4))
+    return MOE_FFN_ERR_MISALIGNED;
+  rc = check_device(&P.sms);
+  if (rc != MOE_FFN_OK) return rc;
+  P.page_size = a->page_size;
+  P.pages = a->pages;
+  P.max_pages = cached ? a->max_pages : 0;
+  P.mask_words = a->mask_words;
+  P.scale = a->scale;
+  P.softcap = a->softcap;
+  P.q_stride = a->q_stride;
+  P.q_head = a->q_head_stride;
+  P.o_stride = a->out_stride;
+  P.o_head = a->out_head_stride;
+  P.kc_page = a->kc_page_stride;
+  P.kc_slot = a->kc_slot_stride;
+  P.kc_head = a->kc_head_stride;
+  P.vc_page = a->vc_page_stride;
+  P.vc_slot = a->vc_slot_stride;
+  P.vc_head = a->vc_head_stride;
+  P.table_stride = a->table_stride;
+  P.mask_stride = a->mask_stride;
+  P.q = static_cast<const uint16_t*>(q);
+  P.k = static_cast<const uint16_t*>(k_cache);
+  P.v = static_cast<const uint16_t*>(v_cache);
+  P.table = page_table;
+  P.lens = lens;
+  P.q_start = q_start;
+  P.mask = mask;
+  P.out = out;
+  P.lse = lse;
+  P.ws = workspace;
+  return cuda_status(launch_attend(P, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -335,4 +335,54 @@ struct AdapterParams {
 size_t adapters_workspace(int T, int K, int N, int R);
 cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream);
 
+// ---- the attention half of a block (moe_project.cu, moe_append.cu,
+// moe_attend.cu); fields as in the public argument blocks.
+constexpr int kMaxHeads = 65536;
+constexpr int kProjectMaxT = 1024;
+constexpr int kAppendMaxT = 1 << 24, kAppendMaxD = 512;
+constexpr int kAttendMaxT = 1 << 20, kAttendMaxB = 65536, kAttendMaxD = 256;
+constexpr int kAttendMaxGroup = 128;  // query heads a key head
+
+struct ProjectParams {
+  int T, K, N, group, sms;
+  int f16, y_dtype;
+  long long x_stride, y_stride, w_stride;
+  const uint16_t* x;
+  const uint8_t* w;
+  const float* bias;
+  void* y;
+};
+cudaError_t launch_project(ProjectParams p, cudaStream_t stream);
+
+struct AppendParams {
+  int T, Hq, Hkv, D, rot, sms;
+  int interleaved, x_dtype, q_dtype, c_dtype;
+  int page_size, slots;  // slots: of all pages
+  float scale;
+  long long q_stride, q_head, k_stride, k_head, v_stride, v_head, qo_stride, qo_head;
+  long long kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
+  const void *q, *k, *v;
+  const int32_t *positions, *slot;
+  const float* inv_freq;
+  void *q_out, *k_cache, *v_cache;
+};
+cudaError_t launch_append(AppendParams p, cudaStream_t stream);
+
+struct AttendParams {
+  int T, B, Hq, Hkv, G, D, sms;  // G query heads a key head
+  int f16, out_dtype;
+  int page_size, pages, max_pages, mask_words;
+  float scale, softcap;
+  long long q_stride, q_head, o_stride, o_head;
+  long long kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
+  long long table_stride, mask_stride;
+  const uint16_t *q, *k, *v;
+  const int32_t *table, *lens, *q_start, *mask;
+  void* out;
+  float* lse;
+  void* ws;
+};
+size_t attend_workspace(const AttendParams& p);
+cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
+
 }  // namespace moe

@@ -397,6 +397,115 @@ int moe_ffn_add_adapters(const moe_ffn_adapters_args* args, moe_ffn_stream_t str
                          size_t workspace_bytes, const void* x, const int32_t* adapter_ids, const void* A,
                          const void* B, const int32_t* ranks, const float* scales, const void* y, void* out);
 
+/* ---------------------------------------------------------------------------
+ * The attention half of a block, as calls of their own like those above:
+ * products with 4-bit weights, the append of keys and values to a paged cache
+ * and attention over that cache, for decode steps with drafted tokens.
+ */
+
+/*
+ * Product of few tokens with 4-bit weights:
+ *   y_tn = sum_k W_nk x_tk + bias_n,    W_nk = d_n,g(k) (c_nk - 8)
+ * Rows of W are those of MOE_FFN_W_Q4B32 with groups of `group` weights: K/2
+ * bytes of codes (element 2j in the low nibble of byte j), then K/group fp16
+ * scales; with group = 32 any stored matrix of the layer's 4-bit format is
+ * such a W.  Rows are w_stride bytes apart.
+ * x [T,K] bf16 or fp16, y [T,N] of any type, bias fp32 [N] or NULL.  Codes and
+ * x enter the products exactly; sums, scales and bias are in fp32, y is rounded
+ * once.  y overlaps no other tensor.
+ * x 16-byte aligned, its stride a multiple of 8; w 16-byte aligned, w_stride a
+ * multiple of 16.  T <= 1024, group 32, 64 or 128, K <= 65536 a multiple of
+ * group, 1 <= N <= 16777216.
+ */
+typedef struct {
+  int32_t T, K, N, group;
+  int32_t x_dtype;  /* MOE_FFN_ACT_BF16 or MOE_FFN_ACT_F16 */
+  int32_t y_dtype;  /* moe_ffn_act_dtype */
+  int64_t x_stride, y_stride;
+  int64_t w_stride; /* bytes */
+} moe_ffn_project_args;
+int moe_ffn_project(const moe_ffn_project_args* args, moe_ffn_stream_t stream, const void* x, const void* w,
+                    const float* bias, void* y);
+
+/*
+ * Keys and values of new tokens into a paged cache, rotated by their position
+ * on the way; the tokens' queries, rotated, beside them.  Per token t and head,
+ * with the angle th_i = positions_t inv_freq_i of pair i < rot / 2:
+ *   a' = scale (a cos th_i - b sin th_i),  b' = scale (a sin th_i + b cos th_i)
+ * (a, b) = elements (i, i + rot/2) of the head, or (2i, 2i + 1) if interleaved.
+ * Elements from rot on, and values, are taken as they are.  In fp32, rounded
+ * once; the angle is reduced exactly (positions over all of int32, inv_freq
+ * fp32 with |inv_freq| < 256; others give NaN).
+ * k, v [T,kv_heads,D] and q [T,q_heads,D] of x_dtype, q NULL: none.
+ * Caches: element (page, slot, head, d) of k at k_cache + page kc_page_stride +
+ * slot kc_slot_stride + head kc_head_stride + d, page < pages, slot <
+ * page_size; v likewise.
+ * slots int32 [T]: the token goes to page slots_t / page_size, slot slots_t %
+ * page_size.  A token whose slot is outside 0..pages page_size - 1 (-1 by
+ * convention) is padding: nothing is written for it, q_out neither.  Tokens of
+ * one call have different slots (where two have the same, either's elements may
+ * remain).
+ * q_out may be q (same dtype and strides); nothing else overlaps.
+ * T <= 16777216, 1 <= D <= 512, rot even, 0 <= rot <= D, heads <= 65536, pages
+ * page_size < 2^31.  Head strides are at least D.
+ */
+typedef struct {
+  int32_t T, q_heads, kv_heads, D, rot;
+  int32_t interleaved;
+  int32_t x_dtype, q_out_dtype, cache_dtype;  /* moe_ffn_act_dtype */
+  int32_t page_size, pages;
+  float scale;                                /* finite */
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+  int64_t q_out_stride, q_out_head_stride;
+  int64_t kc_page_stride, kc_slot_stride, kc_head_stride, vc_page_stride, vc_slot_stride, vc_head_stride;
+} moe_ffn_append_args;
+int moe_ffn_append_kv(const moe_ffn_append_args* args, moe_ffn_stream_t stream, const void* q, const void* k,
+                      const void* v, const int32_t* positions, const int32_t* slots, const float* inv_freq,
+                      void* q_out, void* k_cache, void* v_cache);
+
+/*
+ * Attention of B sequences' newest tokens over the paged cache that holds them:
+ * one token each, a tree of drafted tokens, or the end of a prompt.
+ * Sequence b has the rows t = q_start_b .. q_start_{b+1} - 1 of q, n of them;
+ * its cache holds lens_b tokens, the last n of which are these rows' own (row
+ * q_start_b + j is cached token lens_b - n + j).  Cached token i lies in page
+ * page_table[b][i / page_size], slot i % page_size.
+ *   s_ti   = scale q_t k_i;  softcap > 0: softcap tanh(s_ti / softcap)
+ *   out_t  = sum_i exp(s_ti) v_i / sum_i exp(s_ti),   lse_t = log sum_i exp(s_ti)
+ * over the tokens i that row t sees: all before the sequence's own n, and of
+ * those the j-th where bit j % 32 of mask[t][j / 32] is set; mask NULL: those up
+ * to the row's own.  Query head h reads key head h / (q_heads / kv_heads).
+ * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not
+ * see has no effect on it, infinities and NaN included.  Tokens of pages outside
+ * 0..pages - 1 are not seen.  lens is taken within 0..max_pages page_size,
+ * q_start within 0..T; rows of no sequence (padding behind the last) are left as
+ * they are, those of several get any of the results.
+ * q [T,q_heads,D] and the caches are bf16 or fp16 (dtype), out any type, lse
+ * fp32 [T,q_heads] or NULL.  Scores, statistics and sums are in fp32; weights
+ * enter the second product as the sum of two numbers of the cache's type (bf16
+ * with fp32 out: three).  Caches as in moe_ffn_append_kv, 16-byte aligned with
+ * strides that are multiples of 8.
+ * T <= 1048576, B <= 65536, q_heads a multiple of kv_heads and at most 128 kv_heads,
+ * D a multiple of 8 up to 256, pages page_size and max_pages page_size < 2^31.
+ * The workspace (256-byte aligned, scratch) holds what
+ * moe_ffn_attend_workspace reports; calls that overlap on the GPU need one each.
+ */
+typedef struct {
+  int32_t T, B, q_heads, kv_heads, D;
+  int32_t dtype;      /* MOE_FFN_ACT_BF16 or MOE_FFN_ACT_F16: q and the caches */
+  int32_t out_dtype;  /* moe_ffn_act_dtype */
+  int32_t page_size, pages, max_pages;
+  int32_t mask_words; /* int32 words a row of the mask */
+  float scale, softcap; /* finite, softcap >= 0 (0: no cap) */
+  int64_t q_stride, q_head_stride, out_stride, out_head_stride;
+  int64_t kc_page_stride, kc_slot_stride, kc_head_stride, vc_page_stride, vc_slot_stride, vc_head_stride;
+  int64_t table_stride, mask_stride;
+} moe_ffn_attend_args;
+int moe_ffn_attend_workspace(const moe_ffn_attend_args* args, size_t* bytes);
+int moe_ffn_attend(const moe_ffn_attend_args* args, moe_ffn_stream_t stream, void* workspace, size_t workspace_bytes,
+                   const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                   const int32_t* lens, const int32_t* q_start, const int32_t* mask, void* out, float* lse);
+
 /* Queries on a plan. */
 typedef enum {
   MOE_FFN_QUERY_PATH = 0,                 /* 0 = decode, 1 = grouped GEMM */
