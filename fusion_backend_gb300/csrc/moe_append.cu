@@ -6,6 +6,11 @@
 // integer position modulo 2^64, so that whole turns fall away by themselves: at
 // position 2^31 the error is 2^-33 turns.  (A product in fp32 has lost the angle
 // at position 2^24, and fp64 is slow on this GPU.)
+//
+// One block a token: its angles once, in shared memory, for all heads.  What the
+// heads hold is on its way meanwhile: a thread asks for its first two items before
+// the angles are formed.  An item is VEC elements, or VEC pairs whose halves lie
+// apart.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,7 +21,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
+constexpr int kAhead = 2;  // items a thread asks for at once
 
 // f / 2 pi modulo 1 in units of 2^-64.  |f| < 256.
 MOE_DEV uint64_t turn_fraction(float f) {
@@ -44,48 +50,200 @@ MOE_DEV float2 cos_sin(uint64_t phase) {
   return quarter & 2u ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// One block a token.
-__global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ AppendParams P) {
-  __shared__ float2 s_turn[kAppendMaxD / 2];
+// VEC elements as they lie in memory.
+template <int VEC>
+struct Raw {
+  uint4 w[VEC == 8 ? 2 : 1];
+};
+template <int VEC>
+MOE_DEV void raw_read(Raw<VEC>& r, const void* p, int dtype, size_t i) {
+  if constexpr (VEC == 8) {
+    if (dtype == kF32) {
+      const uint4* const a = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+      r.w[0] = a[0];
+      r.w[1] = a[1];
+    } else {
+      r.w[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    }
+  } else if constexpr (VEC == 4) {
+    r.w[0] = raw_load4(p, dtype, i);
+  } else {
+    r.w[0].x = raw_load(p, dtype, i);
+  }
+}
+template <int VEC>
+MOE_DEV void raw_floats(const Raw<VEC>& r, int dtype, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    if (dtype == kF32) {
+      raw_values4(r.w[0], kF32, v);
+      raw_values4(r.w[1], kF32, v + 4);
+    } else {
+      unpack2(dtype, r.w[0].x, v[0], v[1]);
+      unpack2(dtype, r.w[0].y, v[2], v[3]);
+      unpack2(dtype, r.w[0].z, v[4], v[5]);
+      unpack2(dtype, r.w[0].w, v[6], v[7]);
+    }
+  } else if constexpr (VEC == 4) {
+    raw_values4(r.w[0], dtype, v);
+  } else {
+    v[0] = raw_value(r.w[0].x, dtype);
+  }
+}
+template <int VEC>
+MOE_DEV void write_floats(void* p, int dtype, size_t i, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    if (dtype == kF32) {
+      elem_store4(p, kF32, i, v);
+      elem_store4(p, kF32, i + 4, v + 4);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+          make_uint4(pack2(dtype, v[0], v[1]), pack2(dtype, v[2], v[3]), pack2(dtype, v[4], v[5]), pack2(dtype, v[6], v[7]));
+    }
+  } else if constexpr (VEC == 4) {
+    elem_store4(p, dtype, i, v);
+  } else {
+    elem_store(p, dtype, i, v[0]);
+  }
+}
+
+// Where an item lies: `pair` elements behind its first half the second one
+// (0: none), its first pair of the angles (-1: taken as it is).
+struct Item {
+  const void* from;
+  void* to;
+  size_t at, out;
+  int dtype, pair, angle;
+};
+
+// VEC: elements an access; interleaved pairs with VEC 1 are two accesses too.
+template <int VEC>
+__global__ void __launch_bounds__(kMaxThreads) k_append(const __grid_constant__ AppendParams P) {
+  __shared__ __align__(16) float2 s_turn[kAppendMaxD / 2];
   const int tid = threadIdx.x, t = blockIdx.x;
   pdl_wait();
   const int slot = P.slot[t];
   if ((uint32_t)slot >= (uint32_t)P.slots) return;
-  const int half = P.rot / 2;
-  const long long pos = P.positions[t];
-  for (int i = tid; i < half; i += kThreads) {
-    const float f = P.inv_freq[i];
-    float2 cs = cos_sin(turn_fraction(f) * (uint64_t)pos);
-    const float scale = fabsf(f) < 256.f ? P.scale : __int_as_float(0x7FFFFFFF);
-    s_turn[i] = make_float2(cs.x * scale, cs.y * scale);
-  }
-  __syncthreads();
-  const int page = slot / P.page_size, at = slot % P.page_size;
-  auto rotate_head = [&](const void* x, size_t from, void* out, int dtype, size_t to) {
-    for (int i = tid; i < half; i += kThreads) {
-      const int a = P.interleaved ? 2 * i : i, b = P.interleaved ? 2 * i + 1 : i + half;
-      const float va = elem_load(x, P.x_dtype, from + a), vb = elem_load(x, P.x_dtype, from + b);
-      const float2 cs = s_turn[i];
-      elem_store(out, dtype, to + a, va * cs.x - vb * cs.y);
-      elem_store(out, dtype, to + b, va * cs.y + vb * cs.x);
+  const int half = P.rot / 2, page = slot / P.page_size, at = slot % P.page_size;
+  // items of a rotated head: pairs first, then what is not rotated
+  const bool apart = VEC == 1 || !P.interleaved;  // an item's pairs have their halves apart
+  const int pairs = apart ? half / VEC : P.rot / VEC, head_items = pairs + (P.D - P.rot) / VEC, v_items = P.D / VEC;
+  const int turned = (P.Hq + P.Hkv) * head_items, items = turned + P.Hkv * v_items;
+
+  auto find = [&](int i) {
+    Item m;
+    int h, j, d;
+    m.pair = 0;
+    m.angle = -1;
+    if (i < turned) {
+      h = i / head_items;
+      j = i - h * head_items;
+      if (j < pairs) {
+        m.angle = apart ? j * VEC : j * VEC / 2;
+        m.pair = !apart ? 0 : P.interleaved ? 1 : half;
+        d = VEC == 1 && P.interleaved ? 2 * j : j * VEC;
+      } else {
+        d = P.rot + (j - pairs) * VEC;
+      }
+    } else {
+      h = (i - turned) / v_items;
+      d = (i - turned - h * v_items) * VEC;
+      h += P.Hq + P.Hkv;
     }
-    for (int d = P.rot + tid; d < P.D; d += kThreads) elem_store(out, dtype, to + d, elem_load(x, P.x_dtype, from + d));
+    if (h < P.Hq) {
+      m.from = P.q, m.at = t * P.q_stride + h * P.q_head + d;
+      m.to = P.q_out, m.out = t * P.qo_stride + h * P.qo_head + d, m.dtype = P.q_dtype;
+    } else if (h < P.Hq + P.Hkv) {
+      h -= P.Hq;
+      m.from = P.k, m.at = t * P.k_stride + h * P.k_head + d;
+      m.to = P.k_cache, m.out = page * P.kc_page + at * P.kc_slot + h * P.kc_head + d, m.dtype = P.c_dtype;
+    } else {
+      h -= P.Hq + P.Hkv;
+      m.from = P.v, m.at = t * P.v_stride + h * P.v_head + d;
+      m.to = P.v_cache, m.out = page * P.vc_page + at * P.vc_slot + h * P.vc_head + d, m.dtype = P.c_dtype;
+    }
+    return m;
   };
-  for (int h = 0; h < P.Hq; ++h)
-    rotate_head(P.q, t * P.q_stride + h * P.q_head, P.q_out, P.q_dtype, t * P.qo_stride + h * P.qo_head);
-  for (int h = 0; h < P.Hkv; ++h) {
-    rotate_head(P.k, t * P.k_stride + h * P.k_head, P.k_cache, P.c_dtype,
-                page * P.kc_page + at * P.kc_slot + h * P.kc_head);
-    for (int d = tid; d < P.D; d += kThreads)
-      elem_store(P.v_cache, P.c_dtype, page * P.vc_page + at * P.vc_slot + h * P.vc_head + d,
-                 elem_load(P.v, P.x_dtype, t * P.v_stride + h * P.v_head + d));
+
+  bool first = true;
+  for (int i0 = tid; first || i0 < items; i0 += kAhead * blockDim.x) {
+    Item m[kAhead];
+    Raw<VEC> a[kAhead], b[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * blockDim.x;
+      if (i >= items) continue;
+      m[u] = find(i);
+      raw_read<VEC>(a[u], m[u].from, P.x_dtype, m[u].at);
+      if (m[u].pair) raw_read<VEC>(b[u], m[u].from, P.x_dtype, m[u].at + m[u].pair);
+    }
+    if (first) {
+      const long long pos = P.positions[t];
+      for (int i = tid; i < half; i += blockDim.x) {
+        const float f = P.inv_freq[i];
+        const float2 cs = cos_sin(turn_fraction(f) * (uint64_t)pos);
+        const float scale = fabsf(f) < 256.f ? P.scale : __int_as_float(0x7FFFFFFF);
+        s_turn[i] = make_float2(cs.x * scale, cs.y * scale);
+      }
+      __syncthreads();
+      first = false;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (i0 + u * blockDim.x >= items) continue;
+      float x[VEC], y[VEC];
+      raw_floats<VEC>(a[u], P.x_dtype, x);
+      if (m[u].pair) {
+        raw_floats<VEC>(b[u], P.x_dtype, y);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 cs = s_turn[m[u].angle + e];
+          const float v = x[e];
+          x[e] = v * cs.x - y[e] * cs.y;
+          y[e] = v * cs.y + y[e] * cs.x;
+        }
+        write_floats<VEC>(m[u].to, m[u].dtype, m[u].out + m[u].pair, y);
+      } else if (VEC > 1 && m[u].angle >= 0) {
+#pragma unroll
+        for (int e = 0; e + 1 < VEC; e += 2) {
+          const float2 cs = s_turn[m[u].angle + e / 2];
+          const float v = x[e];
+          x[e] = v * cs.x - x[e + 1] * cs.y;
+          x[e + 1] = v * cs.y + x[e + 1] * cs.x;
+        }
+      }
+      write_floats<VEC>(m[u].to, m[u].dtype, m[u].out, x);
+    }
   }
+}
+
+// Every tensor's rows allow accesses of vec elements.
+bool fits(const AppendParams& p, int vec) {
+  auto ok = [vec](const void* t, int dtype, long long a, long long b, long long c) {
+    // an access is 16 bytes at most (fp32: two of them)
+    const uintptr_t bytes = (uintptr_t)vec * elem_bytes(dtype);
+    return !t || (reinterpret_cast<uintptr_t>(t) % (bytes < 16 ? bytes : 16) == 0 && a % vec == 0 && b % vec == 0 &&
+                  c % vec == 0);
+  };
+  return p.D % vec == 0 && (p.interleaved ? p.rot : p.rot / 2) % vec == 0 && p.rot % vec == 0 &&
+         ok(p.q, p.x_dtype, p.q_stride, p.q_head, 0) && ok(p.k, p.x_dtype, p.k_stride, p.k_head, 0) &&
+         ok(p.v, p.x_dtype, p.v_stride, p.v_head, 0) && ok(p.q_out, p.q_dtype, p.qo_stride, p.qo_head, 0) &&
+         ok(p.k_cache, p.c_dtype, p.kc_page, p.kc_slot, p.kc_head) &&
+         ok(p.v_cache, p.c_dtype, p.vc_page, p.vc_slot, p.vc_head);
+}
+
+template <int VEC>
+cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
+  const int each = VEC > 1 && !p.interleaved ? 2 * VEC : VEC;
+  const int items = ((p.Hq + p.Hkv) * p.D + each - 1) / each + p.Hkv * p.D / VEC;
+  const int want = (items + kAhead - 1) / kAhead;
+  const int threads = want >= kMaxThreads ? kMaxThreads : want < 64 ? 64 : (want + 31) / 32 * 32;
+  return launch_behind(k_append<VEC>, dim3(p.T), threads, 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_append(AppendParams p, cudaStream_t stream) {
-  return launch_behind(k_append, dim3(p.T), kThreads, 0, stream, p);
+  return fits(p, 8) ? launch<8>(p, stream) : fits(p, 4) ? launch<4>(p, stream) : launch<1>(p, stream);
 }
 
 }  // namespace moe

@@ -1,78 +1,526 @@
 // Attention over a paged cache (moe_ffn_attend):
 //   out_t = sum_i exp(s_ti) v_i / sum_i exp(s_ti),  s_ti = cap(scale q_t k_i)
+// See moe_attend.cuh for the division of the work.
+//
+// k_attend, up to 16 rows a unit: bound by the stream of the cache.  Every warp
+// takes 16 tokens of a chunk at a time by itself, with a ring of its own in shared
+// memory that asynchronous copies fill ahead, across the ends of units too, and
+// with a running maximum, sum and output of its own: the warps meet only at the end
+// of a unit, and no barrier stands in the stream.  Scores and weighted values on
+// mma.m16n8k16, the rows being the rows; a weight enters the second product as the
+// sum of two or three numbers of the cache's type.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "moe_attend.cuh"
 #include "moe_elem.cuh"
 #include "moe_internal.h"
+#include "moe_mma.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTok = 16;  // tokens a warp and step
 
-// One warp a row and query head, its lanes over the elements of a head.
-__global__ void __launch_bounds__(128) k_attend(const __grid_constant__ AttendParams P) {
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y;
+__host__ __device__ constexpr int warps_for(int dp) { return dp <= 128 ? 8 : 4; }
+__host__ __device__ constexpr int stages_for(int dp) { return dp <= 64 ? 6 : dp == 192 ? 4 : 3; }
+__host__ __device__ constexpr int slot_bytes(int dp) { return 2 * kTok * dp * 2; }
+__host__ __device__ constexpr int attend_smem(int dp) {
+  return warps_for(dp) * stages_for(dp) * slot_bytes(dp) + 16 * dp * 2;
+}
+
+// Non-finite: all exponent bits set.
+template <bool F16>
+MOE_DEV bool odd16(uint32_t h) {
+  const uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  return (h & e) == e;
+}
+
+// DP: elements of a head in shared memory (D rounded up); TERMS: numbers that
+// stand for a weight.
+template <bool F16, int DP, int TERMS>
+__global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_constant__ AttendParams P) {
+  constexpr int W = warps_for(DP), S = stages_for(DP), kSlot = slot_bytes(DP), kChunks = DP / 8;
+  constexpr int NT = DP / 8, KS = DP / 16;
+  constexpr bool kHoldQ = DP <= 128;  // queries stay in registers
+  constexpr int kDt = F16 ? kF16 : kBf16;
+  // weights in fp16 are held 2^15 up, sums and outputs with them: two numbers then
+  // resolve 2^-40 of the largest weight (2^-25 without)
+  constexpr float kUp = F16 ? 15.f : 0.f;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ long long s_scan[40];
+  __shared__ float2 s_stat[W][16];
+  __shared__ uint32_t s_valid[W][S];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  uint8_t* const ring = smem + warp * S * kSlot;
+  const uint32_t ring_at = smem_u32(ring);
+  uint8_t* const qs = smem + W * S * kSlot;
+  const uint32_t q_at = smem_u32(qs);
   pdl_wait();
-  const int t_first = min(max(P.q_start[b], 0), P.T), t_end = min(max(P.q_start[b + 1], 0), P.T);
-  const int n = t_end - t_first;
-  const int len = (int)min((long long)max(P.lens[b], 0), (long long)P.max_pages * P.page_size);
-  const int dt = P.f16 ? kF16 : kBf16;
-  const int units = n * P.Hq;
-  for (int u = blockIdx.x * 4 + (threadIdx.x >> 5); u < units; u += gridDim.x * 4) {
-    const int j = u / P.Hq, h = u % P.Hq, t = t_first + j, hk = h / P.G;
-    float q[8], o[8], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < 8; ++e) {
-      const int d = lane + 32 * e;
-      q[e] = d < P.D ? elem_load(P.q, dt, (size_t)t * P.q_stride + h * P.q_head + d) : 0.f;
-      o[e] = 0.f;
-    }
-    for (int i = 0; i < len; ++i) {
-      const int own = i - (len - n);
-      if (own >= 0 && (P.mask ? own / 32 >= P.mask_words || !(P.mask[t * P.mask_stride + own / 32] >> own % 32 & 1)
-                              : own > j))
-        continue;
-      const int page = P.table[b * P.table_stride + i / P.page_size], at = i % P.page_size;
-      if ((uint32_t)page >= (uint32_t)P.pages) continue;
-      const size_t ka = page * P.kc_page + at * P.kc_slot + hk * P.kc_head;
-      const size_t va = page * P.vc_page + at * P.vc_slot + hk * P.vc_head;
-      float s = 0.f;
-      for (int e = 0; e < 8; ++e) {
-        const int d = lane + 32 * e;
-        if (d < P.D) s = fmaf(q[e], elem_load(P.k, dt, ka + d), s);
+  pdl_launch_dependents();
+  AttendStep now = attend_begin<32 * W>(P, s_scan);
+  if (now.left <= 0) return;
+  // columns that no copy writes
+  if (P.D < DP)
+    for (int i = tid * 16; i < W * S * kSlot; i += 32 * W * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+
+  const int pieces = P.D >> 3;
+  // the page of the step's tokens (of token lane % 16 where a step may hold several)
+  const bool one_page = P.page_size % kTok == 0;
+  AttendStep ahead = now;
+  int page_ahead = -1;
+  auto look = [&]() {  // the page of `ahead`
+    page_ahead = -1;
+    if (ahead.left <= 0) return;
+    const int i = ahead.chunk * (W * kTok) + warp * kTok + (one_page ? 0 : lane & 15);
+    if (i < ahead.s.len) page_ahead = P.table[ahead.b * P.table_stride + attend_page(P, i)];
+  };
+  auto load = [&](int stage) {  // the tokens of `ahead`, then the next step's page
+    if (ahead.left > 0) {
+      const int first = ahead.chunk * (W * kTok) + warp * kTok;
+      const uint32_t k_dst = ring_at + stage * kSlot, v_dst = k_dst + kSlot / 2;
+      const bool ok = (uint32_t)page_ahead < (uint32_t)P.pages;
+      if (one_page) {
+        const int count = ok ? min(max(ahead.s.len - first, 0), kTok) : 0;
+        const int slot = first - attend_page(P, first) * P.page_size;
+        const long long page = ok ? page_ahead : 0;
+        const uint16_t* const k = P.k + page * P.kc_page + (long long)slot * P.kc_slot + ahead.head * P.kc_head;
+        const uint16_t* const v = P.v + page * P.vc_page + (long long)slot * P.vc_slot + ahead.head * P.vc_head;
+        if (count > 0) {
+#pragma unroll
+          for (int j = 0; j < kTok * kChunks / 32; ++j) {
+            const int i = j * 32 + lane, r = i / kChunks, c = i % kChunks;
+            const bool on = r < count;
+            const uint32_t to = r * (DP * 2) + ((c ^ (r & 7)) << 4);
+            if (c < pieces) {
+              copy16(k_dst + to, on ? k + r * P.kc_slot + 8 * c : P.k, on ? 16u : 0u);
+              copy16(v_dst + to, on ? v + r * P.vc_slot + 8 * c : P.v, on ? 16u : 0u);
+            }
+          }
+        }
+        if (lane == 0) s_valid[warp][stage] = count >= kTok ? 0xFFFFu : (1u << count) - 1u;
+      } else {
+        const int i = first + (lane & 15);
+        const bool in = ok && i < ahead.s.len;
+        const uint32_t valid = __ballot_sync(kAll, in) & 0xFFFFu;
+        const int slot = in ? i - attend_page(P, i) * P.page_size : 0;
+        const long long page = in ? page_ahead : 0;
+        const long long k_off = page * P.kc_page + (long long)slot * P.kc_slot + ahead.head * P.kc_head;
+        const long long v_off = page * P.vc_page + (long long)slot * P.vc_slot + ahead.head * P.vc_head;
+        if (valid) {
+#pragma unroll
+          for (int j = 0; j < kTok * kChunks / 32; ++j) {
+            const int x = j * 32 + lane, r = x / kChunks, c = x % kChunks;
+            const long long ko = __shfl_sync(kAll, k_off, r), vo = __shfl_sync(kAll, v_off, r);
+            const bool on = valid >> r & 1u;
+            const uint32_t to = r * (DP * 2) + ((c ^ (r & 7)) << 4);
+            if (c < pieces) {
+              copy16(k_dst + to, on ? P.k + ko + 8 * c : P.k, on ? 16u : 0u);
+              copy16(v_dst + to, on ? P.v + vo + 8 * c : P.v, on ? 16u : 0u);
+            }
+          }
+        }
+        if (lane == 0) s_valid[warp][stage] = valid;
       }
-      for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(kAll, s, x);
-      s *= P.scale;
-      if (P.softcap > 0.f) s = P.softcap * tanhf(s / P.softcap);
-      const float m1 = fmaxf(m, s);
-      if (m1 == -INFINITY && s == s) continue;
-      const float old = m == -INFINITY ? 0.f : expf(m - m1), p = expf(s - m1);
-      l = l * old + p;
-      for (int e = 0; e < 8; ++e) {
-        const int d = lane + 32 * e;
-        if (d < P.D) o[e] = o[e] * old + p * elem_load(P.v, dt, va + d);
+      ahead.next(P);
+      look();
+    }
+    copy_commit();
+  };
+  look();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) load(s);
+
+  // (kept finite: 0 times infinity)
+  auto kept = [](float v) { return fminf(fmaxf(v, -3.4e38f), 3.4e38f); };
+  const float c1 = kept(P.softcap > 0.f ? P.scale / P.softcap * (2.f * kLog2e) : P.scale * kLog2e);
+  const float c2 = kept(P.softcap * kLog2e);
+  int stage = 0, stage_in = S - 1;
+  bool begin = true, from_start = false;
+  uint32_t qf[kHoldQ ? KS : 1][4];
+  float o[NT][4];
+  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // rows g and g + 8 (log2 units)
+  int row_t[2], row_j[2];                        // the rows' tokens (t: -1 behind the last)
+  while (now.left > 0) {
+    if (begin) {
+      begin = false;
+      from_start = now.chunk == 0;
+      // queries of the unit
+      const int rows = now.s.n * P.G, r0 = now.tile * 16;
+      for (int i = tid; i < 16 * DP; i += 32 * W) {
+        const int r = i / DP, d = i % DP;
+        uint16_t v = 0;
+        if (r0 + r < rows && d < P.D) {
+          const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
+          v = P.q[(long long)(now.s.t0 + j) * P.q_stride + h * P.q_head + d];
+        }
+        *reinterpret_cast<uint16_t*>(qs + r * (DP * 2) + (((d >> 3) ^ (r & 7)) << 4) + (d & 7) * 2) = v;
       }
-      m = m1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = r0 + g + 8 * x;
+        row_j[x] = r / P.G;
+        row_t[x] = r < rows ? now.s.t0 + row_j[x] : -1;
+      }
+      __syncthreads();
+      if constexpr (kHoldQ) {
+        const int r = lane & 15;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) ldmatrix4(qf[s], q_at + r * (DP * 2) + (((2 * s + (lane >> 4)) ^ (r & 7)) << 4));
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
     }
-    for (int e = 0; e < 8; ++e) {
-      const int d = lane + 32 * e;
-      if (d < P.D)
-        elem_store(P.out, P.out_dtype, (size_t)t * P.o_stride + h * P.o_head + d, l == 0.f ? 0.f : o[e] / l);
+    copy_wait<S - 2>();
+    __syncwarp();
+    load(stage_in);
+    stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
+    const uint32_t valid = s_valid[warp][stage];
+    if (valid) {
+      const uint32_t k_at = ring_at + stage * kSlot, v_at = k_at + kSlot / 2;
+      float s[2][4] = {};
+      {
+        const int r = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b[4];
+          ldmatrix4(b, k_at + r * (DP * 2) + (((2 * ks + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+          if constexpr (kHoldQ) {
+            mma16<F16>(s[0], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b[0], b[1]);
+            mma16<F16>(s[1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b[2], b[3]);
+          } else {
+            uint32_t a[4];
+            const int qr = lane & 15;
+            ldmatrix4(a, q_at + qr * (DP * 2) + (((2 * ks + (lane >> 4)) ^ (qr & 7)) << 4));
+            mma16<F16>(s[0], a[0], a[1], a[2], a[3], b[0], b[1]);
+            mma16<F16>(s[1], a[0], a[1], a[2], a[3], b[2], b[3]);
+          }
+        }
+      }
+      if (P.softcap > 0.f) {
+        // tanh(x) = 1 - 2 / (exp(2 x) + 1): off by some 2^-23 of the cap
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = c2 * (1.f - __fdividef(2.f, exp2_fast(s[n][e] * c1) + 1.f));
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] *= c1;
+      }
+      const int first = now.chunk * (W * kTok) + warp * kTok, own = first - (now.s.len - now.s.n);
+      bool odd_tile = false;
+      if (valid != 0xFFFFu || own + kTok > 0) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 8 * n + 2 * q + (e & 1), x = e >> 1;
+            const bool on = (valid >> i & 1u) && row_t[x] >= 0 && attend_sees(P, row_t[x], row_j[x], own + i);
+            if (!on) s[n][e] = -INFINITY;
+          }
+        // values that a row does not see have no effect on it: a product with a
+        // weight of 0 has, where they are not finite.  They are taken out of the tile
+        // and added to the rows that see them.
+        bool odd = false;
+        for (int i = lane; i < kTok * kChunks; i += 32) {
+          const uint4 v = *reinterpret_cast<const uint4*>(ring + stage * kSlot + kSlot / 2 + 16 * i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) odd |= odd16<F16>(w[x] & 0xFFFFu) || odd16<F16>(w[x] >> 16);
+        }
+        odd_tile = __any_sync(kAll, odd);
+      }
+      // running maximum and sum
+      float a0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+      float a1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) {
+        a0 = fmaxf(a0, __shfl_xor_sync(kAll, a0, x));
+        a1 = fmaxf(a1, __shfl_xor_sync(kAll, a1, x));
+      }
+      if (__any_sync(kAll, a0 > m0 || a1 > m1)) {
+        a0 = fmaxf(a0, m0);
+        a1 = fmaxf(a1, m1);
+        const float f0 = exp2_fast(m0 - attend_base(a0)), f1 = exp2_fast(m1 - attend_base(a1));
+        m0 = a0;
+        m1 = a1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[n][0] *= f0;
+          o[n][1] *= f0;
+          o[n][2] *= f1;
+          o[n][3] *= f1;
+        }
+      }
+      if (odd_tile) {
+        for (int i = 0; i < kTok; ++i) {
+          bool sees[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            sees[x] = (valid >> i & 1u) && row_t[x] >= 0 && attend_sees(P, row_t[x], row_j[x], own + i);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + stage * kSlot + kSlot / 2 + i * (DP * 2) +
+                                                                  ((n ^ (i & 7)) << 4) + 4 * q);
+            float v[2];
+            unpack2(kDt, w, v[0], v[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (odd16<F16>(e & 1 ? w >> 16 : w & 0xFFFFu) && sees[e >> 1]) o[n][e] += v[e & 1];
+          }
+        }
+        __syncwarp();
+        for (int i = lane; i < kTok * DP; i += 32) {
+          uint16_t* const at = reinterpret_cast<uint16_t*>(ring + stage * kSlot + kSlot / 2) + i;
+          if (odd16<F16>(*at)) *at = 0;
+        }
+        __syncwarp();
+      }
+      const float b0 = attend_base(m0) - kUp, b1 = attend_base(m1) - kUp;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = exp2_fast(s[n][0] - b0);
+        s[n][1] = exp2_fast(s[n][1] - b0);
+        s[n][2] = exp2_fast(s[n][2] - b1);
+        s[n][3] = exp2_fast(s[n][3] - b1);
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
+      }
+      // a weight = the sum of TERMS numbers, each the rest rounded
+      uint32_t p[TERMS][4];
+#pragma unroll
+      for (int x = 0; x < TERMS; ++x)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t w = pack2(kDt, s[n][2 * e], s[n][2 * e + 1]);
+            p[x][2 * n + e] = w;
+            if (x + 1 < TERMS) {
+              float lo, hi;
+              unpack2(kDt, w, lo, hi);
+              s[n][2 * e] -= lo;
+              s[n][2 * e + 1] -= hi;
+            }
+          }
+      const int r = (lane & 7) + (lane & 8);
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b[4];
+        ldmatrix4_trans(b, v_at + r * (DP * 2) + (((n + (lane >> 4)) ^ (r & 7)) << 4));
+#pragma unroll
+        for (int x = TERMS - 1; x >= 0; --x) {
+          mma16<F16>(o[n], p[x][0], p[x][1], p[x][2], p[x][3], b[0], b[1]);
+          mma16<F16>(o[n + 1], p[x][0], p[x][1], p[x][2], p[x][3], b[2], b[3]);
+        }
+      }
     }
-    if (P.lse && lane == 0) P.lse[(size_t)t * P.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+    const bool end = now.chunk + 1 == now.s.chunks;
+    if (end || now.left == 1) {
+      // the warps' sums meet: each leaves its own in the slot that it has just used
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) {
+        l0 += __shfl_xor_sync(kAll, l0, x);
+        l1 += __shfl_xor_sync(kAll, l1, x);
+      }
+      __syncwarp();
+      float* const left = reinterpret_cast<float*>(ring + stage * kSlot);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2*>(left + g * DP + 8 * n + 2 * q) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(left + (g + 8) * DP + 8 * n + 2 * q) = make_float2(o[n][2], o[n][3]);
+      }
+      if (q == 0) {
+        s_stat[warp][g] = make_float2(m0 - kUp, l0);
+        s_stat[warp][g + 8] = make_float2(m1 - kUp, l1);
+      }
+      __syncthreads();
+      const bool whole = from_start && end;
+      const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+      const int rows = now.s.n * P.G, r0 = now.tile * 16;
+      for (int i = tid; i < 16 * (DP / 4); i += 32 * W) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (r0 + r >= rows || d >= P.D) continue;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) m = fmaxf(m, s_stat[w][r].x);
+        const float base = attend_base(m);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float2 st = s_stat[w][r];
+          const float f = exp2_fast(st.x - base);
+          const float4 a = *reinterpret_cast<const float4*>(smem + (w * S + stage) * kSlot + (r * DP + d) * 4);
+          l = fmaf(st.y, f, l);
+          v.x = fmaf(a.x, f, v.x);
+          v.y = fmaf(a.y, f, v.y);
+          v.z = fmaf(a.z, f, v.z);
+          v.w = fmaf(a.w, f, v.w);
+        }
+        if (!whole) {
+          *reinterpret_cast<float4*>(P.part + ((long long)slot * 16 + r) * P.width + d) = v;
+          if (d == 0) P.stat[slot * 16 + r] = make_float2(m, l);
+          continue;
+        }
+        const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
+        const long long t = now.s.t0 + j;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          elem_store(P.out, P.out_dtype, t * P.o_stride + h * P.o_head + d + e, l == 0.f ? 0.f : y[e] * inv);
+        if (d == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      __syncthreads();
+      // (padded columns of the next use of the slot are 0 again)
+      if (P.D < DP)
+        for (int i = lane; i < kSlot / 16; i += 32) *reinterpret_cast<uint4*>(ring + stage * kSlot + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+      begin = true;
+    }
+    stage = stage + 1 == S ? 0 : stage + 1;
+    now.next(P);
   }
+  copy_wait<0>();
+}
+
+// Joins the parts of a unit: block (c, y) those of the unit that goes on in block
+// c's range, if it began in the range before it, for a share of its rows.  With few
+// parts a warp a row, else all warps a row.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_constant__ AttendParams P) {
+  __shared__ float s_o[kJoinWarps][kAttendMaxD];
+  __shared__ float s_l[kJoinWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+  pdl_wait();
+  const AttendFrom at = P.from[c];
+  const long long total = at.total, from = attend_from(total, c, P.blocks);
+  if (at.chunk == 0 || from == attend_from(total, c + 1, P.blocks)) return;
+  // the range before this one (where there are fewer chunks than blocks, ranges between may be empty)
+  int c0 = c - 1;
+  while (c0 > 0 && attend_from(total, c0, P.blocks) == from) --c0;
+  const long long unit = from - at.chunk;
+  if (unit < attend_from(total, c0, P.blocks)) return;
+  const AttendSeq s = attend_seq(P, at.b);
+  const int c1 = attend_block_of(total, unit + s.chunks - 1, P.blocks);
+  const int rows = min(s.n * P.G - at.tile * P.rows, P.rows), each = P.rows / gridDim.y;
+  const bool together = each == 1 || c1 - c0 >= 2 * kJoinWarps;
+  // the first part begins its unit, the others go on
+  auto has = [&](int i) { return attend_from(total, i + 1, P.blocks) > attend_from(total, i, P.blocks); };
+  for (int r = blockIdx.y * each + (together ? 0 : warp); r < min(rows, (int)(blockIdx.y + 1) * each);
+       r += together ? 1 : kJoinWarps) {
+    auto slot_of = [&](int i) { return (long long)(i == c0 ? 2 * c0 + 1 : 2 * i) * P.rows + r; };
+    float m = -INFINITY;
+    for (int i = c0 + lane; i <= c1; i += 32)
+      if (has(i)) m = fmaxf(m, P.stat[slot_of(i)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    const float base = attend_base(m);
+    float l = 0.f, acc[kAttendMaxD / 32] = {};
+#pragma unroll 4
+    for (int i = c0 + (together ? warp : 0); i <= c1; i += together ? kJoinWarps : 1) {
+      if (!has(i)) continue;
+      const float2 st = P.stat[slot_of(i)];
+      const float f = exp2_fast(st.x - base);
+      l = fmaf(st.y, f, l);
+      const float* const row = P.part + slot_of(i) * P.width;
+#pragma unroll
+      for (int e = 0; e < kAttendMaxD / 32; ++e)
+        if (lane + 32 * e < P.D) acc[e] = fmaf(row[lane + 32 * e], f, acc[e]);
+    }
+    const int in = at.tile * P.rows + r, j = in / P.G, h = at.head * P.G + in - j * P.G;
+    const long long t = s.t0 + j, out = t * P.o_stride + h * P.o_head;
+    if (!together) {
+#pragma unroll
+      for (int e = 0; e < kAttendMaxD / 32; ++e)
+        if (lane + 32 * e < P.D)
+          elem_store(P.out, P.out_dtype, out + lane + 32 * e, l == 0.f ? 0.f : acc[e] / l);
+      if (lane == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < kAttendMaxD / 32; ++e) s_o[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
+    for (int d = tid; d < P.D; d += 32 * kJoinWarps) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][d];
+      elem_store(P.out, P.out_dtype, out + d, l == 0.f ? 0.f : v / l);
+    }
+    if (tid == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    __syncthreads();
+  }
+}
+
+constexpr int kMaxBlocks = kMaxGrid;  // the workspace does not depend on the device
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+int width_for(int D) { return (D + 63) / 64 * 64; }
+
+template <bool F16, int DP, int TERMS>
+cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+  auto* const kern = k_attend<F16, DP, TERMS>;
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), attend_smem(DP));
+  if (e != cudaSuccess) return e;
+  return launch_behind(kern, dim3(p.blocks), 32 * warps_for(DP), attend_smem(DP), stream, p);
+}
+
+template <bool F16, int TERMS>
+cudaError_t launch_width(const AttendParams& p, cudaStream_t stream) {
+  return p.D <= 64    ? launch<F16, 64, TERMS>(p, stream)
+         : p.D <= 128 ? launch<F16, 128, TERMS>(p, stream)
+         : p.D <= 192 ? launch<F16, 192, TERMS>(p, stream)
+                      : launch<F16, 256, TERMS>(p, stream);
 }
 
 }  // namespace
 
-size_t attend_workspace(const AttendParams& p) { return 256; }
+cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream) {
+  return launch_behind(k_attend_join, dim3(p.blocks, p.rows < 32 ? p.rows : 32), 32 * kJoinWarps, 0, stream, p);
+}
+
+size_t attend_workspace(const AttendParams& p) {
+  const size_t rows = 16;
+  return align256(kMaxBlocks * sizeof(AttendFrom)) + align256((size_t)2 * kMaxBlocks * rows * 8) +
+         (size_t)2 * kMaxBlocks * rows * width_for(p.D) * 4;
+}
 
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
-  const int units = (p.T * p.Hq + 3) / 4;
-  return launch_behind(k_attend, dim3(units < 1024 ? units : 1024, p.B), 128, 0, stream, p);
+  p.blocks = p.sms;
+  p.rows = 16;
+  const int dp = width_for(p.D);
+  p.chunk = warps_for(dp) * kTok;
+  p.width = dp;
+  uint8_t* w = static_cast<uint8_t*>(p.ws);
+  p.from = reinterpret_cast<AttendFrom*>(w);
+  w += align256(kMaxBlocks * sizeof(AttendFrom));
+  p.stat = reinterpret_cast<float2*>(w);
+  w += align256((size_t)2 * kMaxBlocks * p.rows * 8);
+  p.part = reinterpret_cast<float*>(w);
+  // floor(i / d) for i < 2^31: i ceil(2^(32 + s) / d) >> (32 + s), 2^s >= d
+  int s = 0;
+  while ((1ll << s) < p.page_size) ++s;
+  p.page_shift = 32 + s;
+  p.page_mul = (unsigned long long)((((unsigned __int128)1 << (32 + s)) + p.page_size - 1) / p.page_size);
+  const bool f32 = p.out_dtype == kF32;
+  const cudaError_t e = p.f16 ? launch_width<true, 2>(p, stream)
+                        : f32 ? launch_width<false, 3>(p, stream)
+                              : launch_width<false, 2>(p, stream);
+  return e != cudaSuccess ? e : launch_attend_join(p, stream);
 }
 
 }  // namespace moe

@@ -1,0 +1,167 @@
+// What the kernels of attention over a paged cache (moe_ffn_attend) share: the
+// sequences, the division of the work over the blocks, the partial results.
+//
+// A unit is a tile of rows of one sequence and one key head: its rows are the
+// pairs (drafted token j, query head g of the group), r = j G + g.  Its work is the
+// sequence's cached tokens in chunks.  All units' chunks, one behind the other, are
+// divided evenly over the blocks, whatever the lengths: a block takes a range of
+// chunks, which ends or begins inside a unit where it has to.  A unit that one
+// block has whole is finished by it; the parts of another go to the workspace, at
+// most two a block (the one that goes on in its first unit, the one that begins in
+// its last), and a second kernel joins them.  The division depends on the lengths
+// alone, and parts are joined in their order: results repeat bit for bit.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_elem.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+struct AttendSeq {
+  int t0, n, len;     // first row, rows, cached tokens
+  int tiles, chunks;  // of rows, of tokens
+  MOE_DEV long long work(int heads) const { return (long long)tiles * heads * chunks; }
+};
+
+MOE_DEV AttendSeq attend_seq(const AttendParams& P, int b) {
+  AttendSeq s;
+  s.t0 = min(max(P.q_start[b], 0), P.T);
+  s.n = max(min(P.q_start[b + 1], P.T) - s.t0, 0);
+  const long long most = (long long)P.max_pages * P.page_size;
+  s.len = (int)min((long long)max(P.lens[b], 0), most);
+  s.tiles = (s.n * P.G + P.rows - 1) / P.rows;
+  s.chunks = (int)(((long long)s.len + P.chunk - 1) / P.chunk);
+  return s;
+}
+
+// First chunk of block c's range out of `total`.
+__host__ __device__ inline long long attend_from(long long total, int c, int blocks) {
+  return total / blocks * c + (total % blocks * c) / blocks;
+}
+// The block whose range holds chunk w.
+MOE_DEV int attend_block_of(long long total, long long w, int blocks) {
+  int c = (int)min((long long)(blocks - 1), (long long)((double)w / (double)total * blocks));
+  while (c > 0 && attend_from(total, c, blocks) > w) --c;
+  while (c + 1 < blocks && attend_from(total, c + 1, blocks) <= w) ++c;
+  return c;
+}
+
+// i / page_size.
+MOE_DEV int attend_page(const AttendParams& P, int i) {
+  return (int)(((unsigned long long)(uint32_t)i * P.page_mul) >> P.page_shift);
+}
+
+// A step of a block's range: one chunk of one unit.
+struct AttendStep {
+  AttendSeq s;
+  int b, head, tile, chunk;
+  long long left;  // steps to the end of the range, this one included
+  MOE_DEV void next(const AttendParams& P) {
+    --left;
+    if (++chunk < s.chunks) return;
+    chunk = 0;
+    if (++tile < s.tiles) return;
+    tile = 0;
+    if (++head < P.Hkv) return;
+    head = 0;
+    while (left > 0 && ++b < P.B) {
+      s = attend_seq(P, b);
+      if (s.work(P.Hkv) > 0) break;
+    }
+  }
+};
+
+// What the second kernel has to know of a block's range: where it begins.
+struct AttendFrom {
+  long long total;
+  int b, head, tile, chunk;
+};
+
+// The range of this block: its first step, also left in the workspace.  All
+// threads of the block call it; scratch: THREADS / 32 + 2 words.  Rows of sequences
+// without tokens belong to no unit: the blocks write their results here, in turn.
+template <int THREADS>
+MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int W = THREADS / 32;
+  auto work_of = [&](int b) { return b < P.B ? attend_seq(P, b).work(P.Hkv) : 0ll; };
+  // the thread's sequences behind one another, THREADS at a time
+  const long long own = work_of(tid);
+  long long sum = own;
+  for (int b = tid + THREADS; b < P.B; b += THREADS) sum += work_of(b);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) total += scratch[w];
+  const long long from = attend_from(total, blockIdx.x, gridDim.x), to = attend_from(total, blockIdx.x + 1, gridDim.x);
+  long long base = 0;
+  for (int b0 = 0; b0 < P.B && from < to && base <= from; b0 += THREADS) {
+    const int b = b0 + tid;
+    const long long mine = b0 == 0 ? own : work_of(b);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = upto;
+    __syncthreads();
+    long long before = base;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      before += w < warp ? scratch[w] : 0ll;
+      base += scratch[w];
+    }
+    upto += before;
+    if (upto - mine <= from && from < upto) {
+      scratch[W] = b;
+      scratch[W + 1] = from - (upto - mine);
+    }
+  }
+  __syncthreads();
+  AttendStep a = {};
+  a.left = to - from;
+  if (a.left > 0) {
+    a.b = (int)scratch[W];
+    a.s = attend_seq(P, a.b);
+    const long long at = scratch[W + 1], unit = at / a.s.chunks;
+    a.chunk = (int)(at - unit * a.s.chunks);
+    a.head = (int)(unit / a.s.tiles);
+    a.tile = (int)(unit - (long long)a.head * a.s.tiles);
+  }
+  if (tid == 0) P.from[blockIdx.x] = AttendFrom{total, a.b, a.head, a.tile, a.chunk};
+  for (int b = blockIdx.x + gridDim.x * tid; b < P.B; b += gridDim.x * THREADS) {
+    const AttendSeq s = attend_seq(P, b);
+    if (s.chunks > 0) continue;
+    for (int t = s.t0; t < s.t0 + s.n; ++t)
+      for (int h = 0; h < P.Hq; ++h) {
+        for (int d = 0; d < P.D; ++d) elem_store(P.out, P.out_dtype, t * P.o_stride + h * P.o_head + d, 0.f);
+        if (P.lse) P.lse[(long long)t * P.Hq + h] = -INFINITY;
+      }
+  }
+  return a;
+}
+
+// Whether row t, the j-th of its sequence, sees the token `own` places behind the
+// first of the sequence's own ones.
+MOE_DEV bool attend_sees(const AttendParams& P, int t, int j, int own) {
+  if (own < 0) return true;
+  if (!P.mask) return own <= j;
+  return (own >> 5) < P.mask_words && (P.mask[(long long)t * P.mask_stride + (own >> 5)] >> (own & 31) & 1);
+}
+
+// The largest running maximum is taken for 0 where there is none, so that
+// exp2(-inf - 0) = 0.
+MOE_DEV float attend_base(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Joins the parts of the units that several blocks share (moe_attend.cu).
+cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream);
+
+}  // namespace moe

@@ -337,7 +337,7 @@ cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream);
 
 // ---- the attention half of a block (moe_project.cu, moe_append.cu,
 // moe_attend.cu); fields as in the public argument blocks.
-constexpr int kMaxHeads = 65536;
+constexpr int kMaxHeads = 65535;
 constexpr int kProjectMaxT = 1024;
 constexpr int kAppendMaxT = 1 << 24, kAppendMaxD = 512;
 constexpr int kAttendMaxT = 1 << 20, kAttendMaxB = 65536, kAttendMaxD = 256;
@@ -345,6 +345,7 @@ constexpr int kAttendMaxGroup = 128;  // query heads a key head
 
 struct ProjectParams {
   int T, K, N, group, sms;
+  int k_warps;  // set by the launch: warps of a block over K
   int f16, y_dtype;
   long long x_stride, y_stride, w_stride;
   const uint16_t* x;
@@ -368,6 +369,7 @@ struct AppendParams {
 };
 cudaError_t launch_append(AppendParams p, cudaStream_t stream);
 
+struct AttendFrom;
 struct AttendParams {
   int T, B, Hq, Hkv, G, D, sms;  // G query heads a key head
   int f16, out_dtype;
@@ -380,7 +382,16 @@ struct AttendParams {
   const int32_t *table, *lens, *q_start, *mask;
   void* out;
   float* lse;
+  // set by the launch: blocks, rows and tokens of a unit's steps, columns of a
+  // part's row, i / page_size = i page_mul >> page_shift
+  int blocks, rows, chunk, width, page_shift;
+  unsigned long long page_mul;
+  // workspace: where the blocks' ranges begin, the parts' sums [2 blocks][rows]
+  // [width] and their maximum and sum of weights [2 blocks][rows]
   void* ws;
+  AttendFrom* from;
+  float* part;
+  float2* stat;
 };
 size_t attend_workspace(const AttendParams& p);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
