@@ -7,10 +7,11 @@
 // position 2^31 the error is 2^-33 turns.  (A product in fp32 has lost the angle
 // at position 2^24, and fp64 is slow on this GPU.)
 //
-// One block a token: its angles once, in shared memory, for all heads.  What the
-// heads hold is on its way meanwhile: a thread asks for its first two items before
-// the angles are formed.  An item is VEC elements, or VEC pairs whose halves lie
-// apart.
+// A block takes some neighbouring tokens: their angles once, in shared memory, for
+// all heads.  What the heads hold is on its way meanwhile: a thread asks for its
+// items of all the block's tokens before the angles are formed.  An item is VEC
+// elements, or VEC pairs whose halves lie apart; where it lies in a head is found
+// once for all tokens.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,7 +23,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kAhead = 2;  // items a thread asks for at once
 
 // f / 2 pi modulo 1 in units of 2^-64.  |f| < 256.
 MOE_DEV uint64_t turn_fraction(float f) {
@@ -50,47 +50,44 @@ MOE_DEV float2 cos_sin(uint64_t phase) {
   return quarter & 2u ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// VEC elements as they lie in memory.
-template <int VEC>
+// VEC elements as they lie in memory, fp32 or 16-bit ones.
+template <int VEC, bool F32>
 struct Raw {
-  uint4 w[VEC == 8 ? 2 : 1];
+  uint4 w[VEC == 8 && F32 ? 2 : 1];
 };
-template <int VEC>
-MOE_DEV void raw_read(Raw<VEC>& r, const void* p, int dtype, size_t i) {
-  if constexpr (VEC == 8) {
-    if (dtype == kF32) {
-      const uint4* const a = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-      r.w[0] = a[0];
-      r.w[1] = a[1];
-    } else {
-      r.w[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    }
+template <int VEC, bool F32>
+MOE_DEV void raw_read(Raw<VEC, F32>& r, const void* p, long long i) {
+  constexpr int kAny = F32 ? kF32 : kBf16;
+  if constexpr (VEC == 8 && F32) {
+    const uint4* const a = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    r.w[0] = a[0];
+    r.w[1] = a[1];
+  } else if constexpr (VEC == 8) {
+    r.w[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
   } else if constexpr (VEC == 4) {
-    r.w[0] = raw_load4(p, dtype, i);
+    r.w[0] = raw_load4(p, kAny, i);
   } else {
-    r.w[0].x = raw_load(p, dtype, i);
+    r.w[0].x = raw_load(p, kAny, i);
+  }
+}
+template <int VEC, bool F32>
+MOE_DEV void raw_floats(const Raw<VEC, F32>& r, int dtype, float (&v)[VEC]) {
+  if constexpr (VEC == 8 && F32) {
+    raw_values4(r.w[0], kF32, v);
+    raw_values4(r.w[1], kF32, v + 4);
+  } else if constexpr (VEC == 8) {
+    unpack2(dtype, r.w[0].x, v[0], v[1]);
+    unpack2(dtype, r.w[0].y, v[2], v[3]);
+    unpack2(dtype, r.w[0].z, v[4], v[5]);
+    unpack2(dtype, r.w[0].w, v[6], v[7]);
+  } else if constexpr (VEC == 4) {
+    raw_values4(r.w[0], F32 ? kF32 : dtype, v);
+  } else {
+    v[0] = raw_value(r.w[0].x, F32 ? kF32 : dtype);
   }
 }
 template <int VEC>
-MOE_DEV void raw_floats(const Raw<VEC>& r, int dtype, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    if (dtype == kF32) {
-      raw_values4(r.w[0], kF32, v);
-      raw_values4(r.w[1], kF32, v + 4);
-    } else {
-      unpack2(dtype, r.w[0].x, v[0], v[1]);
-      unpack2(dtype, r.w[0].y, v[2], v[3]);
-      unpack2(dtype, r.w[0].z, v[4], v[5]);
-      unpack2(dtype, r.w[0].w, v[6], v[7]);
-    }
-  } else if constexpr (VEC == 4) {
-    raw_values4(r.w[0], dtype, v);
-  } else {
-    v[0] = raw_value(r.w[0].x, dtype);
-  }
-}
-template <int VEC>
-MOE_DEV void write_floats(void* p, int dtype, size_t i, const float (&v)[VEC]) {
+MOE_DEV void write_floats(void* p, int dtype, long long i, const float (&v)[VEC]) {
   if constexpr (VEC == 8) {
     if (dtype == kF32) {
       elem_store4(p, kF32, i, v);
@@ -106,112 +103,111 @@ MOE_DEV void write_floats(void* p, int dtype, size_t i, const float (&v)[VEC]) {
   }
 }
 
-// Where an item lies: `pair` elements behind its first half the second one
-// (0: none), its first pair of the angles (-1: taken as it is).
-struct Item {
-  const void* from;
-  void* to;
-  size_t at, out;
-  int dtype, pair, angle;
-};
-
-// VEC: elements an access; interleaved pairs with VEC 1 are two accesses too.
-template <int VEC>
+// VEC: elements an access.  TB: tokens a block.
+template <int VEC, bool F32, int TB>
 __global__ void __launch_bounds__(kMaxThreads) k_append(const __grid_constant__ AppendParams P) {
-  __shared__ __align__(16) float2 s_turn[kAppendMaxD / 2];
-  const int tid = threadIdx.x, t = blockIdx.x;
+  __shared__ __align__(16) float2 s_turn[TB][kAppendMaxD / 2];
+  const int tid = threadIdx.x, t0 = blockIdx.x * TB, tokens = TB == 1 ? 1 : min(TB, P.T - t0);
   pdl_wait();
-  const int slot = P.slot[t];
-  if ((uint32_t)slot >= (uint32_t)P.slots) return;
-  const int half = P.rot / 2, page = slot / P.page_size, at = slot % P.page_size;
+  int slot[TB];
+#pragma unroll
+  for (int u = 0; u < TB; ++u) slot[u] = u < tokens ? P.slot[t0 + u] : -1;
+  const int half = P.rot / 2;
   // items of a rotated head: pairs first, then what is not rotated
   const bool apart = VEC == 1 || !P.interleaved;  // an item's pairs have their halves apart
   const int pairs = apart ? half / VEC : P.rot / VEC, head_items = pairs + (P.D - P.rot) / VEC, v_items = P.D / VEC;
   const int turned = (P.Hq + P.Hkv) * head_items, items = turned + P.Hkv * v_items;
 
-  auto find = [&](int i) {
-    Item m;
-    int h, j, d;
-    m.pair = 0;
-    m.angle = -1;
-    if (i < turned) {
-      h = i / head_items;
-      j = i - h * head_items;
-      if (j < pairs) {
-        m.angle = apart ? j * VEC : j * VEC / 2;
-        m.pair = !apart ? 0 : P.interleaved ? 1 : half;
-        d = VEC == 1 && P.interleaved ? 2 * j : j * VEC;
-      } else {
-        d = P.rot + (j - pairs) * VEC;
-      }
-    } else {
-      h = (i - turned) / v_items;
-      d = (i - turned - h * v_items) * VEC;
-      h += P.Hq + P.Hkv;
-    }
-    if (h < P.Hq) {
-      m.from = P.q, m.at = t * P.q_stride + h * P.q_head + d;
-      m.to = P.q_out, m.out = t * P.qo_stride + h * P.qo_head + d, m.dtype = P.q_dtype;
-    } else if (h < P.Hq + P.Hkv) {
-      h -= P.Hq;
-      m.from = P.k, m.at = t * P.k_stride + h * P.k_head + d;
-      m.to = P.k_cache, m.out = page * P.kc_page + at * P.kc_slot + h * P.kc_head + d, m.dtype = P.c_dtype;
-    } else {
-      h -= P.Hq + P.Hkv;
-      m.from = P.v, m.at = t * P.v_stride + h * P.v_head + d;
-      m.to = P.v_cache, m.out = page * P.vc_page + at * P.vc_slot + h * P.vc_head + d, m.dtype = P.c_dtype;
-    }
-    return m;
-  };
-
   bool first = true;
-  for (int i0 = tid; first || i0 < items; i0 += kAhead * blockDim.x) {
-    Item m[kAhead];
-    Raw<VEC> a[kAhead], b[kAhead];
+  for (int i = tid; first || i < items; i += blockDim.x) {
+    // where the item lies: element d of a head, its second half `pair` elements
+    // behind (0: none), its first pair's angle (-1: taken as it is)
+    const void* from = nullptr;
+    void* to = nullptr;
+    long long at = 0, step = 0, head = 0;
+    int d = 0, pair = 0, angle = -1, kind = 0;  // kind: 0 query, 1 key, 2 value
+    const bool on = i < items;
+    if (on) {
+      int h;
+      if (i < turned) {
+        h = i / head_items;
+        const int j = i - h * head_items;
+        if (j < pairs) {
+          angle = apart ? j * VEC : j * VEC / 2;
+          pair = !apart ? 0 : P.interleaved ? 1 : half;
+          d = VEC == 1 && P.interleaved ? 2 * j : j * VEC;
+        } else {
+          d = P.rot + (j - pairs) * VEC;
+        }
+      } else {
+        h = (i - turned) / v_items;
+        d = (i - turned - h * v_items) * VEC;
+        h += P.Hq + P.Hkv;
+      }
+      if (h < P.Hq) {
+        from = P.q, step = P.q_stride, at = h * P.q_head, to = P.q_out, head = h * P.qo_head + d;
+      } else if (h < P.Hq + P.Hkv) {
+        h -= P.Hq;
+        kind = 1;
+        from = P.k, step = P.k_stride, at = h * P.k_head, to = P.k_cache, head = h * P.kc_head + d;
+      } else {
+        h -= P.Hq + P.Hkv;
+        kind = 2;
+        from = P.v, step = P.v_stride, at = h * P.v_head, to = P.v_cache, head = h * P.vc_head + d;
+      }
+      at += t0 * step + d;
+    }
+    Raw<VEC, F32> a[TB], b[TB];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * blockDim.x;
-      if (i >= items) continue;
-      m[u] = find(i);
-      raw_read<VEC>(a[u], m[u].from, P.x_dtype, m[u].at);
-      if (m[u].pair) raw_read<VEC>(b[u], m[u].from, P.x_dtype, m[u].at + m[u].pair);
+    for (int u = 0; u < TB; ++u) {
+      if (!on || u >= tokens) continue;
+      raw_read<VEC, F32>(a[u], from, at + u * step);
+      if (pair) raw_read<VEC, F32>(b[u], from, at + u * step + pair);
     }
     if (first) {
-      const long long pos = P.positions[t];
-      for (int i = tid; i < half; i += blockDim.x) {
-        const float f = P.inv_freq[i];
-        const float2 cs = cos_sin(turn_fraction(f) * (uint64_t)pos);
+      for (int x = tid; x < half * tokens; x += blockDim.x) {
+        const int u = x / half, p = x - u * half;
+        const float f = P.inv_freq[p];
+        const float2 cs = cos_sin(turn_fraction(f) * (uint64_t)(long long)P.positions[t0 + u]);
         const float scale = fabsf(f) < 256.f ? P.scale : __int_as_float(0x7FFFFFFF);
-        s_turn[i] = make_float2(cs.x * scale, cs.y * scale);
+        s_turn[u][p] = make_float2(cs.x * scale, cs.y * scale);
       }
       __syncthreads();
       first = false;
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (i0 + u * blockDim.x >= items) continue;
+    for (int u = 0; u < TB; ++u) {
+      if (!on || (uint32_t)slot[u] >= (uint32_t)P.slots) continue;
       float x[VEC], y[VEC];
-      raw_floats<VEC>(a[u], P.x_dtype, x);
-      if (m[u].pair) {
-        raw_floats<VEC>(b[u], P.x_dtype, y);
+      raw_floats<VEC, F32>(a[u], P.x_dtype, x);
+      const int dtype = kind == 0 ? P.q_dtype : P.c_dtype;
+      long long out = head;
+      if (kind == 0) {
+        out += (t0 + u) * P.qo_stride;
+      } else {
+        const int page = slot[u] / P.page_size, in = slot[u] - page * P.page_size;
+        out += page * (kind == 1 ? P.kc_page : P.vc_page) + in * (kind == 1 ? P.kc_slot : P.vc_slot);
+      }
+      if (pair) {
+        raw_floats<VEC, F32>(b[u], P.x_dtype, y);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float2 cs = s_turn[m[u].angle + e];
+          const float2 cs = s_turn[u][angle + e];
           const float v = x[e];
           x[e] = v * cs.x - y[e] * cs.y;
           y[e] = v * cs.y + y[e] * cs.x;
         }
-        write_floats<VEC>(m[u].to, m[u].dtype, m[u].out + m[u].pair, y);
-      } else if (VEC > 1 && m[u].angle >= 0) {
+        write_floats<VEC>(to, dtype, out + pair, y);
+      } else if (VEC > 1 && angle >= 0) {
 #pragma unroll
         for (int e = 0; e + 1 < VEC; e += 2) {
-          const float2 cs = s_turn[m[u].angle + e / 2];
+          const float2 cs = s_turn[u][angle + e / 2];
           const float v = x[e];
           x[e] = v * cs.x - x[e + 1] * cs.y;
           x[e + 1] = v * cs.y + x[e + 1] * cs.x;
         }
       }
-      write_floats<VEC>(m[u].to, m[u].dtype, m[u].out, x);
+      write_floats<VEC>(to, dtype, out, x);
     }
   }
 }
@@ -231,19 +227,25 @@ bool fits(const AppendParams& p, int vec) {
          ok(p.v_cache, p.c_dtype, p.vc_page, p.vc_slot, p.vc_head);
 }
 
-template <int VEC>
+template <int VEC, bool F32>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
   const int each = VEC > 1 && !p.interleaved ? 2 * VEC : VEC;
   const int items = ((p.Hq + p.Hkv) * p.D + each - 1) / each + p.Hkv * p.D / VEC;
-  const int want = (items + kAhead - 1) / kAhead;
-  const int threads = want >= kMaxThreads ? kMaxThreads : want < 64 ? 64 : (want + 31) / 32 * 32;
-  return launch_behind(k_append<VEC>, dim3(p.T), threads, 0, stream, p);
+  const int threads = items >= kMaxThreads ? kMaxThreads : items < 64 ? 64 : (items + 31) / 32 * 32;
+  constexpr int kMany = F32 ? 2 : 4;
+  if (p.T < kMany * 2 * p.sms) return launch_behind(k_append<VEC, F32, 1>, dim3(p.T), threads, 0, stream, p);
+  return launch_behind(k_append<VEC, F32, kMany>, dim3((p.T + kMany - 1) / kMany), threads, 0, stream, p);
+}
+
+template <int VEC>
+cudaError_t launch_type(const AppendParams& p, cudaStream_t stream) {
+  return p.x_dtype == kF32 ? launch<VEC, true>(p, stream) : launch<VEC, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_append(AppendParams p, cudaStream_t stream) {
-  return fits(p, 8) ? launch<8>(p, stream) : fits(p, 4) ? launch<4>(p, stream) : launch<1>(p, stream);
+  return fits(p, 8) ? launch_type<8>(p, stream) : fits(p, 4) ? launch_type<4>(p, stream) : launch_type<1>(p, stream);
 }
 
 }  // namespace moe

@@ -17,6 +17,7 @@
 #include "moe_elem.cuh"
 #include "moe_internal.h"
 #include "moe_mma.cuh"
+#include "moe_tma.cuh"
 
 namespace moe {
 
@@ -30,8 +31,11 @@ __host__ __device__ constexpr int warps_for(int dp) { return dp <= 128 ? 8 : 4; 
 __host__ __device__ constexpr int stages_for(int dp) { return dp <= 64 ? 6 : dp == 192 ? 4 : 3; }
 __host__ __device__ constexpr int slot_bytes(int dp) { return 2 * kTok * dp * 2; }
 __host__ __device__ constexpr int attend_smem(int dp) {
-  return warps_for(dp) * stages_for(dp) * slot_bytes(dp) + 16 * dp * 2;
+  return warps_for(dp) * stages_for(dp) * (slot_bytes(dp) + 8) + 16 * dp * 2 + 1024;  // (slots at multiples of 1024)
 }
+// Byte of 16-byte piece c of row r in a tile of keys or values: 64 columns are
+// 128 bytes of a row, swizzled; the next 64 lie behind all rows.
+MOE_DEV uint32_t piece(int r, int c) { return (c >> 3) * (kTok * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
 // Non-finite: all exponent bits set.
 template <bool F16>
@@ -42,42 +46,55 @@ MOE_DEV bool odd16(uint32_t h) {
 
 // DP: elements of a head in shared memory (D rounded up); TERMS: numbers that
 // stand for a weight.
-template <bool F16, int DP, int TERMS>
+// PAGED: 16 tokens lie in one page, which tensor copies fetch; else asynchronous
+// copies by the lanes, each token from a page of its own.
+template <bool F16, int DP, int TERMS, bool PAGED>
 __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_constant__ AttendParams P) {
   constexpr int W = warps_for(DP), S = stages_for(DP), kSlot = slot_bytes(DP), kChunks = DP / 8;
   constexpr int NT = DP / 8, KS = DP / 16;
   constexpr bool kHoldQ = DP <= 128;  // queries stay in registers
   constexpr int kDt = F16 ? kF16 : kBf16;
-  // weights in fp16 are held 2^15 up, sums and outputs with them: two numbers then
-  // resolve 2^-40 of the largest weight (2^-25 without)
-  constexpr float kUp = F16 ? 15.f : 0.f;
-  extern __shared__ __align__(1024) uint8_t smem[];
+  // The maximum of the sums stays while scores pass it by no more than 2^8, so that
+  // the output is hardly ever scaled anew.  Weights in fp16 are held 2^7 up, sums and
+  // outputs with them: they stay below 2^15, and two numbers resolve 2^-32 of that
+  // maximum's weight (2^-25 without).
+  constexpr float kLazy = 8.f, kUp = F16 ? 7.f : 0.f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ long long s_scan[40];
   __shared__ float2 s_stat[W][16];
   __shared__ uint32_t s_valid[W][S];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   uint8_t* const ring = smem + warp * S * kSlot;
   const uint32_t ring_at = smem_u32(ring);
-  uint8_t* const qs = smem + W * S * kSlot;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + W * S * kSlot) + warp * S;
+  uint8_t* const qs = smem + W * S * (kSlot + 8);
   const uint32_t q_at = smem_u32(qs);
+  if (PAGED && lane == 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) mbar_init(full + s, 1);
+    mbar_fence_init();
+    prefetch_tensormap(&P.tm_k);
+    prefetch_tensormap(&P.tm_v);
+  }
   pdl_wait();
   pdl_launch_dependents();
   AttendStep now = attend_begin<32 * W>(P, s_scan);
   if (now.left <= 0) return;
   // columns that no copy writes
-  if (P.D < DP)
+  if (!PAGED && P.D < DP)
     for (int i = tid * 16; i < W * S * kSlot; i += 32 * W * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 
   const int pieces = P.D >> 3;
   // the page of the step's tokens (of token lane % 16 where a step may hold several)
-  const bool one_page = P.page_size % kTok == 0;
   AttendStep ahead = now;
   int page_ahead = -1;
+  const uint64_t once = policy_evict_first(), again = policy_evict_last();
   auto look = [&]() {  // the page of `ahead`
     page_ahead = -1;
     if (ahead.left <= 0) return;
-    const int i = ahead.chunk * (W * kTok) + warp * kTok + (one_page ? 0 : lane & 15);
+    const int i = ahead.chunk * (W * kTok) + warp * kTok + (PAGED ? 0 : lane & 15);
     if (i < ahead.s.len) page_ahead = P.table[ahead.b * P.table_stride + attend_page(P, i)];
   };
   auto load = [&](int stage) {  // the tokens of `ahead`, then the next step's page
@@ -85,25 +102,28 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       const int first = ahead.chunk * (W * kTok) + warp * kTok;
       const uint32_t k_dst = ring_at + stage * kSlot, v_dst = k_dst + kSlot / 2;
       const bool ok = (uint32_t)page_ahead < (uint32_t)P.pages;
-      if (one_page) {
+      if constexpr (PAGED) {
         const int count = ok ? min(max(ahead.s.len - first, 0), kTok) : 0;
-        const int slot = first - attend_page(P, first) * P.page_size;
-        const long long page = ok ? page_ahead : 0;
-        const uint16_t* const k = P.k + page * P.kc_page + (long long)slot * P.kc_slot + ahead.head * P.kc_head;
-        const uint16_t* const v = P.v + page * P.vc_page + (long long)slot * P.vc_slot + ahead.head * P.vc_head;
-        if (count > 0) {
+        if (lane == 0) {
+          if (count > 0) {
+            const int slot = first - attend_page(P, first) * P.page_size;
+            // keys and values are read again where a sequence has further tiles of rows
+            const uint64_t policy = ahead.s.tiles > 1 ? again : once;
+            const int x1 = P.slot_first ? slot : ahead.head, x2 = P.slot_first ? ahead.head : slot;
+            mbar_arrive_expect_tx(full + stage, kSlot);
 #pragma unroll
-          for (int j = 0; j < kTok * kChunks / 32; ++j) {
-            const int i = j * 32 + lane, r = i / kChunks, c = i % kChunks;
-            const bool on = r < count;
-            const uint32_t to = r * (DP * 2) + ((c ^ (r & 7)) << 4);
-            if (c < pieces) {
-              copy16(k_dst + to, on ? k + r * P.kc_slot + 8 * c : P.k, on ? 16u : 0u);
-              copy16(v_dst + to, on ? v + r * P.vc_slot + 8 * c : P.v, on ? 16u : 0u);
-            }
+            for (int c = 0; c < DP / 64; ++c)
+              tensor_load_4d(ring + stage * kSlot + c * kTok * 128, &P.tm_k, 64 * c, x1, x2, page_ahead, full + stage,
+                             policy);
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c)
+              tensor_load_4d(ring + stage * kSlot + kSlot / 2 + c * kTok * 128, &P.tm_v, 64 * c, x1, x2, page_ahead,
+                             full + stage, policy);
+          } else {
+            mbar_arrive(full + stage);
           }
+          s_valid[warp][stage] = count >= kTok ? 0xFFFFu : (1u << count) - 1u;
         }
-        if (lane == 0) s_valid[warp][stage] = count >= kTok ? 0xFFFFu : (1u << count) - 1u;
       } else {
         const int i = first + (lane & 15);
         const bool in = ok && i < ahead.s.len;
@@ -118,7 +138,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
             const int x = j * 32 + lane, r = x / kChunks, c = x % kChunks;
             const long long ko = __shfl_sync(kAll, k_off, r), vo = __shfl_sync(kAll, v_off, r);
             const bool on = valid >> r & 1u;
-            const uint32_t to = r * (DP * 2) + ((c ^ (r & 7)) << 4);
+            const uint32_t to = piece(r, c);
             if (c < pieces) {
               copy16(k_dst + to, on ? P.k + ko + 8 * c : P.k, on ? 16u : 0u);
               copy16(v_dst + to, on ? P.v + vo + 8 * c : P.v, on ? 16u : 0u);
@@ -130,7 +150,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       ahead.next(P);
       look();
     }
-    copy_commit();
+    if (!PAGED) copy_commit();
   };
   look();
 #pragma unroll
@@ -138,10 +158,12 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
 
   // (kept finite: 0 times infinity)
   auto kept = [](float v) { return fminf(fmaxf(v, -3.4e38f), 3.4e38f); };
-  const float c1 = kept(P.softcap > 0.f ? P.scale / P.softcap * (2.f * kLog2e) : P.scale * kLog2e);
+  const float c1 = kept(P.softcap > 0.f ? P.scale / P.softcap : P.scale * kLog2e);
   const float c2 = kept(P.softcap * kLog2e);
   int stage = 0, stage_in = S - 1;
+  uint32_t parity = 0;
   bool begin = true, from_start = false;
+  bool dead = false;  // a copy never came: results are NaN
   uint32_t qf[kHoldQ ? KS : 1][4];
   float o[NT][4];
   float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // rows g and g + 8 (log2 units)
@@ -152,14 +174,22 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       from_start = now.chunk == 0;
       // queries of the unit
       const int rows = now.s.n * P.G, r0 = now.tile * 16;
-      for (int i = tid; i < 16 * DP; i += 32 * W) {
-        const int r = i / DP, d = i % DP;
-        uint16_t v = 0;
-        if (r0 + r < rows && d < P.D) {
+      for (int i = tid; i < 16 * kChunks; i += 32 * W) {
+        const int r = i / kChunks, c = i % kChunks;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r0 + r < rows && 8 * c < P.D) {
           const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
-          v = P.q[(long long)(now.s.t0 + j) * P.q_stride + h * P.q_head + d];
+          const uint16_t* const from = P.q + (long long)(now.s.t0 + j) * P.q_stride + h * P.q_head + 8 * c;
+          if (P.q_vec) {
+            v = *reinterpret_cast<const uint4*>(from);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = from[2 * e] | (uint32_t)from[2 * e + 1] << 16;
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        *reinterpret_cast<uint16_t*>(qs + r * (DP * 2) + (((d >> 3) ^ (r & 7)) << 4) + (d & 7) * 2) = v;
+        *reinterpret_cast<uint4*>(qs + r * (DP * 2) + ((c ^ (r & 7)) << 4)) = v;
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -178,10 +208,11 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
     }
-    copy_wait<S - 2>();
+    if (!PAGED) copy_wait<S - 2>();
     __syncwarp();
     load(stage_in);
     stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
+    if (PAGED && !dead) dead = !mbar_wait(full + stage, parity);
     const uint32_t valid = s_valid[warp][stage];
     if (valid) {
       const uint32_t k_at = ring_at + stage * kSlot, v_at = k_at + kSlot / 2;
@@ -191,7 +222,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t b[4];
-          ldmatrix4(b, k_at + r * (DP * 2) + (((2 * ks + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+          ldmatrix4(b, k_at + piece(r, 2 * ks + ((lane >> 3) & 1)));
           if constexpr (kHoldQ) {
             mma16<F16>(s[0], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b[0], b[1]);
             mma16<F16>(s[1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b[2], b[3]);
@@ -205,11 +236,10 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         }
       }
       if (P.softcap > 0.f) {
-        // tanh(x) = 1 - 2 / (exp(2 x) + 1): off by some 2^-23 of the cap
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = c2 * (1.f - __fdividef(2.f, exp2_fast(s[n][e] * c1) + 1.f));
+          for (int e = 0; e < 4; ++e) s[n][e] = c2 * attend_tanh(s[n][e] * c1);
       } else {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -247,7 +277,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         a0 = fmaxf(a0, __shfl_xor_sync(kAll, a0, x));
         a1 = fmaxf(a1, __shfl_xor_sync(kAll, a1, x));
       }
-      if (__any_sync(kAll, a0 > m0 || a1 > m1)) {
+      if (__any_sync(kAll, a0 > m0 + kLazy || a1 > m1 + kLazy)) {
         a0 = fmaxf(a0, m0);
         a1 = fmaxf(a1, m1);
         const float f0 = exp2_fast(m0 - attend_base(a0)), f1 = exp2_fast(m1 - attend_base(a1));
@@ -271,8 +301,8 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
             sees[x] = (valid >> i & 1u) && row_t[x] >= 0 && attend_sees(P, row_t[x], row_j[x], own + i);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + stage * kSlot + kSlot / 2 + i * (DP * 2) +
-                                                                  ((n ^ (i & 7)) << 4) + 4 * q);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + stage * kSlot + kSlot / 2 + piece(i, n) +
+                                                                  4 * q);
             float v[2];
             unpack2(kDt, w, v[0], v[1]);
 #pragma unroll
@@ -285,6 +315,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
           uint16_t* const at = reinterpret_cast<uint16_t*>(ring + stage * kSlot + kSlot / 2) + i;
           if (odd16<F16>(*at)) *at = 0;
         }
+        fence_proxy_async();
         __syncwarp();
       }
       const float b0 = attend_base(m0) - kUp, b1 = attend_base(m1) - kUp;
@@ -318,7 +349,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         uint32_t b[4];
-        ldmatrix4_trans(b, v_at + r * (DP * 2) + (((n + (lane >> 4)) ^ (r & 7)) << 4));
+        ldmatrix4_trans(b, v_at + piece(r, n + (lane >> 4)));
 #pragma unroll
         for (int x = TERMS - 1; x >= 0; --x) {
           mma16<F16>(o[n], p[x][0], p[x][1], p[x][2], p[x][3], b[0], b[1]);
@@ -342,8 +373,9 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         *reinterpret_cast<float2*>(left + (g + 8) * DP + 8 * n + 2 * q) = make_float2(o[n][2], o[n][3]);
       }
       if (q == 0) {
-        s_stat[warp][g] = make_float2(m0 - kUp, l0);
-        s_stat[warp][g + 8] = make_float2(m1 - kUp, l1);
+        const float none = __int_as_float(0x7FFFFFFF);
+        s_stat[warp][g] = make_float2(m0 - kUp, dead ? none : l0);
+        s_stat[warp][g + 8] = make_float2(m1 - kUp, dead ? none : l1);
       }
       __syncthreads();
       const bool whole = from_start && end;
@@ -382,16 +414,20 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
           elem_store(P.out, P.out_dtype, t * P.o_stride + h * P.o_head + d + e, l == 0.f ? 0.f : y[e] * inv);
         if (d == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
+      fence_proxy_async();
       __syncthreads();
       // (padded columns of the next use of the slot are 0 again)
-      if (P.D < DP)
+      if (!PAGED && P.D < DP)
         for (int i = lane; i < kSlot / 16; i += 32) *reinterpret_cast<uint4*>(ring + stage * kSlot + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
       begin = true;
     }
-    stage = stage + 1 == S ? 0 : stage + 1;
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1u;
+    }
     now.next(P);
   }
-  copy_wait<0>();
+  if (!PAGED) copy_wait<0>();
 }
 
 // Joins the parts of a unit: block (c, y) those of the unit that goes on in block
@@ -404,32 +440,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   pdl_wait();
   const AttendFrom at = P.from[c];
-  const long long total = at.total, from = attend_from(total, c, P.blocks);
-  if (at.chunk == 0 || from == attend_from(total, c + 1, P.blocks)) return;
-  // the range before this one (where there are fewer chunks than blocks, ranges between may be empty)
-  int c0 = c - 1;
-  while (c0 > 0 && attend_from(total, c0, P.blocks) == from) --c0;
-  const long long unit = from - at.chunk;
-  if (unit < attend_from(total, c0, P.blocks)) return;
-  const AttendSeq s = attend_seq(P, at.b);
-  const int c1 = attend_block_of(total, unit + s.chunks - 1, P.blocks);
-  const int rows = min(s.n * P.G - at.tile * P.rows, P.rows), each = P.rows / gridDim.y;
-  const bool together = each == 1 || c1 - c0 >= 2 * kJoinWarps;
+  if (at.chunk == 0) return;
+  const long long unit = at.share.from(c) - at.chunk;
+  if (unit < at.share.from(c - 1)) return;
   // the first part begins its unit, the others go on
-  auto has = [&](int i) { return attend_from(total, i + 1, P.blocks) > attend_from(total, i, P.blocks); };
+  const int c0 = c - 1, c1 = at.share.block_of(unit + at.chunks - 1);
+  const int rows = min(at.n * P.G - at.tile * P.rows, P.rows), each = P.rows / gridDim.y;
+  const bool together = each == 1 || c1 - c0 >= 2 * kJoinWarps;
   for (int r = blockIdx.y * each + (together ? 0 : warp); r < min(rows, (int)(blockIdx.y + 1) * each);
        r += together ? 1 : kJoinWarps) {
     auto slot_of = [&](int i) { return (long long)(i == c0 ? 2 * c0 + 1 : 2 * i) * P.rows + r; };
     float m = -INFINITY;
-    for (int i = c0 + lane; i <= c1; i += 32)
-      if (has(i)) m = fmaxf(m, P.stat[slot_of(i)].x);
+    for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, P.stat[slot_of(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     const float base = attend_base(m);
     float l = 0.f, acc[kAttendMaxD / 32] = {};
 #pragma unroll 4
     for (int i = c0 + (together ? warp : 0); i <= c1; i += together ? kJoinWarps : 1) {
-      if (!has(i)) continue;
       const float2 st = P.stat[slot_of(i)];
       const float f = exp2_fast(st.x - base);
       l = fmaf(st.y, f, l);
@@ -439,7 +467,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
         if (lane + 32 * e < P.D) acc[e] = fmaf(row[lane + 32 * e], f, acc[e]);
     }
     const int in = at.tile * P.rows + r, j = in / P.G, h = at.head * P.G + in - j * P.G;
-    const long long t = s.t0 + j, out = t * P.o_stride + h * P.o_head;
+    const long long t = at.t0 + j, out = t * P.o_stride + h * P.o_head;
     if (!together) {
 #pragma unroll
       for (int e = 0; e < kAttendMaxD / 32; ++e)
@@ -470,21 +498,46 @@ constexpr int kMaxBlocks = kMaxGrid;  // the workspace does not depend on the de
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 int width_for(int D) { return (D + 63) / 64 * 64; }
 
-template <bool F16, int DP, int TERMS>
+// The cache as (column, head, slot, page) or (column, slot, head, page), by their
+// strides, in boxes of 64 columns of 16 tokens of a head.
+bool encode_cache(CUtensorMap* m, const AttendParams& p, const uint16_t* base, long long page, long long slot,
+                  long long head) {
+  const auto encode = tensor_map_encoder();
+  if (!encode || 2 * page >= 1ll << 40 || 2 * slot >= 1ll << 40 || 2 * head >= 1ll << 40) return false;
+  const cuuint64_t heads = p.Hkv, slots = p.page_size;
+  const bool sf = p.slot_first;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, sf ? slots : heads, sf ? heads : slots, (cuuint64_t)p.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)(2 * (sf ? slot : head)), (cuuint64_t)(2 * (sf ? head : slot)),
+                                 (cuuint64_t)(2 * page)};
+  const cuuint32_t box[4] = {64, sf ? kTok : 1u, sf ? 1u : kTok, 1}, ones[4] = {1, 1, 1, 1};
+  return encode(m, p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<uint16_t*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool F16, int DP, int TERMS, bool PAGED>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
-  auto* const kern = k_attend<F16, DP, TERMS>;
+  static_assert(attend_smem(DP) <= 229376, "shared memory");
+  auto* const kern = k_attend<F16, DP, TERMS, PAGED>;
   static SmemLimit limit;
   const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), attend_smem(DP));
   if (e != cudaSuccess) return e;
   return launch_behind(kern, dim3(p.blocks), 32 * warps_for(DP), attend_smem(DP), stream, p);
 }
 
-template <bool F16, int TERMS>
+template <bool F16, int TERMS, bool PAGED>
 cudaError_t launch_width(const AttendParams& p, cudaStream_t stream) {
-  return p.D <= 64    ? launch<F16, 64, TERMS>(p, stream)
-         : p.D <= 128 ? launch<F16, 128, TERMS>(p, stream)
-         : p.D <= 192 ? launch<F16, 192, TERMS>(p, stream)
-                      : launch<F16, 256, TERMS>(p, stream);
+  return p.D <= 64    ? launch<F16, 64, TERMS, PAGED>(p, stream)
+         : p.D <= 128 ? launch<F16, 128, TERMS, PAGED>(p, stream)
+         : p.D <= 192 ? launch<F16, 192, TERMS, PAGED>(p, stream)
+                      : launch<F16, 256, TERMS, PAGED>(p, stream);
+}
+
+template <bool PAGED>
+cudaError_t launch_terms(const AttendParams& p, cudaStream_t stream) {
+  if (p.f16) return launch_width<true, 2, PAGED>(p, stream);
+  return p.out_dtype == kF32 ? launch_width<false, 3, PAGED>(p, stream) : launch_width<false, 2, PAGED>(p, stream);
 }
 
 }  // namespace
@@ -516,10 +569,11 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   while ((1ll << s) < p.page_size) ++s;
   p.page_shift = 32 + s;
   p.page_mul = (unsigned long long)((((unsigned __int128)1 << (32 + s)) + p.page_size - 1) / p.page_size);
-  const bool f32 = p.out_dtype == kF32;
-  const cudaError_t e = p.f16 ? launch_width<true, 2>(p, stream)
-                        : f32 ? launch_width<false, 3>(p, stream)
-                              : launch_width<false, 2>(p, stream);
+  p.q_vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0 && p.q_head % 8 == 0;
+  p.slot_first = p.kc_slot < p.kc_head;
+  const bool paged = p.page_size % kTok == 0 && p.pages > 0 && encode_cache(&p.tm_k, p, p.k, p.kc_page, p.kc_slot, p.kc_head) &&
+                     encode_cache(&p.tm_v, p, p.v, p.vc_page, p.vc_slot, p.vc_head);
+  const cudaError_t e = paged ? launch_terms<true>(p, stream) : launch_terms<false>(p, stream);
   return e != cudaSuccess ? e : launch_attend_join(p, stream);
 }
 

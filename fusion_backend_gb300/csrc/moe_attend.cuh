@@ -17,6 +17,7 @@
 
 #include "moe_elem.cuh"
 #include "moe_internal.h"
+#include "moe_mma.cuh"
 
 namespace moe {
 
@@ -37,17 +38,16 @@ MOE_DEV AttendSeq attend_seq(const AttendParams& P, int b) {
   return s;
 }
 
-// First chunk of block c's range out of `total`.
-__host__ __device__ inline long long attend_from(long long total, int c, int blocks) {
-  return total / blocks * c + (total % blocks * c) / blocks;
-}
-// The block whose range holds chunk w.
-MOE_DEV int attend_block_of(long long total, long long w, int blocks) {
-  int c = (int)min((long long)(blocks - 1), (long long)((double)w / (double)total * blocks));
-  while (c > 0 && attend_from(total, c, blocks) > w) --c;
-  while (c + 1 < blocks && attend_from(total, c + 1, blocks) <= w) ++c;
-  return c;
-}
+// All chunks over the blocks: `base` each, one more for the first `rest`.
+struct AttendShare {
+  long long base;
+  int rest;
+  MOE_DEV long long from(int c) const { return base * c + min(c, rest); }
+  MOE_DEV int block_of(long long w) const {  // whose range holds chunk w
+    const long long more = (base + 1) * rest;
+    return (int)(w < more ? w / (base + 1) : rest + (w - more) / base);
+  }
+};
 
 // i / page_size.
 MOE_DEV int attend_page(const AttendParams& P, int i) {
@@ -74,10 +74,11 @@ struct AttendStep {
   }
 };
 
-// What the second kernel has to know of a block's range: where it begins.
+// What the second kernel has to know of a block's range: where it begins (chunk 0:
+// not inside a unit, or no range).
 struct AttendFrom {
-  long long total;
-  int b, head, tile, chunk;
+  AttendShare share;
+  int t0, n, chunks, head, tile, chunk;
 };
 
 // The range of this block: its first step, also left in the workspace.  All
@@ -99,7 +100,8 @@ MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) total += scratch[w];
-  const long long from = attend_from(total, blockIdx.x, gridDim.x), to = attend_from(total, blockIdx.x + 1, gridDim.x);
+  const AttendShare share{total / gridDim.x, (int)(total % gridDim.x)};
+  const long long from = share.from(blockIdx.x), to = share.from(blockIdx.x + 1);
   long long base = 0;
   for (int b0 = 0; b0 < P.B && from < to && base <= from; b0 += THREADS) {
     const int b = b0 + tid;
@@ -136,7 +138,7 @@ MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
     a.head = (int)(unit / a.s.tiles);
     a.tile = (int)(unit - (long long)a.head * a.s.tiles);
   }
-  if (tid == 0) P.from[blockIdx.x] = AttendFrom{total, a.b, a.head, a.tile, a.chunk};
+  if (tid == 0) P.from[blockIdx.x] = AttendFrom{share, a.s.t0, a.s.n, a.s.chunks, a.head, a.tile, a.chunk};
   for (int b = blockIdx.x + gridDim.x * tid; b < P.B; b += gridDim.x * THREADS) {
     const AttendSeq s = attend_seq(P, b);
     if (s.chunks > 0) continue;
@@ -155,6 +157,21 @@ MOE_DEV bool attend_sees(const AttendParams& P, int t, int j, int own) {
   if (own < 0) return true;
   if (!P.mask) return own <= j;
   return (own >> 5) < P.mask_words && (P.mask[(long long)t * P.mask_stride + (own >> 5)] >> (own & 31) & 1);
+}
+
+// tanh, relative error some 2^-22: by its series below 1/2, else by
+// 1 - 2 / (exp(2 x) + 1), which has lost that many bits where it is small.
+MOE_DEV float attend_tanh(float x) {
+  const float y = x * x;
+  float p = -929569.f / 638512875.f;
+  p = fmaf(p, y, 21844.f / 6081075.f);
+  p = fmaf(p, y, -1382.f / 155925.f);
+  p = fmaf(p, y, 62.f / 2835.f);
+  p = fmaf(p, y, -17.f / 315.f);
+  p = fmaf(p, y, 2.f / 15.f);
+  p = fmaf(p, y, -1.f / 3.f);
+  const float far = 1.f - __fdividef(2.f, exp2_fast(x * 2.8853900817779268f) + 1.f);
+  return fabsf(x) < 0.5f ? fmaf(p * y, x, x) : far;
 }
 
 // The largest running maximum is taken for 0 where there is none, so that

@@ -352,6 +352,7 @@ struct ProjectParams {
   const uint8_t* w;
   const float* bias;
   void* y;
+  CUtensorMap tm_codes, tm_scales;  // set by the launch
 };
 cudaError_t launch_project(ProjectParams p, cudaStream_t stream);
 
@@ -384,7 +385,7 @@ struct AttendParams {
   float* lse;
   // set by the launch: blocks, rows and tokens of a unit's steps, columns of a
   // part's row, i / page_size = i page_mul >> page_shift
-  int blocks, rows, chunk, width, page_shift;
+  int blocks, rows, chunk, width, page_shift, q_vec, slot_first;
   unsigned long long page_mul;
   // workspace: where the blocks' ranges begin, the parts' sums [2 blocks][rows]
   // [width] and their maximum and sum of weights [2 blocks][rows]
@@ -392,6 +393,7 @@ struct AttendParams {
   AttendFrom* from;
   float* part;
   float2* stat;
+  CUtensorMap tm_k, tm_v;  // of caches whose pages hold multiples of 16 tokens
 };
 size_t attend_workspace(const AttendParams& p);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);

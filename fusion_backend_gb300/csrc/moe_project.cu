@@ -2,20 +2,21 @@
 //   y_tn = sum_g d_ng sum_{k in g} (c_nk - 8) x_tk + bias_n
 //
 // Bound by the stream of codes and scales up to some 16 tokens, by the warp-level
-// tensor-core instruction above.  A tile is 16 MT rows of W and all of K; the KW
-// warps over K of a block take slabs of 256 columns in turn, each with a ring of
-// its own in shared memory that asynchronous copies fill tiles ahead, and meet
-// once a tile to add their sums.  So every SM has its whole share of a small
-// matrix on its way at once, and of a large one as much as the rings hold.
+// tensor-core instruction above.  A tile is 16 MT rows of W and all of K; the warps
+// of a block that share a tile take slabs of 256 columns in turn, each with a ring
+// of its own in shared memory that tensor copies fill tiles ahead, and meet once a
+// batch of tiles to add their sums.  So every SM has its whole share of a small
+// matrix on its way at once, and of a large one as much as the rings hold; a block's
+// tiles are neighbours, as many for each block as for any other.
 //
 // mma.m16n8k16 with the rows of W as its rows: 16-byte pieces of 8 rows are what
 // ldmatrix hands out, a lane then holds 8 codes of rows g and g + 8 that lie in
 // one group, as bf16 (fp16) numbers c - 8 exactly.  The order of k inside those 8
 // follows the nibbles (0 4, 1 5, 2 6, 3 7), x is put in the same order where it is
 // loaded: straight from global memory, since each warp of a block has other
-// columns of it.  A group's products go to sums of their own and from there, times
-// the group's scale, to the row's: the products are exact and everything is added
-// in fp32.
+// columns of it, and once for all tiles where a warp has one slab of every tile.  A
+// group's products go to sums of their own and from there, times the group's scale,
+// to the row's: the products are exact and everything is added in fp32.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,13 +24,14 @@
 #include "moe_elem.cuh"
 #include "moe_internal.h"
 #include "moe_mma.cuh"
+#include "moe_tma.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kSlab = 256;  // columns of a slab: 128 bytes of codes, 16 bytes of scales (group 32)
+constexpr int kSlab = 256;  // columns of a slab: 128 bytes of codes
 constexpr int kChunks = kSlab / 32;
 
 // Code pairs (nibbles 0, 4 of v) as numbers c - 8: the nibble in the mantissa of
@@ -45,189 +47,230 @@ MOE_DEV uint32_t code_pair(uint32_t v) {
   return r;
 }
 
-template <int MT>
-__host__ __device__ constexpr int stage_bytes() {
-  return 16 * MT * (128 + 16);
-}
+// Shared memory: the warps' rings of codes, of scales (16 bytes a row and slab),
+// the sums of a batch of BT tiles, the barriers.
+template <int NT, int MT, int STAGES, int BT>
+struct Layout {
+  static constexpr int kCodes = 16 * MT * 128, kScales = 16 * MT * 16, kPitch = 8 * NT + 1, kRows = BT * 16 * MT;
+  static constexpr int scales_at = kWarps * STAGES * kCodes, sums_at = scales_at + kWarps * STAGES * kScales,
+                       bars_at = sums_at + (kWarps * kRows * kPitch * 4 + 15) / 16 * 16,
+                       bytes = bars_at + kWarps * STAGES * 8 + 1024;  // (rings start at a multiple of 1024)
+};
 
-template <int NT, int MT, int STAGES>
-__host__ __device__ constexpr int smem_bytes() {
-  return kWarps * (STAGES * stage_bytes<MT>() + 16 * MT * (8 * NT + 1) * 4);
-}
-
-// NT: tiles of 8 tokens.  GL: log2(group / 32).
-template <bool F16, int NT, int MT, int STAGES, int GL>
+// NT: tiles of 8 tokens.  GL: log2(group / 32).  HOLD: a warp has one slab of
+// every tile, whose x stays in registers.
+template <bool F16, int NT, int MT, int STAGES, int BT, int GL, bool HOLD>
 __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const __grid_constant__ ProjectParams P) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kStage = stage_bytes<MT>();
+  using L = Layout<NT, MT, STAGES, BT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int kw = P.k_warps, kpart = warp % kw, tpart = warp / kw, tiles_at_once = kWarps / kw;
+  const int kw = P.k_warps, kpart = warp % kw, tpart = warp / kw, at_once = kWarps / kw;
   const int t0 = blockIdx.y * 8 * NT;
-  const int slabs = (P.K + kSlab - 1) / kSlab, mine = (slabs - kpart + kw - 1) / kw;  // slabs of the warp in a tile
+  const int slabs = (P.K + kSlab - 1) / kSlab, mine = HOLD ? 1 : (slabs - kpart + kw - 1) / kw;
   const int ntiles = (P.N + 16 * MT - 1) / (16 * MT);
-  uint8_t* const ring = smem + warp * STAGES * kStage;
-  float* const sums = reinterpret_cast<float*>(smem + kWarps * STAGES * kStage);
-  constexpr int kPitch = 8 * NT + 1, kSums = 16 * MT * kPitch;
+  const int lo = (int)((long long)ntiles * blockIdx.x / gridDim.x), hi = (int)((long long)ntiles * (blockIdx.x + 1) / gridDim.x);
+  uint8_t* const codes = smem + warp * STAGES * L::kCodes;
+  uint8_t* const scales = smem + L::scales_at + warp * STAGES * L::kScales;
+  float* const sums = reinterpret_cast<float*>(smem + L::sums_at);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::bars_at) + warp * STAGES;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) mbar_init(full + s, 1);
+    mbar_fence_init();
+    prefetch_tensormap(&P.tm_codes);
+    prefetch_tensormap(&P.tm_scales);
+  }
+  __syncwarp();
   pdl_wait();
 
   // the warp's steps: its slabs of its tiles, in order
-  struct At {
-    int tile, j;
-  };
-  const int tile_step = gridDim.x * tiles_at_once;
-  auto next = [&](At& a) {
-    if (++a.j >= mine) {
-      a.j = 0;
-      a.tile += tile_step;
-    }
-  };
-  auto load = [&](const At& a, int stage) {
-    if (a.tile < ntiles && mine > 0) {
-      const int k0 = (kpart + a.j * kw) * kSlab, chunks = min(kChunks, (P.K - k0) >> 5);
-      const uint32_t dst = smem_u32(ring + stage * kStage);
-#pragma unroll
-      for (int i = 0; i < 4 * MT; ++i) {
-        const int r = 4 * i + (lane >> 3), c = lane & 7, n = a.tile * 16 * MT + r;
-        const bool on = n < P.N && c < chunks;
-        const uint8_t* const row = P.w + (long long)(n < P.N ? n : 0) * P.w_stride;
-        copy16(dst + r * 128 + ((c ^ (r & 7)) << 4), on ? row + (k0 >> 1) + 16 * c : P.w, on ? 16u : 0u);
+  int tile_in = lo + tpart, slab_in = 0;
+  const uint64_t policy = policy_evict_first();
+  auto load = [&](int stage) {
+    if (tile_in < hi && mine > 0) {
+      if (lane == 0) {
+        const int k0 = (kpart + slab_in * kw) * kSlab;
+        mbar_arrive_expect_tx(full + stage, L::kCodes + L::kScales);
+        tensor_load_2d(codes + stage * L::kCodes, &P.tm_codes, k0 >> 1, tile_in * 16 * MT, full + stage, policy);
+        // 16 bytes that hold the slab's scales: of one slab, two or four
+        tensor_load_2d(scales + stage * L::kScales, &P.tm_scales, (P.K >> 1) + (k0 >> (4 + GL) & ~15), tile_in * 16 * MT,
+                       full + stage, policy);
       }
-      if (lane < 16 * MT) {
-        const int n = a.tile * 16 * MT + lane;
-        const uint8_t* const row = P.w + (long long)(n < P.N ? n : 0) * P.w_stride + (P.K >> 1);
-        const uint32_t at = dst + 16 * MT * 128 + lane * 16;
-        const uint32_t bytes = n < P.N ? (uint32_t)(2 * (chunks >> GL)) : 0u;
-        const uint8_t* const src = bytes ? row + (k0 >> (4 + GL)) : P.w;
-        if (GL == 0) copy16(at, src, bytes);
-        if (GL == 1) copy8(at, src, bytes);
-        if (GL == 2) copy4(at, src, bytes);
+      if (HOLD || ++slab_in >= mine) {
+        slab_in = 0;
+        tile_in += at_once;
       }
     }
-    copy_commit();
   };
-
-  At ahead{(int)blockIdx.x * tiles_at_once + tpart, 0}, now = ahead;
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) {
-    load(ahead, s);
-    next(ahead);
-  }
-  // x of one chunk, in the order of the codes' nibbles
-  auto load_x = [&](uint4 (&x)[NT], int k) {
+  for (int s = 0; s < STAGES - 1; ++s) load(s);
+  // x of one chunk (B of the chunk's two products), in the order of the codes' nibbles
+  auto load_x = [&](uint32_t (&x)[NT][4], int k) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int t = t0 + 8 * j + g;
-      x[j] = t < P.T ? __ldg(reinterpret_cast<const uint4*>(P.x + (size_t)t * P.x_stride + k + 8 * q))
-                     : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 v = t < P.T ? __ldg(reinterpret_cast<const uint4*>(P.x + (size_t)t * P.x_stride + k + 8 * q))
+                              : make_uint4(0u, 0u, 0u, 0u);
+      x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
     }
   };
+  auto order_x = [&](uint32_t (&x)[NT][4]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint32_t a = x[j][0], b = x[j][1], c = x[j][2], d = x[j][3];
+      x[j][0] = __byte_perm(a, c, 0x5410), x[j][1] = __byte_perm(a, c, 0x7632);
+      x[j][2] = __byte_perm(b, d, 0x5410), x[j][3] = __byte_perm(b, d, 0x7632);
+    }
+  };
+  uint32_t xh[HOLD ? kChunks : 1][NT][4];
+  if constexpr (HOLD) {
+    const int chunks = min(kChunks, (P.K - kpart * kSlab) >> 5);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      if (c < chunks) load_x(xh[c], kpart * kSlab + 32 * c);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) order_x(xh[c]);
+  }
   int stage = 0, stage_in = STAGES - 1;
-  for (int base = blockIdx.x * tiles_at_once; base < ntiles; base += tile_step) {
-    float acc[MT][NT][4] = {};
-    for (int j = 0; j < mine; ++j) {
-      const int k0 = (kpart + j * kw) * kSlab, chunks = min(kChunks, (P.K - k0) >> 5);
-      uint4 x[NT];
-      load_x(x, k0);
-      copy_wait<STAGES - 2>();
-      __syncwarp();
-      load(ahead, stage_in);
-      next(ahead);
-      stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
-      const uint32_t codes = smem_u32(ring + stage * kStage);
-      const __half* const scales = reinterpret_cast<const __half*>(ring + stage * kStage + 16 * MT * 128);
-      float part[MT][NT][4];
+  uint32_t parity = 0;
+  bool dead = false;  // a copy never came: results are NaN
+  for (int base = lo; base < hi; base += BT) {
+    const int in_batch = min(BT, hi - base);
+    for (int u = tpart; u < in_batch; u += at_once) {
+      float acc[MT][NT][4] = {};
+      for (int j = 0; j < mine; ++j) {
+        const int k0 = (kpart + j * kw) * kSlab, chunks = min(kChunks, (P.K - k0) >> 5);
+        uint32_t x[NT][4];
+        if constexpr (!HOLD) load_x(x, k0);
+        __syncwarp();
+        load(stage_in);
+        stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
+        if (!dead) dead = !mbar_wait(full + stage, parity);
+        const uint32_t codes_at = smem_u32(codes + stage * L::kCodes);
+        const __half* const sc = reinterpret_cast<const __half*>(scales + stage * L::kScales) +
+                                 (k0 >> (5 + GL) & 7);  // of row 0
+        float part[MT][NT][4];
 #pragma unroll
-      for (int c2 = 0; c2 < kChunks; c2 += 2) {
-        if (c2 >= chunks) break;
-        // codes of two chunks: (rows, chunk) of matrix i = (i & 1, i >> 1)
-        uint32_t w[MT][4];
-        const int r = (lane & 7) + (lane & 8), c = c2 + (lane >> 4);
+        for (int c2 = 0; c2 < kChunks; c2 += 2) {
+          if (c2 >= chunks) break;
+          // codes of two chunks: (rows, chunk) of matrix i = (i & 1, i >> 1)
+          uint32_t w[MT][4];
+          const int r = (lane & 7) + (lane & 8), c = c2 + (lane >> 4);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) ldmatrix4(w[m], codes + (16 * m + r) * 128 + ((c ^ (r & 7)) << 4));
+          for (int m = 0; m < MT; ++m) ldmatrix4(w[m], codes_at + (16 * m + r) * 128 + ((c ^ (r & 7)) << 4));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (c2 + h >= chunks) break;
-          uint4 xn[NT];
-          if (c2 + h + 1 < chunks) load_x(xn, k0 + 32 * (c2 + h + 1));
-          const bool first = ((c2 + h) & ((1 << GL) - 1)) == 0;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t a = w[m][2 * h], b = w[m][2 * h + 1];  // rows g and g + 8
-            const uint32_t a0 = code_pair<F16>(a), b0 = code_pair<F16>(b), a1 = code_pair<F16>(a >> 4),
-                           b1 = code_pair<F16>(b >> 4), a2 = code_pair<F16>(a >> 8), b2 = code_pair<F16>(b >> 8),
-                           a3 = code_pair<F16>(a >> 12), b3 = code_pair<F16>(b >> 12);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float(&d)[4] = part[m][n];
-              if (first) d[0] = d[1] = d[2] = d[3] = 0.f;
-              mma16<F16>(d, a0, b0, a1, b1, __byte_perm(x[n].x, x[n].z, 0x5410), __byte_perm(x[n].x, x[n].z, 0x7632));
-              mma16<F16>(d, a2, b2, a3, b3, __byte_perm(x[n].y, x[n].w, 0x5410), __byte_perm(x[n].y, x[n].w, 0x7632));
+          for (int h = 0; h < 2; ++h) {
+            if (c2 + h >= chunks) break;
+            uint32_t xn[NT][4];
+            if constexpr (!HOLD) {
+              if (c2 + h + 1 < chunks) load_x(xn, k0 + 32 * (c2 + h + 1));
+              order_x(x);
             }
-          }
-          if (((c2 + h + 1) & ((1 << GL) - 1)) == 0) {
-            const int at = (c2 + h) >> GL;
+            uint32_t(&b)[NT][4] = HOLD ? xh[HOLD ? c2 + h : 0] : x;
+            const bool first = ((c2 + h) & ((1 << GL) - 1)) == 0;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              const float s0 = __half2float(scales[(16 * m + g) * 8 + at]);
-              const float s1 = __half2float(scales[(16 * m + g + 8) * 8 + at]);
+              const uint32_t v0 = w[m][2 * h], v1 = w[m][2 * h + 1];  // rows g and g + 8
+              const uint32_t a0 = code_pair<F16>(v0), b0 = code_pair<F16>(v1), a1 = code_pair<F16>(v0 >> 4),
+                             b1 = code_pair<F16>(v1 >> 4), a2 = code_pair<F16>(v0 >> 8), b2 = code_pair<F16>(v1 >> 8),
+                             a3 = code_pair<F16>(v0 >> 12), b3 = code_pair<F16>(v1 >> 12);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                acc[m][n][0] = fmaf(part[m][n][0], s0, acc[m][n][0]);
-                acc[m][n][1] = fmaf(part[m][n][1], s0, acc[m][n][1]);
-                acc[m][n][2] = fmaf(part[m][n][2], s1, acc[m][n][2]);
-                acc[m][n][3] = fmaf(part[m][n][3], s1, acc[m][n][3]);
+                float(&d)[4] = part[m][n];
+                if (first) d[0] = d[1] = d[2] = d[3] = 0.f;
+                mma16<F16>(d, a0, b0, a1, b1, b[n][0], b[n][1]);
+                mma16<F16>(d, a2, b2, a3, b3, b[n][2], b[n][3]);
               }
             }
-          }
+            if (((c2 + h + 1) & ((1 << GL) - 1)) == 0) {
+              const int at = (c2 + h) >> GL;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) x[n] = xn[n];
+              for (int m = 0; m < MT; ++m) {
+                const float s0 = __half2float(sc[(16 * m + g) * 8 + at]);
+                const float s1 = __half2float(sc[(16 * m + g + 8) * 8 + at]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  acc[m][n][0] = fmaf(part[m][n][0], s0, acc[m][n][0]);
+                  acc[m][n][1] = fmaf(part[m][n][1], s0, acc[m][n][1]);
+                  acc[m][n][2] = fmaf(part[m][n][2], s1, acc[m][n][2]);
+                  acc[m][n][3] = fmaf(part[m][n][3], s1, acc[m][n][3]);
+                }
+              }
+            }
+            if constexpr (!HOLD) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] = xn[n][e];
+            }
+          }
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          parity ^= 1u;
         }
       }
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      if (dead) acc[0][0][0] = __int_as_float(0x7FFFFFFF);
+      float* const own = sums + (kpart * L::kRows + u * 16 * MT) * L::kPitch;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            own[(16 * m + g + 8 * (e >> 1)) * L::kPitch + 8 * n + 2 * q + (e & 1)] = acc[m][n][e];
     }
-    // the warps' sums, in their order
-    float* const own = sums + warp * kSums;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) own[(16 * m + g + 8 * (e >> 1)) * kPitch + 8 * n + 2 * q + (e & 1)] = acc[m][n][e];
     __syncthreads();
+    // the warps' sums, in their order
     const int tokens = min(8 * NT, P.T - t0);
-    for (int i = threadIdx.x; i < tiles_at_once * 16 * MT * tokens; i += 32 * kWarps) {
-      const int r = i % (16 * MT), u = i / (16 * MT), t = u % tokens, p = u / tokens;
-      const int n = (base + p) * 16 * MT + r;
-      if (n >= P.N) continue;
+    for (int i = threadIdx.x; i < L::kRows * tokens; i += 32 * kWarps) {
+      const int r = i % L::kRows, t = i / L::kRows, n = base * 16 * MT + r;
+      if (r >= in_batch * 16 * MT || n >= P.N) continue;
       float v = 0.f;
-      for (int k = 0; k < kw; ++k) v += sums[(p * kw + k) * kSums + r * kPitch + t];
+      for (int k = 0; k < kw; ++k) v += sums[(k * L::kRows + r) * L::kPitch + t];
       if (P.bias) v += P.bias[n];
       elem_store(P.y, P.y_dtype, (size_t)(t0 + t) * P.y_stride + n, v);
     }
     __syncthreads();
   }
-  copy_wait<0>();
 }
 
-template <bool F16, int NT, int MT, int STAGES, int GL>
-cudaError_t launch(const ProjectParams& p, cudaStream_t stream) {
-  constexpr int smem = smem_bytes<NT, MT, STAGES>();
-  auto* const kern = k_project<F16, NT, MT, STAGES, GL>;
+template <bool F16, int NT, int MT, int STAGES, int BT, int GL, bool HOLD>
+cudaError_t launch(ProjectParams& p, cudaStream_t stream) {
+  using L = Layout<NT, MT, STAGES, BT>;
+  static_assert(L::bytes <= 232448, "shared memory");
+  auto* const kern = k_project<F16, NT, MT, STAGES, BT, GL, HOLD>;
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), smem);
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), L::bytes);
   if (e != cudaSuccess) return e;
+  const auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)(p.K / 2 + p.K / p.group * 2), (cuuint64_t)p.N}, strides[1] = {(cuuint64_t)p.w_stride};
+  const cuuint32_t ones[2] = {1, 1}, code_box[2] = {128, 16 * MT}, scale_box[2] = {16, 16 * MT};
+  if (encode(&p.tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.w), dims, strides, code_box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      encode(&p.tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.w), dims, strides, scale_box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  // (a batch has a tile at least for the warps of each; warps without a slab add zeros)
+  if (p.k_warps < kWarps / BT) p.k_warps = kWarps / BT;
   const int at_once = kWarps / p.k_warps, tiles = (p.N + 16 * MT - 1) / (16 * MT);
   const int want = (tiles + at_once - 1) / at_once, most = p.sms * (NT <= 2 ? 2 : 1);
-  return launch_behind(kern, dim3(want < most ? want : most, (p.T + 8 * NT - 1) / (8 * NT)), 32 * kWarps, smem, stream,
-                       p);
+  return launch_behind(kern, dim3(want < most ? want : most, (p.T + 8 * NT - 1) / (8 * NT)), 32 * kWarps, L::bytes,
+                       stream, p);
 }
 
 template <bool F16, int GL>
-cudaError_t launch_tokens(const ProjectParams& p, cudaStream_t stream) {
-  if (p.T <= 8) return launch<F16, 1, 1, 4, GL>(p, stream);
-  if (p.T <= 16) return launch<F16, 2, 1, 4, GL>(p, stream);
-  if (p.T <= 32) return launch<F16, 4, 2, 3, GL>(p, stream);
-  return launch<F16, 8, 2, 3, GL>(p, stream);
+cudaError_t launch_tokens(ProjectParams& p, cudaStream_t stream) {
+  if (p.T <= 8)
+    return p.K <= p.k_warps * kSlab ? launch<F16, 1, 1, 4, 8, GL, true>(p, stream)
+                                    : launch<F16, 1, 1, 4, 8, GL, false>(p, stream);
+  if (p.T <= 16) return launch<F16, 2, 1, 4, 4, GL, false>(p, stream);
+  if (p.T <= 32) return launch<F16, 4, 2, 3, 2, GL, false>(p, stream);
+  return launch<F16, 8, 2, 3, 1, GL, false>(p, stream);
 }
 
 }  // namespace
