@@ -46,8 +46,8 @@ MOE_DEV bool odd16(uint32_t h) {
 
 // DP: elements of a head in shared memory (D rounded up); TERMS: numbers that
 // stand for a weight.
-// PAGED: 16 tokens lie in one page, which tensor copies fetch; else asynchronous
-// copies by the lanes, each token from a page of its own.
+// PAGED: pages hold multiples of 8 tokens: tensor copies of boxes of 8 or 16; else
+// asynchronous copies by the lanes, each token from a page of its own.
 template <bool F16, int DP, int TERMS, bool PAGED>
 __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_constant__ AttendParams P) {
   constexpr int W = warps_for(DP), S = stages_for(DP), kSlot = slot_bytes(DP), kChunks = DP / 8;
@@ -87,15 +87,15 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   __syncthreads();
 
   const int pieces = P.D >> 3;
-  // the page of the step's tokens (of token lane % 16 where a step may hold several)
+  // the page of the lane's box of the step's tokens (of its token lane % 16)
   AttendStep ahead = now;
   int page_ahead = -1;
   const uint64_t once = policy_evict_first(), again = policy_evict_last();
   auto look = [&]() {  // the page of `ahead`
     page_ahead = -1;
     if (ahead.left <= 0) return;
-    const int i = ahead.chunk * (W * kTok) + warp * kTok + (PAGED ? 0 : lane & 15);
-    if (i < ahead.s.len) page_ahead = P.table[ahead.b * P.table_stride + attend_page(P, i)];
+    const int i = ahead.chunk * (W * kTok) + warp * kTok + (PAGED ? lane * P.box : lane & 15);
+    if (i < ahead.s.len && (!PAGED || lane * P.box < kTok)) page_ahead = P.table[ahead.b * P.table_stride + attend_page(P, i)];
   };
   auto load = [&](int stage) {  // the tokens of `ahead`, then the next step's page
     if (ahead.left > 0) {
@@ -103,26 +103,34 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       const uint32_t k_dst = ring_at + stage * kSlot, v_dst = k_dst + kSlot / 2;
       const bool ok = (uint32_t)page_ahead < (uint32_t)P.pages;
       if constexpr (PAGED) {
-        const int count = ok ? min(max(ahead.s.len - first, 0), kTok) : 0;
+        const uint32_t there = __ballot_sync(kAll, ok && lane * P.box < kTok);  // boxes whose page exists
+        const int count = min(max(ahead.s.len - first, 0), kTok);
+        uint32_t valid = (1u << count) - 1u;
+        if (P.box < kTok)
+          valid &= (there & 1u ? 0xFFu : 0u) | (there & 2u ? 0xFF00u : 0u);
+        else if (!there)
+          valid = 0u;
         if (lane == 0) {
-          if (count > 0) {
-            const int slot = first - attend_page(P, first) * P.page_size;
-            // keys and values are read again where a sequence has further tiles of rows
-            const uint64_t policy = ahead.s.tiles > 1 ? again : once;
-            const int x1 = P.slot_first ? slot : ahead.head, x2 = P.slot_first ? ahead.head : slot;
+          if (valid)
             mbar_arrive_expect_tx(full + stage, kSlot);
-#pragma unroll
-            for (int c = 0; c < DP / 64; ++c)
-              tensor_load_4d(ring + stage * kSlot + c * kTok * 128, &P.tm_k, 64 * c, x1, x2, page_ahead, full + stage,
-                             policy);
-#pragma unroll
-            for (int c = 0; c < DP / 64; ++c)
-              tensor_load_4d(ring + stage * kSlot + kSlot / 2 + c * kTok * 128, &P.tm_v, 64 * c, x1, x2, page_ahead,
-                             full + stage, policy);
-          } else {
+          else
             mbar_arrive(full + stage);
-          }
-          s_valid[warp][stage] = count >= kTok ? 0xFFFFu : (1u << count) - 1u;
+          s_valid[warp][stage] = valid;
+        }
+        __syncwarp();
+        if (valid && lane * P.box < kTok) {
+          // (a page behind the cache: zeros)
+          const int t = first + lane * P.box, slot = t - attend_page(P, t) * P.page_size, page = ok ? page_ahead : P.pages;
+          const int x1 = P.slot_first ? slot : ahead.head, x2 = P.slot_first ? ahead.head : slot;
+          // keys and values are read again where a sequence has further tiles of rows
+          const uint64_t policy = ahead.s.tiles > 1 ? again : once;
+          uint8_t* const dst = ring + stage * kSlot + lane * P.box * 128;
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c)
+            tensor_load_4d(dst + c * kTok * 128, &P.tm_k, 64 * c, x1, x2, page, full + stage, policy);
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c)
+            tensor_load_4d(dst + kSlot / 2 + c * kTok * 128, &P.tm_v, 64 * c, x1, x2, page, full + stage, policy);
         }
       } else {
         const int i = first + (lane & 15);
@@ -499,7 +507,7 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 int width_for(int D) { return (D + 63) / 64 * 64; }
 
 // The cache as (column, head, slot, page) or (column, slot, head, page), by their
-// strides, in boxes of 64 columns of 16 tokens of a head.
+// strides, in boxes of 64 columns of p.box tokens of a head.
 bool encode_cache(CUtensorMap* m, const AttendParams& p, const uint16_t* base, long long page, long long slot,
                   long long head) {
   const auto encode = tensor_map_encoder();
@@ -509,7 +517,7 @@ bool encode_cache(CUtensorMap* m, const AttendParams& p, const uint16_t* base, l
   const cuuint64_t dims[4] = {(cuuint64_t)p.D, sf ? slots : heads, sf ? heads : slots, (cuuint64_t)p.pages};
   const cuuint64_t strides[3] = {(cuuint64_t)(2 * (sf ? slot : head)), (cuuint64_t)(2 * (sf ? head : slot)),
                                  (cuuint64_t)(2 * page)};
-  const cuuint32_t box[4] = {64, sf ? kTok : 1u, sf ? 1u : kTok, 1}, ones[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, sf ? (cuuint32_t)p.box : 1u, sf ? 1u : (cuuint32_t)p.box, 1}, ones[4] = {1, 1, 1, 1};
   return encode(m, p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                 const_cast<uint16_t*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -546,17 +554,36 @@ cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream) {
   return launch_behind(k_attend_join, dim3(p.blocks, p.rows < 32 ? p.rows : 32), 32 * kJoinWarps, 0, stream, p);
 }
 
+// Rows of a unit: 128 (k_attend_wide) where a sequence has more than 16 on average,
+// whatever the rest of the call; its heads have to fit into tensor memory.
+static int attend_rows(const AttendParams& p) {
+  return p.D <= 128 && (long long)p.T * p.G > 16ll * p.B ? 128 : 16;
+}
+
 size_t attend_workspace(const AttendParams& p) {
-  const size_t rows = 16;
+  const size_t rows = attend_rows(p);
   return align256(kMaxBlocks * sizeof(AttendFrom)) + align256((size_t)2 * kMaxBlocks * rows * 8) +
          (size_t)2 * kMaxBlocks * rows * width_for(p.D) * 4;
 }
 
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   p.blocks = p.sms;
-  p.rows = 16;
+  // floor(i / d) for i < 2^31: i ceil(2^(32 + s) / d) >> (32 + s), 2^s >= d
+  int s = 0;
+  while ((1ll << s) < p.page_size) ++s;
+  p.page_shift = 32 + s;
+  p.page_mul = (unsigned long long)((((unsigned __int128)1 << (32 + s)) + p.page_size - 1) / p.page_size);
+  p.q_vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0 && p.q_head % 8 == 0;
+  p.o_vec = reinterpret_cast<uintptr_t>(p.out) % (4 * elem_bytes(p.out_dtype)) == 0 && p.o_stride % 4 == 0 && p.o_head % 4 == 0;
+  p.slot_first = p.kc_slot < p.kc_head;
+  p.box = p.page_size % 16 == 0 ? 16 : 8;
+  const bool paged = p.page_size % 8 == 0 && p.pages > 0 && encode_cache(&p.tm_k, p, p.k, p.kc_page, p.kc_slot, p.kc_head) &&
+                     encode_cache(&p.tm_v, p, p.v, p.vc_page, p.vc_slot, p.vc_head);
+  // (three numbers a weight do not fit beside the scores)
+  const bool wide = attend_rows(p) == 128 && paged && (p.f16 || p.out_dtype != kF32);
   const int dp = width_for(p.D);
-  p.chunk = warps_for(dp) * kTok;
+  p.rows = wide ? 128 : 16;
+  p.chunk = wide ? 128 : warps_for(dp) * kTok;
   p.width = dp;
   uint8_t* w = static_cast<uint8_t*>(p.ws);
   p.from = reinterpret_cast<AttendFrom*>(w);
@@ -564,16 +591,9 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   p.stat = reinterpret_cast<float2*>(w);
   w += align256((size_t)2 * kMaxBlocks * p.rows * 8);
   p.part = reinterpret_cast<float*>(w);
-  // floor(i / d) for i < 2^31: i ceil(2^(32 + s) / d) >> (32 + s), 2^s >= d
-  int s = 0;
-  while ((1ll << s) < p.page_size) ++s;
-  p.page_shift = 32 + s;
-  p.page_mul = (unsigned long long)((((unsigned __int128)1 << (32 + s)) + p.page_size - 1) / p.page_size);
-  p.q_vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0 && p.q_head % 8 == 0;
-  p.slot_first = p.kc_slot < p.kc_head;
-  const bool paged = p.page_size % kTok == 0 && p.pages > 0 && encode_cache(&p.tm_k, p, p.k, p.kc_page, p.kc_slot, p.kc_head) &&
-                     encode_cache(&p.tm_v, p, p.v, p.vc_page, p.vc_slot, p.vc_head);
-  const cudaError_t e = paged ? launch_terms<true>(p, stream) : launch_terms<false>(p, stream);
+  const cudaError_t e = wide    ? launch_attend_wide(p, stream)
+                        : paged ? launch_terms<true>(p, stream)
+                                : launch_terms<false>(p, stream);
   return e != cudaSuccess ? e : launch_attend_join(p, stream);
 }
 

@@ -180,5 +180,7 @@ MOE_DEV float attend_base(float m) { return m == -INFINITY ? 0.f : m; }
 
 // Joins the parts of the units that several blocks share (moe_attend.cu).
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream);
+// Units of 128 rows (moe_attend_wide.cu).
+cudaError_t launch_attend_wide(const AttendParams& p, cudaStream_t stream);
 
 }  // namespace moe

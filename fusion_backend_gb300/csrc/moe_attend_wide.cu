@@ -1,0 +1,603 @@
+// Attention over a paged cache for units of up to 128 rows: trees of drafted tokens
+// and ends of prompts (see moe_attend.cuh for the division of the work).
+//
+// With 128 rows a token's key and value enter 4 D 128 products for 4 D bytes: more
+// than the warp-level instruction can do at the rate of the stream, a third of what
+// tcgen05 can.  So the rows are the 128 lanes of tensor memory.  A step is 128
+// tokens, its two halves two streams with scores, output, running maximum and sum
+// of their own, so that one stream's weights are formed while the other's products
+// run; they meet at the end of the unit.  Tensor memory (D <= 128): two buffers of
+// 64 columns of scores a stream, which the weights (two numbers of the cache's type
+// each, 32 columns each) overwrite as operand of the second product, and the
+// output, 64 or 128 columns a stream.
+//
+//   warp 0       issues the products: scores of step i, then weighted values of i - 1
+//   warp 1       tensor copies of keys and values into a ring, in that order
+//   warps 2, 3   queries of the next unit; and in the tiles that hold tokens which
+//                some rows do not see, they take values that are not finite out (a
+//                product with a weight of 0 has an effect then); the rows that do see
+//                them get them at the end
+//   warps 4-11   a thread a row: scores to weights, four warps a stream
+//
+// Every wait is bounded; a thread whose wait ran out goes on without waiting, so that
+// nobody is left at a barrier, and results become NaN.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_attend.cuh"
+#include "moe_elem.cuh"
+#include "moe_internal.h"
+#include "moe_mma.cuh"
+#include "moe_tc.cuh"
+#include "moe_tma.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 384, kTok = 64;  // tokens of a stream's half step
+constexpr int kOddUnits = 16;  // units whose mark of values taken out is kept
+
+__host__ __device__ constexpr int slots_for(int dp) { return dp == 64 ? 14 : 9; }
+__host__ __device__ constexpr int wide_smem(int dp) { return slots_for(dp) * kTok * dp * 2 + 2 * 128 * dp * 2 + 1024; }
+
+__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 lanes x 16 (64) columns, and the wait for them: nothing can use them before it
+__device__ __forceinline__ void tmem_read16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}"
+      ", [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_read64(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%"
+      "26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%"
+      "50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}"
+      ", [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <bool F16>
+MOE_DEV bool odd16(uint32_t h) {  // not finite
+  const uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  return (h & e) == e;
+}
+
+// A wait that ran out once is not waited for again.
+MOE_DEV void await(uint64_t* bar, uint32_t parity, bool& dead) {
+  if (!dead) dead = !mbar_wait(bar, parity);
+}
+
+// First token that some row of the unit's sequence may not see.
+MOE_DEV int seen_by_all(const AttendParams& P, const AttendSeq& s) {
+  return s.n > 1 || P.mask ? max(s.len - s.n, 0) : s.len;
+}
+
+// Bits of the 64 tokens from `first` on that row t, the j-th of its sequence, sees.
+MOE_DEV uint64_t seen_tokens(const AttendParams& P, const AttendSeq& s, int first, int t, int j) {
+  const int left = s.len - first, o = first - (s.len - s.n);  // o: the first one's place among the sequence's own
+  uint64_t seen = left >= kTok ? ~0ull : left > 0 ? (1ull << left) - 1ull : 0ull;
+  if (t < 0 || o + kTok <= 0) return seen;
+  if (!P.mask) {
+    const int k = j - o + 1;
+    return k >= kTok ? seen : k > 0 ? seen & ((1ull << k) - 1ull) : 0ull;
+  }
+  const int32_t* const row = P.mask + (long long)t * P.mask_stride;
+  auto word = [&](int i) { return i < P.mask_words ? (uint64_t)(uint32_t)row[i] : 0ull; };
+  if (o < 0) return seen & ((word(0) | word(1) << 32) << -o | ((1ull << -o) - 1ull));
+  const int w = o >> 5, sh = o & 31;
+  const uint64_t lo = word(w) | word(w + 1) << 32;
+  return seen & (sh ? lo >> sh | word(w + 2) << (64 - sh) : lo);
+}
+
+template <bool F16, int DP>
+__global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_constant__ AttendParams P) {
+  constexpr int NS = slots_for(DP), kSlot = kTok * DP * 2, kQ = 128 * DP * 2, kHalves = DP / 64;
+  constexpr int kDt = F16 ? kF16 : kBf16;
+  // (as in k_attend: the maximum stays within 2^8, fp16 weights are held 2^7 up)
+  constexpr float kLazy = 8.f, kUp = F16 ? 7.f : 0.f;
+  constexpr uint32_t kOut = 256;  // columns of tensor memory before the outputs
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* const qs = smem + NS * kSlot;
+  __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_full[2][2], o_done[2], o_free, q_full[2], q_empty[2], clean[NS];
+  __shared__ uint32_t s_tmem;
+  __shared__ long long s_scan[kThreads / 32 + 2];
+  __shared__ float2 s_stat[2][2][128];
+  __shared__ uint32_t s_boxes[2][16], s_odd[kOddUnits];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[x][b], 1);
+        mbar_init(&p_full[x][b], 128);
+      }
+      mbar_init(&o_done[x], 1);
+      mbar_init(&q_full[x], 64);
+      mbar_init(&q_empty[x], 1);
+    }
+    mbar_init(&o_free, 256);
+    for (int i = 0; i < NS; ++i) mbar_init(clean + i, 64);
+    mbar_fence_init();
+    for (int i = 0; i < kOddUnits; ++i) s_odd[i] = 0u;
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 1 && lane == 0) {
+    prefetch_tensormap(&P.tm_k);
+    prefetch_tensormap(&P.tm_v);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  AttendStep a = attend_begin<kThreads>(P, s_scan);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  bool dead = false;
+  auto first_of = [](const AttendStep& s, int x) { return s.chunk * 2 * kTok + x * kTok; };
+  auto there = [&](const AttendStep& s, int x) { return x == 0 || first_of(s, 1) < s.s.len; };
+  auto last_of_unit = [](const AttendStep& s) { return s.left == 1 || s.chunk + 1 == s.s.chunks; };
+  // a tile that holds tokens which some rows do not see
+  auto mixed = [&](const AttendStep& s, int x) { return first_of(s, x) + kTok > seen_by_all(P, s.s); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16), o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
+      int slot = 0, unit = 0, count[2] = {0, 0}, cleaned = 0;
+      uint32_t turn = 0;
+      auto next_slot = [&] {
+        if (++slot == NS) {
+          slot = 0;
+          turn ^= 1u;
+        }
+      };
+      // mixed tiles in their order: as many barriers as slots, since those that are
+      // clean and not yet used lie in the ring
+      uint32_t clean_turn = 0;
+      auto next_clean = [&] {
+        if (++cleaned == NS) {
+          cleaned = 0;
+          clean_turn ^= 1u;
+        }
+      };
+      AttendStep before = a;
+      bool have = false, fresh[2] = {true, true};  // of the step before: its unit's first product
+      int unit_before = 0;
+      for (bool more = a.left > 0; more || have;) {
+        const bool begins = more && (!have || last_of_unit(before));
+        if (more) {
+          if (begins) await(&q_full[unit & 1], unit >> 1 & 1, dead);
+          for (int x = 0; x < 2; ++x) {
+            if (!there(a, x)) continue;
+            await(full + slot, turn, dead);
+            tc::tc_fence_after();
+            const uint32_t k_at = smem_u32(smem + slot * kSlot), q_at = smem_u32(qs + (unit & 1) * kQ);
+            const int buf = count[x] & 1;
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks)
+              tc::umma(tmem + x * 128 + buf * 64, tc::smem_desc(q_at + (ks >> 2) * 128 * 128 + (ks & 3) * 32, 16, 1024),
+                       tc::smem_desc(k_at + (ks >> 2) * kTok * 128 + (ks & 3) * 32, 16, 1024), s_desc, ks > 0);
+            tc::umma_commit(empty + slot);
+            tc::umma_commit(&s_full[x][buf]);
+            next_slot();
+            ++count[x];
+          }
+          if (last_of_unit(a)) tc::umma_commit(&q_empty[unit & 1]);
+        }
+        if (have) {
+          for (int x = 0; x < 2; ++x) {
+            if (!there(before, x)) continue;
+            // the chunk's number in its stream: the one before a chunk of `a`, if that has one
+            const int c = count[x] - 1 - (more && there(a, x) ? 1 : 0), buf = c & 1;
+            await(full + slot, turn, dead);
+            if (mixed(before, x)) {
+              await(clean + cleaned, clean_turn, dead);
+              next_clean();
+            }
+            await(&p_full[x][buf], c >> 1 & 1, dead);
+            if (fresh[x] && unit_before > 0) await(&o_free, (unit_before - 1) & 1, dead);
+            tc::tc_fence_after();
+            const uint32_t v_at = smem_u32(smem + slot * kSlot);
+#pragma unroll
+            for (int term = 1; term >= 0; --term)
+#pragma unroll
+              for (int ks = 0; ks < kTok / 16; ++ks)
+                umma_ts(tmem + kOut + x * DP, tmem + x * 128 + buf * 64 + term * 32 + ks * 8,
+                        tc::smem_desc(v_at + ks * 16 * 128, kTok * 128, 1024), o_desc, !(fresh[x] && term == 1 && ks == 0));
+            tc::umma_commit(empty + slot);
+            tc::umma_commit(&o_done[x]);
+            next_slot();
+            fresh[x] = false;
+          }
+          if (last_of_unit(before)) {
+            fresh[0] = fresh[1] = true;
+            ++unit_before;
+          }
+        }
+        if (more && last_of_unit(a)) ++unit;
+        have = more;
+        before = a;
+        if (more) a.next(P);
+        more = a.left > 0;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ keys and values
+    const int per = kTok / P.box, box = lane % per, half = lane / per;
+    const bool on = half < kHalves;
+    const uint64_t once = policy_evict_first(), again = policy_evict_last();
+    int slot = 0, i = 0;
+    uint32_t turn = 1;  // the first pass finds the slots empty
+    struct Where {
+      int page[2], at;  // pages of the lane's boxes (behind the cache: zeros), its first token's slot in the page
+    };
+    auto look = [&](const AttendStep& s) {
+      Where w;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = first_of(s, x) + box * P.box;
+        w.page[x] = -1;
+        if (s.left > 0 && t < s.s.len) w.page[x] = P.table[s.b * P.table_stride + attend_page(P, t)];
+      }
+      return w;
+    };
+    auto load = [&](const CUtensorMap* map, const AttendStep& s, int x, int page) {
+      await(empty + slot, turn, dead);
+      if (lane == 0) mbar_arrive_expect_tx(full + slot, kSlot);
+      __syncwarp();
+      if (on) {
+        const int t = first_of(s, x) + box * P.box, in = t - attend_page(P, t) * P.page_size;
+        const int c1 = P.slot_first ? in : s.head, c2 = P.slot_first ? s.head : in;
+        tensor_load_4d(smem + slot * kSlot + half * kTok * 128 + box * P.box * 128, map, 64 * half, c1, c2,
+                       (uint32_t)page < (uint32_t)P.pages ? page : P.pages, full + slot, s.s.tiles > 1 ? again : once);
+      }
+      if (++slot == NS) {
+        slot = 0;
+        turn ^= 1u;
+      }
+    };
+    AttendStep before = a;
+    Where now = look(a), then = now;
+    for (; a.left > 0; ++i) {
+      AttendStep next = a;
+      next.next(P);
+      const Where soon = look(next);
+      for (int x = 0; x < 2; ++x) {
+        if (!there(a, x)) continue;
+        const uint32_t boxes = __ballot_sync(kAll, half == 0 && (uint32_t)now.page[x] < (uint32_t)P.pages);
+        if (lane == 0) s_boxes[x][i & 15] = boxes;
+        load(&P.tm_k, a, x, now.page[x]);
+      }
+      if (i > 0)
+        for (int x = 0; x < 2; ++x)
+          if (there(before, x)) load(&P.tm_v, before, x, then.page[x]);
+      before = a;
+      then = now;
+      a = next;
+      now = soon;
+    }
+    if (i > 0)
+      for (int x = 0; x < 2; ++x)
+        if (there(before, x)) load(&P.tm_v, before, x, then.page[x]);
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ queries; values that are not finite
+    const int th = tid - 64;
+    int slot = 0, unit = 0, unit_before = 0, i = 0, cleaned = 0;
+    uint32_t turn = 0;
+    auto next_slot = [&] {
+      if (++slot == NS) {
+        slot = 0;
+        turn ^= 1u;
+      }
+    };
+    auto queries = [&](const AttendStep& s) {
+      if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
+      // (marks of units far behind, cleared for those as far ahead)
+      if (th == 0) s_odd[(unit + kOddUnits / 2) % kOddUnits] = 0u;
+      uint8_t* const to = qs + (unit & 1) * kQ;
+      const int rows = s.s.n * P.G, r0 = s.tile * 128;
+      const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;  // the scale's sign
+#pragma unroll 4
+      for (int x = th; x < 128 * DP / 8; x += 64) {
+        const int r = x / (DP / 8), c = x % (DP / 8);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r0 + r < rows && 8 * c < P.D) {
+          const int j = (r0 + r) / P.G, h = s.head * P.G + (r0 + r) - j * P.G;
+          const uint16_t* const from = P.q + (long long)(s.s.t0 + j) * P.q_stride + h * P.q_head + 8 * c;
+          if (P.q_vec) {
+            v = *reinterpret_cast<const uint4*>(from);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = from[2 * e] | (uint32_t)from[2 * e + 1] << 16;
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+        }
+        *reinterpret_cast<uint4*>(to + (c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async();
+      mbar_arrive(&q_full[unit & 1]);
+    };
+    auto values = [&](const AttendStep& s, int x) {
+      if (mixed(s, x)) {
+        await(full + slot, turn, dead);
+        const int from = max(seen_by_all(P, s.s) - first_of(s, x), 0);
+        uint8_t* const tile = smem + slot * kSlot;
+        bool odd = false;
+        for (int y = th; y < kTok * DP / 8; y += 64) {
+          const int r = y / (DP / 8), c = y % (DP / 8);
+          if (r < from) continue;
+          uint4* const at = reinterpret_cast<uint4*>(tile + (c >> 3) * kTok * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          bool any = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (odd16<F16>(w[e] & 0xFFFFu)) any = true, w[e] &= 0xFFFF0000u;
+            if (odd16<F16>(w[e] >> 16)) any = true, w[e] &= 0xFFFFu;
+          }
+          if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+          odd |= any;
+        }
+        if (odd) s_odd[unit_before % kOddUnits] = 1u;
+        fence_proxy_async();
+        mbar_arrive(clean + cleaned);
+        cleaned = cleaned + 1 == NS ? 0 : cleaned + 1;
+      }
+      next_slot();
+    };
+    AttendStep before = a;
+    while (a.left > 0 || i > 0) {
+      const bool more = a.left > 0;
+      if (more) {
+        if (i == 0 || last_of_unit(before)) queries(a);
+        for (int x = 0; x < 2; ++x)
+          if (there(a, x)) next_slot();
+      }
+      if (i > 0) {
+        for (int x = 0; x < 2; ++x)
+          if (there(before, x)) values(before, x);
+        if (last_of_unit(before)) ++unit_before;
+      }
+      if (!more) break;
+      if (last_of_unit(a)) ++unit;
+      before = a;
+      a.next(P);
+      ++i;
+    }
+  } else {
+    // ------------------------------------------------------------ weights
+    const int x = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    auto kept = [](float v) { return fminf(v, 3.4e38f); };  // (finite: 0 times infinity)
+    const float scale = fabsf(P.scale);
+    // (not 0 either: masked scores of -inf)
+    const float mul = P.softcap > 0.f ? 1.f : fmaxf(kept(scale * kLog2e), 1.2e-38f);
+    const float c1 = P.softcap > 0.f ? kept(scale / P.softcap) : 0.f, c2 = kept(P.softcap * kLog2e);
+    int count = 0, unit = 0, i = 0;
+    while (a.left > 0) {
+      const int r = a.tile * 128 + row, rows = a.s.n * P.G, j = r / P.G, t = r < rows ? a.s.t0 + j : -1;
+      const int chunk0 = a.chunk;
+      float m = -INFINITY, l = 0.f;
+      bool some = false, end = false, other = false;  // this stream, the second one have had a chunk
+      for (; !end; ++i) {
+        end = last_of_unit(a);
+        other |= there(a, 1);
+        if (there(a, x)) {
+          const int buf = count & 1;
+          const uint32_t at = tmem + lanes + x * 128 + buf * 64;
+          await(&s_full[x][buf], count >> 1 & 1, dead);
+          tc::tc_fence_after();
+          uint32_t w[kTok];
+          tmem_read64(at, w);
+          float s[kTok];
+#pragma unroll
+          for (int e = 0; e < kTok; ++e) s[e] = __uint_as_float(w[e]);
+          if (P.softcap > 0.f) {
+#pragma unroll
+            for (int e = 0; e < kTok; ++e) s[e] = c2 * attend_tanh(s[e] * c1);
+          }
+          const int first = first_of(a, x);
+          const uint32_t boxes = s_boxes[x][i & 15], all = kTok / P.box == 8 ? 0xFFu : 0xFu;
+          if (mixed(a, x) || boxes != all) {
+            uint64_t seen = seen_tokens(P, a.s, first, t, j);
+            for (int b = 0; b < kTok / P.box; ++b)
+              if (!(boxes >> b & 1u)) seen &= ~(((1ull << P.box) - 1ull) << (b * P.box));
+            const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(lo >> e & 1u)) s[e] = -INFINITY;
+              if (!(hi >> e & 1u)) s[32 + e] = -INFINITY;
+            }
+          }
+          float top[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = s[e];
+#pragma unroll
+          for (int e = 4; e < kTok; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul;
+          if (!some) {
+            m = mx;
+          } else if (__any_sync(kAll, mx > m + kLazy)) {
+            const float up = fmaxf(m, mx), f = exp2_fast(m - attend_base(up));
+            m = up;
+            l *= f;
+            await(&o_done[x], count - 1 & 1, dead);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              uint32_t o[16];
+              tmem_read16(tmem + lanes + kOut + x * DP + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tmem + lanes + kOut + x * DP + c, o);
+            }
+          }
+          const float base = attend_base(m) - kUp;
+          float sum[4] = {};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = exp2_fast(fmaf(s[32 * h + 2 * e], mul, -base));
+              const float p1 = exp2_fast(fmaf(s[32 * h + 2 * e + 1], mul, -base));
+              sum[2 * (e & 1)] += p0;
+              sum[2 * (e & 1) + 1] += p1;
+              hi[e] = pack2(kDt, p0, p1);
+              float a0, a1;
+              unpack2(kDt, hi[e], a0, a1);
+              lo[e] = pack2(kDt, p0 - a0, p1 - a1);
+            }
+            tmem_st16(at + 16 * h, hi);
+            tmem_st16(at + 32 + 16 * h, lo);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+          tc::tc_fence_before();
+          mbar_arrive(&p_full[x][buf]);
+          some = true;
+          ++count;
+        }
+        if (!end) a.next(P);
+      }
+      // the streams meet: each half of the threads joins half of the columns
+      if (some) await(&o_done[x], count - 1 & 1, dead);
+      s_stat[unit & 1][x][row] = make_float2(m - kUp, dead ? __int_as_float(0x7FFFFFFF) : l);
+      named_bar_sync(1, 256);
+      tc::tc_fence_after();
+      const float2 st0 = s_stat[unit & 1][0][row], st1 = s_stat[unit & 1][1][row];
+      const float top = fmaxf(st0.x, st1.x), base = attend_base(top);
+      const float f0 = exp2_fast(st0.x - base), f1 = exp2_fast(st1.x - base), sum = fmaf(st0.y, f0, st1.y * f1);
+      const bool from_start = chunk0 == 0, whole = from_start && a.chunk + 1 == a.s.chunks;
+      const bool odd = s_odd[unit % kOddUnits] != 0u;
+      const long long slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+      const int h = a.head * P.G + r - j * P.G;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+      for (int c = x * (DP / 2); c < (x + 1) * (DP / 2); c += 16) {
+        uint32_t o0[16], o1[16];
+        tmem_read16(tmem + lanes + kOut + c, o0);
+        if (other) tmem_read16(tmem + lanes + kOut + DP + c, o1);
+        if (t < 0 || c >= P.D) continue;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          v[e] = __uint_as_float(o0[e]) * f0;
+          if (other) v[e] = fmaf(__uint_as_float(o1[e]), f1, v[e]);
+        }
+        if (odd) {
+          // what was taken out of the tiles, for the rows that see it
+          const int end_at = min(a.s.len, (a.chunk + 1) * 2 * kTok);
+          for (int y = max(seen_by_all(P, a.s), chunk0 * 2 * kTok); y < end_at; ++y) {
+            if (!attend_sees(P, t, j, y - (a.s.len - a.s.n))) continue;
+            const int at = attend_page(P, y), page = P.table[a.b * P.table_stride + at];
+            if ((uint32_t)page >= (uint32_t)P.pages) continue;
+            const uint16_t* const from =
+                P.v + page * P.vc_page + (long long)(y - at * P.page_size) * P.vc_slot + a.head * P.vc_head + c;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e < P.D && odd16<F16>(from[e])) v[e] += raw_value(from[e], kDt);
+          }
+        }
+        if (whole) {
+          const long long to = t * P.o_stride + h * P.o_head + c;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = sum == 0.f ? 0.f : v[e] * inv;
+          if (P.o_vec && c + 16 <= P.D) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) elem_store4(P.out, P.out_dtype, to + e, v + e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e < P.D) elem_store(P.out, P.out_dtype, to + e, v[e]);
+          }
+        } else {
+          float* const to = P.part + (slot * 128 + row) * P.width + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+      tc::tc_fence_before();
+      mbar_arrive(&o_free);
+      if (x == 0 && t >= 0) {
+        if (!whole)
+          P.stat[slot * 128 + row] = make_float2(top, sum);
+        else if (P.lse)
+          P.lse[(long long)t * P.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      }
+      ++unit;
+      a.next(P);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <bool F16, int DP>
+cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+  static_assert(wide_smem(DP) + 4096 + 2048 <= 232448, "shared memory");
+  auto* const kern = k_attend_wide<F16, DP>;
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), wide_smem(DP));
+  if (e != cudaSuccess) return e;
+  return launch_behind(kern, dim3(p.blocks), kThreads, wide_smem(DP), stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_wide(const AttendParams& p, cudaStream_t stream) {
+  if (p.f16) return p.D <= 64 ? launch<true, 64>(p, stream) : launch<true, 128>(p, stream);
+  return p.D <= 64 ? launch<false, 64>(p, stream) : launch<false, 128>(p, stream);
+}
+
+}  // namespace moe

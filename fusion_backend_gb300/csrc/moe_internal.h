@@ -384,8 +384,10 @@ struct AttendParams {
   void* out;
   float* lse;
   // set by the launch: blocks, rows and tokens of a unit's steps, columns of a
-  // part's row, i / page_size = i page_mul >> page_shift
-  int blocks, rows, chunk, width, page_shift, q_vec, slot_first;
+  // part's row, i / page_size = i page_mul >> page_shift, accesses of 16 bytes to q,
+  // of four elements to out; tensor copies of the cache: its order of dimensions,
+  // tokens a box
+  int blocks, rows, chunk, width, page_shift, q_vec, o_vec, slot_first, box;
   unsigned long long page_mul;
   // workspace: where the blocks' ranges begin, the parts' sums [2 blocks][rows]
   // [width] and their maximum and sum of weights [2 blocks][rows]
@@ -393,7 +395,7 @@ struct AttendParams {
   AttendFrom* from;
   float* part;
   float2* stat;
-  CUtensorMap tm_k, tm_v;  // of caches whose pages hold multiples of 16 tokens
+  CUtensorMap tm_k, tm_v;  // of caches whose pages hold multiples of 8 tokens
 };
 size_t attend_workspace(const AttendParams& p);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
