@@ -25,17 +25,20 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kTok = 16;  // tokens a warp and step
-
 __host__ __device__ constexpr int warps_for(int dp) { return dp <= 128 ? 8 : 4; }
-__host__ __device__ constexpr int stages_for(int dp) { return dp <= 64 ? 6 : dp == 192 ? 4 : 3; }
-__host__ __device__ constexpr int slot_bytes(int dp) { return 2 * kTok * dp * 2; }
+// tokens a warp and step: with 16 of 64 columns the steps, not the stream, took the time
+__host__ __device__ constexpr int tokens_for(int dp) { return dp <= 64 ? 32 : 16; }
+__host__ __device__ constexpr int stages_for(int dp) { return dp == 192 ? 4 : 3; }
+__host__ __device__ constexpr int slot_bytes(int dp) { return 2 * tokens_for(dp) * dp * 2; }
 __host__ __device__ constexpr int attend_smem(int dp) {
   return warps_for(dp) * stages_for(dp) * (slot_bytes(dp) + 8) + 16 * dp * 2 + 1024;  // (slots at multiples of 1024)
 }
 // Byte of 16-byte piece c of row r in a tile of keys or values: 64 columns are
 // 128 bytes of a row, swizzled; the next 64 lie behind all rows.
-MOE_DEV uint32_t piece(int r, int c) { return (c >> 3) * (kTok * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+template <int TOK>
+MOE_DEV uint32_t piece(int r, int c) {
+  return (c >> 3) * (TOK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
 
 // Non-finite: all exponent bits set.
 template <bool F16>
@@ -50,8 +53,9 @@ MOE_DEV bool odd16(uint32_t h) {
 // asynchronous copies by the lanes, each token from a page of its own.
 template <bool F16, int DP, int TERMS, bool PAGED>
 __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_constant__ AttendParams P) {
-  constexpr int W = warps_for(DP), S = stages_for(DP), kSlot = slot_bytes(DP), kChunks = DP / 8;
-  constexpr int NT = DP / 8, KS = DP / 16;
+  constexpr int W = warps_for(DP), S = stages_for(DP), kSlot = slot_bytes(DP), kChunks = DP / 8, kTok = tokens_for(DP);
+  constexpr int NT = DP / 8, KS = DP / 16, KT = kTok / 8;  // tiles of 8 columns, of 16, of 8 tokens
+  constexpr uint32_t kFull = kTok == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   constexpr bool kHoldQ = DP <= 128;  // queries stay in registers
   constexpr int kDt = F16 ? kF16 : kBf16;
   // The maximum of the sums stays while scores pass it by no more than 2^8, so that
@@ -87,14 +91,14 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   __syncthreads();
 
   const int pieces = P.D >> 3;
-  // the page of the lane's box of the step's tokens (of its token lane % 16)
+  // the page of the lane's box of the step's tokens (of its token lane % kTok)
   AttendStep ahead = now;
   int page_ahead = -1;
   const uint64_t once = policy_evict_first(), again = policy_evict_last();
   auto look = [&]() {  // the page of `ahead`
     page_ahead = -1;
     if (ahead.left <= 0) return;
-    const int i = ahead.chunk * (W * kTok) + warp * kTok + (PAGED ? lane * P.box : lane & 15);
+    const int i = ahead.chunk * (W * kTok) + warp * kTok + (PAGED ? lane * P.box : lane & (kTok - 1));
     if (i < ahead.s.len && (!PAGED || lane * P.box < kTok)) page_ahead = P.table[ahead.b * P.table_stride + attend_page(P, i)];
   };
   auto load = [&](int stage) {  // the tokens of `ahead`, then the next step's page
@@ -105,11 +109,10 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       if constexpr (PAGED) {
         const uint32_t there = __ballot_sync(kAll, ok && lane * P.box < kTok);  // boxes whose page exists
         const int count = min(max(ahead.s.len - first, 0), kTok);
-        uint32_t valid = (1u << count) - 1u;
-        if (P.box < kTok)
-          valid &= (there & 1u ? 0xFFu : 0u) | (there & 2u ? 0xFF00u : 0u);
-        else if (!there)
-          valid = 0u;
+        uint32_t valid = count >= 32 ? ~0u : (1u << count) - 1u;
+#pragma unroll
+        for (int b = 0; b < kTok / 8; ++b)
+          if (b * P.box < kTok && !(there >> b & 1u)) valid &= ~(((1u << P.box) - 1u) << (b * P.box));
         if (lane == 0) {
           if (valid)
             mbar_arrive_expect_tx(full + stage, kSlot);
@@ -133,9 +136,9 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
             tensor_load_4d(dst + kSlot / 2 + c * kTok * 128, &P.tm_v, 64 * c, x1, x2, page, full + stage, policy);
         }
       } else {
-        const int i = first + (lane & 15);
+        const int i = first + (lane & (kTok - 1));
         const bool in = ok && i < ahead.s.len;
-        const uint32_t valid = __ballot_sync(kAll, in) & 0xFFFFu;
+        const uint32_t valid = __ballot_sync(kAll, in) & kFull;
         const int slot = in ? i - attend_page(P, i) * P.page_size : 0;
         const long long page = in ? page_ahead : 0;
         const long long k_off = page * P.kc_page + (long long)slot * P.kc_slot + ahead.head * P.kc_head;
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
             const int x = j * 32 + lane, r = x / kChunks, c = x % kChunks;
             const long long ko = __shfl_sync(kAll, k_off, r), vo = __shfl_sync(kAll, v_off, r);
             const bool on = valid >> r & 1u;
-            const uint32_t to = piece(r, c);
+            const uint32_t to = piece<kTok>(r, c);
             if (c < pieces) {
               copy16(k_dst + to, on ? P.k + ko + 8 * c : P.k, on ? 16u : 0u);
               copy16(v_dst + to, on ? P.v + vo + 8 * c : P.v, on ? 16u : 0u);
@@ -176,28 +179,30 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   float o[NT][4];
   float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // rows g and g + 8 (log2 units)
   int row_t[2], row_j[2];                        // the rows' tokens (t: -1 behind the last)
+  // queries of a unit, on their way while the warps meet at the end of the one before
+  constexpr int kQueries = (16 * kChunks + 32 * W - 1) / (32 * W);
+  uint4 queries[kQueries];
+  auto ask = [&](const AttendStep& at) {
+#pragma unroll
+    for (int u = 0; u < kQueries; ++u) {
+      const int i = tid + u * 32 * W, in = at.tile * 16 + i / kChunks, c = i % kChunks;
+      queries[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < 16 * kChunks && in < at.s.n * P.G && 8 * c < P.D) {
+        const int j = in / P.G;
+        queries[u] = attend_query(P, at.s.t0 + j, at.head * P.G + in - j * P.G, c);
+      }
+    }
+  };
+  ask(now);
   while (now.left > 0) {
     if (begin) {
       begin = false;
       from_start = now.chunk == 0;
-      // queries of the unit
       const int rows = now.s.n * P.G, r0 = now.tile * 16;
-      for (int i = tid; i < 16 * kChunks; i += 32 * W) {
-        const int r = i / kChunks, c = i % kChunks;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r0 + r < rows && 8 * c < P.D) {
-          const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
-          const uint16_t* const from = P.q + (long long)(now.s.t0 + j) * P.q_stride + h * P.q_head + 8 * c;
-          if (P.q_vec) {
-            v = *reinterpret_cast<const uint4*>(from);
-          } else {
-            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = from[2 * e] | (uint32_t)from[2 * e + 1] << 16;
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        *reinterpret_cast<uint4*>(qs + r * (DP * 2) + ((c ^ (r & 7)) << 4)) = v;
+      for (int u = 0; u < kQueries; ++u) {
+        const int i = tid + u * 32 * W, r = i / kChunks, c = i % kChunks;
+        if (i < 16 * kChunks) *reinterpret_cast<uint4*>(qs + r * (DP * 2) + ((c ^ (r & 7)) << 4)) = queries[u];
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -224,41 +229,42 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
     const uint32_t valid = s_valid[warp][stage];
     if (valid) {
       const uint32_t k_at = ring_at + stage * kSlot, v_at = k_at + kSlot / 2;
-      float s[2][4] = {};
-      {
-        const int r = (lane & 7) + ((lane >> 4) << 3);
+      float s[KT][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t a[4];
+        if constexpr (kHoldQ) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = qf[ks][e];
+        } else {
+          const int qr = lane & 15;
+          ldmatrix4(a, q_at + qr * (DP * 2) + (((2 * ks + (lane >> 4)) ^ (qr & 7)) << 4));
+        }
+#pragma unroll
+        for (int n = 0; n < KT; n += 2) {
+          const int r = 8 * n + (lane & 7) + ((lane >> 4) << 3);
           uint32_t b[4];
-          ldmatrix4(b, k_at + piece(r, 2 * ks + ((lane >> 3) & 1)));
-          if constexpr (kHoldQ) {
-            mma16<F16>(s[0], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b[0], b[1]);
-            mma16<F16>(s[1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b[2], b[3]);
-          } else {
-            uint32_t a[4];
-            const int qr = lane & 15;
-            ldmatrix4(a, q_at + qr * (DP * 2) + (((2 * ks + (lane >> 4)) ^ (qr & 7)) << 4));
-            mma16<F16>(s[0], a[0], a[1], a[2], a[3], b[0], b[1]);
-            mma16<F16>(s[1], a[0], a[1], a[2], a[3], b[2], b[3]);
-          }
+          ldmatrix4(b, k_at + piece<kTok>(r, 2 * ks + ((lane >> 3) & 1)));
+          mma16<F16>(s[n], a[0], a[1], a[2], a[3], b[0], b[1]);
+          mma16<F16>(s[n + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
         }
       }
       if (P.softcap > 0.f) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < KT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] = c2 * attend_tanh(s[n][e] * c1);
       } else {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < KT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] *= c1;
       }
       const int first = now.chunk * (W * kTok) + warp * kTok, own = first - (now.s.len - now.s.n);
       bool odd_tile = false;
-      if (valid != 0xFFFFu || own + kTok > 0) {
+      if (valid != kFull || own + kTok > 0) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < KT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 8 * n + 2 * q + (e & 1), x = e >> 1;
@@ -278,8 +284,12 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         odd_tile = __any_sync(kAll, odd);
       }
       // running maximum and sum
-      float a0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float a1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < KT; ++n) {
+        a0 = fmaxf(a0, fmaxf(s[n][0], s[n][1]));
+        a1 = fmaxf(a1, fmaxf(s[n][2], s[n][3]));
+      }
 #pragma unroll
       for (int x = 1; x < 4; x <<= 1) {
         a0 = fmaxf(a0, __shfl_xor_sync(kAll, a0, x));
@@ -309,7 +319,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
             sees[x] = (valid >> i & 1u) && row_t[x] >= 0 && attend_sees(P, row_t[x], row_j[x], own + i);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + stage * kSlot + kSlot / 2 + piece(i, n) +
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + stage * kSlot + kSlot / 2 + piece<kTok>(i, n) +
                                                                   4 * q);
             float v[2];
             unpack2(kDt, w, v[0], v[1]);
@@ -328,7 +338,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       }
       const float b0 = attend_base(m0) - kUp, b1 = attend_base(m1) - kUp;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < KT; ++n) {
         s[n][0] = exp2_fast(s[n][0] - b0);
         s[n][1] = exp2_fast(s[n][1] - b0);
         s[n][2] = exp2_fast(s[n][2] - b1);
@@ -337,11 +347,11 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         l1 += s[n][2] + s[n][3];
       }
       // a weight = the sum of TERMS numbers, each the rest rounded
-      uint32_t p[TERMS][4];
+      uint32_t p[TERMS][2 * KT];
 #pragma unroll
       for (int x = 0; x < TERMS; ++x)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < KT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t w = pack2(kDt, s[n][2 * e], s[n][2 * e + 1]);
@@ -353,20 +363,26 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
               s[n][2 * e + 1] -= hi;
             }
           }
-      const int r = (lane & 7) + (lane & 8);
 #pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t b[4];
-        ldmatrix4_trans(b, v_at + piece(r, n + (lane >> 4)));
+      for (int n = 0; n < NT; n += 2)
 #pragma unroll
-        for (int x = TERMS - 1; x >= 0; --x) {
-          mma16<F16>(o[n], p[x][0], p[x][1], p[x][2], p[x][3], b[0], b[1]);
-          mma16<F16>(o[n + 1], p[x][0], p[x][1], p[x][2], p[x][3], b[2], b[3]);
+        for (int k = 0; k < KT / 2; ++k) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, v_at + piece<kTok>(16 * k + (lane & 15), n + (lane >> 4)));
+#pragma unroll
+          for (int x = TERMS - 1; x >= 0; --x) {
+            mma16<F16>(o[n], p[x][4 * k], p[x][4 * k + 1], p[x][4 * k + 2], p[x][4 * k + 3], b[0], b[1]);
+            mma16<F16>(o[n + 1], p[x][4 * k], p[x][4 * k + 1], p[x][4 * k + 2], p[x][4 * k + 3], b[2], b[3]);
+          }
         }
-      }
     }
     const bool end = now.chunk + 1 == now.s.chunks;
     if (end || now.left == 1) {
+      if (now.left > 1) {
+        AttendStep next = now;
+        next.next(P);
+        ask(next);
+      }
       // the warps' sums meet: each leaves its own in the slot that it has just used
 #pragma unroll
       for (int x = 1; x < 4; x <<= 1) {
@@ -416,10 +432,15 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
         const long long t = now.s.t0 + j;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float y[4] = {v.x, v.y, v.z, v.w};
+        float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+        if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
+        const long long to = t * P.o_stride + h * P.o_head + d;
+        if (P.o_vec) {
+          elem_store4(P.out, P.out_dtype, to, y);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          elem_store(P.out, P.out_dtype, t * P.o_stride + h * P.o_head + d + e, l == 0.f ? 0.f : y[e] * inv);
+          for (int e = 0; e < 4; ++e) elem_store(P.out, P.out_dtype, to + e, y[e]);
+        }
         if (d == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       fence_proxy_async();
@@ -438,67 +459,101 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   if (!PAGED) copy_wait<0>();
 }
 
-// Joins the parts of a unit: block (c, y) those of the unit that goes on in block
-// c's range, if it began in the range before it, for a share of its rows.  With few
-// parts a warp a row, else all warps a row.
-constexpr int kJoinWarps = 4;
+// Joins the parts of a unit.  Its rows are shared by the blocks (c, y) of the ranges
+// c in which it goes on; with few parts a warp a row, else all warps a row.
+constexpr int kJoinWarps = 8;
+template <int NV>  // accesses of 128 columns a row
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_constant__ AttendParams P) {
-  __shared__ float s_o[kJoinWarps][kAttendMaxD];
+  __shared__ float4 s_o[kJoinWarps][32 * NV];
   __shared__ float s_l[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   pdl_wait();
   const AttendFrom at = P.from[c];
   if (at.chunk == 0) return;
   const long long unit = at.share.from(c) - at.chunk;
-  if (unit < at.share.from(c - 1)) return;
   // the first part begins its unit, the others go on
-  const int c0 = c - 1, c1 = at.share.block_of(unit + at.chunks - 1);
-  const int rows = min(at.n * P.G - at.tile * P.rows, P.rows), each = P.rows / gridDim.y;
-  const bool together = each == 1 || c1 - c0 >= 2 * kJoinWarps;
-  for (int r = blockIdx.y * each + (together ? 0 : warp); r < min(rows, (int)(blockIdx.y + 1) * each);
-       r += together ? 1 : kJoinWarps) {
+  const int c0 = at.share.block_of(unit), c1 = at.share.block_of(unit + at.chunks - 1), parts = c1 - c0 + 1;
+  const int rows = min(at.n * P.G - at.tile * P.rows, P.rows);
+  const bool together = parts > kJoinWarps;
+  const int workers = (parts - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
+  for (int k = together ? 0 : warp;; k += together ? 1 : kJoinWarps) {
+    const int r = worker + workers * k;
+    if (r >= rows) break;
     auto slot_of = [&](int i) { return (long long)(i == c0 ? 2 * c0 + 1 : 2 * i) * P.rows + r; };
+    const int first = c0 + (together ? warp : 0), step = together ? kJoinWarps : 1;
     float m = -INFINITY;
     for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, P.stat[slot_of(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     const float base = attend_base(m);
-    float l = 0.f, acc[kAttendMaxD / 32] = {};
-#pragma unroll 4
-    for (int i = c0 + (together ? warp : 0); i <= c1; i += together ? kJoinWarps : 1) {
-      const float2 st = P.stat[slot_of(i)];
-      const float f = exp2_fast(st.x - base);
-      l = fmaf(st.y, f, l);
-      const float* const row = P.part + slot_of(i) * P.width;
+    float l = 0.f;
+    float4 acc[NV];
 #pragma unroll
-      for (int e = 0; e < kAttendMaxD / 32; ++e)
-        if (lane + 32 * e < P.D) acc[e] = fmaf(row[lane + 32 * e], f, acc[e]);
+    for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = first; i0 <= c1; i0 += 8 * step) {
+      float2 st[8];
+      float4 a[8][NV];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = min(i0 + u * step, c1);
+        st[u] = P.stat[slot_of(i)];
+        const float* const row = P.part + slot_of(i) * P.width;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          a[u][v] = 4 * lane + 128 * v < P.D ? *reinterpret_cast<const float4*>(row + 4 * lane + 128 * v)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (i0 + u * step > c1) break;
+        const float f = exp2_fast(st[u].x - base);
+        l = fmaf(st[u].y, f, l);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          acc[v].x = fmaf(a[u][v].x, f, acc[v].x);
+          acc[v].y = fmaf(a[u][v].y, f, acc[v].y);
+          acc[v].z = fmaf(a[u][v].z, f, acc[v].z);
+          acc[v].w = fmaf(a[u][v].w, f, acc[v].w);
+        }
+      }
+    }
+    if (together) {
+      if (lane == 0) s_l[warp] = l;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) s_o[warp][lane + 32 * v] = acc[v];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll 1
+        for (int w = 1; w < kJoinWarps; ++w) {
+          l += s_l[w];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const float4 o = s_o[w][lane + 32 * v];
+            acc[v].x += o.x, acc[v].y += o.y, acc[v].z += o.z, acc[v].w += o.w;
+          }
+        }
+      }
+      __syncthreads();
+      if (warp > 0) continue;
     }
     const int in = at.tile * P.rows + r, j = in / P.G, h = at.head * P.G + in - j * P.G;
     const long long t = at.t0 + j, out = t * P.o_stride + h * P.o_head;
-    if (!together) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int e = 0; e < kAttendMaxD / 32; ++e)
-        if (lane + 32 * e < P.D)
-          elem_store(P.out, P.out_dtype, out + lane + 32 * e, l == 0.f ? 0.f : acc[e] / l);
-      if (lane == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      continue;
+    for (int v = 0; v < NV; ++v) {
+      const int d = 4 * lane + 128 * v;
+      if (d >= P.D) continue;
+      float y[4] = {acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv};
+      if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
+      if (P.o_vec) {
+        elem_store4(P.out, P.out_dtype, out + d, y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) elem_store(P.out, P.out_dtype, out + d + e, y[e]);
+      }
     }
-#pragma unroll
-    for (int e = 0; e < kAttendMaxD / 32; ++e) s_o[warp][lane + 32 * e] = acc[e];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
-    for (int d = tid; d < P.D; d += 32 * kJoinWarps) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][d];
-      elem_store(P.out, P.out_dtype, out + d, l == 0.f ? 0.f : v / l);
-    }
-    if (tid == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    __syncthreads();
+    if (lane == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -551,7 +606,9 @@ cudaError_t launch_terms(const AttendParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream) {
-  return launch_behind(k_attend_join, dim3(p.blocks, p.rows < 32 ? p.rows : 32), 32 * kJoinWarps, 0, stream, p);
+  const dim3 grid(p.blocks, p.rows / 8 < 8 ? p.rows / 4 : p.rows / 8);
+  return p.width <= 128 ? launch_behind(k_attend_join<1>, grid, 32 * kJoinWarps, 0, stream, p)
+                        : launch_behind(k_attend_join<2>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
 // Rows of a unit: 128 (k_attend_wide) where a sequence has more than 16 on average,
@@ -583,7 +640,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   const bool wide = attend_rows(p) == 128 && paged && (p.f16 || p.out_dtype != kF32);
   const int dp = width_for(p.D);
   p.rows = wide ? 128 : 16;
-  p.chunk = wide ? 128 : warps_for(dp) * kTok;
+  p.chunk = wide ? 128 : warps_for(dp) * tokens_for(dp);
   p.width = dp;
   uint8_t* w = static_cast<uint8_t*>(p.ws);
   p.from = reinterpret_cast<AttendFrom*>(w);

@@ -151,6 +151,16 @@ MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
   return a;
 }
 
+// Elements 8 c .. 8 c + 7 of a query.
+MOE_DEV uint4 attend_query(const AttendParams& P, int t, int h, int c) {
+  const uint16_t* const from = P.q + (long long)t * P.q_stride + h * P.q_head + 8 * c;
+  if (P.q_vec) return *reinterpret_cast<const uint4*>(from);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = from[2 * e] | (uint32_t)from[2 * e + 1] << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Whether row t, the j-th of its sequence, sees the token `own` places behind the
 // first of the sequence's own ones.
 MOE_DEV bool attend_sees(const AttendParams& P, int t, int j, int own) {

@@ -52,17 +52,8 @@ __device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64
       "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 32 lanes x 16 (64) columns, and the wait for them: nothing can use them before it
-__device__ __forceinline__ void tmem_read16(uint32_t taddr, uint32_t* r) {
+// 32 lanes x 16 or 32 columns; a read waits for itself: nothing can use it before
+__device__ __forceinline__ void tmem_read16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}"
@@ -72,24 +63,41 @@ __device__ __forceinline__ void tmem_read16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_read64(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%"
-      "26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%"
-      "50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}"
-      ", [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      "26,%27,%28,%29,%30,%31}"
+      ", [%32];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_write16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16}"
+      ";" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_write32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31,%32}"
+      ";" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <bool F16>
 MOE_DEV bool odd16(uint32_t h) {  // not finite
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             for (int term = 1; term >= 0; --term)
 #pragma unroll
               for (int ks = 0; ks < kTok / 16; ++ks)
-                umma_ts(tmem + kOut + x * DP, tmem + x * 128 + buf * 64 + term * 32 + ks * 8,
+                umma_ts(tmem + kOut + x * DP, tmem + x * 128 + buf * 64 + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8,
                         tc::smem_desc(v_at + ks * 16 * 128, kTok * 128, 1024), o_desc, !(fresh[x] && term == 1 && ks == 0));
             tc::umma_commit(empty + slot);
             tc::umma_commit(&o_done[x]);
@@ -341,24 +349,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       uint8_t* const to = qs + (unit & 1) * kQ;
       const int rows = s.s.n * P.G, r0 = s.tile * 128;
       const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;  // the scale's sign
-#pragma unroll 4
-      for (int x = th; x < 128 * DP / 8; x += 64) {
-        const int r = x / (DP / 8), c = x % (DP / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r0 + r < rows && 8 * c < P.D) {
-          const int j = (r0 + r) / P.G, h = s.head * P.G + (r0 + r) - j * P.G;
-          const uint16_t* const from = P.q + (long long)(s.s.t0 + j) * P.q_stride + h * P.q_head + 8 * c;
-          if (P.q_vec) {
-            v = *reinterpret_cast<const uint4*>(from);
-          } else {
-            uint32_t w[4];
+      // eight pieces of 16 bytes are asked for at a time
+#pragma unroll 1
+      for (int x0 = th; x0 < 128 * DP / 8; x0 += 8 * 64) {
+        uint4 v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = from[2 * e] | (uint32_t)from[2 * e + 1] << 16;
-            v = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int u = 0; u < 8; ++u) {
+          const int x = x0 + 64 * u, r = x / (DP / 8), c = x % (DP / 8);
+          v[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r0 + r < rows && 8 * c < P.D) {
+            const int j = (r0 + r) / P.G, h = s.head * P.G + (r0 + r) - j * P.G;
+            v[u] = attend_query(P, s.s.t0 + j, h, c);
           }
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
         }
-        *reinterpret_cast<uint4*>(to + (c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int x = x0 + 64 * u, r = x / (DP / 8), c = x % (DP / 8);
+          *reinterpret_cast<uint4*>(to + (c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+              make_uint4(v[u].x ^ flip, v[u].y ^ flip, v[u].z ^ flip, v[u].w ^ flip);
+        }
       }
       fence_proxy_async();
       mbar_arrive(&q_full[unit & 1]);
@@ -433,34 +442,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
           const uint32_t at = tmem + lanes + x * 128 + buf * 64;
           await(&s_full[x][buf], count >> 1 & 1, dead);
           tc::tc_fence_after();
-          uint32_t w[kTok];
-          tmem_read64(at, w);
-          float s[kTok];
-#pragma unroll
-          for (int e = 0; e < kTok; ++e) s[e] = __uint_as_float(w[e]);
-          if (P.softcap > 0.f) {
-#pragma unroll
-            for (int e = 0; e < kTok; ++e) s[e] = c2 * attend_tanh(s[e] * c1);
-          }
-          const int first = first_of(a, x);
           const uint32_t boxes = s_boxes[x][i & 15], all = kTok / P.box == 8 ? 0xFFu : 0xFu;
-          if (mixed(a, x) || boxes != all) {
-            uint64_t seen = seen_tokens(P, a.s, first, t, j);
+          const bool part = mixed(a, x) || boxes != all;
+          uint64_t seen = ~0ull;
+          if (part) {
+            seen = seen_tokens(P, a.s, first_of(a, x), t, j);
             for (int b = 0; b < kTok / P.box; ++b)
               if (!(boxes >> b & 1u)) seen &= ~(((1ull << P.box) - 1ull) << (b * P.box));
-            const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(lo >> e & 1u)) s[e] = -INFINITY;
-              if (!(hi >> e & 1u)) s[32 + e] = -INFINITY;
-            }
           }
-          float top[4];
+          // twice over the scores, 32 columns at a time: short loops, since what each
+          // warp runs through once a step comes from beyond the nearest instruction cache
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
+            tmem_read32(at + 32 * h, w);
+            if (P.softcap > 0.f || part) {
+              if (P.softcap > 0.f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top[e] = s[e];
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(c2 * attend_tanh(__uint_as_float(w[e]) * c1));
+              }
+              if (part) {
+                const uint32_t bits = (uint32_t)(seen >> (32 * h));
 #pragma unroll
-          for (int e = 4; e < kTok; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul;
+                for (int e = 0; e < 32; ++e)
+                  if (!(bits >> e & 1u)) w[e] = 0xFF800000u;  // -inf
+              }
+              tmem_write32(at + 32 * h, w);
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(w[e]));
+            mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          }
+          if (P.softcap > 0.f || part) tmem_wait_st();
+          mx *= mul;
           if (!some) {
             m = mx;
           } else if (__any_sync(kAll, mx > m + kLazy)) {
@@ -475,18 +491,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
               tmem_read16(tmem + lanes + kOut + x * DP + c, o);
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(tmem + lanes + kOut + x * DP + c, o);
+              tmem_write16(tmem + lanes + kOut + x * DP + c, o);
             }
           }
           const float base = attend_base(m) - kUp;
           float sum[4] = {};
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            uint32_t hi[16], lo[16];
+            uint32_t w[32], hi[16], lo[16];
+            tmem_read32(at + 32 * h, w);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = exp2_fast(fmaf(s[32 * h + 2 * e], mul, -base));
-              const float p1 = exp2_fast(fmaf(s[32 * h + 2 * e + 1], mul, -base));
+              const float p0 = exp2_fast(fmaf(__uint_as_float(w[2 * e]), mul, -base));
+              const float p1 = exp2_fast(fmaf(__uint_as_float(w[2 * e + 1]), mul, -base));
               sum[2 * (e & 1)] += p0;
               sum[2 * (e & 1) + 1] += p1;
               hi[e] = pack2(kDt, p0, p1);
@@ -494,8 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
               unpack2(kDt, hi[e], a0, a1);
               lo[e] = pack2(kDt, p0 - a0, p1 - a1);
             }
-            tmem_st16(at + 16 * h, hi);
-            tmem_st16(at + 32 + 16 * h, lo);
+            // (where the scores of these 32 tokens were)
+            tmem_write16(at + 32 * h, hi);
+            tmem_write16(at + 32 * h + 16, lo);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
