@@ -581,6 +581,7 @@ bool encode_cache(CUtensorMap* m, const AttendParams& p, const uint16_t* base, l
 
 template <bool F16, int DP, int TERMS, bool PAGED>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+  static_assert(warps_for(DP) * tokens_for(DP) == (DP <= 64 ? 256 : DP <= 128 ? 128 : 64), "launch_attend's chunks");
   static_assert(attend_smem(DP) <= 229376, "shared memory");
   auto* const kern = k_attend<F16, DP, TERMS, PAGED>;
   static SmemLimit limit;
@@ -597,6 +598,12 @@ cudaError_t launch_width(const AttendParams& p, cudaStream_t stream) {
                       : launch<F16, 256, TERMS, PAGED>(p, stream);
 }
 
+cudaError_t launch_join(const AttendParams& p, cudaStream_t stream) {
+  const dim3 grid(p.blocks, p.rows / 4);
+  return p.width <= 128 ? launch_behind(k_attend_join<1>, grid, 32 * kJoinWarps, 0, stream, p)
+                        : launch_behind(k_attend_join<2>, grid, 32 * kJoinWarps, 0, stream, p);
+}
+
 template <bool PAGED>
 cudaError_t launch_terms(const AttendParams& p, cudaStream_t stream) {
   if (p.f16) return launch_width<true, 2, PAGED>(p, stream);
@@ -605,14 +612,8 @@ cudaError_t launch_terms(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream) {
-  const dim3 grid(p.blocks, p.rows / 8 < 8 ? p.rows / 4 : p.rows / 8);
-  return p.width <= 128 ? launch_behind(k_attend_join<1>, grid, 32 * kJoinWarps, 0, stream, p)
-                        : launch_behind(k_attend_join<2>, grid, 32 * kJoinWarps, 0, stream, p);
-}
-
-// Rows of a unit: 128 (k_attend_wide) where a sequence has more than 16 on average,
-// whatever the rest of the call; its heads have to fit into tensor memory.
+// Rows of a unit: up to 128 (k_attend_wide) where a sequence has more than 16 on
+// average, whatever the rest of the call; its heads have to fit into tensor memory.
 static int attend_rows(const AttendParams& p) {
   return p.D <= 128 && (long long)p.T * p.G > 16ll * p.B ? 128 : 16;
 }
@@ -638,20 +639,21 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
                      encode_cache(&p.tm_v, p, p.v, p.vc_page, p.vc_slot, p.vc_head);
   // (three numbers a weight do not fit beside the scores)
   const bool wide = attend_rows(p) == 128 && paged && (p.f16 || p.out_dtype != kF32);
-  const int dp = width_for(p.D);
-  p.rows = wide ? 128 : 16;
-  p.chunk = wide ? 128 : warps_for(dp) * tokens_for(dp);
+  const int dp = width_for(p.D), slots = wide ? 128 : 16;  // rows of a part
+  // (whole tokens of a group's heads)
+  p.rows = wide ? 128 / p.G * p.G : 16;
+  p.chunk_log = wide || dp >= 128 ? 7 : 8;
+  if (dp > 128) p.chunk_log = 6;
   p.width = dp;
   uint8_t* w = static_cast<uint8_t*>(p.ws);
   p.from = reinterpret_cast<AttendFrom*>(w);
   w += align256(kMaxBlocks * sizeof(AttendFrom));
   p.stat = reinterpret_cast<float2*>(w);
-  w += align256((size_t)2 * kMaxBlocks * p.rows * 8);
+  w += align256((size_t)2 * kMaxBlocks * slots * 8);
   p.part = reinterpret_cast<float*>(w);
-  const cudaError_t e = wide    ? launch_attend_wide(p, stream)
-                        : paged ? launch_terms<true>(p, stream)
-                                : launch_terms<false>(p, stream);
-  return e != cudaSuccess ? e : launch_attend_join(p, stream);
+  if (wide) return launch_attend_wide(p, stream);
+  const cudaError_t e = paged ? launch_terms<true>(p, stream) : launch_terms<false>(p, stream);
+  return e != cudaSuccess ? e : launch_join(p, stream);
 }
 
 }  // namespace moe

@@ -27,6 +27,11 @@ struct AttendSeq {
   MOE_DEV long long work(int heads) const { return (long long)tiles * heads * chunks; }
 };
 
+// a / b, by 32 bits where they do: a division in 64 takes a microsecond of a thread.
+MOE_DEV long long attend_div(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 MOE_DEV AttendSeq attend_seq(const AttendParams& P, int b) {
   AttendSeq s;
   s.t0 = min(max(P.q_start[b], 0), P.T);
@@ -34,7 +39,7 @@ MOE_DEV AttendSeq attend_seq(const AttendParams& P, int b) {
   const long long most = (long long)P.max_pages * P.page_size;
   s.len = (int)min((long long)max(P.lens[b], 0), most);
   s.tiles = (s.n * P.G + P.rows - 1) / P.rows;
-  s.chunks = (int)(((long long)s.len + P.chunk - 1) / P.chunk);
+  s.chunks = (int)(((uint32_t)s.len + (1u << P.chunk_log) - 1u) >> P.chunk_log);
   return s;
 }
 
@@ -45,7 +50,7 @@ struct AttendShare {
   MOE_DEV long long from(int c) const { return base * c + min(c, rest); }
   MOE_DEV int block_of(long long w) const {  // whose range holds chunk w
     const long long more = (base + 1) * rest;
-    return (int)(w < more ? w / (base + 1) : rest + (w - more) / base);
+    return (int)(w < more ? attend_div(w, base + 1) : rest + attend_div(w - more, base));
   }
 };
 
@@ -100,7 +105,8 @@ MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) total += scratch[w];
-  const AttendShare share{total / gridDim.x, (int)(total % gridDim.x)};
+  const long long even = attend_div(total, gridDim.x);
+  const AttendShare share{even, (int)(total - even * gridDim.x)};
   const long long from = share.from(blockIdx.x), to = share.from(blockIdx.x + 1);
   long long base = 0;
   for (int b0 = 0; b0 < P.B && from < to && base <= from; b0 += THREADS) {
@@ -133,9 +139,9 @@ MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
   if (a.left > 0) {
     a.b = (int)scratch[W];
     a.s = attend_seq(P, a.b);
-    const long long at = scratch[W + 1], unit = at / a.s.chunks;
+    const long long at = scratch[W + 1], unit = attend_div(at, a.s.chunks);
     a.chunk = (int)(at - unit * a.s.chunks);
-    a.head = (int)(unit / a.s.tiles);
+    a.head = (int)attend_div(unit, a.s.tiles);
     a.tile = (int)(unit - (long long)a.head * a.s.tiles);
   }
   if (tid == 0) P.from[blockIdx.x] = AttendFrom{share, a.s.t0, a.s.n, a.s.chunks, a.head, a.tile, a.chunk};
@@ -188,9 +194,7 @@ MOE_DEV float attend_tanh(float x) {
 // exp2(-inf - 0) = 0.
 MOE_DEV float attend_base(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Joins the parts of the units that several blocks share (moe_attend.cu).
-cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t stream);
-// Units of 128 rows (moe_attend_wide.cu).
-cudaError_t launch_attend_wide(const AttendParams& p, cudaStream_t stream);
+// Units of up to 128 rows and the join of their parts (moe_attend_wide.cu).
+cudaError_t launch_attend_wide(AttendParams p, cudaStream_t stream);
 
 }  // namespace moe

@@ -105,6 +105,9 @@ MOE_DEV bool odd16(uint32_t h) {  // not finite
   return (h & e) == e;
 }
 
+// A shared-memory descriptor with its address moved by `bytes`.
+MOE_DEV uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
 // A wait that ran out once is not waited for again.
 MOE_DEV void await(uint64_t* bar, uint32_t parity, bool& dead) {
   if (!dead) dead = !mbar_wait(bar, parity);
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         mbar_init(&p_full[x][b], 128);
       }
       mbar_init(&o_done[x], 1);
-      mbar_init(&q_full[x], 64);
+      mbar_init(&q_full[x], P.q_box ? 1 : 64);
       mbar_init(&q_empty[x], 1);
     }
     mbar_init(&o_free, 256);
@@ -194,6 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
     // ------------------------------------------------------------ products
     if (lane == 0) {
       const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16), o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
+      // descriptors of the first slot and buffer; of values: columns are what lies together
+      const uint64_t k_desc0 = tc::smem_desc(smem_u32(smem), 16, 1024), q_desc0 = tc::smem_desc(smem_u32(qs), 16, 1024),
+                     v_desc0 = tc::smem_desc(smem_u32(smem), kTok * 128, 1024);
       int slot = 0, unit = 0, count[2] = {0, 0}, cleaned = 0;
       uint32_t turn = 0;
       auto next_slot = [&] {
@@ -222,12 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             if (!there(a, x)) continue;
             await(full + slot, turn, dead);
             tc::tc_fence_after();
-            const uint32_t k_at = smem_u32(smem + slot * kSlot), q_at = smem_u32(qs + (unit & 1) * kQ);
+            const uint64_t k_desc = desc_at(k_desc0, slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
             const int buf = count[x] & 1;
+            const uint32_t to = tmem + x * 128 + buf * 64;
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks)
-              tc::umma(tmem + x * 128 + buf * 64, tc::smem_desc(q_at + (ks >> 2) * 128 * 128 + (ks & 3) * 32, 16, 1024),
-                       tc::smem_desc(k_at + (ks >> 2) * kTok * 128 + (ks & 3) * 32, 16, 1024), s_desc, ks > 0);
+              tc::umma(to, desc_at(q_desc, (ks >> 2) * 128 * 128 + (ks & 3) * 32),
+                       desc_at(k_desc, (ks >> 2) * kTok * 128 + (ks & 3) * 32), s_desc, ks > 0);
             tc::umma_commit(empty + slot);
             tc::umma_commit(&s_full[x][buf]);
             next_slot();
@@ -248,13 +255,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             await(&p_full[x][buf], c >> 1 & 1, dead);
             if (fresh[x] && unit_before > 0) await(&o_free, (unit_before - 1) & 1, dead);
             tc::tc_fence_after();
-            const uint32_t v_at = smem_u32(smem + slot * kSlot);
+            const uint64_t v_desc = desc_at(v_desc0, slot * kSlot);
+            const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64;
+            uint32_t add = !fresh[x];
 #pragma unroll
             for (int term = 1; term >= 0; --term)
 #pragma unroll
-              for (int ks = 0; ks < kTok / 16; ++ks)
-                umma_ts(tmem + kOut + x * DP, tmem + x * 128 + buf * 64 + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8,
-                        tc::smem_desc(v_at + ks * 16 * 128, kTok * 128, 1024), o_desc, !(fresh[x] && term == 1 && ks == 0));
+              for (int ks = 0; ks < kTok / 16; ++ks) {
+                umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc, add);
+                add = 1u;
+              }
             tc::umma_commit(empty + slot);
             tc::umma_commit(&o_done[x]);
             next_slot();
@@ -310,7 +320,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
     };
     AttendStep before = a;
     Where now = look(a), then = now;
+    int unit = 0;
     for (; a.left > 0; ++i) {
+      if (P.q_box && (i == 0 || last_of_unit(before))) {
+        // the unit's queries: q_box tokens of the group's heads are its rows in their order
+        if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
+        if (lane == 0) mbar_arrive_expect_tx(&q_full[unit & 1], kHalves * 128 * P.G * P.q_box);
+        __syncwarp();
+        if (lane < kHalves)
+          tensor_load_3d(qs + (unit & 1) * kQ + lane * 128 * 128, &P.tm_q, 64 * lane, a.head * P.G,
+                         a.s.t0 + a.tile * P.q_box, &q_full[unit & 1], again);
+        ++unit;
+      }
       AttendStep next = a;
       next.next(P);
       const Where soon = look(next);
@@ -343,12 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       }
     };
     auto queries = [&](const AttendStep& s) {
-      if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
       // (marks of units far behind, cleared for those as far ahead)
+      if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
       if (th == 0) s_odd[(unit + kOddUnits / 2) % kOddUnits] = 0u;
+      if (P.q_box) return;  // by tensor copies
       uint8_t* const to = qs + (unit & 1) * kQ;
-      const int rows = s.s.n * P.G, r0 = s.tile * 128;
-      const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;  // the scale's sign
+      const int rows = s.s.n * P.G, r0 = s.tile * P.rows;
       // eight pieces of 16 bytes are asked for at a time
 #pragma unroll 1
       for (int x0 = th; x0 < 128 * DP / 8; x0 += 8 * 64) {
@@ -357,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         for (int u = 0; u < 8; ++u) {
           const int x = x0 + 64 * u, r = x / (DP / 8), c = x % (DP / 8);
           v[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r0 + r < rows && 8 * c < P.D) {
+          if (r < P.rows && r0 + r < rows && 8 * c < P.D) {
             const int j = (r0 + r) / P.G, h = s.head * P.G + (r0 + r) - j * P.G;
             v[u] = attend_query(P, s.s.t0 + j, h, c);
           }
@@ -365,8 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int x = x0 + 64 * u, r = x / (DP / 8), c = x % (DP / 8);
-          *reinterpret_cast<uint4*>(to + (c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-              make_uint4(v[u].x ^ flip, v[u].y ^ flip, v[u].z ^ flip, v[u].w ^ flip);
+          *reinterpret_cast<uint4*>(to + (c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[u];
         }
       }
       fence_proxy_async();
@@ -425,12 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     auto kept = [](float v) { return fminf(v, 3.4e38f); };  // (finite: 0 times infinity)
     const float scale = fabsf(P.scale);
+    const uint32_t flip = P.scale < 0.f ? 0x80000000u : 0u;  // the scale's sign goes to the scores
     // (not 0 either: masked scores of -inf)
     const float mul = P.softcap > 0.f ? 1.f : fmaxf(kept(scale * kLog2e), 1.2e-38f);
     const float c1 = P.softcap > 0.f ? kept(scale / P.softcap) : 0.f, c2 = kept(P.softcap * kLog2e);
     int count = 0, unit = 0, i = 0;
     while (a.left > 0) {
-      const int r = a.tile * 128 + row, rows = a.s.n * P.G, j = r / P.G, t = r < rows ? a.s.t0 + j : -1;
+      const int r = a.tile * P.rows + row, rows = a.s.n * P.G, j = r / P.G;
+      const int t = row < P.rows && r < rows ? a.s.t0 + j : -1;
       const int chunk0 = a.chunk;
       float m = -INFINITY, l = 0.f;
       bool some = false, end = false, other = false;  // this stream, the second one have had a chunk
@@ -443,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
           await(&s_full[x][buf], count >> 1 & 1, dead);
           tc::tc_fence_after();
           const uint32_t boxes = s_boxes[x][i & 15], all = kTok / P.box == 8 ? 0xFFu : 0xFu;
-          const bool part = mixed(a, x) || boxes != all;
+          const bool part = mixed(a, x) || boxes != all, changed = part || P.softcap > 0.f || flip;
           uint64_t seen = ~0ull;
           if (part) {
             seen = seen_tokens(P, a.s, first_of(a, x), t, j);
@@ -457,7 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
           for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
             tmem_read32(at + 32 * h, w);
-            if (P.softcap > 0.f || part) {
+            if (changed) {
+              if (flip) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] ^= flip;
+              }
               if (P.softcap > 0.f) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(c2 * attend_tanh(__uint_as_float(w[e]) * c1));
@@ -475,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(w[e]));
             mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
           }
-          if (P.softcap > 0.f || part) tmem_wait_st();
+          if (changed) tmem_wait_st();
           mx *= mul;
           if (!some) {
             m = mx;
@@ -576,9 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
               if (c + e < P.D) elem_store(P.out, P.out_dtype, to + e, v[e]);
           }
         } else {
-          float* const to = P.part + (slot * 128 + row) * P.width + c;
+          // four columns of all rows lie together: the lanes' rows are neighbours
+          float4* const to = reinterpret_cast<float4*>(P.part) + (slot * (DP / 4) + c / 4) * 128 + row;
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < 4; ++e) to[128 * e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       }
       tc::tc_fence_before();
@@ -601,6 +628,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   }
 }
 
+// Joins the parts of a unit, as k_attend_join does.  An item is 8 rows of 16 columns:
+// lane 8 q + r has row r, columns 4 q .. 4 q + 3.  With few parts a warp an item, else
+// all warps of a block.
+constexpr int kJoinWarps = 8, kJoinShare = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join_wide(const __grid_constant__ AttendParams P) {
+  __shared__ float4 s_o[kJoinWarps][32];
+  __shared__ float s_l[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  pdl_wait();
+  const AttendFrom at = P.from[c];
+  if (at.chunk == 0) return;
+  const long long unit = at.share.from(c) - at.chunk;
+  const int c0 = at.share.block_of(unit), c1 = at.share.block_of(unit + at.chunks - 1), parts = c1 - c0 + 1;
+  const int rows = min(at.n * P.G - at.tile * P.rows, P.rows), groups = (P.D + 15) / 16, items = (rows + 7) / 8 * groups;
+  const bool together = parts > kJoinWarps;
+  const int worker = (c - c0 - 1) * kJoinShare + blockIdx.y, workers = (parts - 1) * kJoinShare;
+  const int quads = P.width / 4;
+  for (int i = together ? worker : worker * kJoinWarps + warp; i < items; i += together ? workers : workers * kJoinWarps) {
+    const int r = i / groups * 8 + (lane & 7), q = i % groups * 4 + (lane >> 3);
+    auto slot_of = [&](int p) { return (long long)(p == c0 ? 2 * c0 + 1 : 2 * p); };
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int p = c0; p <= c1; ++p) m = fmaxf(m, P.stat[slot_of(p) * 128 + r].x);
+    const float base = attend_base(m);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int step = together ? kJoinWarps : 1;
+#pragma unroll 1
+    for (int p0 = c0 + (together ? warp : 0); p0 <= c1; p0 += 4 * step) {
+      float2 st[4];
+      float4 a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const long long slot = slot_of(min(p0 + u * step, c1));
+        st[u] = P.stat[slot * 128 + r];
+        a[u] = reinterpret_cast<const float4*>(P.part)[(slot * quads + q) * 128 + r];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (p0 + u * step > c1) break;
+        const float f = exp2_fast(st[u].x - base);
+        l = fmaf(st[u].y, f, l);
+        o.x = fmaf(a[u].x, f, o.x);
+        o.y = fmaf(a[u].y, f, o.y);
+        o.z = fmaf(a[u].z, f, o.z);
+        o.w = fmaf(a[u].w, f, o.w);
+      }
+    }
+    if (together) {
+      s_o[warp][lane] = o;
+      s_l[warp][lane] = l;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll 1
+        for (int w = 1; w < kJoinWarps; ++w) {
+          const float4 a = s_o[w][lane];
+          l += s_l[w][lane];
+          o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
+        }
+      }
+      __syncthreads();
+      if (warp > 0) continue;
+    }
+    if (r >= rows) continue;
+    const int in = at.tile * P.rows + r, j = in / P.G, h = at.head * P.G + in - j * P.G, d = 4 * q;
+    const long long t = at.t0 + j, out = t * P.o_stride + h * P.o_head + d;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
+    if (d < P.D) {
+      if (P.o_vec) {
+        elem_store4(P.out, P.out_dtype, out, y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) elem_store(P.out, P.out_dtype, out + e, y[e]);
+      }
+    }
+    if (q == 0 && P.lse) P.lse[t * P.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
 template <bool F16, int DP>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   static_assert(wide_smem(DP) + 4096 + 2048 <= 232448, "shared memory");
@@ -613,9 +721,23 @@ cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_attend_wide(const AttendParams& p, cudaStream_t stream) {
-  if (p.f16) return p.D <= 64 ? launch<true, 64>(p, stream) : launch<true, 128>(p, stream);
-  return p.D <= 64 ? launch<false, 64>(p, stream) : launch<false, 128>(p, stream);
+cudaError_t launch_attend_wide(AttendParams p, cudaStream_t stream) {
+  // q as (column, head, token), a box the rows of a unit
+  if (p.q_vec && 2 * p.q_stride < 1ll << 40 && 2 * p.q_head < 1ll << 40) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)(2 * p.q_head), (cuuint64_t)(2 * p.q_stride)};
+    const cuuint32_t tokens = p.rows / p.G, box[3] = {64, (cuuint32_t)p.G, tokens}, ones[3] = {1, 1, 1};
+    if (tensor_map_encoder()(&p.tm_q, p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                             const_cast<uint16_t*>(p.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+      p.q_box = (int)tokens;
+  }
+  const cudaError_t e = p.f16 ? p.D <= 64 ? launch<true, 64>(p, stream) : launch<true, 128>(p, stream)
+                        : p.D <= 64 ? launch<false, 64>(p, stream)
+                                    : launch<false, 128>(p, stream);
+  if (e != cudaSuccess) return e;
+  return launch_behind(k_attend_join_wide, dim3(p.blocks, kJoinShare), 32 * kJoinWarps, 0, stream, p);
 }
 
 }  // namespace moe

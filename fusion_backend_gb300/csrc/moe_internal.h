@@ -383,11 +383,11 @@ struct AttendParams {
   const int32_t *table, *lens, *q_start, *mask;
   void* out;
   float* lse;
-  // set by the launch: blocks, rows and tokens of a unit's steps, columns of a
+  // set by the launch: blocks, rows and (log2) tokens of a unit's steps, columns of a
   // part's row, i / page_size = i page_mul >> page_shift, accesses of 16 bytes to q,
-  // of four elements to out; tensor copies of the cache: its order of dimensions,
-  // tokens a box
-  int blocks, rows, chunk, width, page_shift, q_vec, o_vec, slot_first, box;
+  // of four elements to out, tokens of a tensor copy of q (0: none); tensor copies of
+  // the cache: its order of dimensions, tokens a box
+  int blocks, rows, chunk_log, width, page_shift, q_vec, q_box, o_vec, slot_first, box;
   unsigned long long page_mul;
   // workspace: where the blocks' ranges begin, the parts' sums [2 blocks][rows]
   // [width] and their maximum and sum of weights [2 blocks][rows]
@@ -396,6 +396,7 @@ struct AttendParams {
   float* part;
   float2* stat;
   CUtensorMap tm_k, tm_v;  // of caches whose pages hold multiples of 8 tokens
+  CUtensorMap tm_q;
 };
 size_t attend_workspace(const AttendParams& p);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
