@@ -65,7 +65,6 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   constexpr float kLazy = 8.f, kUp = F16 ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ long long s_scan[40];
   __shared__ float2 s_stat[W][16];
   __shared__ uint32_t s_valid[W][S];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   }
   pdl_wait();
   pdl_launch_dependents();
-  AttendStep now = attend_begin<32 * W>(P, s_scan);
+  AttendStep now = attend_begin<32 * W>(P);
   if (now.left <= 0) return;
   // columns that no copy writes
   if (!PAGED && P.D < DP)
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         uint32_t valid = count >= 32 ? ~0u : (1u << count) - 1u;
 #pragma unroll
         for (int b = 0; b < kTok / 8; ++b)
-          if (b * P.box < kTok && !(there >> b & 1u)) valid &= ~(((1u << P.box) - 1u) << (b * P.box));
+          if (b * P.box < kTok && !(there >> b & 1u)) valid &= ~((~0u >> (32 - P.box)) << (b * P.box));
         if (lane == 0) {
           if (valid)
             mbar_arrive_expect_tx(full + stage, kSlot);
@@ -634,12 +633,14 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   p.q_vec = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_stride % 8 == 0 && p.q_head % 8 == 0;
   p.o_vec = reinterpret_cast<uintptr_t>(p.out) % (4 * elem_bytes(p.out_dtype)) == 0 && p.o_stride % 4 == 0 && p.o_head % 4 == 0;
   p.slot_first = p.kc_slot < p.kc_head;
-  p.box = p.page_size % 16 == 0 ? 16 : 8;
+  const int dp = width_for(p.D);
+  // (three numbers a weight do not fit beside the scores)
+  bool wide = attend_rows(p) == 128 && p.page_size % 8 == 0 && (p.f16 || p.out_dtype != kF32);
+  for (p.box = wide ? 64 : tokens_for(dp); p.box > 8 && p.page_size % p.box;) p.box /= 2;
   const bool paged = p.page_size % 8 == 0 && p.pages > 0 && encode_cache(&p.tm_k, p, p.k, p.kc_page, p.kc_slot, p.kc_head) &&
                      encode_cache(&p.tm_v, p, p.v, p.vc_page, p.vc_slot, p.vc_head);
-  // (three numbers a weight do not fit beside the scores)
-  const bool wide = attend_rows(p) == 128 && paged && (p.f16 || p.out_dtype != kF32);
-  const int dp = width_for(p.D), slots = wide ? 128 : 16;  // rows of a part
+  wide = wide && paged;
+  const int slots = wide ? 128 : 16;  // rows of a part
   // (whole tokens of a group's heads)
   p.rows = wide ? 128 / p.G * p.G : 16;
   p.chunk_log = wide || dp >= 128 ? 7 : 8;

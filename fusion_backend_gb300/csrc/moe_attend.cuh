@@ -86,74 +86,81 @@ struct AttendFrom {
   int t0, n, chunks, head, tile, chunk;
 };
 
-// The range of this block: its first step, also left in the workspace.  All
-// threads of the block call it; scratch: THREADS / 32 + 2 words.  Rows of sequences
-// without tokens belong to no unit: the blocks write their results here, in turn.
+// The range of this block: its first step, where it begins also left in the
+// workspace.  All threads of the block call it.  Rows of sequences without tokens
+// belong to no unit: the blocks write their results here, in turn.
 template <int THREADS>
-MOE_DEV AttendStep attend_begin(const AttendParams& P, long long* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+MOE_DEV AttendStep attend_begin(const AttendParams& P) {
   constexpr int W = THREADS / 32;
-  auto work_of = [&](int b) { return b < P.B ? attend_seq(P, b).work(P.Hkv) : 0ll; };
-  // the thread's sequences behind one another, THREADS at a time
-  const long long own = work_of(tid);
-  long long sum = own;
-  for (int b = tid + THREADS; b < P.B; b += THREADS) sum += work_of(b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) total += scratch[w];
-  const long long even = attend_div(total, gridDim.x);
-  const AttendShare share{even, (int)(total - even * gridDim.x)};
-  const long long from = share.from(blockIdx.x), to = share.from(blockIdx.x + 1);
-  long long base = 0;
-  for (int b0 = 0; b0 < P.B && from < to && base <= from; b0 += THREADS) {
-    const int b = b0 + tid;
-    const long long mine = b0 == 0 ? own : work_of(b);
-    long long upto = mine;
+  __shared__ long long s_warp[2][W], s_at;
+  __shared__ AttendSeq s_seq;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto seq_of = [&](int b) { return b < P.B ? attend_seq(P, b) : AttendSeq{0, 0, 0, 0, 0}; };
+  // what lies before the thread, and all of the block's
+  int turn = 0;
+  auto scan = [&](long long own, long long& all) {
+    long long upto = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
+    if (lane == 31) s_warp[turn][warp] = upto;
     __syncthreads();
-    if (lane == 31) scratch[warp] = upto;
-    __syncthreads();
-    long long before = base;
+    long long before = upto - own;
+    all = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      before += w < warp ? scratch[w] : 0ll;
-      base += scratch[w];
+      const long long v = s_warp[turn][w];
+      before += w < warp ? v : 0;
+      all += v;
     }
-    upto += before;
-    if (upto - mine <= from && from < upto) {
-      scratch[W] = b;
-      scratch[W + 1] = from - (upto - mine);
+    turn ^= 1;
+    return before;
+  };
+  // the sequences, THREADS at a time: mostly one round
+  AttendSeq s = seq_of(tid);
+  long long all, before = scan(s.work(P.Hkv), all), total = all, base = 0;
+  for (int b0 = THREADS; b0 < P.B; b0 += THREADS) {
+    long long more;
+    scan(seq_of(b0 + tid).work(P.Hkv), more);
+    total += more;
+  }
+  const long long even = attend_div(total, gridDim.x);
+  const AttendShare share{even, (int)(total - even * gridDim.x)};
+  const long long from = share.from(blockIdx.x), to = share.from(blockIdx.x + 1);
+  for (int b0 = 0;;) {
+    const int b = b0 + tid;
+    const long long first = base + before;
+    if (first <= from && from < first + s.work(P.Hkv)) {
+      s_seq = s;
+      s_b = b;
+      s_at = from - first;
     }
+    if (s.n > 0 && s.chunks == 0 && b % gridDim.x == blockIdx.x)
+      for (int t = s.t0; t < s.t0 + s.n; ++t)
+        for (int h = 0; h < P.Hq; ++h) {
+          for (int d = 0; d < P.D; ++d) elem_store(P.out, P.out_dtype, t * P.o_stride + h * P.o_head + d, 0.f);
+          if (P.lse) P.lse[(long long)t * P.Hq + h] = -INFINITY;
+        }
+    base += all;
+    if ((b0 += THREADS) >= P.B) break;
+    s = seq_of(b0 + tid);
+    before = scan(s.work(P.Hkv), all);
   }
   __syncthreads();
   AttendStep a = {};
   a.left = to - from;
   if (a.left > 0) {
-    a.b = (int)scratch[W];
-    a.s = attend_seq(P, a.b);
-    const long long at = scratch[W + 1], unit = attend_div(at, a.s.chunks);
-    a.chunk = (int)(at - unit * a.s.chunks);
+    a.b = s_b;
+    a.s = s_seq;
+    const long long unit = attend_div(s_at, a.s.chunks);
+    a.chunk = (int)(s_at - unit * a.s.chunks);
     a.head = (int)attend_div(unit, a.s.tiles);
     a.tile = (int)(unit - (long long)a.head * a.s.tiles);
   }
   if (tid == 0) P.from[blockIdx.x] = AttendFrom{share, a.s.t0, a.s.n, a.s.chunks, a.head, a.tile, a.chunk};
-  for (int b = blockIdx.x + gridDim.x * tid; b < P.B; b += gridDim.x * THREADS) {
-    const AttendSeq s = attend_seq(P, b);
-    if (s.chunks > 0) continue;
-    for (int t = s.t0; t < s.t0 + s.n; ++t)
-      for (int h = 0; h < P.Hq; ++h) {
-        for (int d = 0; d < P.D; ++d) elem_store(P.out, P.out_dtype, t * P.o_stride + h * P.o_head + d, 0.f);
-        if (P.lse) P.lse[(long long)t * P.Hq + h] = -INFINITY;
-      }
-  }
   return a;
 }
 

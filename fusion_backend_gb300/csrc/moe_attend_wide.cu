@@ -11,7 +11,8 @@
 // each, 32 columns each) overwrite as operand of the second product, and the
 // output, 64 or 128 columns a stream.
 //
-//   warp 0       issues the products: scores of step i, then weighted values of i - 1
+//   warps 0, 12  issue the products, of a stream each: scores of step i, then weighted
+//                values of i - 1 (one warp for both took longer than the stream)
 //   warp 1       tensor copies of keys and values into a ring, in that order
 //   warps 2, 3   queries of the next unit; and in the tiles that hold tokens which
 //                some rows do not see, they take values that are not finite out (a
@@ -39,7 +40,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 384, kTok = 64;  // tokens of a stream's half step
+constexpr int kThreads = 416, kTok = 64;  // tokens of a stream's half step
 constexpr int kOddUnits = 16;  // units whose mark of values taken out is kept
 
 __host__ __device__ constexpr int slots_for(int dp) { return dp == 64 ? 14 : 9; }
@@ -108,6 +109,15 @@ MOE_DEV bool odd16(uint32_t h) {  // not finite
 // A shared-memory descriptor with its address moved by `bytes`.
 MOE_DEV uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
+// One lane of a warp that is here as a whole.  The products and copies are issued
+// under this, with operands that all lanes form alike: from a branch on the lane's
+// number an instruction took 110 to 190 cycles.
+MOE_DEV bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0u;
+}
+
 // A wait that ran out once is not waited for again.
 MOE_DEV void await(uint64_t* bar, uint32_t parity, bool& dead) {
   if (!dead) dead = !mbar_wait(bar, parity);
@@ -147,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   uint8_t* const qs = smem + NS * kSlot;
   __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_full[2][2], o_done[2], o_free, q_full[2], q_empty[2], clean[NS];
   __shared__ uint32_t s_tmem;
-  __shared__ long long s_scan[kThreads / 32 + 2];
   __shared__ float2 s_stat[2][2][128];
   __shared__ uint32_t s_boxes[2][16], s_odd[kOddUnits];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       }
       mbar_init(&o_done[x], 1);
       mbar_init(&q_full[x], P.q_box ? 1 : 64);
-      mbar_init(&q_empty[x], 1);
+      mbar_init(&q_empty[x], 2);
     }
     mbar_init(&o_free, 256);
     for (int i = 0; i < NS; ++i) mbar_init(clean + i, 64);
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   }
   pdl_wait();
   pdl_launch_dependents();
-  AttendStep a = attend_begin<kThreads>(P, s_scan);
+  AttendStep a = attend_begin<kThreads>(P);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -193,125 +202,145 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   // a tile that holds tokens which some rows do not see
   auto mixed = [&](const AttendStep& s, int x) { return first_of(s, x) + kTok > seen_by_all(P, s.s); };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 12) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16), o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
-      // descriptors of the first slot and buffer; of values: columns are what lies together
-      const uint64_t k_desc0 = tc::smem_desc(smem_u32(smem), 16, 1024), q_desc0 = tc::smem_desc(smem_u32(qs), 16, 1024),
-                     v_desc0 = tc::smem_desc(smem_u32(smem), kTok * 128, 1024);
-      int slot = 0, unit = 0, count[2] = {0, 0}, cleaned = 0;
-      uint32_t turn = 0;
-      auto next_slot = [&] {
-        if (++slot == NS) {
-          slot = 0;
-          turn ^= 1u;
-        }
-      };
-      // mixed tiles in their order: as many barriers as slots, since those that are
-      // clean and not yet used lie in the ring
-      uint32_t clean_turn = 0;
-      auto next_clean = [&] {
-        if (++cleaned == NS) {
-          cleaned = 0;
-          clean_turn ^= 1u;
-        }
-      };
-      AttendStep before = a;
-      bool have = false, fresh[2] = {true, true};  // of the step before: its unit's first product
-      int unit_before = 0;
-      for (bool more = a.left > 0; more || have;) {
-        const bool begins = more && (!have || last_of_unit(before));
-        if (more) {
-          if (begins) await(&q_full[unit & 1], unit >> 1 & 1, dead);
-          for (int x = 0; x < 2; ++x) {
-            if (!there(a, x)) continue;
-            await(full + slot, turn, dead);
-            tc::tc_fence_after();
-            const uint64_t k_desc = desc_at(k_desc0, slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
-            const int buf = count[x] & 1;
-            const uint32_t to = tmem + x * 128 + buf * 64;
+    const int x = warp == 0 ? 0 : 1;  // the warp's stream
+    const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16), o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
+    // descriptors of the first slot and buffer; of values: columns are what lies together
+    const uint64_t k_desc0 = tc::smem_desc(smem_u32(smem), 16, 1024), q_desc0 = tc::smem_desc(smem_u32(qs), 16, 1024),
+                   v_desc0 = tc::smem_desc(smem_u32(smem), kTok * 128, 1024);
+    int slot = 0, unit = 0, unit_before = 0, count = 0, cleaned = 0;
+    // mixed tiles in their order: as many barriers as slots, since those that are clean
+    // and not yet used lie in the ring
+    uint32_t turn = 0, clean_turn = 0;
+    auto next_slot = [&] {
+      if (++slot == NS) {
+        slot = 0;
+        turn ^= 1u;
+      }
+    };
+    auto next_clean = [&] {
+      if (++cleaned == NS) {
+        cleaned = 0;
+        clean_turn ^= 1u;
+      }
+    };
+    AttendStep before = a;
+    bool have = false, fresh = true;  // of the step before: its unit's first product
+    for (bool more = a.left > 0; more || have;) {
+      const bool here = more && there(a, x);
+      if (more) {
+        if (!have || last_of_unit(before)) await(&q_full[unit & 1], unit >> 1 & 1, dead);
+        if (x == 1) next_slot();
+        if (here) {
+          await(full + slot, turn, dead);
+          tc::tc_fence_after();
+          const uint64_t k_desc = desc_at(k_desc0, slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
+          const int buf = count & 1;
+          const uint32_t to = tmem + x * 128 + buf * 64;
+          if (elected()) {
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks)
               tc::umma(to, desc_at(q_desc, (ks >> 2) * 128 * 128 + (ks & 3) * 32),
                        desc_at(k_desc, (ks >> 2) * kTok * 128 + (ks & 3) * 32), s_desc, ks > 0);
             tc::umma_commit(empty + slot);
             tc::umma_commit(&s_full[x][buf]);
-            next_slot();
-            ++count[x];
           }
-          if (last_of_unit(a)) tc::umma_commit(&q_empty[unit & 1]);
+          __syncwarp();
+          next_slot();
+          ++count;
         }
-        if (have) {
-          for (int x = 0; x < 2; ++x) {
-            if (!there(before, x)) continue;
-            // the chunk's number in its stream: the one before a chunk of `a`, if that has one
-            const int c = count[x] - 1 - (more && there(a, x) ? 1 : 0), buf = c & 1;
-            await(full + slot, turn, dead);
-            if (mixed(before, x)) {
-              await(clean + cleaned, clean_turn, dead);
-              next_clean();
-            }
-            await(&p_full[x][buf], c >> 1 & 1, dead);
-            if (fresh[x] && unit_before > 0) await(&o_free, (unit_before - 1) & 1, dead);
-            tc::tc_fence_after();
-            const uint64_t v_desc = desc_at(v_desc0, slot * kSlot);
-            const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64;
-            uint32_t add = !fresh[x];
+        if (x == 0 && there(a, 1)) next_slot();
+        if (last_of_unit(a)) {
+          if (elected()) tc::umma_commit(&q_empty[unit & 1]);
+          __syncwarp();
+        }
+      }
+      if (have) {
+        if (x == 1) {
+          if (mixed(before, 0)) next_clean();
+          next_slot();
+        }
+        if (there(before, x)) {
+          // the chunk's number in its stream: the one before a chunk of `a`, if that has one
+          const int c = count - (here ? 2 : 1), buf = c & 1;
+          await(full + slot, turn, dead);
+          if (mixed(before, x)) {
+            await(clean + cleaned, clean_turn, dead);
+            next_clean();
+          }
+          await(&p_full[x][buf], c >> 1 & 1, dead);
+          if (fresh && unit_before > 0) await(&o_free, (unit_before - 1) & 1, dead);
+          tc::tc_fence_after();
+          const uint64_t v_desc = desc_at(v_desc0, slot * kSlot);
+          const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64;
+          const uint32_t add = !fresh;
+          if (elected()) {
 #pragma unroll
             for (int term = 1; term >= 0; --term)
 #pragma unroll
-              for (int ks = 0; ks < kTok / 16; ++ks) {
-                umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc, add);
-                add = 1u;
-              }
+              for (int ks = 0; ks < kTok / 16; ++ks)
+                umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc,
+                        term == 1 && ks == 0 ? add : 1u);
             tc::umma_commit(empty + slot);
             tc::umma_commit(&o_done[x]);
-            next_slot();
-            fresh[x] = false;
           }
-          if (last_of_unit(before)) {
-            fresh[0] = fresh[1] = true;
-            ++unit_before;
-          }
+          __syncwarp();
+          next_slot();
+          fresh = false;
         }
-        if (more && last_of_unit(a)) ++unit;
-        have = more;
-        before = a;
-        if (more) a.next(P);
-        more = a.left > 0;
+        if (x == 0 && there(before, 1)) {
+          if (mixed(before, 1)) next_clean();
+          next_slot();
+        }
+        if (last_of_unit(before)) {
+          fresh = true;
+          ++unit_before;
+        }
       }
+      if (more && last_of_unit(a)) ++unit;
+      have = more;
+      before = a;
+      if (more) a.next(P);
+      more = a.left > 0;
     }
-    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ keys and values
-    const int per = kTok / P.box, box = lane % per, half = lane / per;
-    const bool on = half < kHalves;
+    const int boxes = kTok / P.box;  // of a tile; lane b < boxes knows box b's page
     const uint64_t once = policy_evict_first(), again = policy_evict_last();
     int slot = 0, i = 0;
     uint32_t turn = 1;  // the first pass finds the slots empty
     struct Where {
-      int page[2], at;  // pages of the lane's boxes (behind the cache: zeros), its first token's slot in the page
+      int page[2], in[2];  // the box's page (behind the cache: zeros) and its first slot there
     };
     auto look = [&](const AttendStep& s) {
       Where w;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int t = first_of(s, x) + box * P.box;
+        const int t = first_of(s, x) + lane * P.box, at = attend_page(P, t);
+        w.in[x] = t - at * P.page_size;
         w.page[x] = -1;
-        if (s.left > 0 && t < s.s.len) w.page[x] = P.table[s.b * P.table_stride + attend_page(P, t)];
+        if (lane < boxes && s.left > 0 && t < s.s.len) w.page[x] = P.table[s.b * P.table_stride + at];
       }
       return w;
     };
-    auto load = [&](const CUtensorMap* map, const AttendStep& s, int x, int page) {
+    auto load = [&](const CUtensorMap* map, const AttendStep& s, int page, int in) {
       await(empty + slot, turn, dead);
-      if (lane == 0) mbar_arrive_expect_tx(full + slot, kSlot);
+      const uint64_t policy = s.s.tiles > 1 ? again : once;
+      uint8_t* const to = smem + slot * kSlot;
+      const int known = (uint32_t)page < (uint32_t)P.pages ? page : P.pages;
+      if (elected()) mbar_arrive_expect_tx(full + slot, kSlot);
       __syncwarp();
-      if (on) {
-        const int t = first_of(s, x) + box * P.box, in = t - attend_page(P, t) * P.page_size;
-        const int c1 = P.slot_first ? in : s.head, c2 = P.slot_first ? s.head : in;
-        tensor_load_4d(smem + slot * kSlot + half * kTok * 128 + box * P.box * 128, map, 64 * half, c1, c2,
-                       (uint32_t)page < (uint32_t)P.pages ? page : P.pages, full + slot, s.s.tiles > 1 ? again : once);
+#pragma unroll 1
+      for (int b = 0; b < boxes; ++b) {
+        const int pg = __shfl_sync(kAll, known, b), at = __shfl_sync(kAll, in, b);
+        const int c1 = P.slot_first ? at : s.head, c2 = P.slot_first ? s.head : at;
+        if (elected()) {
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half)
+            tensor_load_4d(to + half * kTok * 128 + b * P.box * 128, map, 64 * half, c1, c2, pg, full + slot, policy);
+        }
+        __syncwarp();
       }
       if (++slot == NS) {
         slot = 0;
@@ -325,11 +354,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       if (P.q_box && (i == 0 || last_of_unit(before))) {
         // the unit's queries: q_box tokens of the group's heads are its rows in their order
         if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
-        if (lane == 0) mbar_arrive_expect_tx(&q_full[unit & 1], kHalves * 128 * P.G * P.q_box);
+        if (elected()) {
+          mbar_arrive_expect_tx(&q_full[unit & 1], kHalves * 128 * P.G * P.q_box);
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half)
+            tensor_load_3d(qs + (unit & 1) * kQ + half * 128 * 128, &P.tm_q, 64 * half, a.head * P.G,
+                           a.s.t0 + a.tile * P.q_box, &q_full[unit & 1], again);
+        }
         __syncwarp();
-        if (lane < kHalves)
-          tensor_load_3d(qs + (unit & 1) * kQ + lane * 128 * 128, &P.tm_q, 64 * lane, a.head * P.G,
-                         a.s.t0 + a.tile * P.q_box, &q_full[unit & 1], again);
         ++unit;
       }
       AttendStep next = a;
@@ -337,13 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       const Where soon = look(next);
       for (int x = 0; x < 2; ++x) {
         if (!there(a, x)) continue;
-        const uint32_t boxes = __ballot_sync(kAll, half == 0 && (uint32_t)now.page[x] < (uint32_t)P.pages);
-        if (lane == 0) s_boxes[x][i & 15] = boxes;
-        load(&P.tm_k, a, x, now.page[x]);
+        const uint32_t known = __ballot_sync(kAll, (uint32_t)now.page[x] < (uint32_t)P.pages);
+        if (lane == 0) s_boxes[x][i & 15] = known;
+        load(&P.tm_k, a, now.page[x], now.in[x]);
       }
       if (i > 0)
         for (int x = 0; x < 2; ++x)
-          if (there(before, x)) load(&P.tm_v, before, x, then.page[x]);
+          if (there(before, x)) load(&P.tm_v, before, then.page[x], then.in[x]);
       before = a;
       then = now;
       a = next;
@@ -351,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
     }
     if (i > 0)
       for (int x = 0; x < 2; ++x)
-        if (there(before, x)) load(&P.tm_v, before, x, then.page[x]);
+        if (there(before, x)) load(&P.tm_v, before, then.page[x], then.in[x]);
   } else if (warp < 4) {
     // ------------------------------------------------------------ queries; values that are not finite
     const int th = tid - 64;
@@ -464,13 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
           const uint32_t at = tmem + lanes + x * 128 + buf * 64;
           await(&s_full[x][buf], count >> 1 & 1, dead);
           tc::tc_fence_after();
-          const uint32_t boxes = s_boxes[x][i & 15], all = kTok / P.box == 8 ? 0xFFu : 0xFu;
+          const uint32_t boxes = s_boxes[x][i & 15], all = (1u << kTok / P.box) - 1u;
           const bool part = mixed(a, x) || boxes != all, changed = part || P.softcap > 0.f || flip;
           uint64_t seen = ~0ull;
           if (part) {
             seen = seen_tokens(P, a.s, first_of(a, x), t, j);
             for (int b = 0; b < kTok / P.box; ++b)
-              if (!(boxes >> b & 1u)) seen &= ~(((1ull << P.box) - 1ull) << (b * P.box));
+              if (!(boxes >> b & 1u)) seen &= ~((~0ull >> (64 - P.box)) << (b * P.box));
           }
           // twice over the scores, 32 columns at a time: short loops, since what each
           // warp runs through once a step comes from beyond the nearest instruction cache
