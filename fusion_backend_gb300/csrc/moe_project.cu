@@ -2,7 +2,7 @@
 //   y_tn = sum_g d_ng sum_{k in g} (c_nk - 8) x_tk + bias_n
 //
 // Bound by the stream of codes and scales up to some 16 tokens, by the warp-level
-// tensor-core instruction above.  A tile is 16 MT rows of W and all of K; the warps
+// tensor-core instruction above.  A tile is 16 rows of W and all of K; the warps
 // of a block that share a tile take slabs of 256 columns in turn, each with a ring
 // of its own in shared memory that tensor copies fill tiles ahead, and meet once a
 // batch of tiles to add their sums.  So every SM has its whole share of a small
@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_elem.cuh"
 #include "moe_internal.h"
 #include "moe_mma.cuh"
@@ -30,7 +32,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kSlab = 256;  // columns of a slab: 128 bytes of codes
 constexpr int kChunks = kSlab / 32;
 
@@ -49,26 +50,26 @@ MOE_DEV uint32_t code_pair(uint32_t v) {
 
 // Shared memory: the warps' rings of codes, of scales (16 bytes a row and slab),
 // the sums of a batch of BT tiles, the barriers.
-template <int NT, int MT, int STAGES, int BT>
+template <int WARPS, int NT, int STAGES, int BT>
 struct Layout {
-  static constexpr int kCodes = 16 * MT * 128, kScales = 16 * MT * 16, kPitch = 8 * NT + 1, kRows = BT * 16 * MT;
-  static constexpr int scales_at = kWarps * STAGES * kCodes, sums_at = scales_at + kWarps * STAGES * kScales,
-                       bars_at = sums_at + (kWarps * kRows * kPitch * 4 + 15) / 16 * 16,
-                       bytes = bars_at + kWarps * STAGES * 8 + 1024;  // (rings start at a multiple of 1024)
+  static constexpr int kCodes = 16 * 128, kScales = 16 * 16, kPitch = 8 * NT + 1, kRows = BT * 16;
+  static constexpr int scales_at = WARPS * STAGES * kCodes, sums_at = scales_at + WARPS * STAGES * kScales,
+                       bars_at = sums_at + (WARPS * kRows * kPitch * 4 + 15) / 16 * 16,
+                       bytes = bars_at + WARPS * STAGES * 8 + 1024;  // (rings start at a multiple of 1024)
 };
 
 // NT: tiles of 8 tokens.  GL: log2(group / 32).  HOLD: a warp has one slab of
 // every tile, whose x stays in registers.
-template <bool F16, int NT, int MT, int STAGES, int BT, int GL, bool HOLD>
-__global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const __grid_constant__ ProjectParams P) {
-  using L = Layout<NT, MT, STAGES, BT>;
+template <bool F16, int WARPS, int NT, int STAGES, int BT, int GL, bool HOLD, int OCC>
+__global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_constant__ ProjectParams P) {
+  using L = Layout<WARPS, NT, STAGES, BT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int kw = P.k_warps, kpart = warp % kw, tpart = warp / kw, at_once = kWarps / kw;
+  const int kw = P.k_warps, kpart = warp % kw, tpart = warp / kw, at_once = WARPS / kw;
   const int t0 = blockIdx.y * 8 * NT;
-  const int slabs = (P.K + kSlab - 1) / kSlab, mine = HOLD ? 1 : (slabs - kpart + kw - 1) / kw;
-  const int ntiles = (P.N + 16 * MT - 1) / (16 * MT);
+  const int slabs = (P.K + kSlab - 1) / kSlab, mine = HOLD ? kpart < slabs : (slabs - kpart + kw - 1) / kw;
+  const int ntiles = (P.N + 16 - 1) / (16);
   const int lo = (int)((long long)ntiles * blockIdx.x / gridDim.x), hi = (int)((long long)ntiles * (blockIdx.x + 1) / gridDim.x);
   uint8_t* const codes = smem + warp * STAGES * L::kCodes;
   uint8_t* const scales = smem + L::scales_at + warp * STAGES * L::kScales;
@@ -92,9 +93,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const 
       if (lane == 0) {
         const int k0 = (kpart + slab_in * kw) * kSlab;
         mbar_arrive_expect_tx(full + stage, L::kCodes + L::kScales);
-        tensor_load_2d(codes + stage * L::kCodes, &P.tm_codes, k0 >> 1, tile_in * 16 * MT, full + stage, policy);
+        tensor_load_2d(codes + stage * L::kCodes, &P.tm_codes, k0 >> 1, tile_in * 16, full + stage, policy);
         // 16 bytes that hold the slab's scales: of one slab, two or four
-        tensor_load_2d(scales + stage * L::kScales, &P.tm_scales, (P.K >> 1) + (k0 >> (4 + GL) & ~15), tile_in * 16 * MT,
+        tensor_load_2d(scales + stage * L::kScales, &P.tm_scales, (P.K >> 1) + (k0 >> (4 + GL) & ~15), tile_in * 16,
                        full + stage, policy);
       }
       if (HOLD || ++slab_in >= mine) {
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const 
   };
   uint32_t xh[HOLD ? kChunks : 1][NT][4];
   if constexpr (HOLD) {
-    const int chunks = min(kChunks, (P.K - kpart * kSlab) >> 5);
+    const int chunks = min(kChunks, (P.K - kpart * kSlab) >> 5);  // (negative: no slab)
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
       if (c < chunks) load_x(xh[c], kpart * kSlab + 32 * c);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const 
   for (int base = lo; base < hi; base += BT) {
     const int in_batch = min(BT, hi - base);
     for (int u = tpart; u < in_batch; u += at_once) {
-      float acc[MT][NT][4] = {};
+      float acc[NT][4] = {};
       for (int j = 0; j < mine; ++j) {
         const int k0 = (kpart + j * kw) * kSlab, chunks = min(kChunks, (P.K - k0) >> 5);
         uint32_t x[NT][4];
@@ -148,54 +149,58 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const 
         stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
         if (!dead) dead = !mbar_wait(full + stage, parity);
         const uint32_t codes_at = smem_u32(codes + stage * L::kCodes);
-        const __half* const sc = reinterpret_cast<const __half*>(scales + stage * L::kScales) +
-                                 (k0 >> (5 + GL) & 7);  // of row 0
-        float part[MT][NT][4];
+        // the slab's scales of rows g and g + 8: 8, 4 or 2 each
+        uint32_t sc0[4], sc1[4];
+        {
+          const uint8_t* const from = scales + stage * L::kScales + g * 16 + (k0 >> (4 + GL) & 15);
 #pragma unroll
-        for (int c2 = 0; c2 < kChunks; c2 += 2) {
-          if (c2 >= chunks) break;
+          for (int e = 0; e < 4 >> GL; ++e) {
+            sc0[e] = *reinterpret_cast<const uint32_t*>(from + 4 * e);
+            sc1[e] = *reinterpret_cast<const uint32_t*>(from + 128 + 4 * e);
+          }
+        }
+        auto scale_of = [](const uint32_t(&sc)[4], int i) {
+          const __half2 v = *reinterpret_cast<const __half2*>(&sc[i >> 1]);
+          return i & 1 ? __high2float(v) : __low2float(v);
+        };
+        float part[NT][4];
+        // two chunks, c2 and the next; ALL: both are there
+        auto pair = [&](int c2, auto whole) {
+          constexpr bool ALL = decltype(whole)::value;
           // codes of two chunks: (rows, chunk) of matrix i = (i & 1, i >> 1)
-          uint32_t w[MT][4];
-          const int r = (lane & 7) + (lane & 8), c = c2 + (lane >> 4);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) ldmatrix4(w[m], codes_at + (16 * m + r) * 128 + ((c ^ (r & 7)) << 4));
+          uint32_t w[4];
+          const int r = lane & 15, c = c2 + (lane >> 4);
+          ldmatrix4(w, codes_at + r * 128 + ((c ^ (r & 7)) << 4));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (c2 + h >= chunks) break;
-            uint32_t xn[NT][4];
+            if (!ALL && c2 + h >= chunks) break;
+            [[maybe_unused]] uint32_t xn[NT][4];
             if constexpr (!HOLD) {
               if (c2 + h + 1 < chunks) load_x(xn, k0 + 32 * (c2 + h + 1));
               order_x(x);
             }
             uint32_t(&b)[NT][4] = HOLD ? xh[HOLD ? c2 + h : 0] : x;
             const bool first = ((c2 + h) & ((1 << GL) - 1)) == 0;
+            const uint32_t v0 = w[2 * h], v1 = w[2 * h + 1];  // rows g and g + 8
+            const uint32_t a0 = code_pair<F16>(v0), b0 = code_pair<F16>(v1), a1 = code_pair<F16>(v0 >> 4),
+                           b1 = code_pair<F16>(v1 >> 4), a2 = code_pair<F16>(v0 >> 8), b2 = code_pair<F16>(v1 >> 8),
+                           a3 = code_pair<F16>(v0 >> 12), b3 = code_pair<F16>(v1 >> 12);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const uint32_t v0 = w[m][2 * h], v1 = w[m][2 * h + 1];  // rows g and g + 8
-              const uint32_t a0 = code_pair<F16>(v0), b0 = code_pair<F16>(v1), a1 = code_pair<F16>(v0 >> 4),
-                             b1 = code_pair<F16>(v1 >> 4), a2 = code_pair<F16>(v0 >> 8), b2 = code_pair<F16>(v1 >> 8),
-                             a3 = code_pair<F16>(v0 >> 12), b3 = code_pair<F16>(v1 >> 12);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                float(&d)[4] = part[m][n];
-                if (first) d[0] = d[1] = d[2] = d[3] = 0.f;
-                mma16<F16>(d, a0, b0, a1, b1, b[n][0], b[n][1]);
-                mma16<F16>(d, a2, b2, a3, b3, b[n][2], b[n][3]);
-              }
+            for (int n = 0; n < NT; ++n) {
+              if (first)
+                mma16_first<F16>(part[n], a0, b0, a1, b1, b[n][0], b[n][1]);
+              else
+                mma16<F16>(part[n], a0, b0, a1, b1, b[n][0], b[n][1]);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16<F16>(part[n], a2, b2, a3, b3, b[n][2], b[n][3]);
             if (((c2 + h + 1) & ((1 << GL) - 1)) == 0) {
               const int at = (c2 + h) >> GL;
+              const float s0 = scale_of(sc0, at), s1 = scale_of(sc1, at);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                const float s0 = __half2float(sc[(16 * m + g) * 8 + at]);
-                const float s1 = __half2float(sc[(16 * m + g + 8) * 8 + at]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  acc[m][n][0] = fmaf(part[m][n][0], s0, acc[m][n][0]);
-                  acc[m][n][1] = fmaf(part[m][n][1], s0, acc[m][n][1]);
-                  acc[m][n][2] = fmaf(part[m][n][2], s1, acc[m][n][2]);
-                  acc[m][n][3] = fmaf(part[m][n][3], s1, acc[m][n][3]);
-                }
+              for (int n = 0; n < NT; ++n) {
+                fma_pair(acc[n][0], acc[n][1], part[n][0], part[n][1], s0);
+                fma_pair(acc[n][2], acc[n][3], part[n][2], part[n][3], s1);
               }
             }
             if constexpr (!HOLD) {
@@ -205,28 +210,35 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const 
                 for (int e = 0; e < 4; ++e) x[n][e] = xn[n][e];
             }
           }
+        };
+        if (chunks == kChunks) {
+#pragma unroll
+          for (int c2 = 0; c2 < kChunks; c2 += 2) pair(c2, std::true_type{});
+        } else {
+#pragma unroll
+          for (int c2 = 0; c2 < kChunks; c2 += 2) {
+            if (c2 >= chunks) break;
+            pair(c2, std::false_type{});
+          }
         }
         if (++stage == STAGES) {
           stage = 0;
           parity ^= 1u;
         }
       }
-      if (dead) acc[0][0][0] = __int_as_float(0x7FFFFFFF);
-      float* const own = sums + (kpart * L::kRows + u * 16 * MT) * L::kPitch;
+      if (dead) acc[0][0] = __int_as_float(0x7FFFFFFF);
+      float* const own = sums + (kpart * L::kRows + u * 16) * L::kPitch;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            own[(16 * m + g + 8 * (e >> 1)) * L::kPitch + 8 * n + 2 * q + (e & 1)] = acc[m][n][e];
+        for (int e = 0; e < 4; ++e) own[(g + 8 * (e >> 1)) * L::kPitch + 8 * n + 2 * q + (e & 1)] = acc[n][e];
     }
     __syncthreads();
     // the warps' sums, in their order
     const int tokens = min(8 * NT, P.T - t0);
-    for (int i = threadIdx.x; i < L::kRows * tokens; i += 32 * kWarps) {
-      const int r = i % L::kRows, t = i / L::kRows, n = base * 16 * MT + r;
-      if (r >= in_batch * 16 * MT || n >= P.N) continue;
+    for (int i = threadIdx.x; i < L::kRows * tokens; i += 32 * WARPS) {
+      const int r = i % L::kRows, t = i / L::kRows, n = base * 16 + r;
+      if (r >= in_batch * 16 || n >= P.N) continue;
       float v = 0.f;
       for (int k = 0; k < kw; ++k) v += sums[(k * L::kRows + r) * L::kPitch + t];
       if (P.bias) v += P.bias[n];
@@ -236,18 +248,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 2 ? 2 : 1) k_project(const 
   }
 }
 
-template <bool F16, int NT, int MT, int STAGES, int BT, int GL, bool HOLD>
+template <bool F16, int WARPS, int NT, int STAGES, int BT, int GL, bool HOLD, int OCC>
 cudaError_t launch(ProjectParams& p, cudaStream_t stream) {
-  using L = Layout<NT, MT, STAGES, BT>;
-  static_assert(L::bytes <= 232448, "shared memory");
-  auto* const kern = k_project<F16, NT, MT, STAGES, BT, GL, HOLD>;
+  using L = Layout<WARPS, NT, STAGES, BT>;
+  static_assert(OCC * (L::bytes + 1024) <= 233472, "shared memory");
+  auto* const kern = k_project<F16, WARPS, NT, STAGES, BT, GL, HOLD, OCC>;
   static SmemLimit limit;
   const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), L::bytes);
   if (e != cudaSuccess) return e;
   const auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)(p.K / 2 + p.K / p.group * 2), (cuuint64_t)p.N}, strides[1] = {(cuuint64_t)p.w_stride};
-  const cuuint32_t ones[2] = {1, 1}, code_box[2] = {128, 16 * MT}, scale_box[2] = {16, 16 * MT};
+  const cuuint32_t ones[2] = {1, 1}, code_box[2] = {128, 16}, scale_box[2] = {16, 16};
   if (encode(&p.tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.w), dims, strides, code_box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
@@ -255,29 +267,36 @@ cudaError_t launch(ProjectParams& p, cudaStream_t stream) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  // (a batch has a tile at least for the warps of each; warps without a slab add zeros)
-  if (p.k_warps < kWarps / BT) p.k_warps = kWarps / BT;
-  const int at_once = kWarps / p.k_warps, tiles = (p.N + 16 * MT - 1) / (16 * MT);
-  const int want = (tiles + at_once - 1) / at_once, most = p.sms * (NT <= 2 ? 2 : 1);
-  return launch_behind(kern, dim3(want < most ? want : most, (p.T + 8 * NT - 1) / (8 * NT)), 32 * kWarps, L::bytes,
-                       stream, p);
+  // warps over K: a power of two, as many as there are slabs at most, where a batch
+  // has a tile for the warps of each (warps without a slab add zeros)
+  const int slabs = (p.K + kSlab - 1) / kSlab;
+  p.k_warps = 1;
+  while (p.k_warps < WARPS && (HOLD ? p.k_warps < slabs : 2 * p.k_warps <= slabs)) p.k_warps *= 2;
+  if (p.k_warps < WARPS / BT) p.k_warps = WARPS / BT;
+  const int at_once = WARPS / p.k_warps, tiles = (p.N + 15) / 16, parts = (p.T + 8 * NT - 1) / (8 * NT);
+  const int want = (tiles + at_once - 1) / at_once, most = (OCC * p.sms + parts - 1) / parts;
+  return launch_behind(kern, dim3(want < most ? want : most, parts), 32 * WARPS, L::bytes, stream, p);
 }
 
+// x in registers where K has a warp for every slab: 8 tokens and 16 with up to 16
+// warps, 32 with 8 (128 registers a thread); more tokens take turns, the weights
+// then come from the L2 cache.
 template <bool F16, int GL>
 cudaError_t launch_tokens(ProjectParams& p, cudaStream_t stream) {
-  if (p.T <= 8)
-    return p.K <= p.k_warps * kSlab ? launch<F16, 1, 1, 4, 8, GL, true>(p, stream)
-                                    : launch<F16, 1, 1, 4, 8, GL, false>(p, stream);
-  if (p.T <= 16) return launch<F16, 2, 1, 4, 4, GL, false>(p, stream);
-  if (p.T <= 32) return launch<F16, 4, 2, 3, 2, GL, false>(p, stream);
-  return launch<F16, 8, 2, 3, 1, GL, false>(p, stream);
+  const int slabs = (p.K + kSlab - 1) / kSlab;
+  if (p.T <= 8) {
+    if (slabs <= 8) return launch<F16, 8, 1, 3, 4, GL, true, 3>(p, stream);
+    if (slabs <= 16) return launch<F16, 16, 1, 3, 4, GL, true, 1>(p, stream);
+    return launch<F16, 8, 1, 4, 8, GL, false, 2>(p, stream);
+  }
+  if (slabs <= 8 && p.T > 16) return launch<F16, 8, 4, 4, 4, GL, true, 1>(p, stream);
+  if (slabs <= 16) return launch<F16, 16, 2, 3, 4, GL, true, 1>(p, stream);
+  return p.T <= 16 ? launch<F16, 8, 2, 4, 4, GL, false, 2>(p, stream) : launch<F16, 8, 4, 4, 4, GL, false, 1>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_project(ProjectParams p, cudaStream_t stream) {
-  const int slabs = (p.K + kSlab - 1) / kSlab;
-  p.k_warps = slabs >= 8 ? 8 : slabs >= 4 ? 4 : slabs >= 2 ? 2 : 1;
   const int gl = p.group == 32 ? 0 : p.group == 64 ? 1 : 2;
   if (p.f16)
     return gl == 0 ? launch_tokens<true, 0>(p, stream)
