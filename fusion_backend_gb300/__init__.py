@@ -632,7 +632,8 @@ def moe_ffn_project(x, w, group: int = 32, bias=None, out=None, out_dtype=None, 
         out = _new(stream, (x.shape[0], w.shape[0]), out_dtype or x.dtype, x.device)
     else:
         _require(out_dtype is None or out_dtype == out.dtype, "out: not of out_dtype")
-    key = (3, _sig(x), _sig(w), group, _sig(bias), _sig(out))
+    key = (3, x.shape, x.stride(), x.dtype, x.get_device(), w.shape, w.stride(), w.dtype, w.get_device(), group,
+           _sig(bias), out.shape, out.stride(), out.dtype, out.get_device())
     a = _blocks.get(key) or _remember(key, _project_block(x, w, group, bias, out))
     rc = (_lib or lib()).moe_ffn_project(a, _raw_stream(stream, x), x.data_ptr(), w.data_ptr(),
                                          None if bias is None else bias.data_ptr(), out.data_ptr())
@@ -699,7 +700,10 @@ def moe_ffn_append_kv(k, v, positions, slots, inv_freq, k_cache, v_cache, q=None
     Returns q_out."""
     if q_out is None:
         q_out = q
-    key = (4, _sig(k), _sig(v), _sig(positions), _sig(slots), _sig(inv_freq), _sig(k_cache), _sig(v_cache), _sig(q),
+    key = (4, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype, v.get_device(),
+           positions.shape, positions.stride(), positions.dtype, positions.get_device(), slots.shape, slots.stride(),
+           slots.dtype, slots.get_device(), _sig(inv_freq), k_cache.shape, k_cache.stride(), k_cache.dtype,
+           k_cache.get_device(), v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.get_device(), _sig(q),
            _sig(q_out), interleaved, scale)
     a = _blocks.get(key) or _remember(key, _append_block(k, v, positions, slots, inv_freq, k_cache, v_cache, q, q_out,
                                                          interleaved, scale))
@@ -764,8 +768,11 @@ def moe_ffn_attend(q, k_cache, v_cache, page_table, lens, q_start, mask=None, sc
     one.  Returns out."""
     if out is None:
         out = _new(stream, q.shape, q.dtype, q.device, zero=True)
-    key = (5, _sig(q), _sig(k_cache), _sig(v_cache), _sig(page_table), _sig(lens), _sig(q_start), _sig(mask), scale,
-           softcap, _sig(out), _sig(lse), _sig(workspace))
+    key = (5, q.shape, q.stride(), q.dtype, q.get_device(), k_cache.shape, k_cache.stride(), k_cache.dtype,
+           k_cache.get_device(), v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.get_device(), page_table.shape,
+           page_table.stride(), page_table.dtype, page_table.get_device(), lens.shape, lens.stride(), lens.dtype,
+           lens.get_device(), q_start.shape, q_start.stride(), q_start.dtype, q_start.get_device(), _sig(mask), scale,
+           softcap, out.shape, out.stride(), out.dtype, out.get_device(), _sig(lse), _flat(workspace))
     a = _blocks.get(key) or _remember(key, _attend_block(q, k_cache, v_cache, page_table, lens, q_start, mask, scale,
                                                          softcap, out, lse, workspace))
     if workspace is None:

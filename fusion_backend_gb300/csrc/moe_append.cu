@@ -10,8 +10,9 @@
 // A thread has one item of every token that its block takes: VEC elements of one
 // head, or VEC pairs whose halves lie apart; where it lies is found once.  The
 // angles of a token are formed once for all its heads, a thread an angle, into shared
-// memory, for the next token while this one is turned, and what the next token's
-// heads hold is on its way meanwhile: one barrier a token.  (A block a token, or two
+// memory, for the next token while this one is turned, and what the next tokens'
+// heads hold is on its way meanwhile, into a ring of the thread's own: one barrier a
+// token.  (A block a token, or two
 // or four neighbouring ones with their items all at once, waited for one phase after
 // the other: 41, 37 and 28 us for 4096 tokens of 40 heads of 128.)
 #include <cuda_runtime.h>
@@ -19,6 +20,7 @@
 
 #include "moe_elem.cuh"
 #include "moe_internal.h"
+#include "moe_mma.cuh"
 
 namespace moe {
 
@@ -26,6 +28,7 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 constexpr int kThreadsPerSm = 1024;  // (64 registers a thread)
+constexpr int kStages = 4;           // tokens on their way
 
 // f / 2 pi modulo 1 in units of 2^-64.  |f| < 256.
 MOE_DEV uint64_t turn_fraction(float f) {
@@ -53,33 +56,19 @@ MOE_DEV float2 cos_sin(uint64_t phase) {
   return quarter & 2u ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// VEC elements as they lie in memory, fp32 (up to four) or 16-bit ones.
+// VEC elements in shared memory, fp32 (up to four) or 16-bit ones.
 template <int VEC, bool F32>
-struct Raw {
-  uint4 w[1];
-};
-template <int VEC, bool F32>
-MOE_DEV void raw_read(Raw<VEC, F32>& r, const void* p, long long i) {
-  constexpr int kAny = F32 ? kF32 : kBf16;
+MOE_DEV void read_floats(const void* p, int dtype, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
-    r.w[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint4 w = *static_cast<const uint4*>(p);
+    unpack2(dtype, w.x, v[0], v[1]);
+    unpack2(dtype, w.y, v[2], v[3]);
+    unpack2(dtype, w.z, v[4], v[5]);
+    unpack2(dtype, w.w, v[6], v[7]);
   } else if constexpr (VEC == 4) {
-    r.w[0] = raw_load4(p, kAny, i);
+    raw_values4(raw_load4(p, F32 ? kF32 : kBf16, 0), F32 ? kF32 : dtype, v);
   } else {
-    r.w[0].x = raw_load(p, kAny, i);
-  }
-}
-template <int VEC, bool F32>
-MOE_DEV void raw_floats(const Raw<VEC, F32>& r, int dtype, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    unpack2(dtype, r.w[0].x, v[0], v[1]);
-    unpack2(dtype, r.w[0].y, v[2], v[3]);
-    unpack2(dtype, r.w[0].z, v[4], v[5]);
-    unpack2(dtype, r.w[0].w, v[6], v[7]);
-  } else if constexpr (VEC == 4) {
-    raw_values4(r.w[0], F32 ? kF32 : dtype, v);
-  } else {
-    v[0] = raw_value(r.w[0].x, F32 ? kF32 : dtype);
+    v[0] = raw_value(raw_load(p, F32 ? kF32 : kBf16, 0), F32 ? kF32 : dtype);
   }
 }
 template <int VEC>
@@ -97,6 +86,19 @@ MOE_DEV void write_floats(void* p, int dtype, long long i, const float (&v)[VEC]
   } else {
     elem_store(p, dtype, i, v[0]);
   }
+}
+
+// Global -> shared; 2 bytes have no asynchronous copy.
+template <int BYTES>
+MOE_DEV void copy_item(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    copy16(smem_u32(dst), src, 16u);
+  else if constexpr (BYTES == 8)
+    copy8(smem_u32(dst), src, 8u);
+  else if constexpr (BYTES == 4)
+    copy4(smem_u32(dst), src, 4u);
+  else
+    *static_cast<uint16_t*>(dst) = *static_cast<const uint16_t*>(src);
 }
 
 // VEC: elements an access.  APART: the halves of an item's pairs lie apart (for
@@ -170,29 +172,39 @@ __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads) k_ap
       s_place[buf][1] = in ? page * P.vc_page + place * P.vc_slot : -1;
     }
   };
-  auto ask = [&](int t, Raw<VEC, F32>& a, Raw<VEC, F32>& b) {
-    if (!on) return;
-    raw_read<VEC, F32>(a, from, at + t * step);
-    if (APART && pair) raw_read<VEC, F32>(b, from, at + t * step + pair);
+  // the item of token t, its two halves, into the thread's own places of a ring
+  constexpr int kBytes = VEC * (F32 ? 4 : 2);
+  extern __shared__ __align__(16) uint8_t ring[];
+  uint8_t* const mine = ring + tid * kBytes;
+  const int half_step = blockDim.x * kBytes, stage_step = 2 * half_step;
+  auto ask = [&](int t, int stage) {
+    if (on && t < P.T) {
+      const uint8_t* const src = static_cast<const uint8_t*>(from) + (at + t * step) * (F32 ? 4 : 2);
+      uint8_t* const dst = mine + stage * stage_step;
+      copy_item<kBytes>(dst, src);
+      if (APART && pair) copy_item<kBytes>(dst + half_step, src + pair * (F32 ? 4 : 2));
+    }
+    copy_commit();
   };
-  Raw<VEC, F32> a, b, a1, b1;
-  int t = blockIdx.x, buf = 0;
-  ask(t, a, b);
+  int t = blockIdx.x, buf = 0, stage = 0;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) ask(t + s * gridDim.x, s);
   prepare(0, P.positions[t], P.slot[t]);
   for (; t < P.T; t += gridDim.x, buf ^= 1) {
-    // the next token's elements are on their way while this one is turned
+    // the next tokens' elements are on their way while this one is turned
     const int t1 = t + gridDim.x;
     int position = 0, slot = -1;
+    ask(t + (kStages - 1) * gridDim.x, (stage + kStages - 1) % kStages);
     if (t1 < P.T) {
-      ask(t1, a1, b1);
       position = P.positions[t1];
       slot = P.slot[t1];
     }
+    copy_wait<kStages - 1>();
     __syncthreads();
     const long long place = s_place[buf][kind == 2];
     if (on && place >= 0) {
       float x[VEC];
-      raw_floats<VEC, F32>(a, P.x_dtype, x);
+      read_floats<VEC, F32>(mine + stage * stage_step, P.x_dtype, x);
       const long long out = head + (kind == 0 ? t * P.qo_stride : place);
       float2 cs[GA];
       if (turn >= 0) {
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads) k_ap
       }
       if (APART && pair) {
         float y[VEC];
-        raw_floats<VEC, F32>(b, P.x_dtype, y);
+        read_floats<VEC, F32>(mine + stage * stage_step + half_step, P.x_dtype, y);
 #pragma unroll
         for (int e = 0; e < GA; ++e) {
           const float v = x[e];
@@ -229,8 +241,7 @@ __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads) k_ap
       write_floats<VEC>(to, dtype, out, x);
     }
     if (t1 < P.T) prepare(buf ^ 1, position, slot);
-    a = a1;
-    b = b1;
+    stage = (stage + 1) % kStages;
   }
 }
 
@@ -257,7 +268,11 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
   const int shares = (items + kMaxThreads - 1) / kMaxThreads, each = (items + shares - 1) / shares;
   const int threads = ((each > half ? each : half) + 31) / 32 * 32;
   const int most = (p.sms * (kThreadsPerSm / threads) + shares - 1) / shares;
-  return launch_behind(k_append<VEC, F32, APART>, dim3(p.T < most ? p.T : most, shares), threads, 0, stream, p);
+  const int smem = kStages * 2 * threads * VEC * (F32 ? 4 : 2);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k_append<VEC, F32, APART>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_behind(k_append<VEC, F32, APART>, dim3(p.T < most ? p.T : most, shares), threads, smem, stream, p);
 }
 
 template <int VEC, bool F32>

@@ -11,8 +11,9 @@
 // each, 32 columns each) overwrite as operand of the second product, and the
 // output, 64 or 128 columns a stream.
 //
-//   warps 0, 12  issue the products, of a stream each: scores of step i, then weighted
-//                values of i - 1 (one warp for both took longer than the stream)
+//   warps 0, 12  issue the products for the scores of a stream each, warps 13 and 14
+//                those of its weighted values (one warp for all took three times as
+//                long as the stream, one a stream half as long again)
 //   warp 1       tensor copies of keys and values into a ring, in that order
 //   warps 2, 3   queries of the next unit; and in the tiles that hold tokens which
 //                some rows do not see, they take values that are not finite out (a
@@ -40,7 +41,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 416, kTok = 64;  // tokens of a stream's half step
+constexpr int kThreads = 480, kTok = 64;  // tokens of a stream's half step
 constexpr int kOddUnits = 16;  // units whose mark of values taken out is kept
 
 __host__ __device__ constexpr int slots_for(int dp) { return dp == 64 ? 14 : 9; }
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* const qs = smem + NS * kSlot;
-  __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_full[2][2], o_done[2], o_free, q_full[2], q_empty[2], clean[NS];
+  __shared__ uint64_t full[NS], empty[NS], s_full[2][2], s_free[2][2], p_full[2][2], o_done[2], o_free, q_full[2], q_empty[2], clean[NS];
   __shared__ uint32_t s_tmem;
   __shared__ float2 s_stat[2][2][128];
   __shared__ uint32_t s_boxes[2][16], s_odd[kOddUnits];
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&s_full[x][b], 1);
+        mbar_init(&s_free[x][b], 1);
         mbar_init(&p_full[x][b], 128);
       }
       mbar_init(&o_done[x], 1);
@@ -202,14 +204,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   // a tile that holds tokens which some rows do not see
   auto mixed = [&](const AttendStep& s, int x) { return first_of(s, x) + kTok > seen_by_all(P, s.s); };
 
-  if (warp == 0 || warp == 12) {
+  if (warp == 0 || warp >= 12) {
     // ------------------------------------------------------------ products
-    const int x = warp == 0 ? 0 : 1;  // the warp's stream
+    const int x = warp == 0 || warp == 13 ? 0 : 1;  // the warp's stream
+    const bool scores = warp == 0 || warp == 12;
     const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16), o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
     // descriptors of the first slot and buffer; of values: columns are what lies together
     const uint64_t k_desc0 = tc::smem_desc(smem_u32(smem), 16, 1024), q_desc0 = tc::smem_desc(smem_u32(qs), 16, 1024),
                    v_desc0 = tc::smem_desc(smem_u32(smem), kTok * 128, 1024);
-    int slot = 0, unit = 0, unit_before = 0, count = 0, cleaned = 0;
+    int slot = 0, unit = 0, count = 0, cleaned = 0;  // count: the stream's chunks so far
     // mixed tiles in their order: as many barriers as slots, since those that are clean
     // and not yet used lie in the ring
     uint32_t turn = 0, clean_turn = 0;
@@ -226,79 +229,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       }
     };
     AttendStep before = a;
-    bool have = false, fresh = true;  // of the step before: its unit's first product
+    bool have = false, fresh = true;  // the unit's first product is still to come
     for (bool more = a.left > 0; more || have;) {
-      const bool here = more && there(a, x);
+      // the keys of this step
       if (more) {
-        if (!have || last_of_unit(before)) await(&q_full[unit & 1], unit >> 1 & 1, dead);
+        if (scores && (!have || last_of_unit(before))) await(&q_full[unit & 1], unit >> 1 & 1, dead);
         if (x == 1) next_slot();
-        if (here) {
-          await(full + slot, turn, dead);
-          tc::tc_fence_after();
-          const uint64_t k_desc = desc_at(k_desc0, slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
-          const int buf = count & 1;
-          const uint32_t to = tmem + x * 128 + buf * 64;
-          if (elected()) {
+        if (there(a, x)) {
+          if (scores) {
+            const int buf = count & 1;
+            if (count > 1) await(&s_free[x][buf], (count >> 1) - 1 & 1, dead);
+            await(full + slot, turn, dead);
+            tc::tc_fence_after();
+            const uint64_t k_desc = desc_at(k_desc0, slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
+            const uint32_t to = tmem + x * 128 + buf * 64;
+            if (elected()) {
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks)
-              tc::umma(to, desc_at(q_desc, (ks >> 2) * 128 * 128 + (ks & 3) * 32),
-                       desc_at(k_desc, (ks >> 2) * kTok * 128 + (ks & 3) * 32), s_desc, ks > 0);
-            tc::umma_commit(empty + slot);
-            tc::umma_commit(&s_full[x][buf]);
+              for (int ks = 0; ks < DP / 16; ++ks)
+                tc::umma(to, desc_at(q_desc, (ks >> 2) * 128 * 128 + (ks & 3) * 32),
+                         desc_at(k_desc, (ks >> 2) * kTok * 128 + (ks & 3) * 32), s_desc, ks > 0);
+              tc::umma_commit(empty + slot);
+              tc::umma_commit(&s_full[x][buf]);
+            }
+            __syncwarp();
+            ++count;
           }
-          __syncwarp();
           next_slot();
-          ++count;
         }
         if (x == 0 && there(a, 1)) next_slot();
-        if (last_of_unit(a)) {
+        if (scores && last_of_unit(a)) {
           if (elected()) tc::umma_commit(&q_empty[unit & 1]);
           __syncwarp();
+          ++unit;
         }
       }
+      // the values of the step before
       if (have) {
         if (x == 1) {
           if (mixed(before, 0)) next_clean();
           next_slot();
         }
         if (there(before, x)) {
-          // the chunk's number in its stream: the one before a chunk of `a`, if that has one
-          const int c = count - (here ? 2 : 1), buf = c & 1;
-          await(full + slot, turn, dead);
-          if (mixed(before, x)) {
-            await(clean + cleaned, clean_turn, dead);
-            next_clean();
-          }
-          await(&p_full[x][buf], c >> 1 & 1, dead);
-          if (fresh && unit_before > 0) await(&o_free, (unit_before - 1) & 1, dead);
-          tc::tc_fence_after();
-          const uint64_t v_desc = desc_at(v_desc0, slot * kSlot);
-          const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64;
-          const uint32_t add = !fresh;
-          if (elected()) {
+          const bool mix = mixed(before, x);
+          if (!scores) {
+            const int buf = count & 1;
+            await(full + slot, turn, dead);
+            if (mix) await(clean + cleaned, clean_turn, dead);
+            await(&p_full[x][buf], count >> 1 & 1, dead);
+            if (fresh && unit > 0) await(&o_free, (unit - 1) & 1, dead);
+            tc::tc_fence_after();
+            const uint64_t v_desc = desc_at(v_desc0, slot * kSlot);
+            const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64;
+            const uint32_t add = !fresh;
+            if (elected()) {
 #pragma unroll
-            for (int term = 1; term >= 0; --term)
+              for (int term = 1; term >= 0; --term)
 #pragma unroll
-              for (int ks = 0; ks < kTok / 16; ++ks)
-                umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc,
-                        term == 1 && ks == 0 ? add : 1u);
-            tc::umma_commit(empty + slot);
-            tc::umma_commit(&o_done[x]);
+                for (int ks = 0; ks < kTok / 16; ++ks)
+                  umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc,
+                          term == 1 && ks == 0 ? add : 1u);
+              tc::umma_commit(empty + slot);
+              tc::umma_commit(&s_free[x][buf]);
+              tc::umma_commit(&o_done[x]);
+            }
+            __syncwarp();
+            fresh = false;
+            ++count;
           }
-          __syncwarp();
+          if (mix) next_clean();
           next_slot();
-          fresh = false;
         }
         if (x == 0 && there(before, 1)) {
           if (mixed(before, 1)) next_clean();
           next_slot();
         }
-        if (last_of_unit(before)) {
+        if (!scores && last_of_unit(before)) {
           fresh = true;
-          ++unit_before;
+          ++unit;
         }
       }
-      if (more && last_of_unit(a)) ++unit;
       have = more;
       before = a;
       if (more) a.next(P);
