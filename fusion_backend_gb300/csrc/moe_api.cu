@@ -540,7 +540,8 @@ int check_adapters(const moe_ffn_adapters_args* a) {
   return MOE_FFN_OK;
 }
 
-constexpr int64_t kMaxSlots = 2147483647;  // slots of a cache, tokens of a sequence
+constexpr int64_t kMaxSlots = 2147483647;   // slots of a cache
+constexpr int64_t kMaxTokens = 1073741824;  // of a sequence
 
 int check_attend(const moe_ffn_attend_args* a) {
   if (!a || a->T < 0 || a->B < 0 || a->pages < 0 || a->max_pages < 0 || a->mask_words < 0)
@@ -551,7 +552,7 @@ int check_attend(const moe_ffn_attend_args* a) {
   if (a->T > kAttendMaxT || a->B > kAttendMaxB || a->kv_heads < 1 || a->q_heads < 1 || a->q_heads % a->kv_heads ||
       a->q_heads / a->kv_heads > kAttendMaxGroup || a->kv_heads > kMaxHeads || a->D < 8 || a->D > kAttendMaxD ||
       a->D % 8 || a->page_size < 1 || (int64_t)a->pages * a->page_size > kMaxSlots ||
-      (int64_t)a->max_pages * a->page_size > kMaxSlots)
+      (int64_t)a->max_pages * a->page_size > kMaxTokens)
     return MOE_FFN_ERR_UNSUPPORTED;
   const int64_t row = (int64_t)a->D;
   if (a->q_stride < row || a->q_head_stride < row || a->out_stride < row || a->out_head_stride < row ||

@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         a1 = fmaxf(a1, __shfl_xor_sync(kAll, a1, x));
       }
       if (__any_sync(kAll, a0 > m0 + kLazy || a1 > m1 + kLazy)) {
-        a0 = fmaxf(a0, m0);
-        a1 = fmaxf(a1, m1);
-        const float f0 = exp2_fast(m0 - attend_base(a0)), f1 = exp2_fast(m1 - attend_base(a1));
-        m0 = a0;
-        m1 = a1;
+        // (each row by its own: what the others hold must not change its roundings)
+        const bool own0 = a0 > m0 + kLazy, own1 = a1 > m1 + kLazy;
+        const float f0 = own0 ? exp2_fast(m0 - a0) : 1.f, f1 = own1 ? exp2_fast(m1 - a1) : 1.f;
+        if (own0) m0 = a0;
+        if (own1) m1 = a1;
         l0 *= f0;
         l1 *= f1;
 #pragma unroll

@@ -11,18 +11,24 @@
 // each, 32 columns each) overwrite as operand of the second product, and the
 // output, 64 or 128 columns a stream.
 //
-//   warps 0, 12  issue the products for the scores of a stream each, warps 13 and 14
-//                those of its weighted values (one warp for all took three times as
-//                long as the stream, one a stream half as long again)
-//   warp 1       tensor copies of keys and values into a ring, in that order
-//   warps 2, 3   queries of the next unit; and in the tiles that hold tokens which
-//                some rows do not see, they take values that are not finite out (a
-//                product with a weight of 0 has an effect then); the rows that do see
-//                them get them at the end
-//   warps 4-11   a thread a row: scores to weights, four warps a stream
+//   warps 0, 12   issue the products for the scores of a stream each,
+//   warps 13, 14  those of its weighted values (one warp for all took three times as
+//                 long as the stream of the cache, one a stream half as long again)
+//   warps 1, 15   tensor copies of keys (and queries), of values (one warp for both
+//                 took longer than the stream, too)
+//   warps 2, 3    in the tiles that hold tokens which some rows do not see, take values
+//                 that are not finite out (a product with a weight of 0 has an effect
+//                 then); the rows that do see them get them at the end.  Queries that
+//                 tensor copies cannot fetch
+//   warps 4-11    a thread a row: scores to weights, four warps a stream
 //
-// Every wait is bounded; a thread whose wait ran out goes on without waiting, so that
-// nobody is left at a barrier, and results become NaN.
+// Keys and values of each stream have rings of their own: every barrier then has one
+// waiter that meets all of its phases in turn.  (A wait by parity tells a phase from
+// the next only: with one ring for all, a waiter could be two phases ahead.)
+//
+// Every wait is bounded.  After one that ran out, in whichever thread, nobody waits,
+// issues or arrives any more, but all still meet at the block's barriers, and results
+// become NaN.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,11 +47,11 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 480, kTok = 64;  // tokens of a stream's half step
-constexpr int kOddUnits = 16;  // units whose mark of values taken out is kept
+constexpr int kThreads = 512, kTok = 64;  // tokens of a stream's half step
+constexpr int kOddUnits = 16;  // marks of values taken out: more than the units under way
 
-__host__ __device__ constexpr int slots_for(int dp) { return dp == 64 ? 14 : 9; }
-__host__ __device__ constexpr int wide_smem(int dp) { return slots_for(dp) * kTok * dp * 2 + 2 * 128 * dp * 2 + 1024; }
+__host__ __device__ constexpr int depth_for(int dp) { return dp == 64 ? 4 : 2; }  // tiles of a ring
+__host__ __device__ constexpr int wide_smem(int dp) { return 4 * depth_for(dp) * kTok * dp * 2 + 2 * 128 * dp * 2 + 1024; }
 
 __device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -119,10 +125,32 @@ MOE_DEV bool elected() {
   return r != 0u;
 }
 
-// A wait that ran out once is not waited for again.
-MOE_DEV void await(uint64_t* bar, uint32_t parity, bool& dead) {
-  if (!dead) dead = !mbar_wait(bar, parity);
+// A bounded wait.  `gone` is the block's: some wait has run out.
+MOE_DEV void await(uint64_t* bar, uint32_t parity, bool& dead, volatile int* gone) {
+  if (dead || mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t i = 1; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 31) == 0 && (*gone || global_ns() - t0 > kWaitLimitNs)) break;
+    if (i > 64) __nanosleep(32);
+  }
+  dead = true;
+  *gone = 1;
 }
+
+// A place in a ring and its pass.
+template <int DEPTH>
+struct Ring {
+  int slot, end;
+  uint32_t turn;
+  MOE_DEV Ring(int ring, uint32_t first) : slot(ring * DEPTH), end((ring + 1) * DEPTH), turn(first) {}
+  MOE_DEV void next() {
+    if (++slot == end) {
+      slot -= DEPTH;
+      turn ^= 1u;
+    }
+  }
+};
 
 // First token that some row of the unit's sequence may not see.
 MOE_DEV int seen_by_all(const AttendParams& P, const AttendSeq& s) {
@@ -148,7 +176,7 @@ MOE_DEV uint64_t seen_tokens(const AttendParams& P, const AttendSeq& s, int firs
 
 template <bool F16, int DP>
 __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_constant__ AttendParams P) {
-  constexpr int NS = slots_for(DP), kSlot = kTok * DP * 2, kQ = 128 * DP * 2, kHalves = DP / 64;
+  constexpr int kDepth = depth_for(DP), NS = 4 * kDepth, kSlot = kTok * DP * 2, kQ = 128 * DP * 2, kHalves = DP / 64;
   constexpr int kDt = F16 ? kF16 : kBf16;
   // (as in k_attend: the maximum stays within 2^8, fp16 weights are held 2^7 up)
   constexpr float kLazy = 8.f, kUp = F16 ? 7.f : 0.f;
@@ -156,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* const qs = smem + NS * kSlot;
-  __shared__ uint64_t full[NS], empty[NS], s_full[2][2], s_free[2][2], p_full[2][2], o_done[2], o_free, q_full[2], q_empty[2], clean[NS];
+  __shared__ uint64_t full[NS], empty[NS], s_full[2][2], s_free[2][2], p_full[2][2], o_free, q_full[2], q_empty[2], raw[2 * kDepth];
+  __shared__ int s_gone;
   __shared__ uint32_t s_tmem;
   __shared__ float2 s_stat[2][2][128];
   __shared__ uint32_t s_boxes[2][16], s_odd[kOddUnits];
@@ -172,12 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         mbar_init(&s_free[x][b], 1);
         mbar_init(&p_full[x][b], 128);
       }
-      mbar_init(&o_done[x], 1);
       mbar_init(&q_full[x], P.q_box ? 1 : 64);
       mbar_init(&q_empty[x], 2);
     }
     mbar_init(&o_free, 256);
-    for (int i = 0; i < NS; ++i) mbar_init(clean + i, 64);
+    for (int i = 0; i < 2 * kDepth; ++i) mbar_init(raw + i, 1);
+    s_gone = 0;
     mbar_fence_init();
     for (int i = 0; i < kOddUnits; ++i) s_odd[i] = 0u;
   }
@@ -204,121 +233,94 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   // a tile that holds tokens which some rows do not see
   auto mixed = [&](const AttendStep& s, int x) { return first_of(s, x) + kTok > seen_by_all(P, s.s); };
 
-  if (warp == 0 || warp >= 12) {
-    // ------------------------------------------------------------ products
-    const int x = warp == 0 || warp == 13 ? 0 : 1;  // the warp's stream
-    const bool scores = warp == 0 || warp == 12;
-    const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16), o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
-    // descriptors of the first slot and buffer; of values: columns are what lies together
-    const uint64_t k_desc0 = tc::smem_desc(smem_u32(smem), 16, 1024), q_desc0 = tc::smem_desc(smem_u32(qs), 16, 1024),
-                   v_desc0 = tc::smem_desc(smem_u32(smem), kTok * 128, 1024);
-    int slot = 0, unit = 0, count = 0, cleaned = 0;  // count: the stream's chunks so far
-    // mixed tiles in their order: as many barriers as slots, since those that are clean
-    // and not yet used lie in the ring
-    uint32_t turn = 0, clean_turn = 0;
-    auto next_slot = [&] {
-      if (++slot == NS) {
-        slot = 0;
-        turn ^= 1u;
-      }
-    };
-    auto next_clean = [&] {
-      if (++cleaned == NS) {
-        cleaned = 0;
-        clean_turn ^= 1u;
-      }
-    };
-    AttendStep before = a;
-    bool have = false, fresh = true;  // the unit's first product is still to come
-    for (bool more = a.left > 0; more || have;) {
-      // the keys of this step
-      if (more) {
-        if (scores && (!have || last_of_unit(before))) await(&q_full[unit & 1], unit >> 1 & 1, dead);
-        if (x == 1) next_slot();
-        if (there(a, x)) {
-          if (scores) {
-            const int buf = count & 1;
-            if (count > 1) await(&s_free[x][buf], (count >> 1) - 1 & 1, dead);
-            await(full + slot, turn, dead);
-            tc::tc_fence_after();
-            const uint64_t k_desc = desc_at(k_desc0, slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
-            const uint32_t to = tmem + x * 128 + buf * 64;
-            if (elected()) {
+  // (by whole warps, which stay of one mind)
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    await(bar, parity, dead, &s_gone);
+    dead = __any_sync(kAll, dead);
+  };
+  // (rings 0, 1: keys of the streams; 2, 3: values)
+  if (warp == 0 || warp == 12) {
+    // ------------------------------------------------------------ products: scores
+    const int x = warp == 0 ? 0 : 1;  // the warp's stream
+    const uint32_t s_desc = tc::instr_desc(128, kTok, 0, F16);
+    const uint64_t k_desc0 = tc::smem_desc(smem_u32(smem), 16, 1024), q_desc0 = tc::smem_desc(smem_u32(qs), 16, 1024);
+    Ring<kDepth> ring(x, 0u);
+    int unit = 0, count = 0;  // count: the stream's chunks so far
+    bool begin = true;
+    for (; a.left > 0; a.next(P)) {
+      if (begin) wait(&q_full[unit & 1], unit >> 1 & 1);
+      begin = last_of_unit(a);
+      if (there(a, x)) {
+        const int buf = count & 1;
+        if (count > 1) wait(&s_free[x][buf], (count >> 1) - 1 & 1);
+        wait(full + ring.slot, ring.turn);
+        tc::tc_fence_after();
+        const uint64_t k_desc = desc_at(k_desc0, ring.slot * kSlot), q_desc = desc_at(q_desc0, (unit & 1) * kQ);
+        const uint32_t to = tmem + x * 128 + buf * 64;
+        if (!dead && elected()) {
 #pragma unroll
-              for (int ks = 0; ks < DP / 16; ++ks)
-                tc::umma(to, desc_at(q_desc, (ks >> 2) * 128 * 128 + (ks & 3) * 32),
-                         desc_at(k_desc, (ks >> 2) * kTok * 128 + (ks & 3) * 32), s_desc, ks > 0);
-              tc::umma_commit(empty + slot);
-              tc::umma_commit(&s_full[x][buf]);
-            }
-            __syncwarp();
-            ++count;
-          }
-          next_slot();
+          for (int ks = 0; ks < DP / 16; ++ks)
+            tc::umma(to, desc_at(q_desc, (ks >> 2) * 128 * 128 + (ks & 3) * 32),
+                     desc_at(k_desc, (ks >> 2) * kTok * 128 + (ks & 3) * 32), s_desc, ks > 0);
+          tc::umma_commit(empty + ring.slot);
+          tc::umma_commit(&s_full[x][buf]);
         }
-        if (x == 0 && there(a, 1)) next_slot();
-        if (scores && last_of_unit(a)) {
-          if (elected()) tc::umma_commit(&q_empty[unit & 1]);
-          __syncwarp();
-          ++unit;
-        }
+        __syncwarp();
+        ring.next();
+        ++count;
       }
-      // the values of the step before
-      if (have) {
-        if (x == 1) {
-          if (mixed(before, 0)) next_clean();
-          next_slot();
-        }
-        if (there(before, x)) {
-          const bool mix = mixed(before, x);
-          if (!scores) {
-            const int buf = count & 1;
-            await(full + slot, turn, dead);
-            if (mix) await(clean + cleaned, clean_turn, dead);
-            await(&p_full[x][buf], count >> 1 & 1, dead);
-            if (fresh && unit > 0) await(&o_free, (unit - 1) & 1, dead);
-            tc::tc_fence_after();
-            const uint64_t v_desc = desc_at(v_desc0, slot * kSlot);
-            const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64;
-            const uint32_t add = !fresh;
-            if (elected()) {
-#pragma unroll
-              for (int term = 1; term >= 0; --term)
-#pragma unroll
-                for (int ks = 0; ks < kTok / 16; ++ks)
-                  umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc,
-                          term == 1 && ks == 0 ? add : 1u);
-              tc::umma_commit(empty + slot);
-              tc::umma_commit(&s_free[x][buf]);
-              tc::umma_commit(&o_done[x]);
-            }
-            __syncwarp();
-            fresh = false;
-            ++count;
-          }
-          if (mix) next_clean();
-          next_slot();
-        }
-        if (x == 0 && there(before, 1)) {
-          if (mixed(before, 1)) next_clean();
-          next_slot();
-        }
-        if (!scores && last_of_unit(before)) {
-          fresh = true;
-          ++unit;
-        }
+      if (begin) {
+        if (!dead && elected()) tc::umma_commit(&q_empty[unit & 1]);
+        __syncwarp();
+        ++unit;
       }
-      have = more;
-      before = a;
-      if (more) a.next(P);
-      more = a.left > 0;
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ keys and values
+  } else if (warp == 13 || warp == 14) {
+    // ------------------------------------------------------------ products: weighted values
+    const int x = warp - 13;
+    // (values: columns are what lies together)
+    const uint32_t o_desc = tc::instr_desc(128, DP, 0, F16) | 1u << 16;
+    const uint64_t v_desc0 = tc::smem_desc(smem_u32(smem), kTok * 128, 1024);
+    Ring<kDepth> ring(2 + x, 0u);
+    int unit = 0, count = 0;
+    bool fresh = true;  // the unit's first product is still to come
+    for (; a.left > 0; a.next(P)) {
+      if (there(a, x)) {
+        const int buf = count & 1;
+        wait(full + ring.slot, ring.turn);
+        wait(&p_full[x][buf], count >> 1 & 1);
+        if (fresh && unit > 0) wait(&o_free, (unit - 1) & 1);
+        tc::tc_fence_after();
+        const uint64_t v_desc = desc_at(v_desc0, ring.slot * kSlot);
+        const uint32_t to = tmem + kOut + x * DP, p_at = tmem + x * 128 + buf * 64, add = !fresh;
+        if (!dead && elected()) {
+#pragma unroll
+          for (int term = 1; term >= 0; --term)
+#pragma unroll
+            for (int ks = 0; ks < kTok / 16; ++ks)
+              umma_ts(to, p_at + (ks >> 1) * 32 + term * 16 + (ks & 1) * 8, desc_at(v_desc, ks * 16 * 128), o_desc,
+                      term == 1 && ks == 0 ? add : 1u);
+          tc::umma_commit(empty + ring.slot);
+          tc::umma_commit(&s_free[x][buf]);
+        }
+        __syncwarp();
+        ring.next();
+        ++count;
+        fresh = false;
+      }
+      if (last_of_unit(a)) {
+        fresh = true;
+        ++unit;
+      }
+    }
+  } else if (warp == 1 || warp == 15) {
+    // ------------------------------------------------------------ copies
+    const bool keys = warp == 1;
+    const CUtensorMap* const map = keys ? &P.tm_k : &P.tm_v;
     const int boxes = kTok / P.box;  // of a tile; lane b < boxes knows box b's page
     const uint64_t once = policy_evict_first(), again = policy_evict_last();
-    int slot = 0, i = 0;
-    uint32_t turn = 1;  // the first pass finds the slots empty
+    Ring<kDepth> rings[2] = {Ring<kDepth>(keys ? 0 : 2, 1u), Ring<kDepth>(keys ? 1 : 3, 1u)};  // (empty at first)
+    int unit = 0, mixed_at = 0;
     struct Where {
       int page[2], in[2];  // the box's page (behind the cache: zeros) and its first slot there
     };
@@ -333,37 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       }
       return w;
     };
-    auto load = [&](const CUtensorMap* map, const AttendStep& s, int page, int in) {
-      await(empty + slot, turn, dead);
-      const uint64_t policy = s.s.tiles > 1 ? again : once;
-      uint8_t* const to = smem + slot * kSlot;
-      const int known = (uint32_t)page < (uint32_t)P.pages ? page : P.pages;
-      if (elected()) mbar_arrive_expect_tx(full + slot, kSlot);
-      __syncwarp();
-#pragma unroll 1
-      for (int b = 0; b < boxes; ++b) {
-        const int pg = __shfl_sync(kAll, known, b), at = __shfl_sync(kAll, in, b);
-        const int c1 = P.slot_first ? at : s.head, c2 = P.slot_first ? s.head : at;
-        if (elected()) {
-#pragma unroll
-          for (int half = 0; half < kHalves; ++half)
-            tensor_load_4d(to + half * kTok * 128 + b * P.box * 128, map, 64 * half, c1, c2, pg, full + slot, policy);
-        }
-        __syncwarp();
-      }
-      if (++slot == NS) {
-        slot = 0;
-        turn ^= 1u;
-      }
-    };
-    AttendStep before = a;
-    Where now = look(a), then = now;
-    int unit = 0;
-    for (; a.left > 0; ++i) {
-      if (P.q_box && (i == 0 || last_of_unit(before))) {
+    Where now = look(a);
+    bool begin = true;
+    for (int i = 0; a.left > 0; ++i) {
+      if (keys && begin && P.q_box) {
         // the unit's queries: q_box tokens of the group's heads are its rows in their order
-        if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
-        if (elected()) {
+        if (unit >= 2) wait(&q_empty[unit & 1], (unit >> 1) - 1 & 1);
+        if (!dead && elected()) {
           mbar_arrive_expect_tx(&q_full[unit & 1], kHalves * 128 * P.G * P.q_box);
 #pragma unroll
           for (int half = 0; half < kHalves; ++half)
@@ -373,42 +351,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         __syncwarp();
         ++unit;
       }
+      begin = last_of_unit(a);
       AttendStep next = a;
       next.next(P);
       const Where soon = look(next);
+      const uint64_t policy = a.s.tiles > 1 ? again : once;
+#pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!there(a, x)) continue;
-        const uint32_t known = __ballot_sync(kAll, (uint32_t)now.page[x] < (uint32_t)P.pages);
-        if (lane == 0) s_boxes[x][i & 15] = known;
-        load(&P.tm_k, a, now.page[x], now.in[x]);
+        const int known = (uint32_t)now.page[x] < (uint32_t)P.pages ? now.page[x] : P.pages;
+        if (keys) {
+          const uint32_t real = __ballot_sync(kAll, known < P.pages);
+          if (lane == 0) s_boxes[x][i & 15] = real;
+        }
+        wait(empty + rings[x].slot, rings[x].turn);
+        // (values that have to be looked through first: on a barrier of their own)
+        uint64_t* bar = full + rings[x].slot;
+        if (!keys && mixed(a, x)) {
+          bar = raw + mixed_at;
+          mixed_at = mixed_at + 1 == 2 * kDepth ? 0 : mixed_at + 1;
+        }
+        uint8_t* const to = smem + rings[x].slot * kSlot;
+        if (!dead && elected()) mbar_arrive_expect_tx(bar, kSlot);
+        __syncwarp();
+#pragma unroll 1
+        for (int b = 0; b < boxes; ++b) {
+          const int page = __shfl_sync(kAll, known, b), in = __shfl_sync(kAll, now.in[x], b);
+          const int c1 = P.slot_first ? in : a.head, c2 = P.slot_first ? a.head : in;
+          if (!dead && elected()) {
+#pragma unroll
+            for (int half = 0; half < kHalves; ++half)
+              tensor_load_4d(to + half * kTok * 128 + b * P.box * 128, map, 64 * half, c1, c2, page, bar, policy);
+          }
+          __syncwarp();
+        }
+        rings[x].next();
       }
-      if (i > 0)
-        for (int x = 0; x < 2; ++x)
-          if (there(before, x)) load(&P.tm_v, before, then.page[x], then.in[x]);
-      before = a;
-      then = now;
       a = next;
       now = soon;
     }
-    if (i > 0)
-      for (int x = 0; x < 2; ++x)
-        if (there(before, x)) load(&P.tm_v, before, then.page[x], then.in[x]);
   } else if (warp < 4) {
-    // ------------------------------------------------------------ queries; values that are not finite
+    // ------------------------------------------------------------ values that are not finite; queries
     const int th = tid - 64;
-    int slot = 0, unit = 0, unit_before = 0, i = 0, cleaned = 0;
-    uint32_t turn = 0;
-    auto next_slot = [&] {
-      if (++slot == NS) {
-        slot = 0;
-        turn ^= 1u;
-      }
-    };
+    Ring<kDepth> rings[2] = {Ring<kDepth>(2, 0u), Ring<kDepth>(3, 0u)};
+    int unit = 0, mixed_at = 0;
+    uint32_t mixed_turn = 0;
     auto queries = [&](const AttendStep& s) {
-      // (marks of units far behind, cleared for those as far ahead)
-      if (unit >= 2) await(&q_empty[unit & 1], (unit >> 1) - 1 & 1, dead);
-      if (th == 0) s_odd[(unit + kOddUnits / 2) % kOddUnits] = 0u;
-      if (P.q_box) return;  // by tensor copies
+      if (unit >= 2) wait(&q_empty[unit & 1], (unit >> 1) - 1 & 1);
       uint8_t* const to = qs + (unit & 1) * kQ;
       const int rows = s.s.n * P.G, r0 = s.tile * P.rows;
       // eight pieces of 16 bytes are asked for at a time
@@ -431,54 +420,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         }
       }
       fence_proxy_async();
-      mbar_arrive(&q_full[unit & 1]);
+      if (!dead) mbar_arrive(&q_full[unit & 1]);
     };
-    auto values = [&](const AttendStep& s, int x) {
-      if (mixed(s, x)) {
-        await(full + slot, turn, dead);
-        const int from = max(seen_by_all(P, s.s) - first_of(s, x), 0);
-        uint8_t* const tile = smem + slot * kSlot;
-        bool odd = false;
-        for (int y = th; y < kTok * DP / 8; y += 64) {
-          const int r = y / (DP / 8), c = y % (DP / 8);
-          if (r < from) continue;
-          uint4* const at = reinterpret_cast<uint4*>(tile + (c >> 3) * kTok * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          uint4 v = *at;
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          bool any = false;
+    bool begin = true;
+    for (; a.left > 0; a.next(P)) {
+      if (begin && !P.q_box) queries(a);
+      begin = last_of_unit(a);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (odd16<F16>(w[e] & 0xFFFFu)) any = true, w[e] &= 0xFFFF0000u;
-            if (odd16<F16>(w[e] >> 16)) any = true, w[e] &= 0xFFFFu;
+      for (int x = 0; x < 2; ++x) {
+        if (!there(a, x)) continue;
+        if (mixed(a, x)) {
+          wait(raw + mixed_at, mixed_turn);
+          if (++mixed_at == 2 * kDepth) {
+            mixed_at = 0;
+            mixed_turn ^= 1u;
           }
-          if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
-          odd |= any;
+          const int from = max(seen_by_all(P, a.s) - first_of(a, x), 0);
+          uint8_t* const tile = smem + rings[x].slot * kSlot;
+          bool odd = false;
+          for (int y = th; y < kTok * DP / 8; y += 64) {
+            const int r = y / (DP / 8), c = y % (DP / 8);
+            if (r < from) continue;
+            uint4* const at = reinterpret_cast<uint4*>(tile + (c >> 3) * kTok * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (odd16<F16>(w[e] & 0xFFFFu)) any = true, w[e] &= 0xFFFF0000u;
+              if (odd16<F16>(w[e] >> 16)) any = true, w[e] &= 0xFFFFu;
+            }
+            if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+            odd |= any;
+          }
+          if (odd) s_odd[unit % kOddUnits] = (uint32_t)unit + 1u;  // the unit's mark: its number
+          fence_proxy_async();
+          named_bar_sync(2, 64);
+          if (th == 0 && !dead) mbar_arrive(full + rings[x].slot);
         }
-        if (odd) s_odd[unit_before % kOddUnits] = 1u;
-        fence_proxy_async();
-        mbar_arrive(clean + cleaned);
-        cleaned = cleaned + 1 == NS ? 0 : cleaned + 1;
+        rings[x].next();
       }
-      next_slot();
-    };
-    AttendStep before = a;
-    while (a.left > 0 || i > 0) {
-      const bool more = a.left > 0;
-      if (more) {
-        if (i == 0 || last_of_unit(before)) queries(a);
-        for (int x = 0; x < 2; ++x)
-          if (there(a, x)) next_slot();
-      }
-      if (i > 0) {
-        for (int x = 0; x < 2; ++x)
-          if (there(before, x)) values(before, x);
-        if (last_of_unit(before)) ++unit_before;
-      }
-      if (!more) break;
-      if (last_of_unit(a)) ++unit;
-      before = a;
-      a.next(P);
-      ++i;
+      if (begin) ++unit;
     }
   } else {
     // ------------------------------------------------------------ weights
@@ -503,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         if (there(a, x)) {
           const int buf = count & 1;
           const uint32_t at = tmem + lanes + x * 128 + buf * 64;
-          await(&s_full[x][buf], count >> 1 & 1, dead);
+          wait(&s_full[x][buf], count >> 1 & 1);
           tc::tc_fence_after();
           const uint32_t boxes = s_boxes[x][i & 15], all = (1u << kTok / P.box) - 1u;
           const bool part = mixed(a, x) || boxes != all, changed = part || P.softcap > 0.f || flip;
@@ -547,10 +529,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
           if (!some) {
             m = mx;
           } else if (__any_sync(kAll, mx > m + kLazy)) {
-            const float up = fmaxf(m, mx), f = exp2_fast(m - attend_base(up));
-            m = up;
+            // (each row by its own: what the others hold, behind the unit's rows too, must not
+            // change its roundings)
+            const bool own = mx > m + kLazy;
+            const float f = own ? exp2_fast(m - mx) : 1.f;
+            if (own) m = mx;
             l *= f;
-            await(&o_done[x], count - 1 & 1, dead);
+            wait(&s_free[x][count - 1 & 1], count - 1 >> 1 & 1);
             tc::tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < DP; c += 16) {
@@ -585,14 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
           tc::tc_fence_before();
-          mbar_arrive(&p_full[x][buf]);
+          if (!dead) mbar_arrive(&p_full[x][buf]);
           some = true;
           ++count;
         }
         if (!end) a.next(P);
       }
       // the streams meet: each half of the threads joins half of the columns
-      if (some) await(&o_done[x], count - 1 & 1, dead);
+      if (some) wait(&s_free[x][count - 1 & 1], count - 1 >> 1 & 1);
       s_stat[unit & 1][x][row] = make_float2(m - kUp, dead ? __int_as_float(0x7FFFFFFF) : l);
       named_bar_sync(1, 256);
       tc::tc_fence_after();
@@ -600,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       const float top = fmaxf(st0.x, st1.x), base = attend_base(top);
       const float f0 = exp2_fast(st0.x - base), f1 = exp2_fast(st1.x - base), sum = fmaf(st0.y, f0, st1.y * f1);
       const bool from_start = chunk0 == 0, whole = from_start && a.chunk + 1 == a.s.chunks;
-      const bool odd = s_odd[unit % kOddUnits] != 0u;
+      const bool odd = s_odd[unit % kOddUnits] == (uint32_t)unit + 1u;
       const long long slot = 2 * blockIdx.x + (from_start ? 1 : 0);
       const int h = a.head * P.G + r - j * P.G;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -650,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         }
       }
       tc::tc_fence_before();
-      mbar_arrive(&o_free);
+      if (!dead) mbar_arrive(&o_free);
       if (x == 0 && t >= 0) {
         if (!whole)
           P.stat[slot * 128 + row] = make_float2(top, sum);
@@ -663,6 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (s_gone)  // copies and products that are under way end by themselves, in microseconds
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   if (warp == 0) {
     tc::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");

@@ -486,7 +486,7 @@ int moe_ffn_append_kv(const moe_ffn_append_args* args, moe_ffn_stream_t stream, 
  * with fp32 out: three).  Caches as in moe_ffn_append_kv, 16-byte aligned with
  * strides that are multiples of 8.
  * T <= 1048576, B <= 65536, q_heads a multiple of kv_heads and at most 128 kv_heads, kv_heads <= 65535,
- * D a multiple of 8 up to 256, pages page_size and max_pages page_size < 2^31.
+ * D a multiple of 8 up to 256, pages page_size < 2^31, max_pages page_size <= 2^30.
  * The workspace (256-byte aligned, scratch) holds what
  * moe_ffn_attend_workspace reports; calls that overlap on the GPU need one each.
  */

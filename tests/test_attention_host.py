@@ -108,7 +108,7 @@ def attend_args(**kw):
        (dict(q_heads=0), UNSUPPORTED), (dict(q_heads=9), UNSUPPORTED), (dict(q_heads=258), UNSUPPORTED),
        (dict(D=0), UNSUPPORTED), (dict(D=60), UNSUPPORTED), (dict(D=264), UNSUPPORTED), (dict(page_size=0), UNSUPPORTED),
        (dict(page_size=1 << 20, pages=1 << 11), UNSUPPORTED),
-       (dict(page_size=1 << 20, pages=1, max_pages=1 << 11, table_stride=1 << 11), UNSUPPORTED)])
+       (dict(page_size=1 << 20, pages=1, max_pages=1025, table_stride=1025), UNSUPPORTED)])
 def test_attend_refuses(lib, change, status):
     assert lib.moe_ffn_attend(attend_args(**change), None, P, 1 << 40, *[P] * 9) == status
     n = ctypes.c_size_t()

@@ -352,3 +352,24 @@ def test_a_sequence_by_itself_and_among_others():
 def test_many_sequences():
     host = random.Random(1)
     Case([(host.randint(0, 90), host.choice([1, 1, 2])) for _ in range(1500)], D=64, Hq=2, Hkv=1, page=16).check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [8, 64])
+def test_many_units_of_many_rows(D, page):
+    """Several units of a few steps for every block, one behind the other, the same bits every time."""
+    host = random.Random(D)
+    seqs = [(host.choice([16, 40, 64, 65, 128, 129, 300]), host.choice([16, 16, 3, 9])) for _ in range(1300)]
+    c = Case(seqs, D=D, Hq=8, Hkv=1, page=page, mask="tree", seed=D, poison=True)
+    want = c.check()
+    for _ in range(5):
+        assert torch.equal(c.call(), want)
+
+
+@pytest.mark.parametrize("n,G", [(16, 8), (1, 64), (40, 3)])
+def test_long_units_of_many_rows(n, G):
+    """Many steps a block, parts of units in many blocks, the same bits every time."""
+    c = Case([(8192, n), (5000, n), (7300, n)] + [(2048, n)] * 9, D=128, Hq=4 * G, Hkv=4, page=64, mask="tree" if n > 1 else None, seed=n)
+    want = c.check()
+    for _ in range(20):
+        assert torch.equal(c.call(), want)
