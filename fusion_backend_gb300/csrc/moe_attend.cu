@@ -389,11 +389,13 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         l1 += __shfl_xor_sync(kAll, l1, x);
       }
       __syncwarp();
+      // (the eight rows that a store holds in different banks)
       float* const left = reinterpret_cast<float*>(ring + stage * kSlot);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        *reinterpret_cast<float2*>(left + g * DP + 8 * n + 2 * q) = make_float2(o[n][0], o[n][1]);
-        *reinterpret_cast<float2*>(left + (g + 8) * DP + 8 * n + 2 * q) = make_float2(o[n][2], o[n][3]);
+        const int at = (8 * n + 2 * q) ^ (g << 3);
+        *reinterpret_cast<float2*>(left + g * DP + at) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(left + (g + 8) * DP + at) = make_float2(o[n][2], o[n][3]);
       }
       if (q == 0) {
         const float none = __int_as_float(0x7FFFFFFF);
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         for (int w = 0; w < W; ++w) {
           const float2 st = s_stat[w][r];
           const float f = exp2_fast(st.x - base);
-          const float4 a = *reinterpret_cast<const float4*>(smem + (w * S + stage) * kSlot + (r * DP + d) * 4);
+          const float4 a = *reinterpret_cast<const float4*>(smem + (w * S + stage) * kSlot +
+                                                             (r * DP + (d ^ ((r & 7) << 3))) * 4);
           l = fmaf(st.y, f, l);
           v.x = fmaf(a.x, f, v.x);
           v.y = fmaf(a.y, f, v.y);

@@ -11,7 +11,7 @@
 //
 // mma.m16n8k16 with the rows of W as its rows: 16-byte pieces of 8 rows are what
 // ldmatrix hands out, a lane then holds 8 codes of rows g and g + 8 that lie in
-// one group, as bf16 (fp16) numbers c - 8 exactly.  The order of k inside those 8
+// one group, as bf16 (fp16) numbers (c - 8) / 64 (c - 8) exactly.  The order of k inside those 8
 // follows the nibbles (0 4, 1 5, 2 6, 3 7), x is put in the same order where it is
 // loaded: straight from global memory, since each warp of a block has other
 // columns of it, and once for all tiles where a warp has one slab of every tile.  A
@@ -35,18 +35,35 @@ namespace {
 constexpr int kSlab = 256;  // columns of a slab: 128 bytes of codes
 constexpr int kChunks = kSlab / 32;
 
-// Code pairs (nibbles 0, 4 of v) as numbers c - 8: the nibble in the mantissa of
-// 128 (bf16), 1024 (fp16), less 136 (1032), exact.
+// The codes of a word as four pairs of numbers: nibbles (0, 4), (1, 5), (2, 6),
+// (3, 7).  bf16: (c - 8) / 64; fp16: c - 8; exactly.  A mask and a multiply-add a
+// pair, and one shift for all.  bf16: the low byte of a number with nothing else set,
+// N, is N 2^-133, the subnormal range and the first exponent above it being one
+// scale: so a nibble at bit 0 or 4 is c 2^-133 or c 2^-129.  fp16: a nibble at bit 0
+// or 4 of 1024 is 1024 + c or 1024 + 16 c.  (A shift for every pair: 7 integer
+// instructions a word instead of 5, which run at half the rate, and bound the kernel.)
 template <bool F16>
-MOE_DEV uint32_t code_pair(uint32_t v) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(0x000F000Fu), "r"(F16 ? 0x64006400u : 0x43004300u));
-  if constexpr (F16)
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x64086408u));
-  else
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x43084308u));
-  return r;
+MOE_DEV void code_pairs(uint32_t v, uint32_t (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? v : v >> 8, mask = i & 1 ? 0x00F000F0u : 0x000F000Fu;
+    if constexpr (F16) {
+      uint32_t n;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(n) : "r"(w), "r"(mask), "r"(0x64006400u));
+      // 1 n - 1032, n / 16 - 72
+      asm("fma.rn.f16x2 %0, %1, %2, %3;"
+          : "=r"(r[i])
+          : "r"(n), "r"(i & 1 ? 0x2C002C00u : 0x3C003C00u), "r"(i & 1 ? 0xD480D480u : 0xE408E408u));
+    } else {
+      // 2^127 n - 1 / 8, 2^123 n - 1 / 8
+      asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+          : "=r"(r[i])
+          : "r"(w & mask), "r"(i & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(0xBE00BE00u));
+    }
+  }
 }
+template <bool F16>
+constexpr float kCodeScale = F16 ? 1.f : 64.f;
 
 // Shared memory: the warps' rings of codes, of scales (16 bytes a row and slab),
 // the sums of a batch of BT tiles, the barriers.
@@ -182,18 +199,18 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
             uint32_t(&b)[NT][4] = HOLD ? xh[HOLD ? c2 + h : 0] : x;
             const bool first = ((c2 + h) & ((1 << GL) - 1)) == 0;
             const uint32_t v0 = w[2 * h], v1 = w[2 * h + 1];  // rows g and g + 8
-            const uint32_t a0 = code_pair<F16>(v0), b0 = code_pair<F16>(v1), a1 = code_pair<F16>(v0 >> 4),
-                           b1 = code_pair<F16>(v1 >> 4), a2 = code_pair<F16>(v0 >> 8), b2 = code_pair<F16>(v1 >> 8),
-                           a3 = code_pair<F16>(v0 >> 12), b3 = code_pair<F16>(v1 >> 12);
+            uint32_t a[4], e[4];
+            code_pairs<F16>(v0, a);
+            code_pairs<F16>(v1, e);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               if (first)
-                mma16_first<F16>(part[n], a0, b0, a1, b1, b[n][0], b[n][1]);
+                mma16_first<F16>(part[n], a[0], e[0], a[1], e[1], b[n][0], b[n][1]);
               else
-                mma16<F16>(part[n], a0, b0, a1, b1, b[n][0], b[n][1]);
+                mma16<F16>(part[n], a[0], e[0], a[1], e[1], b[n][0], b[n][1]);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<F16>(part[n], a2, b2, a3, b3, b[n][2], b[n][3]);
+            for (int n = 0; n < NT; ++n) mma16<F16>(part[n], a[2], e[2], a[3], e[3], b[n][2], b[n][3]);
             if (((c2 + h + 1) & ((1 << GL) - 1)) == 0) {
               const int at = (c2 + h) >> GL;
               const float s0 = scale_of(sc0, at), s1 = scale_of(sc1, at);
@@ -231,7 +248,7 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) own[(g + 8 * (e >> 1)) * L::kPitch + 8 * n + 2 * q + (e & 1)] = acc[n][e];
+        for (int e = 0; e < 4; ++e) own[(g + 8 * (e >> 1)) * L::kPitch + 8 * n + 2 * q + (e & 1)] = acc[n][e] * kCodeScale<F16>;
     }
     __syncthreads();
     // the warps' sums, in their order
