@@ -729,7 +729,7 @@ int moe_ffn_project(const moe_ffn_project_args* a, moe_ffn_stream_t stream, cons
   if ((a->x_dtype != MOE_FFN_ACT_BF16 && a->x_dtype != MOE_FFN_ACT_F16) || !valid_elem(a->y_dtype))
     return MOE_FFN_ERR_INVALID_ARG;
   if (a->T > kProjectMaxT || (a->group != 32 && a->group != 64 && a->group != 128) || a->K < a->group ||
-      a->K > 65536 || a->K % a->group || a->N < 1 || a->N > (1 << 24))
+      a->K > 65536 || a->K % a->group || a->N < 1 || a->N > (1 << 24) || a->w_stride >= 1ll << 40)
     return MOE_FFN_ERR_UNSUPPORTED;
   if (a->x_stride < a->K || a->y_stride < a->N || a->w_stride < a->K / 2 + a->K / a->group * 2)
     return MOE_FFN_ERR_INVALID_ARG;

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   }
   pdl_wait();
   pdl_launch_dependents();
+  fence_proxy_async_global();  // what the kernel before wrote, for the tensor copies
   AttendStep now = attend_begin<32 * W>(P);
   if (now.left <= 0) return;
   // columns that no copy writes

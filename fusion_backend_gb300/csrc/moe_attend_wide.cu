@@ -14,7 +14,7 @@
 //   warps 0, 12   issue the products for the scores of a stream each,
 //   warps 13, 14  those of its weighted values (one warp for all took three times as
 //                 long as the stream of the cache, one a stream half as long again)
-//   warps 1, 15   tensor copies of keys (and queries), of values (one warp for both
+//   warps 1, 15   tensor copies of keys, of values (and queries) (one warp for both
 //                 took longer than the stream, too)
 //   warps 2, 3    in the tiles that hold tokens which some rows do not see, take values
 //                 that are not finite out (a product with a weight of 0 has an effect
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   }
   pdl_wait();
   pdl_launch_dependents();
+  fence_proxy_async_global();  // what the kernel before wrote, for the tensor copies
   AttendStep a = attend_begin<kThreads>(P);
   tc::tc_fence_before();
   __syncthreads();
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
     Where now = look(a);
     bool begin = true;
     for (int i = 0; a.left > 0; ++i) {
-      if (keys && begin && P.q_box) {
+      if (!keys && begin && P.q_box) {
         // the unit's queries: q_box tokens of the group's heads are its rows in their order
         if (unit >= 2) wait(&q_empty[unit & 1], (unit >> 1) - 1 & 1);
         if (!dead && elected()) {
@@ -353,11 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
       }
       begin = last_of_unit(a);
       AttendStep next = a;
-      next.next(P);
-      const Where soon = look(next);
+      Where soon;
       const uint64_t policy = a.s.tiles > 1 ? again : once;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
+        if (x == 1) {
+          // the next step's pages, behind this one's first copy
+          next.next(P);
+          soon = look(next);
+        }
         if (!there(a, x)) continue;
         const int known = (uint32_t)now.page[x] < (uint32_t)P.pages ? now.page[x] : P.pages;
         if (keys) {

@@ -337,7 +337,7 @@ cudaError_t launch_adapters(AdapterParams p, cudaStream_t stream);
 
 // ---- the attention half of a block (moe_project.cu, moe_append.cu,
 // moe_attend.cu); fields as in the public argument blocks.
-constexpr int kMaxHeads = 65535;
+constexpr int kMaxHeads = 4096;
 constexpr int kProjectMaxT = 1024;
 constexpr int kAppendMaxT = 1 << 24, kAppendMaxD = 512;
 constexpr int kAttendMaxT = 1 << 20, kAttendMaxB = 65536, kAttendMaxD = 256;

@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
   }
   __syncwarp();
   pdl_wait();
+  fence_proxy_async_global();
 
   // the warp's steps: its slabs of its tiles, in order
   int tile_in = lo + tpart, slab_in = 0;
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int t = t0 + 8 * j + g;
-      const uint4 v = t < P.T ? __ldg(reinterpret_cast<const uint4*>(P.x + (size_t)t * P.x_stride + k + 8 * q))
+      const uint4 v = t < P.T ? *reinterpret_cast<const uint4*>(P.x + (size_t)t * P.x_stride + k + 8 * q)
                               : make_uint4(0u, 0u, 0u, 0u);
       x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
     }

@@ -414,7 +414,7 @@ int moe_ffn_add_adapters(const moe_ffn_adapters_args* args, moe_ffn_stream_t str
  * x enter the products exactly; sums, scales and bias are in fp32, y is rounded
  * once.  y overlaps no other tensor.
  * x 16-byte aligned, its stride a multiple of 8; w 16-byte aligned, w_stride a
- * multiple of 16.  T <= 1024, group 32, 64 or 128, K <= 65536 a multiple of
+ * multiple of 16 below 2^40.  T <= 1024, group 32, 64 or 128, K <= 65536 a multiple of
  * group, 1 <= N <= 16777216.
  */
 typedef struct {
@@ -446,7 +446,7 @@ int moe_ffn_project(const moe_ffn_project_args* args, moe_ffn_stream_t stream, c
  * one call have different slots (where two have the same, either's elements may
  * remain).
  * q_out may be q (same dtype and strides); nothing else overlaps.
- * T <= 16777216, 1 <= D <= 512, rot even, 0 <= rot <= D, heads <= 65535, pages
+ * T <= 16777216, 1 <= D <= 512, rot even, 0 <= rot <= D, at most 4096 heads each, pages
  * page_size < 2^31.  Head strides are at least D.
  */
 typedef struct {
@@ -485,7 +485,7 @@ int moe_ffn_append_kv(const moe_ffn_append_args* args, moe_ffn_stream_t stream, 
  * enter the second product as the sum of two numbers of the cache's type (bf16
  * with fp32 out: three).  Caches as in moe_ffn_append_kv, 16-byte aligned with
  * strides that are multiples of 8.
- * T <= 1048576, B <= 65536, q_heads a multiple of kv_heads and at most 128 kv_heads, kv_heads <= 65535,
+ * T <= 1048576, B <= 65536, q_heads a multiple of kv_heads and at most 128 kv_heads, kv_heads <= 4096,
  * D a multiple of 8 up to 256, pages page_size < 2^31, max_pages page_size <= 2^30.
  * The workspace (256-byte aligned, scratch) holds what
  * moe_ffn_attend_workspace reports; calls that overlap on the GPU need one each.

@@ -37,7 +37,7 @@ INVALID, UNSUPPORTED, MISALIGNED = fb.ERR_INVALID_ARG, fb.ERR_UNSUPPORTED, fb.ER
     (dict(x_stride=255), INVALID), (dict(y_stride=63), INVALID), (dict(w_stride=128), INVALID), (dict(w_stride=0), INVALID),
     (dict(w_stride=-144), INVALID), (dict(T=1025), UNSUPPORTED), (dict(group=16), UNSUPPORTED), (dict(group=0), UNSUPPORTED),
     (dict(K=0), UNSUPPORTED), (dict(K=240), UNSUPPORTED), (dict(K=65568), UNSUPPORTED), (dict(K=-32), UNSUPPORTED),
-    (dict(group=64, K=288), UNSUPPORTED), (dict(N=0), UNSUPPORTED), (dict(N=(1 << 24) + 1), UNSUPPORTED),
+    (dict(group=64, K=288), UNSUPPORTED), (dict(N=0), UNSUPPORTED), (dict(N=(1 << 24) + 1), UNSUPPORTED), (dict(w_stride=1 << 40), UNSUPPORTED),
     (dict(x_stride=260), MISALIGNED), (dict(w_stride=152), MISALIGNED)])
 def test_project_refuses(lib, change, status):
     assert lib.moe_ffn_project(project_args(**change), None, P, P, P, P) == status
@@ -69,8 +69,8 @@ def append_args(**kw):
     + [({n: 63}, INVALID) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride", "v_stride", "v_head_stride",
                                     "q_out_stride", "q_out_head_stride", "kc_page_stride", "kc_slot_stride",
                                     "kc_head_stride", "vc_page_stride", "vc_slot_stride", "vc_head_stride")]
-    + [(dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(kv_heads=0), UNSUPPORTED), (dict(kv_heads=65537), UNSUPPORTED),
-       (dict(q_heads=65537), UNSUPPORTED), (dict(D=0), UNSUPPORTED), (dict(D=513), UNSUPPORTED), (dict(rot=-2), UNSUPPORTED),
+    + [(dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(kv_heads=0), UNSUPPORTED), (dict(kv_heads=4097), UNSUPPORTED),
+       (dict(q_heads=4097), UNSUPPORTED), (dict(D=0), UNSUPPORTED), (dict(D=513), UNSUPPORTED), (dict(rot=-2), UNSUPPORTED),
        (dict(rot=66), UNSUPPORTED), (dict(rot=31), UNSUPPORTED), (dict(page_size=0), UNSUPPORTED),
        (dict(page_size=1 << 16, pages=1 << 15), UNSUPPORTED)])
 def test_append_refuses(lib, change, status):
