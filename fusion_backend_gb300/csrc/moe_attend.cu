@@ -472,10 +472,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   pdl_wait();
   const AttendFrom at = P.from[c];
-  if (at.chunk == 0) return;
-  const long long unit = at.share.from(c) - at.chunk;
+  if (at.parts == 0) return;
   // the first part begins its unit, the others go on
-  const int c0 = at.share.block_of(unit), c1 = at.share.block_of(unit + at.chunks - 1), parts = c1 - c0 + 1;
+  const int c0 = at.first, parts = at.parts, c1 = c0 + parts - 1;
   const int rows = min(at.n * P.G - at.tile * P.rows, P.rows);
   const bool together = parts > kJoinWarps;
   const int workers = (parts - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
@@ -483,23 +482,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
     const int r = worker + workers * k;
     if (r >= rows) break;
     auto slot_of = [&](int i) { return (long long)(i == c0 ? 2 * c0 + 1 : 2 * i) * P.rows + r; };
-    const int first = c0 + (together ? warp : 0), step = together ? kJoinWarps : 1;
-    float m = -INFINITY;
-    for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, P.stat[slot_of(i)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-    const float base = attend_base(m);
-    float l = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 acc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (together) {
+      for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, P.stat[slot_of(i)].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    }
+    // eight parts at a time; few parts: all of them, their maximum is found on the way
+    const int first = c0 + (together ? warp : 0), step = together ? kJoinWarps : 1;
 #pragma unroll 1
     for (int i0 = first; i0 <= c1; i0 += 8 * step) {
       float2 st[8];
       float4 a[8][NV];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int i = min(i0 + u * step, c1);
+        const int i = i0 + u * step;
+        if (i > c1) break;
         st[u] = P.stat[slot_of(i)];
         const float* const row = P.part + slot_of(i) * P.width;
 #pragma unroll
@@ -507,6 +508,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
           a[u][v] = 4 * lane + 128 * v < P.D ? *reinterpret_cast<const float4*>(row + 4 * lane + 128 * v)
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      if (!together) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (i0 + u <= c1) m = fmaxf(m, st[u].x);
+      }
+      const float base = attend_base(m);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (i0 + u * step > c1) break;

@@ -79,11 +79,12 @@ struct AttendStep {
   }
 };
 
-// What the second kernel has to know of a block's range: where it begins (chunk 0:
-// not inside a unit, or no range).
+// What the second kernel has to know of a block's range that begins inside a unit:
+// the unit, the block in which it began and the number of its parts (0: the range
+// begins with a unit, or there is none).
 struct AttendFrom {
-  AttendShare share;
-  int t0, n, chunks, head, tile, chunk;
+  int first, parts;
+  int t0, n, head, tile;
 };
 
 // The range of this block: its first step, where it begins also left in the
@@ -160,7 +161,15 @@ MOE_DEV AttendStep attend_begin(const AttendParams& P) {
     a.head = (int)attend_div(unit, a.s.tiles);
     a.tile = (int)(unit - (long long)a.head * a.s.tiles);
   }
-  if (tid == 0) P.from[blockIdx.x] = AttendFrom{share, a.s.t0, a.s.n, a.s.chunks, a.head, a.tile, a.chunk};
+  if (tid == 64) {
+    AttendFrom at = {0, 0, a.s.t0, a.s.n, a.head, a.tile};
+    if (a.chunk > 0) {
+      const long long unit = from - a.chunk;
+      at.first = share.block_of(unit);
+      at.parts = share.block_of(unit + a.s.chunks - 1) - at.first + 1;
+    }
+    P.from[blockIdx.x] = at;
+  }
   return a;
 }
 

@@ -664,42 +664,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
 // Joins the parts of a unit, as k_attend_join does.  An item is 8 rows of 16 columns:
 // lane 8 q + r has row r, columns 4 q .. 4 q + 3.  With few parts a warp an item, else
 // all warps of a block.
-constexpr int kJoinWarps = 8, kJoinShare = 16;
+constexpr int kJoinWarps = 8, kJoinShare = 16, kFew = 6;
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join_wide(const __grid_constant__ AttendParams P) {
   __shared__ float4 s_o[kJoinWarps][32];
   __shared__ float s_l[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   pdl_wait();
   const AttendFrom at = P.from[c];
-  if (at.chunk == 0) return;
-  const long long unit = at.share.from(c) - at.chunk;
-  const int c0 = at.share.block_of(unit), c1 = at.share.block_of(unit + at.chunks - 1), parts = c1 - c0 + 1;
+  if (at.parts == 0) return;
+  const int c0 = at.first, parts = at.parts, c1 = c0 + parts - 1;
   const int rows = min(at.n * P.G - at.tile * P.rows, P.rows), groups = (P.D + 15) / 16, items = (rows + 7) / 8 * groups;
-  const bool together = parts > kJoinWarps;
+  const bool together = parts > kFew;
   const int worker = (c - c0 - 1) * kJoinShare + blockIdx.y, workers = (parts - 1) * kJoinShare;
   const int quads = P.width / 4;
   for (int i = together ? worker : worker * kJoinWarps + warp; i < items; i += together ? workers : workers * kJoinWarps) {
     const int r = i / groups * 8 + (lane & 7), q = i % groups * 4 + (lane >> 3);
     auto slot_of = [&](int p) { return (long long)(p == c0 ? 2 * c0 + 1 : 2 * p); };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int p = c0; p <= c1; ++p) m = fmaxf(m, P.stat[slot_of(p) * 128 + r].x);
-    const float base = attend_base(m);
-    float l = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (together) {
+#pragma unroll 4
+      for (int p = c0; p <= c1; ++p) m = fmaxf(m, P.stat[slot_of(p) * 128 + r].x);
+    }
+    // kFew parts at a time; no more: all of them, their maximum is found on the way
     const int step = together ? kJoinWarps : 1;
 #pragma unroll 1
-    for (int p0 = c0 + (together ? warp : 0); p0 <= c1; p0 += 4 * step) {
-      float2 st[4];
-      float4 a[4];
+    for (int p0 = c0 + (together ? warp : 0); p0 <= c1; p0 += kFew * step) {
+      float2 st[kFew];
+      float4 a[kFew];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const long long slot = slot_of(min(p0 + u * step, c1));
+      for (int u = 0; u < kFew; ++u) {
+        if (p0 + u * step > c1) break;
+        const long long slot = slot_of(p0 + u * step);
         st[u] = P.stat[slot * 128 + r];
         a[u] = reinterpret_cast<const float4*>(P.part)[(slot * quads + q) * 128 + r];
       }
+      if (!together) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kFew; ++u)
+          if (p0 + u <= c1) m = fmaxf(m, st[u].x);
+      }
+      const float base = attend_base(m);
+#pragma unroll
+      for (int u = 0; u < kFew; ++u) {
         if (p0 + u * step > c1) break;
         const float f = exp2_fast(st[u].x - base);
         l = fmaf(st[u].y, f, l);
