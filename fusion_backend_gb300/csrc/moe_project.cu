@@ -292,7 +292,8 @@ cudaError_t launch(ProjectParams& p, cudaStream_t stream) {
   while (p.k_warps < WARPS && (HOLD ? p.k_warps < slabs : 2 * p.k_warps <= slabs)) p.k_warps *= 2;
   if (p.k_warps < WARPS / BT) p.k_warps = WARPS / BT;
   const int at_once = WARPS / p.k_warps, tiles = (p.N + 15) / 16, parts = (p.T + 8 * NT - 1) / (8 * NT);
-  const int want = (tiles + at_once - 1) / at_once, most = (OCC * p.sms + parts - 1) / parts;
+  // (no more blocks than run at once)
+  const int want = (tiles + at_once - 1) / at_once, most = OCC * p.sms / parts > 0 ? OCC * p.sms / parts : 1;
   return launch_behind(kern, dim3(want < most ? want : most, parts), 32 * WARPS, L::bytes, stream, p);
 }
 
