@@ -12,7 +12,9 @@
 // angles of a token are formed once for all its heads, a thread an angle, into shared
 // memory, for the next token while this one is turned, and what the next tokens'
 // heads hold is on its way meanwhile, into a ring of the thread's own: one barrier a
-// token.  (A block a token, or two
+// token.  4096 tokens of 32 + 2 x 4 heads of 128 in bf16: 18.6 us, 4.5 TB/s read and
+// written; two tokens a barrier and three blocks an SM instead of two made no
+// difference.  (A block a token, or two
 // or four neighbouring ones with their items all at once, waited for one phase after
 // the other: 41, 37 and 28 us for 4096 tokens of 40 heads of 128.)
 #include <cuda_runtime.h>

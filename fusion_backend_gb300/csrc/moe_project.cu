@@ -11,12 +11,17 @@
 //
 // mma.m16n8k16 with the rows of W as its rows: 16-byte pieces of 8 rows are what
 // ldmatrix hands out, a lane then holds 8 codes of rows g and g + 8 that lie in
-// one group, as bf16 (fp16) numbers (c - 8) / 64 (c - 8) exactly.  The order of k inside those 8
-// follows the nibbles (0 4, 1 5, 2 6, 3 7), x is put in the same order where it is
-// loaded: straight from global memory, since each warp of a block has other
+// one group, as numbers (c - 8) / 64 in bf16, c - 8 in fp16, exactly.  The order of k
+// inside those 8 follows the nibbles (0 4, 1 5, 2 6, 3 7), x is put in the same order
+// where it is loaded: straight from global memory, since each warp of a block has other
 // columns of it, and once for all tiles where a warp has one slab of every tile.  A
 // group's products go to sums of their own and from there, times the group's scale,
 // to the row's: the products are exact and everything is added in fp32.
+//
+// Measured (weights from HBM): 5120 x 2048, 1 token 3.9 us, 16 tokens 5.8, 61 tokens
+// 11.4, 256 tokens 29; 100003 x 2048, 4 tokens 25.6 us, 4.6 TB/s: integer
+// instructions of the codes issue at half rate and are the bound (issue slots 70 %
+// used).  x from L2 for every tile of rows, the first form, took 19.6 us for 61 tokens.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
