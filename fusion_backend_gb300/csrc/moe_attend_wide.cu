@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         if (keys) {
           const uint32_t real = __ballot_sync(kAll, known < P.pages);
           if (lane == 0) s_boxes[x][i & 15] = real;
+          __syncwarp();
         }
         wait(empty + rings[x].slot, rings[x].turn);
         // (values that have to be looked through first: on a barrier of their own)

@@ -373,3 +373,43 @@ def test_long_units_of_many_rows(n, G):
     want = c.check()
     for _ in range(20):
         assert torch.equal(c.call(), want)
+
+
+@pytest.mark.parametrize("i", [4, 9, 14, 15, 17, 19])
+def test_a_row_that_is_not_finite_stays_alone(i):
+    """NaN and infinities in one query touch no other row or head, whatever shares its tile."""
+    c = Case(**SIZES[i], seed=i, mask="tree" if i > 12 else None)
+    clean = c.check().clone()
+    t, h = c.starts[-1] // 2, c.Hq // 2
+    for value in (NAN, INF):
+        c.q[t, h, 1] = value
+        got = c.call()
+        assert bool(got[t, h].isnan().all())
+        got[t, h] = clean[t, h]
+        assert torch.equal(got, clean)
+
+
+def test_a_prompt():
+    """Rows by the thousand, several tiles of a sequence, another one's next tokens beside them."""
+    Case([(1500, 1000), (700, 1), (64, 64)], D=128, Hq=8, Hkv=2, page=32, seed=2).check()
+    Case([(900, 900), (40, 2)], D=64, Hq=6, Hkv=2, page=16, dtype=F16, seed=3).check(out_dtype=F32)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own: narrow beside wide, the results of each alone."""
+    cases = [Case([(3000, 16), (700, 16)], D=128, Hq=16, Hkv=2, page=64, mask="tree", seed=1),
+             Case([(5000, 1)] * 6, D=128, Hq=16, Hkv=2, page=16, seed=2),
+             Case([(900, 40)] * 3, D=64, Hq=8, Hkv=2, page=8, mask="tree", seed=3)]
+    want = [c.call() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[torch.zeros_like(w) for _ in range(10)] for w in want]
+    ws = [torch.empty(fb.moe_ffn_attend_workspace(c.T, len(c.seqs), c.Hq, c.Hkv, c.D), dtype=torch.uint8, device="cuda")
+          for c in cases]
+    torch.cuda.synchronize()
+    for k in range(10):
+        for c, s, g, w in zip(cases, streams, got, ws):
+            c.call(out=g[k], workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in g)
