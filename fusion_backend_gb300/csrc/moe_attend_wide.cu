@@ -294,6 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         const int buf = count & 1;
         wait(full + ring.slot, ring.turn);
         wait(&p_full[x][buf], count >> 1 & 1);
+        // (the unit's first weights are there: its stream's threads have left the unit before,
+        // and met the others there, who had left the one before that: no phase but the last
+        // can be open)
         if (fresh && unit > 0) wait(&o_free, (unit - 1) & 1);
         tc::tc_fence_after();
         const uint64_t v_desc = desc_at(v_desc0, ring.slot * kSlot);
@@ -545,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             const float f = own ? exp2_fast(m - mx) : 1.f;
             if (own) m = mx;
             l *= f;
+            // (the buffer's phase before is closed: its present scores were formed behind it)
             wait(&s_free[x][count - 1 & 1], count - 1 >> 1 & 1);
             tc::tc_fence_after();
 #pragma unroll 1
