@@ -12,7 +12,7 @@
 //
 // Measured: a step of 64 KB an SM 1.36 us, 7.3 TB/s (D = 128, long sequences); the end
 // of a unit costs 3 us of a block, in part behind what is on its way; 48 sequences of
-// 500 to 12,000 tokens, 426 MB, 82 us; one of 2,000 tokens 8.6 us with the join.
+// 500 to 12,000 tokens, 426 MB, 73 us; one of 2,000 tokens 8.6 us with the join.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
       if (now.left > 1) {
         AttendStep next = now;
         next.next(P);
-        ask(next);
+        if (next.left > 0) ask(next);
       }
       // the warps' sums meet: each leaves its own in the slot that it has just used
 #pragma unroll
@@ -660,6 +660,8 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   p.rows = wide ? 128 / p.G * p.G : 16;
   p.chunk_log = wide || dp >= 128 ? 7 : 8;
   if (dp > 128) p.chunk_log = 6;
+  // (in steps of 1.4 us: 2.9 us a unit; the wide kernel 7)
+  p.extra = wide ? 4 : 2;
   p.width = dp;
   uint8_t* w = static_cast<uint8_t*>(p.ws);
   p.from = reinterpret_cast<AttendFrom*>(w);

@@ -28,7 +28,7 @@
 //
 // Measured: a step of 64 KB an SM 1.4 us, 7 TB/s (D = 128); a call of one step 13 us
 // (the way from the lengths to the page, the tile, the first scores, and cold
-// instructions everywhere); 16 trees of 16 tokens, 139 MB, 41 us.
+// instructions everywhere); 16 trees of 16 tokens, 139 MB, 40 us.
 //
 // Every wait is bounded.  After one that ran out, in whichever thread, nobody waits,
 // issues or arrives any more, but all still meet at the block's barriers, and results

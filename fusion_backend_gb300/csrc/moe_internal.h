@@ -383,11 +383,11 @@ struct AttendParams {
   const int32_t *table, *lens, *q_start, *mask;
   void* out;
   float* lse;
-  // set by the launch: blocks, rows and (log2) tokens of a unit's steps, columns of a
+  // set by the launch: blocks, rows and (log2) tokens of a unit's steps, what a unit costs besides, columns of a
   // part's row, i / page_size = i page_mul >> page_shift, accesses of 16 bytes to q,
   // of four elements to out, tokens of a tensor copy of q (0: none); tensor copies of
   // the cache: its order of dimensions, tokens a box
-  int blocks, rows, chunk_log, width, page_shift, q_vec, q_box, o_vec, slot_first, box;
+  int blocks, rows, chunk_log, extra, width, page_shift, q_vec, q_box, o_vec, slot_first, box;
   unsigned long long page_mul;
   // workspace: where the blocks' ranges begin, the parts' sums [2 blocks][rows]
   // [width] and their maximum and sum of weights [2 blocks][rows]
