@@ -44,13 +44,6 @@ MOE_DEV uint32_t piece(int r, int c) {
   return (c >> 3) * (TOK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// Non-finite: all exponent bits set.
-template <bool F16>
-MOE_DEV bool odd16(uint32_t h) {
-  const uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  return (h & e) == e;
-}
-
 // DP: elements of a head in shared memory (D rounded up); TERMS: numbers that
 // stand for a weight.
 // PAGED: pages hold multiples of 8 tokens: tensor copies of boxes of 8 or 16; else
@@ -71,6 +64,10 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ float2 s_stat[W][16];
   __shared__ uint32_t s_valid[W][S];
+  // of the unit under way: its first chunk here, whether a sum is not finite, whether values were taken out, and
+  // what the values of tokens that all rows see hold (attend_odd), 8 columns a word
+  __shared__ int s_chunk, s_sum_odd, s_own_odd;
+  __shared__ uint32_t s_odd[kChunks];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   uint8_t* const ring = smem + warp * S * kSlot;
   const uint32_t ring_at = smem_u32(ring);
@@ -177,7 +174,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   const float c2 = kept(P.softcap * kLog2e);
   int stage = 0, stage_in = S - 1;
   uint32_t parity = 0;
-  bool begin = true, from_start = false;
+  bool begin = true;
   bool dead = false;  // a copy never came: results are NaN
   uint32_t qf[kHoldQ ? KS : 1][4];
   float o[NT][4];
@@ -201,7 +198,11 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   while (now.left > 0) {
     if (begin) {
       begin = false;
-      from_start = now.chunk == 0;
+      if (tid == 0) {
+        s_chunk = now.chunk;
+        s_sum_odd = s_own_odd = 0;
+      }
+      if (tid < kChunks) s_odd[tid] = 0u;
       const int rows = now.s.n * P.G, r0 = now.tile * 16;
 #pragma unroll
       for (int u = 0; u < kQueries; ++u) {
@@ -265,7 +266,6 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
           for (int e = 0; e < 4; ++e) s[n][e] *= c1;
       }
       const int first = now.chunk * (W * kTok) + warp * kTok, own = first - (now.s.len - now.s.n);
-      bool odd_tile = false;
       if (valid != kFull || own + kTok > 0) {
 #pragma unroll
         for (int n = 0; n < KT; ++n)
@@ -275,17 +275,29 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
             const bool on = (valid >> i & 1u) && row_t[x] >= 0 && attend_sees(P, row_t[x], row_j[x], own + i);
             if (!on) s[n][e] = -INFINITY;
           }
-        // values that a row does not see have no effect on it: a product with a
-        // weight of 0 has, where they are not finite.  They are taken out of the tile
-        // and added to the rows that see them.
+        // values that a row does not see have no effect on it: a product with a weight of 0 has, where they are not
+        // finite
         bool odd = false;
+        const int from = attend_common(P, now.s) - first;  // of the tile's tokens, the first that some row may not see
         for (int i = lane; i < kTok * kChunks; i += 32) {
-          const uint4 v = *reinterpret_cast<const uint4*>(ring + stage * kSlot + kSlot / 2 + 16 * i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if ((i >> 3 & (kTok - 1)) < from) continue;
+          uint4* const at = reinterpret_cast<uint4*>(ring + stage * kSlot + kSlot / 2 + 16 * i);
+          const uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          bool any = false;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) odd |= odd16<F16>(w[x] & 0xFFFFu) || odd16<F16>(w[x] >> 16);
+          for (int x = 0; x < 4; ++x) {
+            if (odd16<F16>(w[x] & 0xFFFFu)) any = true, w[x] &= 0xFFFF0000u;
+            if (odd16<F16>(w[x] >> 16)) any = true, w[x] &= 0xFFFFu;
+          }
+          if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+          odd |= any;
         }
-        odd_tile = __any_sync(kAll, odd);
+        if (__any_sync(kAll, odd)) {
+          if (lane == 0) s_own_odd = 1;
+          fence_proxy_async();
+          __syncwarp();
+        }
       }
       // running maximum and sum
       float a0 = -INFINITY, a1 = -INFINITY;
@@ -314,31 +326,6 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
           o[n][2] *= f1;
           o[n][3] *= f1;
         }
-      }
-      if (odd_tile) {
-        for (int i = 0; i < kTok; ++i) {
-          bool sees[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            sees[x] = (valid >> i & 1u) && row_t[x] >= 0 && attend_sees(P, row_t[x], row_j[x], own + i);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + stage * kSlot + kSlot / 2 + piece<kTok>(i, n) +
-                                                                  4 * q);
-            float v[2];
-            unpack2(kDt, w, v[0], v[1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (odd16<F16>(e & 1 ? w >> 16 : w & 0xFFFFu) && sees[e >> 1]) o[n][e] += v[e & 1];
-          }
-        }
-        __syncwarp();
-        for (int i = lane; i < kTok * DP; i += 32) {
-          uint16_t* const at = reinterpret_cast<uint16_t*>(ring + stage * kSlot + kSlot / 2) + i;
-          if (odd16<F16>(*at)) *at = 0;
-        }
-        fence_proxy_async();
-        __syncwarp();
       }
       const float b0 = attend_base(m0) - kUp, b1 = attend_base(m1) - kUp;
 #pragma unroll
@@ -407,8 +394,23 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
         s_stat[warp][g] = make_float2(m0 - kUp, dead ? none : l0);
         s_stat[warp][g + 8] = make_float2(m1 - kUp, dead ? none : l1);
       }
+      float finite = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) finite = fmaf(o[n][e], 0.f, finite);
+      if (finite != 0.f) s_sum_odd = 1;  // (NaN then)
       __syncthreads();
-      const bool whole = from_start && end;
+      const int chunk0 = s_chunk, first = chunk0 * (W * kTok), last = min((now.chunk + 1) * (W * kTok), now.s.len);
+      const bool from_start = chunk0 == 0, whole = from_start && end, sum_odd = s_sum_odd, own_odd = s_own_odd;
+      if (sum_odd) {
+        const int c = tid % kChunks, step = 32 * W / kChunks, y = tid / kChunks;
+        if (y < step && c < pieces) {
+          const uint32_t bits = attend_odd<F16>(P, now.b, now.head, first + y, step, min(last, attend_common(P, now.s)), 8 * c);
+          if (bits) atomicOr(s_odd + c, bits);
+        }
+        __syncthreads();
+      }
       const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
       const int rows = now.s.n * P.G, r0 = now.tile * 16;
       for (int i = tid; i < 16 * (DP / 4); i += 32 * W) {
@@ -431,13 +433,28 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
           v.z = fmaf(a.z, f, v.z);
           v.w = fmaf(a.w, f, v.w);
         }
+        const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
+        const long long t = now.s.t0 + j;
+        if (sum_odd) {
+          const uint32_t bits = s_odd[d >> 3] >> (2 * (d & 7));
+          attend_put_odd(v.x, bits);
+          attend_put_odd(v.y, bits >> 2);
+          attend_put_odd(v.z, bits >> 4);
+          attend_put_odd(v.w, bits >> 6);
+        }
+        if (own_odd) {
+          const float4 x = attend_own<F16>(P, now.b, now.head, now.s.len - now.s.n, (int)t, j,
+                                           max(first, attend_common(P, now.s)), last, d);
+          attend_add_odd(v.x, x.x);
+          attend_add_odd(v.y, x.y);
+          attend_add_odd(v.z, x.z);
+          attend_add_odd(v.w, x.w);
+        }
         if (!whole) {
           *reinterpret_cast<float4*>(P.part + ((long long)slot * 16 + r) * P.width + d) = v;
           if (d == 0) P.stat[slot * 16 + r] = make_float2(m, l);
           continue;
         }
-        const int j = (r0 + r) / P.G, h = now.head * P.G + (r0 + r) - j * P.G;
-        const long long t = now.s.t0 + j;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
         if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
@@ -551,6 +568,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
       __syncthreads();
       if (warp > 0) continue;
     }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (4 * lane + 128 * v < P.D && !attend_finite(acc[v])) {
+        float4 odd = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i = c0; i <= c1; ++i)
+          attend_part_odd(odd, *reinterpret_cast<const float4*>(P.part + slot_of(i) * P.width + 4 * lane + 128 * v));
+        attend_take_odd(acc[v], odd);
+      }
     const int in = at.tile * P.rows + r, j = in / P.G, h = at.head * P.G + in - j * P.G;
     const long long t = at.t0 + j, out = t * P.o_stride + h * P.o_head;
     const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -215,6 +215,89 @@ MOE_DEV float attend_tanh(float x) {
   return fabsf(x) < 0.5f ? fmaf(p * y, x, x) : far;
 }
 
+// First token that some row of the sequence may not see.
+MOE_DEV int attend_common(const AttendParams& P, const AttendSeq& s) {
+  return s.n > 1 || P.mask ? max(s.len - s.n, 0) : s.len;
+}
+
+// Values that are not finite.  A weight enters the second product as a sum of numbers
+// of either sign, so that an infinity gives NaN there, and what a row does not see must
+// not enter it at all.  So they are taken out of the tiles that hold tokens which some
+// rows do not see, and found again for the rows that do (attend_own).  Those of the
+// other tokens, which all rows see, leave sums that are not finite: these columns are
+// looked through once more in the cache (attend_odd), and what is there takes the sum's
+// place.  Neither slows the stream of a cache without such values.
+template <bool F16>
+MOE_DEV bool odd16(uint32_t h) {  // all exponent bits set
+  const uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  return (h & e) == e;
+}
+
+// What columns c .. c + 7 of the values of tokens first, first + step, ... before end
+// hold of them, two bits a column: infinity, minus infinity, both for NaN.
+template <bool F16>
+__device__ __noinline__ uint32_t attend_odd(const AttendParams& P, int b, int head, int first, int step, int end, int c) {
+  uint32_t bits = 0u;
+#pragma unroll 4
+  for (int i = first; i < end; i += step) {
+    const int at = attend_page(P, i), page = P.table[b * P.table_stride + at];
+    if ((uint32_t)page >= (uint32_t)P.pages) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(P.v + page * P.vc_page + (long long)(i - at * P.page_size) * P.vc_slot +
+                                                    head * P.vc_head + c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = w[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+      if (odd16<F16>(h)) bits |= (h & (F16 ? 0x3FFu : 0x7Fu) ? 3u : h >> 15 ? 2u : 1u) << (2 * e);
+    }
+  }
+  return bits;
+}
+// One column's two bits in the place of its sum, where they are not 0.
+MOE_DEV void attend_put_odd(float& sum, uint32_t bits) {
+  if (bits & 3u) sum = __int_as_float((bits & 3u) == 3u ? 0x7FFFFFFF : bits & 1u ? 0x7F800000 : (int)0xFF800000);
+}
+
+// The sum of those in columns d .. d + 3 of tokens first .. end - 1 that row t, the j-th,
+// sees.  The sequence's own tokens begin at `own`.
+template <bool F16>
+__device__ __noinline__ float4 attend_own(const AttendParams& P, int b, int head, int own, int t, int j, int first, int end,
+                                          int d) {
+  float x[4] = {};
+  for (int i = first; i < end; ++i) {
+    if (!attend_sees(P, t, j, i - own)) continue;
+    const int at = attend_page(P, i), page = P.table[b * P.table_stride + at];
+    if ((uint32_t)page >= (uint32_t)P.pages) continue;
+    const uint16_t* const v = P.v + page * P.vc_page + (long long)(i - at * P.page_size) * P.vc_slot + head * P.vc_head + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (odd16<F16>(v[e])) x[e] += raw_value(v[e], F16 ? kF16 : kBf16);
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+// v += x, but for the sign of a zero.
+MOE_DEV void attend_add_odd(float& v, float x) {
+  if (x != 0.f) v += x;
+}
+
+MOE_DEV bool attend_finite(float v) { return fabsf(v) < INFINITY; }
+// In the join: a part's infinities count without its factor, which may be 0.
+MOE_DEV void attend_part_odd(float4& odd, const float4& part) {
+  if (!attend_finite(part.x)) odd.x += part.x;
+  if (!attend_finite(part.y)) odd.y += part.y;
+  if (!attend_finite(part.z)) odd.z += part.z;
+  if (!attend_finite(part.w)) odd.w += part.w;
+}
+MOE_DEV void attend_take_odd(float4& sum, const float4& odd) {
+  if (odd.x != 0.f) sum.x = odd.x;
+  if (odd.y != 0.f) sum.y = odd.y;
+  if (odd.z != 0.f) sum.z = odd.z;
+  if (odd.w != 0.f) sum.w = odd.w;
+}
+MOE_DEV bool attend_finite(const float4& v) {
+  return attend_finite(v.x) && attend_finite(v.y) && attend_finite(v.z) && attend_finite(v.w);
+}
+
 // The largest running maximum is taken for 0 where there is none, so that
 // exp2(-inf - 0) = 0.
 MOE_DEV float attend_base(float m) { return m == -INFINITY ? 0.f : m; }

@@ -111,12 +111,6 @@ __device__ __forceinline__ void tmem_write32(uint32_t taddr, const uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <bool F16>
-MOE_DEV bool odd16(uint32_t h) {  // not finite
-  const uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  return (h & e) == e;
-}
-
 // A shared-memory descriptor with its address moved by `bytes`.
 MOE_DEV uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
@@ -155,11 +149,6 @@ struct Ring {
     }
   }
 };
-
-// First token that some row of the unit's sequence may not see.
-MOE_DEV int seen_by_all(const AttendParams& P, const AttendSeq& s) {
-  return s.n > 1 || P.mask ? max(s.len - s.n, 0) : s.len;
-}
 
 // Bits of the 64 tokens from `first` on that row t, the j-th of its sequence, sees.
 MOE_DEV uint64_t seen_tokens(const AttendParams& P, const AttendSeq& s, int first, int t, int j) {
@@ -236,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
   auto there = [&](const AttendStep& s, int x) { return x == 0 || first_of(s, 1) < s.s.len; };
   auto last_of_unit = [](const AttendStep& s) { return s.left == 1 || s.chunk + 1 == s.s.chunks; };
   // a tile that holds tokens which some rows do not see
-  auto mixed = [&](const AttendStep& s, int x) { return first_of(s, x) + kTok > seen_by_all(P, s.s); };
+  auto mixed = [&](const AttendStep& s, int x) { return first_of(s, x) + kTok > attend_common(P, s.s); };
 
   // (by whole warps, which stay of one mind)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -448,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             mixed_at = 0;
             mixed_turn ^= 1u;
           }
-          const int from = max(seen_by_all(P, a.s) - first_of(a, x), 0);
+          const int from = max(attend_common(P, a.s) - first_of(a, x), 0);
           uint8_t* const tile = smem + rings[x].slot * kSlot;
           bool odd = false;
           for (int y = th; y < kTok * DP / 8; y += 64) {
@@ -608,25 +597,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
         uint32_t o0[16], o1[16];
         tmem_read16(tmem + lanes + kOut + c, o0);
         if (other) tmem_read16(tmem + lanes + kOut + DP + c, o1);
-        if (t < 0 || c >= P.D) continue;
-        float v[16];
+        float v[16], finite = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           v[e] = __uint_as_float(o0[e]) * f0;
           if (other) v[e] = fmaf(__uint_as_float(o1[e]), f1, v[e]);
+          finite = fmaf(v[e], 0.f, finite);
         }
+        const int end_at = min(a.s.len, (a.chunk + 1) * 2 * kTok);
+        if (__any_sync(kAll, t >= 0 && finite != 0.f)) {  // (NaN then)
+          // the warp looks through its columns, two lanes a token
+          const int first = chunk0 * 2 * kTok + (lane >> 1), at = c + 8 * (lane & 1);
+          uint32_t bits = 0u;
+          if (at < P.D) bits = attend_odd<F16>(P, a.b, a.head, first, 16, min(end_at, attend_common(P, a.s)), at);
+          __syncwarp();
+          bits = __reduce_or_sync(kAll, bits << (16 * (lane & 1)));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) attend_put_odd(v[e], bits >> (2 * e));
+        }
+        if (t < 0 || c >= P.D) continue;
         if (odd) {
           // what was taken out of the tiles, for the rows that see it
-          const int end_at = min(a.s.len, (a.chunk + 1) * 2 * kTok);
-          for (int y = max(seen_by_all(P, a.s), chunk0 * 2 * kTok); y < end_at; ++y) {
-            if (!attend_sees(P, t, j, y - (a.s.len - a.s.n))) continue;
-            const int at = attend_page(P, y), page = P.table[a.b * P.table_stride + at];
-            if ((uint32_t)page >= (uint32_t)P.pages) continue;
-            const uint16_t* const from =
-                P.v + page * P.vc_page + (long long)(y - at * P.page_size) * P.vc_slot + a.head * P.vc_head + c;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c + e < P.D && odd16<F16>(from[e])) v[e] += raw_value(from[e], kDt);
+          for (int e = 0; e < 16; e += 4) {
+            if (c + e >= P.D) break;
+            const float4 x = attend_own<F16>(P, a.b, a.head, a.s.len - a.s.n, t, j,
+                                             max(attend_common(P, a.s), chunk0 * 2 * kTok), end_at, c + e);
+            attend_add_odd(v[e], x.x);
+            attend_add_odd(v[e + 1], x.y);
+            attend_add_odd(v[e + 2], x.z);
+            attend_add_odd(v[e + 3], x.w);
           }
         }
         if (whole) {
@@ -741,6 +741,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join_wide(const __gr
       if (warp > 0) continue;
     }
     if (r >= rows) continue;
+    if (!attend_finite(o)) {
+      float4 odd = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int p = c0; p <= c1; ++p)
+        attend_part_odd(odd, reinterpret_cast<const float4*>(P.part)[(slot_of(p) * quads + q) * 128 + r]);
+      attend_take_odd(o, odd);
+    }
     const int in = at.tile * P.rows + r, j = in / P.G, h = at.head * P.G + in - j * P.G, d = 4 * q;
     const long long t = at.t0 + j, out = t * P.o_stride + h * P.o_head + d;
     const float inv = l == 0.f ? 0.f : 1.f / l;

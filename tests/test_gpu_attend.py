@@ -413,3 +413,65 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert all(torch.equal(x, w) for x in g)
+
+
+ODD = [
+    dict(seqs=[(3000, 1), (700, 1)], D=128, Hq=16, Hkv=2), dict(seqs=[(300, 1)] * 400, D=64, Hq=8, Hkv=1),
+    dict(seqs=[(700, 3), (130, 2)], D=80, Hq=12, Hkv=2, page=5), dict(seqs=[(400, 2), (90, 1)], D=256, Hq=8, Hkv=1, page=32),
+    dict(seqs=[(260, 3)], D=192, Hq=16, Hkv=1, page=8), dict(seqs=[(3000, 16), (700, 9)], D=128, Hq=32, Hkv=4, page=64),
+    dict(seqs=[(200, 16)] * 400, D=64, Hq=8, Hkv=1), dict(seqs=[(900, 40), (500, 40)], D=72, Hq=12, Hkv=2, page=24),
+    dict(seqs=[(1500, 1000)], D=128, Hq=8, Hkv=2, page=32), dict(seqs=[(40000, 1)], D=64, Hq=2, Hkv=2)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("i", range(len(ODD)))
+def test_infinities_in_tokens_that_all_rows_see(i, dtype):
+    """A value that is not finite makes its column so for its sequence and heads, wherever in the cache its token lies:
+    weights are above 0, so an infinity stays one, NaN and infinities of both signs give NaN."""
+    c = Case(**ODD[i], seed=i, dtype=dtype, mask="tree" if max(n for _, n in ODD[i]["seqs"]) > 1 else None, poison=True)
+    clean = c.check().clone()
+    G, b = c.Hq // c.Hkv, len(c.seqs) - 1
+    rows, common = slice(c.starts[b], c.starts[b + 1]), c.seqs[b][0] - c.seqs[b][1]
+    place = lambda at: (int(c.table[b, at // c.page]), at % c.page)  # noqa: E731
+    for tokens, values, want in (([0], [INF], INF), ([common - 1], [-INF], -INF), ([common // 2], [NAN], NAN),
+                                 ([1, common // 2], [INF, INF], INF), ([common // 3, common - 2], [-INF, INF], NAN)):
+        kept = c.v.clone()
+        for at, value in zip(tokens, values):
+            c.v[place(at)][0, 3] = value
+        got = c.call()
+        hit = got[rows, :G, 3].clone()
+        assert bool(hit.isnan().all()) if math.isnan(want) else bool((hit == want).all())
+        got[rows, :G, 3] = clean[rows, :G, 3]
+        assert torch.equal(got, clean)
+        c.v.copy_(kept)
+
+
+@pytest.mark.parametrize("i", range(len(ODD)))
+def test_infinities_of_small_weights(i):
+    """Tokens whose weights are far below what fp32 holds beside the largest one's: the formula's weights are above 0."""
+    c = Case(**ODD[i], seed=i, dtype=F16 if i % 2 else BF16, spread=40.0)
+    clean = c.call(out=torch.zeros_like(c.q))
+    length, n = c.seqs[0]
+    k = c.k[c.table[0].long()[torch.arange(length - n, device="cuda") // c.page], torch.arange(length - n, device="cuda") % c.page]
+    score = k[:, 0].double() @ c.q[0, 0].double()
+    least, most = int(score.argmin()), int(score.argmax())
+    for at, value in ((least, INF), (most, -INF)):
+        c.v[int(c.table[0, at // c.page]), at % c.page, 0, 5] = value
+        got = c.call(out=torch.zeros_like(clean))
+        G = c.Hq // c.Hkv
+        want = INF if at == least else NAN
+        hit = got[:n, :G, 5].clone()
+        assert bool(hit.isnan().all()) if math.isnan(want) else bool((hit == want).all())
+        got[:n, :G, 5] = clean[:n, :G, 5]
+        assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 1), (64, 9), (128, 9), (256, 2)])
+def test_an_infinity_gives_the_same_as_the_sequence_grows(D, n):
+    """The same cached token while its tile is the last one, and once it is full."""
+    c = Case([(800, n)], D=D, Hq=8, Hkv=1, seed=D + n)
+    c.v[int(c.table[0, 2]), 5, 0, 1] = INF
+    for length in (2 * 16 + 5 + n, 60, 64, 65, 128, 129, 300, 800):
+        c.lens.fill_(max(length, 2 * 16 + 6 + n))
+        got = c.call()
+        assert bool((got[..., 1] == INF).all()) and bool(got[..., 0].isfinite().all())
