@@ -346,6 +346,7 @@ constexpr int kAttendMaxGroup = 128;  // query heads a key head
 struct ProjectParams {
   int T, K, N, group, sms;
   int k_warps;  // set by the launch: warps of a block over K
+  int lost;     // bytes that a copy is waited for beyond its own: 0, or the wait runs out (for the test of that)
   int f16, y_dtype;
   long long x_stride, y_stride, w_stride;
   const uint16_t* x;

@@ -111,11 +111,12 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
   // the warp's steps: its slabs of its tiles, in order
   int tile_in = lo + tpart, slab_in = 0;
   const uint64_t policy = policy_evict_first();
+  bool dead = false;  // the warp's: a copy never came; nothing is asked for any more, results are NaN
   auto load = [&](int stage) {
     if (tile_in < hi && mine > 0) {
-      if (lane == 0) {
+      if (lane == 0 && !dead) {
         const int k0 = (kpart + slab_in * kw) * kSlab;
-        mbar_arrive_expect_tx(full + stage, L::kCodes + L::kScales);
+        mbar_arrive_expect_tx(full + stage, L::kCodes + L::kScales + P.lost);
         tensor_load_2d(codes + stage * L::kCodes, &P.tm_codes, k0 >> 1, tile_in * 16, full + stage, policy);
         // 16 bytes that hold the slab's scales: of one slab, two or four
         tensor_load_2d(scales + stage * L::kScales, &P.tm_scales, (P.K >> 1) + (k0 >> (4 + GL) & ~15), tile_in * 16,
@@ -158,7 +159,6 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
   }
   int stage = 0, stage_in = STAGES - 1;
   uint32_t parity = 0;
-  bool dead = false;  // a copy never came: results are NaN
   for (int base = lo; base < hi; base += BT) {
     const int in_batch = min(BT, hi - base);
     for (int u = tpart; u < in_batch; u += at_once) {
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
         __syncwarp();
         load(stage_in);
         stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
-        if (!dead) dead = !mbar_wait(full + stage, parity);
+        if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(full + stage, parity));
         const uint32_t codes_at = smem_u32(codes + stage * L::kCodes);
         // the slab's scales of rows g and g + 8: 8, 4 or 2 each
         uint32_t sc0[4], sc1[4];
@@ -249,7 +249,10 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
           parity ^= 1u;
         }
       }
-      if (dead) acc[0][0] = __int_as_float(0x7FFFFFFF);
+      if (dead) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = __int_as_float(0x7FFFFFFF);
+      }
       float* const own = sums + (kpart * L::kRows + u * 16) * L::kPitch;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -269,6 +272,8 @@ __global__ void __launch_bounds__(32 * WARPS, OCC) k_project(const __grid_consta
     }
     __syncthreads();
   }
+  if (dead)  // the block's shared memory is its own until copies that are under way have come
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 template <bool F16, int WARPS, int NT, int STAGES, int BT, int GL, bool HOLD, int OCC>
