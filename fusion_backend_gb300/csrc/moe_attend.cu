@@ -102,8 +102,9 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
     const int i = ahead.chunk * (W * kTok) + warp * kTok + (PAGED ? lane * P.box : lane & (kTok - 1));
     if (i < ahead.s.len && (!PAGED || lane * P.box < kTok)) page_ahead = P.table[ahead.b * P.table_stride + attend_page(P, i)];
   };
+  bool dead = false;            // the warp's: a copy never came; nothing is asked for any more, results are NaN
   auto load = [&](int stage) {  // the tokens of `ahead`, then the next step's page
-    if (ahead.left > 0) {
+    if (ahead.left > 0 && !dead) {
       const int first = ahead.chunk * (W * kTok) + warp * kTok;
       const uint32_t k_dst = ring_at + stage * kSlot, v_dst = k_dst + kSlot / 2;
       const bool ok = (uint32_t)page_ahead < (uint32_t)P.pages;
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
           if (b * P.box < kTok && !(there >> b & 1u)) valid &= ~((~0u >> (32 - P.box)) << (b * P.box));
         if (lane == 0) {
           if (valid)
-            mbar_arrive_expect_tx(full + stage, kSlot);
+            mbar_arrive_expect_tx(full + stage, kSlot + P.lost);
           else
             mbar_arrive(full + stage);
           s_valid[warp][stage] = valid;
@@ -175,7 +176,6 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
   int stage = 0, stage_in = S - 1;
   uint32_t parity = 0;
   bool begin = true;
-  bool dead = false;  // a copy never came: results are NaN
   uint32_t qf[kHoldQ ? KS : 1][4];
   float o[NT][4];
   float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // rows g and g + 8 (log2 units)
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
     __syncwarp();
     load(stage_in);
     stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
-    if (PAGED && !dead) dead = !mbar_wait(full + stage, parity);
+    if (PAGED && !dead) dead = __any_sync(kAll, !mbar_wait(full + stage, parity));
     const uint32_t valid = s_valid[warp][stage];
     if (valid) {
       const uint32_t k_at = ring_at + stage * kSlot, v_at = k_at + kSlot / 2;
@@ -481,6 +481,8 @@ __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_c
     now.next(P);
   }
   if (!PAGED) copy_wait<0>();
+  if (dead)  // the block's shared memory is its own until copies that are under way have come
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // Joins the parts of a unit.  Its rows are shared by the blocks (c, y) of the ranges

@@ -374,6 +374,7 @@ cudaError_t launch_append(AppendParams p, cudaStream_t stream);
 struct AttendFrom;
 struct AttendParams {
   int T, B, Hq, Hkv, G, D, sms;  // G query heads a key head
+  int lost;                      // as in ProjectParams (warp-level kernel)
   int f16, out_dtype;
   int page_size, pages, max_pages, mask_words;
   float scale, softcap;

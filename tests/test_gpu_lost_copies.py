@@ -46,3 +46,35 @@ def test_project(launches, T, K, N):
         assert launches.lost_project(T, K, N, 32, sms, lost, ptr(x), ptr(w), ptr(y)) == 0
         torch.cuda.synchronize()
         assert bool(y.isnan().all()) if lost else torch.equal(y, want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend(launches, D):
+    """Units of one block and of several, with a sequence that the bounded wait cannot touch: it has no tokens."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    lens = [9000, 50, 1, 0, 700]
+    pages = sum(-(-n // 16) for n in lens)
+    table, at = torch.zeros(5, -(-9000 // 16), dtype=torch.int32), 0
+    for b, n in enumerate(lens):
+        m = -(-n // 16)
+        table[b, :m] = torch.arange(at, at + m)
+        at += m
+    table = table.cuda()
+    k, v = (torch.randn(pages, 16, 2, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(5, 8, D, generator=g, device="cuda").bfloat16()
+    lens, starts = torch.tensor(lens, dtype=torch.int32).cuda(), torch.arange(6, dtype=torch.int32).cuda()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty(fb.moe_ffn_attend_workspace(5, 5, 8, 2, D), dtype=torch.uint8, device="cuda")
+    want, want_lse = torch.zeros_like(q), torch.zeros(5, 8, device="cuda")
+    fb.moe_ffn_attend(q, k, v, table, lens, starts, scale=0.125, out=want, lse=want_lse)
+    has = lens > 0
+    for lost in (0, 16, 0):
+        out, lse = torch.full_like(q, 5.0), torch.full((5, 8), 5.0, device="cuda")
+        torch.cuda.synchronize()
+        assert launches.lost_attend(5, 8, 2, D, 16, pages, table.shape[1], sms, lost, ptr(q), ptr(k), ptr(v), ptr(table),
+                                    ptr(lens), ptr(starts), ptr(out), ptr(lse), ptr(ws)) == 0
+        torch.cuda.synchronize()
+        if lost:
+            assert bool(out[has].isnan().all()) and bool(lse[has].isnan().all()) and bool((out[~has] == 0).all())
+        else:
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
