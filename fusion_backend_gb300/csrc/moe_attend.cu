@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   pdl_wait();
   const AttendFrom at = P.from[c];
+  if (at.none) attend_none<kJoinWarps>(P);
   if (at.parts == 0) return;
   // the first part begins its unit, the others go on
   const int c0 = at.first, parts = at.parts, c1 = c0 + parts - 1;

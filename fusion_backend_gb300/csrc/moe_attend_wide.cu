@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join_wide(const __gr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   pdl_wait();
   const AttendFrom at = P.from[c];
+  if (at.none) attend_none<kJoinWarps>(P);
   if (at.parts == 0) return;
   const int c0 = at.first, parts = at.parts, c1 = c0 + parts - 1;
   const int rows = min(at.n * P.G - at.tile * P.rows, P.rows), groups = (P.D + 15) / 16, items = (rows + 7) / 8 * groups;

@@ -475,3 +475,32 @@ def test_an_infinity_gives_the_same_as_the_sequence_grows(D, n):
         c.lens.fill_(max(length, 2 * 16 + 6 + n))
         got = c.call()
         assert bool((got[..., 1] == INF).all()) and bool(got[..., 0].isfinite().all())
+
+
+@pytest.mark.parametrize("page,n", [(16, 1), (16, 40), (5, 1)])
+def test_rows_of_sequences_without_tokens(page, n):
+    """Thousands of them, beside sequences that have some: zeros, in strided rows too, and nothing beside them."""
+    c = Case([(0, 4000), (300, n), (0, 1), (0, 77), (90, n)] + [(0, 1)] * 700 + [(40, n)], Hq=6, Hkv=2, D=72, page=page, rest=3)
+    c.check()
+    c.check(strided=True)
+    c.check(out_dtype=F32)
+    c.lens.zero_()
+    out, lse = torch.ones_like(c.q), torch.ones(c.T, 6, device="cuda")
+    c.call(out=out, lse=lse)
+    end = c.starts[-1]
+    assert bool((out[:end] == 0).all()) and bool((lse[:end] == -INF).all()) and bool((out[end:] == 1).all()) and bool((lse[end:] == 1).all())
+
+
+def test_rows_of_sequences_without_tokens_hold_up_nobody():
+    """512 rows of 32 heads of 128 are 4 MB of zeros: microseconds, and not a thread's work, element by element (30 ms)."""
+    c = Case([(0, 512), (2000, 1)], D=128, Hq=32, Hkv=4)
+    out, times = torch.ones_like(c.q), []
+    for _ in range(5):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        c.call(out=out)
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    assert min(times) < 3.0, times
+    assert bool((out[:512] == 0).all())
