@@ -717,7 +717,7 @@ def moe_ffn_append_kv(k, v, positions, slots, inv_freq, k_cache, v_cache, q=None
 
 
 def moe_ffn_attend_workspace(T: int, B: int, q_heads: int, kv_heads: int, D: int) -> int:
-    """Workspace bytes of moe_ffn_attend for T rows of B sequences and heads of D elements."""
+    """Workspace bytes of moe_ffn_attend for up to T rows of up to B sequences and heads of D elements."""
     n = ctypes.c_size_t()
     a = _block(AttendArgs, T, B, q_heads, kv_heads, D, ACT_BF16, ACT_F32, 1, 0, 0, 0, 1.0, 0.0, *(10 * [256]), 0, 0)
     _check(lib().moe_ffn_attend_workspace(a, ctypes.byref(n)), "moe_ffn_attend_workspace")

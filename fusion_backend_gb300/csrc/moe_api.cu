@@ -847,14 +847,14 @@ int moe_ffn_attend(const moe_ffn_attend_args* a, moe_ffn_stream_t stream, void* 
     return MOE_FFN_ERR_INVALID_ARG;
   AttendParams P = {};
   attend_sizes(a, P);
-  if (workspace_bytes < attend_workspace(P)) return MOE_FFN_ERR_WORKSPACE;
+  P.page_size = a->page_size;
+  if (workspace_bytes < attend_needs(P)) return MOE_FFN_ERR_WORKSPACE;
   if (!aligned(workspace, 256) || !aligned(q, 2) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(q_start, 4) || !aligned(mask, 4) ||
       !elem_aligned(out, a->out_dtype) || !aligned(lse, 4))
     return MOE_FFN_ERR_MISALIGNED;
   rc = check_device(&P.sms);
   if (rc != MOE_FFN_OK) return rc;
-  P.page_size = a->page_size;
   P.pages = a->pages;
   P.max_pages = cached ? a->max_pages : 0;
   P.mask_words = a->mask_words;

@@ -655,17 +655,23 @@ cudaError_t launch_terms(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Rows of a unit: up to 128 (k_attend_wide) where a sequence has more than 16 on
-// average, whatever the rest of the call; its heads have to fit into tensor memory.
-static int attend_rows(const AttendParams& p) {
-  return p.D <= 128 && (long long)p.T * p.G > 16ll * p.B ? 128 : 16;
+// Units of up to 128 rows (k_attend_wide) where a sequence has more than 16 on average;
+// its heads have to fit into tensor memory, boxes of 8 tokens into its pages (and three
+// numbers a weight do not fit beside the scores).
+static bool attend_wide(const AttendParams& p) {
+  return p.D <= 128 && (long long)p.T * p.G > 16ll * p.B && p.page_size % 8 == 0 && (p.f16 || p.out_dtype != kF32);
 }
 
-size_t attend_workspace(const AttendParams& p) {
-  const size_t rows = attend_rows(p);
+static size_t attend_bytes(bool wide, int D) {
+  const size_t rows = wide ? 128 : 16;
   return align256(kMaxBlocks * sizeof(AttendFrom)) + align256((size_t)2 * kMaxBlocks * rows * 8) +
-         (size_t)2 * kMaxBlocks * rows * width_for(p.D) * 4;
+         (size_t)2 * kMaxBlocks * rows * width_for(D) * 4;
 }
+
+size_t attend_needs(const AttendParams& p) { return attend_bytes(attend_wide(p), p.D); }
+
+// As many rows may be one sequence's.
+size_t attend_workspace(const AttendParams& p) { return attend_bytes(p.D <= 128 && (long long)p.T * p.G > 16, p.D); }
 
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   p.blocks = p.sms;
@@ -678,8 +684,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
   p.o_vec = reinterpret_cast<uintptr_t>(p.out) % (4 * elem_bytes(p.out_dtype)) == 0 && p.o_stride % 4 == 0 && p.o_head % 4 == 0;
   p.slot_first = p.kc_slot < p.kc_head;
   const int dp = width_for(p.D);
-  // (three numbers a weight do not fit beside the scores)
-  bool wide = attend_rows(p) == 128 && p.page_size % 8 == 0 && (p.f16 || p.out_dtype != kF32);
+  bool wide = attend_wide(p);
   for (p.box = wide ? 64 : tokens_for(dp); p.box > 8 && p.page_size % p.box;) p.box /= 2;
   const bool paged = p.page_size % 8 == 0 && p.pages > 0 && encode_cache(&p.tm_k, p, p.k, p.kc_page, p.kc_slot, p.kc_head) &&
                      encode_cache(&p.tm_v, p, p.v, p.vc_page, p.vc_slot, p.vc_head);

@@ -400,6 +400,8 @@ struct AttendParams {
   CUtensorMap tm_k, tm_v;  // of caches whose pages hold multiples of 8 tokens
   CUtensorMap tm_q;
 };
+// What the call needs, and what every call with as many rows and sequences, or fewer, does.
+size_t attend_needs(const AttendParams& p);
 size_t attend_workspace(const AttendParams& p);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
 

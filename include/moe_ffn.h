@@ -488,7 +488,8 @@ int moe_ffn_append_kv(const moe_ffn_append_args* args, moe_ffn_stream_t stream, 
  * T <= 1048576, B <= 65536, q_heads a multiple of kv_heads and at most 128 kv_heads, kv_heads <= 4096,
  * D a multiple of 8 up to 256, pages page_size < 2^31, max_pages page_size <= 2^30.
  * The workspace (256-byte aligned, scratch) holds what
- * moe_ffn_attend_workspace reports; calls that overlap on the GPU need one each.
+ * moe_ffn_attend_workspace reports for these heads and for T and B or any larger
+ * ones; calls that overlap on the GPU need one each.
  */
 typedef struct {
   int32_t T, B, q_heads, kv_heads, D;

@@ -270,3 +270,29 @@ def test_a_number_held_in_a_tensor_is_read_on_every_call(rec):
     cap.fill_(30.0)
     fb.moe_ffn_attend(**a, softcap=cap, stream=1)
     assert [c[1].softcap for c in rec.calls] == [10.0, 30.0]
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,D", [(32, 4, 128), (8, 8, 64), (12, 2, 80), (128, 1, 128), (16, 1, 256)])
+def test_a_workspace_serves_smaller_calls(lib, q_heads, kv_heads, D):
+    """One that is reported for the largest T and B is large enough for fewer of either, whatever the page size and the
+    types: such a call gets as far as the check of its (here misaligned) queries."""
+    sizes = (1, 2, 3, 8, 16, 17, 64, 300, 4096)
+
+    def args(T, B, **kw):
+        return attend_args(**(dict(T=T, B=B, q_heads=q_heads, kv_heads=kv_heads, D=D) | {n: 4096 for n in (
+            "q_stride", "q_head_stride", "out_stride", "out_head_stride", "kc_page_stride", "kc_slot_stride", "kc_head_stride",
+            "vc_page_stride", "vc_slot_stride", "vc_head_stride")} | kw))
+
+    def reported(T, B):
+        n = ctypes.c_size_t()
+        assert lib.moe_ffn_attend_workspace(args(T, B), ctypes.byref(n)) == fb.OK
+        return n.value
+
+    for T in sizes:
+        for B in sizes:
+            have = reported(T, B)
+            for t in (s for s in sizes if s <= T):
+                for b in (s for s in sizes if s <= B):
+                    assert reported(t, b) <= have, (T, B, t, b)
+                    for kw in (dict(), dict(page_size=5), dict(out_dtype=fb.ACT_F32), dict(dtype=fb.ACT_F16)):
+                        assert lib.moe_ffn_attend(args(t, b, **kw), None, P, have, P + 1, *[P] * 8) == MISALIGNED
