@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
             seen = seen_tokens(P, a.s, first_of(a, x), t, j);
             for (int b = 0; b < kTok / P.box; ++b)
               if (!(boxes >> b & 1u)) seen &= ~((~0ull >> (64 - P.box)) << (b * P.box));
+            __syncwarp();  // (each lane by its own way here; what follows takes whole warps)
           }
           // twice over the scores, 32 columns at a time: short loops, since what each
           // warp runs through once a step comes from beyond the nearest instruction cache
@@ -519,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
                 for (int e = 0; e < 32; ++e)
                   if (!(bits >> e & 1u)) w[e] = 0xFF800000u;  // -inf
               }
+              __syncwarp();
               tmem_write32(at + 32 * h, w);
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -615,38 +617,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_wide(const __grid_consta
 #pragma unroll
           for (int e = 0; e < 16; ++e) attend_put_odd(v[e], bits >> (2 * e));
         }
-        if (t < 0 || c >= P.D) continue;
-        if (odd) {
-          // what was taken out of the tiles, for the rows that see it
+        if (t >= 0 && c < P.D) {
+          if (odd) {
+            // what was taken out of the tiles, for the rows that see it
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            if (c + e >= P.D) break;
-            const float4 x = attend_own<F16>(P, a.b, a.head, a.s.len - a.s.n, t, j,
-                                             max(attend_common(P, a.s), chunk0 * 2 * kTok), end_at, c + e);
-            attend_add_odd(v[e], x.x);
-            attend_add_odd(v[e + 1], x.y);
-            attend_add_odd(v[e + 2], x.z);
-            attend_add_odd(v[e + 3], x.w);
+            for (int e = 0; e < 16; e += 4) {
+              if (c + e >= P.D) break;
+              const float4 x = attend_own<F16>(P, a.b, a.head, a.s.len - a.s.n, t, j,
+                                               max(attend_common(P, a.s), chunk0 * 2 * kTok), end_at, c + e);
+              attend_add_odd(v[e], x.x);
+              attend_add_odd(v[e + 1], x.y);
+              attend_add_odd(v[e + 2], x.z);
+              attend_add_odd(v[e + 3], x.w);
+            }
           }
-        }
-        if (whole) {
-          const long long to = t * P.o_stride + h * P.o_head + c;
+          if (whole) {
+            const long long to = t * P.o_stride + h * P.o_head + c;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = sum == 0.f ? 0.f : v[e] * inv;
-          if (P.o_vec && c + 16 <= P.D) {
+            for (int e = 0; e < 16; ++e) v[e] = sum == 0.f ? 0.f : v[e] * inv;
+            if (P.o_vec && c + 16 <= P.D) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) elem_store4(P.out, P.out_dtype, to + e, v + e);
+              for (int e = 0; e < 16; e += 4) elem_store4(P.out, P.out_dtype, to + e, v + e);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (c + e < P.D) elem_store(P.out, P.out_dtype, to + e, v[e]);
+            }
           } else {
+            // four columns of all rows lie together: the lanes' rows are neighbours
+            float4* const to = reinterpret_cast<float4*>(P.part) + (slot * (DP / 4) + c / 4) * 128 + row;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c + e < P.D) elem_store(P.out, P.out_dtype, to + e, v[e]);
+            for (int e = 0; e < 4; ++e) to[128 * e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
-        } else {
-          // four columns of all rows lie together: the lanes' rows are neighbours
-          float4* const to = reinterpret_cast<float4*>(P.part) + (slot * (DP / 4) + c / 4) * 128 + row;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[128 * e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
+        __syncwarp();  // (the next columns are read by whole warps)
       }
       tc::tc_fence_before();
       if (!dead) mbar_arrive(&o_free);
