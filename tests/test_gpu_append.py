@@ -207,3 +207,15 @@ def test_repeats_graphs_and_streams(T):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("xt,ct,interleaved,in_place", [(BF16, BF16, False, False), (F16, F16, True, True), (F32, BF16, False, True),
+                                                        (F32, F32, True, False)])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,page", [
+    (4096, 32, 4, 128, 128, 16), (2003, 64, 8, 128, 64, 64), (20011, 4, 2, 64, 64, 128), (5003, 14, 2, 96, 48, 24),
+    (9001, 6, 1, 36, 20, 7), (7001, 2, 1, 512, 512, 8)])
+def test_many_tokens_a_block(T, Hq, Hkv, D, rot, page, xt, ct, interleaved, in_place):
+    """Every block takes tokens one behind the other, more of them than lie in its ring, padding among them; heads
+    of more items than a block has threads are shared by several."""
+    run(T, Hq, Hkv, D, rot, page, xt=xt, ct=ct, qt=ct, interleaved=interleaved, in_place=in_place, layout="head" if in_place else "token",
+        drop=0.1, first=70000, scale=0.75)

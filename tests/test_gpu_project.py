@@ -151,3 +151,21 @@ def test_repeats_graphs_and_streams(T):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("xt", [BF16, F16])
+@pytest.mark.parametrize("T,K,N", [(3, 1024, 70001), (8, 2048, 40003), (5, 256, 150001), (3, 4096, 20005), (2, 8192, 50003),
+                                   (20, 1024, 30001), (31, 2048, 12007), (12, 2048, 20005), (16, 4096, 20005), (12, 8192, 50003),
+                                   (20, 8192, 20005), (100, 1024, 5003), (150, 5120, 3001)])
+def test_many_tiles_a_block(T, K, N, xt, group):
+    """Every block takes several batches of tiles, every warp more of them than its ring holds."""
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    x = torch.randn(T, K, generator=g, device="cuda").to(xt)
+    w = weights(g, N, K, group)
+    bias = torch.randn(N, generator=g, device="cuda")
+    y = fb.moe_ffn_project(x, w, group=group, bias=bias, out_dtype=F32)
+    for n in range(0, N, 10007):
+        rows = slice(n, n + 10007)
+        check(x, w[rows], group, bias[rows], y[:, rows])
+    assert torch.equal(fb.moe_ffn_project(x, w, group=group, bias=bias, out_dtype=F32), y)
