@@ -40,8 +40,9 @@ MOE_DEV long long attend_div(long long a, long long b) {
 
 MOE_DEV AttendSeq attend_seq(const AttendParams& P, int b) {
   AttendSeq s;
+  // (both bounds first: the difference of any two numbers may pass 32 bits)
   s.t0 = min(max(P.q_start[b], 0), P.T);
-  s.n = max(min(P.q_start[b + 1], P.T) - s.t0, 0);
+  s.n = max(min(max(P.q_start[b + 1], 0), P.T) - s.t0, 0);
   const long long most = (long long)P.max_pages * P.page_size;
   s.len = (int)min((long long)max(P.lens[b], 0), most);
   s.tiles = (s.n * P.G + P.rows - 1) / P.rows;

@@ -504,3 +504,20 @@ def test_rows_of_sequences_without_tokens_hold_up_nobody():
         times.append(start.elapsed_time(end))
     assert min(times) < 3.0, times
     assert bool((out[:512] == 0).all())
+
+
+@pytest.mark.parametrize("low", [-2**31, -2**31 + 1, -2**31 + 5, -1])
+@pytest.mark.parametrize("page", [16, 5])
+def test_row_starts_far_below_zero(low, page):
+    """A sequence whose rows end below 0 has none, however far: the difference of its bounds passes 32 bits."""
+    c = Case([(50, 2), (60, 20), (70, 2)], rest=3, page=page)
+    for bad, has in (([0, 2, low, 24], [2, 0, 24]), ([4, low, low, 3], [0, 0, 3]), ([20, low, 10, low], [0, 10, 0])):
+        full = torch.full((c.T + 4, c.Hq, c.D), 5.0, device="cuda", dtype=BF16)
+        starts = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        got = fb.moe_ffn_attend(c.q, c.k, c.v, c.table, c.lens, starts, out=full[2:-2])
+        rows = torch.zeros(c.T + 4, dtype=torch.bool, device="cuda")
+        for b in range(3):
+            first = max(bad[b], 0)
+            rows[2 + first:2 + first + has[b]] = True
+        assert bool((full[~rows] == 5).all()) and not bool((full[rows] == 5).all(-1).any())
+        assert bool(got.isfinite().all())
