@@ -764,8 +764,8 @@ def moe_ffn_attend(q, k_cache, v_cache, page_table, lens, q_start, mask=None, sc
     which lie in the pages ``page_table[b]`` (int32 [B, max_pages]).  mask int32 [T, words]: which of its sequence's
     rows a row sees (bit j: the j-th), None: those up to itself.  scale defaults to D ** -0.5; softcap 0: no cap (see
     ``include/moe_ffn.h``).  out defaults to a new tensor of q's shape and type (rows of no sequence are then 0), lse
-    (fp32 [T, q_heads]) is written where given.  workspace (a tensor of moe_ffn_attend_workspace bytes) defaults to a new
-    one.  Returns out."""
+    (fp32 [T, q_heads]) is written where given; neither overlaps another tensor.  workspace (a tensor of
+    moe_ffn_attend_workspace bytes) defaults to a new one.  Returns out."""
     if out is None:
         out = _new(stream, q.shape, q.dtype, q.device, zero=True)
     key = (5, q.shape, q.stride(), q.dtype, q.get_device(), k_cache.shape, k_cache.stride(), k_cache.dtype,

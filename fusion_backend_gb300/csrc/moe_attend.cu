@@ -10,9 +10,9 @@
 // mma.m16n8k16, the rows being the rows; a weight enters the second product as the
 // sum of two or three numbers of the cache's type.
 //
-// Measured: a step of 64 KB an SM 1.36 us, 7.3 TB/s (D = 128, long sequences); the end
+// Measured: a step of 64 KB an SM 1.4 us, 7 TB/s (D = 128, long sequences); the end
 // of a unit costs 3 us of a block, in part behind what is on its way; 48 sequences of
-// 500 to 12,000 tokens, 426 MB, 73 us; one of 2,000 tokens 8.6 us with the join.
+// 500 to 12,000 tokens, 426 MB, 75 us; one of 2,000 tokens 8.9 us with the join.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -46,8 +46,9 @@ MOE_DEV uint32_t piece(int r, int c) {
 
 // DP: elements of a head in shared memory (D rounded up); TERMS: numbers that
 // stand for a weight.
-// PAGED: pages hold multiples of 8 tokens: tensor copies of boxes of 8 or 16; else
-// asynchronous copies by the lanes, each token from a page of its own.
+// PAGED: pages hold multiples of 8 tokens: tensor copies of boxes of 8, 16 or (heads of
+// up to 64) 32; else asynchronous copies by the lanes, each token from a page of its own
+// (16 sequences of 4,000 tokens of 4 heads of 128: 28.5 us by boxes, 34 with pages of 1 or 5).
 template <bool F16, int DP, int TERMS, bool PAGED>
 __global__ void __launch_bounds__(32 * warps_for(DP), 1) k_attend(const __grid_constant__ AttendParams P) {
   constexpr int W = warps_for(DP), S = stages_for(DP), kSlot = slot_bytes(DP), kChunks = DP / 8, kTok = tokens_for(DP);

@@ -18,7 +18,8 @@
 //                 took longer than the stream, too)
 //   warps 2, 3    in the tiles that hold tokens which some rows do not see, take values
 //                 that are not finite out (a product with a weight of 0 has an effect
-//                 then); the rows that do see them get them at the end.  Queries that
+//                 then); the rows that do see them get them at the end, as those of
+//                 the other tiles, which leave sums that are not finite.  Queries that
 //                 tensor copies cannot fetch
 //   warps 4-11    a thread a row: scores to weights, four warps a stream
 //
@@ -28,7 +29,7 @@
 //
 // Measured: a step of 64 KB an SM 1.4 us, 7 TB/s (D = 128); a call of one step 13 us
 // (the way from the lengths to the page, the tile, the first scores, and cold
-// instructions everywhere); 16 trees of 16 tokens, 139 MB, 40 us.
+// instructions everywhere); 16 trees of 16 tokens, 139 MB, 39 us.
 //
 // Every wait is bounded.  After one that ran out, in whichever thread, nobody waits,
 // issues or arrives any more, but all still meet at the block's barriers, and results

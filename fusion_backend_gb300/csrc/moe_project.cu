@@ -18,10 +18,13 @@
 // group's products go to sums of their own and from there, times the group's scale,
 // to the row's: the products are exact and everything is added in fp32.
 //
-// Measured (weights from HBM): 5120 x 2048, 1 token 3.9 us, 16 tokens 5.8, 61 tokens
-// 11.4, 256 tokens 29; 100003 x 2048, 4 tokens 25.6 us, 4.6 TB/s: integer
-// instructions of the codes issue at half rate and are the bound (issue slots 70 %
-// used).  x from L2 for every tile of rows, the first form, took 19.6 us for 61 tokens.
+// Measured (weights from HBM): 5120 x 2048, 1 token 3.9 us, 16 tokens 6.0, 61 tokens
+// 11.6, 256 tokens 30, 1024 tokens 123: above 32 tokens each further 32 turn the codes
+// into numbers again.  100003 x 2048, 4 tokens 25.3 us, 4.6 TB/s: no unit is full (issue
+// slots 65 %, integer pipe 51 %, HBM 53 %); warps wait for each other's issue, for fixed
+// latencies and for the integer pipe about as long, and at the barriers of a batch a
+// third of that.  x from L2 for every tile of rows, the first form, took 19.6 us for 61
+// tokens.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -45,8 +48,8 @@ constexpr int kChunks = kSlab / 32;
 // pair, and one shift for all.  bf16: the low byte of a number with nothing else set,
 // N, is N 2^-133, the subnormal range and the first exponent above it being one
 // scale: so a nibble at bit 0 or 4 is c 2^-133 or c 2^-129.  fp16: a nibble at bit 0
-// or 4 of 1024 is 1024 + c or 1024 + 16 c.  (A shift for every pair: 7 integer
-// instructions a word instead of 5, which run at half the rate, and bound the kernel.)
+// or 4 of 1024 is 1024 + c or 1024 + 16 c.  (A shift for every pair is 7 integer
+// instructions a word instead of 5: 27.0 us for 100003 rows where this took 25.7.)
 template <bool F16>
 MOE_DEV void code_pairs(uint32_t v, uint32_t (&r)[4]) {
 #pragma unroll

@@ -475,16 +475,20 @@ int moe_ffn_append_kv(const moe_ffn_append_args* args, moe_ffn_stream_t stream, 
  * over the tokens i that row t sees: all before the sequence's own n, and of
  * those the j-th where bit j % 32 of mask[t][j / 32] is set; mask NULL: those up
  * to the row's own.  Query head h reads key head h / (q_heads / kv_heads).
- * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not
- * see has no effect on it, infinities and NaN included.  Tokens of pages outside
- * 0..pages - 1 are not seen.  lens is taken within 0..max_pages page_size,
+ * A row that sees nothing, or only scores of -inf, gets out = 0 and lse = -inf.
+ * What a row does not see has no effect on it, infinities and NaN included.  A value
+ * that it sees counts however small its weight: an infinity makes that element of out
+ * the same infinity, NaN or infinities of both signs make it NaN.  Tokens of pages
+ * outside 0..pages - 1 are not seen.  lens is taken within 0..max_pages page_size,
  * q_start within 0..T; rows of no sequence (padding behind the last) are left as
- * they are, those of several get any of the results.
+ * they are, those of several get any of the results.  out and lse overlap no other
+ * tensor.
  * q [T,q_heads,D] and the caches are bf16 or fp16 (dtype), out any type, lse
  * fp32 [T,q_heads] or NULL.  Scores, statistics and sums are in fp32; weights
  * enter the second product as the sum of two numbers of the cache's type (bf16
- * with fp32 out: three).  Caches as in moe_ffn_append_kv, 16-byte aligned with
- * strides that are multiples of 8.
+ * with fp32 out: three).  Weights are held up to 2^8 (fp16: 2^15) before they are
+ * divided by their sum: bf16 values from 2^119 / lens on may overflow.  Caches as in
+ * moe_ffn_append_kv, 16-byte aligned with strides that are multiples of 8.
  * T <= 1048576, B <= 65536, q_heads a multiple of kv_heads and at most 128 kv_heads, kv_heads <= 4096,
  * D a multiple of 8 up to 256, pages page_size < 2^31, max_pages page_size <= 2^30.
  * The workspace (256-byte aligned, scratch) holds what
