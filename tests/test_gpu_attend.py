@@ -521,3 +521,84 @@ def test_row_starts_far_below_zero(low, page):
             rows[2 + first:2 + first + has[b]] = True
         assert bool((full[~rows] == 5).all()) and not bool((full[rows] == 5).all(-1).any())
         assert bool(got.isfinite().all())
+
+
+@pytest.mark.parametrize("n", [1, 16])
+@pytest.mark.parametrize("page", [8, 3])
+def test_the_largest_batch(n, page):
+    """65,536 sequences, a row or 16 of each, some without tokens or with fewer than rows, pages in any order."""
+    B, D, most = 65536, 8, 24
+    g = torch.Generator(device="cuda").manual_seed(n + page)
+    lens = torch.randint(0, most + 1, (B,), generator=g, device="cuda").to(torch.int32)
+    pages = 40000
+    k, v = (torch.randn(pages, page, 1, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randint(0, pages, (B, most // page), generator=g, device="cuda").to(torch.int32)
+    q = torch.randn(B * n, 1, D, generator=g, device="cuda").bfloat16()
+    starts = (torch.arange(B + 1, device="cuda") * n).to(torch.int32)
+    out, lse = torch.full((B * n, 1, D), 5.0, device="cuda"), torch.full((B * n, 1), 5.0, device="cuda")
+    fb.moe_ffn_attend(q, k, v, table, lens, starts, out=out, lse=lse)
+    i = torch.arange(most, device="cuda")
+    at = table.long()[:, i // page], (i % page)[None]
+    keys, values = k[at][:, :, 0].double(), v[at][:, :, 0].double()  # [B, most, D]
+    rows = q.view(B, n, D).double()
+    s = torch.einsum("bjd,bid->bji", rows, keys) * D**-0.5
+    # as in Case.reference, with sums of 24 tokens of 8 elements
+    ds = torch.einsum("bjd,bid->bji", rows.abs(), keys.abs()) * (D**-0.5 * (D / 8 + 10) * 2.0**-23)
+    own = i[None] - (lens[:, None] - n)
+    seen = (own[:, None] <= torch.arange(n, device="cuda")[None, :, None]) & (i[None] < lens[:, None])[:, None]
+    s = s.masked_fill(~seen, -INF)
+    top = s.amax(-1, keepdim=True)
+    none = top == -INF
+    top = top.masked_fill(none, 0.0)
+    p = torch.exp(s - top)
+    total = p.sum(-1, keepdim=True).masked_fill(none, 1.0)
+    p = p / total
+    dp = ds + (s.abs().masked_fill(~seen, 0.0) + top.abs() + 2) * 2.0**-22
+    e, adds = (p * dp).sum(-1, keepdim=True), (most / 8 + 64) * 2.0**-23
+    want, size = torch.einsum("bji,bid->bjd", p, values), torch.einsum("bji,bid->bjd", p, values.abs())
+    err = torch.einsum("bji,bid->bjd", p * dp, values.abs()) + size * (e + 2 * adds + 2.0**-20)
+    d = (out.view(B, n, D).double() - want).abs() - err - half_step(want.abs() + err, F32)
+    assert float(d.max()) <= 0, float(d.max())
+    none = none.view(-1, 1)
+    assert torch.equal(lse == -INF, none) and bool((out[none[:, 0]] == 0).all())
+    wl, el = (top + torch.log(total)).view(-1, 1), e.view(-1, 1) + adds
+    dl = ((lse.double() - wl).abs() - el - (wl.abs() + 8) * 2.0**-22)[~none]
+    assert float(dl.max()) <= 0, float(dl.max())
+
+
+def test_the_first_call_in_a_capture():
+    """A process whose first calls of the library are captured, replayed then."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import fusion_backend_gb300 as fb
+z = lambda *s, dtype=torch.bfloat16: torch.ones(s, device="cuda", dtype=dtype)
+x, w = z(40, 256), z(64, 160, dtype=torch.uint8)
+q, k, kc, vc = z(40, 8, 64), z(40, 1, 64), z(9, 16, 1, 64), z(9, 16, 1, 64)
+i = torch.arange(40, device="cuda", dtype=torch.int32)
+table, lens, starts = i[:3].view(1, 3).contiguous(), i[:1] + 40, i[:2] * 40
+f = torch.zeros(32, device="cuda")
+out, y, qo = torch.zeros_like(q), z(40, 64), torch.zeros_like(q)
+ws = torch.empty(fb.moe_ffn_attend_workspace(40, 1, 8, 1, 64), dtype=torch.uint8, device="cuda")
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    fb.moe_ffn_project(x, w, out=y)
+    fb.moe_ffn_append_kv(k, k, i, i, f, kc, vc, q=q, q_out=qo)
+    fb.moe_ffn_attend(qo, kc, vc, table, lens, starts, out=out, workspace=ws)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, qo, kc, vc, out)]
+fb.moe_ffn_project(x, w, out=y)
+fb.moe_ffn_append_kv(k, k, i, i, f, kc, vc, q=q, q_out=qo)
+fb.moe_ffn_attend(qo, kc, vc, table, lens, starts, out=out, workspace=ws)
+assert all(torch.equal(a, b) for a, b in zip(got, (y, qo, kc, vc, out)))
+assert bool((out == 1).all())
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
